@@ -310,6 +310,168 @@ KDA_API int kda_commit_verify(const kda_params* p, int32_t B, int32_t W, const i
                               const int32_t* slots, void* conv_state, float* rec_state, void* log,
                               void* out, int32_t* dev_status, cudaStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * The gated delta rule with one decay per head, and what stands around it in
+ * a layer: its convolution, the norms of a block, and the state pools' slots.
+ * The conventions above hold for these calls too.  None of the source pages
+ * has these operators in this form; they complete the layer for models that
+ * mix such heads with the per-key-dim ones.
+ *
+ * Per (sequence, value head h), row by row, with key head h / (Hv / Hk):
+ *     log alpha = -exp(A_log_h) * softplus(a_h + dt_bias_h),  beta = sigmoid(b_h)
+ *     q, k L2-normalised over dk (optional): x * (sum x^2 + l2_eps)^(-1/2)
+ *     S = alpha S + k u^T,  u = beta (v - alpha S^T k),  o = scale S^T q
+ * (rows arrive after their convolution).  The state is fp32 [dk][dv].
+ * ------------------------------------------------------------------------ */
+typedef struct kda_gdn_params {
+    int32_t num_heads_k;   /* Hk >= 1                                           */
+    int32_t num_heads_v;   /* Hv, a multiple of Hk, <= 1024                     */
+    int32_t head_dim_k;    /* dk in {32, 64, 128}                               */
+    int32_t head_dim_v;    /* dv in {32, 64, 128}                               */
+    int32_t l2_norm;       /* 0: q and k as they are; 1: L2-normalised          */
+    float l2_eps;          /* >= 0, read with l2_norm = 1                       */
+    float scale;           /* output scale, finite                              */
+    int32_t io_dtype;      /* q, k, v, gate, beta: KDA_DTYPE_F32 / _BF16        */
+    int32_t out_dtype;     /* out: KDA_DTYPE_F32 / _BF16 (fp32 rows: fp32 only) */
+    int32_t num_slots;     /* state slots in rec_state                          */
+    int64_t q_row_stride;  /* elements from a row of q to the next; 0: dense    */
+    int64_t k_row_stride;  /*   (Hk*dk); at least that, and a multiple of       */
+    int64_t v_row_stride;  /*   16 bytes.  v: Hv*dv                             */
+    const float* A_log;    /* [Hv] fp32                                         */
+    const float* dt_bias;  /* [Hv] fp32                                         */
+} kda_gdn_params;
+
+/*
+ * Prompt rows of N variable-length sequences (cu_seqlens, slots, T, N and
+ * dev_status as in kda_prefill_varlen).  q, k: [T][Hk][dk], v: [T][Hv][dv]
+ * with the row strides of p (a slice of one row of q|k|v channels each, for
+ * instance), gate logits a and beta logits b: dense [T][Hv], out: dense
+ * [T][Hv][dv], rec_state: fp32 [num_slots][Hv][dk][dv], updated in place.  An empty
+ * or skipped sequence leaves its state, and a skipped one its out rows, as
+ * they were.  The non-negative slots of one call are distinct.  `out` overlaps
+ * no input.
+ *   - bf16 rows run in chunks of 64 on the tensor cores.  The states keep fp32
+ *     accuracy (every product that reaches them has operands split into
+ *     bf16 high and low parts where one bf16 does not hold the value);
+ *     fp32 rows run row by row in fp32.
+ *   - A prompt cut into several calls agrees with one uncut call to rounding.
+ *   - Values up to 2^60 in magnitude keep that accuracy (operands are rescaled
+ *     by powers of two within 2^+-60).  With l2_norm = 0 keys are expected to
+ *     satisfy beta |k|^2 <= 2, beyond which the rule itself grows without bound.
+ *   - A NaN or an infinity in a row reaches no other sequence or head; in its
+ *     own it may reach rows from its 64-row chunk's first on.
+ *   - workspace: kda_gdn_prefill_workspace_bytes(p, N, T) bytes (may be NULL
+ *     when that is 0); contents need no init.  Calls that may run at the same
+ *     time take a workspace each.
+ */
+KDA_API int kda_gdn_prefill_varlen(const kda_gdn_params* p, const int32_t* cu_seqlens, int32_t N, int32_t T,
+                                   const void* q, const void* k, const void* v, const void* gate, const void* beta,
+                                   const int32_t* slots, float* rec_state, void* out, void* workspace,
+                                   size_t ws_bytes, int32_t* dev_status, cudaStream_t stream);
+KDA_API size_t kda_gdn_prefill_workspace_bytes(const kda_gdn_params* p, int32_t N, int32_t T);
+
+/* One row per sequence (row b belongs to sequence b), states in place. */
+KDA_API int kda_gdn_decode(const kda_gdn_params* p, int32_t B, const void* q, const void* k, const void* v,
+                           const void* gate, const void* beta, const int32_t* slots, float* rec_state, void* out,
+                           int32_t* dev_status, cudaStream_t stream);
+
+/*
+ * Causal depthwise convolution with carried state, then SiLU: per channel
+ *     y_t = silu(sum_j w[c][j] x_{t-K+1+j}),
+ * rows before a sequence's first from its slot of conv_state
+ * ([num_slots][K-1][channels], oldest row first), which takes the last K-1
+ * raw rows in return.  x and y: dense [rows][channels] of io_dtype, apart
+ * (KDA_ERR_INVALID_ARGUMENT where they overlap).  A zero-length sequence
+ * leaves its state, a skipped one its state and y rows.  The non-negative
+ * slots of one call are distinct.
+ */
+typedef struct kda_conv_params {
+    int32_t channels;         /* a multiple of 8, <= 2^20                       */
+    int32_t conv_kernel;      /* K in {2, 3, 4}                                 */
+    int32_t io_dtype;         /* x, y and the state: KDA_DTYPE_F32 / _BF16      */
+    int32_t num_slots;        /* slots in conv_state                            */
+    const float* conv_weight; /* [channels][K] fp32, tap K-1 = current row      */
+} kda_conv_params;
+KDA_API int kda_conv_varlen(const kda_conv_params* p, const int32_t* cu_seqlens, int32_t N, int32_t T, const void* x,
+                            const int32_t* slots, void* conv_state, void* y, int32_t* dev_status,
+                            cudaStream_t stream);
+/* One row per sequence. */
+KDA_API int kda_conv_decode(const kda_conv_params* p, int32_t B, const void* x, const int32_t* slots,
+                            void* conv_state, void* y, int32_t* dev_status, cudaStream_t stream);
+
+/*
+ * The norms around a block, in one pass over its rows:
+ *     t = y;  t = t * (mean t^2 + eps)^(-1/2) * post_weight      (post_norm = 1)
+ *     t = t * sigmoid(g)  or  t * g * sigmoid(g)                 (gate_act)
+ *     h = residual + residual_scale * t     (residual null: residual_scale * t)
+ *     x = h * (mean h^2 + eps)^(-1/2) * pre_weight               (x_out given)
+ * over rows of `dim` values: dim = dv for the norm and gate of each head's
+ * outputs, dim = the model's width for a block's exit and the next one's
+ * entry.  The sums and h are fp32; x comes from h before its rounding.
+ *   y, gate, x_out: io_dtype; residual, h_out: res_dtype; all dense
+ *   [rows][dim].  gate: required unless gate_act is NONE.  h_out and x_out:
+ *   nullable, not both.  An output may be the very buffer of an input of its
+ *   type (row for row in place); any other overlap with an input or with the
+ *   other output is KDA_ERR_INVALID_ARGUMENT.  A row of infinities or NaN
+ *   gives NaN in that row alone.
+ */
+#define KDA_NORM_GATE_NONE 0
+#define KDA_NORM_GATE_SIGMOID 1
+#define KDA_NORM_GATE_SILU 2
+typedef struct kda_norm_params {
+    int32_t dim;              /* a multiple of 8, <= 16384                      */
+    int32_t post_norm;        /* 0 or 1                                         */
+    int32_t gate_act;         /* KDA_NORM_GATE_*                                */
+    float residual_scale;     /* finite                                         */
+    float norm_eps;           /* >= 0                                           */
+    int32_t io_dtype;         /* y, gate, x_out: KDA_DTYPE_F32 / _BF16          */
+    int32_t res_dtype;        /* residual, h_out                                */
+    const float* post_weight; /* [dim] fp32, nullable = unit weight             */
+    const float* pre_weight;  /* [dim] fp32, nullable = unit weight             */
+} kda_norm_params;
+KDA_API int kda_block_norm(const kda_norm_params* p, int64_t rows, const void* y, const void* gate,
+                           const void* residual, void* h_out, void* x_out, cudaStream_t stream);
+
+/*
+ * Slots of a state pool: [num_layers] blocks, layer_stride_bytes apart, of
+ * [num_slots][slot_bytes] (conv or recurrent states of any layer kind).
+ */
+typedef struct kda_slot_pool {
+    void* pool;                 /* device, 16-byte aligned                      */
+    int64_t layer_stride_bytes; /* >= num_slots * slot_bytes, multiple of 16    */
+    int64_t slot_bytes;         /* > 0, multiple of 16                          */
+    int32_t num_layers;         /* >= 1                                         */
+    int32_t num_slots;          /* 1 .. KDA_MAX_POOL_SLOTS                      */
+} kda_slot_pool;
+#define KDA_MAX_POOL_SLOTS 262144
+
+/*
+ * Copies slot src[i] to slot dst[i] in every layer, for i < n: a fork (one
+ * source, several targets), a copy, or the moves of a compaction.  A pair
+ * with a negative entry is skipped, one with src = dst does nothing.  The
+ * order of the pairs has no meaning, so a pair is flagged (KDA_DEV_BAD_SLOT)
+ * and skipped if an entry is >= num_slots, if its target is another pair's
+ * target too, or if its target is the source of any other copying pair: what is
+ * read is always what the call found.
+ */
+KDA_API int kda_slots_copy(const kda_slot_pool* pool, int32_t n, const int32_t* src, const int32_t* dst,
+                           int32_t* dev_status, cudaStream_t stream);
+/* Zeroes slot slots[i] in every layer, for i < n (a freed slot; negative:
+ * skipped; >= num_slots: flagged and skipped; the same slot twice is fine). */
+KDA_API int kda_slots_zero(const kda_slot_pool* pool, int32_t n, const int32_t* slots, int32_t* dev_status,
+                           cudaStream_t stream);
+/*
+ * The moves that close a pool's holes.  live: int32 [num_slots], non-zero for
+ * a slot in use; with L of them in use, the i-th live slot at or above L moves
+ * to the i-th hole below L.  Writes src and dst (int32 [num_slots], the moves
+ * first, then -1: the arguments of kda_slots_copy with n = num_slots, for each
+ * pool that shares the slot numbers) and remap (int32 [num_slots]: where each
+ * live slot is afterwards, -1 for a free one).  Reads nothing of the pool but
+ * its num_slots.  The four arrays do not overlap.
+ */
+KDA_API int kda_slots_compact_plan(const kda_slot_pool* pool, const int32_t* live, int32_t* src, int32_t* dst,
+                                   int32_t* remap, cudaStream_t stream);
+
 /* Human-readable name of a return code. */
 KDA_API const char* kda_status_string(int status);
 

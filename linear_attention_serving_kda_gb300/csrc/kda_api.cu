@@ -8,16 +8,13 @@
 #include <cmath>
 #include <cstring>
 
+#include "kda_check.h"
 #include "kda_common.cuh"
 #include "kda_internal.h"
 
 namespace {
 
 using namespace kda;
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-int io_size(int dtype) { return dtype == KDA_DTYPE_BF16 ? 2 : 4; }
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 size_t align1024(size_t x) { return (x + 1023) & ~size_t(1023); }
@@ -42,34 +39,6 @@ int check_params(const kda_params* p)
     if (!aligned16(p->A_log) || !aligned16(p->dt_bias) || !aligned16(p->conv_weight)) return KDA_ERR_INVALID_ARGUMENT;
     if (p->norm_weight && !aligned16(p->norm_weight)) return KDA_ERR_INVALID_ARGUMENT;
     return KDA_OK;
-}
-
-// Every pointer in the list must be non-null and 16-byte aligned.
-int check_ptrs(std::initializer_list<const void*> ps)
-{
-    for (const void* x : ps)
-        if (!x || !aligned16(x)) return KDA_ERR_INVALID_ARGUMENT;
-    return KDA_OK;
-}
-
-int check_opt(const void* x) { return (x && !aligned16(x)) ? KDA_ERR_INVALID_ARGUMENT : KDA_OK; }
-
-// The library is built for sm_103a only; remember the answer per device
-// (the set-up object records only a successful check; -1 marks another GPU).
-int check_device()
-{
-    static PerDeviceOnce once;
-    static std::atomic<signed char> ok[kMaxDevices];  // 0 unknown, 1 yes, -1 no
-    int dev = 0;
-    cudaError_t e = once.run([&](int d) {
-        int major = 0, minor = 0;
-        cudaError_t r = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, d);
-        if (r == cudaSuccess) r = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, d);
-        if (r == cudaSuccess) ok[d].store((major == 10 && minor == 3) ? 1 : -1, std::memory_order_relaxed);
-        return r;
-    });
-    if (e != cudaSuccess || cudaGetDevice(&dev) != cudaSuccess) return KDA_ERR_DEVICE;
-    return ok[dev].load(std::memory_order_relaxed) == 1 ? KDA_OK : KDA_ERR_DEVICE;
 }
 
 void fill_common(RecArgs& a, const kda_params* p)
@@ -97,6 +66,35 @@ size_t log_float_bytes(const kda_params* p, int32_t B, int32_t W)
 }
 
 }  // namespace
+
+// The library is built for sm_103a only; remember the answer per device
+// (the set-up object records only a successful check; -1 marks another GPU).
+int kda::check_device()
+{
+    static PerDeviceOnce once;
+    static std::atomic<signed char> ok[kMaxDevices];  // 0 unknown, 1 yes, -1 no
+    int dev = 0;
+    cudaError_t e = once.run([&](int d) {
+        int major = 0, minor = 0;
+        cudaError_t r = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, d);
+        if (r == cudaSuccess) r = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, d);
+        if (r == cudaSuccess) ok[d].store((major == 10 && minor == 3) ? 1 : -1, std::memory_order_relaxed);
+        return r;
+    });
+    if (e != cudaSuccess || cudaGetDevice(&dev) != cudaSuccess) return KDA_ERR_DEVICE;
+    return ok[dev].load(std::memory_order_relaxed) == 1 ? KDA_OK : KDA_ERR_DEVICE;
+}
+
+int kda::sm_count()
+{
+    static std::atomic<int> count[kMaxDevices];  // 0 unknown
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+    int n = count[dev].load(std::memory_order_relaxed);
+    if (n == 0 && cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess)
+        count[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
 
 extern "C" {
 

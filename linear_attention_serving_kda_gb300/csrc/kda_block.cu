@@ -1,0 +1,529 @@
+// kda_block.cu -- the memory-bound operators around a recurrent layer: the
+// causal depthwise convolution with carried state and SiLU, and the norms
+// around a block.  Each reads and writes every value once; HBM bandwidth
+// bounds both.
+#include <cmath>
+
+#include "kda_check.h"
+#include "kda_common.cuh"
+
+namespace kda {
+namespace {
+
+// ------------------------------------------------------------ eight values
+
+template <typename T> struct Vec8;
+template <> struct Vec8<__nv_bfloat16> {
+    uint4 r;
+    __device__ __forceinline__ void load(const void* p) { r = *static_cast<const uint4*>(p); }
+    __device__ __forceinline__ void store(void* p) const { *static_cast<uint4*>(p) = r; }
+    __device__ __forceinline__ void zero() { r = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void get(float (&x)[8]) const
+    {
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+    __device__ __forceinline__ void set(const float (&x)[8])
+    {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        r = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+template <> struct Vec8<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const void* p)
+    {
+        a = static_cast<const float4*>(p)[0];
+        b = static_cast<const float4*>(p)[1];
+    }
+    __device__ __forceinline__ void store(void* p) const
+    {
+        static_cast<float4*>(p)[0] = a;
+        static_cast<float4*>(p)[1] = b;
+    }
+    __device__ __forceinline__ void zero() { a = b = make_float4(0, 0, 0, 0); }
+    __device__ __forceinline__ void get(float (&x)[8]) const
+    {
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    }
+    __device__ __forceinline__ void set(const float (&x)[8])
+    {
+        a = make_float4(x[0], x[1], x[2], x[3]);
+        b = make_float4(x[4], x[5], x[6], x[7]);
+    }
+};
+
+// ------------------------------------------------------------ convolution
+
+struct ConvArgs {
+    int C, N, T, num_slots;
+    const int32_t* cu_seqlens;
+    const void* x;
+    const float* w;
+    const int32_t* slots;
+    void* state;
+    void* y;
+    int32_t* dev_status;
+};
+
+// Each thread owns eight channels: K taps for each of them in registers and
+// the last K-1 rows beside them, so a tile of rows is read once.
+template <typename IO, int K> struct ConvLane {
+    float w[8][K];
+    float win[K][8];  // win[j]: the row j before the current one is win[K-1-j]
+    __device__ __forceinline__ void taps(const float* p, int c)
+    {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int j = 0; j < K; ++j) w[i][j] = p[(size_t)(c + i) * K + j];
+    }
+    // win[K-1] holds the current row: the row's outputs, then the window moves on
+    __device__ __forceinline__ void step(Vec8<IO>& out)
+    {
+        float y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float acc = 0.f;
+#pragma unroll
+            for (int j = 0; j < K; ++j) acc = fmaf(w[i][j], win[j][i], acc);
+            y[i] = siluf_(acc);
+        }
+        out.set(y);
+#pragma unroll
+        for (int j = 0; j + 1 < K; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) win[j][i] = win[j + 1][i];
+    }
+};
+
+constexpr int CT = 128;       // threads: 1024 channels
+constexpr int CONV_ROWS = 32; // rows of a tile (K - 1 more are read again)
+constexpr int CONV_AHEAD = 8; // rows in flight
+
+// Tiles start at a sequence's first row, so only its tile 0 reads the old
+// state: that CTA also writes the new one, after its reads, and no other CTA
+// touches the slot.  blockIdx.x counts tiles over the sequences.
+template <typename IO, int K> __global__ void __launch_bounds__(CT) conv_varlen_kernel(const ConvArgs a)
+{
+    __shared__ int found[3];  // sequence, tile in it, tiles before a step of the search
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (warp == 0) {
+        int before = 0, seq = -1, tile = 0;
+        bool bad = false;
+        for (int n0 = 0; n0 < a.N && seq < 0; n0 += 32) {
+            int tiles = 0;
+            if (n0 + lane < a.N) {
+                const int b = a.cu_seqlens[n0 + lane], e = a.cu_seqlens[n0 + lane + 1];
+                if (b < 0 || e < b || e > a.T) bad = true;
+                else tiles = (e - b + CONV_ROWS - 1) / CONV_ROWS;
+            }
+            int inc = tiles;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int up = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += up;
+            }
+            const bool mine = (int)blockIdx.x >= before + inc - tiles && (int)blockIdx.x < before + inc;
+            const uint32_t m = __ballot_sync(0xffffffffu, mine);
+            if (m) {
+                const int l = __ffs(m) - 1;
+                seq = n0 + l;
+                tile = __shfl_sync(0xffffffffu, (int)blockIdx.x - (before + inc - tiles), l);
+            }
+            before += __shfl_sync(0xffffffffu, inc, 31);
+        }
+        if (bad) flag_status(a.dev_status, KDA_DEV_BAD_SEQLENS);
+        if (lane == 0) {
+            found[0] = seq;
+            found[1] = tile;
+        }
+    }
+    __syncthreads();
+    const int seq = found[0];
+    if (seq < 0) return;
+    const int slot = a.slots ? a.slots[seq] : seq;
+    if (slot >= a.num_slots) {
+        if (tid == 0) flag_status(a.dev_status, KDA_DEV_BAD_SLOT);
+        return;
+    }
+    const int c = (blockIdx.y * CT + tid) * 8;
+    if (slot < 0 || c >= a.C) return;
+    const int b = a.cu_seqlens[seq], e = a.cu_seqlens[seq + 1];
+    const int r0 = b + found[1] * CONV_ROWS, r1 = min(r0 + CONV_ROWS, e);
+    const size_t C = a.C;
+    const IO* x = static_cast<const IO*>(a.x);
+    IO* y = static_cast<IO*>(a.y);
+    IO* st = static_cast<IO*>(a.state) + (size_t)slot * (K - 1) * C;
+
+    Vec8<IO> hist[K - 1];
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j)
+        hist[j].load(r0 == b ? st + j * C + c : x + (size_t)(r0 - (K - 1) + j) * C + c);
+    ConvLane<IO, K> ln;
+    ln.taps(a.w, c);
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) hist[j].get(ln.win[j]);
+    if (r0 == b) {
+        // the new state: the last K-1 rows of old state and sequence
+        const int len = e - b;
+        Vec8<IO> nw[K - 1];
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) {
+            const int r = len - (K - 1) + j;  // row of the sequence; negative: old row K-1+r
+            if (r >= 0) nw[j].load(x + (size_t)(b + r) * C + c);
+            else {
+#pragma unroll
+                for (int i = 0; i < K - 1; ++i)
+                    if (i == K - 1 + r) nw[j] = hist[i];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) nw[j].store(st + j * C + c);
+    }
+    for (int r = r0; r < r1; r += CONV_AHEAD) {
+        Vec8<IO> in[CONV_AHEAD];
+#pragma unroll
+        for (int i = 0; i < CONV_AHEAD; ++i)
+            if (r + i < r1) in[i].load(x + (size_t)(r + i) * C + c);
+#pragma unroll
+        for (int i = 0; i < CONV_AHEAD; ++i)
+            if (r + i < r1) {
+                in[i].get(ln.win[K - 1]);
+                Vec8<IO> o;
+                ln.step(o);
+                o.store(y + (size_t)(r + i) * C + c);
+            }
+    }
+}
+
+// One row per sequence.
+template <typename IO, int K> __global__ void __launch_bounds__(CT) conv_decode_kernel(const ConvArgs a)
+{
+    const int seq = blockIdx.x;
+    const int c = (blockIdx.y * CT + threadIdx.x) * 8;
+    const int slot = a.slots ? a.slots[seq] : seq;
+    if (slot >= a.num_slots) {
+        if (threadIdx.x == 0) flag_status(a.dev_status, KDA_DEV_BAD_SLOT);
+        return;
+    }
+    if (slot < 0 || c >= a.C) return;
+    const size_t C = a.C;
+    IO* st = static_cast<IO*>(a.state) + (size_t)slot * (K - 1) * C;
+    Vec8<IO> v[K];
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) v[j].load(st + j * C + c);
+    v[K - 1].load(static_cast<const IO*>(a.x) + (size_t)seq * C + c);
+    ConvLane<IO, K> ln;
+    ln.taps(a.w, c);
+#pragma unroll
+    for (int j = 0; j < K; ++j) v[j].get(ln.win[j]);
+    Vec8<IO> o;
+    ln.step(o);
+    o.store(static_cast<IO*>(a.y) + (size_t)seq * C + c);
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) v[j + 1].store(st + j * C + c);
+}
+
+template <typename IO> void launch_conv(const ConvArgs& a, int K, bool varlen, cudaStream_t st)
+{
+    const int cols = (a.C / 8 + CT - 1) / CT;
+    if (varlen) {
+        const dim3 g(a.N + a.T / CONV_ROWS, cols);  // sum of ceil(len / rows) <= N + T / rows
+        if (K == 2) conv_varlen_kernel<IO, 2><<<g, CT, 0, st>>>(a);
+        else if (K == 3) conv_varlen_kernel<IO, 3><<<g, CT, 0, st>>>(a);
+        else conv_varlen_kernel<IO, 4><<<g, CT, 0, st>>>(a);
+    } else {
+        const dim3 g(a.N, cols);
+        if (K == 2) conv_decode_kernel<IO, 2><<<g, CT, 0, st>>>(a);
+        else if (K == 3) conv_decode_kernel<IO, 3><<<g, CT, 0, st>>>(a);
+        else conv_decode_kernel<IO, 4><<<g, CT, 0, st>>>(a);
+    }
+}
+
+int check_conv(const kda_conv_params* p)
+{
+    if (!p) return KDA_ERR_INVALID_ARGUMENT;
+    if (p->conv_kernel < 2 || p->conv_kernel > 4) return KDA_ERR_UNSUPPORTED_GEOMETRY;
+    if (p->channels <= 0) return KDA_ERR_INVALID_ARGUMENT;
+    if (p->channels % 8 != 0 || p->channels > (1 << 20)) return KDA_ERR_UNSUPPORTED_GEOMETRY;
+    if (!known_dtype(p->io_dtype) || p->num_slots <= 0) return KDA_ERR_INVALID_ARGUMENT;
+    return check_ptrs({p->conv_weight});
+}
+
+int conv_call(const kda_conv_params* p, const int32_t* cu_seqlens, int32_t N, int32_t T, const void* x,
+              const int32_t* slots, void* conv_state, void* y, int32_t* dev_status, bool varlen, cudaStream_t stream)
+{
+    int rc;
+    if ((rc = check_ptrs({x, conv_state, y})) != KDA_OK || (rc = check_opt(slots)) != KDA_OK) return rc;
+    const size_t row = (size_t)p->channels * io_size(p->io_dtype);
+    const size_t state = (size_t)p->num_slots * (p->conv_kernel - 1) * row;
+    if (overlap(x, T * row, y, T * row) || overlap(conv_state, state, y, T * row) || overlap(conv_state, state, x, T * row))
+        return KDA_ERR_INVALID_ARGUMENT;
+    if ((rc = check_device()) != KDA_OK) return rc;
+    ConvArgs a;
+    a.C = p->channels;
+    a.N = N;
+    a.T = T;
+    a.num_slots = p->num_slots;
+    a.cu_seqlens = cu_seqlens;
+    a.x = x;
+    a.w = p->conv_weight;
+    a.slots = slots;
+    a.state = conv_state;
+    a.y = y;
+    a.dev_status = dev_status;
+    if (p->io_dtype == KDA_DTYPE_BF16) launch_conv<__nv_bfloat16>(a, p->conv_kernel, varlen, stream);
+    else launch_conv<float>(a, p->conv_kernel, varlen, stream);
+    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_LAUNCH;
+}
+
+// ------------------------------------------------------------ block norms
+
+struct NormArgs {
+    int D, post, act;
+    long long rows;
+    float scale, eps, inv_d;
+    const void* y;
+    const void* gate;
+    const void* res;
+    const float* post_w;
+    const float* pre_w;
+    void* h;
+    void* x;
+};
+
+// The row's values in fp32 across a group of threads, VPT vectors of eight
+// each; sum() adds over the group.
+template <typename IO, typename RES, int VPT, class Sum>
+__device__ __forceinline__ void norm_row(const NormArgs& a, long long row, int first, int step, bool live, Sum&& sum)
+{
+    const int nv = a.D / 8;
+    const size_t base = (size_t)row * a.D;
+    const IO* y = static_cast<const IO*>(a.y) + base;
+    const IO* g = static_cast<const IO*>(a.gate) + base;
+    const RES* res = static_cast<const RES*>(a.res) + base;
+    Vec8<IO> yv[VPT], gv[VPT];
+    Vec8<RES> rv[VPT];
+    // every load of the row first
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int v = first + j * step;
+        const bool in = live && v < nv;
+        if (in) yv[j].load(y + v * 8);
+        else yv[j].zero();
+        if (a.act != KDA_NORM_GATE_NONE && in) gv[j].load(g + v * 8);
+        else gv[j].zero();
+        if (a.res && in) rv[j].load(res + v * 8);
+        else rv[j].zero();
+    }
+    float t[VPT][8];
+    float ss = 0.f;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        yv[j].get(t[j]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss = fmaf(t[j][i], t[j][i], ss);
+    }
+    const float post = a.post ? rsqrtf(sum(ss) * a.inv_d + a.eps) : 1.f;
+    ss = 0.f;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int v = first + j * step;
+        const bool in = live && v < nv;
+        float w[8], gx[8], rx[8];
+        if (a.post && a.post_w && in) {
+            Vec8<float> wv;
+            wv.load(a.post_w + v * 8);
+            wv.get(w);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = 1.f;
+        }
+        gv[j].get(gx);
+        rv[j].get(rx);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float z = t[j][i] * post * w[i];
+            if (a.act == KDA_NORM_GATE_SIGMOID) z *= sigmoidf_(gx[i]);
+            else if (a.act == KDA_NORM_GATE_SILU) z *= siluf_(gx[i]);
+            z *= a.scale;
+            if (a.res) z += rx[i];
+            t[j][i] = in ? z : 0.f;
+            ss = fmaf(t[j][i], t[j][i], ss);
+        }
+        if (a.h && in) {
+            Vec8<RES> o;
+            o.set(t[j]);
+            o.store(static_cast<RES*>(a.h) + base + v * 8);
+        }
+    }
+    if (!a.x) return;
+    const float pre = rsqrtf(sum(ss) * a.inv_d + a.eps);
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int v = first + j * step;
+        if (!(live && v < nv)) continue;
+        float w[8];
+        if (a.pre_w) {
+            Vec8<float> wv;
+            wv.load(a.pre_w + v * 8);
+            wv.get(w);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = 1.f;
+        }
+        float o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = t[j][i] * pre * w[i];
+        Vec8<IO> ov;
+        ov.set(o);
+        ov.store(static_cast<IO*>(a.x) + base + v * 8);
+    }
+}
+
+// Rows of up to 1024 values: a power of two of lanes for each.
+template <typename IO, typename RES, int VPT>
+__global__ void __launch_bounds__(128) norm_warp_kernel(const NormArgs a, int lanes)
+{
+    const int lane = threadIdx.x & 31, per_warp = 32 / lanes;
+    const long long row = ((long long)blockIdx.x * 4 + (threadIdx.x >> 5)) * per_warp + lane / lanes;
+    norm_row<IO, RES, VPT>(a, row < a.rows ? row : 0, lane % lanes, lanes, row < a.rows, [&](float s) {
+        for (int o = lanes >> 1; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        return s;
+    });
+}
+
+// Longer rows: a CTA for each.
+template <typename IO, typename RES, int VPT>
+__global__ void __launch_bounds__(512) norm_block_kernel(const NormArgs a)
+{
+    __shared__ float part[2][16];
+    int turn = 0;
+    norm_row<IO, RES, VPT>(a, blockIdx.x, threadIdx.x, blockDim.x, true, [&](float s) {
+        s = warp_sum(s);
+        float* p = part[turn++];
+        if ((threadIdx.x & 31) == 0) p[threadIdx.x >> 5] = s;
+        __syncthreads();
+        s = 0.f;
+        for (int w = 0; w < (int)(blockDim.x >> 5); ++w) s += p[w];
+        return s;
+    });
+}
+
+template <typename IO, typename RES> void launch_norm(const NormArgs& a, cudaStream_t st)
+{
+    const int nv = a.D / 8;
+    if (nv <= 128) {
+        int lanes = 1;
+        while (lanes < nv && lanes < 32) lanes <<= 1;
+        const long long per_cta = 4 * (32 / lanes);
+        const unsigned g = (unsigned)((a.rows + per_cta - 1) / per_cta);
+        if (nv <= 32) norm_warp_kernel<IO, RES, 1><<<g, 128, 0, st>>>(a, lanes);
+        else if (nv <= 64) norm_warp_kernel<IO, RES, 2><<<g, 128, 0, st>>>(a, lanes);
+        else norm_warp_kernel<IO, RES, 4><<<g, 128, 0, st>>>(a, lanes);
+        return;
+    }
+    const unsigned g = (unsigned)a.rows;
+    auto threads = [&](int vpt) { return ((nv + vpt - 1) / vpt + 31) / 32 * 32; };
+    if (nv <= 1024) norm_block_kernel<IO, RES, 2><<<g, threads(2), 0, st>>>(a);
+    else norm_block_kernel<IO, RES, 4><<<g, threads(4), 0, st>>>(a);
+}
+
+}  // namespace
+}  // namespace kda
+
+using namespace kda;
+
+extern "C" {
+
+KDA_API int kda_conv_varlen(const kda_conv_params* p, const int32_t* cu_seqlens, int32_t N, int32_t T, const void* x,
+                            const int32_t* slots, void* conv_state, void* y, int32_t* dev_status,
+                            cudaStream_t stream)
+{
+    int rc = check_conv(p);
+    if (rc != KDA_OK) return rc;
+    if (N < 0 || T < 0) return KDA_ERR_INVALID_ARGUMENT;
+    if (N == 0 || T == 0) return KDA_OK;
+    if ((rc = check_ptrs({cu_seqlens})) != KDA_OK) return rc;
+    return conv_call(p, cu_seqlens, N, T, x, slots, conv_state, y, dev_status, true, stream);
+}
+
+KDA_API int kda_conv_decode(const kda_conv_params* p, int32_t B, const void* x, const int32_t* slots,
+                            void* conv_state, void* y, int32_t* dev_status, cudaStream_t stream)
+{
+    int rc = check_conv(p);
+    if (rc != KDA_OK) return rc;
+    if (B < 0) return KDA_ERR_INVALID_ARGUMENT;
+    if (B == 0) return KDA_OK;
+    return conv_call(p, nullptr, B, B, x, slots, conv_state, y, dev_status, false, stream);
+}
+
+KDA_API int kda_block_norm(const kda_norm_params* p, int64_t rows, const void* y, const void* gate,
+                           const void* residual, void* h_out, void* x_out, cudaStream_t stream)
+{
+    if (!p || rows < 0) return KDA_ERR_INVALID_ARGUMENT;
+    if (p->dim <= 0) return KDA_ERR_INVALID_ARGUMENT;
+    if (p->dim % 8 != 0 || p->dim > 16384) return KDA_ERR_UNSUPPORTED_GEOMETRY;
+    if ((p->post_norm != 0 && p->post_norm != 1) || p->gate_act < KDA_NORM_GATE_NONE || p->gate_act > KDA_NORM_GATE_SILU)
+        return KDA_ERR_INVALID_ARGUMENT;
+    if (!std::isfinite(p->residual_scale) || !(std::isfinite(p->norm_eps) && p->norm_eps >= 0.0f))
+        return KDA_ERR_INVALID_ARGUMENT;
+    if (!known_dtype(p->io_dtype) || !known_dtype(p->res_dtype)) return KDA_ERR_INVALID_ARGUMENT;
+    int rc;
+    if ((rc = check_opt(p->post_weight)) != KDA_OK || (rc = check_opt(p->pre_weight)) != KDA_OK) return rc;
+    if (rows == 0) return KDA_OK;
+    if (rows > INT32_MAX) return KDA_ERR_INVALID_ARGUMENT;
+    if ((rc = check_ptrs({y})) != KDA_OK) return rc;
+    if (p->gate_act != KDA_NORM_GATE_NONE && (rc = check_ptrs({gate})) != KDA_OK) return rc;
+    if ((rc = check_opt(residual)) != KDA_OK || (rc = check_opt(h_out)) != KDA_OK || (rc = check_opt(x_out)) != KDA_OK)
+        return rc;
+    if (!h_out && !x_out) return KDA_ERR_INVALID_ARGUMENT;
+    if (p->gate_act == KDA_NORM_GATE_NONE) gate = nullptr;
+    const size_t io = (size_t)rows * p->dim * io_size(p->io_dtype), rs = (size_t)rows * p->dim * io_size(p->res_dtype);
+    // in place is the very buffer, of one type; anything else that overlaps is refused
+    auto clash = [](const void* out, size_t no, const void* in, size_t ni) {
+        return overlap(out, no, in, ni) && !(out == in && no == ni);
+    };
+    if (clash(h_out, rs, y, io) || clash(h_out, rs, gate, io) || clash(h_out, rs, residual, rs) ||
+        clash(x_out, io, y, io) || clash(x_out, io, gate, io) || clash(x_out, io, residual, rs) ||
+        overlap(h_out, rs, x_out, io))
+        return KDA_ERR_INVALID_ARGUMENT;
+    for (const float* w : {p->post_weight, p->pre_weight})
+        if (overlap(h_out, rs, w, p->dim * sizeof(float)) || overlap(x_out, io, w, p->dim * sizeof(float)))
+            return KDA_ERR_INVALID_ARGUMENT;
+    if ((rc = check_device()) != KDA_OK) return rc;
+    NormArgs a;
+    a.D = p->dim;
+    a.post = p->post_norm;
+    a.act = p->gate_act;
+    a.rows = rows;
+    a.scale = p->residual_scale;
+    a.eps = p->norm_eps;
+    a.inv_d = 1.0f / (float)p->dim;
+    a.y = y;
+    a.gate = gate;
+    a.res = residual;
+    a.post_w = p->post_weight;
+    a.pre_w = p->pre_weight;
+    a.h = h_out;
+    a.x = x_out;
+    const bool iob = p->io_dtype == KDA_DTYPE_BF16, rsb = p->res_dtype == KDA_DTYPE_BF16;
+    if (iob && rsb) launch_norm<__nv_bfloat16, __nv_bfloat16>(a, stream);
+    else if (iob) launch_norm<__nv_bfloat16, float>(a, stream);
+    else if (rsb) launch_norm<float, __nv_bfloat16>(a, stream);
+    else launch_norm<float, float>(a, stream);
+    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_LAUNCH;
+}
+
+}  // extern "C"

@@ -34,6 +34,10 @@ KDA_DTYPE_F32 = 0
 KDA_DTYPE_BF16 = 1
 KDA_GATE_SOFTPLUS = 0
 KDA_GATE_SAFE = 1
+KDA_NORM_GATE_NONE = 0
+KDA_NORM_GATE_SIGMOID = 1
+KDA_NORM_GATE_SILU = 2
+KDA_MAX_POOL_SLOTS = 262144
 
 
 class kda_params(ctypes.Structure):
@@ -46,6 +50,39 @@ class kda_params(ctypes.Structure):
         ("out_dtype", ctypes.c_int32), ("num_slots", ctypes.c_int32),
         ("A_log", ctypes.c_void_p), ("dt_bias", ctypes.c_void_p),
         ("conv_weight", ctypes.c_void_p), ("norm_weight", ctypes.c_void_p),
+    ]
+
+
+class kda_gdn_params(ctypes.Structure):
+    _fields_ = [
+        ("num_heads_k", ctypes.c_int32), ("num_heads_v", ctypes.c_int32),
+        ("head_dim_k", ctypes.c_int32), ("head_dim_v", ctypes.c_int32),
+        ("l2_norm", ctypes.c_int32), ("l2_eps", ctypes.c_float), ("scale", ctypes.c_float),
+        ("io_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("num_slots", ctypes.c_int32),
+        ("q_row_stride", ctypes.c_int64), ("k_row_stride", ctypes.c_int64), ("v_row_stride", ctypes.c_int64),
+        ("A_log", ctypes.c_void_p), ("dt_bias", ctypes.c_void_p),
+    ]
+
+
+class kda_conv_params(ctypes.Structure):
+    _fields_ = [
+        ("channels", ctypes.c_int32), ("conv_kernel", ctypes.c_int32), ("io_dtype", ctypes.c_int32),
+        ("num_slots", ctypes.c_int32), ("conv_weight", ctypes.c_void_p),
+    ]
+
+
+class kda_norm_params(ctypes.Structure):
+    _fields_ = [
+        ("dim", ctypes.c_int32), ("post_norm", ctypes.c_int32), ("gate_act", ctypes.c_int32),
+        ("residual_scale", ctypes.c_float), ("norm_eps", ctypes.c_float), ("io_dtype", ctypes.c_int32),
+        ("res_dtype", ctypes.c_int32), ("post_weight", ctypes.c_void_p), ("pre_weight", ctypes.c_void_p),
+    ]
+
+
+class kda_slot_pool(ctypes.Structure):
+    _fields_ = [
+        ("pool", ctypes.c_void_p), ("layer_stride_bytes", ctypes.c_int64), ("slot_bytes", ctypes.c_int64),
+        ("num_layers", ctypes.c_int32), ("num_slots", ctypes.c_int32),
     ]
 
 
@@ -73,6 +110,16 @@ _SIG = {
     "kda_commit_verify": (ctypes.c_int, [ctypes.POINTER(kda_params), _I32, _I32] + [_VP] * 14 + [_VP]),
     "kda_commit": (ctypes.c_int, [ctypes.POINTER(kda_params), _I32, _I32, _VP, _VP, _VP, _VP, _VP,
                                   _VP, _VP]),
+    "kda_gdn_prefill_varlen": (ctypes.c_int, [ctypes.POINTER(kda_gdn_params), _VP, _I32, _I32] + [_VP] * 9 +
+                               [ctypes.c_size_t, _VP, _VP]),
+    "kda_gdn_prefill_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(kda_gdn_params), _I32, _I32]),
+    "kda_gdn_decode": (ctypes.c_int, [ctypes.POINTER(kda_gdn_params), _I32] + [_VP] * 9 + [_VP]),
+    "kda_conv_varlen": (ctypes.c_int, [ctypes.POINTER(kda_conv_params), _VP, _I32, _I32] + [_VP] * 6),
+    "kda_conv_decode": (ctypes.c_int, [ctypes.POINTER(kda_conv_params), _I32] + [_VP] * 6),
+    "kda_block_norm": (ctypes.c_int, [ctypes.POINTER(kda_norm_params), ctypes.c_int64] + [_VP] * 6),
+    "kda_slots_copy": (ctypes.c_int, [ctypes.POINTER(kda_slot_pool), _I32] + [_VP] * 4),
+    "kda_slots_zero": (ctypes.c_int, [ctypes.POINTER(kda_slot_pool), _I32] + [_VP] * 3),
+    "kda_slots_compact_plan": (ctypes.c_int, [ctypes.POINTER(kda_slot_pool)] + [_VP] * 5),
     "kda_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "kda_abi_version": (ctypes.c_int, []),
 }
@@ -143,6 +190,86 @@ class Params:
             out_dtype=self.out_dtype, num_slots=self.num_slots,
             A_log=_ptr(self.A_log), dt_bias=_ptr(self.dt_bias),
             conv_weight=_ptr(self.conv_weight), norm_weight=_ptr(self.norm_weight))
+
+
+@dataclass
+class GdnParams:
+    """Heads of the gated delta rule with one decay per head (kda_gdn_params)."""
+
+    num_heads_k: int
+    num_heads_v: int
+    head_dim_k: int
+    head_dim_v: int
+    A_log: object
+    dt_bias: object
+    l2_norm: bool = True
+    l2_eps: float = 1e-6
+    scale: float = 1.0
+    io_dtype: int = KDA_DTYPE_BF16
+    out_dtype: int = KDA_DTYPE_BF16
+    num_slots: int = 1
+    q_row_stride: int = 0
+    k_row_stride: int = 0
+    v_row_stride: int = 0
+
+    def c_struct(self) -> kda_gdn_params:
+        return kda_gdn_params(
+            num_heads_k=self.num_heads_k, num_heads_v=self.num_heads_v, head_dim_k=self.head_dim_k,
+            head_dim_v=self.head_dim_v, l2_norm=int(self.l2_norm), l2_eps=self.l2_eps, scale=self.scale,
+            io_dtype=self.io_dtype, out_dtype=self.out_dtype, num_slots=self.num_slots,
+            q_row_stride=self.q_row_stride, k_row_stride=self.k_row_stride, v_row_stride=self.v_row_stride,
+            A_log=_ptr(self.A_log), dt_bias=_ptr(self.dt_bias))
+
+
+@dataclass
+class ConvParams:
+    """A causal depthwise convolution with SiLU (kda_conv_params)."""
+
+    channels: int
+    conv_kernel: int
+    conv_weight: object
+    io_dtype: int = KDA_DTYPE_BF16
+    num_slots: int = 1
+
+    def c_struct(self) -> kda_conv_params:
+        return kda_conv_params(channels=self.channels, conv_kernel=self.conv_kernel, io_dtype=self.io_dtype,
+                               num_slots=self.num_slots, conv_weight=_ptr(self.conv_weight))
+
+
+@dataclass
+class NormParams:
+    """The norms around a block (kda_norm_params)."""
+
+    dim: int
+    post_norm: bool = True
+    gate_act: int = KDA_NORM_GATE_NONE
+    residual_scale: float = 1.0
+    norm_eps: float = 1e-6
+    post_weight: object = None
+    pre_weight: object = None
+    io_dtype: int = KDA_DTYPE_BF16
+    res_dtype: int = KDA_DTYPE_BF16
+
+    def c_struct(self) -> kda_norm_params:
+        return kda_norm_params(
+            dim=self.dim, post_norm=int(self.post_norm), gate_act=self.gate_act, residual_scale=self.residual_scale,
+            norm_eps=self.norm_eps, io_dtype=self.io_dtype, res_dtype=self.res_dtype,
+            post_weight=_ptr(self.post_weight), pre_weight=_ptr(self.pre_weight))
+
+
+@dataclass
+class SlotPool:
+    """A pool of state slots over layers (kda_slot_pool)."""
+
+    pool: object
+    num_layers: int
+    num_slots: int
+    slot_bytes: int
+    layer_stride_bytes: int
+
+    def c_struct(self) -> kda_slot_pool:
+        return kda_slot_pool(pool=_ptr(self.pool), layer_stride_bytes=self.layer_stride_bytes,
+                             slot_bytes=self.slot_bytes, num_layers=self.num_layers, num_slots=self.num_slots)
 
 
 def _ptr(t):
@@ -256,6 +383,63 @@ def kda_commit_verify(params: Params, B: int, W: int, accepted, log_prev, q, k, 
         _ptr(out), _ptr(dev_status), _stream(stream))
 
 
+def kda_gdn_prefill_workspace_bytes(params: GdnParams, N: int, T: int) -> int:
+    return load().kda_gdn_prefill_workspace_bytes(ctypes.byref(params.c_struct()), N, T)
+
+
+def kda_gdn_prefill_varlen(params: GdnParams, cu_seqlens, N: int, T: int, q, k, v, gate, beta, slots, rec_state, out,
+                           workspace=None, ws_bytes: int = 0, dev_status=None, stream=None) -> int:
+    """Prompt rows through the gated delta rule with one decay per head."""
+    return load().kda_gdn_prefill_varlen(
+        ctypes.byref(params.c_struct()), _ptr(cu_seqlens), N, T, _ptr(q), _ptr(k), _ptr(v), _ptr(gate), _ptr(beta),
+        _ptr(slots), _ptr(rec_state), _ptr(out), _ptr(workspace), ws_bytes, _ptr(dev_status), _stream(stream))
+
+
+def kda_gdn_decode(params: GdnParams, B: int, q, k, v, gate, beta, slots, rec_state, out, dev_status=None,
+                   stream=None) -> int:
+    """One row per sequence through the gated delta rule with one decay per head."""
+    return load().kda_gdn_decode(
+        ctypes.byref(params.c_struct()), B, _ptr(q), _ptr(k), _ptr(v), _ptr(gate), _ptr(beta), _ptr(slots),
+        _ptr(rec_state), _ptr(out), _ptr(dev_status), _stream(stream))
+
+
+def kda_conv_varlen(params: ConvParams, cu_seqlens, N: int, T: int, x, slots, conv_state, y, dev_status=None,
+                    stream=None) -> int:
+    """Causal depthwise convolution with carried state and SiLU over prompt rows."""
+    return load().kda_conv_varlen(ctypes.byref(params.c_struct()), _ptr(cu_seqlens), N, T, _ptr(x), _ptr(slots),
+                                  _ptr(conv_state), _ptr(y), _ptr(dev_status), _stream(stream))
+
+
+def kda_conv_decode(params: ConvParams, B: int, x, slots, conv_state, y, dev_status=None, stream=None) -> int:
+    """The same for one row per sequence."""
+    return load().kda_conv_decode(ctypes.byref(params.c_struct()), B, _ptr(x), _ptr(slots), _ptr(conv_state), _ptr(y),
+                                  _ptr(dev_status), _stream(stream))
+
+
+def kda_block_norm(params: NormParams, rows: int, y, gate=None, residual=None, h_out=None, x_out=None,
+                   stream=None) -> int:
+    """Norm after a block with its gate, scaled residual, norm before the next block."""
+    return load().kda_block_norm(ctypes.byref(params.c_struct()), rows, _ptr(y), _ptr(gate), _ptr(residual),
+                                 _ptr(h_out), _ptr(x_out), _stream(stream))
+
+
+def kda_slots_copy(pool: SlotPool, n: int, src, dst, dev_status=None, stream=None) -> int:
+    """Copies slot src[i] to slot dst[i] in every layer of the pool."""
+    return load().kda_slots_copy(ctypes.byref(pool.c_struct()), n, _ptr(src), _ptr(dst), _ptr(dev_status),
+                                 _stream(stream))
+
+
+def kda_slots_zero(pool: SlotPool, n: int, slots, dev_status=None, stream=None) -> int:
+    """Zeroes slots in every layer of the pool."""
+    return load().kda_slots_zero(ctypes.byref(pool.c_struct()), n, _ptr(slots), _ptr(dev_status), _stream(stream))
+
+
+def kda_slots_compact_plan(pool: SlotPool, live, src, dst, remap, stream=None) -> int:
+    """The moves (for kda_slots_copy) that close the holes of a pool."""
+    return load().kda_slots_compact_plan(ctypes.byref(pool.c_struct()), _ptr(live), _ptr(src), _ptr(dst), _ptr(remap),
+                                         _stream(stream))
+
+
 class Prepared:
     """A call of one entry point with its arguments marshalled once.
 
@@ -263,7 +447,7 @@ class Prepared:
     the same pointers every time (the tensors must stay alive and in place).
     """
 
-    def __init__(self, name: str, params: Params, *args, stream=None):
+    def __init__(self, name: str, params, *args, stream=None):
         self.fn = getattr(load(), name)
         self.pstruct = params.c_struct()
         conv = []

@@ -1,0 +1,377 @@
+"""The gated delta rule with one decay per head on the GPU, against its
+definition in 64 bits.
+
+Tolerances (2-norm, relative), from the roundings on the way:
+  - fp32 results.  An operand split into two fp16 values is off by 2^-22 of
+    the largest value of its 16-term tile column at most, a gate's exponential by
+    2 ulp plus its argument's rounding (about 2^-22 for |G| up to 4), an fp32
+    accumulation of n terms by about sqrt(n) 2^-24.  A handful of these in a row: STATE = 2^-18.
+  - bf16 outputs: half a step is 2^-8 of the value, and the high fp16 parts
+    (2^-11 of the operands) of S, U and P in front of it: OUT = 2^-8 + 2^-10.
+  - fp32 rows and the single-token form run in fp32 throughout: 2^-20.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from linear_attention_serving_kda_gb300.runtime import Guarded
+from tests import plain64 as P
+
+pytestmark = pytest.mark.gpu
+
+STATE, OUT, FP32 = 2.0 ** -18, 2.0 ** -8 + 2.0 ** -10, 2.0 ** -20
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+class Case:
+    """Rows of q|k|v side by side, guarded outputs and states on the GPU, and the 64-bit arrays of the same values."""
+
+    def __init__(self, lens, Hk=2, Hv=4, dk=128, dv=128, io="bf16", out="bf16", seed=0, slots=None, num_slots=None,
+                 l2=True, scale=None, dense=False, gate=0.0, dt=None, beta=0.0, spread=1.0):
+        r = np.random.default_rng(seed)
+        self.lens, self.T, self.N = list(lens), int(sum(lens)), len(lens)
+        self.Hk, self.Hv, self.dk, self.dv, self.io, self.out_t, self.l2 = Hk, Hv, dk, dv, io, out, l2
+        self.scale = dk ** -0.5 if scale is None else scale
+        T = max(self.T, 1)
+        x = r.standard_normal((T, 2 * Hk * dk + Hv * dv))
+        x = x / (1 + np.exp(-x)) * spread
+        self.rows = torch.from_numpy(x).to(DT[io]).cuda()
+        if not l2:  # unit keys, as a caller without the option passes them
+            kq = self.rows[:, :2 * Hk * dk].float().reshape(T, 2 * Hk, dk)
+            self.rows[:, :2 * Hk * dk] = (kq / kq.norm(dim=-1, keepdim=True)).reshape(T, -1).to(DT[io])
+        w = [Hk * dk, Hk * dk, Hv * dv]
+        parts = self.rows.split(w, 1)
+        self.stride = 0 if dense else self.rows.shape[1]
+        self.q, self.k, self.v = (p.contiguous() for p in parts) if dense else parts
+        self.a = torch.from_numpy(r.standard_normal((T, Hv)) + gate).to(DT[io]).cuda()
+        self.b = torch.from_numpy(r.standard_normal((T, Hv)) + beta).to(DT[io]).cuda()
+        self.A_log = torch.from_numpy(np.log(r.uniform(1, 16, Hv))).float().cuda()
+        step = np.exp(r.uniform(math.log(1e-3), math.log(1e-1), Hv))
+        self.dt_bias = torch.from_numpy(np.log(np.expm1(step)) if dt is None else np.full(Hv, dt)).float().cuda()
+        self.slots_h = list(range(self.N)) if slots is None else list(slots)
+        self.slots = None if slots is None else torch.tensor(slots, dtype=torch.int32, device="cuda")
+        self.num_slots = num_slots or max(self.N, 1)
+        self.state0 = torch.from_numpy(r.standard_normal((self.num_slots, Hv, dk, dv)) * 0.1).float().cuda()
+        self.g_state = Guarded(self.state0.shape, torch.float32, "cuda")
+        self.g_out = Guarded((T, Hv, dv), DT[out], "cuda")
+        self.status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        self.cu = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+        self.reset()
+
+    def reset(self):
+        self.g_state.tensor.copy_(self.state0)
+        self.g_out.tensor.fill_(7.0)
+
+    def params(self, kda):
+        code = {"bf16": kda.KDA_DTYPE_BF16, "f32": kda.KDA_DTYPE_F32}
+        return kda.GdnParams(num_heads_k=self.Hk, num_heads_v=self.Hv, head_dim_k=self.dk, head_dim_v=self.dv,
+                             A_log=self.A_log, dt_bias=self.dt_bias, l2_norm=self.l2, scale=self.scale,
+                             io_dtype=code[self.io], out_dtype=code[self.out_t], num_slots=self.num_slots,
+                             q_row_stride=self.stride, k_row_stride=self.stride, v_row_stride=self.stride)
+
+    def prefill(self, kda, r0=0, lens=None, stream=None):
+        """The call over sequences of `lens` starting at row r0 (default: all)."""
+        lens = self.lens if lens is None else lens
+        cu = self.cu if lens is self.lens else torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+        p, T = self.params(kda), int(sum(lens))
+        need = kda.kda_gdn_prefill_workspace_bytes(p, len(lens), T)
+        ws = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
+        kda.check(kda.kda_gdn_prefill_varlen(p, cu, len(lens), T, self.q[r0:], self.k[r0:], self.v[r0:], self.a[r0:].clone(),
+                                             self.b[r0:].clone(), self.slots, self.g_state.tensor,
+                                             self.g_out.tensor[r0:], ws, need, self.status, stream))
+        torch.cuda.synchronize()
+
+    def decode(self, kda, stream=None):
+        kda.check(kda.kda_gdn_decode(self.params(kda), self.N, self.q, self.k, self.v, self.a, self.b, self.slots,
+                                     self.g_state.tensor, self.g_out.tensor, self.status, stream))
+        torch.cuda.synchronize()
+
+    def want(self):
+        T = self.T
+        f = lambda x, *s: x[:T].double().cpu().numpy().reshape(T, *s)  # noqa: E731
+        return P.gdn(self.lens, f(self.q, self.Hk, self.dk), f(self.k, self.Hk, self.dk), f(self.v, self.Hv, self.dv),
+                     f(self.a, self.Hv), f(self.b, self.Hv), self.A_log.double().cpu().numpy(),
+                     self.dt_bias.double().cpu().numpy(), self.state0.double().cpu().numpy(), self.slots_h, self.scale, self.l2)
+
+    def check(self, tol_out=None, tol_state=None, status=0):
+        out, state = self.want()
+        chunk = self.io == "bf16"
+        tol_out = tol_out or (OUT if self.out_t == "bf16" else STATE if chunk else FP32)
+        tol_state = tol_state or (STATE if chunk else FP32)
+        got_o, got_s = self.g_out.tensor[:self.T].double().cpu().numpy(), self.g_state.tensor.double().cpu().numpy()
+        assert np.isfinite(got_o).all() and np.isfinite(got_s).all()
+        eo, es = P.rel(got_o, out), P.rel(got_s, state)
+        assert es <= tol_state, f"state off by {es:.3g}"
+        assert eo <= tol_out, f"out off by {eo:.3g}"
+        assert (got_o[np.isnan(out)] == 7.0).all()  # rows that are nobody's stay as they were
+        assert int(self.status.item()) == status
+        assert self.g_state.intact() and self.g_out.intact()
+        return eo, es
+
+
+@pytest.mark.parametrize("lens", [[1], [2], [15], [16], [17], [63], [64], [65], [127], [128], [129], [193], [320],
+                                  [1, 0, 130, 64, 0, 7], [0, 0, 5]])
+def test_prefill_lengths(cuda_lib, lens):
+    c = Case(lens, seed=sum(lens))
+    c.prefill(cuda_lib)
+    c.check()
+
+
+@pytest.mark.parametrize("io,out", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
+@pytest.mark.parametrize("dk,dv", [(32, 32), (32, 128), (64, 64), (128, 32), (128, 64), (64, 128), (128, 128)])
+def test_prefill_types_and_widths(cuda_lib, dk, dv, io, out):
+    c = Case([70, 1, 150], dk=dk, dv=dv, io=io, out=out, seed=dk + dv)
+    c.prefill(cuda_lib)
+    c.check()
+
+
+@pytest.mark.parametrize("Hk,Hv", [(1, 1), (1, 4), (3, 3), (3, 6), (5, 20)])
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_prefill_head_groups(cuda_lib, Hk, Hv, io):
+    c = Case([100, 30], Hk=Hk, Hv=Hv, dk=64, dv=64, io=io, out="f32", seed=Hv)
+    c.prefill(cuda_lib)
+    c.check()
+
+
+@pytest.mark.parametrize("heads", [1, 40])
+def test_prefill_both_cta_widths(cuda_lib, heads):
+    """Few chains take two chain warps a CTA, many take four: the same bits."""
+    c = Case([200, 90], Hk=heads, Hv=heads, seed=3)
+    c.prefill(cuda_lib)
+    c.check()
+    if heads == 1:
+        return
+    one = Case([200, 90], Hk=heads, Hv=heads, seed=3)
+    one.q, one.k, one.v = (x[:, :128] for x in (one.q, one.k, one.v))
+    one.a, one.b = one.a[:, :1].contiguous(), one.b[:, :1].contiguous()
+    one.Hk = one.Hv = 1
+    one.state0 = one.state0[:, :1].contiguous()
+    one.g_state, one.g_out = Guarded(one.state0.shape, torch.float32, "cuda"), Guarded((290, 1, 128), torch.bfloat16, "cuda")
+    one.reset()
+    one.prefill(cuda_lib)
+    assert torch.equal(one.g_out.tensor[:, 0], c.g_out.tensor[:, 0])
+    assert torch.equal(one.g_state.tensor[:, 0], c.g_state.tensor[:, 0])
+
+
+@pytest.mark.parametrize("dense", [False, True])
+def test_prefill_strides(cuda_lib, dense):
+    c = Case([90, 41], dense=dense, seed=8)
+    c.prefill(cuda_lib)
+    c.check()
+
+
+@pytest.mark.parametrize("io,out", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
+def test_prefill_without_l2_norm(cuda_lib, io, out):
+    c = Case([130, 65], l2=False, io=io, out=out, seed=9)
+    c.prefill(cuda_lib)
+    c.check()
+
+
+@pytest.mark.parametrize("kw", [
+    dict(gate=-30.0),                  # no decay at all
+    dict(gate=30.0, dt=5.0),           # every row forgets everything
+    dict(gate=1e30, dt=0.0),           # an infinite log decay is a clean reset
+    dict(gate=2.0, dt=1.0),            # strong decays: sums far below zero within a chunk
+    dict(beta=12.0, gate=-30.0),       # beta near one: full corrections
+    dict(beta=-25.0),                  # beta near zero: the state hardly takes anything
+    dict(spread=1e-12), dict(spread=1e12),
+], ids=str)
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_prefill_gates_and_ranges(cuda_lib, kw, io):
+    c = Case([150, 64], seed=11, io=io, out="f32", **kw)
+    if kw.get("spread"):
+        c.state0 *= kw["spread"]
+        c.reset()
+    c.prefill(cuda_lib)
+    c.check(tol_out=2 * STATE)
+
+
+def test_prefill_mixed_decays(cuda_lib):
+    """Rows that reset the state between rows that keep it: a row's reset may
+    not cost the digits of the small decays after it."""
+    c = Case([200], Hk=2, Hv=2, seed=12, out="f32")
+    c.a[::3] = 60.0
+    c.a[1::3] = -4.0
+    c.prefill(cuda_lib)
+    c.check()
+
+
+def test_prefill_correlated_keys(cuda_lib):
+    """Nearly equal keys: I + A is far from the identity."""
+    c = Case([256], Hk=2, Hv=2, seed=13, out="f32", beta=3.0, gate=-10.0)
+    c.k[:] = c.k[:1] + 0.05 * c.k
+    c.prefill(cuda_lib)
+    c.check(tol_out=2.0 ** -16, tol_state=2.0 ** -16)  # products of the 64 corrections, each 2^-22 off
+
+
+def test_prefill_slots(cuda_lib):
+    """A pool larger than the batch, a padded sequence, a slot out of range:
+    what is nobody's stays as it was."""
+    c = Case([40, 70, 5, 130], slots=[5, -1, 0, 3], num_slots=7, seed=14)
+    c.prefill(cuda_lib)
+    c.check()
+    bad = Case([40, 70], slots=[7, 2], num_slots=7, seed=15)
+    bad.slots_h = [-1, 2]
+    bad.prefill(cuda_lib)
+    bad.check(status=cuda_lib.KDA_DEV_BAD_SLOT)
+
+
+def test_prefill_bad_cu_seqlens(cuda_lib):
+    c = Case([50, 60, 40], seed=16)
+    c.cu[2] = 40       # sequence 1 would run backwards, sequence 2 from 40 to 150
+    c.prefill(cuda_lib)
+    assert int(c.status.item()) == cuda_lib.KDA_DEV_BAD_SEQLENS
+    assert torch.equal(c.g_state.tensor[1], c.state0[1])
+    c = Case([50, 60], seed=16)
+    c.cu[2] = 111      # past the last row
+    c.prefill(cuda_lib)
+    assert int(c.status.item()) == cuda_lib.KDA_DEV_BAD_SEQLENS
+    assert torch.equal(c.g_state.tensor[1], c.state0[1]) and (c.g_out.tensor[50:] == 7.0).all()
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("cuts", [(64, 128, 108), (1, 99, 200)])
+def test_prefill_in_pieces(cuda_lib, out, cuts):
+    c = Case([300], seed=17, out=out)
+    r0 = 0
+    for ln in cuts:
+        c.prefill(cuda_lib, r0, [ln])
+        r0 += ln
+    c.check()
+
+
+def test_prefill_nan_stays_in_its_sequence_and_head(cuda_lib):
+    c = Case([70, 70], Hk=2, Hv=2, seed=18)
+    clean = Case([70, 70], Hk=2, Hv=2, seed=18)
+    clean.prefill(cuda_lib)
+    c.v[80, 5] = float("nan")     # sequence 1, head 0, column 5
+    c.q[10, 3] = float("inf")     # sequence 0, head 0: its row alone
+    c.prefill(cuda_lib)
+    a, b = c.g_out.tensor, clean.g_out.tensor
+    keep = torch.ones_like(a, dtype=torch.bool)
+    keep[10, 0] = False
+    keep[70:, 0, 5] = False
+    assert torch.equal(a[keep], b[keep])
+    assert torch.equal(c.g_state.tensor[0], clean.g_state.tensor[0])
+    assert a[10, 0].isnan().all() and a[80:, 0, 5].isnan().all()
+
+
+def test_prefill_many_sequences(cuda_lib):
+    """More sequences than threads of a CTA: they keep their order."""
+    r = np.random.default_rng(1)
+    lens = r.integers(0, 6, 300).tolist()
+    c = Case(lens, Hk=1, Hv=1, dk=32, dv=32, seed=19)
+    c.prefill(cuda_lib)
+    c.check()
+
+
+@pytest.mark.parametrize("B", [1, 2, 7, 33])
+@pytest.mark.parametrize("io,out", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
+@pytest.mark.parametrize("dk,dv", [(128, 128), (32, 64), (64, 32), (128, 32), (32, 128)])
+def test_decode(cuda_lib, B, io, out, dk, dv):
+    c = Case([1] * B, Hk=2, Hv=6, dk=dk, dv=dv, io=io, out=out, seed=B + dk)
+    c.decode(cuda_lib)
+    c.check(tol_out=2.0 ** -8 if out == "bf16" else FP32, tol_state=FP32)
+
+
+def test_decode_large_batch_slots(cuda_lib):
+    c = Case([1] * 40, Hk=4, Hv=8, slots=[-1] + list(range(41, 2, -1)), num_slots=42, seed=20)
+    c.decode(cuda_lib)
+    c.check(tol_out=2.0 ** -8, tol_state=FP32)
+    bad = Case([1] * 3, slots=[1, 9, 0], num_slots=3, seed=21)
+    bad.slots_h = [1, -1, 0]
+    bad.decode(cuda_lib)
+    bad.check(tol_out=2.0 ** -8, tol_state=FP32, status=cuda_lib.KDA_DEV_BAD_SLOT)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_prefill_then_decode(cuda_lib, io):
+    """A prompt's rows cut after any row: prefill, then single tokens, is one recurrence."""
+    lens, tail = [70, 33], 3
+    c = Case(lens, io=io, out="f32", seed=22)
+    heads = [ln - tail for ln in lens]
+    first = np.concatenate([[0], np.cumsum(lens)])[:-1]
+    idx = np.concatenate([np.arange(f, f + h) for f, h in zip(first, heads)])
+    p = c.params(cuda_lib)
+    cu = torch.tensor([0, heads[0], sum(heads)], dtype=torch.int32, device="cuda")
+    take = lambda x: x[idx].contiguous()  # noqa: E731
+    stride = dict(q_row_stride=0, k_row_stride=0, v_row_stride=0)
+    p.__dict__.update(stride)
+    T = sum(heads)
+    out = torch.empty(T, c.Hv, c.dv, device="cuda")
+    need = cuda_lib.kda_gdn_prefill_workspace_bytes(p, 2, T)
+    ws = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
+    cuda_lib.check(cuda_lib.kda_gdn_prefill_varlen(p, cu, 2, T, take(c.q), take(c.k), take(c.v), take(c.a), take(c.b),
+                                                   None, c.g_state.tensor, out, ws, need, c.status))
+    c.g_out.tensor[idx] = out
+    for i in range(tail):
+        rows = [f + h + i for f, h in zip(first, heads)]
+        one = lambda x: x[rows].contiguous()  # noqa: E731
+        o = torch.empty(2, c.Hv, c.dv, device="cuda")
+        cuda_lib.check(cuda_lib.kda_gdn_decode(p, 2, one(c.q), one(c.k), one(c.v), one(c.a), one(c.b), None,
+                                               c.g_state.tensor, o, c.status))
+        c.g_out.tensor[rows] = o
+    torch.cuda.synchronize()
+    c.check(tol_out=STATE, tol_state=STATE)
+
+
+def test_graph_replay_and_other_stream(cuda_lib):
+    """Captured on a stream of its own and replayed: the eager calls' bits,
+    each replay on what the buffers hold by then."""
+    c, d = Case([130, 20], seed=23), Case([1] * 5, seed=24)
+    c.prefill(cuda_lib)
+    d.decode(cuda_lib)
+    want = [x.clone() for x in (c.g_out.tensor, c.g_state.tensor, d.g_out.tensor, d.g_state.tensor)]
+    for x in (c, d):
+        x.reset()
+    p = c.params(cuda_lib)
+    need = cuda_lib.kda_gdn_prefill_workspace_bytes(p, 2, 150)
+    ws = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cuda_lib.check(cuda_lib.kda_gdn_prefill_varlen(p, c.cu, 2, 150, c.q, c.k, c.v, c.a, c.b, None, c.g_state.tensor,
+                                                       c.g_out.tensor, ws, need, c.status))
+        cuda_lib.check(cuda_lib.kda_gdn_decode(d.params(cuda_lib), 5, d.q, d.k, d.v, d.a, d.b, None, d.g_state.tensor,
+                                               d.g_out.tensor, d.status))
+    for _ in range(2):
+        for x in (c, d):
+            x.reset()
+        graph.replay()
+        torch.cuda.synchronize()
+        for got, w in zip((c.g_out.tensor, c.g_state.tensor, d.g_out.tensor, d.g_state.tensor), want):
+            assert torch.equal(got, w)
+
+
+def test_two_calls_at_once(cuda_lib):
+    """Two calls on two streams, a workspace each: each has its own result."""
+    cs = [Case([257, 100], seed=25 + i) for i in range(2)]
+    for c in cs:
+        c.prefill(cuda_lib)
+    want = [(c.g_out.tensor.clone(), c.g_state.tensor.clone()) for c in cs]
+    streams = [torch.cuda.Stream() for _ in cs]
+    for c in cs:
+        c.reset()
+    torch.cuda.synchronize()
+    keep = []
+    for c, s in zip(cs, streams):
+        p = c.params(cuda_lib)
+        need = cuda_lib.kda_gdn_prefill_workspace_bytes(p, 2, 357)
+        keep.append(torch.empty(max(need, 16), dtype=torch.uint8, device="cuda"))
+        torch.cuda.synchronize()
+    for c, s, ws in zip(cs, streams, keep):
+        p = c.params(cuda_lib)
+        need = cuda_lib.kda_gdn_prefill_workspace_bytes(p, 2, 357)
+        cuda_lib.check(cuda_lib.kda_gdn_prefill_varlen(p, c.cu, 2, 357, c.q, c.k, c.v, c.a, c.b, None, c.g_state.tensor,
+                                                       c.g_out.tensor, ws, need, c.status, s))
+    torch.cuda.synchronize()
+    for c, (o, st) in zip(cs, want):
+        assert torch.equal(c.g_out.tensor, o) and torch.equal(c.g_state.tensor, st)
+
+
+def test_long_prompt(cuda_lib):
+    """Many chunks of one sequence: errors do not pile up."""
+    c = Case([4000], Hk=1, Hv=2, out="f32", seed=30)
+    c.prefill(cuda_lib)
+    c.check()
