@@ -9,19 +9,21 @@
 // All exponents are differences that are <= 0.
 //
 // A CTA owns one (sequence, value head, DVT columns of dv); nothing crosses
-// columns, so these never meet.  Two roles:
+// columns, so these never meet.  Three roles:
 //   - prep warps (4): load the chunk's rows, normalise and rescale them, form
 //     P and T (state-independent), one chunk ahead of
 //   - chain warps (NW): each keeps S^T for 16 columns in registers as the
 //     accumulator of a 16 x dk product and walks the chunks alone: S^T K^T,
-//     (V - ..)^T T^T, U^T P^T and U^T K take their left operand straight from
+//     R^T T^T (R = beta (V - ..)) and U^T K take their left operand straight from
 //     the accumulators of the product before (the two fragment layouts agree),
-//     so no chain warp ever waits for another one.
+//     so no chain warp ever waits for another one;
+//   - output warps (NW): take S^T and U^T of one chain warp each through shared
+//     memory, form Q S and P U and store the outputs beside the chain.
 //
 // Precision: the state keeps fp32 accuracy.  One decay per head leaves k and q
 // unscaled inside every product, so the rows' bf16 values are operands without
-// loss: prep rescales each row by a power of two and stores it as fp16 (exact
-// down to 2^-17 of the row's largest value).  Every other operand that
+// loss: prep rescales each row by a power of two to a norm in [1, 2) and stores
+// it as fp16 (exact down to 2^-17).  Every other operand that
 // reaches the state is two fp16 values, high and low, about 22 bits: S and
 // U and V - .. are scaled by a power of two per column so that the low part stays
 // in fp16's range.  P and the outputs' reading of S keep the high part only
@@ -42,8 +44,14 @@ constexpr int XS = 72;     // row stride of the fp32 scratch: fragment reads hit
 
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// the same on bf16 values
+__device__ __forceinline__ void mma_bf(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -100,78 +108,54 @@ __device__ __forceinline__ void pow2_scale(float m, float& down, float& up)
     down = __uint_as_float((254u - e) << 23);
     up = __uint_as_float(e << 23);
 }
+// The same for sqrt(m), m >= 0.
+__device__ __forceinline__ void pow2_scale_sqrt(float m, float& down, float& up)
+{
+    const int e = min(max((((int)(__float_as_uint(m) >> 23) & 255) + 1 - 128) >> 1, -60), 60);
+    down = __uint_as_float((uint32_t)(127 - e) << 23);
+    up = __uint_as_float((uint32_t)(127 + e) << 23);
+}
 
 // ------------------------------------------------------------ shared memory
 
 template <int DK, int DVT, bool F32> struct Smem {
-    unsigned char k[3][C * DK * 2];
+    static constexpr int NW = DVT / 16, PARTS = F32 ? 2 : 1;
+    unsigned char k[3][C * DK * 2];        // bf16 rows, then fp16
     unsigned char q[3][C * DK * 2];
-    unsigned char v[3][C * DVT * 2];       // bf16; a chain warp's columns take its outputs afterwards
+    unsigned char v[3][C * DVT * 2];       // bf16; an output warp's columns take its outputs afterwards
     unsigned char t[2][2][C * C * 2];      // T, high and low
-    unsigned char p[2][F32 ? 2 : 1][C * C * 2];
+    unsigned char p[2][PARTS][C * C * 2];
+    uint4 hs[NW][PARTS][DK / 16][32];      // S^T as left-operand fragments, from a chain warp to its output warp
+    uint4 hu[NW][PARTS][4][32];            // U^T likewise
+    float4 hf[NW][8];                      // and their scales
     float x[C * XS];                       // A, then T, in fp32
     // per chunk row: beta; beta sk e^G; sk; e^{G_C - G}; e^G; scale sq
     float beta[2][C], ek[2][C], sk[2][C], w[2][C], eg[2][C], oq[2][C];
     float last[2];                         // e^{G_C}
-    float g[C], gh[C], gl[C], sq[C];
-    unsigned long long ready[2], done[2];
+    float g[C], gh[C], gl[C], bk[C], nk[C], nq[C];
+    uint64_t ready[2], done[2];            // a chunk's operands; their last use
+    uint64_t s_full[NW], s_free[NW], u_full[NW], u_free[NW];
 };
 
 __device__ __forceinline__ void prep_sync() { asm volatile("bar.sync 1, %0;" ::"n"(PREP) : "memory"); }
 
 // ------------------------------------------------------------ prep
 
-// Starts the copies of the chunk of rows r0 .. r0 + n - 1 (rows past n: zeros).
-template <int DK, int DVT, class S>
-__device__ __forceinline__ void load_chunk(S& sm, int slot, const GdnArgs& a, const __nv_bfloat16* q,
-                                           const __nv_bfloat16* k, const __nv_bfloat16* v, int r0, int n, int t)
+// Starts the copies of a tile of W-wide rows r0 .. r0 + n - 1 (rows past n:
+// zeros).  A thread keeps its 16-byte piece and steps down the rows.
+template <int W>
+__device__ __forceinline__ void load_tile(unsigned char* tile, const __nv_bfloat16* src, long long stride, int n, int t)
 {
-    constexpr int KP = DK / 8, VP = DVT / 8;
+    constexpr int P = W / 8, RS = PREP / P;  // pieces of a row; rows between a thread's pieces
+    static_assert(C % RS == 0 && RS % 8 == 0, "the swizzle repeats every eight rows");
+    const int r = t / P, c = t % P;
+    const __nv_bfloat16* s = src + r * stride + c * 8;
+    unsigned char* d = tile + at<W>(r, c);
 #pragma unroll
-    for (int i = t; i < C * KP; i += PREP) {
-        const int r = i / KP, c = i % KP;
-        const uint32_t o = at<DK>(r, c), bytes = r < n ? 16 : 0;
-        const long long row = r0 + (r < n ? r : 0);
-        ptx::cp_async16(sm.k[slot] + o, k + row * a.ks + c * 8, bytes);
-        ptx::cp_async16(sm.q[slot] + o, q + row * a.qs + c * 8, bytes);
+    for (int i = 0; i < C / RS; ++i) {
+        const bool in = r + i * RS < n;
+        ptx::cp_async16(d + i * RS * W * 2, in ? s + (long long)i * RS * stride : src, in ? 16 : 0);
     }
-#pragma unroll
-    for (int i = t; i < C * VP; i += PREP) {
-        const int r = i / VP, c = i % VP;
-        ptx::cp_async16(sm.v[slot] + at<DVT>(r, c), v + (r0 + (r < n ? r : 0)) * a.vs + c * 8, r < n ? 16 : 0);
-    }
-    ptx::cp_async_commit();
-}
-
-// One row of a tile: bf16 -> fp16 times a power of two, in place.  Returns the
-// factor that makes the stored row the (normalised) row.
-template <int DK> __device__ __forceinline__ float convert_row(unsigned char* tile, int r, bool l2, float eps)
-{
-    constexpr int KP = DK / 8;
-    uint4 raw[KP];
-    __nv_bfloat162 m = __float2bfloat162_rn(0.f);
-    float ss = 0.f;
-#pragma unroll
-    for (int c = 0; c < KP; ++c) {
-        raw[c] = *reinterpret_cast<const uint4*>(tile + at<DK>(r, c));
-        const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            m = __hmax2(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[i])));
-            ss = fmaf(bf_lo(w[i]), bf_lo(w[i]), ss);
-            ss = fmaf(bf_hi(w[i]), bf_hi(w[i]), ss);
-        }
-    }
-    float down, up;
-    pow2_scale(fmaxf(__low2float(m), __high2float(m)), down, up);
-#pragma unroll
-    for (int c = 0; c < KP; ++c) {
-        uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = pack_h(bf_lo(w[i]) * down, bf_hi(w[i]) * down);
-        *reinterpret_cast<uint4*>(tile + at<DK>(r, c)) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-    return l2 ? up * rsqrtf(ss + eps) : up;
 }
 
 // (h, l) += (oh, ol) in double-word fp32
@@ -184,13 +168,13 @@ __device__ __forceinline__ void dw_add(float& h, float& l, float oh, float ol)
     l = __fsub_rn(r, __fsub_rn(h, s));
 }
 
-// One warp: running sums of the chunk's log decays (two rows a lane; double
-// word: differences of large sums keep their small part) and the chain's coefficients.
-template <class S> __device__ __forceinline__ void scan_rows(S& sm, int b, float scale, int lane)
+// One warp: running sums of the chunk's log decays, two rows a lane (double
+// word: differences of large sums keep their small part).
+template <class S> __device__ __forceinline__ void scan_rows(S& sm, int b, int lane)
 {
-    const float g0 = sm.g[2 * lane], g1 = sm.g[2 * lane + 1];
-    float h = g0, l = 0.f;
-    dw_add(h, l, g1, 0.f);
+    const float2 g = *reinterpret_cast<const float2*>(&sm.g[2 * lane]);
+    float h = g.x, l = 0.f;
+    dw_add(h, l, g.y, 0.f);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const float oh = __shfl_up_sync(0xffffffffu, h, o), ol = __shfl_up_sync(0xffffffffu, l, o);
@@ -199,20 +183,32 @@ template <class S> __device__ __forceinline__ void scan_rows(S& sm, int b, float
     const float th = __shfl_sync(0xffffffffu, h, 31), tl = __shfl_sync(0xffffffffu, l, 31);
     float ph = __shfl_up_sync(0xffffffffu, h, 1), pl = __shfl_up_sync(0xffffffffu, l, 1);
     if (lane == 0) ph = pl = 0.f;
-    dw_add(ph, pl, g0, 0.f);  // the lane's first row
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int r = 2 * lane + i;
-        const float rh = i ? h : ph, rl = i ? l : pl;
-        sm.gh[r] = rh;
-        sm.gl[r] = rl;
-        const float e = exp_sfu(rh + rl);
-        sm.eg[b][r] = e;
-        sm.ek[b][r] = sm.beta[b][r] * sm.sk[b][r] * e;
-        sm.w[b][r] = exp_sfu((th - rh) + (tl - rl));
-        sm.oq[b][r] = scale * sm.sq[r];
-    }
+    dw_add(ph, pl, g.x, 0.f);  // the lane's first row
+    *reinterpret_cast<float2*>(&sm.gh[2 * lane]) = make_float2(ph, h);
+    *reinterpret_cast<float2*>(&sm.gl[2 * lane]) = make_float2(pl, l);
+    *reinterpret_cast<float2*>(&sm.eg[b][2 * lane]) = make_float2(exp_sfu(ph + pl), exp_sfu(h + l));
+    *reinterpret_cast<float2*>(&sm.w[b][2 * lane]) =
+        make_float2(exp_sfu((th - ph) + (tl - pl)), exp_sfu((th - h) + (tl - l)));
     if (lane == 0) sm.last[b] = exp_sfu(th + tl);
+}
+
+// One row of a tile: bf16 -> fp16 times a power of two, in place.
+template <int DK> __device__ __forceinline__ void convert_row(unsigned char* tile, int r, float down)
+{
+    const __nv_bfloat162 d = __float2bfloat162_rn(down);
+#pragma unroll
+    for (int c = 0; c < DK / 8; ++c) {
+        uint4* p = reinterpret_cast<uint4*>(tile + at<DK>(r, c));
+        const uint4 x = *p;
+        uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]), d);
+            const uint32_t u = *reinterpret_cast<const uint32_t*>(&y);
+            w[i] = pack_h(bf_lo(u), bf_hi(u));
+        }
+        *p = make_uint4(w[0], w[1], w[2], w[3]);
+    }
 }
 
 // The panel of 16 columns n0 of  T21 = -T22 (A21 T11)  for the SIZE-blocks at
@@ -280,32 +276,31 @@ template <int SIZE, class S> __device__ __forceinline__ void merge_panel(S& sm, 
         }
 }
 
-// The chunk's P and T into buffer b from the rows in slot `slot`.
+// The 16 x 16 blocks on and below the diagonal, by warp: two or three each.
+__device__ __forceinline__ void block_of(int warp, int j, int& bi, int& bj)
+{
+    // (3,0) (3,1) (0,0) | (3,2) (3,3) (1,1) | (2,0) (2,1) | (2,2) (1,0)
+    const int i = warp * 3 + j;
+    bi = (int)((0b00'01'10'00'10'10'01'11'11'00'11'11u >> (2 * i)) & 3);
+    bj = (int)((0b00'00'10'00'01'00'01'11'10'00'01'00u >> (2 * i)) & 3);
+}
+
+// The chunk's P and T into buffer b from the rows in slot `slot`; g, beta: the
+// log decay and beta of row t & 63 (zero for a padded row).
 template <int DK, int DVT, bool F32, class S>
-__device__ __forceinline__ void prep_chunk(S& sm, int slot, int b, const GdnArgs& a, bool real, float graw, float braw,
-                                           float a_log, float dt, int t)
+__device__ __forceinline__ void prep_chunk(S& sm, int slot, int b, const GdnArgs& a, bool real, int t)
 {
     const int warp = t >> 5, lane = t & 31, gq = lane >> 2, q2 = (lane & 3) * 2;
-    {
-        const int r = t & (C - 1);
-        // a padded row (zeros) stays out of everything whatever the epsilon
-        const float f = convert_row<DK>(t < C ? sm.k[slot] : sm.q[slot], r, a.l2 != 0, a.l2_eps);
-        if (t < C) {
-            sm.sk[b][r] = real ? f : 0.f;
-            sm.g[r] = real ? gdn_log_alpha(a_log, graw, dt) : 0.f;
-            sm.beta[b][r] = real ? sigmoidf_(braw) : 0.f;
-        } else sm.sq[r] = real ? f : 0.f;
-    }
-    prep_sync();
-    if (warp == 3) scan_rows(sm, b, a.scale, lane);
-    // the ten 16 x 16 blocks on and below the diagonal of K K^T and Q K^T
+    if (warp == 3) scan_rows(sm, b, lane);
+    // K K^T and Q K^T of the raw rows: bf16 values, exact products
     const uint32_t kb = ptx::smem_u32(sm.k[slot]), qb = ptx::smem_u32(sm.q[slot]);
+    const int arow = lane & 15, acol = lane >> 4, brow = (lane & 7) + ((lane >> 4) & 1) * 8, bcol = (lane >> 3) & 1;
     float kk[3][2][4], qk[3][2][4];
 #pragma unroll
     for (int j = 0; j < 3; ++j) {
-        const int blk = warp + 4 * j;
-        if (blk >= 10) break;
-        const int bi = blk < 1 ? 0 : blk < 3 ? 1 : blk < 6 ? 2 : 3, bj = blk - bi * (bi + 1) / 2;
+        if (j == 2 && warp >= 2) break;
+        int bi, bj;
+        block_of(warp, j, bi, bj);
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -313,41 +308,95 @@ __device__ __forceinline__ void prep_chunk(S& sm, int slot, int b, const GdnArgs
 #pragma unroll
         for (int kt = 0; kt < DK / 16; ++kt) {
             uint32_t ka[4], qa[4], bb[4];
-            const uint32_t ao = at<DK>(bi * 16 + (lane & 15), kt * 2 + (lane >> 4));
+            const uint32_t ao = at<DK>(bi * 16 + arow, kt * 2 + acol);
             ldsm(ka, kb + ao);
             ldsm(qa, qb + ao);
-            ldsm(bb, kb + at<DK>(bj * 16 + (lane & 7) + ((lane >> 4) & 1) * 8, kt * 2 + ((lane >> 3) & 1)));
-            mma(kk[j][0], ka, bb[0], bb[1]);
-            mma(kk[j][1], ka, bb[2], bb[3]);
-            mma(qk[j][0], qa, bb[0], bb[1]);
-            mma(qk[j][1], qa, bb[2], bb[3]);
+            ldsm(bb, kb + at<DK>(bj * 16 + brow, kt * 2 + bcol));
+            mma_bf(kk[j][0], ka, bb[0], bb[1]);
+            mma_bf(kk[j][1], ka, bb[2], bb[3]);
+            mma_bf(qk[j][0], qa, bb[0], bb[1]);
+            mma_bf(qk[j][1], qa, bb[2], bb[3]);
         }
+        if (bi == bj) {  // squared norms of k's rows
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (q2 == gq) sm.nk[bi * 16 + i * 8 + gq] = kk[j][i][2 * i];
+                if (q2 + 1 == gq) sm.nk[bi * 16 + i * 8 + gq] = kk[j][i][2 * i + 1];
+            }
+        }
+    }
+    {
+        // and of q's
+        float qq[2][4] = {};
+#pragma unroll
+        for (int kt = 0; kt < DK / 16; ++kt) {
+            uint32_t qa[4], bb[4];
+            ldsm(qa, qb + at<DK>(warp * 16 + arow, kt * 2 + acol));
+            ldsm(bb, qb + at<DK>(warp * 16 + brow, kt * 2 + bcol));
+            mma_bf(qq[0], qa, bb[0], bb[1]);
+            mma_bf(qq[1], qa, bb[2], bb[3]);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (q2 == gq) sm.nq[warp * 16 + i * 8 + gq] = qq[i][2 * i];
+            if (q2 + 1 == gq) sm.nq[warp * 16 + i * 8 + gq] = qq[i][2 * i + 1];
+        }
+    }
+    prep_sync();
+    {
+        const int r = t & (C - 1);
+        const float ss = t < C ? sm.nk[r] : sm.nq[r];
+        float down, up;
+        pow2_scale_sqrt(ss, down, up);
+        // the factor that makes the stored row the (normalised) row; none for a padded one
+        const float norm = a.l2 ? rsqrtf(ss + a.l2_eps) : 1.f;
+        if (t < C) {
+            const float f = real ? norm * up : 0.f, e = sm.eg[b][r];
+            sm.sk[b][r] = f;
+            sm.ek[b][r] = sm.beta[b][r] * f * e;
+            sm.nk[r] = real ? norm : 0.f;               // raw rows enter A and P
+            sm.bk[r] = real ? sm.beta[b][r] * norm : 0.f;
+        } else sm.oq[b][r] = real ? a.scale * norm * up : 0.f;
+        if (t >= C) sm.nq[r] = down;
+        convert_row<DK>(t < C ? sm.k[slot] : sm.q[slot], r, down);
+        // P = e^{G_r - G_s} q'_r.k'_s on the stored rows' scale: k's part
+        if (t < C) sm.g[r] = down;
     }
     prep_sync();
 #pragma unroll
     for (int j = 0; j < 3; ++j) {
-        const int blk = warp + 4 * j;
-        if (blk >= 10) break;
-        const int bi = blk < 1 ? 0 : blk < 3 ? 1 : blk < 6 ? 2 : 3, bj = blk - bi * (bi + 1) / 2;
+        if (j == 2 && warp >= 2) break;
+        int bi, bj;
+        block_of(warp, j, bi, bj);
+        float2 ch[2], cl[2], cn[2], cd[2];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            const int s = bj * 16 + n * 8 + q2;
+            ch[n] = *reinterpret_cast<const float2*>(&sm.gh[s]);
+            cl[n] = *reinterpret_cast<const float2*>(&sm.gl[s]);
+            cn[n] = *reinterpret_cast<const float2*>(&sm.nk[s]);
+            cd[n] = *reinterpret_cast<const float2*>(&sm.g[s]);
+        }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int r = bi * 16 + gq + i * 8;
-            const float rh = sm.gh[r], rl = sm.gl[r], br = sm.beta[b][r] * sm.sk[b][r];
+            const float rh = sm.gh[r], rl = sm.gl[r], br = sm.bk[r], qd = sm.nq[r];
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
                 const int s = bj * 16 + n * 8 + q2;
-                float av[2], pv[2];
-#pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                    const float d = s + z <= r ? exp_sfu((rh - sm.gh[s + z]) + (rl - sm.gl[s + z])) : 0.f;
-                    av[z] = s + z < r ? br * sm.sk[b][s + z] * d * kk[j][n][2 * i + z] : 0.f;
-                    pv[z] = s + z <= r ? d * qk[j][n][2 * i + z] : 0.f;
-                }
-                *reinterpret_cast<float2*>(&sm.x[r * XS + s]) = make_float2(av[0], av[1]);
-                uint32_t hi, lo;
-                split_h(pv[0], pv[1], hi, lo);
-                *reinterpret_cast<uint32_t*>(sm.p[b][0] + at<C>(r, s >> 3) + (s & 7) * 2) = hi;
-                if (F32) *reinterpret_cast<uint32_t*>(sm.p[b][F32 ? 1 : 0] + at<C>(r, s >> 3) + (s & 7) * 2) = lo;
+                const float d0 = exp_sfu((rh - ch[n].x) + (rl - cl[n].x)), d1 = exp_sfu((rh - ch[n].y) + (rl - cl[n].y));
+                const float a0 = s < r ? (br * cn[n].x) * d0 * kk[j][n][2 * i] : 0.f;
+                const float a1 = s + 1 < r ? (br * cn[n].y) * d1 * kk[j][n][2 * i + 1] : 0.f;
+                const float p0 = s <= r ? (qd * cd[n].x) * d0 * qk[j][n][2 * i] : 0.f;
+                const float p1 = s + 1 <= r ? (qd * cd[n].y) * d1 * qk[j][n][2 * i + 1] : 0.f;
+                *reinterpret_cast<float2*>(&sm.x[r * XS + s]) = make_float2(a0, a1);
+                const uint32_t o = at<C>(r, s >> 3) + (s & 7) * 2;
+                if constexpr (F32) {
+                    uint32_t hi, lo;
+                    split_h(p0, p1, hi, lo);
+                    *reinterpret_cast<uint32_t*>(sm.p[b][0] + o) = hi;
+                    *reinterpret_cast<uint32_t*>(sm.p[b][1] + o) = lo;
+                } else *reinterpret_cast<uint32_t*>(sm.p[b][0] + o) = pack_h(p0, p1);
             }
         }
     }
@@ -358,10 +407,16 @@ __device__ __forceinline__ void prep_chunk(S& sm, int slot, int b, const GdnArgs
         float x[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            float acc = i == c ? 1.f : 0.f;
+            float acc = i == c ? 1.f : 0.f, acc2 = 0.f;
 #pragma unroll
-            for (int m = 0; m < i; ++m) acc = fmaf(-sm.x[(d0 + i) * XS + d0 + m], x[m], acc);
-            x[i] = acc;
+            for (int m = 0; m < i; m += 4) {
+                const float4 f = *reinterpret_cast<const float4*>(&sm.x[(d0 + i) * XS + d0 + m]);
+                acc = fmaf(-f.x, x[m], acc);
+                if (m + 1 < i) acc2 = fmaf(-f.y, x[m + 1], acc2);
+                if (m + 2 < i) acc = fmaf(-f.z, x[m + 2], acc);
+                if (m + 3 < i) acc2 = fmaf(-f.w, x[m + 3], acc2);
+            }
+            x[i] = acc + acc2;
         }
         __syncwarp();
         if (lane < 16) {
@@ -383,28 +438,59 @@ __device__ __forceinline__ void prep_chunk(S& sm, int slot, int b, const GdnArgs
 
 // ------------------------------------------------------------ chain
 
-// The chunk's share of a chain warp: 16 columns of dv.  S holds S^T times g0
-// (columns gq) and g1 (columns gq + 8).
-template <int DK, int DVT, bool F32, class S>
-__device__ __forceinline__ void chain_chunk(S& sm, int slot, int b, float (&s)[DK / 8][4], float (&g)[2], float (&ig)[2],
-                                            const GdnArgs& a, void* out, long long row_stride, int n, int warp, int lane)
+// A bounded wait that gives up once: later ones are skipped, the status word says so.
+struct Waiter {
+    int32_t* dev_status;
+    bool dead;
+    __device__ __forceinline__ void operator()(uint64_t& bar, int phase)
+    {
+        if (!dead && !ptx::mbar_wait(&bar, phase & 1)) {
+            dead = true;
+            flag_status(dev_status, KDA_DEV_TIMEOUT);
+        }
+    }
+};
+
+__device__ __forceinline__ void warp_arrive(uint64_t& bar, int lane)
 {
-    const int q2 = (lane & 3) * 2;
-    const uint32_t kb = ptx::smem_u32(sm.k[slot]), qb = ptx::smem_u32(sm.q[slot]), vb = ptx::smem_u32(sm.v[slot]);
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(&bar);
+}
+
+__device__ __forceinline__ float quad_max(float x)
+{
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+    return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+}
+
+// Chunk m of a chain warp: 16 columns of dv.  s holds S^T times g[0] (column
+// lane / 4) and g[1] (eight further), ig their inverses.
+template <int DK, int DVT, bool F32, class S>
+__device__ __forceinline__ void chain_chunk(S& sm, int m, float (&s)[DK / 8][4], float (&ig)[2], Waiter& wait, int warp,
+                                            int lane)
+{
+    const int slot = m % 3, b = m & 1, q2 = (lane & 3) * 2;
+    const uint32_t kb = ptx::smem_u32(sm.k[slot]), vb = ptx::smem_u32(sm.v[slot]);
     const uint32_t tb[2] = {ptx::smem_u32(sm.t[b][0]), ptx::smem_u32(sm.t[b][1])};
-    const uint32_t pb[2] = {ptx::smem_u32(sm.p[b][0]), ptx::smem_u32(sm.p[b][F32 ? 1 : 0])};
     const int brow = (lane & 7) + ((lane >> 4) & 1) * 8, bcol = (lane >> 3) & 1;  // K-contiguous operand
     const int trow = lane & 15, tcol = lane >> 4;                                 // transposed operand
+    if (m > 0) wait(sm.s_free[warp], m - 1);
 
-    // S^T K^T and S^T Q^T
-    float r[8][4], o[8][4];
+    // S^T K^T, each k-tile's fragments loaded a tile ahead
+    float r[8][4];
 #pragma unroll
     for (int t = 0; t < 8; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) r[t][i] = o[t][i] = 0.f;
+        for (int i = 0; i < 4; ++i) r[t][i] = 0.f;
     __half2 m0 = __float2half2_rn(0.f), m1 = m0;
+    uint32_t f[2][4][4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) ldsm(f[0][t], kb + at<DK>(t * 16 + brow, bcol));
 #pragma unroll
     for (int kt = 0; kt < DK / 16; ++kt) {
+        if (kt + 1 < DK / 16)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) ldsm(f[(kt + 1) & 1][t], kb + at<DK>(t * 16 + brow, (kt + 1) * 2 + bcol));
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -414,29 +500,21 @@ __device__ __forceinline__ void chain_chunk(S& sm, int slot, int b, float (&s)[D
             if (i & 1) m1 = __hmax2(m1, h);
             else m0 = __hmax2(m0, h);
         }
+        sm.hs[warp][0][kt][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        if (F32) sm.hs[warp][F32 ? 1 : 0][kt][lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        uint32_t(&e)[4][4] = f[kt & 1];
 #pragma unroll
-        for (int t = 0; t < 8; t += 2) {
-            uint32_t f[4];
-            ldsm(f, kb + at<DK>(t * 8 + brow, kt * 2 + bcol));
-            mma(r[t], hi, f[0], f[1]);
-            mma(r[t + 1], hi, f[2], f[3]);
-            mma(r[t], lo, f[0], f[1]);
-            mma(r[t + 1], lo, f[2], f[3]);
-            ldsm(f, qb + at<DK>(t * 8 + brow, kt * 2 + bcol));
-            mma(o[t], hi, f[0], f[1]);
-            mma(o[t + 1], hi, f[2], f[3]);
-            if (F32) {
-                mma(o[t], lo, f[0], f[1]);
-                mma(o[t + 1], lo, f[2], f[3]);
-            }
-        }
+        for (int t = 0; t < 8; ++t) mma(r[t], hi, e[t >> 1][2 * (t & 1)], e[t >> 1][2 * (t & 1) + 1]);
+#pragma unroll
+        for (int t = 0; t < 8; ++t) mma(r[t], lo, e[t >> 1][2 * (t & 1)], e[t >> 1][2 * (t & 1) + 1]);
     }
+    warp_arrive(sm.s_full[warp], lane);
     // beta (V - e^G k.S), and each column's largest value
     float mr[2] = {0.f, 0.f};
 #pragma unroll
     for (int t = 0; t < 8; t += 2) {
-        uint32_t f[4];  // V^T: rows t*8.. of columns gq, gq+8; then the next eight rows
-        ldsm_t(f, vb + at<DVT>(t * 8 + brow, warp * 2 + bcol));
+        uint32_t v[4];  // V^T: rows t*8.. of columns gq, gq+8; then the next eight rows
+        ldsm_t(v, vb + at<DVT>(t * 8 + brow, warp * 2 + bcol));
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
             const float2 be = *reinterpret_cast<const float2*>(&sm.beta[b][(t + z) * 8 + q2]);
@@ -444,19 +522,15 @@ __device__ __forceinline__ void chain_chunk(S& sm, int slot, int b, float (&s)[D
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 float* x = &r[t + z][2 * i];
-                x[0] = fmaf(-ek.x, x[0] * ig[i], be.x * bf_lo(f[2 * z + i]));
-                x[1] = fmaf(-ek.y, x[1] * ig[i], be.y * bf_hi(f[2 * z + i]));
+                x[0] = fmaf(-ek.x, x[0] * ig[i], be.x * bf_lo(v[2 * z + i]));
+                x[1] = fmaf(-ek.y, x[1] * ig[i], be.y * bf_hi(v[2 * z + i]));
                 mr[i] = fmaxf(mr[i], fmaxf(fabsf(x[0]), fabsf(x[1])));
             }
         }
     }
     float rd[2], ru[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        mr[i] = fmaxf(mr[i], __shfl_xor_sync(0xffffffffu, mr[i], 1));
-        mr[i] = fmaxf(mr[i], __shfl_xor_sync(0xffffffffu, mr[i], 2));
-        pow2_scale(mr[i], rd[i], ru[i]);
-    }
+    for (int i = 0; i < 2; ++i) pow2_scale(quad_max(mr[i]), rd[i], ru[i]);
     // U^T = R^T T^T (T is lower triangular: k-tile kt meets rows from 16 kt on)
     float u[8][4];
 #pragma unroll
@@ -465,24 +539,23 @@ __device__ __forceinline__ void chain_chunk(S& sm, int slot, int b, float (&s)[D
         for (int i = 0; i < 4; ++i) u[t][i] = 0.f;
 #pragma unroll
     for (int kt = 0; kt < 4; ++kt) {
-        uint32_t hi[4], lo[4];
+        uint32_t hi[4], lo[4], th[4][4], tl[4][4];
+#pragma unroll
+        for (int t = kt; t < 4; ++t) {
+            ldsm(th[t], tb[0] + at<C>(t * 16 + brow, kt * 2 + bcol));
+            ldsm(tl[t], tb[1] + at<C>(t * 16 + brow, kt * 2 + bcol));
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float* x = &r[2 * kt + (i >> 1)][2 * (i & 1)];
             split_h(x[0] * rd[i & 1], x[1] * rd[i & 1], hi[i], lo[i]);
         }
 #pragma unroll
-        for (int t = 2 * kt; t < 8; t += 2) {
-            uint32_t f[4], e[4];
-            ldsm(f, tb[0] + at<C>(t * 8 + brow, kt * 2 + bcol));
-            ldsm(e, tb[1] + at<C>(t * 8 + brow, kt * 2 + bcol));
-            mma(u[t], hi, f[0], f[1]);
-            mma(u[t + 1], hi, f[2], f[3]);
-            mma(u[t], lo, f[0], f[1]);
-            mma(u[t + 1], lo, f[2], f[3]);
-            mma(u[t], hi, e[0], e[1]);
-            mma(u[t + 1], hi, e[2], e[3]);
-        }
+        for (int t = 2 * kt; t < 8; ++t) mma(u[t], hi, th[t >> 1][2 * (t & 1)], th[t >> 1][2 * (t & 1) + 1]);
+#pragma unroll
+        for (int t = 2 * kt; t < 8; ++t) mma(u[t], lo, th[t >> 1][2 * (t & 1)], th[t >> 1][2 * (t & 1) + 1]);
+#pragma unroll
+        for (int t = 2 * kt; t < 8; ++t) mma(u[t], hi, tl[t >> 1][2 * (t & 1)], tl[t >> 1][2 * (t & 1) + 1]);
     }
     // times k's row factor; the largest values with and without the decay to the chunk's end
     float mu[2] = {0.f, 0.f}, mw[2] = {0.f, 0.f};
@@ -500,30 +573,20 @@ __device__ __forceinline__ void chain_chunk(S& sm, int slot, int b, float (&s)[D
         }
     }
     const float last = sm.last[b];
-    const float ms[2] = {fmaxf(__low2float(m0), __high2float(m0)), fmaxf(__low2float(m1), __high2float(m1))};
-    float ud[2], uu[2], dec[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        float x = ms[i] * ig[i] * last;
-        mw[i] = fmaxf(mw[i], x);
-        mu[i] = fmaxf(mu[i], ms[i] * ig[i] * 0x1p-20f);  // keeps the outputs' first term in range beside a tiny U
-#pragma unroll
-        for (int z = 1; z <= 2; z <<= 1) {
-            mu[i] = fmaxf(mu[i], __shfl_xor_sync(0xffffffffu, mu[i], z));
-            mw[i] = fmaxf(mw[i], __shfl_xor_sync(0xffffffffu, mw[i], z));
-        }
-        pow2_scale(mu[i], ud[i], uu[i]);
-    }
-    // O^T = scale sq (e^G S^T Q^T + U^T P^T)
-#pragma unroll
-    for (int t = 0; t < 8; ++t) {
-        const float2 eg = *reinterpret_cast<const float2*>(&sm.eg[b][t * 8 + q2]);
+    float ud[2], dec[2], g[2];
+    {
+        const float ms[2] = {fmaxf(__low2float(m0), __high2float(m0)) * ig[0],
+                             fmaxf(__low2float(m1), __high2float(m1)) * ig[1]};
+        float old[2] = {ig[0], ig[1]}, up;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const float f = ud[i] * ig[i];
-            o[t][2 * i] *= eg.x * f;
-            o[t][2 * i + 1] *= eg.y * f;
+            // 2^-20: keeps the outputs' S term in range beside a tiny U
+            pow2_scale(quad_max(fmaxf(mu[i], ms[i] * 0x1p-20f)), ud[i], up);
+            pow2_scale(quad_max(fmaxf(mw[i], ms[i] * last)), g[i], ig[i]);
+            dec[i] = last * (g[i] * old[i]);
         }
+        if (m > 0) wait(sm.u_free[warp], m - 1);
+        if ((lane & 3) == 0) sm.hf[warp][lane >> 2] = make_float4(ud[0], ud[1], old[0], old[1]);
     }
 #pragma unroll
     for (int kt = 0; kt < 4; ++kt) {
@@ -534,21 +597,120 @@ __device__ __forceinline__ void chain_chunk(S& sm, int slot, int b, float (&s)[D
             if (F32) split_h(x[0] * ud[i & 1], x[1] * ud[i & 1], hi[i], lo[i]);
             else hi[i] = pack_h(x[0] * ud[i & 1], x[1] * ud[i & 1]);
         }
+        sm.hu[warp][0][kt][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        if (F32) sm.hu[warp][F32 ? 1 : 0][kt][lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+    warp_arrive(sm.u_full[warp], lane);
+    // S^T = e^{G_C} S^T + (U^T diag(e^{G_C - G})) K, in a scale that both terms fit
 #pragma unroll
-        for (int t = 2 * kt; t < 8; t += 2) {
-            uint32_t f[4];
-            ldsm(f, pb[0] + at<C>(t * 8 + brow, kt * 2 + bcol));
-            mma(o[t], hi, f[0], f[1]);
-            mma(o[t + 1], hi, f[2], f[3]);
-            if (F32) {
-                mma(o[t], lo, f[0], f[1]);
-                mma(o[t + 1], lo, f[2], f[3]);
-                ldsm(f, pb[1] + at<C>(t * 8 + brow, kt * 2 + bcol));
-                mma(o[t], hi, f[0], f[1]);
-                mma(o[t + 1], hi, f[2], f[3]);
+    for (int t = 0; t < DK / 8; ++t) {
+        s[t][0] *= dec[0];
+        s[t][1] *= dec[0];
+        s[t][2] *= dec[1];
+        s[t][3] *= dec[1];
+    }
+    constexpr int G = DK >= 64 ? 4 : 2, NG = DK / 16 / G;  // fragments loaded at a time, and such groups in a k-tile
+#pragma unroll
+    for (int t = 0; t < G; ++t) ldsm_t(f[0][t], kb + at<DK>(trow, t * 2 + tcol));
+#pragma unroll
+    for (int kt = 0; kt < 4; ++kt) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+            const float2 w = *reinterpret_cast<const float2*>(&sm.w[b][(2 * kt + z) * 8 + q2]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float* x = &u[2 * kt + z][2 * i];
+                split_h(x[0] * (w.x * g[i]), x[1] * (w.y * g[i]), hi[2 * z + i], lo[2 * z + i]);
             }
         }
+#pragma unroll
+        for (int n = 0; n < NG; ++n) {
+            const int step = kt * NG + n;
+            if (step + 1 < 4 * NG)
+#pragma unroll
+                for (int t = 0; t < G; ++t)
+                    ldsm_t(f[(step + 1) & 1][t],
+                           kb + at<DK>((step + 1) / NG * 16 + trow, ((step + 1) % NG * G + t) * 2 + tcol));
+            uint32_t(&e)[4][4] = f[step & 1];
+#pragma unroll
+            for (int t = 0; t < 2 * G; ++t) mma(s[n * 2 * G + t], hi, e[t >> 1][2 * (t & 1)], e[t >> 1][2 * (t & 1) + 1]);
+#pragma unroll
+            for (int t = 0; t < 2 * G; ++t) mma(s[n * 2 * G + t], lo, e[t >> 1][2 * (t & 1)], e[t >> 1][2 * (t & 1) + 1]);
+        }
     }
+}
+
+// Chunk m of an output warp, from its chain warp's fragments:
+// O^T = scale sq (e^G S^T Q^T + U^T P^T).
+template <int DK, int DVT, bool F32, class S>
+__device__ __forceinline__ void output_chunk(S& sm, int m, void* out, long long row_stride, int n, Waiter& wait, int warp,
+                                             int lane)
+{
+    const int slot = m % 3, b = m & 1, q2 = (lane & 3) * 2;
+    const uint32_t qb = ptx::smem_u32(sm.q[slot]), vb = ptx::smem_u32(sm.v[slot]);
+    const uint32_t pb[2] = {ptx::smem_u32(sm.p[b][0]), ptx::smem_u32(sm.p[b][F32 ? 1 : 0])};
+    const int brow = (lane & 7) + ((lane >> 4) & 1) * 8, bcol = (lane >> 3) & 1;
+    float o[8][4];
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[t][i] = 0.f;
+    wait(sm.s_full[warp], m);
+#pragma unroll
+    for (int kt = 0; kt < DK / 16; ++kt) {
+        const uint4 h4 = sm.hs[warp][0][kt][lane];
+        const uint32_t hi[4] = {h4.x, h4.y, h4.z, h4.w};
+        uint4 l4 = h4;
+        if (F32) l4 = sm.hs[warp][F32 ? 1 : 0][kt][lane];
+        const uint32_t lo[4] = {l4.x, l4.y, l4.z, l4.w};
+        uint32_t f[4][4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) ldsm(f[t], qb + at<DK>(t * 16 + brow, kt * 2 + bcol));
+#pragma unroll
+        for (int t = 0; t < 8; ++t) mma(o[t], hi, f[t >> 1][2 * (t & 1)], f[t >> 1][2 * (t & 1) + 1]);
+        if (F32)
+#pragma unroll
+            for (int t = 0; t < 8; ++t) mma(o[t], lo, f[t >> 1][2 * (t & 1)], f[t >> 1][2 * (t & 1) + 1]);
+    }
+    warp_arrive(sm.s_free[warp], lane);
+    wait(sm.u_full[warp], m);
+    const float4 sc = sm.hf[warp][lane >> 2];
+    const float ud[2] = {sc.x, sc.y}, fs[2] = {sc.x * sc.z, sc.y * sc.w};
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+        const float2 eg = *reinterpret_cast<const float2*>(&sm.eg[b][t * 8 + q2]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            o[t][2 * i] *= eg.x * fs[i];
+            o[t][2 * i + 1] *= eg.y * fs[i];
+        }
+    }
+#pragma unroll
+    for (int kt = 0; kt < 4; ++kt) {
+        const uint4 h4 = sm.hu[warp][0][kt][lane];
+        const uint32_t hi[4] = {h4.x, h4.y, h4.z, h4.w};
+        uint4 l4 = h4;
+        if (F32) l4 = sm.hu[warp][F32 ? 1 : 0][kt][lane];
+        const uint32_t lo[4] = {l4.x, l4.y, l4.z, l4.w};
+        uint32_t f[4][4];
+#pragma unroll
+        for (int t = kt; t < 4; ++t) ldsm(f[t], pb[0] + at<C>(t * 16 + brow, kt * 2 + bcol));
+#pragma unroll
+        for (int t = 2 * kt; t < 8; ++t) mma(o[t], hi, f[t >> 1][2 * (t & 1)], f[t >> 1][2 * (t & 1) + 1]);
+        if (F32) {
+#pragma unroll
+            for (int t = 2 * kt; t < 8; ++t) mma(o[t], lo, f[t >> 1][2 * (t & 1)], f[t >> 1][2 * (t & 1) + 1]);
+#pragma unroll
+            for (int t = kt; t < 4; ++t) ldsm(f[t], pb[1] + at<C>(t * 16 + brow, kt * 2 + bcol));
+#pragma unroll
+            for (int t = 2 * kt; t < 8; ++t) mma(o[t], hi, f[t >> 1][2 * (t & 1)], f[t >> 1][2 * (t & 1) + 1]);
+        }
+    }
+    warp_arrive(sm.u_free[warp], lane);
+    float uu[2];  // 1 / ud: a power of two
+#pragma unroll
+    for (int i = 0; i < 2; ++i) uu[i] = __uint_as_float((254u << 23) - __float_as_uint(ud[i]));
 #pragma unroll
     for (int t = 0; t < 8; ++t) {
         const float2 oq = *reinterpret_cast<const float2*>(&sm.oq[b][t * 8 + q2]);
@@ -591,44 +753,6 @@ __device__ __forceinline__ void chain_chunk(S& sm, int slot, int b, float (&s)[D
                     *reinterpret_cast<const uint4*>(sm.v[slot] + at<DVT>(rr, warp * 2 + c));
         }
     }
-    // S^T = e^{G_C} S^T + (U^T diag(e^{G_C - G})) K, in the scale both terms fit
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        float down, up;
-        pow2_scale(mw[i], down, up);
-        dec[i] = last * (down * ig[i]);
-        g[i] = down;
-        ig[i] = up;
-    }
-#pragma unroll
-    for (int t = 0; t < DK / 8; ++t) {
-        s[t][0] *= dec[0];
-        s[t][1] *= dec[0];
-        s[t][2] *= dec[1];
-        s[t][3] *= dec[1];
-    }
-#pragma unroll
-    for (int kt = 0; kt < 4; ++kt) {
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int z = 0; z < 2; ++z) {
-            const float2 w = *reinterpret_cast<const float2*>(&sm.w[b][(2 * kt + z) * 8 + q2]);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float* x = &u[2 * kt + z][2 * i];
-                split_h(x[0] * (w.x * g[i]), x[1] * (w.y * g[i]), hi[2 * z + i], lo[2 * z + i]);
-            }
-        }
-#pragma unroll
-        for (int t = 0; t < DK / 8; t += 2) {
-            uint32_t f[4];
-            ldsm_t(f, kb + at<DK>(kt * 16 + trow, t + tcol));
-            mma(s[t], hi, f[0], f[1]);
-            mma(s[t + 1], hi, f[2], f[3]);
-            mma(s[t], lo, f[0], f[1]);
-            mma(s[t + 1], lo, f[2], f[3]);
-        }
-    }
 }
 
 // ------------------------------------------------------------ kernel
@@ -655,9 +779,9 @@ __device__ __forceinline__ int ranked_seq(const int32_t* cu, int N, int rank, in
 }
 
 template <int DK, int NW, bool F32>
-__global__ void __launch_bounds__(NW * 32 + PREP, 1) gdn_chunk_kernel(const GdnArgs a, int dv)
+__global__ void __launch_bounds__(NW * 64 + PREP, 1) gdn_chunk_kernel(const GdnArgs a, int dv)
 {
-    constexpr int DVT = NW * 16;
+    constexpr int DVT = NW * 16, THREADS = NW * 64 + PREP;
     extern __shared__ __align__(1024) unsigned char dyn[];
     using S = Smem<DK, DVT, F32>;
     S& sm = *reinterpret_cast<S*>(dyn);
@@ -673,23 +797,23 @@ __global__ void __launch_bounds__(NW * 32 + PREP, 1) gdn_chunk_kernel(const GdnA
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            ptx::mbar_init(reinterpret_cast<uint64_t*>(&sm.ready[i]), PREP);
-            ptx::mbar_init(reinterpret_cast<uint64_t*>(&sm.done[i]), NW);
+            ptx::mbar_init(&sm.ready[i], PREP);
+            ptx::mbar_init(&sm.done[i], 2 * NW);
+        }
+        for (int i = 0; i < NW; ++i) {
+            ptx::mbar_init(&sm.s_full[i], 1);
+            ptx::mbar_init(&sm.s_free[i], 1);
+            ptx::mbar_init(&sm.u_full[i], 1);
+            ptx::mbar_init(&sm.u_free[i], 1);
         }
         ptx::fence_mbar_init();
     }
-    for (int i = tid; i < C * XS; i += NW * 32 + PREP) sm.x[i] = 0.f;  // blocks above the diagonal stay zero
+    for (int i = tid; i < C * XS; i += THREADS) sm.x[i] = 0.f;  // blocks above the diagonal stay zero
     __syncthreads();
-    bool dead = false;  // a bounded wait gave up: go on without waiting, the status word says so
-    auto wait = [&](unsigned long long* bar, int phase) {
-        if (!dead && !ptx::mbar_wait(reinterpret_cast<uint64_t*>(bar), phase & 1)) {
-            dead = true;
-            flag_status(a.dev_status, KDA_DEV_TIMEOUT);
-        }
-    };
+    Waiter wait{a.dev_status, false};
 
-    if (warp >= NW) {
-        const int t = tid - NW * 32, hk = h / (a.Hv / a.Hk);
+    if (warp >= 2 * NW) {
+        const int t = tid - NW * 64, hk = h / (a.Hv / a.Hk);
         const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + hk * DK;
         const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(a.k) + hk * DK;
         const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v) + h * dv + col0;
@@ -697,33 +821,55 @@ __global__ void __launch_bounds__(NW * 32 + PREP, 1) gdn_chunk_kernel(const GdnA
         const __nv_bfloat16* be = static_cast<const __nv_bfloat16*>(a.b) + h;
         const float a_log = a.A_log[h], dt = a.dt_bias[h];
         float graw = 0.f, braw = 0.f;
-        auto gates = [&](int r0) {
-            const int r = r0 + (t & (C - 1));
+        auto load = [&](int m) {
+            const int r0 = begin + m * C, n = min(C, end - r0), s = m % 3, r = r0 + (t & (C - 1));
+            load_tile<DK>(sm.k[s], k + r0 * a.ks, a.ks, n, t);
+            load_tile<DK>(sm.q[s], q + r0 * a.qs, a.qs, n, t);
+            load_tile<DVT>(sm.v[s], v + r0 * a.vs, a.vs, n, t);
+            ptx::cp_async_commit();
             if (t < C && r < end) {
                 graw = ldv(ga + (size_t)r * a.Hv);
                 braw = ldv(be + (size_t)r * a.Hv);
             }
         };
-        load_chunk<DK, DVT>(sm, 0, a, q, k, v, begin, min(C, end - begin), t);
-        gates(begin);
+        load(0);
         for (int m = 0; m < chunks; ++m) {
-            const int r0 = begin + m * C;
+            const int b = m & 1;
+            const bool real = begin + m * C + (t & (C - 1)) < end;
             const float g0 = graw, b0 = braw;
-            if (m >= 2) wait(&sm.done[m & 1], (m - 2) >> 1);
+            if (m >= 2) wait(sm.done[b], (m - 2) >> 1);
+            if (t < C) {
+                sm.g[t] = real ? gdn_log_alpha(a_log, g0, dt) : 0.f;
+                sm.beta[b][t] = real ? sigmoidf_(b0) : 0.f;
+            }
             if (m + 1 < chunks) {
-                load_chunk<DK, DVT>(sm, (m + 1) % 3, a, q, k, v, r0 + C, min(C, end - r0 - C), t);
-                gates(r0 + C);
+                load(m + 1);
                 ptx::cp_async_wait_prev();
             } else ptx::cp_async_wait_all();
             prep_sync();
-            prep_chunk<DK, DVT, F32>(sm, m % 3, m & 1, a, r0 + (t & (C - 1)) < end, g0, b0, a_log, dt, t);
-            ptx::mbar_arrive(reinterpret_cast<uint64_t*>(&sm.ready[m & 1]));
+            prep_chunk<DK, DVT, F32>(sm, m % 3, b, a, real, t);
+            ptx::mbar_arrive(&sm.ready[b]);
+            prep_sync();  // the scratch and the decays are free again
+        }
+        return;
+    }
+
+    if (warp >= NW) {
+        const int w = warp - NW;
+        const long long row_stride = (long long)a.Hv * dv;
+        const size_t osize = F32 ? 4 : 2;
+        unsigned char* out = static_cast<unsigned char*>(a.out) + ((size_t)begin * row_stride + (size_t)h * dv + col0) * osize;
+        for (int m = 0; m < chunks; ++m) {
+            wait(sm.ready[m & 1], m >> 1);
+            output_chunk<DK, DVT, F32>(sm, m, out + (size_t)m * C * row_stride * osize, row_stride,
+                                       min(C, end - begin - m * C), wait, w, lane);
+            warp_arrive(sm.done[m & 1], lane);
         }
         return;
     }
 
     const size_t sbase = ((size_t)slot * a.Hv + h) * DK * dv + col0 + warp * 16 + (lane >> 2);
-    float s[DK / 8][4], g[2] = {1.f, 1.f}, ig[2] = {1.f, 1.f}, ms[2] = {0.f, 0.f};
+    float s[DK / 8][4], ig[2], ms[2] = {0.f, 0.f};
 #pragma unroll
     for (int t = 0; t < DK / 8; ++t)
 #pragma unroll
@@ -731,25 +877,19 @@ __global__ void __launch_bounds__(NW * 32 + PREP, 1) gdn_chunk_kernel(const GdnA
             s[t][i] = a.state[sbase + (size_t)(t * 8 + (lane & 3) * 2 + (i & 1)) * dv + (i >> 1) * 8];
             ms[i >> 1] = fmaxf(ms[i >> 1], fabsf(s[t][i]));
         }
+    {
+        float g[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        ms[i] = fmaxf(ms[i], __shfl_xor_sync(0xffffffffu, ms[i], 1));
-        ms[i] = fmaxf(ms[i], __shfl_xor_sync(0xffffffffu, ms[i], 2));
-        pow2_scale(ms[i], g[i], ig[i]);
+        for (int i = 0; i < 2; ++i) pow2_scale(quad_max(ms[i]), g[i], ig[i]);
+#pragma unroll
+        for (int t = 0; t < DK / 8; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[t][i] *= g[i >> 1];
     }
-#pragma unroll
-    for (int t = 0; t < DK / 8; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[t][i] *= g[i >> 1];
-    const long long row_stride = (long long)a.Hv * dv;
-    const size_t osize = F32 ? 4 : 2;
-    unsigned char* out = static_cast<unsigned char*>(a.out) + ((size_t)begin * row_stride + (size_t)h * dv + col0) * osize;
     for (int m = 0; m < chunks; ++m) {
-        wait(&sm.ready[m & 1], m >> 1);
-        chain_chunk<DK, DVT, F32>(sm, m % 3, m & 1, s, g, ig, a, out + (size_t)m * C * row_stride * osize, row_stride,
-                                  min(C, end - begin - m * C), warp, lane);
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(reinterpret_cast<uint64_t*>(&sm.done[m & 1]));
+        wait(sm.ready[m & 1], m >> 1);
+        chain_chunk<DK, DVT, F32>(sm, m, s, ig, wait, warp, lane);
+        warp_arrive(sm.done[m & 1], lane);
     }
 #pragma unroll
     for (int t = 0; t < DK / 8; ++t)
@@ -767,16 +907,18 @@ template <int DK, int NW, bool F32> cudaError_t launch(const GdnArgs& a, int dv,
         return cudaFuncSetAttribute(gdn_chunk_kernel<DK, NW, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     });
     if (e != cudaSuccess) return e;
-    gdn_chunk_kernel<DK, NW, F32><<<a.N * a.Hv * (dv / (NW * 16)), NW * 32 + PREP, smem, st>>>(a, dv);
+    gdn_chunk_kernel<DK, NW, F32><<<a.N * a.Hv * (dv / (NW * 16)), NW * 64 + PREP, smem, st>>>(a, dv);
     return cudaGetLastError();
 }
 
 template <int DK> cudaError_t launch_dk(const GdnArgs& a, int dv, bool bf16, cudaStream_t st)
 {
-    // Two chain warps a CTA where four would leave SMs without one.
+    // Two chain warps a CTA where four would leave SMs without one, and where
+    // the fp32 outputs' low parts take the shared memory of the other two.
     if (dv == 32 || (long long)a.N * a.Hv * (dv / 64) * 2 <= sm_count())
         return bf16 ? launch<DK, 2, false>(a, dv, st) : launch<DK, 2, true>(a, dv, st);
-    return bf16 ? launch<DK, 4, false>(a, dv, st) : launch<DK, 4, true>(a, dv, st);
+    if (bf16) return launch<DK, 4, false>(a, dv, st);
+    return launch<DK, DK == 128 ? 2 : 4, true>(a, dv, st);
 }
 
 }  // namespace
