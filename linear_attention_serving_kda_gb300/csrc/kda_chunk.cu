@@ -1918,8 +1918,6 @@ bool chunk_supported(const kda_params* p)
     return p->head_dim_k == 128 && p->head_dim_v == 128 && p->io_dtype == KDA_DTYPE_BF16;
 }
 
-namespace {
-
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
 {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
@@ -1934,6 +1932,8 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
     });
     return fn;
 }
+
+namespace {
 
 // [T][H * 128] bf16 rows (16-byte aligned base, row pitch H * 256 bytes); box of
 // one head's 128 channels x box_rows rows; zero fill outside the tensor.

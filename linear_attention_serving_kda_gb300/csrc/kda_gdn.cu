@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(GD_WARPS * 32) gdn_decode_kernel(const GdnArgs
     load_n<IO, PER>(static_cast<const IO*>(a.k) + row * a.ks + hk * DK + lane * PER, k);
     load_n<IO, 4>(static_cast<const IO*>(a.v) + row * a.vs + h * dv + col, v);
     const size_t gi = (size_t)row * a.Hv + h;
-    const float alpha = expf(gdn_log_alpha(a.A_log[h], ldv(static_cast<const IO*>(a.a) + gi), a.dt_bias[h]));
+    const float alpha = expf(gdn_log_alpha(expf(a.A_log[h]), ldv(static_cast<const IO*>(a.a) + gi), a.dt_bias[h]));
     const float beta = sigmoidf_(ldv(static_cast<const IO*>(a.b) + gi));
     float qq = 0.f, kk = 0.f, qk = 0.f;
 #pragma unroll
@@ -195,7 +195,7 @@ template <int DK> __global__ void __launch_bounds__(GR_WARPS * 32) gdn_rows_kern
     const float* k = static_cast<const float*>(a.k) + hk * DK + lane * PER;
     const float* v = static_cast<const float*>(a.v) + h * dv + tile * GR_COLS;
     float* out = static_cast<float*>(a.out) + (size_t)h * dv + tile * GR_COLS + c;
-    const float a_log = a.A_log[h], dt = a.dt_bias[h];
+    const float ea = expf(a.A_log[h]), dt = a.dt_bias[h];
 
     for (int r0 = begin; r0 < end; r0 += GR_ROWS) {
         const int n = min(GR_ROWS, end - r0);
@@ -234,7 +234,7 @@ template <int DK> __global__ void __launch_bounds__(GR_WARPS * 32) gdn_rows_kern
             vs[i / GR_COLS][i % GR_COLS] = v[(long long)(r0 + i / GR_COLS) * a.vs + i % GR_COLS];
         if (tid < n) {
             const size_t gi = (size_t)(r0 + tid) * a.Hv + h;
-            al[tid] = expf(gdn_log_alpha(a_log, static_cast<const float*>(a.a)[gi], dt));
+            al[tid] = expf(gdn_log_alpha(ea, static_cast<const float*>(a.a)[gi], dt));
             be[tid] = sigmoidf_(static_cast<const float*>(a.b)[gi]);
         }
         __syncthreads();

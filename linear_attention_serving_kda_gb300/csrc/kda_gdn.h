@@ -2,6 +2,8 @@
 // head share.
 #pragma once
 
+#include <cudaTypedefs.h>
+
 #include "kda_check.h"
 #include "kda_common.cuh"
 
@@ -31,9 +33,10 @@ struct GdnArgs {
 // differences of running sums NaN).  NaN passes through.
 constexpr float GDN_MIN_LOG = -150.0f;
 
-__device__ __forceinline__ float gdn_log_alpha(float a_log, float a, float dt)
+// ea: e^A_log of the head.
+__device__ __forceinline__ float gdn_log_alpha(float ea, float a, float dt)
 {
-    const float g = -expf(a_log) * softplusf_(a + dt);
+    const float g = -ea * softplusf_(a + dt);
     return g < GDN_MIN_LOG ? GDN_MIN_LOG : g;
 }
 
@@ -58,6 +61,9 @@ __device__ __forceinline__ bool gdn_unit(const GdnArgs& a, int seq, int& begin, 
     }
     return slot >= 0 && end > begin;
 }
+
+// The driver's encoder of tensor maps, null where it has none (kda_chunk.cu).
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
 // Prefill row by row (fp32 rows), and in chunks on the tensor cores (bf16 rows).
 cudaError_t launch_gdn_rows(const GdnArgs& a, int dk, int dv, cudaStream_t st);

@@ -10,7 +10,7 @@
 //
 // A CTA owns one (sequence, value head, DVT columns of dv); nothing crosses
 // columns, so these never meet.  Three roles:
-//   - prep warps (4): load the chunk's rows, normalise and rescale them, form
+//   - prep warps (8): load the chunk's rows, normalise and rescale them, form
 //     P and T (state-independent), one chunk ahead of
 //   - chain warps (NW): each keeps S^T for 16 columns in registers as the
 //     accumulator of a 16 x dk product and walks the chunks alone: S^T K^T,
@@ -28,6 +28,8 @@
 // U and V - .. are scaled by a power of two per column so that the low part stays
 // in fp16's range.  P and the outputs' reading of S keep the high part only
 // where the outputs are bf16 (11 bits against their 8).
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_fp16.h>
 
 #include "kda_gdn.h"
@@ -37,8 +39,8 @@ namespace kda {
 namespace {
 
 constexpr int C = 64;
-constexpr int PREP = 128;  // prep threads
-constexpr int XS = 72;     // row stride of the fp32 scratch: fragment reads hit distinct banks
+constexpr int PREP = 256;  // prep threads
+constexpr int XS = 20;     // row stride of the fp32 diagonal blocks
 
 // ------------------------------------------------------------ fragments
 
@@ -91,13 +93,14 @@ __device__ __forceinline__ void split_h(float x, float y, uint32_t& hi, uint32_t
 __device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
 
-// Byte offset of 16-byte piece `c` of row `r` in a tile of W 16-bit values a
-// row: pieces permuted within the row so that eight rows' same piece lie in
-// distinct banks.
+// Byte offset of 16-byte piece `c` of row `r` in a tile of 64 rows of W 16-bit
+// values, as a tensor copy with 128-byte (W >= 64: 64 values a row, one such
+// tile after the other) or 64-byte (W = 32) swizzle leaves it: eight rows' same
+// piece lie in distinct banks.
 template <int W> __device__ __forceinline__ uint32_t at(int r, int c)
 {
-    if constexpr (W >= 64) return (uint32_t)(r * (W * 2) + (((c & ~7) | ((c ^ r) & 7)) << 4));
-    else return (uint32_t)(r * (W * 2) + ((c ^ ((r >> 1) & 3)) << 4));
+    if constexpr (W >= 64) return (uint32_t)((c >> 3) * (C * 128) + r * 128 + (((c ^ r) & 7) << 4));
+    else return (uint32_t)(r * 64 + ((c ^ (r >> 1)) & 3) * 16);
 }
 
 // 2^-e and 2^e for the e that brings m into [1, 2), kept within 2^+-60 (so
@@ -128,12 +131,13 @@ template <int DK, int DVT, bool F32> struct Smem {
     uint4 hs[NW][PARTS][DK / 16][32];      // S^T as left-operand fragments, from a chain warp to its output warp
     uint4 hu[NW][PARTS][4][32];            // U^T likewise
     float4 hf[NW][8];                      // and their scales
-    float x[C * XS];                       // A, then T, in fp32
+    float x[C * XS];                       // A's diagonal blocks, 16 x 16 each
     // per chunk row: beta; beta sk e^G; sk; e^{G_C - G}; e^G; scale sq
     float beta[2][C], ek[2][C], sk[2][C], w[2][C], eg[2][C], oq[2][C];
     float last[2];                         // e^{G_C}
     float g[C], gh[C], gl[C], bk[C], nk[C], nq[C];
-    uint64_t ready[2], done[2];            // a chunk's operands; their last use
+    uint64_t loaded[3], ready[2], done[2]; // a chunk's rows; its operands; their last use
+    int found;
     uint64_t s_full[NW], s_free[NW], u_full[NW], u_free[NW];
 };
 
@@ -141,21 +145,21 @@ __device__ __forceinline__ void prep_sync() { asm volatile("bar.sync 1, %0;" ::"
 
 // ------------------------------------------------------------ prep
 
-// Starts the copies of a tile of W-wide rows r0 .. r0 + n - 1 (rows past n:
-// zeros).  A thread keeps its 16-byte piece and steps down the rows.
+// Starts the copy of 64 rows from row r0, W values from column x, of a row
+// tensor (rows past the tensor: zeros).
 template <int W>
-__device__ __forceinline__ void load_tile(unsigned char* tile, const __nv_bfloat16* src, long long stride, int n, int t)
+__device__ __forceinline__ void load_tile(unsigned char* tile, const CUtensorMap* map, int x, int r0, uint64_t* bar,
+                                          uint64_t policy)
 {
-    constexpr int P = W / 8, RS = PREP / P;  // pieces of a row; rows between a thread's pieces
-    static_assert(C % RS == 0 && RS % 8 == 0, "the swizzle repeats every eight rows");
-    const int r = t / P, c = t % P;
-    const __nv_bfloat16* s = src + r * stride + c * 8;
-    unsigned char* d = tile + at<W>(r, c);
+    constexpr int B = W >= 64 ? 64 : W;  // values a box is wide
 #pragma unroll
-    for (int i = 0; i < C / RS; ++i) {
-        const bool in = r + i * RS < n;
-        ptx::cp_async16(d + i * RS * W * 2, in ? s + (long long)i * RS * stride : src, in ? 16 : 0);
-    }
+    for (int i = 0; i < W / B; ++i) ptx::tma_load_2d(tile + i * C * B * 2, map, x + i * B, r0, bar, policy);
+}
+
+template <int W> __device__ __forceinline__ void zero_row(unsigned char* tile, int r)
+{
+#pragma unroll 1
+    for (int c = 0; c < W / 8; ++c) *reinterpret_cast<uint4*>(tile + at<W>(r, c)) = make_uint4(0, 0, 0, 0);
 }
 
 // (h, l) += (oh, ol) in double-word fp32
@@ -175,7 +179,7 @@ template <class S> __device__ __forceinline__ void scan_rows(S& sm, int b, int l
     const float2 g = *reinterpret_cast<const float2*>(&sm.g[2 * lane]);
     float h = g.x, l = 0.f;
     dw_add(h, l, g.y, 0.f);
-#pragma unroll
+#pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
         const float oh = __shfl_up_sync(0xffffffffu, h, o), ol = __shfl_up_sync(0xffffffffu, l, o);
         if (lane >= o) dw_add(h, l, oh, ol);
@@ -192,217 +196,197 @@ template <class S> __device__ __forceinline__ void scan_rows(S& sm, int b, int l
     if (lane == 0) sm.last[b] = exp_sfu(th + tl);
 }
 
-// One row of a tile: bf16 -> fp16 times a power of two, in place.
-template <int DK> __device__ __forceinline__ void convert_row(unsigned char* tile, int r, float down)
+// Half a row of a tile: bf16 -> fp16 times a power of two, in place.
+template <int DK> __device__ __forceinline__ void convert_row(unsigned char* tile, int r, int half, float down)
 {
     const __nv_bfloat162 d = __float2bfloat162_rn(down);
+    constexpr int P = DK / 16 < 4 ? DK / 16 : 4;  // pieces in flight
 #pragma unroll
-    for (int c = 0; c < DK / 8; ++c) {
-        uint4* p = reinterpret_cast<uint4*>(tile + at<DK>(r, c));
-        const uint4 x = *p;
-        uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    for (int c0 = 0; c0 < DK / 16; c0 += P) {
+        uint4 x[P];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]), d);
-            const uint32_t u = *reinterpret_cast<const uint32_t*>(&y);
-            w[i] = pack_h(bf_lo(u), bf_hi(u));
-        }
-        *p = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-}
-
-// The panel of 16 columns n0 of  T21 = -T22 (A21 T11)  for the SIZE-blocks at
-// (i0, j0) of the scratch, its 16-row part `mt`; all operands split in two.
-template <int SIZE, class S> __device__ __forceinline__ void merge_panel(S& sm, int b, int i0, int j0, int n0, int mt, int lane)
-{
-    const int gq = lane >> 2, q2 = (lane & 3) * 2;
-    const float* X = sm.x;
-    float pt[SIZE / 8][4];  // (A21 T11)^T, rows n
+        for (int c = 0; c < P; ++c) x[c] = *reinterpret_cast<const uint4*>(tile + at<DK>(r, half * (DK / 16) + c0 + c));
 #pragma unroll
-    for (int t = 0; t < SIZE / 8; ++t) pt[t][0] = pt[t][1] = pt[t][2] = pt[t][3] = 0.f;
+        for (int c = 0; c < P; ++c) {
+            uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
 #pragma unroll
-    for (int kt = 0; kt < SIZE / 16; ++kt) {
-        uint32_t ah[4], al[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int n = j0 + n0 + gq + (i & 1) * 8, j = j0 + kt * 16 + q2 + (i >> 1) * 8;
-            split_h(X[j * XS + n], X[(j + 1) * XS + n], ah[i], al[i]);
-        }
-#pragma unroll
-        for (int t = 0; t < SIZE / 8; ++t) {
-            uint32_t bh[2], bl[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float2 f = *reinterpret_cast<const float2*>(&X[(i0 + t * 8 + gq) * XS + j0 + kt * 16 + q2 + i * 8]);
-                split_h(f.x, f.y, bh[i], bl[i]);
+            for (int i = 0; i < 4; ++i) {
+                const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]), d);
+                const uint32_t u = *reinterpret_cast<const uint32_t*>(&y);
+                w[i] = pack_h(bf_lo(u), bf_hi(u));
             }
-            mma(pt[t], ah, bh[0], bh[1]);
-            mma(pt[t], ah, bl[0], bl[1]);
-            mma(pt[t], al, bh[0], bh[1]);
+            x[c] = make_uint4(w[0], w[1], w[2], w[3]);
         }
+#pragma unroll
+        for (int c = 0; c < P; ++c) *reinterpret_cast<uint4*>(tile + at<DK>(r, half * (DK / 16) + c0 + c)) = x[c];
     }
-    float o[2][4] = {};
-#pragma unroll
-    for (int kt = 0; kt < SIZE / 16; ++kt) {
-        uint32_t ah[4], al[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = *reinterpret_cast<const float2*>(
-                &X[(i0 + mt * 16 + gq + (i & 1) * 8) * XS + i0 + kt * 16 + q2 + (i >> 1) * 8]);
-            split_h(f.x, f.y, ah[i], al[i]);
-        }
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-            uint32_t bh[2], bl[2];
-            split_h(pt[2 * kt][2 * nt], pt[2 * kt][2 * nt + 1], bh[0], bl[0]);
-            split_h(pt[2 * kt + 1][2 * nt], pt[2 * kt + 1][2 * nt + 1], bh[1], bl[1]);
-            mma(o[nt], ah, bh[0], bh[1]);
-            mma(o[nt], ah, bl[0], bl[1]);
-            mma(o[nt], al, bh[0], bh[1]);
-        }
-    }
-    // the merged blocks: into the operand tiles, and for the next size into the scratch
-#pragma unroll
-    for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = i0 + mt * 16 + gq + i * 8, s = j0 + n0 + nt * 8 + q2;
-            const float x = -o[nt][2 * i], y = -o[nt][2 * i + 1];
-            if (SIZE == 16) *reinterpret_cast<float2*>(&sm.x[r * XS + s]) = make_float2(x, y);
-            uint32_t hi, lo;
-            split_h(x, y, hi, lo);
-            *reinterpret_cast<uint32_t*>(sm.t[b][0] + at<C>(r, s >> 3) + (s & 7) * 2) = hi;
-            *reinterpret_cast<uint32_t*>(sm.t[b][1] + at<C>(r, s >> 3) + (s & 7) * 2) = lo;
-        }
 }
 
-// The 16 x 16 blocks on and below the diagonal, by warp: two or three each.
-__device__ __forceinline__ void block_of(int warp, int j, int& bi, int& bj)
+// x, y as fp16 high and low pairs at (r, s), (r, s + 1) of two operand tiles
+__device__ __forceinline__ void put_pair(unsigned char* hi_tile, unsigned char* lo_tile, int r, int s, float x, float y)
 {
-    // (3,0) (3,1) (0,0) | (3,2) (3,3) (1,1) | (2,0) (2,1) | (2,2) (1,0)
-    const int i = warp * 3 + j;
-    bi = (int)((0b00'01'10'00'10'10'01'11'11'00'11'11u >> (2 * i)) & 3);
-    bj = (int)((0b00'00'10'00'01'00'01'11'10'00'01'00u >> (2 * i)) & 3);
+    uint32_t hi, lo;
+    split_h(x, y, hi, lo);
+    const uint32_t o = at<C>(r, s >> 3) + (s & 7) * 2;
+    *reinterpret_cast<uint32_t*>(hi_tile + o) = hi;
+    *reinterpret_cast<uint32_t*>(lo_tile + o) = lo;
 }
 
-// The chunk's P and T into buffer b from the rows in slot `slot`; g, beta: the
-// log decay and beta of row t & 63 (zero for a padded row).
+// Columns n0 .. n0 + 15, rows mt * 16 .. + 15 of  T21 = -T22 (A21 T11)  for the
+// SIZE-blocks at (i0, j0): T11 and T22 are in the operand tiles, A21 in
+// T21's place.
+template <int SIZE> struct Merge {
+    float pt[SIZE / 8][4];  // (A21 T11)^T, rows n: its accumulators are the next product's right operand
+    template <class S> __device__ __forceinline__ void first(S& sm, int b, int i0, int j0, int n0, int lane)
+    {
+        const uint32_t th = ptx::smem_u32(sm.t[b][0]), tl = ptx::smem_u32(sm.t[b][1]);
+        const int brow = (lane & 7) + ((lane >> 4) & 1) * 8, bcol = (lane >> 3) & 1;
+#pragma unroll
+        for (int t = 0; t < SIZE / 8; ++t) pt[t][0] = pt[t][1] = pt[t][2] = pt[t][3] = 0.f;
+#pragma unroll
+        for (int kt = 0; kt < SIZE / 16; ++kt) {
+            uint32_t ah[4], al[4], bh[SIZE / 16][4], bl[SIZE / 16][4];
+            const uint32_t ao = at<C>(j0 + kt * 16 + brow, ((j0 + n0) >> 3) + bcol);
+            ldsm_t(ah, th + ao);
+            ldsm_t(al, tl + ao);
+#pragma unroll
+            for (int t = 0; t < SIZE / 16; ++t) {
+                const uint32_t bo = at<C>(i0 + t * 16 + brow, ((j0 + kt * 16) >> 3) + bcol);
+                ldsm(bh[t], th + bo);
+                ldsm(bl[t], tl + bo);
+            }
+#pragma unroll
+            for (int t = 0; t < SIZE / 8; ++t) mma(pt[t], ah, bh[t >> 1][2 * (t & 1)], bh[t >> 1][2 * (t & 1) + 1]);
+#pragma unroll
+            for (int t = 0; t < SIZE / 8; ++t) mma(pt[t], ah, bl[t >> 1][2 * (t & 1)], bl[t >> 1][2 * (t & 1) + 1]);
+#pragma unroll
+            for (int t = 0; t < SIZE / 8; ++t) mma(pt[t], al, bh[t >> 1][2 * (t & 1)], bh[t >> 1][2 * (t & 1) + 1]);
+        }
+    }
+    template <class S> __device__ __forceinline__ void second(S& sm, int b, int i0, int mt, float (&o)[2][4], int lane)
+    {
+        const uint32_t th = ptx::smem_u32(sm.t[b][0]), tl = ptx::smem_u32(sm.t[b][1]);
+#pragma unroll
+        for (int n = 0; n < 2; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+#pragma unroll
+        for (int kt = 0; kt < SIZE / 16; ++kt) {
+            uint32_t ah[4], al[4], bh[2][2], bl[2][2];
+            const uint32_t ao = at<C>(i0 + mt * 16 + (lane & 15), ((i0 + kt * 16) >> 3) + (lane >> 4));
+            ldsm(ah, th + ao);
+            ldsm(al, tl + ao);
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) split_h(pt[2 * kt + i][2 * n], pt[2 * kt + i][2 * n + 1], bh[n][i], bl[n][i]);
+#pragma unroll
+            for (int n = 0; n < 2; ++n) mma(o[n], ah, bh[n][0], bh[n][1]);
+#pragma unroll
+            for (int n = 0; n < 2; ++n) mma(o[n], ah, bl[n][0], bl[n][1]);
+#pragma unroll
+            for (int n = 0; n < 2; ++n) mma(o[n], al, bh[n][0], bh[n][1]);
+        }
+    }
+    template <class S>
+    __device__ __forceinline__ void store(S& sm, int b, int i0, int j0, int n0, int mt, const float (&o)[2][4], int lane)
+    {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                put_pair(sm.t[b][0], sm.t[b][1], i0 + mt * 16 + (lane >> 2) + i * 8, j0 + n0 + n * 8 + (lane & 3) * 2,
+                         -o[n][2 * i], -o[n][2 * i + 1]);
+    }
+};
+
+// The chunk's P and T into buffer b from the rows in slot `slot`.  The code is
+// kept short (rolled loops): it runs once a chunk beside the other roles', and
+// what does not fit the instruction caches is fetched anew each time.
 template <int DK, int DVT, bool F32, class S>
 __device__ __forceinline__ void prep_chunk(S& sm, int slot, int b, const GdnArgs& a, bool real, int t)
 {
     const int warp = t >> 5, lane = t & 31, gq = lane >> 2, q2 = (lane & 3) * 2;
-    if (warp == 3) scan_rows(sm, b, lane);
-    // K K^T and Q K^T of the raw rows: bf16 values, exact products
     const uint32_t kb = ptx::smem_u32(sm.k[slot]), qb = ptx::smem_u32(sm.q[slot]);
     const int arow = lane & 15, acol = lane >> 4, brow = (lane & 7) + ((lane >> 4) & 1) * 8, bcol = (lane >> 3) & 1;
-    float kk[3][2][4], qk[3][2][4];
-#pragma unroll
-    for (int j = 0; j < 3; ++j) {
-        if (j == 2 && warp >= 2) break;
-        int bi, bj;
-        block_of(warp, j, bi, bj);
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) kk[j][n][i] = qk[j][n][i] = 0.f;
-#pragma unroll
-        for (int kt = 0; kt < DK / 16; ++kt) {
-            uint32_t ka[4], qa[4], bb[4];
-            const uint32_t ao = at<DK>(bi * 16 + arow, kt * 2 + acol);
-            ldsm(ka, kb + ao);
-            ldsm(qa, qb + ao);
-            ldsm(bb, kb + at<DK>(bj * 16 + brow, kt * 2 + bcol));
-            mma_bf(kk[j][0], ka, bb[0], bb[1]);
-            mma_bf(kk[j][1], ka, bb[2], bb[3]);
-            mma_bf(qk[j][0], qa, bb[0], bb[1]);
-            mma_bf(qk[j][1], qa, bb[2], bb[3]);
-        }
-        if (bi == bj) {  // squared norms of k's rows
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                if (q2 == gq) sm.nk[bi * 16 + i * 8 + gq] = kk[j][i][2 * i];
-                if (q2 + 1 == gq) sm.nk[bi * 16 + i * 8 + gq] = kk[j][i][2 * i + 1];
-            }
-        }
-    }
+    if (warp == 7) scan_rows(sm, b, lane);
     {
-        // and of q's
-        float qq[2][4] = {};
+        // squared norms of 16 rows of k (warps 0 - 3) or q: the diagonal of their products (bf16 values, exact)
+        float d[2][4] = {};
+        const uint32_t base = warp < 4 ? kb : qb;
+        const int r0 = (warp & 3) * 16;
 #pragma unroll
         for (int kt = 0; kt < DK / 16; ++kt) {
-            uint32_t qa[4], bb[4];
-            ldsm(qa, qb + at<DK>(warp * 16 + arow, kt * 2 + acol));
-            ldsm(bb, qb + at<DK>(warp * 16 + brow, kt * 2 + bcol));
-            mma_bf(qq[0], qa, bb[0], bb[1]);
-            mma_bf(qq[1], qa, bb[2], bb[3]);
+            uint32_t x[4], y[4];
+            ldsm(x, base + at<DK>(r0 + arow, kt * 2 + acol));
+            ldsm(y, base + at<DK>(r0 + brow, kt * 2 + bcol));
+            mma_bf(d[0], x, y[0], y[1]);
+            mma_bf(d[1], x, y[2], y[3]);
         }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            if (q2 == gq) sm.nq[warp * 16 + i * 8 + gq] = qq[i][2 * i];
-            if (q2 + 1 == gq) sm.nq[warp * 16 + i * 8 + gq] = qq[i][2 * i + 1];
+        if (q2 == (gq & 6)) {
+            float* n = warp < 4 ? sm.nk : sm.nq;
+            n[r0 + gq] = gq & 1 ? d[0][1] : d[0][0];
+            n[r0 + gq + 8] = gq & 1 ? d[1][3] : d[1][2];
         }
     }
     prep_sync();
     {
-        const int r = t & (C - 1);
-        const float ss = t < C ? sm.nk[r] : sm.nq[r];
+        const int r = t & (C - 1), part = t >> 6;  // halves of k's rows, then of q's
+        const float ss = part < 2 ? sm.nk[r] : sm.nq[r];
         float down, up;
         pow2_scale_sqrt(ss, down, up);
+        convert_row<DK>(part < 2 ? sm.k[slot] : sm.q[slot], r, part & 1, down);
         // the factor that makes the stored row the (normalised) row; none for a padded one
-        const float norm = a.l2 ? rsqrtf(ss + a.l2_eps) : 1.f;
-        if (t < C) {
-            const float f = real ? norm * up : 0.f, e = sm.eg[b][r];
+        const float f = real ? (a.l2 ? rsqrtf(ss + a.l2_eps) : 1.f) * up : 0.f;
+        if (part == 0) {
             sm.sk[b][r] = f;
-            sm.ek[b][r] = sm.beta[b][r] * f * e;
-            sm.nk[r] = real ? norm : 0.f;               // raw rows enter A and P
-            sm.bk[r] = real ? sm.beta[b][r] * norm : 0.f;
-        } else sm.oq[b][r] = real ? a.scale * norm * up : 0.f;
-        if (t >= C) sm.nq[r] = down;
-        convert_row<DK>(t < C ? sm.k[slot] : sm.q[slot], r, down);
-        // P = e^{G_r - G_s} q'_r.k'_s on the stored rows' scale: k's part
-        if (t < C) sm.g[r] = down;
+            sm.bk[r] = sm.beta[b][r] * f;
+            sm.ek[b][r] = sm.beta[b][r] * f * sm.eg[b][r];
+        } else if (part == 2) sm.oq[b][r] = a.scale * f;
     }
     prep_sync();
+    // A and P by 16 x 8 tiles on and below the diagonal: twenty over the warps
+#pragma unroll 1
+    for (int h = warp; h < 20; h += 8) {
+        const int blk = h >> 1, bi = blk < 1 ? 0 : blk < 3 ? 1 : blk < 6 ? 2 : 3, bj = blk - bi * (bi + 1) / 2;
+        const int s0 = bj * 16 + (h & 1) * 8, s = s0 + q2;
+        float kk[4] = {}, qk[4] = {};
 #pragma unroll
-    for (int j = 0; j < 3; ++j) {
-        if (j == 2 && warp >= 2) break;
-        int bi, bj;
-        block_of(warp, j, bi, bj);
-        float2 ch[2], cl[2], cn[2], cd[2];
+        for (int kp = 0; kp < DK / 32; ++kp) {
+            uint32_t ka[2][4], qa[2][4], f[4];
+            ldsm(f, kb + at<DK>(s0 + (lane & 7), kp * 4 + (lane >> 3)));
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            const int s = bj * 16 + n * 8 + q2;
-            ch[n] = *reinterpret_cast<const float2*>(&sm.gh[s]);
-            cl[n] = *reinterpret_cast<const float2*>(&sm.gl[s]);
-            cn[n] = *reinterpret_cast<const float2*>(&sm.nk[s]);
-            cd[n] = *reinterpret_cast<const float2*>(&sm.g[s]);
+            for (int z = 0; z < 2; ++z) {
+                const uint32_t ao = at<DK>(bi * 16 + arow, kp * 4 + z * 2 + acol);
+                ldsm(ka[z], kb + ao);
+                ldsm(qa[z], qb + ao);
+            }
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+                mma(kk, ka[z], f[2 * z], f[2 * z + 1]);
+                mma(qk, qa[z], f[2 * z], f[2 * z + 1]);
+            }
         }
+        const float2 ch = *reinterpret_cast<const float2*>(&sm.gh[s]);
+        const float2 cl = *reinterpret_cast<const float2*>(&sm.gl[s]);
+        const float2 cn = *reinterpret_cast<const float2*>(&sm.sk[b][s]);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int r = bi * 16 + gq + i * 8;
-            const float rh = sm.gh[r], rl = sm.gl[r], br = sm.bk[r], qd = sm.nq[r];
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                const int s = bj * 16 + n * 8 + q2;
-                const float d0 = exp_sfu((rh - ch[n].x) + (rl - cl[n].x)), d1 = exp_sfu((rh - ch[n].y) + (rl - cl[n].y));
-                const float a0 = s < r ? (br * cn[n].x) * d0 * kk[j][n][2 * i] : 0.f;
-                const float a1 = s + 1 < r ? (br * cn[n].y) * d1 * kk[j][n][2 * i + 1] : 0.f;
-                const float p0 = s <= r ? (qd * cd[n].x) * d0 * qk[j][n][2 * i] : 0.f;
-                const float p1 = s + 1 <= r ? (qd * cd[n].y) * d1 * qk[j][n][2 * i + 1] : 0.f;
-                *reinterpret_cast<float2*>(&sm.x[r * XS + s]) = make_float2(a0, a1);
-                const uint32_t o = at<C>(r, s >> 3) + (s & 7) * 2;
-                if constexpr (F32) {
-                    uint32_t hi, lo;
-                    split_h(p0, p1, hi, lo);
-                    *reinterpret_cast<uint32_t*>(sm.p[b][0] + o) = hi;
-                    *reinterpret_cast<uint32_t*>(sm.p[b][1] + o) = lo;
-                } else *reinterpret_cast<uint32_t*>(sm.p[b][0] + o) = pack_h(p0, p1);
-            }
+            const float rh = sm.gh[r], rl = sm.gl[r], br = sm.bk[r];
+            const float d0 = s <= r ? exp_sfu((rh - ch.x) + (rl - cl.x)) : 0.f;
+            const float d1 = s < r ? exp_sfu((rh - ch.y) + (rl - cl.y)) : 0.f;
+            const float a0 = s < r ? (br * cn.x) * d0 * kk[2 * i] : 0.f;
+            const float a1 = s + 1 < r ? (br * cn.y) * d1 * kk[2 * i + 1] : 0.f;
+            const float p0 = s <= r ? d0 * qk[2 * i] : 0.f, p1 = s < r ? d1 * qk[2 * i + 1] : 0.f;
+            if (bi == bj) *reinterpret_cast<float2*>(&sm.x[r * XS + (s & 15)]) = make_float2(a0, a1);
+            else put_pair(sm.t[b][0], sm.t[b][1], r, s, a0, a1);
+            if constexpr (F32) put_pair(sm.p[b][0], sm.p[b][1], r, s, p0, p1);
+            else *reinterpret_cast<uint32_t*>(sm.p[b][0] + at<C>(r, s >> 3) + (s & 7) * 2) = pack_h(p0, p1);
         }
     }
     prep_sync();
-    {
-        // the diagonal block of each warp: forward substitution, a column a lane
+    if (warp < 4) {
+        // a diagonal block for each of four warps: forward substitution, a column a lane
+        // (both halves of the warp: one stores the high parts, one the low)
         const int d0 = warp * 16, c = lane & 15;
         float x[16];
 #pragma unroll
@@ -410,7 +394,7 @@ __device__ __forceinline__ void prep_chunk(S& sm, int slot, int b, const GdnArgs
             float acc = i == c ? 1.f : 0.f, acc2 = 0.f;
 #pragma unroll
             for (int m = 0; m < i; m += 4) {
-                const float4 f = *reinterpret_cast<const float4*>(&sm.x[(d0 + i) * XS + d0 + m]);
+                const float4 f = *reinterpret_cast<const float4*>(&sm.x[(d0 + i) * XS + m]);
                 acc = fmaf(-f.x, x[m], acc);
                 if (m + 1 < i) acc2 = fmaf(-f.y, x[m + 1], acc2);
                 if (m + 2 < i) acc = fmaf(-f.z, x[m + 2], acc);
@@ -418,22 +402,33 @@ __device__ __forceinline__ void prep_chunk(S& sm, int slot, int b, const GdnArgs
             }
             x[i] = acc + acc2;
         }
-        __syncwarp();
-        if (lane < 16) {
+        unsigned char* tile = sm.t[b][lane >> 4];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                sm.x[(d0 + i) * XS + d0 + c] = x[i];
-                const __half hi = __float2half_rn(x[i]);
-                const uint32_t o = at<C>(d0 + i, (d0 + c) >> 3) + (c & 7) * 2;
-                *reinterpret_cast<__half*>(sm.t[b][0] + o) = hi;
-                *reinterpret_cast<__half*>(sm.t[b][1] + o) = __float2half_rn(x[i] - __half2float(hi));
-            }
+        for (int i = 0; i < 16; ++i) {
+            const __half hi = __float2half_rn(x[i]);
+            const __half lo = __float2half_rn(x[i] - __half2float(hi));
+            *reinterpret_cast<__half*>(tile + at<C>(d0 + i, (d0 + c) >> 3) + (c & 7) * 2) = lane < 16 ? hi : lo;
         }
     }
     prep_sync();
-    if (warp < 2) merge_panel<16>(sm, b, 16 + warp * 32, warp * 32, 0, 0, lane);
+    float o[2][4];
+    if (warp < 2) {
+        const int j0 = warp * 32, i0 = j0 + 16;
+        Merge<16> g;
+        g.first(sm, b, i0, j0, 0, lane);
+        g.second(sm, b, i0, 0, o, lane);
+        __syncwarp();
+        g.store(sm, b, i0, j0, 0, 0, o, lane);
+    }
     prep_sync();
-    merge_panel<32>(sm, b, 32, 0, (warp & 1) * 16, warp >> 1, lane);
+    if (warp < 4) {
+        Merge<32> g;
+        const int n0 = (warp & 1) * 16, mt = warp >> 1;
+        g.first(sm, b, 32, 0, n0, lane);
+        g.second(sm, b, 32, mt, o, lane);
+        asm volatile("bar.sync 2, 128;" ::: "memory");  // these four warps have read A21
+        g.store(sm, b, 32, 0, n0, mt, o, lane);
+    }
 }
 
 // ------------------------------------------------------------ chain
@@ -476,37 +471,38 @@ __device__ __forceinline__ void chain_chunk(S& sm, int m, float (&s)[DK / 8][4],
     const int trow = lane & 15, tcol = lane >> 4;                                 // transposed operand
     if (m > 0) wait(sm.s_free[warp], m - 1);
 
-    // S^T K^T, each k-tile's fragments loaded a tile ahead
+    // S^T K^T, each k-tile's fragments made a tile ahead
     float r[8][4];
 #pragma unroll
     for (int t = 0; t < 8; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i) r[t][i] = 0.f;
     __half2 m0 = __float2half2_rn(0.f), m1 = m0;
-    uint32_t f[2][4][4];
+    uint32_t f[2][4][4], hi[2][4], lo[2][4];
+    auto left = [&](int kt) {  // k-tile kt of S^T, split, also for the output warp
 #pragma unroll
-    for (int t = 0; t < 4; ++t) ldsm(f[0][t], kb + at<DK>(t * 16 + brow, bcol));
-#pragma unroll
-    for (int kt = 0; kt < DK / 16; ++kt) {
-        if (kt + 1 < DK / 16)
-#pragma unroll
-            for (int t = 0; t < 4; ++t) ldsm(f[(kt + 1) & 1][t], kb + at<DK>(t * 16 + brow, (kt + 1) * 2 + bcol));
-        uint32_t hi[4], lo[4];
+        for (int t = 0; t < 4; ++t) ldsm(f[kt & 1][t], kb + at<DK>(t * 16 + brow, kt * 2 + bcol));
+        uint32_t(&x)[4] = hi[kt & 1], (&y)[4] = lo[kt & 1];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float* x = &s[2 * kt + (i >> 1)][2 * (i & 1)];
-            split_h(x[0], x[1], hi[i], lo[i]);
-            const __half2 h = __habs2(*reinterpret_cast<const __half2*>(&hi[i]));
+            const float* v = &s[2 * kt + (i >> 1)][2 * (i & 1)];
+            split_h(v[0], v[1], x[i], y[i]);
+            const __half2 h = __habs2(*reinterpret_cast<const __half2*>(&x[i]));
             if (i & 1) m1 = __hmax2(m1, h);
             else m0 = __hmax2(m0, h);
         }
-        sm.hs[warp][0][kt][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        if (F32) sm.hs[warp][F32 ? 1 : 0][kt][lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        sm.hs[warp][0][kt][lane] = make_uint4(x[0], x[1], x[2], x[3]);
+        if (F32) sm.hs[warp][F32 ? 1 : 0][kt][lane] = make_uint4(y[0], y[1], y[2], y[3]);
+    };
+    left(0);
+#pragma unroll
+    for (int kt = 0; kt < DK / 16; ++kt) {
+        if (kt + 1 < DK / 16) left(kt + 1);
         uint32_t(&e)[4][4] = f[kt & 1];
 #pragma unroll
-        for (int t = 0; t < 8; ++t) mma(r[t], hi, e[t >> 1][2 * (t & 1)], e[t >> 1][2 * (t & 1) + 1]);
+        for (int t = 0; t < 8; ++t) mma(r[t], hi[kt & 1], e[t >> 1][2 * (t & 1)], e[t >> 1][2 * (t & 1) + 1]);
 #pragma unroll
-        for (int t = 0; t < 8; ++t) mma(r[t], lo, e[t >> 1][2 * (t & 1)], e[t >> 1][2 * (t & 1) + 1]);
+        for (int t = 0; t < 8; ++t) mma(r[t], lo[kt & 1], e[t >> 1][2 * (t & 1)], e[t >> 1][2 * (t & 1) + 1]);
     }
     warp_arrive(sm.s_full[warp], lane);
     // beta (V - e^G k.S), and each column's largest value
@@ -537,25 +533,30 @@ __device__ __forceinline__ void chain_chunk(S& sm, int m, float (&s)[DK / 8][4],
     for (int t = 0; t < 8; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i) u[t][i] = 0.f;
-#pragma unroll
-    for (int kt = 0; kt < 4; ++kt) {
-        uint32_t hi[4], lo[4], th[4][4], tl[4][4];
+    uint32_t f2[2][4][4];
+    auto part = [&](int kt) {
 #pragma unroll
         for (int t = kt; t < 4; ++t) {
-            ldsm(th[t], tb[0] + at<C>(t * 16 + brow, kt * 2 + bcol));
-            ldsm(tl[t], tb[1] + at<C>(t * 16 + brow, kt * 2 + bcol));
+            ldsm(f[kt & 1][t], tb[0] + at<C>(t * 16 + brow, kt * 2 + bcol));
+            ldsm(f2[kt & 1][t], tb[1] + at<C>(t * 16 + brow, kt * 2 + bcol));
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float* x = &r[2 * kt + (i >> 1)][2 * (i & 1)];
-            split_h(x[0] * rd[i & 1], x[1] * rd[i & 1], hi[i], lo[i]);
+            split_h(x[0] * rd[i & 1], x[1] * rd[i & 1], hi[kt & 1][i], lo[kt & 1][i]);
         }
+    };
+    part(0);
 #pragma unroll
-        for (int t = 2 * kt; t < 8; ++t) mma(u[t], hi, th[t >> 1][2 * (t & 1)], th[t >> 1][2 * (t & 1) + 1]);
+    for (int kt = 0; kt < 4; ++kt) {
+        if (kt + 1 < 4) part(kt + 1);
+        uint32_t(&th)[4][4] = f[kt & 1], (&tl)[4][4] = f2[kt & 1], (&x)[4] = hi[kt & 1], (&y)[4] = lo[kt & 1];
 #pragma unroll
-        for (int t = 2 * kt; t < 8; ++t) mma(u[t], lo, th[t >> 1][2 * (t & 1)], th[t >> 1][2 * (t & 1) + 1]);
+        for (int t = 2 * kt; t < 8; ++t) mma(u[t], x, th[t >> 1][2 * (t & 1)], th[t >> 1][2 * (t & 1) + 1]);
 #pragma unroll
-        for (int t = 2 * kt; t < 8; ++t) mma(u[t], hi, tl[t >> 1][2 * (t & 1)], tl[t >> 1][2 * (t & 1) + 1]);
+        for (int t = 2 * kt; t < 8; ++t) mma(u[t], y, th[t >> 1][2 * (t & 1)], th[t >> 1][2 * (t & 1) + 1]);
+#pragma unroll
+        for (int t = 2 * kt; t < 8; ++t) mma(u[t], x, tl[t >> 1][2 * (t & 1)], tl[t >> 1][2 * (t & 1) + 1]);
     }
     // times k's row factor; the largest values with and without the decay to the chunk's end
     float mu[2] = {0.f, 0.f}, mw[2] = {0.f, 0.f};
@@ -590,15 +591,15 @@ __device__ __forceinline__ void chain_chunk(S& sm, int m, float (&s)[DK / 8][4],
     }
 #pragma unroll
     for (int kt = 0; kt < 4; ++kt) {
-        uint32_t hi[4], lo[4];
+        uint32_t x[4], y[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float* x = &u[2 * kt + (i >> 1)][2 * (i & 1)];
-            if (F32) split_h(x[0] * ud[i & 1], x[1] * ud[i & 1], hi[i], lo[i]);
-            else hi[i] = pack_h(x[0] * ud[i & 1], x[1] * ud[i & 1]);
+            const float* v = &u[2 * kt + (i >> 1)][2 * (i & 1)];
+            if (F32) split_h(v[0] * ud[i & 1], v[1] * ud[i & 1], x[i], y[i]);
+            else x[i] = pack_h(v[0] * ud[i & 1], v[1] * ud[i & 1]);
         }
-        sm.hu[warp][0][kt][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        if (F32) sm.hu[warp][F32 ? 1 : 0][kt][lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        sm.hu[warp][0][kt][lane] = make_uint4(x[0], x[1], x[2], x[3]);
+        if (F32) sm.hu[warp][F32 ? 1 : 0][kt][lane] = make_uint4(y[0], y[1], y[2], y[3]);
     }
     warp_arrive(sm.u_full[warp], lane);
     // S^T = e^{G_C} S^T + (U^T diag(e^{G_C - G})) K, in a scale that both terms fit
@@ -610,33 +611,38 @@ __device__ __forceinline__ void chain_chunk(S& sm, int m, float (&s)[DK / 8][4],
         s[t][3] *= dec[1];
     }
     constexpr int G = DK >= 64 ? 4 : 2, NG = DK / 16 / G;  // fragments loaded at a time, and such groups in a k-tile
+    auto right = [&](int step) {
 #pragma unroll
-    for (int t = 0; t < G; ++t) ldsm_t(f[0][t], kb + at<DK>(trow, t * 2 + tcol));
-#pragma unroll
-    for (int kt = 0; kt < 4; ++kt) {
-        uint32_t hi[4], lo[4];
+        for (int t = 0; t < G; ++t)
+            ldsm_t(f[step & 1][t], kb + at<DK>(step / NG * 16 + trow, (step % NG * G + t) * 2 + tcol));
+    };
+    auto decayed = [&](int kt) {
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
             const float2 w = *reinterpret_cast<const float2*>(&sm.w[b][(2 * kt + z) * 8 + q2]);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const float* x = &u[2 * kt + z][2 * i];
-                split_h(x[0] * (w.x * g[i]), x[1] * (w.y * g[i]), hi[2 * z + i], lo[2 * z + i]);
+                split_h(x[0] * (w.x * g[i]), x[1] * (w.y * g[i]), hi[kt & 1][2 * z + i], lo[kt & 1][2 * z + i]);
             }
         }
+    };
+    right(0);
+    decayed(0);
+#pragma unroll
+    for (int kt = 0; kt < 4; ++kt) {
+        if (kt + 1 < 4) decayed(kt + 1);
 #pragma unroll
         for (int n = 0; n < NG; ++n) {
             const int step = kt * NG + n;
-            if (step + 1 < 4 * NG)
-#pragma unroll
-                for (int t = 0; t < G; ++t)
-                    ldsm_t(f[(step + 1) & 1][t],
-                           kb + at<DK>((step + 1) / NG * 16 + trow, ((step + 1) % NG * G + t) * 2 + tcol));
+            if (step + 1 < 4 * NG) right(step + 1);
             uint32_t(&e)[4][4] = f[step & 1];
 #pragma unroll
-            for (int t = 0; t < 2 * G; ++t) mma(s[n * 2 * G + t], hi, e[t >> 1][2 * (t & 1)], e[t >> 1][2 * (t & 1) + 1]);
+            for (int t = 0; t < 2 * G; ++t)
+                mma(s[n * 2 * G + t], hi[kt & 1], e[t >> 1][2 * (t & 1)], e[t >> 1][2 * (t & 1) + 1]);
 #pragma unroll
-            for (int t = 0; t < 2 * G; ++t) mma(s[n * 2 * G + t], lo, e[t >> 1][2 * (t & 1)], e[t >> 1][2 * (t & 1) + 1]);
+            for (int t = 0; t < 2 * G; ++t)
+                mma(s[n * 2 * G + t], lo[kt & 1], e[t >> 1][2 * (t & 1)], e[t >> 1][2 * (t & 1) + 1]);
         }
     }
 }
@@ -657,7 +663,7 @@ __device__ __forceinline__ void output_chunk(S& sm, int m, void* out, long long 
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[t][i] = 0.f;
     wait(sm.s_full[warp], m);
-#pragma unroll
+#pragma unroll 2
     for (int kt = 0; kt < DK / 16; ++kt) {
         const uint4 h4 = sm.hs[warp][0][kt][lane];
         const uint32_t hi[4] = {h4.x, h4.y, h4.z, h4.w};
@@ -778,18 +784,28 @@ __device__ __forceinline__ int ranked_seq(const int32_t* cu, int N, int rank, in
     return *found;
 }
 
+// Sets the register count of the calling warpgroup's threads.
+template <bool UP, int N> __device__ __forceinline__ void set_regs()
+{
+    if constexpr (UP) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+struct RowMaps {
+    CUtensorMap q, k, v;
+};
+
 template <int DK, int NW, bool F32>
-__global__ void __launch_bounds__(NW * 64 + PREP, 1) gdn_chunk_kernel(const GdnArgs a, int dv)
+__global__ void __launch_bounds__(NW * 64 + PREP, 1) gdn_chunk_kernel(const GdnArgs a, const __grid_constant__ RowMaps maps, int dv)
 {
     constexpr int DVT = NW * 16, THREADS = NW * 64 + PREP;
     extern __shared__ __align__(1024) unsigned char dyn[];
     using S = Smem<DK, DVT, F32>;
     S& sm = *reinterpret_cast<S*>(dyn);
-    __shared__ int found;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int parts = dv / DVT;
     const int part = blockIdx.x % parts, h = (blockIdx.x / parts) % a.Hv;
-    const int seq = ranked_seq(a.cu_seqlens, a.N, blockIdx.x / (parts * a.Hv), &found);
+    const int seq = ranked_seq(a.cu_seqlens, a.N, blockIdx.x / (parts * a.Hv), &sm.found);
     int begin, end, slot;
     if (!gdn_unit(a, seq, begin, end, slot)) return;
     const int chunks = (end - begin + C - 1) / C;
@@ -797,9 +813,10 @@ __global__ void __launch_bounds__(NW * 64 + PREP, 1) gdn_chunk_kernel(const GdnA
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            ptx::mbar_init(&sm.ready[i], PREP);
+            ptx::mbar_init(&sm.ready[i], PREP / 32);
             ptx::mbar_init(&sm.done[i], 2 * NW);
         }
+        for (int i = 0; i < 3; ++i) ptx::mbar_init(&sm.loaded[i], 1);
         for (int i = 0; i < NW; ++i) {
             ptx::mbar_init(&sm.s_full[i], 1);
             ptx::mbar_init(&sm.s_free[i], 1);
@@ -808,53 +825,67 @@ __global__ void __launch_bounds__(NW * 64 + PREP, 1) gdn_chunk_kernel(const GdnA
         }
         ptx::fence_mbar_init();
     }
-    for (int i = tid; i < C * XS; i += THREADS) sm.x[i] = 0.f;  // blocks above the diagonal stay zero
+    // T's blocks above the diagonal stay zero
+    for (int i = tid; i < (int)sizeof(sm.t) / 16; i += THREADS)
+        reinterpret_cast<uint4*>(sm.t)[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
     Waiter wait{a.dev_status, false};
 
+    // Registers: the launch gives every thread 128 (NW = 4) or 168; the chain
+    // warps' warpgroup takes what the others leave.
     if (warp >= 2 * NW) {
+        if constexpr (NW == 4) set_regs<false, 104>();
+        else set_regs<false, 144>();
         const int t = tid - NW * 64, hk = h / (a.Hv / a.Hk);
-        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + hk * DK;
-        const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(a.k) + hk * DK;
-        const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v) + h * dv + col0;
         const __nv_bfloat16* ga = static_cast<const __nv_bfloat16*>(a.a) + h;
         const __nv_bfloat16* be = static_cast<const __nv_bfloat16*>(a.b) + h;
-        const float a_log = a.A_log[h], dt = a.dt_bias[h];
-        float graw = 0.f, braw = 0.f;
+        const float ea = expf(a.A_log[h]), dt = a.dt_bias[h];
+        __nv_bfloat16 graw = __float2bfloat16(0.f), braw = graw;  // the next chunk's, as loaded
+        const uint64_t policy = ptx::policy_evict_normal();  // other heads and columns read the same rows
         auto load = [&](int m) {
-            const int r0 = begin + m * C, n = min(C, end - r0), s = m % 3, r = r0 + (t & (C - 1));
-            load_tile<DK>(sm.k[s], k + r0 * a.ks, a.ks, n, t);
-            load_tile<DK>(sm.q[s], q + r0 * a.qs, a.qs, n, t);
-            load_tile<DVT>(sm.v[s], v + r0 * a.vs, a.vs, n, t);
-            ptx::cp_async_commit();
+            const int r0 = begin + m * C, s = m % 3, r = r0 + (t & (C - 1));
+            if (t == PREP - 32) {
+                ptx::mbar_arrive_expect_tx(&sm.loaded[s], C * (2 * DK + DVT) * 2);
+                load_tile<DK>(sm.k[s], &maps.k, hk * DK, r0, &sm.loaded[s], policy);
+                load_tile<DK>(sm.q[s], &maps.q, hk * DK, r0, &sm.loaded[s], policy);
+                load_tile<DVT>(sm.v[s], &maps.v, h * dv + col0, r0, &sm.loaded[s], policy);
+            }
             if (t < C && r < end) {
-                graw = ldv(ga + (size_t)r * a.Hv);
-                braw = ldv(be + (size_t)r * a.Hv);
+                graw = ga[(size_t)r * a.Hv];
+                braw = be[(size_t)r * a.Hv];
             }
         };
         load(0);
         for (int m = 0; m < chunks; ++m) {
             const int b = m & 1;
             const bool real = begin + m * C + (t & (C - 1)) < end;
-            const float g0 = graw, b0 = braw;
+            const float g0 = __bfloat162float(graw), b0 = __bfloat162float(braw);
             if (m >= 2) wait(sm.done[b], (m - 2) >> 1);
             if (t < C) {
-                sm.g[t] = real ? gdn_log_alpha(a_log, g0, dt) : 0.f;
+                sm.g[t] = real ? gdn_log_alpha(ea, g0, dt) : 0.f;
                 sm.beta[b][t] = real ? sigmoidf_(b0) : 0.f;
             }
-            if (m + 1 < chunks) {
-                load(m + 1);
-                ptx::cp_async_wait_prev();
-            } else ptx::cp_async_wait_all();
+            if (m + 1 < chunks) load(m + 1);
+            wait(sm.loaded[m % 3], m / 3);
+            if (begin + m * C + C > end) {
+                // the copies took the next sequence's rows along: zeros instead
+                const int r = t & (C - 1);
+                if (!real && t < C) zero_row<DK>(sm.k[m % 3], r);
+                else if (!real && t < 2 * C) zero_row<DK>(sm.q[m % 3], r);
+                else if (!real && t < 3 * C) zero_row<DVT>(sm.v[m % 3], r);
+            }
             prep_sync();
             prep_chunk<DK, DVT, F32>(sm, m % 3, b, a, real, t);
-            ptx::mbar_arrive(&sm.ready[b]);
+            ptx::fence_proxy_async_smem();  // the rows written above, before a later copy into their place
+            warp_arrive(sm.ready[b], lane);
             prep_sync();  // the scratch and the decays are free again
         }
         return;
     }
 
+    if constexpr (NW == 2) set_regs<true, 208>();
     if (warp >= NW) {
+        if constexpr (NW == 4) set_regs<false, 112>();
         const int w = warp - NW;
         const long long row_stride = (long long)a.Hv * dv;
         const size_t osize = F32 ? 4 : 2;
@@ -863,11 +894,13 @@ __global__ void __launch_bounds__(NW * 64 + PREP, 1) gdn_chunk_kernel(const GdnA
             wait(sm.ready[m & 1], m >> 1);
             output_chunk<DK, DVT, F32>(sm, m, out + (size_t)m * C * row_stride * osize, row_stride,
                                        min(C, end - begin - m * C), wait, w, lane);
+            ptx::fence_proxy_async_smem();  // outputs staged in the V tile
             warp_arrive(sm.done[m & 1], lane);
         }
         return;
     }
 
+    if constexpr (NW == 4) set_regs<true, 184>();
     const size_t sbase = ((size_t)slot * a.Hv + h) * DK * dv + col0 + warp * 16 + (lane >> 2);
     float s[DK / 8][4], ig[2], ms[2] = {0.f, 0.f};
 #pragma unroll
@@ -898,6 +931,20 @@ __global__ void __launch_bounds__(NW * 64 + PREP, 1) gdn_chunk_kernel(const GdnA
             a.state[sbase + (size_t)(t * 8 + (lane & 3) * 2 + (i & 1)) * dv + (i >> 1) * 8] = s[t][i] * ig[i >> 1];
 }
 
+// [T][width] bf16 rows with a row stride; boxes of 64 rows.
+bool encode_rows(CUtensorMap* m, const void* base, long long width, long long stride, int T, int box)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)T};
+    const cuuint64_t strides[1] = {(cuuint64_t)stride * 2};
+    const cuuint32_t boxes[2] = {(cuuint32_t)box, C};
+    const cuuint32_t estr[2] = {1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, boxes, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, box == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int DK, int NW, bool F32> cudaError_t launch(const GdnArgs& a, int dv, cudaStream_t st)
 {
     constexpr int smem = sizeof(Smem<DK, NW * 16, F32>);
@@ -907,7 +954,12 @@ template <int DK, int NW, bool F32> cudaError_t launch(const GdnArgs& a, int dv,
         return cudaFuncSetAttribute(gdn_chunk_kernel<DK, NW, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     });
     if (e != cudaSuccess) return e;
-    gdn_chunk_kernel<DK, NW, F32><<<a.N * a.Hv * (dv / (NW * 16)), NW * 64 + PREP, smem, st>>>(a, dv);
+    RowMaps maps;
+    if (!encode_rows(&maps.q, a.q, (long long)a.Hk * DK, a.qs, a.T, std::min(DK, 64)) ||
+        !encode_rows(&maps.k, a.k, (long long)a.Hk * DK, a.ks, a.T, std::min(DK, 64)) ||
+        !encode_rows(&maps.v, a.v, (long long)a.Hv * dv, a.vs, a.T, std::min(NW * 16, 64)))
+        return cudaErrorInvalidValue;
+    gdn_chunk_kernel<DK, NW, F32><<<a.N * a.Hv * (dv / (NW * 16)), NW * 64 + PREP, smem, st>>>(a, maps, dv);
     return cudaGetLastError();
 }
 
