@@ -9,25 +9,31 @@
 // All exponents are differences that are <= 0.
 //
 // A CTA owns one (sequence, value head, DVT columns of dv); nothing crosses
-// columns, so these never meet.  Three roles:
-//   - prep warps (8): load the chunk's rows, normalise and rescale them, form
-//     P and T (state-independent), one chunk ahead of
-//   - chain warps (NW): each keeps S^T for 16 columns in registers as the
+// columns, so these never meet.  Sixteen warps in four roles, a chunk apart:
+//   - a loader: rows by tensor copies, and the raw products [K; Q] [K; Q]^T of
+//     the next chunk as one tcgen05 product into TMEM (k.k, q.k and, on the
+//     diagonal, both squared norms);
+//   - eight prep warps, one row of [K; Q] a lane: the norms, P and A from
+//     those, then T by forward substitution of the 16 x 16 diagonal blocks and
+//     doubling; k and q rescaled in place;
+//   - NW chain warps: each keeps S^T for 16 columns in registers as the
 //     accumulator of a 16 x dk product and walks the chunks alone: S^T K^T,
-//     R^T T^T (R = beta (V - ..)) and U^T K take their left operand straight from
-//     the accumulators of the product before (the two fragment layouts agree),
-//     so no chain warp ever waits for another one;
-//   - output warps (NW): take S^T and U^T of one chain warp each through shared
-//     memory, form Q S and P U and store the outputs beside the chain.
+//     R^T T^T (R = beta (V - ..)) and U^T K take their left operand straight
+//     from the accumulators of the product before (the two fragment layouts
+//     agree), so no chain warp ever waits for another one;
+//   - an issuer and two output warps: Q S and P U as tcgen05 products of the
+//     tiles that chain and prep leave, and the outputs' rows from TMEM.
 //
 // Precision: the state keeps fp32 accuracy.  One decay per head leaves k and q
 // unscaled inside every product, so the rows' bf16 values are operands without
 // loss: prep rescales each row by a power of two to a norm in [1, 2) and stores
-// it as fp16 (exact down to 2^-17).  Every other operand that
-// reaches the state is two fp16 values, high and low, about 22 bits: S and
-// U and V - .. are scaled by a power of two per column so that the low part stays
-// in fp16's range.  P and the outputs' reading of S keep the high part only
-// where the outputs are bf16 (11 bits against their 8).
+// it as fp16 (exact down to 2^-17).  Every other operand that reaches the state
+// is two fp16 values, high and low, about 22 bits: S and U and V - .. are scaled
+// by a power of two per column so that the low part stays in fp16's range.  P
+// and the outputs' reading of S and U keep the high part only where the
+// outputs are bf16 (11 bits against their 8).
+#include <cstddef>
+
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_fp16.h>
@@ -39,21 +45,17 @@ namespace kda {
 namespace {
 
 constexpr int C = 64;
-constexpr int PREP = 256;  // prep threads
-constexpr int XS = 20;     // row stride of the fp32 diagonal blocks
+constexpr int THREADS = 512;
+constexpr int PREP_WARP = 8, PREP = 256;  // first prep warp, prep threads
+constexpr int XS = 20;                    // row stride of the fp32 diagonal blocks
+// TMEM columns: two raw products of 128, Q S, P U
+constexpr int TM_PROD = 0, TM_QS = 256, TM_PU = 320, TM_COLS = 512;
 
 // ------------------------------------------------------------ fragments
 
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-// the same on bf16 values
-__device__ __forceinline__ void mma_bf(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
-{
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -71,10 +73,10 @@ __device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t addr)
                  : "r"(addr)
                  : "memory");
 }
-__device__ __forceinline__ void stsm_t(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+__device__ __forceinline__ void stsm(uint32_t addr, const uint32_t (&r)[4])
 {
-    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b),
-                 "r"(c), "r"(d)
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3])
                  : "memory");
 }
 __device__ __forceinline__ uint32_t pack_h(float x, float y)
@@ -93,13 +95,22 @@ __device__ __forceinline__ void split_h(float x, float y, uint32_t& hi, uint32_t
 __device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
 
-// Byte offset of 16-byte piece `c` of row `r` in a tile of 64 rows of W 16-bit
-// values, as a tensor copy with 128-byte (W >= 64: 64 values a row, one such
-// tile after the other) or 64-byte (W = 32) swizzle leaves it: eight rows' same
-// piece lie in distinct banks.
-template <int W> __device__ __forceinline__ uint32_t at(int r, int c)
+// Byte offsets of 16-byte piece `c` of row `r` in the tiles, all with 128-byte
+// rows, pieces permuted within eight rows (as a tensor copy with the 128-byte
+// swizzle leaves them and the tensor core's descriptors expect them), so that
+// eight rows' same piece lie in distinct banks.
+__device__ __forceinline__ uint32_t tile_at(int r, int c) { return (uint32_t)(r * 128 + (((c ^ r) & 7) << 4)); }
+// [K; Q]: 128 rows, 64 values wide, one such tile after the other
+__device__ __forceinline__ uint32_t kq_at(int r, int c) { return (uint32_t)((c >> 3) * 16384) + tile_at(r, c); }
+// the same with ROWS rows
+template <int ROWS> __device__ __forceinline__ uint32_t half_at(int r, int c)
 {
-    if constexpr (W >= 64) return (uint32_t)((c >> 3) * (C * 128) + r * 128 + (((c ^ r) & 7) << 4));
+    return (uint32_t)((c >> 3) * ROWS * 128) + tile_at(r, c);
+}
+// V: 64 rows of W values; 64-byte rows with the 64-byte swizzle where W = 32
+template <int W> __device__ __forceinline__ uint32_t v_at(int r, int c)
+{
+    if constexpr (W == 64) return tile_at(r, c);
     else return (uint32_t)(r * 64 + ((c ^ (r >> 1)) & 3) * 16);
 }
 
@@ -119,48 +130,75 @@ __device__ __forceinline__ void pow2_scale_sqrt(float m, float& down, float& up)
     up = __uint_as_float((uint32_t)(127 + e) << 23);
 }
 
+__device__ __forceinline__ float exp2_sfu(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // ------------------------------------------------------------ shared memory
 
 template <int DK, int DVT, bool F32> struct Smem {
-    static constexpr int NW = DVT / 16, PARTS = F32 ? 2 : 1;
-    unsigned char k[3][C * DK * 2];        // bf16 rows, then fp16
-    unsigned char q[3][C * DK * 2];
-    unsigned char v[3][C * DVT * 2];       // bf16; an output warp's columns take its outputs afterwards
-    unsigned char t[2][2][C * C * 2];      // T, high and low
-    unsigned char p[2][PARTS][C * C * 2];
-    uint4 hs[NW][PARTS][DK / 16][32];      // S^T as left-operand fragments, from a chain warp to its output warp
-    uint4 hu[NW][PARTS][4][32];            // U^T likewise
-    float4 hf[NW][8];                      // and their scales
-    float x[C * XS];                       // A's diagonal blocks, 16 x 16 each
-    // per chunk row: beta; beta sk e^G; sk; e^{G_C - G}; e^G; scale sq
-    float beta[2][C], ek[2][C], sk[2][C], w[2][C], eg[2][C], oq[2][C];
+    static constexpr int PARTS = F32 ? 2 : 1;
+    static constexpr int HALVES = DK <= 64 ? 1 : DK / 64;  // 64-wide tiles a row spans (dk = 32: half of one)
+    unsigned char kq[3][HALVES * 16384];   // bf16 rows of k, then q; fp16 later
+    unsigned char v[3][C * DVT * 2];
+    // T high, P high, T low (and P low): 64 x 64 fp16 tiles; T over P is one 128-row operand
+    unsigned char tp[2][(2 + PARTS) * 8192];
+    unsigned char st[PARTS][HALVES * DVT * 128];  // S^T: a row a column of dv
+    unsigned char ut[PARTS][DVT * 128];           // U^T likewise
+    // read four at a time: each on a 16-byte boundary
+    alignas(16) float x[C * XS];           // A's diagonal blocks, 16 x 16 each
+    // per chunk row: beta; beta sk e^G; sk; e^{G_C - G}; scale sq e^G; scale sq
+    float beta[2][C], ek[2][C], sk[2][C], w[2][C], e1[2][C], e2[2][C];
+    alignas(16) float f1[2][DVT], f2[2][DVT];  // the scales of S^T's and U^T's columns
+    alignas(16) float eg[C], gh[C], gl[C];  // e^G and G / ln 2 in two words
+    alignas(16) float norm[2 * C];         // squared norms of k's and q's rows
+    alignas(16) float row[2 * C], colk[C], down[2 * C];  // factors of A's and P's rows, of A's columns; of the stored rows
     float last[2];                         // e^{G_C}
-    float g[C], gh[C], gl[C], bk[C], nk[C], nq[C];
-    uint64_t loaded[3], ready[2], done[2]; // a chunk's rows; its operands; their last use
+    uint64_t loaded[3], kv_free[3];        // a chunk's rows; their last use
+    uint64_t prod_full[2], prod_free[2];   // raw products
+    uint64_t ready[2], tp_free[2];         // T, P and the factors; their last use
+    uint64_t s_full, s_free, u_full[2];    // S^T's tile; U^T's
+    uint64_t o_full, o_free;               // Q S and P U in TMEM (which frees U^T's tile); read
+    uint32_t tmem;
     int found;
-    uint64_t s_full[NW], s_free[NW], u_full[NW], u_free[NW];
+
+    __device__ __forceinline__ unsigned char* t_hi(int b) { return tp[b]; }
+    __device__ __forceinline__ unsigned char* t_lo(int b) { return tp[b] + 16384; }
 };
 
 __device__ __forceinline__ void prep_sync() { asm volatile("bar.sync 1, %0;" ::"n"(PREP) : "memory"); }
+// the four warps that invert T
+__device__ __forceinline__ void invert_sync() { asm volatile("bar.sync 2, 128;" ::: "memory"); }
+
+// A bounded wait that gives up once: later ones are skipped, the status word says so.
+struct Waiter {
+    int32_t* dev_status;
+    bool dead;
+    __device__ __forceinline__ void operator()(uint64_t& bar, int phase)
+    {
+        if (!dead && !ptx::mbar_wait(&bar, phase & 1, 1u << 22)) {
+            dead = true;
+            flag_status(dev_status, KDA_DEV_TIMEOUT);
+        }
+    }
+};
+
+__device__ __forceinline__ void warp_arrive(uint64_t& bar, int lane)
+{
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(&bar);
+}
+
+__device__ __forceinline__ float quad_max(float x)
+{
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+    return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+}
 
 // ------------------------------------------------------------ prep
-
-// Starts the copy of 64 rows from row r0, W values from column x, of a row
-// tensor (rows past the tensor: zeros).
-template <int W>
-__device__ __forceinline__ void load_tile(unsigned char* tile, const CUtensorMap* map, int x, int r0, uint64_t* bar,
-                                          uint64_t policy)
-{
-    constexpr int B = W >= 64 ? 64 : W;  // values a box is wide
-#pragma unroll
-    for (int i = 0; i < W / B; ++i) ptx::tma_load_2d(tile + i * C * B * 2, map, x + i * B, r0, bar, policy);
-}
-
-template <int W> __device__ __forceinline__ void zero_row(unsigned char* tile, int r)
-{
-#pragma unroll 1
-    for (int c = 0; c < W / 8; ++c) *reinterpret_cast<uint4*>(tile + at<W>(r, c)) = make_uint4(0, 0, 0, 0);
-}
 
 // (h, l) += (oh, ol) in double-word fp32
 __device__ __forceinline__ void dw_add(float& h, float& l, float oh, float ol)
@@ -172,14 +210,13 @@ __device__ __forceinline__ void dw_add(float& h, float& l, float oh, float ol)
     l = __fsub_rn(r, __fsub_rn(h, s));
 }
 
-// One warp: running sums of the chunk's log decays, two rows a lane (double
-// word: differences of large sums keep their small part).
-template <class S> __device__ __forceinline__ void scan_rows(S& sm, int b, int lane)
+// One warp, rows 2 lane and 2 lane + 1 of a chunk: running sums of their log2
+// decays g (double word: differences of large sums keep their small part).
+template <class S> __device__ __forceinline__ void scan_rows(S& sm, int b, float2 g, int lane)
 {
-    const float2 g = *reinterpret_cast<const float2*>(&sm.g[2 * lane]);
     float h = g.x, l = 0.f;
     dw_add(h, l, g.y, 0.f);
-#pragma unroll 1
+#pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const float oh = __shfl_up_sync(0xffffffffu, h, o), ol = __shfl_up_sync(0xffffffffu, l, o);
         if (lane >= o) dw_add(h, l, oh, ol);
@@ -190,35 +227,35 @@ template <class S> __device__ __forceinline__ void scan_rows(S& sm, int b, int l
     dw_add(ph, pl, g.x, 0.f);  // the lane's first row
     *reinterpret_cast<float2*>(&sm.gh[2 * lane]) = make_float2(ph, h);
     *reinterpret_cast<float2*>(&sm.gl[2 * lane]) = make_float2(pl, l);
-    *reinterpret_cast<float2*>(&sm.eg[b][2 * lane]) = make_float2(exp_sfu(ph + pl), exp_sfu(h + l));
+    *reinterpret_cast<float2*>(&sm.eg[2 * lane]) = make_float2(exp2_sfu(ph + pl), exp2_sfu(h + l));
     *reinterpret_cast<float2*>(&sm.w[b][2 * lane]) =
-        make_float2(exp_sfu((th - ph) + (tl - pl)), exp_sfu((th - h) + (tl - l)));
-    if (lane == 0) sm.last[b] = exp_sfu(th + tl);
+        make_float2(exp2_sfu((th - ph) + (tl - pl)), exp2_sfu((th - h) + (tl - l)));
+    if (lane == 0) sm.last[b] = exp2_sfu(th + tl);
 }
 
-// Half a row of a tile: bf16 -> fp16 times a power of two, in place.
-template <int DK> __device__ __forceinline__ void convert_row(unsigned char* tile, int r, int half, float down)
+// A row of [K; Q]: bf16 -> fp16 times a power of two, in place; zeros for a
+// padded row (the copies took the next sequence's along).
+template <int DK> __device__ __forceinline__ void convert_row(unsigned char* tile, int r, float down, bool real)
 {
     const __nv_bfloat162 d = __float2bfloat162_rn(down);
-    constexpr int P = DK / 16 < 4 ? DK / 16 : 4;  // pieces in flight
 #pragma unroll
-    for (int c0 = 0; c0 < DK / 16; c0 += P) {
-        uint4 x[P];
+    for (int c0 = 0; c0 < DK / 8; c0 += 4) {
+        uint4 x[4];
 #pragma unroll
-        for (int c = 0; c < P; ++c) x[c] = *reinterpret_cast<const uint4*>(tile + at<DK>(r, half * (DK / 16) + c0 + c));
+        for (int c = 0; c < 4; ++c) x[c] = *reinterpret_cast<const uint4*>(tile + kq_at(r, c0 + c));
 #pragma unroll
-        for (int c = 0; c < P; ++c) {
+        for (int c = 0; c < 4; ++c) {
             uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]), d);
                 const uint32_t u = *reinterpret_cast<const uint32_t*>(&y);
-                w[i] = pack_h(bf_lo(u), bf_hi(u));
+                w[i] = real ? pack_h(bf_lo(u), bf_hi(u)) : 0u;
             }
             x[c] = make_uint4(w[0], w[1], w[2], w[3]);
         }
 #pragma unroll
-        for (int c = 0; c < P; ++c) *reinterpret_cast<uint4*>(tile + at<DK>(r, half * (DK / 16) + c0 + c)) = x[c];
+        for (int c = 0; c < 4; ++c) *reinterpret_cast<uint4*>(tile + kq_at(r, c0 + c)) = x[c];
     }
 }
 
@@ -227,7 +264,7 @@ __device__ __forceinline__ void put_pair(unsigned char* hi_tile, unsigned char* 
 {
     uint32_t hi, lo;
     split_h(x, y, hi, lo);
-    const uint32_t o = at<C>(r, s >> 3) + (s & 7) * 2;
+    const uint32_t o = tile_at(r, s >> 3) + (s & 7) * 2;
     *reinterpret_cast<uint32_t*>(hi_tile + o) = hi;
     *reinterpret_cast<uint32_t*>(lo_tile + o) = lo;
 }
@@ -239,19 +276,19 @@ template <int SIZE> struct Merge {
     float pt[SIZE / 8][4];  // (A21 T11)^T, rows n: its accumulators are the next product's right operand
     template <class S> __device__ __forceinline__ void first(S& sm, int b, int i0, int j0, int n0, int lane)
     {
-        const uint32_t th = ptx::smem_u32(sm.t[b][0]), tl = ptx::smem_u32(sm.t[b][1]);
+        const uint32_t th = ptx::smem_u32(sm.t_hi(b)), tl = ptx::smem_u32(sm.t_lo(b));
         const int brow = (lane & 7) + ((lane >> 4) & 1) * 8, bcol = (lane >> 3) & 1;
 #pragma unroll
         for (int t = 0; t < SIZE / 8; ++t) pt[t][0] = pt[t][1] = pt[t][2] = pt[t][3] = 0.f;
 #pragma unroll
         for (int kt = 0; kt < SIZE / 16; ++kt) {
             uint32_t ah[4], al[4], bh[SIZE / 16][4], bl[SIZE / 16][4];
-            const uint32_t ao = at<C>(j0 + kt * 16 + brow, ((j0 + n0) >> 3) + bcol);
+            const uint32_t ao = tile_at(j0 + kt * 16 + brow, ((j0 + n0) >> 3) + bcol);
             ldsm_t(ah, th + ao);
             ldsm_t(al, tl + ao);
 #pragma unroll
             for (int t = 0; t < SIZE / 16; ++t) {
-                const uint32_t bo = at<C>(i0 + t * 16 + brow, ((j0 + kt * 16) >> 3) + bcol);
+                const uint32_t bo = tile_at(i0 + t * 16 + brow, ((j0 + kt * 16) >> 3) + bcol);
                 ldsm(bh[t], th + bo);
                 ldsm(bl[t], tl + bo);
             }
@@ -265,13 +302,13 @@ template <int SIZE> struct Merge {
     }
     template <class S> __device__ __forceinline__ void second(S& sm, int b, int i0, int mt, float (&o)[2][4], int lane)
     {
-        const uint32_t th = ptx::smem_u32(sm.t[b][0]), tl = ptx::smem_u32(sm.t[b][1]);
+        const uint32_t th = ptx::smem_u32(sm.t_hi(b)), tl = ptx::smem_u32(sm.t_lo(b));
 #pragma unroll
         for (int n = 0; n < 2; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
 #pragma unroll
         for (int kt = 0; kt < SIZE / 16; ++kt) {
             uint32_t ah[4], al[4], bh[2][2], bl[2][2];
-            const uint32_t ao = at<C>(i0 + mt * 16 + (lane & 15), ((i0 + kt * 16) >> 3) + (lane >> 4));
+            const uint32_t ao = tile_at(i0 + mt * 16 + (lane & 15), ((i0 + kt * 16) >> 3) + (lane >> 4));
             ldsm(ah, th + ao);
             ldsm(al, tl + ao);
 #pragma unroll
@@ -293,170 +330,164 @@ template <int SIZE> struct Merge {
         for (int n = 0; n < 2; ++n)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-                put_pair(sm.t[b][0], sm.t[b][1], i0 + mt * 16 + (lane >> 2) + i * 8, j0 + n0 + n * 8 + (lane & 3) * 2,
+                put_pair(sm.t_hi(b), sm.t_lo(b), i0 + mt * 16 + (lane >> 2) + i * 8, j0 + n0 + n * 8 + (lane & 3) * 2,
                          -o[n][2 * i], -o[n][2 * i + 1]);
     }
 };
 
-// The chunk's P and T into buffer b from the rows in slot `slot`.  The code is
-// kept short (rolled loops): it runs once a chunk beside the other roles', and
-// what does not fit the instruction caches is fetched anew each time.
-template <int DK, int DVT, bool F32, class S>
-__device__ __forceinline__ void prep_chunk(S& sm, int slot, int b, const GdnArgs& a, bool real, int t)
+// x[lane]
+__device__ __forceinline__ float pick(const float (&x)[32], int lane)
 {
-    const int warp = t >> 5, lane = t & 31, gq = lane >> 2, q2 = (lane & 3) * 2;
-    const uint32_t kb = ptx::smem_u32(sm.k[slot]), qb = ptx::smem_u32(sm.q[slot]);
-    const int arow = lane & 15, acol = lane >> 4, brow = (lane & 7) + ((lane >> 4) & 1) * 8, bcol = (lane >> 3) & 1;
-    if (warp == 7) scan_rows(sm, b, lane);
-    {
-        // squared norms of 16 rows of k (warps 0 - 3) or q: the diagonal of their products (bf16 values, exact)
-        float d[2][4] = {};
-        const uint32_t base = warp < 4 ? kb : qb;
-        const int r0 = (warp & 3) * 16;
+    float y = x[0];
 #pragma unroll
-        for (int kt = 0; kt < DK / 16; ++kt) {
-            uint32_t x[4], y[4];
-            ldsm(x, base + at<DK>(r0 + arow, kt * 2 + acol));
-            ldsm(y, base + at<DK>(r0 + brow, kt * 2 + bcol));
-            mma_bf(d[0], x, y[0], y[1]);
-            mma_bf(d[1], x, y[2], y[3]);
+    for (int i = 1; i < 32; ++i) y = i == lane ? x[i] : y;
+    return y;
+}
+
+// Chunk m of prep warp w (n rows of it are real).  Lane and w & 3 give the
+// row of [K; Q] whose products the warp reads, w >> 2 which half of k's rows it reads them
+// against; the halves above the diagonal (w = 4 and 6) are left out.
+template <int DK, int DVT, bool F32, class S>
+__device__ __forceinline__ void prep_chunk(S& sm, int m, const GdnArgs& a, int n, float2 g, float2 beta, Waiter& wait,
+                                           uint32_t tmem, int w, int lane)
+{
+    const int b = m & 1, slot = m % 3;
+    const int lr = (w & 3) * 32 + lane, r = lr & (C - 1), type = lr >> 6, s0 = (w >> 2) * 32;  // type 0: k, 1: q
+    float d[32];
+    if (m >= 2) wait(sm.tp_free[b], (m - 2) >> 1);
+    if (w == 4) {
+        *reinterpret_cast<float2*>(&sm.beta[b][2 * lane]) = beta;
+        scan_rows(sm, b, g, lane);
+    } else {
+        wait(sm.prod_full[b], m >> 1);
+        ptx::tc_fence_after();
+        const uint32_t at = tmem + ((uint32_t)((w & 3) * 32) << 16) + TM_PROD + b * 128;
+        if (w >= 6) {  // q's norms: columns of q
+            ptx::tmem_ld32(at + C + (w & 1) * 32, d);
+            sm.norm[lr] = pick(d, lane);
         }
-        if (q2 == (gq & 6)) {
-            float* n = warp < 4 ? sm.nk : sm.nq;
-            n[r0 + gq] = gq & 1 ? d[0][1] : d[0][0];
-            n[r0 + gq + 8] = gq & 1 ? d[1][3] : d[1][2];
-        }
+        if (w != 6) ptx::tmem_ld32(at + s0, d);
+        if (w == 0 || w == 5) sm.norm[lr] = pick(d, lane);  // k's
+        ptx::tc_fence_before();
     }
+    warp_arrive(sm.prod_free[b], lane);
     prep_sync();
-    {
-        const int r = t & (C - 1), part = t >> 6;  // halves of k's rows, then of q's
-        const float ss = part < 2 ? sm.nk[r] : sm.nq[r];
+    if (w < 4) {
+        const float ss = sm.norm[lr];
         float down, up;
         pow2_scale_sqrt(ss, down, up);
-        convert_row<DK>(part < 2 ? sm.k[slot] : sm.q[slot], r, part & 1, down);
         // the factor that makes the stored row the (normalised) row; none for a padded one
-        const float f = real ? (a.l2 ? rsqrtf(ss + a.l2_eps) : 1.f) * up : 0.f;
-        if (part == 0) {
+        const float nrm = r < n ? (a.l2 ? rsqrtf(ss + a.l2_eps) : 1.f) : 0.f, f = nrm * up;
+        sm.down[lr] = down;
+        if (type == 0) {
+            const float be = sm.beta[b][r];
             sm.sk[b][r] = f;
-            sm.bk[r] = sm.beta[b][r] * f;
-            sm.ek[b][r] = sm.beta[b][r] * f * sm.eg[b][r];
-        } else if (part == 2) sm.oq[b][r] = a.scale * f;
+            sm.ek[b][r] = be * f * sm.eg[r];
+            sm.colk[r] = nrm;  // A comes from the raw rows' products
+            sm.row[r] = be * nrm;
+        } else {
+            sm.e1[b][r] = a.scale * f * sm.eg[r];
+            sm.e2[b][r] = a.scale * f;
+            sm.row[lr] = down;  // P is that of the stored rows
+        }
     }
     prep_sync();
-    // A and P by 16 x 8 tiles on and below the diagonal: twenty over the warps
+    if (w != 4 && w != 6) {
+        // the lane's row of A (beta_r |..| e^{G_r - G_s} k_r.k_s) or P, zero from the diagonal (or past it) on
+        const float rh = sm.gh[r], rl = sm.gl[r], rf = sm.row[lr];
+        const float* cf = type == 0 ? sm.colk : sm.down;
+        const int lim = r < n ? r + type : 0;
+        unsigned char* hi_tile = sm.tp[b];
+        unsigned char* lo_tile = sm.tp[b] + 16384;
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            uint32_t hi[4], lo[4];
+            float v[8];
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+                const int s = s0 + p * 8 + z * 4;
+                const float4 ch = *reinterpret_cast<const float4*>(&sm.gh[s]);
+                const float4 cl = *reinterpret_cast<const float4*>(&sm.gl[s]);
+                const float4 c4 = *reinterpret_cast<const float4*>(&cf[s]);
+                const float h4[4] = {ch.x, ch.y, ch.z, ch.w}, l4[4] = {cl.x, cl.y, cl.z, cl.w}, f4[4] = {c4.x, c4.y, c4.z, c4.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float e = exp2_sfu((rh - h4[i]) + (rl - l4[i]));
+                    v[z * 4 + i] = s + i < lim ? (rf * f4[i]) * e * d[p * 8 + z * 4 + i] : 0.f;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) split_h(v[2 * i], v[2 * i + 1], hi[i], lo[i]);
+            const int c = (s0 >> 3) + p;
+            *reinterpret_cast<uint4*>(hi_tile + tile_at(lr, c)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            if (F32 || type == 0) *reinterpret_cast<uint4*>(lo_tile + tile_at(lr, c)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            if (type == 0 && (r >> 4) == (c >> 1)) {
+                float* x = &sm.x[r * XS + (c & 1) * 8];
+                *reinterpret_cast<float4*>(x) = make_float4(v[0], v[1], v[2], v[3]);
+                *reinterpret_cast<float4*>(x + 4) = make_float4(v[4], v[5], v[6], v[7]);
+            }
+        }
+    }
+    prep_sync();
+    if (w >= 4) {
+        // meanwhile the rows themselves
+        const int row = (w - 4) * 32 + lane, rr = row & (C - 1);
+        wait(sm.loaded[slot], m / 3);
+        convert_row<DK>(sm.kq[slot], row, sm.down[row], rr < n);
+        if (row < C && rr >= n)
 #pragma unroll 1
-    for (int h = warp; h < 20; h += 8) {
-        const int blk = h >> 1, bi = blk < 1 ? 0 : blk < 3 ? 1 : blk < 6 ? 2 : 3, bj = blk - bi * (bi + 1) / 2;
-        const int s0 = bj * 16 + (h & 1) * 8, s = s0 + q2;
-        float kk[4] = {}, qk[4] = {};
+            for (int c = 0; c < DVT / 8; ++c)
+                *reinterpret_cast<uint4*>(sm.v[slot] + v_at<DVT>(rr, c)) = make_uint4(0, 0, 0, 0);
+    } else {
+        {
+            // a diagonal block a warp: forward substitution, a column a lane (both
+            // halves of the warp: one stores the high parts, one the low)
+            const int d0 = w * 16, c = lane & 15;
+            float x[16];
 #pragma unroll
-        for (int kp = 0; kp < DK / 32; ++kp) {
-            uint32_t ka[2][4], qa[2][4], f[4];
-            ldsm(f, kb + at<DK>(s0 + (lane & 7), kp * 4 + (lane >> 3)));
+            for (int i = 0; i < 16; ++i) {
+                float acc = i == c ? 1.f : 0.f, acc2 = 0.f;
 #pragma unroll
-            for (int z = 0; z < 2; ++z) {
-                const uint32_t ao = at<DK>(bi * 16 + arow, kp * 4 + z * 2 + acol);
-                ldsm(ka[z], kb + ao);
-                ldsm(qa[z], qb + ao);
+                for (int j = 0; j < i; j += 4) {
+                    const float4 f = *reinterpret_cast<const float4*>(&sm.x[(d0 + i) * XS + j]);
+                    acc = fmaf(-f.x, x[j], acc);
+                    if (j + 1 < i) acc2 = fmaf(-f.y, x[j + 1], acc2);
+                    if (j + 2 < i) acc = fmaf(-f.z, x[j + 2], acc);
+                    if (j + 3 < i) acc2 = fmaf(-f.w, x[j + 3], acc2);
+                }
+                x[i] = acc + acc2;
             }
+            unsigned char* tile = lane < 16 ? sm.t_hi(b) : sm.t_lo(b);
 #pragma unroll
-            for (int z = 0; z < 2; ++z) {
-                mma(kk, ka[z], f[2 * z], f[2 * z + 1]);
-                mma(qk, qa[z], f[2 * z], f[2 * z + 1]);
+            for (int i = 0; i < 16; ++i) {
+                const __half hi = __float2half_rn(x[i]);
+                const __half lo = __float2half_rn(x[i] - __half2float(hi));
+                *reinterpret_cast<__half*>(tile + tile_at(d0 + i, (d0 + c) >> 3) + (c & 7) * 2) = lane < 16 ? hi : lo;
             }
         }
-        const float2 ch = *reinterpret_cast<const float2*>(&sm.gh[s]);
-        const float2 cl = *reinterpret_cast<const float2*>(&sm.gl[s]);
-        const float2 cn = *reinterpret_cast<const float2*>(&sm.sk[b][s]);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = bi * 16 + gq + i * 8;
-            const float rh = sm.gh[r], rl = sm.gl[r], br = sm.bk[r];
-            const float d0 = s <= r ? exp_sfu((rh - ch.x) + (rl - cl.x)) : 0.f;
-            const float d1 = s < r ? exp_sfu((rh - ch.y) + (rl - cl.y)) : 0.f;
-            const float a0 = s < r ? (br * cn.x) * d0 * kk[2 * i] : 0.f;
-            const float a1 = s + 1 < r ? (br * cn.y) * d1 * kk[2 * i + 1] : 0.f;
-            const float p0 = s <= r ? d0 * qk[2 * i] : 0.f, p1 = s < r ? d1 * qk[2 * i + 1] : 0.f;
-            if (bi == bj) *reinterpret_cast<float2*>(&sm.x[r * XS + (s & 15)]) = make_float2(a0, a1);
-            else put_pair(sm.t[b][0], sm.t[b][1], r, s, a0, a1);
-            if constexpr (F32) put_pair(sm.p[b][0], sm.p[b][1], r, s, p0, p1);
-            else *reinterpret_cast<uint32_t*>(sm.p[b][0] + at<C>(r, s >> 3) + (s & 7) * 2) = pack_h(p0, p1);
+        invert_sync();
+        float o[2][4];
+        if (w < 2) {
+            const int j0 = w * 32, i0 = j0 + 16;
+            Merge<16> mg;
+            mg.first(sm, b, i0, j0, 0, lane);
+            mg.second(sm, b, i0, 0, o, lane);
+            __syncwarp();
+            mg.store(sm, b, i0, j0, 0, 0, o, lane);
         }
+        invert_sync();
+        Merge<32> mg;
+        const int n0 = (w & 1) * 16, mt = w >> 1;
+        mg.first(sm, b, 32, 0, n0, lane);
+        mg.second(sm, b, 32, mt, o, lane);
+        invert_sync();  // every warp has read A21
+        mg.store(sm, b, 32, 0, n0, mt, o, lane);
     }
-    prep_sync();
-    if (warp < 4) {
-        // a diagonal block for each of four warps: forward substitution, a column a lane
-        // (both halves of the warp: one stores the high parts, one the low)
-        const int d0 = warp * 16, c = lane & 15;
-        float x[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            float acc = i == c ? 1.f : 0.f, acc2 = 0.f;
-#pragma unroll
-            for (int m = 0; m < i; m += 4) {
-                const float4 f = *reinterpret_cast<const float4*>(&sm.x[(d0 + i) * XS + m]);
-                acc = fmaf(-f.x, x[m], acc);
-                if (m + 1 < i) acc2 = fmaf(-f.y, x[m + 1], acc2);
-                if (m + 2 < i) acc = fmaf(-f.z, x[m + 2], acc);
-                if (m + 3 < i) acc2 = fmaf(-f.w, x[m + 3], acc2);
-            }
-            x[i] = acc + acc2;
-        }
-        unsigned char* tile = sm.t[b][lane >> 4];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const __half hi = __float2half_rn(x[i]);
-            const __half lo = __float2half_rn(x[i] - __half2float(hi));
-            *reinterpret_cast<__half*>(tile + at<C>(d0 + i, (d0 + c) >> 3) + (c & 7) * 2) = lane < 16 ? hi : lo;
-        }
-    }
-    prep_sync();
-    float o[2][4];
-    if (warp < 2) {
-        const int j0 = warp * 32, i0 = j0 + 16;
-        Merge<16> g;
-        g.first(sm, b, i0, j0, 0, lane);
-        g.second(sm, b, i0, 0, o, lane);
-        __syncwarp();
-        g.store(sm, b, i0, j0, 0, 0, o, lane);
-    }
-    prep_sync();
-    if (warp < 4) {
-        Merge<32> g;
-        const int n0 = (warp & 1) * 16, mt = warp >> 1;
-        g.first(sm, b, 32, 0, n0, lane);
-        g.second(sm, b, 32, mt, o, lane);
-        asm volatile("bar.sync 2, 128;" ::: "memory");  // these four warps have read A21
-        g.store(sm, b, 32, 0, n0, mt, o, lane);
-    }
+    ptx::fence_proxy_async_smem();
+    warp_arrive(sm.ready[b], lane);
 }
 
 // ------------------------------------------------------------ chain
-
-// A bounded wait that gives up once: later ones are skipped, the status word says so.
-struct Waiter {
-    int32_t* dev_status;
-    bool dead;
-    __device__ __forceinline__ void operator()(uint64_t& bar, int phase)
-    {
-        if (!dead && !ptx::mbar_wait(&bar, phase & 1)) {
-            dead = true;
-            flag_status(dev_status, KDA_DEV_TIMEOUT);
-        }
-    }
-};
-
-__device__ __forceinline__ void warp_arrive(uint64_t& bar, int lane)
-{
-    __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(&bar);
-}
-
-__device__ __forceinline__ float quad_max(float x)
-{
-    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-    return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-}
 
 // Chunk m of a chain warp: 16 columns of dv.  s holds S^T times g[0] (column
 // lane / 4) and g[1] (eight further), ig their inverses.
@@ -465,11 +496,11 @@ __device__ __forceinline__ void chain_chunk(S& sm, int m, float (&s)[DK / 8][4],
                                             int lane)
 {
     const int slot = m % 3, b = m & 1, q2 = (lane & 3) * 2;
-    const uint32_t kb = ptx::smem_u32(sm.k[slot]), vb = ptx::smem_u32(sm.v[slot]);
-    const uint32_t tb[2] = {ptx::smem_u32(sm.t[b][0]), ptx::smem_u32(sm.t[b][1])};
+    const uint32_t kb = ptx::smem_u32(sm.kq[slot]), vb = ptx::smem_u32(sm.v[slot]);
+    const uint32_t tb[2] = {ptx::smem_u32(sm.t_hi(b)), ptx::smem_u32(sm.t_lo(b))};
     const int brow = (lane & 7) + ((lane >> 4) & 1) * 8, bcol = (lane >> 3) & 1;  // K-contiguous operand
     const int trow = lane & 15, tcol = lane >> 4;                                 // transposed operand
-    if (m > 0) wait(sm.s_free[warp], m - 1);
+    if (m > 0) wait(sm.s_free, m - 1);
 
     // S^T K^T, each k-tile's fragments made a tile ahead
     float r[8][4];
@@ -479,9 +510,9 @@ __device__ __forceinline__ void chain_chunk(S& sm, int m, float (&s)[DK / 8][4],
         for (int i = 0; i < 4; ++i) r[t][i] = 0.f;
     __half2 m0 = __float2half2_rn(0.f), m1 = m0;
     uint32_t f[2][4][4], hi[2][4], lo[2][4];
-    auto left = [&](int kt) {  // k-tile kt of S^T, split, also for the output warp
+    auto left = [&](int kt) {  // k-tile kt of S^T, split, also for the outputs
 #pragma unroll
-        for (int t = 0; t < 4; ++t) ldsm(f[kt & 1][t], kb + at<DK>(t * 16 + brow, kt * 2 + bcol));
+        for (int t = 0; t < 4; ++t) ldsm(f[kt & 1][t], kb + kq_at(t * 16 + brow, kt * 2 + bcol));
         uint32_t(&x)[4] = hi[kt & 1], (&y)[4] = lo[kt & 1];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -491,8 +522,9 @@ __device__ __forceinline__ void chain_chunk(S& sm, int m, float (&s)[DK / 8][4],
             if (i & 1) m1 = __hmax2(m1, h);
             else m0 = __hmax2(m0, h);
         }
-        sm.hs[warp][0][kt][lane] = make_uint4(x[0], x[1], x[2], x[3]);
-        if (F32) sm.hs[warp][F32 ? 1 : 0][kt][lane] = make_uint4(y[0], y[1], y[2], y[3]);
+        const uint32_t o = half_at<DVT>(warp * 16 + trow, kt * 2 + tcol);
+        stsm(ptx::smem_u32(sm.st[0]) + o, x);
+        if (F32) stsm(ptx::smem_u32(sm.st[F32 ? 1 : 0]) + o, y);
     };
     left(0);
 #pragma unroll
@@ -504,13 +536,14 @@ __device__ __forceinline__ void chain_chunk(S& sm, int m, float (&s)[DK / 8][4],
 #pragma unroll
         for (int t = 0; t < 8; ++t) mma(r[t], lo[kt & 1], e[t >> 1][2 * (t & 1)], e[t >> 1][2 * (t & 1) + 1]);
     }
-    warp_arrive(sm.s_full[warp], lane);
+    ptx::fence_proxy_async_smem();
+    warp_arrive(sm.s_full, lane);
     // beta (V - e^G k.S), and each column's largest value
     float mr[2] = {0.f, 0.f};
 #pragma unroll
     for (int t = 0; t < 8; t += 2) {
         uint32_t v[4];  // V^T: rows t*8.. of columns gq, gq+8; then the next eight rows
-        ldsm_t(v, vb + at<DVT>(t * 8 + brow, warp * 2 + bcol));
+        ldsm_t(v, vb + v_at<DVT>(t * 8 + brow, warp * 2 + bcol));
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
             const float2 be = *reinterpret_cast<const float2*>(&sm.beta[b][(t + z) * 8 + q2]);
@@ -537,8 +570,8 @@ __device__ __forceinline__ void chain_chunk(S& sm, int m, float (&s)[DK / 8][4],
     auto part = [&](int kt) {
 #pragma unroll
         for (int t = kt; t < 4; ++t) {
-            ldsm(f[kt & 1][t], tb[0] + at<C>(t * 16 + brow, kt * 2 + bcol));
-            ldsm(f2[kt & 1][t], tb[1] + at<C>(t * 16 + brow, kt * 2 + bcol));
+            ldsm(f[kt & 1][t], tb[0] + tile_at(t * 16 + brow, kt * 2 + bcol));
+            ldsm(f2[kt & 1][t], tb[1] + tile_at(t * 16 + brow, kt * 2 + bcol));
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -578,16 +611,22 @@ __device__ __forceinline__ void chain_chunk(S& sm, int m, float (&s)[DK / 8][4],
     {
         const float ms[2] = {fmaxf(__low2float(m0), __high2float(m0)) * ig[0],
                              fmaxf(__low2float(m1), __high2float(m1)) * ig[1]};
-        float old[2] = {ig[0], ig[1]}, up;
+        const float old[2] = {ig[0], ig[1]};
+        float up[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            // 2^-20: keeps the outputs' S term in range beside a tiny U
-            pow2_scale(quad_max(fmaxf(mu[i], ms[i] * 0x1p-20f)), ud[i], up);
+            pow2_scale(quad_max(mu[i]), ud[i], up[i]);
             pow2_scale(quad_max(fmaxf(mw[i], ms[i] * last)), g[i], ig[i]);
             dec[i] = last * (g[i] * old[i]);
         }
-        if (m > 0) wait(sm.u_free[warp], m - 1);
-        if ((lane & 3) == 0) sm.hf[warp][lane >> 2] = make_float4(ud[0], ud[1], old[0], old[1]);
+        if (m > 0) wait(sm.o_full, m - 1);
+        if ((lane & 3) == 0) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                sm.f1[b][warp * 16 + (lane >> 2) + i * 8] = old[i];
+                sm.f2[b][warp * 16 + (lane >> 2) + i * 8] = up[i];
+            }
+        }
     }
 #pragma unroll
     for (int kt = 0; kt < 4; ++kt) {
@@ -598,10 +637,12 @@ __device__ __forceinline__ void chain_chunk(S& sm, int m, float (&s)[DK / 8][4],
             if (F32) split_h(v[0] * ud[i & 1], v[1] * ud[i & 1], x[i], y[i]);
             else x[i] = pack_h(v[0] * ud[i & 1], v[1] * ud[i & 1]);
         }
-        sm.hu[warp][0][kt][lane] = make_uint4(x[0], x[1], x[2], x[3]);
-        if (F32) sm.hu[warp][F32 ? 1 : 0][kt][lane] = make_uint4(y[0], y[1], y[2], y[3]);
+        const uint32_t o = half_at<DVT>(warp * 16 + trow, kt * 2 + tcol);
+        stsm(ptx::smem_u32(sm.ut[0]) + o, x);
+        if (F32) stsm(ptx::smem_u32(sm.ut[F32 ? 1 : 0]) + o, y);
     }
-    warp_arrive(sm.u_full[warp], lane);
+    ptx::fence_proxy_async_smem();
+    warp_arrive(sm.u_full[b], lane);
     // S^T = e^{G_C} S^T + (U^T diag(e^{G_C - G})) K, in a scale that both terms fit
 #pragma unroll
     for (int t = 0; t < DK / 8; ++t) {
@@ -614,7 +655,7 @@ __device__ __forceinline__ void chain_chunk(S& sm, int m, float (&s)[DK / 8][4],
     auto right = [&](int step) {
 #pragma unroll
         for (int t = 0; t < G; ++t)
-            ldsm_t(f[step & 1][t], kb + at<DK>(step / NG * 16 + trow, (step % NG * G + t) * 2 + tcol));
+            ldsm_t(f[step & 1][t], kb + kq_at(step / NG * 16 + trow, (step % NG * G + t) * 2 + tcol));
     };
     auto decayed = [&](int kt) {
 #pragma unroll
@@ -647,116 +688,97 @@ __device__ __forceinline__ void chain_chunk(S& sm, int m, float (&s)[DK / 8][4],
     }
 }
 
-// Chunk m of an output warp, from its chain warp's fragments:
-// O^T = scale sq (e^G S^T Q^T + U^T P^T).
+// ------------------------------------------------------------ outputs
+
+// Issues the products of chunk m's outputs (one thread issues): with the rows
+// of [K; Q] and [T; P] as left operands, lanes 64 - 127 hold Q S and P U.
 template <int DK, int DVT, bool F32, class S>
-__device__ __forceinline__ void output_chunk(S& sm, int m, void* out, long long row_stride, int n, Waiter& wait, int warp,
-                                             int lane)
+__device__ __forceinline__ void issue_outputs(S& sm, int m, Waiter& wait, uint32_t tmem, int lane)
 {
-    const int slot = m % 3, b = m & 1, q2 = (lane & 3) * 2;
-    const uint32_t qb = ptx::smem_u32(sm.q[slot]), vb = ptx::smem_u32(sm.v[slot]);
-    const uint32_t pb[2] = {ptx::smem_u32(sm.p[b][0]), ptx::smem_u32(sm.p[b][F32 ? 1 : 0])};
-    const int brow = (lane & 7) + ((lane >> 4) & 1) * 8, bcol = (lane >> 3) & 1;
-    float o[8][4];
+    const int slot = m % 3, b = m & 1;
+    constexpr uint32_t id = ptx::idesc_f16(128, DVT);
+    wait(sm.ready[b], m >> 1);
+    wait(sm.s_full, m);
+    if (m > 0) wait(sm.o_free, m - 1);
+    ptx::tc_fence_after();
+    if (lane == 0) {
+        const uint32_t kq = ptx::smem_u32(sm.kq[slot]);
+#pragma unroll 1
+        for (int p = 0; p < (F32 ? 2 : 1); ++p) {
+            const uint32_t st = ptx::smem_u32(sm.st[F32 ? p : 0]);
 #pragma unroll
-    for (int t = 0; t < 8; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[t][i] = 0.f;
-    wait(sm.s_full[warp], m);
-#pragma unroll 2
-    for (int kt = 0; kt < DK / 16; ++kt) {
-        const uint4 h4 = sm.hs[warp][0][kt][lane];
-        const uint32_t hi[4] = {h4.x, h4.y, h4.z, h4.w};
-        uint4 l4 = h4;
-        if (F32) l4 = sm.hs[warp][F32 ? 1 : 0][kt][lane];
-        const uint32_t lo[4] = {l4.x, l4.y, l4.z, l4.w};
-        uint32_t f[4][4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) ldsm(f[t], qb + at<DK>(t * 16 + brow, kt * 2 + bcol));
-#pragma unroll
-        for (int t = 0; t < 8; ++t) mma(o[t], hi, f[t >> 1][2 * (t & 1)], f[t >> 1][2 * (t & 1) + 1]);
-        if (F32)
-#pragma unroll
-            for (int t = 0; t < 8; ++t) mma(o[t], lo, f[t >> 1][2 * (t & 1)], f[t >> 1][2 * (t & 1) + 1]);
-    }
-    warp_arrive(sm.s_free[warp], lane);
-    wait(sm.u_full[warp], m);
-    const float4 sc = sm.hf[warp][lane >> 2];
-    const float ud[2] = {sc.x, sc.y}, fs[2] = {sc.x * sc.z, sc.y * sc.w};
-#pragma unroll
-    for (int t = 0; t < 8; ++t) {
-        const float2 eg = *reinterpret_cast<const float2*>(&sm.eg[b][t * 8 + q2]);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            o[t][2 * i] *= eg.x * fs[i];
-            o[t][2 * i + 1] *= eg.y * fs[i];
+            for (int kt = 0; kt < DK / 16; ++kt)
+                ptx::mma_f16_ss(tmem + TM_QS, ptx::desc_sw128(kq + (kt >> 2) * 16384 + (kt & 3) * 32),
+                                ptx::desc_sw128(st + (kt >> 2) * DVT * 128 + (kt & 3) * 32), id, p > 0 || kt > 0);
         }
+        ptx::mma_commit(&sm.s_free);
     }
+    __syncwarp();
+    wait(sm.u_full[b], m >> 1);
+    ptx::tc_fence_after();
+    if (lane == 0) {
+        // T P high with U high and low, T P low with U high
+        const uint32_t hi = ptx::smem_u32(sm.tp[b]), lo = hi + 16384;
+#pragma unroll 1
+        for (int p = 0; p < (F32 ? 3 : 1); ++p) {
+            const uint32_t x = p < 2 ? hi : lo, u = ptx::smem_u32(sm.ut[F32 && p == 1 ? 1 : 0]);
 #pragma unroll
-    for (int kt = 0; kt < 4; ++kt) {
-        const uint4 h4 = sm.hu[warp][0][kt][lane];
-        const uint32_t hi[4] = {h4.x, h4.y, h4.z, h4.w};
-        uint4 l4 = h4;
-        if (F32) l4 = sm.hu[warp][F32 ? 1 : 0][kt][lane];
-        const uint32_t lo[4] = {l4.x, l4.y, l4.z, l4.w};
-        uint32_t f[4][4];
-#pragma unroll
-        for (int t = kt; t < 4; ++t) ldsm(f[t], pb[0] + at<C>(t * 16 + brow, kt * 2 + bcol));
-#pragma unroll
-        for (int t = 2 * kt; t < 8; ++t) mma(o[t], hi, f[t >> 1][2 * (t & 1)], f[t >> 1][2 * (t & 1) + 1]);
-        if (F32) {
-#pragma unroll
-            for (int t = 2 * kt; t < 8; ++t) mma(o[t], lo, f[t >> 1][2 * (t & 1)], f[t >> 1][2 * (t & 1) + 1]);
-#pragma unroll
-            for (int t = kt; t < 4; ++t) ldsm(f[t], pb[1] + at<C>(t * 16 + brow, kt * 2 + bcol));
-#pragma unroll
-            for (int t = 2 * kt; t < 8; ++t) mma(o[t], hi, f[t >> 1][2 * (t & 1)], f[t >> 1][2 * (t & 1) + 1]);
+            for (int kt = 0; kt < 4; ++kt)
+                ptx::mma_f16_ss(tmem + TM_PU, ptx::desc_sw128(x + kt * 32), ptx::desc_sw128(u + kt * 32), id, p > 0 || kt > 0);
         }
+        ptx::mma_commit(&sm.o_full);
     }
-    warp_arrive(sm.u_free[warp], lane);
-    float uu[2];  // 1 / ud: a power of two
+    __syncwarp();
+}
+
+// Rows of chunk m's outputs: o_r = scale sq (e^G q'.S + (P U)_r), a row a lane.
+template <int DVT, bool F32, class S>
+__device__ __forceinline__ void output_rows(S& sm, int m, void* out, long long row_stride, int n, Waiter& wait,
+                                            uint32_t tmem, int half, int lane)
+{
+    const int b = m & 1, r = half * 32 + lane;
+    wait(sm.ready[b], m >> 1);
+    wait(sm.u_full[b], m >> 1);
+    const float e1 = sm.e1[b][r], e2 = sm.e2[b][r];
+    wait(sm.o_full, m);
+    ptx::tc_fence_after();
+    const uint32_t at = tmem + ((uint32_t)(64 + half * 32) << 16);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) uu[i] = __uint_as_float((254u << 23) - __float_as_uint(ud[i]));
-#pragma unroll
-    for (int t = 0; t < 8; ++t) {
-        const float2 oq = *reinterpret_cast<const float2*>(&sm.oq[b][t * 8 + q2]);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            o[t][2 * i] *= oq.x * uu[i];
-            o[t][2 * i + 1] *= oq.y * uu[i];
+    for (int c0 = 0; c0 < DVT; c0 += 32) {
+        float x[32], y[32];
+        ptx::tmem_ld32(at + TM_QS + c0, x);
+        ptx::tmem_ld32(at + TM_PU + c0, y);
+        if (c0 + 32 == DVT) {
+            ptx::tc_fence_before();
+            warp_arrive(sm.o_free, lane);
         }
-    }
-    if constexpr (F32) {
-        float* op = static_cast<float*>(out) + warp * 16 + (lane >> 2);
 #pragma unroll
-        for (int t = 0; t < 8; ++t)
-#pragma unroll
-            for (int z = 0; z < 2; ++z)
-                if (t * 8 + q2 + z < n) {
-                    float* p = op + (t * 8 + q2 + z) * row_stride;
-                    p[0] = o[t][z];
-                    p[8] = o[t][2 + z];
-                }
-    } else {
-        // through the warp's own columns of the V tile: 32 bytes a row to global memory
-#pragma unroll
-        for (int t = 0; t < 8; t += 2) {
-            uint32_t f[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const __nv_bfloat162 h = __floats2bfloat162_rn(o[t + (i >> 1)][2 * (i & 1)], o[t + (i >> 1)][2 * (i & 1) + 1]);
-                f[i] = *reinterpret_cast<const uint32_t*>(&h);
-            }
-            stsm_t(vb + at<DVT>(t * 8 + brow, warp * 2 + bcol), f[0], f[1], f[2], f[3]);
+        for (int i = 0; i < 32; i += 4) {
+            const float4 f1 = *reinterpret_cast<const float4*>(&sm.f1[b][c0 + i]);
+            const float4 f2 = *reinterpret_cast<const float4*>(&sm.f2[b][c0 + i]);
+            x[i] = fmaf(e1, f1.x * x[i], e2 * (f2.x * y[i]));
+            x[i + 1] = fmaf(e1, f1.y * x[i + 1], e2 * (f2.y * y[i + 1]));
+            x[i + 2] = fmaf(e1, f1.z * x[i + 2], e2 * (f2.z * y[i + 2]));
+            x[i + 3] = fmaf(e1, f1.w * x[i + 3], e2 * (f2.w * y[i + 3]));
         }
         __syncwarp();
-        __nv_bfloat16* op = static_cast<__nv_bfloat16*>(out) + warp * 16;
+        if (r >= n) {
+        } else if constexpr (F32) {
+            float4* p = reinterpret_cast<float4*>(static_cast<float*>(out) + r * row_stride + c0);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int i = lane + 32 * j, rr = i >> 1, c = i & 1;
-            if (rr < n)
-                *reinterpret_cast<uint4*>(op + rr * row_stride + c * 8) =
-                    *reinterpret_cast<const uint4*>(sm.v[slot] + at<DVT>(rr, warp * 2 + c));
+            for (int i = 0; i < 8; ++i) p[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+        } else {
+            uint4* p = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + r * row_stride + c0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t v[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(x[8 * i + 2 * j], x[8 * i + 2 * j + 1]);
+                    v[j] = *reinterpret_cast<const uint32_t*>(&h);
+                }
+                p[i] = make_uint4(v[0], v[1], v[2], v[3]);
+            }
         }
     }
 }
@@ -796,9 +818,9 @@ struct RowMaps {
 };
 
 template <int DK, int NW, bool F32>
-__global__ void __launch_bounds__(NW * 64 + PREP, 1) gdn_chunk_kernel(const GdnArgs a, const __grid_constant__ RowMaps maps, int dv)
+__global__ void __launch_bounds__(THREADS, 1) gdn_chunk_kernel(const GdnArgs a, const __grid_constant__ RowMaps maps, int dv)
 {
-    constexpr int DVT = NW * 16, THREADS = NW * 64 + PREP;
+    constexpr int DVT = NW * 16;
     extern __shared__ __align__(1024) unsigned char dyn[];
     using S = Smem<DK, DVT, F32>;
     S& sm = *reinterpret_cast<S*>(dyn);
@@ -806,129 +828,172 @@ __global__ void __launch_bounds__(NW * 64 + PREP, 1) gdn_chunk_kernel(const GdnA
     const int parts = dv / DVT;
     const int part = blockIdx.x % parts, h = (blockIdx.x / parts) % a.Hv;
     const int seq = ranked_seq(a.cu_seqlens, a.N, blockIdx.x / (parts * a.Hv), &sm.found);
-    int begin, end, slot;
-    if (!gdn_unit(a, seq, begin, end, slot)) return;
+    int begin, end, state_slot;
+    if (!gdn_unit(a, seq, begin, end, state_slot)) return;
     const int chunks = (end - begin + C - 1) / C;
     const int col0 = part * DVT;
 
     if (tid == 0) {
+        for (int i = 0; i < 3; ++i) {
+            ptx::mbar_init(&sm.loaded[i], 1);
+            ptx::mbar_init(&sm.kv_free[i], NW + 2);
+        }
         for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&sm.prod_full[i], 1);
+            ptx::mbar_init(&sm.prod_free[i], PREP / 32);
             ptx::mbar_init(&sm.ready[i], PREP / 32);
-            ptx::mbar_init(&sm.done[i], 2 * NW);
+            ptx::mbar_init(&sm.tp_free[i], NW + 2);
+            ptx::mbar_init(&sm.u_full[i], NW);
         }
-        for (int i = 0; i < 3; ++i) ptx::mbar_init(&sm.loaded[i], 1);
-        for (int i = 0; i < NW; ++i) {
-            ptx::mbar_init(&sm.s_full[i], 1);
-            ptx::mbar_init(&sm.s_free[i], 1);
-            ptx::mbar_init(&sm.u_full[i], 1);
-            ptx::mbar_init(&sm.u_free[i], 1);
-        }
+        ptx::mbar_init(&sm.s_full, NW);
+        ptx::mbar_init(&sm.s_free, 1);
+        ptx::mbar_init(&sm.o_full, 1);
+        ptx::mbar_init(&sm.o_free, 2);
         ptx::fence_mbar_init();
     }
-    // T's blocks above the diagonal stay zero
-    for (int i = tid; i < (int)sizeof(sm.t) / 16; i += THREADS)
-        reinterpret_cast<uint4*>(sm.t)[i] = make_uint4(0, 0, 0, 0);
+    // P's quarter above the diagonal is read and never written
+    for (int i = tid; i < (int)sizeof(sm.tp) / 16; i += THREADS)
+        reinterpret_cast<uint4*>(sm.tp)[i] = make_uint4(0, 0, 0, 0);
+    ptx::fence_proxy_async_smem();
+    if (warp == 5) ptx::tmem_alloc(&sm.tmem, TM_COLS);
+    ptx::tc_fence_before();
     __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = sm.tmem;
     Waiter wait{a.dev_status, false};
 
-    // Registers: the launch gives every thread 128 (NW = 4) or 168; the chain
-    // warps' warpgroup takes what the others leave.
-    if (warp >= 2 * NW) {
-        if constexpr (NW == 4) set_regs<false, 104>();
-        else set_regs<false, 144>();
-        const int t = tid - NW * 64, hk = h / (a.Hv / a.Hk);
+    // Registers: the launch gives every thread 128; the chain's warpgroup takes
+    // what the others leave (184 + 112 + 2 * 104 <= 4 * 128).
+    if (warp < 4) {
+        set_regs<true, 184>();
+        if (warp < NW) {
+            const size_t sbase = ((size_t)state_slot * a.Hv + h) * DK * dv + col0 + warp * 16 + (lane >> 2);
+            float s[DK / 8][4], ig[2], ms[2] = {0.f, 0.f};
+#pragma unroll
+            for (int t = 0; t < DK / 8; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    s[t][i] = a.state[sbase + (size_t)(t * 8 + (lane & 3) * 2 + (i & 1)) * dv + (i >> 1) * 8];
+                    ms[i >> 1] = fmaxf(ms[i >> 1], fabsf(s[t][i]));
+                }
+            {
+                float g[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) pow2_scale(quad_max(ms[i]), g[i], ig[i]);
+#pragma unroll
+                for (int t = 0; t < DK / 8; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s[t][i] *= g[i >> 1];
+            }
+            for (int m = 0; m < chunks; ++m) {
+                wait(sm.loaded[m % 3], m / 3);
+                wait(sm.ready[m & 1], m >> 1);
+                chain_chunk<DK, DVT, F32>(sm, m, s, ig, wait, warp, lane);
+                warp_arrive(sm.kv_free[m % 3], lane);
+                if (lane == 0) ptx::mbar_arrive(&sm.tp_free[m & 1]);
+            }
+#pragma unroll
+            for (int t = 0; t < DK / 8; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    a.state[sbase + (size_t)(t * 8 + (lane & 3) * 2 + (i & 1)) * dv + (i >> 1) * 8] = s[t][i] * ig[i >> 1];
+        }
+    } else if (warp < PREP_WARP) {
+        set_regs<false, 112>();
+        if (warp == 4) {
+            const int hk = h / (a.Hv / a.Hk);
+            const uint64_t policy = ptx::policy_evict_normal();  // other heads and columns read the same rows
+            auto load = [&](int m) {
+                const int s = m % 3, r0 = begin + m * C;
+                if (m >= 3) wait(sm.kv_free[s], m / 3 - 1);
+                if (lane == 0) {
+                    ptx::mbar_arrive_expect_tx(&sm.loaded[s], sizeof(sm.kq[0]) + sizeof(sm.v[0]));
+#pragma unroll
+                    for (int i = 0; i < S::HALVES; ++i) {
+                        ptx::tma_load_2d(sm.kq[s] + i * 16384, &maps.k, hk * DK + i * 64, r0, &sm.loaded[s], policy);
+                        ptx::tma_load_2d(sm.kq[s] + i * 16384 + 8192, &maps.q, hk * DK + i * 64, r0, &sm.loaded[s], policy);
+                    }
+                    ptx::tma_load_2d(sm.v[s], &maps.v, h * dv + col0, r0, &sm.loaded[s], policy);
+                }
+                __syncwarp();
+            };
+            auto product = [&](int m) {
+                const int s = m % 3, b = m & 1;
+                wait(sm.loaded[s], m / 3);
+                if (m >= 2) wait(sm.prod_free[b], (m - 2) >> 1);
+                ptx::tc_fence_after();
+                if (lane == 0) {
+                    const uint32_t kq = ptx::smem_u32(sm.kq[s]);
+#pragma unroll
+                    for (int kt = 0; kt < DK / 16; ++kt) {
+                        const uint64_t d = ptx::desc_sw128(kq + (kt >> 2) * 16384 + (kt & 3) * 32);
+                        ptx::mma_f16_ss(tmem + TM_PROD + b * 128, d, d, ptx::idesc_bf16(128, 128), kt > 0);
+                    }
+                    ptx::mma_commit(&sm.prod_full[b]);
+                }
+                __syncwarp();
+            };
+            load(0);
+            if (chunks > 1) load(1);
+            product(0);
+            for (int m = 0; m < chunks; ++m) {
+                if (m + 1 < chunks) product(m + 1);
+                if (m + 2 < chunks) load(m + 2);
+            }
+        } else if (warp == 5) {
+            for (int m = 0; m < chunks; ++m) issue_outputs<DK, DVT, F32>(sm, m, wait, tmem, lane);
+        } else {
+            const long long row_stride = (long long)a.Hv * dv;
+            const size_t osize = F32 ? 4 : 2;
+            unsigned char* out = static_cast<unsigned char*>(a.out) + ((size_t)begin * row_stride + (size_t)h * dv + col0) * osize;
+            for (int m = 0; m < chunks; ++m) {
+                output_rows<DVT, F32>(sm, m, out + (size_t)m * C * row_stride * osize, row_stride,
+                                      min(C, end - begin - m * C), wait, tmem, warp - 6, lane);
+                warp_arrive(sm.kv_free[m % 3], lane);
+                if (lane == 0) ptx::mbar_arrive(&sm.tp_free[m & 1]);
+            }
+        }
+    } else {
+        set_regs<false, 104>();
+        const int w = warp - PREP_WARP;
         const __nv_bfloat16* ga = static_cast<const __nv_bfloat16*>(a.a) + h;
         const __nv_bfloat16* be = static_cast<const __nv_bfloat16*>(a.b) + h;
-        const float ea = expf(a.A_log[h]), dt = a.dt_bias[h];
-        __nv_bfloat16 graw = __float2bfloat16(0.f), braw = graw;  // the next chunk's, as loaded
-        const uint64_t policy = ptx::policy_evict_normal();  // other heads and columns read the same rows
-        auto load = [&](int m) {
-            const int r0 = begin + m * C, s = m % 3, r = r0 + (t & (C - 1));
-            if (t == PREP - 32) {
-                ptx::mbar_arrive_expect_tx(&sm.loaded[s], C * (2 * DK + DVT) * 2);
-                load_tile<DK>(sm.k[s], &maps.k, hk * DK, r0, &sm.loaded[s], policy);
-                load_tile<DK>(sm.q[s], &maps.q, hk * DK, r0, &sm.loaded[s], policy);
-                load_tile<DVT>(sm.v[s], &maps.v, h * dv + col0, r0, &sm.loaded[s], policy);
-            }
-            if (t < C && r < end) {
-                graw = ga[(size_t)r * a.Hv];
-                braw = be[(size_t)r * a.Hv];
+        const float ea = expf(a.A_log[h]) * 1.44269504088896341f, dt = a.dt_bias[h];
+        __nv_bfloat16 graw[2], braw[2];  // the next chunk's gates of two rows, as loaded (warp 4)
+        auto gates = [&](int r0) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = r0 + 2 * lane + i;
+                if (w == 4 && r < end) {
+                    graw[i] = ga[(size_t)r * a.Hv];
+                    braw[i] = be[(size_t)r * a.Hv];
+                } else graw[i] = braw[i] = __float2bfloat16(0.f);
             }
         };
-        load(0);
+        gates(begin);
         for (int m = 0; m < chunks; ++m) {
-            const int b = m & 1;
-            const bool real = begin + m * C + (t & (C - 1)) < end;
-            const float g0 = __bfloat162float(graw), b0 = __bfloat162float(braw);
-            if (m >= 2) wait(sm.done[b], (m - 2) >> 1);
-            if (t < C) {
-                sm.g[t] = real ? gdn_log_alpha(ea, g0, dt) : 0.f;
-                sm.beta[b][t] = real ? sigmoidf_(b0) : 0.f;
+            const int r0 = begin + m * C, n = min(C, end - r0);
+            float2 g = make_float2(0.f, 0.f), bt = g;
+            if (w == 4) {
+                if (2 * lane < n) {
+                    g.x = gdn_log_alpha(ea, __bfloat162float(graw[0]), dt);
+                    bt.x = sigmoidf_(__bfloat162float(braw[0]));
+                }
+                if (2 * lane + 1 < n) {
+                    g.y = gdn_log_alpha(ea, __bfloat162float(graw[1]), dt);
+                    bt.y = sigmoidf_(__bfloat162float(braw[1]));
+                }
+                gates(r0 + C);
             }
-            if (m + 1 < chunks) load(m + 1);
-            wait(sm.loaded[m % 3], m / 3);
-            if (begin + m * C + C > end) {
-                // the copies took the next sequence's rows along: zeros instead
-                const int r = t & (C - 1);
-                if (!real && t < C) zero_row<DK>(sm.k[m % 3], r);
-                else if (!real && t < 2 * C) zero_row<DK>(sm.q[m % 3], r);
-                else if (!real && t < 3 * C) zero_row<DVT>(sm.v[m % 3], r);
-            }
-            prep_sync();
-            prep_chunk<DK, DVT, F32>(sm, m % 3, b, a, real, t);
-            ptx::fence_proxy_async_smem();  // the rows written above, before a later copy into their place
-            warp_arrive(sm.ready[b], lane);
-            prep_sync();  // the scratch and the decays are free again
+            prep_chunk<DK, DVT, F32>(sm, m, a, n, g, bt, wait, tmem, w, lane);
         }
-        return;
     }
-
-    if constexpr (NW == 2) set_regs<true, 208>();
-    if (warp >= NW) {
-        if constexpr (NW == 4) set_regs<false, 112>();
-        const int w = warp - NW;
-        const long long row_stride = (long long)a.Hv * dv;
-        const size_t osize = F32 ? 4 : 2;
-        unsigned char* out = static_cast<unsigned char*>(a.out) + ((size_t)begin * row_stride + (size_t)h * dv + col0) * osize;
-        for (int m = 0; m < chunks; ++m) {
-            wait(sm.ready[m & 1], m >> 1);
-            output_chunk<DK, DVT, F32>(sm, m, out + (size_t)m * C * row_stride * osize, row_stride,
-                                       min(C, end - begin - m * C), wait, w, lane);
-            ptx::fence_proxy_async_smem();  // outputs staged in the V tile
-            warp_arrive(sm.done[m & 1], lane);
-        }
-        return;
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 5) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, TM_COLS);
     }
-
-    if constexpr (NW == 4) set_regs<true, 184>();
-    const size_t sbase = ((size_t)slot * a.Hv + h) * DK * dv + col0 + warp * 16 + (lane >> 2);
-    float s[DK / 8][4], ig[2], ms[2] = {0.f, 0.f};
-#pragma unroll
-    for (int t = 0; t < DK / 8; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            s[t][i] = a.state[sbase + (size_t)(t * 8 + (lane & 3) * 2 + (i & 1)) * dv + (i >> 1) * 8];
-            ms[i >> 1] = fmaxf(ms[i >> 1], fabsf(s[t][i]));
-        }
-    {
-        float g[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) pow2_scale(quad_max(ms[i]), g[i], ig[i]);
-#pragma unroll
-        for (int t = 0; t < DK / 8; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[t][i] *= g[i >> 1];
-    }
-    for (int m = 0; m < chunks; ++m) {
-        wait(sm.ready[m & 1], m >> 1);
-        chain_chunk<DK, DVT, F32>(sm, m, s, ig, wait, warp, lane);
-        warp_arrive(sm.done[m & 1], lane);
-    }
-#pragma unroll
-    for (int t = 0; t < DK / 8; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            a.state[sbase + (size_t)(t * 8 + (lane & 3) * 2 + (i & 1)) * dv + (i >> 1) * 8] = s[t][i] * ig[i >> 1];
 }
 
 // [T][width] bf16 rows with a row stride; boxes of 64 rows.
@@ -947,6 +1012,13 @@ bool encode_rows(CUtensorMap* m, const void* base, long long width, long long st
 
 template <int DK, int NW, bool F32> cudaError_t launch(const GdnArgs& a, int dv, cudaStream_t st)
 {
+    using S = Smem<DK, NW * 16, F32>;
+    // operand tiles on the swizzle's 1024-byte period, vectors on 16 bytes, barriers on 8
+    static_assert(offsetof(S, v) % 1024 == 0 && offsetof(S, tp) % 1024 == 0 && offsetof(S, st) % 1024 == 0 &&
+                  offsetof(S, ut) % 1024 == 0, "tiles");
+    static_assert(offsetof(S, x) % 16 == 0 && offsetof(S, f1) % 16 == 0 && offsetof(S, f2) % 16 == 0 &&
+                  offsetof(S, gh) % 16 == 0 && offsetof(S, gl) % 16 == 0 && offsetof(S, colk) % 16 == 0 &&
+                  offsetof(S, down) % 16 == 0 && offsetof(S, loaded) % 8 == 0, "vectors");
     constexpr int smem = sizeof(Smem<DK, NW * 16, F32>);
     static_assert(smem <= 227 * 1024, "shared memory");
     static PerDeviceOnce once;
@@ -955,11 +1027,11 @@ template <int DK, int NW, bool F32> cudaError_t launch(const GdnArgs& a, int dv,
     });
     if (e != cudaSuccess) return e;
     RowMaps maps;
-    if (!encode_rows(&maps.q, a.q, (long long)a.Hk * DK, a.qs, a.T, std::min(DK, 64)) ||
-        !encode_rows(&maps.k, a.k, (long long)a.Hk * DK, a.ks, a.T, std::min(DK, 64)) ||
-        !encode_rows(&maps.v, a.v, (long long)a.Hv * dv, a.vs, a.T, std::min(NW * 16, 64)))
+    if (!encode_rows(&maps.q, a.q, (long long)a.Hk * DK, a.qs, a.T, 64) ||
+        !encode_rows(&maps.k, a.k, (long long)a.Hk * DK, a.ks, a.T, 64) ||
+        !encode_rows(&maps.v, a.v, (long long)a.Hv * dv, a.vs, a.T, NW * 16))
         return cudaErrorInvalidValue;
-    gdn_chunk_kernel<DK, NW, F32><<<a.N * a.Hv * (dv / (NW * 16)), NW * 64 + PREP, smem, st>>>(a, maps, dv);
+    gdn_chunk_kernel<DK, NW, F32><<<a.N * a.Hv * (dv / (NW * 16)), THREADS, smem, st>>>(a, maps, dv);
     return cudaGetLastError();
 }
 
