@@ -173,16 +173,13 @@ __device__ __forceinline__ void prep_sync() { asm volatile("bar.sync 1, %0;" ::"
 // the four warps that invert T
 __device__ __forceinline__ void invert_sync() { asm volatile("bar.sync 2, 128;" ::: "memory"); }
 
-// A bounded wait that gives up once: later ones are skipped, the status word says so.
+// Bounded waits: after one that gives up the others only look once, and the
+// role reports it at its end.
 struct Waiter {
-    int32_t* dev_status;
     bool dead;
     __device__ __forceinline__ void operator()(uint64_t& bar, int phase)
     {
-        if (!dead && !ptx::mbar_wait(&bar, phase & 1, 1u << 22)) {
-            dead = true;
-            flag_status(dev_status, KDA_DEV_TIMEOUT);
-        }
+        if (!ptx::mbar_wait_short(&bar, phase & 1, dead ? 1u : 1u << 22)) dead = true;
     }
 };
 
@@ -216,7 +213,7 @@ template <class S> __device__ __forceinline__ void scan_rows(S& sm, int b, float
 {
     float h = g.x, l = 0.f;
     dw_add(h, l, g.y, 0.f);
-#pragma unroll
+#pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
         const float oh = __shfl_up_sync(0xffffffffu, h, o), ol = __shfl_up_sync(0xffffffffu, l, o);
         if (lane >= o) dw_add(h, l, oh, ol);
@@ -238,7 +235,7 @@ template <class S> __device__ __forceinline__ void scan_rows(S& sm, int b, float
 template <int DK> __device__ __forceinline__ void convert_row(unsigned char* tile, int r, float down, bool real)
 {
     const __nv_bfloat162 d = __float2bfloat162_rn(down);
-#pragma unroll
+#pragma unroll 1
     for (int c0 = 0; c0 < DK / 8; c0 += 4) {
         uint4 x[4];
 #pragma unroll
@@ -335,25 +332,19 @@ template <int SIZE> struct Merge {
     }
 };
 
-// x[lane]
-__device__ __forceinline__ float pick(const float (&x)[32], int lane)
-{
-    float y = x[0];
-#pragma unroll
-    for (int i = 1; i < 32; ++i) y = i == lane ? x[i] : y;
-    return y;
-}
-
 // Chunk m of prep warp w (n rows of it are real).  Lane and w & 3 give the
-// row of [K; Q] whose products the warp reads, w >> 2 which half of k's rows it reads them
-// against; the halves above the diagonal (w = 4 and 6) are left out.
+// row of [K; Q] whose products the warp reads, w >> 2 which half of k's rows it
+// reads them against; the halves above the diagonal (w = 4 and 6) are left out.
+// The loops stay rolled: this runs once a chunk beside the other roles' code,
+// and what the instruction cache does not hold is fetched anew each time (at
+// 150 KB of code that was the kernel's first stall).
 template <int DK, int DVT, bool F32, class S>
 __device__ __forceinline__ void prep_chunk(S& sm, int m, const GdnArgs& a, int n, float2 g, float2 beta, Waiter& wait,
                                            uint32_t tmem, int w, int lane)
 {
     const int b = m & 1, slot = m % 3;
     const int lr = (w & 3) * 32 + lane, r = lr & (C - 1), type = lr >> 6, s0 = (w >> 2) * 32;  // type 0: k, 1: q
-    float d[32];
+    const uint32_t at = tmem + ((uint32_t)((w & 3) * 32) << 16) + TM_PROD + b * 128;
     if (m >= 2) wait(sm.tp_free[b], (m - 2) >> 1);
     if (w == 4) {
         *reinterpret_cast<float2*>(&sm.beta[b][2 * lane]) = beta;
@@ -361,16 +352,20 @@ __device__ __forceinline__ void prep_chunk(S& sm, int m, const GdnArgs& a, int n
     } else {
         wait(sm.prod_full[b], m >> 1);
         ptx::tc_fence_after();
-        const uint32_t at = tmem + ((uint32_t)((w & 3) * 32) << 16) + TM_PROD + b * 128;
-        if (w >= 6) {  // q's norms: columns of q
-            ptx::tmem_ld32(at + C + (w & 1) * 32, d);
-            sm.norm[lr] = pick(d, lane);
+        if (w == 0 || w >= 5) {
+            // the squared norms of 32 rows of k (w = 0, 5) or q: the diagonal
+            const int c0 = w == 0 ? 0 : (w - 4) * 32;
+            float y = 0.f;
+#pragma unroll 1
+            for (int c = 0; c < 32; c += 8) {
+                float d[8];
+                ptx::tmem_ld8(at + c0 + c, d);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y = c + i == lane ? d[i] : y;
+            }
+            sm.norm[lr] = y;
         }
-        if (w != 6) ptx::tmem_ld32(at + s0, d);
-        if (w == 0 || w == 5) sm.norm[lr] = pick(d, lane);  // k's
-        ptx::tc_fence_before();
     }
-    warp_arrive(sm.prod_free[b], lane);
     prep_sync();
     if (w < 4) {
         const float ss = sm.norm[lr];
@@ -399,10 +394,11 @@ __device__ __forceinline__ void prep_chunk(S& sm, int m, const GdnArgs& a, int n
         const int lim = r < n ? r + type : 0;
         unsigned char* hi_tile = sm.tp[b];
         unsigned char* lo_tile = sm.tp[b] + 16384;
-#pragma unroll
+#pragma unroll 1
         for (int p = 0; p < 4; ++p) {
             uint32_t hi[4], lo[4];
-            float v[8];
+            float v[8], d[8];
+            ptx::tmem_ld8(at + s0 + p * 8, d);
 #pragma unroll
             for (int z = 0; z < 2; ++z) {
                 const int s = s0 + p * 8 + z * 4;
@@ -413,7 +409,7 @@ __device__ __forceinline__ void prep_chunk(S& sm, int m, const GdnArgs& a, int n
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float e = exp2_sfu((rh - h4[i]) + (rl - l4[i]));
-                    v[z * 4 + i] = s + i < lim ? (rf * f4[i]) * e * d[p * 8 + z * 4 + i] : 0.f;
+                    v[z * 4 + i] = s + i < lim ? (rf * f4[i]) * e * d[z * 4 + i] : 0.f;
                 }
             }
 #pragma unroll
@@ -428,6 +424,8 @@ __device__ __forceinline__ void prep_chunk(S& sm, int m, const GdnArgs& a, int n
             }
         }
     }
+    ptx::tc_fence_before();
+    warp_arrive(sm.prod_free[b], lane);
     prep_sync();
     if (w >= 4) {
         // meanwhile the rows themselves
@@ -706,7 +704,7 @@ __device__ __forceinline__ void issue_outputs(S& sm, int m, Waiter& wait, uint32
 #pragma unroll 1
         for (int p = 0; p < (F32 ? 2 : 1); ++p) {
             const uint32_t st = ptx::smem_u32(sm.st[F32 ? p : 0]);
-#pragma unroll
+#pragma unroll 1
             for (int kt = 0; kt < DK / 16; ++kt)
                 ptx::mma_f16_ss(tmem + TM_QS, ptx::desc_sw128(kq + (kt >> 2) * 16384 + (kt & 3) * 32),
                                 ptx::desc_sw128(st + (kt >> 2) * DVT * 128 + (kt & 3) * 32), id, p > 0 || kt > 0);
@@ -722,7 +720,7 @@ __device__ __forceinline__ void issue_outputs(S& sm, int m, Waiter& wait, uint32
 #pragma unroll 1
         for (int p = 0; p < (F32 ? 3 : 1); ++p) {
             const uint32_t x = p < 2 ? hi : lo, u = ptx::smem_u32(sm.ut[F32 && p == 1 ? 1 : 0]);
-#pragma unroll
+#pragma unroll 1
             for (int kt = 0; kt < 4; ++kt)
                 ptx::mma_f16_ss(tmem + TM_PU, ptx::desc_sw128(x + kt * 32), ptx::desc_sw128(u + kt * 32), id, p > 0 || kt > 0);
         }
@@ -743,17 +741,13 @@ __device__ __forceinline__ void output_rows(S& sm, int m, void* out, long long r
     wait(sm.o_full, m);
     ptx::tc_fence_after();
     const uint32_t at = tmem + ((uint32_t)(64 + half * 32) << 16);
+#pragma unroll 1
+    for (int c0 = 0; c0 < DVT; c0 += 16) {
+        float x[16], y[16];
+        ptx::tmem_ld16(at + TM_QS + c0, x);
+        ptx::tmem_ld16(at + TM_PU + c0, y);
 #pragma unroll
-    for (int c0 = 0; c0 < DVT; c0 += 32) {
-        float x[32], y[32];
-        ptx::tmem_ld32(at + TM_QS + c0, x);
-        ptx::tmem_ld32(at + TM_PU + c0, y);
-        if (c0 + 32 == DVT) {
-            ptx::tc_fence_before();
-            warp_arrive(sm.o_free, lane);
-        }
-#pragma unroll
-        for (int i = 0; i < 32; i += 4) {
+        for (int i = 0; i < 16; i += 4) {
             const float4 f1 = *reinterpret_cast<const float4*>(&sm.f1[b][c0 + i]);
             const float4 f2 = *reinterpret_cast<const float4*>(&sm.f2[b][c0 + i]);
             x[i] = fmaf(e1, f1.x * x[i], e2 * (f2.x * y[i]));
@@ -761,26 +755,29 @@ __device__ __forceinline__ void output_rows(S& sm, int m, void* out, long long r
             x[i + 2] = fmaf(e1, f1.z * x[i + 2], e2 * (f2.z * y[i + 2]));
             x[i + 3] = fmaf(e1, f1.w * x[i + 3], e2 * (f2.w * y[i + 3]));
         }
-        __syncwarp();
-        if (r >= n) {
-        } else if constexpr (F32) {
-            float4* p = reinterpret_cast<float4*>(static_cast<float*>(out) + r * row_stride + c0);
+        if (r < n) {
+            if constexpr (F32) {
+                float4* p = reinterpret_cast<float4*>(static_cast<float*>(out) + r * row_stride + c0);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) p[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-        } else {
-            uint4* p = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + r * row_stride + c0);
+                for (int i = 0; i < 4; ++i) p[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+            } else {
+                uint4* p = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + r * row_stride + c0);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t v[4];
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t v[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const __nv_bfloat162 h = __floats2bfloat162_rn(x[8 * i + 2 * j], x[8 * i + 2 * j + 1]);
-                    v[j] = *reinterpret_cast<const uint32_t*>(&h);
+                    for (int j = 0; j < 4; ++j) {
+                        const __nv_bfloat162 h = __floats2bfloat162_rn(x[8 * i + 2 * j], x[8 * i + 2 * j + 1]);
+                        v[j] = *reinterpret_cast<const uint32_t*>(&h);
+                    }
+                    p[i] = make_uint4(v[0], v[1], v[2], v[3]);
                 }
-                p[i] = make_uint4(v[0], v[1], v[2], v[3]);
             }
         }
+        __syncwarp();
     }
+    ptx::tc_fence_before();
+    warp_arrive(sm.o_free, lane);
 }
 
 // ------------------------------------------------------------ kernel
@@ -852,6 +849,7 @@ __global__ void __launch_bounds__(THREADS, 1) gdn_chunk_kernel(const GdnArgs a, 
         ptx::fence_mbar_init();
     }
     // P's quarter above the diagonal is read and never written
+#pragma unroll 1
     for (int i = tid; i < (int)sizeof(sm.tp) / 16; i += THREADS)
         reinterpret_cast<uint4*>(sm.tp)[i] = make_uint4(0, 0, 0, 0);
     ptx::fence_proxy_async_smem();
@@ -860,12 +858,12 @@ __global__ void __launch_bounds__(THREADS, 1) gdn_chunk_kernel(const GdnArgs a, 
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = sm.tmem;
-    Waiter wait{a.dev_status, false};
+    Waiter wait{false};
 
     // Registers: the launch gives every thread 128; the chain's warpgroup takes
-    // what the others leave (184 + 112 + 2 * 104 <= 4 * 128).
+    // what the others leave (232 + 88 + 2 * 96 <= 4 * 128).
     if (warp < 4) {
-        set_regs<true, 184>();
+        set_regs<true, 232>();
         if (warp < NW) {
             const size_t sbase = ((size_t)state_slot * a.Hv + h) * DK * dv + col0 + warp * 16 + (lane >> 2);
             float s[DK / 8][4], ig[2], ms[2] = {0.f, 0.f};
@@ -899,46 +897,43 @@ __global__ void __launch_bounds__(THREADS, 1) gdn_chunk_kernel(const GdnArgs a, 
                     a.state[sbase + (size_t)(t * 8 + (lane & 3) * 2 + (i & 1)) * dv + (i >> 1) * 8] = s[t][i] * ig[i >> 1];
         }
     } else if (warp < PREP_WARP) {
-        set_regs<false, 112>();
+        set_regs<false, 88>();
         if (warp == 4) {
             const int hk = h / (a.Hv / a.Hk);
             const uint64_t policy = ptx::policy_evict_normal();  // other heads and columns read the same rows
-            auto load = [&](int m) {
-                const int s = m % 3, r0 = begin + m * C;
-                if (m >= 3) wait(sm.kv_free[s], m / 3 - 1);
-                if (lane == 0) {
-                    ptx::mbar_arrive_expect_tx(&sm.loaded[s], sizeof(sm.kq[0]) + sizeof(sm.v[0]));
-#pragma unroll
-                    for (int i = 0; i < S::HALVES; ++i) {
-                        ptx::tma_load_2d(sm.kq[s] + i * 16384, &maps.k, hk * DK + i * 64, r0, &sm.loaded[s], policy);
-                        ptx::tma_load_2d(sm.kq[s] + i * 16384 + 8192, &maps.q, hk * DK + i * 64, r0, &sm.loaded[s], policy);
+            for (int m = 0; m <= chunks; ++m) {
+                if (m > 0) {
+                    // the raw products of chunk m - 1
+                    const int s = (m - 1) % 3, b = (m - 1) & 1;
+                    wait(sm.loaded[s], (m - 1) / 3);
+                    if (m >= 3) wait(sm.prod_free[b], (m - 3) >> 1);
+                    ptx::tc_fence_after();
+                    if (lane == 0) {
+                        const uint32_t kq = ptx::smem_u32(sm.kq[s]);
+#pragma unroll 1
+                        for (int kt = 0; kt < DK / 16; ++kt) {
+                            const uint64_t d = ptx::desc_sw128(kq + (kt >> 2) * 16384 + (kt & 3) * 32);
+                            ptx::mma_f16_ss(tmem + TM_PROD + b * 128, d, d, ptx::idesc_bf16(128, 128), kt > 0);
+                        }
+                        ptx::mma_commit(&sm.prod_full[b]);
                     }
-                    ptx::tma_load_2d(sm.v[s], &maps.v, h * dv + col0, r0, &sm.loaded[s], policy);
+                    __syncwarp();
                 }
-                __syncwarp();
-            };
-            auto product = [&](int m) {
-                const int s = m % 3, b = m & 1;
-                wait(sm.loaded[s], m / 3);
-                if (m >= 2) wait(sm.prod_free[b], (m - 2) >> 1);
-                ptx::tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t kq = ptx::smem_u32(sm.kq[s]);
-#pragma unroll
-                    for (int kt = 0; kt < DK / 16; ++kt) {
-                        const uint64_t d = ptx::desc_sw128(kq + (kt >> 2) * 16384 + (kt & 3) * 32);
-                        ptx::mma_f16_ss(tmem + TM_PROD + b * 128, d, d, ptx::idesc_bf16(128, 128), kt > 0);
+                if (m < chunks) {
+                    const int s = m % 3, r0 = begin + m * C;
+                    if (m >= 3) wait(sm.kv_free[s], m / 3 - 1);
+                    if (lane == 0) {
+                        ptx::mbar_arrive_expect_tx(&sm.loaded[s], sizeof(sm.kq[0]) + sizeof(sm.v[0]));
+#pragma unroll 1
+                        for (int i = 0; i < S::HALVES; ++i) {
+                            ptx::tma_load_2d(sm.kq[s] + i * 16384, &maps.k, hk * DK + i * 64, r0, &sm.loaded[s], policy);
+                            ptx::tma_load_2d(sm.kq[s] + i * 16384 + 8192, &maps.q, hk * DK + i * 64, r0, &sm.loaded[s],
+                                             policy);
+                        }
+                        ptx::tma_load_2d(sm.v[s], &maps.v, h * dv + col0, r0, &sm.loaded[s], policy);
                     }
-                    ptx::mma_commit(&sm.prod_full[b]);
+                    __syncwarp();
                 }
-                __syncwarp();
-            };
-            load(0);
-            if (chunks > 1) load(1);
-            product(0);
-            for (int m = 0; m < chunks; ++m) {
-                if (m + 1 < chunks) product(m + 1);
-                if (m + 2 < chunks) load(m + 2);
             }
         } else if (warp == 5) {
             for (int m = 0; m < chunks; ++m) issue_outputs<DK, DVT, F32>(sm, m, wait, tmem, lane);
@@ -954,7 +949,7 @@ __global__ void __launch_bounds__(THREADS, 1) gdn_chunk_kernel(const GdnArgs a, 
             }
         }
     } else {
-        set_regs<false, 104>();
+        set_regs<false, 96>();
         const int w = warp - PREP_WARP;
         const __nv_bfloat16* ga = static_cast<const __nv_bfloat16*>(a.a) + h;
         const __nv_bfloat16* be = static_cast<const __nv_bfloat16*>(a.b) + h;
@@ -988,6 +983,7 @@ __global__ void __launch_bounds__(THREADS, 1) gdn_chunk_kernel(const GdnArgs a, 
             prep_chunk<DK, DVT, F32>(sm, m, a, n, g, bt, wait, tmem, w, lane);
         }
     }
+    if (wait.dead) flag_status(a.dev_status, KDA_DEV_TIMEOUT);
     ptx::tc_fence_before();
     __syncthreads();
     if (warp == 5) {
