@@ -362,8 +362,7 @@ extern "C" {
 KDA_API size_t kda_gdn_prefill_workspace_bytes(const kda_gdn_params* p, int32_t N, int32_t T)
 {
     if (check_gdn(p) != KDA_OK || N <= 0 || T <= 0 || p->io_dtype != KDA_DTYPE_BF16) return 0;
-    return gdn_chunk_workspace_bytes(p->num_heads_k, p->num_heads_v, p->head_dim_k, p->head_dim_v,
-                                     p->out_dtype == KDA_DTYPE_BF16, N, T);
+    return gdn_chunk_workspace_bytes(p->num_heads_k, p->num_heads_v, p->head_dim_k, p->out_dtype == KDA_DTYPE_BF16, N, T);
 }
 
 KDA_API int kda_gdn_prefill_varlen(const kda_gdn_params* p, const int32_t* cu_seqlens, int32_t N, int32_t T,
@@ -373,7 +372,7 @@ KDA_API int kda_gdn_prefill_varlen(const kda_gdn_params* p, const int32_t* cu_se
 {
     int rc = check_gdn(p);
     if (rc != KDA_OK) return rc;
-    if (N < 0 || T < 0 || (int64_t)N * p->num_heads_v * 4 > INT32_MAX) return KDA_ERR_INVALID_ARGUMENT;
+    if (N < 0 || T < 0 || ((int64_t)T / 64 + 4 * (int64_t)N) * p->num_heads_v > INT32_MAX) return KDA_ERR_INVALID_ARGUMENT;
     if (N == 0 || T == 0) return KDA_OK;
     GdnArgs g;
     fill_gdn(g, p);

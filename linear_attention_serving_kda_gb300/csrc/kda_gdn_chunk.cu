@@ -3,35 +3,27 @@
 //
 // With G the running sum of log alpha in the chunk, row by row:
 //     A_rs = beta_r e^{G_r - G_s} k_r.k_s  (s < r),   T = (I + A)^-1
-//     U    = T diag(beta) (V - diag(e^G) K S)
-//     O    = diag(e^G) Q S + P U,   P_rs = e^{G_r - G_s} q_r.k_s  (s <= r)
-//     S'   = e^{G_C} S + (diag(e^{G_C - G}) K)^T U
+//     R    = diag(beta) V - diag(beta e^G) K S           (U = T R: the rule's updates)
+//     S'   = e^{G_C} S + M^T R,   M = T^T diag(e^{G_C - G}) K
+//     O    = diag(e^G) Q S + (P T) R,   P_rs = e^{G_r - G_s} q_r.k_s  (s <= r)
 // All exponents are differences that are <= 0.
 //
-// A CTA owns one (sequence, value head, DVT columns of dv); nothing crosses
-// columns, so these never meet.  Sixteen warps in four roles, a chunk apart:
-//   - a loader: rows by tensor copies, and the raw products [K; Q] [K; Q]^T of
-//     the next chunk as one tcgen05 product into TMEM (k.k, q.k and, on the
-//     diagonal, both squared norms);
-//   - eight prep warps, one row of [K; Q] a lane: the norms, P and A from
-//     those, then T by forward substitution of the 16 x 16 diagonal blocks and
-//     doubling; k and q rescaled in place;
-//   - NW chain warps: each keeps S^T for 16 columns in registers as the
-//     accumulator of a 16 x dk product and walks the chunks alone: S^T K^T,
-//     R^T T^T (R = beta (V - ..)) and U^T K take their left operand straight
-//     from the accumulators of the product before (the two fragment layouts
-//     agree), so no chain warp ever waits for another one;
-//   - an issuer and two output warps: Q S and P U as tcgen05 products of the
-//     tiles that chain and prep leave, and the outputs' rows from TMEM.
+// Only S goes from chunk to chunk, so the work is cut where S enters:
+//   - gdn_prep_kernel, one CTA per (chunk, value head), all at once: K and Q as
+//     operands, M and P T, into the workspace;
+//   - gdn_chain_kernel, one CTA per (sequence, value head): R and S' chunk
+//     after chunk, two dependent products each, and the outputs beside them.
+// The chain is what a long sequence's time is made of; with M in place of T the
+// updates U never appear on it.
 //
 // Precision: the state keeps fp32 accuracy.  One decay per head leaves k and q
 // unscaled inside every product, so the rows' bf16 values are operands without
 // loss: prep rescales each row by a power of two to a norm in [1, 2) and stores
 // it as fp16 (exact down to 2^-17).  Every other operand that reaches the state
-// is two fp16 values, high and low, about 22 bits: S and U and V - .. are scaled
-// by a power of two per column so that the low part stays in fp16's range.  P
-// and the outputs' reading of S and U keep the high part only where the
-// outputs are bf16 (11 bits against their 8).
+// (S, R, T, M) is two fp16 values, high and low, about 22 bits; S and R are
+// scaled by a power of two per column so that the low part stays in fp16's range.  P, P T
+// and the outputs' reading of S and R keep the high part only where the outputs
+// are bf16 (11 bits against their 8).
 #include <cstddef>
 
 #include <cuda.h>
@@ -45,11 +37,7 @@ namespace kda {
 namespace {
 
 constexpr int C = 64;
-constexpr int THREADS = 512;
-constexpr int PREP_WARP = 8, PREP = 256;  // first prep warp, prep threads
-constexpr int XS = 20;                    // row stride of the fp32 diagonal blocks
-// TMEM columns: two raw products of 128, Q S, P U
-constexpr int TM_PROD = 0, TM_QS = 256, TM_PU = 320, TM_COLS = 512;
+constexpr int XS = 20;  // row stride of the fp32 diagonal blocks
 
 // ------------------------------------------------------------ fragments
 
@@ -95,30 +83,19 @@ __device__ __forceinline__ void split_h(float x, float y, uint32_t& hi, uint32_t
 __device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
 
-// Byte offsets of 16-byte piece `c` of row `r` in the tiles, all with 128-byte
-// rows, pieces permuted within eight rows (as a tensor copy with the 128-byte
-// swizzle leaves them and the tensor core's descriptors expect them), so that
-// eight rows' same piece lie in distinct banks.
+// Byte offsets of 16-byte piece `c` of row `r` in the operand tiles, all with
+// 128-byte rows, pieces permuted within eight rows (as a tensor copy with the
+// 128-byte swizzle leaves them and the tensor core's descriptors expect them),
+// so that eight rows' same piece lie in distinct banks.
 __device__ __forceinline__ uint32_t tile_at(int r, int c) { return (uint32_t)(r * 128 + (((c ^ r) & 7) << 4)); }
 // [K; Q]: 128 rows, 64 values wide, one such tile after the other
 __device__ __forceinline__ uint32_t kq_at(int r, int c) { return (uint32_t)((c >> 3) * 16384) + tile_at(r, c); }
-// the same with ROWS rows
-template <int ROWS> __device__ __forceinline__ uint32_t half_at(int r, int c)
-{
-    return (uint32_t)((c >> 3) * ROWS * 128) + tile_at(r, c);
-}
-// V: 64 rows of W values; 64-byte rows with the 64-byte swizzle where W = 32
-template <int W> __device__ __forceinline__ uint32_t v_at(int r, int c)
-{
-    if constexpr (W == 64) return tile_at(r, c);
-    else return (uint32_t)(r * 64 + ((c ^ (r >> 1)) & 3) * 16);
-}
 
 // 2^-e and 2^e for the e that brings m into [1, 2), kept within 2^+-60 (so
-// that products of two such factors stay finite).
+// that products of two such factors stay finite); 1 for m = 0.
 __device__ __forceinline__ void pow2_scale(float m, float& down, float& up)
 {
-    const uint32_t e = min(max((__float_as_uint(m) >> 23) & 255u, 67u), 187u);
+    const uint32_t e = m == 0.f ? 127u : min(max((__float_as_uint(m) >> 23) & 255u, 67u), 187u);
     down = __uint_as_float((254u - e) << 23);
     up = __uint_as_float(e << 23);
 }
@@ -137,42 +114,6 @@ __device__ __forceinline__ float exp2_sfu(float x)
     return y;
 }
 
-// ------------------------------------------------------------ shared memory
-
-template <int DK, int DVT, bool F32> struct Smem {
-    static constexpr int PARTS = F32 ? 2 : 1;
-    static constexpr int HALVES = DK <= 64 ? 1 : DK / 64;  // 64-wide tiles a row spans (dk = 32: half of one)
-    unsigned char kq[3][HALVES * 16384];   // bf16 rows of k, then q; fp16 later
-    unsigned char v[3][C * DVT * 2];
-    // T high, P high, T low (and P low): 64 x 64 fp16 tiles; T over P is one 128-row operand
-    unsigned char tp[2][(2 + PARTS) * 8192];
-    unsigned char st[PARTS][HALVES * DVT * 128];  // S^T: a row a column of dv
-    unsigned char ut[PARTS][DVT * 128];           // U^T likewise
-    // read four at a time: each on a 16-byte boundary
-    alignas(16) float x[C * XS];           // A's diagonal blocks, 16 x 16 each
-    // per chunk row: beta; beta sk e^G; sk; e^{G_C - G}; scale sq e^G; scale sq
-    float beta[2][C], ek[2][C], sk[2][C], w[2][C], e1[2][C], e2[2][C];
-    alignas(16) float f1[2][DVT], f2[2][DVT];  // the scales of S^T's and U^T's columns
-    alignas(16) float eg[C], gh[C], gl[C];  // e^G and G / ln 2 in two words
-    alignas(16) float norm[2 * C];         // squared norms of k's and q's rows
-    alignas(16) float row[2 * C], colk[C], down[2 * C];  // factors of A's and P's rows, of A's columns; of the stored rows
-    float last[2];                         // e^{G_C}
-    uint64_t loaded[3], kv_free[3];        // a chunk's rows; their last use
-    uint64_t prod_full[2], prod_free[2];   // raw products
-    uint64_t ready[2], tp_free[2];         // T, P and the factors; their last use
-    uint64_t s_full, s_free, u_full[2];    // S^T's tile; U^T's
-    uint64_t o_full, o_free;               // Q S and P U in TMEM (which frees U^T's tile); read
-    uint32_t tmem;
-    int found;
-
-    __device__ __forceinline__ unsigned char* t_hi(int b) { return tp[b]; }
-    __device__ __forceinline__ unsigned char* t_lo(int b) { return tp[b] + 16384; }
-};
-
-__device__ __forceinline__ void prep_sync() { asm volatile("bar.sync 1, %0;" ::"n"(PREP) : "memory"); }
-// the four warps that invert T
-__device__ __forceinline__ void invert_sync() { asm volatile("bar.sync 2, 128;" ::: "memory"); }
-
 // Bounded waits: after one that gives up the others only look once, and the
 // role reports it at its end.
 struct Waiter {
@@ -189,13 +130,66 @@ __device__ __forceinline__ void warp_arrive(uint64_t& bar, int lane)
     if (lane == 0) ptx::mbar_arrive(&bar);
 }
 
-__device__ __forceinline__ float quad_max(float x)
-{
-    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-    return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-}
+// ------------------------------------------------------------ workspace
+
+// What prep leaves for a chunk: [K; Q] for each key head, and for each value head
+// M^T (dk rows over the chunk's rows, high and low), P T (high; and low), and the factors.
+struct Factors {
+    float beta[C], ek[C];  // beta; beta e^G and k's row factor
+    float e1[C], e2[C];    // scale, q's row factor, e^G (e1)
+    float last, x;         // e^{G_C}; what M and P T still have to be multiplied by
+    float pad[30];
+};
+template <int DK, bool F32> struct Slot {
+    static constexpr int HALVES = DK <= 64 ? 1 : DK / 64;  // 64-wide tiles a row spans (dk = 32: half of one)
+    static constexpr int KQ = HALVES * 16384, M = DK * 128, PARTS = F32 ? 2 : 1;
+    static constexpr int V = 2 * M + PARTS * 8192 + (int)sizeof(Factors);
+    static_assert(V % 128 == 0, "slots on the bulk copies' and the operand tiles' boundaries");
+};
+// Chunk c of a sequence that starts at row `begin` is slot begin / 64 + seq + c:
+// sequences never share one, and there are at most T / 64 + N.
+__host__ __device__ __forceinline__ long long slot_count(int N, int T) { return (long long)(T / C) + N; }
+
+struct Work {
+    unsigned char* kq;  // [slot][Hk]
+    unsigned char* v;   // [slot][Hv]
+};
 
 // ------------------------------------------------------------ prep
+
+struct RowMaps {
+    CUtensorMap q, k, v;
+};
+
+constexpr int PREP = 256;
+
+template <int DK, bool F32> struct PrepSmem {
+    using L = Slot<DK, F32>;
+    static constexpr int PARTS = L::PARTS;
+    unsigned char kq[L::KQ];  // bf16 rows of k, then q; fp16 later
+    union {
+        struct {  // 64 x 64 fp16 tiles
+            unsigned char t_hi[8192], t_lo[8192], p_hi[8192], p_lo[F32 ? 8192 : 128];
+            unsigned char ts[PARTS][8192];  // diag(k's row factors / x) T
+            unsigned char tw[2][8192];      // diag(e^{G_C - G}) Ts
+        };
+        struct {  // then what they give, as the slot holds it
+            unsigned char m[2][L::M], pt[PARTS][8192];
+        };
+    };
+    Factors fac;
+    alignas(16) float xd[C * XS];  // A's diagonal blocks, 16 x 16 each
+    alignas(16) float eg[C], gh[C], gl[C], w[C];  // e^G, G / ln 2 in two words, e^{G_C - G}
+    alignas(16) float norm[2 * C];  // squared norms of k's and q's rows
+    alignas(16) float row[2 * C], colk[C], down[2 * C], sk[C];  // factors of A's and P's rows, of A's columns; of the stored rows
+    uint64_t loaded, prod;
+    uint32_t tmem;
+    int seq;
+};
+
+__device__ __forceinline__ void prep_sync() { __syncthreads(); }
+// the four warps that invert T
+__device__ __forceinline__ void invert_sync() { asm volatile("bar.sync 2, 128;" ::: "memory"); }
 
 // (h, l) += (oh, ol) in double-word fp32
 __device__ __forceinline__ void dw_add(float& h, float& l, float oh, float ol)
@@ -209,7 +203,7 @@ __device__ __forceinline__ void dw_add(float& h, float& l, float oh, float ol)
 
 // One warp, rows 2 lane and 2 lane + 1 of a chunk: running sums of their log2
 // decays g (double word: differences of large sums keep their small part).
-template <class S> __device__ __forceinline__ void scan_rows(S& sm, int b, float2 g, int lane)
+template <class S> __device__ __forceinline__ void scan_rows(S& sm, float2 g, int lane)
 {
     float h = g.x, l = 0.f;
     dw_add(h, l, g.y, 0.f);
@@ -225,9 +219,9 @@ template <class S> __device__ __forceinline__ void scan_rows(S& sm, int b, float
     *reinterpret_cast<float2*>(&sm.gh[2 * lane]) = make_float2(ph, h);
     *reinterpret_cast<float2*>(&sm.gl[2 * lane]) = make_float2(pl, l);
     *reinterpret_cast<float2*>(&sm.eg[2 * lane]) = make_float2(exp2_sfu(ph + pl), exp2_sfu(h + l));
-    *reinterpret_cast<float2*>(&sm.w[b][2 * lane]) =
+    *reinterpret_cast<float2*>(&sm.w[2 * lane]) =
         make_float2(exp2_sfu((th - ph) + (tl - pl)), exp2_sfu((th - h) + (tl - l)));
-    if (lane == 0) sm.last[b] = exp2_sfu(th + tl);
+    if (lane == 0) sm.fac.last = exp2_sfu(th + tl);
 }
 
 // A row of [K; Q]: bf16 -> fp16 times a power of two, in place; zeros for a
@@ -271,9 +265,9 @@ __device__ __forceinline__ void put_pair(unsigned char* hi_tile, unsigned char* 
 // T21's place.
 template <int SIZE> struct Merge {
     float pt[SIZE / 8][4];  // (A21 T11)^T, rows n: its accumulators are the next product's right operand
-    template <class S> __device__ __forceinline__ void first(S& sm, int b, int i0, int j0, int n0, int lane)
+    template <class S> __device__ __forceinline__ void first(S& sm, int i0, int j0, int n0, int lane)
     {
-        const uint32_t th = ptx::smem_u32(sm.t_hi(b)), tl = ptx::smem_u32(sm.t_lo(b));
+        const uint32_t th = ptx::smem_u32(sm.t_hi), tl = ptx::smem_u32(sm.t_lo);
         const int brow = (lane & 7) + ((lane >> 4) & 1) * 8, bcol = (lane >> 3) & 1;
 #pragma unroll
         for (int t = 0; t < SIZE / 8; ++t) pt[t][0] = pt[t][1] = pt[t][2] = pt[t][3] = 0.f;
@@ -297,9 +291,9 @@ template <int SIZE> struct Merge {
             for (int t = 0; t < SIZE / 8; ++t) mma(pt[t], al, bh[t >> 1][2 * (t & 1)], bh[t >> 1][2 * (t & 1) + 1]);
         }
     }
-    template <class S> __device__ __forceinline__ void second(S& sm, int b, int i0, int mt, float (&o)[2][4], int lane)
+    template <class S> __device__ __forceinline__ void second(S& sm, int i0, int mt, float (&o)[2][4], int lane)
     {
-        const uint32_t th = ptx::smem_u32(sm.t_hi(b)), tl = ptx::smem_u32(sm.t_lo(b));
+        const uint32_t th = ptx::smem_u32(sm.t_hi), tl = ptx::smem_u32(sm.t_lo);
 #pragma unroll
         for (int n = 0; n < 2; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
 #pragma unroll
@@ -321,50 +315,108 @@ template <int SIZE> struct Merge {
         }
     }
     template <class S>
-    __device__ __forceinline__ void store(S& sm, int b, int i0, int j0, int n0, int mt, const float (&o)[2][4], int lane)
+    __device__ __forceinline__ void store(S& sm, int i0, int j0, int n0, int mt, const float (&o)[2][4], int lane)
     {
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-                put_pair(sm.t_hi(b), sm.t_lo(b), i0 + mt * 16 + (lane >> 2) + i * 8, j0 + n0 + n * 8 + (lane & 3) * 2,
+                put_pair(sm.t_hi, sm.t_lo, i0 + mt * 16 + (lane >> 2) + i * 8, j0 + n0 + n * 8 + (lane & 3) * 2,
                          -o[n][2 * i], -o[n][2 * i + 1]);
     }
 };
 
-// Chunk m of prep warp w (n rows of it are real).  Lane and w & 3 give the
-// row of [K; Q] whose products the warp reads, w >> 2 which half of k's rows it
-// reads them against; the halves above the diagonal (w = 4 and 6) are left out.
-// The loops stay rolled: this runs once a chunk beside the other roles' code,
-// and what the instruction cache does not hold is fetched anew each time (at
-// 150 KB of code that was the kernel's first stall).
-template <int DK, int DVT, bool F32, class S>
-__device__ __forceinline__ void prep_chunk(S& sm, int m, const GdnArgs& a, int n, float2 g, float2 beta, Waiter& wait,
-                                           uint32_t tmem, int w, int lane)
+// One chunk's share of one value head.  Bound: latency (a dozen dependent
+// phases of a few hundred instructions each); two CTAs an SM fill each other's gaps.
+template <int DK, bool F32>
+__global__ void __launch_bounds__(PREP, 2) gdn_prep_kernel(const GdnArgs a, const __grid_constant__ RowMaps maps, const Work ws)
 {
-    const int b = m & 1, slot = m % 3;
-    const int lr = (w & 3) * 32 + lane, r = lr & (C - 1), type = lr >> 6, s0 = (w >> 2) * 32;  // type 0: k, 1: q
-    const uint32_t at = tmem + ((uint32_t)((w & 3) * 32) << 16) + TM_PROD + b * 128;
-    if (m >= 2) wait(sm.tp_free[b], (m - 2) >> 1);
-    if (w == 4) {
-        *reinterpret_cast<float2*>(&sm.beta[b][2 * lane]) = beta;
-        scan_rows(sm, b, g, lane);
-    } else {
-        wait(sm.prod_full[b], m >> 1);
-        ptx::tc_fence_after();
-        if (w == 0 || w >= 5) {
-            // the squared norms of 32 rows of k (w = 0, 5) or q: the diagonal
-            const int c0 = w == 0 ? 0 : (w - 4) * 32;
-            float y = 0.f;
+    extern __shared__ __align__(1024) unsigned char dyn[];
+    using S = PrepSmem<DK, F32>;
+    using L = Slot<DK, F32>;
+    S& sm = *reinterpret_cast<S*>(dyn);
+    const int t = threadIdx.x, w = t >> 5, lane = t & 31;
+    const int h = blockIdx.x % a.Hv, rep = a.Hv / a.Hk, hk = h / rep;
+    const int slot = blockIdx.x / a.Hv;
+    if (t == 0) sm.seq = -1;
+    __syncthreads();
+    // the last sequence whose slots start at or before this one
+    for (int s = t; s < a.N; s += PREP) {
+        const int b = a.cu_seqlens[s], e = a.cu_seqlens[s + 1];
+        const int base = b / C + s;
+        if (b >= 0 && e > b && e <= a.T && slot >= base && slot < base + (e - b + C - 1) / C) atomicMax(&sm.seq, s);
+    }
+    __syncthreads();
+    const int seq = sm.seq;
+    if (seq < 0 || (a.slots && (a.slots[seq] < 0 || a.slots[seq] >= a.num_slots))) return;
+    const int begin = a.cu_seqlens[seq], end = a.cu_seqlens[seq + 1];
+    const int r0 = begin + (slot - begin / C - seq) * C, n = min(C, end - r0);
+
+    if (t == 0) {
+        ptx::mbar_init(&sm.loaded, 1);
+        ptx::mbar_init(&sm.prod, 1);
+        ptx::fence_mbar_init();
+        ptx::mbar_arrive_expect_tx(&sm.loaded, L::KQ);
+        const uint64_t policy = ptx::policy_evict_normal();  // the key head's other value heads read the same rows
 #pragma unroll 1
-            for (int c = 0; c < 32; c += 8) {
-                float d[8];
-                ptx::tmem_ld8(at + c0 + c, d);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) y = c + i == lane ? d[i] : y;
-            }
-            sm.norm[lr] = y;
+        for (int i = 0; i < L::HALVES; ++i) {
+            ptx::tma_load_2d(sm.kq + i * 16384, &maps.k, hk * DK + i * 64, r0, &sm.loaded, policy);
+            ptx::tma_load_2d(sm.kq + i * 16384 + 8192, &maps.q, hk * DK + i * 64, r0, &sm.loaded, policy);
         }
+    }
+    if (w == 1) ptx::tmem_alloc(&sm.tmem, 128);
+    if (w == 4) {
+        // two rows a lane: gates and running sums
+        const float ea = expf(a.A_log[h]) * 1.44269504088896341f, dt = a.dt_bias[h];
+        float g[2] = {0.f, 0.f}, bt[2] = {0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (2 * lane + i < n) {
+                const size_t at = (size_t)(r0 + 2 * lane + i) * a.Hv + h;
+                g[i] = gdn_log_alpha(ea, ldv(static_cast<const __nv_bfloat16*>(a.a) + at), dt);
+                bt[i] = sigmoidf_(ldv(static_cast<const __nv_bfloat16*>(a.b) + at));
+            }
+        sm.fac.beta[2 * lane] = bt[0];
+        sm.fac.beta[2 * lane + 1] = bt[1];
+        scan_rows(sm, make_float2(g[0], g[1]), lane);
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = sm.tmem;
+    Waiter wait{false};
+    wait(sm.loaded, 0);
+    if (w == 0) {
+        if (lane == 0) {
+            // [K; Q] [K; Q]^T: k.k, q.k and, on the diagonal, both squared norms
+            const uint32_t kq = ptx::smem_u32(sm.kq);
+#pragma unroll 1
+            for (int kt = 0; kt < DK / 16; ++kt) {
+                const uint64_t d = ptx::desc_sw128(kq + (kt >> 2) * 16384 + (kt & 3) * 32);
+                ptx::mma_f16_ss(tmem, d, d, ptx::idesc_bf16(128, 128), kt > 0);
+            }
+            ptx::mma_commit(&sm.prod);
+        }
+        __syncwarp();
+    }
+    // a row of [K; Q] a lane (w & 3), against half of k's rows (w >> 2); the
+    // halves above the diagonal (w = 4 and 6) are left out
+    const int lr = (w & 3) * 32 + lane, r = lr & (C - 1), type = lr >> 6, s0 = (w >> 2) * 32;  // type 0: k, 1: q
+    const uint32_t at = tmem + ((uint32_t)((w & 3) * 32) << 16);
+    wait(sm.prod, 0);
+    ptx::tc_fence_after();
+    if (w == 0 || w >= 5) {
+        // the squared norms of 32 rows of k (w = 0, 5) or q: the diagonal
+        const int c0 = w == 0 ? 0 : (w - 4) * 32;
+        float y = 0.f;
+#pragma unroll 1
+        for (int c = 0; c < 32; c += 8) {
+            float d[8];
+            ptx::tmem_ld8(at + c0 + c, d);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y = c + i == lane ? d[i] : y;
+        }
+        sm.norm[lr] = y;
     }
     prep_sync();
     if (w < 4) {
@@ -375,14 +427,14 @@ __device__ __forceinline__ void prep_chunk(S& sm, int m, const GdnArgs& a, int n
         const float nrm = r < n ? (a.l2 ? rsqrtf(ss + a.l2_eps) : 1.f) : 0.f, f = nrm * up;
         sm.down[lr] = down;
         if (type == 0) {
-            const float be = sm.beta[b][r];
-            sm.sk[b][r] = f;
-            sm.ek[b][r] = be * f * sm.eg[r];
+            const float be = sm.fac.beta[r];
+            sm.sk[r] = f;
+            sm.fac.ek[r] = be * f * sm.eg[r];
             sm.colk[r] = nrm;  // A comes from the raw rows' products
             sm.row[r] = be * nrm;
         } else {
-            sm.e1[b][r] = a.scale * f * sm.eg[r];
-            sm.e2[b][r] = a.scale * f;
+            sm.fac.e1[r] = a.scale * f * sm.eg[r];
+            sm.fac.e2[r] = a.scale * f;
             sm.row[lr] = down;  // P is that of the stored rows
         }
     }
@@ -392,9 +444,9 @@ __device__ __forceinline__ void prep_chunk(S& sm, int m, const GdnArgs& a, int n
         const float rh = sm.gh[r], rl = sm.gl[r], rf = sm.row[lr];
         const float* cf = type == 0 ? sm.colk : sm.down;
         const int lim = r < n ? r + type : 0;
-        unsigned char* hi_tile = sm.tp[b];
-        unsigned char* lo_tile = sm.tp[b] + 16384;
-#pragma unroll 1
+        unsigned char* hi_tile = type == 0 ? sm.t_hi : sm.p_hi;
+        unsigned char* lo_tile = type == 0 ? sm.t_lo : sm.p_lo;
+#pragma unroll 2
         for (int p = 0; p < 4; ++p) {
             uint32_t hi[4], lo[4];
             float v[8], d[8];
@@ -415,27 +467,29 @@ __device__ __forceinline__ void prep_chunk(S& sm, int m, const GdnArgs& a, int n
 #pragma unroll
             for (int i = 0; i < 4; ++i) split_h(v[2 * i], v[2 * i + 1], hi[i], lo[i]);
             const int c = (s0 >> 3) + p;
-            *reinterpret_cast<uint4*>(hi_tile + tile_at(lr, c)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            if (F32 || type == 0) *reinterpret_cast<uint4*>(lo_tile + tile_at(lr, c)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            *reinterpret_cast<uint4*>(hi_tile + tile_at(r, c)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            if (F32 || type == 0) *reinterpret_cast<uint4*>(lo_tile + tile_at(r, c)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             if (type == 0 && (r >> 4) == (c >> 1)) {
-                float* x = &sm.x[r * XS + (c & 1) * 8];
+                float* x = &sm.xd[r * XS + (c & 1) * 8];
                 *reinterpret_cast<float4*>(x) = make_float4(v[0], v[1], v[2], v[3]);
                 *reinterpret_cast<float4*>(x + 4) = make_float4(v[4], v[5], v[6], v[7]);
             }
         }
     }
     ptx::tc_fence_before();
-    warp_arrive(sm.prod_free[b], lane);
     prep_sync();
     if (w >= 4) {
-        // meanwhile the rows themselves
-        const int row = (w - 4) * 32 + lane, rr = row & (C - 1);
-        wait(sm.loaded[slot], m / 3);
-        convert_row<DK>(sm.kq[slot], row, sm.down[row], rr < n);
-        if (row < C && rr >= n)
-#pragma unroll 1
-            for (int c = 0; c < DVT / 8; ++c)
-                *reinterpret_cast<uint4*>(sm.v[slot] + v_at<DVT>(rr, c)) = make_uint4(0, 0, 0, 0);
+        // meanwhile the rows themselves, and the largest of k's factors
+        const int row = (w - 4) * 32 + lane;
+        convert_row<DK>(sm.kq, row, sm.down[row], (row & (C - 1)) < n);
+        if (w == 7) {
+            float mx = fmaxf(sm.sk[lane], sm.sk[lane + 32]);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            float down, up;
+            pow2_scale(mx, down, up);
+            if (lane == 0) sm.fac.x = up;
+        }
     } else {
         {
             // a diagonal block a warp: forward substitution, a column a lane (both
@@ -447,7 +501,7 @@ __device__ __forceinline__ void prep_chunk(S& sm, int m, const GdnArgs& a, int n
                 float acc = i == c ? 1.f : 0.f, acc2 = 0.f;
 #pragma unroll
                 for (int j = 0; j < i; j += 4) {
-                    const float4 f = *reinterpret_cast<const float4*>(&sm.x[(d0 + i) * XS + j]);
+                    const float4 f = *reinterpret_cast<const float4*>(&sm.xd[(d0 + i) * XS + j]);
                     acc = fmaf(-f.x, x[j], acc);
                     if (j + 1 < i) acc2 = fmaf(-f.y, x[j + 1], acc2);
                     if (j + 2 < i) acc = fmaf(-f.z, x[j + 2], acc);
@@ -455,7 +509,7 @@ __device__ __forceinline__ void prep_chunk(S& sm, int m, const GdnArgs& a, int n
                 }
                 x[i] = acc + acc2;
             }
-            unsigned char* tile = lane < 16 ? sm.t_hi(b) : sm.t_lo(b);
+            unsigned char* tile = lane < 16 ? sm.t_hi : sm.t_lo;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const __half hi = __float2half_rn(x[i]);
@@ -468,319 +522,158 @@ __device__ __forceinline__ void prep_chunk(S& sm, int m, const GdnArgs& a, int n
         if (w < 2) {
             const int j0 = w * 32, i0 = j0 + 16;
             Merge<16> mg;
-            mg.first(sm, b, i0, j0, 0, lane);
-            mg.second(sm, b, i0, 0, o, lane);
+            mg.first(sm, i0, j0, 0, lane);
+            mg.second(sm, i0, 0, o, lane);
             __syncwarp();
-            mg.store(sm, b, i0, j0, 0, 0, o, lane);
+            mg.store(sm, i0, j0, 0, 0, o, lane);
         }
         invert_sync();
         Merge<32> mg;
         const int n0 = (w & 1) * 16, mt = w >> 1;
-        mg.first(sm, b, 32, 0, n0, lane);
-        mg.second(sm, b, 32, mt, o, lane);
+        mg.first(sm, 32, 0, n0, lane);
+        mg.second(sm, 32, mt, o, lane);
         invert_sync();  // every warp has read A21
-        mg.store(sm, b, 32, 0, n0, mt, o, lane);
+        mg.store(sm, 32, 0, n0, mt, o, lane);
     }
+    prep_sync();
+    {
+        // Ts and Tw, sixteen values of a row a thread; zero above the diagonal
+        const int rr = t >> 2, c0 = (t & 3) * 2;
+        const float f = sm.sk[rr] / sm.fac.x, fw = f * sm.w[rr];
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+            const int c = c0 + z;
+            const uint4 h4 = *reinterpret_cast<const uint4*>(sm.t_hi + tile_at(rr, c));
+            const uint4 l4 = *reinterpret_cast<const uint4*>(sm.t_lo + tile_at(rr, c));
+            const uint32_t hv[4] = {h4.x, h4.y, h4.z, h4.w}, lv[4] = {l4.x, l4.y, l4.z, l4.w};
+            uint32_t sh[4], sl[4], wh[4], wl[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 x = unpack_h(hv[i]), y = unpack_h(lv[i]);
+                const float u0 = c * 8 + 2 * i <= rr ? x.x + y.x : 0.f, u1 = c * 8 + 2 * i + 1 <= rr ? x.y + y.y : 0.f;
+                split_h(u0 * f, u1 * f, sh[i], sl[i]);
+                split_h(u0 * fw, u1 * fw, wh[i], wl[i]);
+            }
+            *reinterpret_cast<uint4*>(sm.ts[0] + tile_at(rr, c)) = make_uint4(sh[0], sh[1], sh[2], sh[3]);
+            if (F32) *reinterpret_cast<uint4*>(sm.ts[F32 ? 1 : 0] + tile_at(rr, c)) = make_uint4(sl[0], sl[1], sl[2], sl[3]);
+            *reinterpret_cast<uint4*>(sm.tw[0] + tile_at(rr, c)) = make_uint4(wh[0], wh[1], wh[2], wh[3]);
+            *reinterpret_cast<uint4*>(sm.tw[1] + tile_at(rr, c)) = make_uint4(wl[0], wl[1], wl[2], wl[3]);
+        }
+    }
+    prep_sync();
+    const int arow = lane & 15, acol = lane >> 4, brow = (lane & 7) + ((lane >> 4) & 1) * 8, bcol = (lane >> 3) & 1;
+    auto store_tile = [&](unsigned char* hi_tile, unsigned char* lo_tile, int row0, const float (&c)[8][4]) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) split_h(c[2 * q + (i >> 1)][2 * (i & 1)], c[2 * q + (i >> 1)][2 * (i & 1) + 1], hi[i], lo[i]);
+            const uint32_t o = tile_at(row0 + arow, q * 2 + acol);
+            stsm(ptx::smem_u32(hi_tile) + o, hi);
+            if (lo_tile) stsm(ptx::smem_u32(lo_tile) + o, lo);
+        }
+    };
+    float cm[8][4], cp[8][4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) cm[i][j] = cp[i][j] = 0.f;
+    if (w * 16 < DK) {
+        // M^T: sixteen of dk's rows a warp, K'^T (exact) times Tw, high and low; row r of Tw meets columns s <= r
+        const uint32_t kb = ptx::smem_u32(sm.kq), th = ptx::smem_u32(sm.tw[0]), tl = ptx::smem_u32(sm.tw[1]);
+#pragma unroll
+        for (int kt = 0; kt < 4; ++kt) {
+            uint32_t x[4], f[4], e[4];
+            // left operand (dk, r) from rows r of k: transposed
+            ldsm_t(x, kb + kq_at(kt * 16 + brow, w * 2 + bcol));
+#pragma unroll
+            for (int q = 0; q <= kt; ++q) {
+                ldsm_t(f, th + tile_at(kt * 16 + arow, q * 2 + acol));
+                ldsm_t(e, tl + tile_at(kt * 16 + arow, q * 2 + acol));
+                mma(cm[2 * q], x, f[0], f[1]);
+                mma(cm[2 * q + 1], x, f[2], f[3]);
+                mma(cm[2 * q], x, e[0], e[1]);
+                mma(cm[2 * q + 1], x, e[2], e[3]);
+            }
+        }
+    }
+    if (w >= 4) {
+        // P T: sixteen rows a warp
+        const int mt = w - 4;
+        const uint32_t pb[2] = {ptx::smem_u32(sm.p_hi), ptx::smem_u32(sm.p_lo)};
+        const uint32_t tb[2] = {ptx::smem_u32(sm.ts[0]), ptx::smem_u32(sm.ts[F32 ? 1 : 0])};
+#pragma unroll
+        for (int kt = 0; kt < 4; ++kt) {
+            if (kt > mt) break;  // P's columns up to its rows
+            uint32_t x[4], y[4], f[4], e[4];
+            ldsm(x, pb[0] + tile_at(mt * 16 + arow, kt * 2 + acol));
+            if (F32) ldsm(y, pb[1] + tile_at(mt * 16 + arow, kt * 2 + acol));
+#pragma unroll
+            for (int q = 0; q <= kt; ++q) {
+                ldsm_t(f, tb[0] + tile_at(kt * 16 + arow, q * 2 + acol));
+                mma(cp[2 * q], x, f[0], f[1]);
+                mma(cp[2 * q + 1], x, f[2], f[3]);
+                if (F32) {
+                    ldsm_t(e, tb[1] + tile_at(kt * 16 + arow, q * 2 + acol));
+                    mma(cp[2 * q], y, f[0], f[1]);
+                    mma(cp[2 * q + 1], y, f[2], f[3]);
+                    mma(cp[2 * q], x, e[0], e[1]);
+                    mma(cp[2 * q + 1], x, e[2], e[3]);
+                }
+            }
+        }
+    }
+    prep_sync();  // the tiles read above make room
+    if (w * 16 < DK) store_tile(sm.m[0], sm.m[1], w * 16, cm);
+    if (w >= 4) store_tile(sm.pt[0], F32 ? sm.pt[F32 ? 1 : 0] : nullptr, (w - 4) * 16, cp);
     ptx::fence_proxy_async_smem();
-    warp_arrive(sm.ready[b], lane);
+    if (wait.dead) flag_status(a.dev_status, KDA_DEV_TIMEOUT);
+    prep_sync();
+    if (t == 0) {
+        unsigned char* d = ws.v + ((long long)slot * a.Hv + h) * L::V;
+        ptx::bulk_s2g(d, sm.m, 2 * L::M + L::PARTS * 8192);
+        ptx::bulk_s2g(d + 2 * L::M + L::PARTS * 8192, &sm.fac, sizeof(Factors));
+        if (h % rep == 0) ptx::bulk_s2g(ws.kq + ((long long)slot * a.Hk + hk) * L::KQ, sm.kq, L::KQ);
+        ptx::bulk_commit();
+        ptx::bulk_wait_all();
+    }
+    if (w == 1) ptx::tmem_dealloc(tmem, 128);
 }
 
 // ------------------------------------------------------------ chain
 
-// Chunk m of a chain warp: 16 columns of dv.  s holds S^T times g[0] (column
-// lane / 4) and g[1] (eight further), ig their inverses.
-template <int DK, int DVT, bool F32, class S>
-__device__ __forceinline__ void chain_chunk(S& sm, int m, float (&s)[DK / 8][4], float (&ig)[2], Waiter& wait, int warp,
-                                            int lane)
+// TMEM columns: the critical products (K S; then M^T R), S high and low, R high
+// and low as left operands (two fp16 a column), Q S, (P T) R
+constexpr int TM_X = 0, TM_SH = 128, TM_SL = 192, TM_RH = 256, TM_RL = 288, TM_QS = 320, TM_PR = 384, TM_COLS = 512;
+constexpr int CHAIN_THREADS = 384;
+
+template <int DK, int DV, bool F32> struct ChainSmem {
+    using L = Slot<DK, F32>;
+    unsigned char kq[2][L::KQ];
+    unsigned char work[2][(L::V + 1023) / 1024 * 1024];  // M^T, P T, factors
+    unsigned char v[2][C * DV * 2];                      // dense rows
+    float f1[2][DV], f2[2][DV];  // the scales of S's and R's columns
+    uint64_t loaded[2], freed[2];
+    uint64_t s_full, ks_full, r_full, su_full, o_full, o_free, f_full[2];
+    uint32_t tmem;
+    int found;
+};
+
+__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(a, fmaxf(b, c)); }
+
+// Packs N values two by two as fp16 high and low parts and stores them to N / 2 columns each.
+template <int N> __device__ __forceinline__ void store_split(uint32_t hi_at, uint32_t lo_at, const float (&x)[N])
 {
-    const int slot = m % 3, b = m & 1, q2 = (lane & 3) * 2;
-    const uint32_t kb = ptx::smem_u32(sm.kq[slot]), vb = ptx::smem_u32(sm.v[slot]);
-    const uint32_t tb[2] = {ptx::smem_u32(sm.t_hi(b)), ptx::smem_u32(sm.t_lo(b))};
-    const int brow = (lane & 7) + ((lane >> 4) & 1) * 8, bcol = (lane >> 3) & 1;  // K-contiguous operand
-    const int trow = lane & 15, tcol = lane >> 4;                                 // transposed operand
-    if (m > 0) wait(sm.s_free, m - 1);
-
-    // S^T K^T, each k-tile's fragments made a tile ahead
-    float r[8][4];
 #pragma unroll
-    for (int t = 0; t < 8; ++t)
+    for (int b = 0; b < N; b += 32) {
+        uint32_t hi[16], lo[16];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) r[t][i] = 0.f;
-    __half2 m0 = __float2half2_rn(0.f), m1 = m0;
-    uint32_t f[2][4][4], hi[2][4], lo[2][4];
-    auto left = [&](int kt) {  // k-tile kt of S^T, split, also for the outputs
-#pragma unroll
-        for (int t = 0; t < 4; ++t) ldsm(f[kt & 1][t], kb + kq_at(t * 16 + brow, kt * 2 + bcol));
-        uint32_t(&x)[4] = hi[kt & 1], (&y)[4] = lo[kt & 1];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float* v = &s[2 * kt + (i >> 1)][2 * (i & 1)];
-            split_h(v[0], v[1], x[i], y[i]);
-            const __half2 h = __habs2(*reinterpret_cast<const __half2*>(&x[i]));
-            if (i & 1) m1 = __hmax2(m1, h);
-            else m0 = __hmax2(m0, h);
-        }
-        const uint32_t o = half_at<DVT>(warp * 16 + trow, kt * 2 + tcol);
-        stsm(ptx::smem_u32(sm.st[0]) + o, x);
-        if (F32) stsm(ptx::smem_u32(sm.st[F32 ? 1 : 0]) + o, y);
-    };
-    left(0);
-#pragma unroll
-    for (int kt = 0; kt < DK / 16; ++kt) {
-        if (kt + 1 < DK / 16) left(kt + 1);
-        uint32_t(&e)[4][4] = f[kt & 1];
-#pragma unroll
-        for (int t = 0; t < 8; ++t) mma(r[t], hi[kt & 1], e[t >> 1][2 * (t & 1)], e[t >> 1][2 * (t & 1) + 1]);
-#pragma unroll
-        for (int t = 0; t < 8; ++t) mma(r[t], lo[kt & 1], e[t >> 1][2 * (t & 1)], e[t >> 1][2 * (t & 1) + 1]);
+        for (int i = 0; i < 16; ++i) split_h(x[b + 2 * i], x[b + 2 * i + 1], hi[i], lo[i]);
+        ptx::tmem_st16_async(hi_at + b / 2, hi);
+        ptx::tmem_st16_async(lo_at + b / 2, lo);
     }
-    ptx::fence_proxy_async_smem();
-    warp_arrive(sm.s_full, lane);
-    // beta (V - e^G k.S), and each column's largest value
-    float mr[2] = {0.f, 0.f};
-#pragma unroll
-    for (int t = 0; t < 8; t += 2) {
-        uint32_t v[4];  // V^T: rows t*8.. of columns gq, gq+8; then the next eight rows
-        ldsm_t(v, vb + v_at<DVT>(t * 8 + brow, warp * 2 + bcol));
-#pragma unroll
-        for (int z = 0; z < 2; ++z) {
-            const float2 be = *reinterpret_cast<const float2*>(&sm.beta[b][(t + z) * 8 + q2]);
-            const float2 ek = *reinterpret_cast<const float2*>(&sm.ek[b][(t + z) * 8 + q2]);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                float* x = &r[t + z][2 * i];
-                x[0] = fmaf(-ek.x, x[0] * ig[i], be.x * bf_lo(v[2 * z + i]));
-                x[1] = fmaf(-ek.y, x[1] * ig[i], be.y * bf_hi(v[2 * z + i]));
-                mr[i] = fmaxf(mr[i], fmaxf(fabsf(x[0]), fabsf(x[1])));
-            }
-        }
-    }
-    float rd[2], ru[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) pow2_scale(quad_max(mr[i]), rd[i], ru[i]);
-    // U^T = R^T T^T (T is lower triangular: k-tile kt meets rows from 16 kt on)
-    float u[8][4];
-#pragma unroll
-    for (int t = 0; t < 8; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) u[t][i] = 0.f;
-    uint32_t f2[2][4][4];
-    auto part = [&](int kt) {
-#pragma unroll
-        for (int t = kt; t < 4; ++t) {
-            ldsm(f[kt & 1][t], tb[0] + tile_at(t * 16 + brow, kt * 2 + bcol));
-            ldsm(f2[kt & 1][t], tb[1] + tile_at(t * 16 + brow, kt * 2 + bcol));
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float* x = &r[2 * kt + (i >> 1)][2 * (i & 1)];
-            split_h(x[0] * rd[i & 1], x[1] * rd[i & 1], hi[kt & 1][i], lo[kt & 1][i]);
-        }
-    };
-    part(0);
-#pragma unroll
-    for (int kt = 0; kt < 4; ++kt) {
-        if (kt + 1 < 4) part(kt + 1);
-        uint32_t(&th)[4][4] = f[kt & 1], (&tl)[4][4] = f2[kt & 1], (&x)[4] = hi[kt & 1], (&y)[4] = lo[kt & 1];
-#pragma unroll
-        for (int t = 2 * kt; t < 8; ++t) mma(u[t], x, th[t >> 1][2 * (t & 1)], th[t >> 1][2 * (t & 1) + 1]);
-#pragma unroll
-        for (int t = 2 * kt; t < 8; ++t) mma(u[t], y, th[t >> 1][2 * (t & 1)], th[t >> 1][2 * (t & 1) + 1]);
-#pragma unroll
-        for (int t = 2 * kt; t < 8; ++t) mma(u[t], x, tl[t >> 1][2 * (t & 1)], tl[t >> 1][2 * (t & 1) + 1]);
-    }
-    // times k's row factor; the largest values with and without the decay to the chunk's end
-    float mu[2] = {0.f, 0.f}, mw[2] = {0.f, 0.f};
-#pragma unroll
-    for (int t = 0; t < 8; ++t) {
-        const float2 sk = *reinterpret_cast<const float2*>(&sm.sk[b][t * 8 + q2]);
-        const float2 w = *reinterpret_cast<const float2*>(&sm.w[b][t * 8 + q2]);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            float* x = &u[t][2 * i];
-            x[0] *= sk.x * ru[i];
-            x[1] *= sk.y * ru[i];
-            mu[i] = fmaxf(mu[i], fmaxf(fabsf(x[0]), fabsf(x[1])));
-            mw[i] = fmaxf(mw[i], fmaxf(fabsf(x[0]) * w.x, fabsf(x[1]) * w.y));
-        }
-    }
-    const float last = sm.last[b];
-    float ud[2], dec[2], g[2];
-    {
-        const float ms[2] = {fmaxf(__low2float(m0), __high2float(m0)) * ig[0],
-                             fmaxf(__low2float(m1), __high2float(m1)) * ig[1]};
-        const float old[2] = {ig[0], ig[1]};
-        float up[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            pow2_scale(quad_max(mu[i]), ud[i], up[i]);
-            pow2_scale(quad_max(fmaxf(mw[i], ms[i] * last)), g[i], ig[i]);
-            dec[i] = last * (g[i] * old[i]);
-        }
-        if (m > 0) wait(sm.o_full, m - 1);
-        if ((lane & 3) == 0) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                sm.f1[b][warp * 16 + (lane >> 2) + i * 8] = old[i];
-                sm.f2[b][warp * 16 + (lane >> 2) + i * 8] = up[i];
-            }
-        }
-    }
-#pragma unroll
-    for (int kt = 0; kt < 4; ++kt) {
-        uint32_t x[4], y[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float* v = &u[2 * kt + (i >> 1)][2 * (i & 1)];
-            if (F32) split_h(v[0] * ud[i & 1], v[1] * ud[i & 1], x[i], y[i]);
-            else x[i] = pack_h(v[0] * ud[i & 1], v[1] * ud[i & 1]);
-        }
-        const uint32_t o = half_at<DVT>(warp * 16 + trow, kt * 2 + tcol);
-        stsm(ptx::smem_u32(sm.ut[0]) + o, x);
-        if (F32) stsm(ptx::smem_u32(sm.ut[F32 ? 1 : 0]) + o, y);
-    }
-    ptx::fence_proxy_async_smem();
-    warp_arrive(sm.u_full[b], lane);
-    // S^T = e^{G_C} S^T + (U^T diag(e^{G_C - G})) K, in a scale that both terms fit
-#pragma unroll
-    for (int t = 0; t < DK / 8; ++t) {
-        s[t][0] *= dec[0];
-        s[t][1] *= dec[0];
-        s[t][2] *= dec[1];
-        s[t][3] *= dec[1];
-    }
-    constexpr int G = DK >= 64 ? 4 : 2, NG = DK / 16 / G;  // fragments loaded at a time, and such groups in a k-tile
-    auto right = [&](int step) {
-#pragma unroll
-        for (int t = 0; t < G; ++t)
-            ldsm_t(f[step & 1][t], kb + kq_at(step / NG * 16 + trow, (step % NG * G + t) * 2 + tcol));
-    };
-    auto decayed = [&](int kt) {
-#pragma unroll
-        for (int z = 0; z < 2; ++z) {
-            const float2 w = *reinterpret_cast<const float2*>(&sm.w[b][(2 * kt + z) * 8 + q2]);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float* x = &u[2 * kt + z][2 * i];
-                split_h(x[0] * (w.x * g[i]), x[1] * (w.y * g[i]), hi[kt & 1][2 * z + i], lo[kt & 1][2 * z + i]);
-            }
-        }
-    };
-    right(0);
-    decayed(0);
-#pragma unroll
-    for (int kt = 0; kt < 4; ++kt) {
-        if (kt + 1 < 4) decayed(kt + 1);
-#pragma unroll
-        for (int n = 0; n < NG; ++n) {
-            const int step = kt * NG + n;
-            if (step + 1 < 4 * NG) right(step + 1);
-            uint32_t(&e)[4][4] = f[step & 1];
-#pragma unroll
-            for (int t = 0; t < 2 * G; ++t)
-                mma(s[n * 2 * G + t], hi[kt & 1], e[t >> 1][2 * (t & 1)], e[t >> 1][2 * (t & 1) + 1]);
-#pragma unroll
-            for (int t = 0; t < 2 * G; ++t)
-                mma(s[n * 2 * G + t], lo[kt & 1], e[t >> 1][2 * (t & 1)], e[t >> 1][2 * (t & 1) + 1]);
-        }
-    }
+    ptx::tmem_wait_st();
 }
-
-// ------------------------------------------------------------ outputs
-
-// Issues the products of chunk m's outputs (one thread issues): with the rows
-// of [K; Q] and [T; P] as left operands, lanes 64 - 127 hold Q S and P U.
-template <int DK, int DVT, bool F32, class S>
-__device__ __forceinline__ void issue_outputs(S& sm, int m, Waiter& wait, uint32_t tmem, int lane)
-{
-    const int slot = m % 3, b = m & 1;
-    constexpr uint32_t id = ptx::idesc_f16(128, DVT);
-    wait(sm.ready[b], m >> 1);
-    wait(sm.s_full, m);
-    if (m > 0) wait(sm.o_free, m - 1);
-    ptx::tc_fence_after();
-    if (lane == 0) {
-        const uint32_t kq = ptx::smem_u32(sm.kq[slot]);
-#pragma unroll 1
-        for (int p = 0; p < (F32 ? 2 : 1); ++p) {
-            const uint32_t st = ptx::smem_u32(sm.st[F32 ? p : 0]);
-#pragma unroll 1
-            for (int kt = 0; kt < DK / 16; ++kt)
-                ptx::mma_f16_ss(tmem + TM_QS, ptx::desc_sw128(kq + (kt >> 2) * 16384 + (kt & 3) * 32),
-                                ptx::desc_sw128(st + (kt >> 2) * DVT * 128 + (kt & 3) * 32), id, p > 0 || kt > 0);
-        }
-        ptx::mma_commit(&sm.s_free);
-    }
-    __syncwarp();
-    wait(sm.u_full[b], m >> 1);
-    ptx::tc_fence_after();
-    if (lane == 0) {
-        // T P high with U high and low, T P low with U high
-        const uint32_t hi = ptx::smem_u32(sm.tp[b]), lo = hi + 16384;
-#pragma unroll 1
-        for (int p = 0; p < (F32 ? 3 : 1); ++p) {
-            const uint32_t x = p < 2 ? hi : lo, u = ptx::smem_u32(sm.ut[F32 && p == 1 ? 1 : 0]);
-#pragma unroll 1
-            for (int kt = 0; kt < 4; ++kt)
-                ptx::mma_f16_ss(tmem + TM_PU, ptx::desc_sw128(x + kt * 32), ptx::desc_sw128(u + kt * 32), id, p > 0 || kt > 0);
-        }
-        ptx::mma_commit(&sm.o_full);
-    }
-    __syncwarp();
-}
-
-// Rows of chunk m's outputs: o_r = scale sq (e^G q'.S + (P U)_r), a row a lane.
-template <int DVT, bool F32, class S>
-__device__ __forceinline__ void output_rows(S& sm, int m, void* out, long long row_stride, int n, Waiter& wait,
-                                            uint32_t tmem, int half, int lane)
-{
-    const int b = m & 1, r = half * 32 + lane;
-    wait(sm.ready[b], m >> 1);
-    wait(sm.u_full[b], m >> 1);
-    const float e1 = sm.e1[b][r], e2 = sm.e2[b][r];
-    wait(sm.o_full, m);
-    ptx::tc_fence_after();
-    const uint32_t at = tmem + ((uint32_t)(64 + half * 32) << 16);
-#pragma unroll 1
-    for (int c0 = 0; c0 < DVT; c0 += 16) {
-        float x[16], y[16];
-        ptx::tmem_ld16(at + TM_QS + c0, x);
-        ptx::tmem_ld16(at + TM_PU + c0, y);
-#pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-            const float4 f1 = *reinterpret_cast<const float4*>(&sm.f1[b][c0 + i]);
-            const float4 f2 = *reinterpret_cast<const float4*>(&sm.f2[b][c0 + i]);
-            x[i] = fmaf(e1, f1.x * x[i], e2 * (f2.x * y[i]));
-            x[i + 1] = fmaf(e1, f1.y * x[i + 1], e2 * (f2.y * y[i + 1]));
-            x[i + 2] = fmaf(e1, f1.z * x[i + 2], e2 * (f2.z * y[i + 2]));
-            x[i + 3] = fmaf(e1, f1.w * x[i + 3], e2 * (f2.w * y[i + 3]));
-        }
-        if (r < n) {
-            if constexpr (F32) {
-                float4* p = reinterpret_cast<float4*>(static_cast<float*>(out) + r * row_stride + c0);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) p[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-            } else {
-                uint4* p = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + r * row_stride + c0);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    uint32_t v[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const __nv_bfloat162 h = __floats2bfloat162_rn(x[8 * i + 2 * j], x[8 * i + 2 * j + 1]);
-                        v[j] = *reinterpret_cast<const uint32_t*>(&h);
-                    }
-                    p[i] = make_uint4(v[0], v[1], v[2], v[3]);
-                }
-            }
-        }
-        __syncwarp();
-    }
-    ptx::tc_fence_before();
-    warp_arrive(sm.o_free, lane);
-}
-
-// ------------------------------------------------------------ kernel
 
 // The sequence of rank `rank` by length, longest first (ties: lowest index):
 // long chains start first.  Up to one sequence a thread; more keep their order.
@@ -810,49 +703,35 @@ template <bool UP, int N> __device__ __forceinline__ void set_regs()
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-struct RowMaps {
-    CUtensorMap q, k, v;
-};
-
-template <int DK, int NW, bool F32>
-__global__ void __launch_bounds__(THREADS, 1) gdn_chunk_kernel(const GdnArgs a, const __grid_constant__ RowMaps maps, int dv)
+template <int DK, int DV, bool F32>
+__global__ void __launch_bounds__(CHAIN_THREADS, 1) gdn_chain_kernel(const GdnArgs a, const __grid_constant__ CUtensorMap vmap, const Work ws)
 {
-    constexpr int DVT = NW * 16;
+    constexpr int NW = DV / 32;
     extern __shared__ __align__(1024) unsigned char dyn[];
-    using S = Smem<DK, DVT, F32>;
+    using S = ChainSmem<DK, DV, F32>;
+    using L = Slot<DK, F32>;
     S& sm = *reinterpret_cast<S*>(dyn);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int parts = dv / DVT;
-    const int part = blockIdx.x % parts, h = (blockIdx.x / parts) % a.Hv;
-    const int seq = ranked_seq(a.cu_seqlens, a.N, blockIdx.x / (parts * a.Hv), &sm.found);
+    const int h = blockIdx.x % a.Hv;
+    const int seq = ranked_seq(a.cu_seqlens, a.N, blockIdx.x / a.Hv, &sm.found);
     int begin, end, state_slot;
     if (!gdn_unit(a, seq, begin, end, state_slot)) return;
     const int chunks = (end - begin + C - 1) / C;
-    const int col0 = part * DVT;
 
     if (tid == 0) {
-        for (int i = 0; i < 3; ++i) {
-            ptx::mbar_init(&sm.loaded[i], 1);
-            ptx::mbar_init(&sm.kv_free[i], NW + 2);
-        }
         for (int i = 0; i < 2; ++i) {
-            ptx::mbar_init(&sm.prod_full[i], 1);
-            ptx::mbar_init(&sm.prod_free[i], PREP / 32);
-            ptx::mbar_init(&sm.ready[i], PREP / 32);
-            ptx::mbar_init(&sm.tp_free[i], NW + 2);
-            ptx::mbar_init(&sm.u_full[i], NW);
+            ptx::mbar_init(&sm.loaded[i], 1);
+            ptx::mbar_init(&sm.freed[i], 2 * NW);
+            ptx::mbar_init(&sm.f_full[i], NW);
         }
         ptx::mbar_init(&sm.s_full, NW);
-        ptx::mbar_init(&sm.s_free, 1);
+        ptx::mbar_init(&sm.ks_full, 1);
+        ptx::mbar_init(&sm.r_full, NW);
+        ptx::mbar_init(&sm.su_full, 1);
         ptx::mbar_init(&sm.o_full, 1);
-        ptx::mbar_init(&sm.o_free, 2);
+        ptx::mbar_init(&sm.o_free, NW);
         ptx::fence_mbar_init();
     }
-    // P's quarter above the diagonal is read and never written
-#pragma unroll 1
-    for (int i = tid; i < (int)sizeof(sm.tp) / 16; i += THREADS)
-        reinterpret_cast<uint4*>(sm.tp)[i] = make_uint4(0, 0, 0, 0);
-    ptx::fence_proxy_async_smem();
     if (warp == 5) ptx::tmem_alloc(&sm.tmem, TM_COLS);
     ptx::tc_fence_before();
     __syncthreads();
@@ -860,127 +739,242 @@ __global__ void __launch_bounds__(THREADS, 1) gdn_chunk_kernel(const GdnArgs a, 
     const uint32_t tmem = sm.tmem;
     Waiter wait{false};
 
-    // Registers: the launch gives every thread 128; the chain's warpgroup takes
-    // what the others leave (232 + 88 + 2 * 96 <= 4 * 128).
+    // Registers: the launch gives every thread 168; the chain's warpgroup takes
+    // what the others leave (248 + 64 + 104 <= 3 * 168).
     if (warp < 4) {
-        set_regs<true, 232>();
+        set_regs<true, 248>();
         if (warp < NW) {
-            const size_t sbase = ((size_t)state_slot * a.Hv + h) * DK * dv + col0 + warp * 16 + (lane >> 2);
-            float s[DK / 8][4], ig[2], ms[2] = {0.f, 0.f};
+            // column c of the state, scaled by g
+            const int c = warp * 32 + lane;
+            const uint32_t lanes = (uint32_t)(warp * 32) << 16, at = tmem + lanes;
+            float* state = a.state + ((size_t)state_slot * a.Hv + h) * DK * DV + c;
+            float s[DK], mx = 0.f, g, ig, rd = 1.f, ru = 1.f;
 #pragma unroll
-            for (int t = 0; t < DK / 8; ++t)
+            for (int i = 0; i < DK; ++i) s[i] = state[(size_t)i * DV];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    s[t][i] = a.state[sbase + (size_t)(t * 8 + (lane & 3) * 2 + (i & 1)) * dv + (i >> 1) * 8];
-                    ms[i >> 1] = fmaxf(ms[i >> 1], fabsf(s[t][i]));
-                }
-            {
-                float g[2];
+            for (int i = 0; i < DK; i += 2) mx = max3(mx, fabsf(s[i]), fabsf(s[i + 1]));
+            pow2_scale(mx, g, ig);
 #pragma unroll
-                for (int i = 0; i < 2; ++i) pow2_scale(quad_max(ms[i]), g[i], ig[i]);
-#pragma unroll
-                for (int t = 0; t < DK / 8; ++t)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) s[t][i] *= g[i >> 1];
-            }
+            for (int i = 0; i < DK; ++i) s[i] *= g;
             for (int m = 0; m < chunks; ++m) {
-                wait(sm.loaded[m % 3], m / 3);
-                wait(sm.ready[m & 1], m >> 1);
-                chain_chunk<DK, DVT, F32>(sm, m, s, ig, wait, warp, lane);
-                warp_arrive(sm.kv_free[m % 3], lane);
-                if (lane == 0) ptx::mbar_arrive(&sm.tp_free[m & 1]);
+                const int b = m & 1, n = end - begin - m * C;
+                store_split<DK>(at + TM_SH, at + TM_SL, s);
+                ptx::tc_fence_before();
+                warp_arrive(sm.s_full, lane);
+
+                // R = beta V - beta e^G k.S, times rd
+                wait(sm.loaded[b], m >> 1);
+                const Factors& fac = *reinterpret_cast<const Factors*>(sm.work[b] + 2 * L::M + L::PARTS * 8192);
+                const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(sm.v[b]) + c;
+                float r[C];
+#pragma unroll
+                for (int i = 0; i < C; i += 4) {
+                    const float4 be = *reinterpret_cast<const float4*>(&fac.beta[i]);
+                    r[i] = be.x * (__bfloat162float(v[i * DV]) * rd);
+                    r[i + 1] = be.y * (__bfloat162float(v[(i + 1) * DV]) * rd);
+                    r[i + 2] = be.z * (__bfloat162float(v[(i + 2) * DV]) * rd);
+                    r[i + 3] = be.w * (__bfloat162float(v[(i + 3) * DV]) * rd);
+                }
+                if (n < C)  // the copies took the next sequence's rows along
+#pragma unroll
+                    for (int i = 0; i < C; ++i) r[i] = i < n ? r[i] : 0.f;
+                const float last = fac.last, x = fac.x;
+                if (m > 0) wait(sm.o_full, m - 1);  // R's place is free
+                wait(sm.ks_full, m);
+                ptx::tc_fence_after();
+                const float fr = ig * rd;
+                mx = 0.f;
+#pragma unroll
+                for (int q = 0; q < C; q += 32) {
+                    float d[32];
+                    ptx::tmem_ld32(at + TM_X + q, d);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        const float4 ek = *reinterpret_cast<const float4*>(&fac.ek[q + i]);
+                        r[q + i] = fmaf(-ek.x, d[i] * fr, r[q + i]);
+                        r[q + i + 1] = fmaf(-ek.y, d[i + 1] * fr, r[q + i + 1]);
+                        r[q + i + 2] = fmaf(-ek.z, d[i + 2] * fr, r[q + i + 2]);
+                        r[q + i + 3] = fmaf(-ek.w, d[i + 3] * fr, r[q + i + 3]);
+                        mx = max3(mx, max3(fabsf(r[q + i]), fabsf(r[q + i + 1]), fabsf(r[q + i + 2])), fabsf(r[q + i + 3]));
+                    }
+                }
+                // fp16 has room for a stale scale; a new one where the largest value has left [2^-6, 2^10)
+                if (__any_sync(0xffffffffu, mx != 0.f && !(mx >= 0x1p-6f && mx < 0x1p10f))) {
+                    float down, up;
+                    pow2_scale(mx * ru, down, up);
+                    const float f = down * ru;
+#pragma unroll
+                    for (int i = 0; i < C; ++i) r[i] *= f;
+                    rd = down;
+                    ru = up;
+                }
+                store_split<C>(at + TM_RH, at + TM_RL, r);
+                ptx::tc_fence_before();
+                warp_arrive(sm.r_full, lane);
+                sm.f1[b][c] = ig;
+                sm.f2[b][c] = ru * x;
+                warp_arrive(sm.f_full[b], lane);
+
+                // S = e^{G_C} S + M^T R
+#pragma unroll
+                for (int i = 0; i < DK; ++i) s[i] *= last;
+                const float fs = (ru * x) * g;
+                wait(sm.su_full, m);
+                ptx::tc_fence_after();
+                mx = 0.f;
+#pragma unroll
+                for (int q = 0; q < DK; q += 32) {
+                    float d[32];
+                    ptx::tmem_ld32(at + TM_X + q, d);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        s[q + i] = fmaf(fs, d[i], s[q + i]);
+                        s[q + i + 1] = fmaf(fs, d[i + 1], s[q + i + 1]);
+                        mx = max3(mx, fabsf(s[q + i]), fabsf(s[q + i + 1]));
+                    }
+                }
+                if (__any_sync(0xffffffffu, mx != 0.f && !(mx >= 0x1p-6f && mx < 0x1p10f))) {
+                    float down, up;
+                    pow2_scale(mx * ig, down, up);
+                    const float f = down * ig;
+#pragma unroll
+                    for (int i = 0; i < DK; ++i) s[i] *= f;
+                    g = down;
+                    ig = up;
+                }
+                warp_arrive(sm.freed[b], lane);
             }
 #pragma unroll
-            for (int t = 0; t < DK / 8; ++t)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    a.state[sbase + (size_t)(t * 8 + (lane & 3) * 2 + (i & 1)) * dv + (i >> 1) * 8] = s[t][i] * ig[i >> 1];
+            for (int i = 0; i < DK; ++i) state[(size_t)i * DV] = s[i] * ig;
         }
-    } else if (warp < PREP_WARP) {
-        set_regs<false, 88>();
+    } else if (warp < 8) {
+        set_regs<false, 64>();
         if (warp == 4) {
-            const int hk = h / (a.Hv / a.Hk);
-            const uint64_t policy = ptx::policy_evict_normal();  // other heads and columns read the same rows
-            for (int m = 0; m <= chunks; ++m) {
-                if (m > 0) {
-                    // the raw products of chunk m - 1
-                    const int s = (m - 1) % 3, b = (m - 1) & 1;
-                    wait(sm.loaded[s], (m - 1) / 3);
-                    if (m >= 3) wait(sm.prod_free[b], (m - 3) >> 1);
-                    ptx::tc_fence_after();
-                    if (lane == 0) {
-                        const uint32_t kq = ptx::smem_u32(sm.kq[s]);
-#pragma unroll 1
-                        for (int kt = 0; kt < DK / 16; ++kt) {
-                            const uint64_t d = ptx::desc_sw128(kq + (kt >> 2) * 16384 + (kt & 3) * 32);
-                            ptx::mma_f16_ss(tmem + TM_PROD + b * 128, d, d, ptx::idesc_bf16(128, 128), kt > 0);
-                        }
-                        ptx::mma_commit(&sm.prod_full[b]);
-                    }
-                    __syncwarp();
+            const uint64_t policy = ptx::policy_evict_first();
+            const long long slot0 = begin / C + seq;
+            for (int m = 0; m < chunks; ++m) {
+                const int b = m & 1;
+                if (m >= 2) wait(sm.freed[b], (m - 2) >> 1);
+                if (lane == 0) {
+                    uint64_t* bar = &sm.loaded[b];
+                    ptx::mbar_arrive_expect_tx(bar, L::KQ + L::V + C * DV * 2);
+                    ptx::bulk_g2s(sm.kq[b], ws.kq + ((slot0 + m) * a.Hk + h / (a.Hv / a.Hk)) * L::KQ, L::KQ, bar);
+                    ptx::tma_load_2d(sm.v[b], &vmap, h * DV, begin + m * C, bar, policy);
+                    ptx::bulk_g2s_stream(sm.work[b], ws.v + ((slot0 + m) * a.Hv + h) * L::V, L::V, bar, policy);
                 }
-                if (m < chunks) {
-                    const int s = m % 3, r0 = begin + m * C;
-                    if (m >= 3) wait(sm.kv_free[s], m / 3 - 1);
-                    if (lane == 0) {
-                        ptx::mbar_arrive_expect_tx(&sm.loaded[s], sizeof(sm.kq[0]) + sizeof(sm.v[0]));
-#pragma unroll 1
-                        for (int i = 0; i < S::HALVES; ++i) {
-                            ptx::tma_load_2d(sm.kq[s] + i * 16384, &maps.k, hk * DK + i * 64, r0, &sm.loaded[s], policy);
-                            ptx::tma_load_2d(sm.kq[s] + i * 16384 + 8192, &maps.q, hk * DK + i * 64, r0, &sm.loaded[s],
-                                             policy);
-                        }
-                        ptx::tma_load_2d(sm.v[s], &maps.v, h * dv + col0, r0, &sm.loaded[s], policy);
-                    }
-                    __syncwarp();
-                }
+                __syncwarp();
             }
         } else if (warp == 5) {
-            for (int m = 0; m < chunks; ++m) issue_outputs<DK, DVT, F32>(sm, m, wait, tmem, lane);
-        } else {
-            const long long row_stride = (long long)a.Hv * dv;
-            const size_t osize = F32 ? 4 : 2;
-            unsigned char* out = static_cast<unsigned char*>(a.out) + ((size_t)begin * row_stride + (size_t)h * dv + col0) * osize;
+            // the products, all from one thread: each commit covers what came before it
             for (int m = 0; m < chunks; ++m) {
-                output_rows<DVT, F32>(sm, m, out + (size_t)m * C * row_stride * osize, row_stride,
-                                      min(C, end - begin - m * C), wait, tmem, warp - 6, lane);
-                warp_arrive(sm.kv_free[m % 3], lane);
-                if (lane == 0) ptx::mbar_arrive(&sm.tp_free[m & 1]);
+                const int b = m & 1;
+                wait(sm.loaded[b], m >> 1);
+                wait(sm.s_full, m);
+                ptx::tc_fence_after();
+                const uint64_t k = ptx::desc_sw128(ptx::smem_u32(sm.kq[b])), q = k + (8192 >> 4);
+                const uint64_t mh = ptx::desc_sw128(ptx::smem_u32(sm.work[b])), ml = mh + (L::M >> 4), pt = ml + (L::M >> 4);
+                constexpr uint32_t id = ptx::idesc_f16(128, C), idm = ptx::idesc_f16(128, DK);
+                auto kq_step = [](int kt) { return (uint64_t)((kt >> 2) * (16384 >> 4) + (kt & 3) * 2); };
+                if (lane == 0) {
+#pragma unroll
+                    for (int kt = 0; kt < DK / 16; ++kt)
+                        ptx::mma_bf16_ts(tmem + TM_X, tmem + TM_SH + kt * 8, k + kq_step(kt), id, kt > 0);
+#pragma unroll
+                    for (int kt = 0; kt < DK / 16; ++kt)
+                        ptx::mma_bf16_ts(tmem + TM_X, tmem + TM_SL + kt * 8, k + kq_step(kt), id, 1);
+                    ptx::mma_commit(&sm.ks_full);
+                }
+                __syncwarp();
+                if (m > 0) wait(sm.o_free, m - 1);
+                ptx::tc_fence_after();
+                if (lane == 0) {
+#pragma unroll 1
+                    for (int kt = 0; kt < DK / 16; ++kt)
+                        ptx::mma_bf16_ts(tmem + TM_QS, tmem + TM_SH + kt * 8, q + kq_step(kt), id, kt > 0);
+                    if (F32)
+#pragma unroll 1
+                        for (int kt = 0; kt < DK / 16; ++kt)
+                            ptx::mma_bf16_ts(tmem + TM_QS, tmem + TM_SL + kt * 8, q + kq_step(kt), id, 1);
+                }
+                __syncwarp();
+                wait(sm.r_full, m);
+                ptx::tc_fence_after();
+                if (lane == 0) {
+#pragma unroll
+                    for (int kt = 0; kt < 4; ++kt)
+                        ptx::mma_bf16_ts(tmem + TM_X, tmem + TM_RH + kt * 8, mh + kt * 2, idm, kt > 0);
+#pragma unroll
+                    for (int kt = 0; kt < 4; ++kt)
+                        ptx::mma_bf16_ts(tmem + TM_X, tmem + TM_RL + kt * 8, mh + kt * 2, idm, 1);
+#pragma unroll
+                    for (int kt = 0; kt < 4; ++kt)
+                        ptx::mma_bf16_ts(tmem + TM_X, tmem + TM_RH + kt * 8, ml + kt * 2, idm, 1);
+                    ptx::mma_commit(&sm.su_full);
+#pragma unroll 1
+                    for (int kt = 0; kt < 4; ++kt)
+                        ptx::mma_bf16_ts(tmem + TM_PR, tmem + TM_RH + kt * 8, pt + kt * 2, id, kt > 0);
+                    if (F32)
+#pragma unroll 1
+                        for (int kt = 0; kt < 4; ++kt) {
+                            ptx::mma_bf16_ts(tmem + TM_PR, tmem + TM_RL + kt * 8, pt + kt * 2, id, 1);
+                            ptx::mma_bf16_ts(tmem + TM_PR, tmem + TM_RH + kt * 8, pt + (8192 >> 4) + kt * 2, id, 1);
+                        }
+                    ptx::mma_commit(&sm.o_full);
+                }
+                __syncwarp();
             }
         }
     } else {
-        set_regs<false, 96>();
-        const int w = warp - PREP_WARP;
-        const __nv_bfloat16* ga = static_cast<const __nv_bfloat16*>(a.a) + h;
-        const __nv_bfloat16* be = static_cast<const __nv_bfloat16*>(a.b) + h;
-        const float ea = expf(a.A_log[h]) * 1.44269504088896341f, dt = a.dt_bias[h];
-        __nv_bfloat16 graw[2], braw[2];  // the next chunk's gates of two rows, as loaded (warp 4)
-        auto gates = [&](int r0) {
+        set_regs<false, 104>();
+        if (warp - 8 < NW) {
+            // column c of the outputs: o_r = e1 q'.S + e2 (P T R)_r
+            const int w = warp - 8, c = w * 32 + lane;
+            const uint32_t at = tmem + ((uint32_t)(w * 32) << 16);
+            const size_t row_stride = (size_t)a.Hv * DV;
+            for (int m = 0; m < chunks; ++m) {
+                const int b = m & 1, n = min(C, end - begin - m * C);
+                wait(sm.loaded[b], m >> 1);
+                wait(sm.f_full[b], m >> 1);
+                const float f1 = sm.f1[b][c], f2 = sm.f2[b][c];
+                const Factors& fac = *reinterpret_cast<const Factors*>(sm.work[b] + 2 * L::M + L::PARTS * 8192);
+                const size_t o0 = ((size_t)begin + (size_t)m * C) * row_stride + (size_t)h * DV;
+                wait(sm.o_full, m);
+                ptx::tc_fence_after();
+#pragma unroll 1
+                for (int i0 = 0; i0 < C; i0 += 16) {
+                    float x[16], y[16];
+                    ptx::tmem_ld16(at + TM_QS + i0, x);
+                    ptx::tmem_ld16(at + TM_PR + i0, y);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int r = r0 + 2 * lane + i;
-                if (w == 4 && r < end) {
-                    graw[i] = ga[(size_t)r * a.Hv];
-                    braw[i] = be[(size_t)r * a.Hv];
-                } else graw[i] = braw[i] = __float2bfloat16(0.f);
-            }
-        };
-        gates(begin);
-        for (int m = 0; m < chunks; ++m) {
-            const int r0 = begin + m * C, n = min(C, end - r0);
-            float2 g = make_float2(0.f, 0.f), bt = g;
-            if (w == 4) {
-                if (2 * lane < n) {
-                    g.x = gdn_log_alpha(ea, __bfloat162float(graw[0]), dt);
-                    bt.x = sigmoidf_(__bfloat162float(braw[0]));
+                    for (int i = 0; i < 16; i += 4) {
+                        const float4 e1 = *reinterpret_cast<const float4*>(&fac.e1[i0 + i]);
+                        const float4 e2 = *reinterpret_cast<const float4*>(&fac.e2[i0 + i]);
+                        x[i] = fmaf(e1.x, f1 * x[i], e2.x * (f2 * y[i]));
+                        x[i + 1] = fmaf(e1.y, f1 * x[i + 1], e2.y * (f2 * y[i + 1]));
+                        x[i + 2] = fmaf(e1.z, f1 * x[i + 2], e2.z * (f2 * y[i + 2]));
+                        x[i + 3] = fmaf(e1.w, f1 * x[i + 3], e2.w * (f2 * y[i + 3]));
+                    }
+                    if constexpr (F32) {
+                        float* p = static_cast<float*>(a.out) + o0 + c + i0 * row_stride;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (i0 + i < n) p[i * row_stride] = x[i];
+                    } else {
+                        // neighbouring lanes trade a value: even ones write two columns of row i, odd ones of row i + 1
+                        __nv_bfloat16* p = static_cast<__nv_bfloat16*>(a.out) + o0 + (c & ~1) + (i0 + (c & 1)) * row_stride;
+#pragma unroll
+                        for (int i = 0; i < 16; i += 2) {
+                            const float y1 = __shfl_xor_sync(0xffffffffu, (c & 1) ? x[i] : x[i + 1], 1);
+                            const __nv_bfloat162 o = (c & 1) ? __floats2bfloat162_rn(y1, x[i + 1]) : __floats2bfloat162_rn(x[i], y1);
+                            if (i0 + i + (c & 1) < n) *reinterpret_cast<__nv_bfloat162*>(p + i * row_stride) = o;
+                        }
+                    }
+                    __syncwarp();
                 }
-                if (2 * lane + 1 < n) {
-                    g.y = gdn_log_alpha(ea, __bfloat162float(graw[1]), dt);
-                    bt.y = sigmoidf_(__bfloat162float(braw[1]));
-                }
-                gates(r0 + C);
+                ptx::tc_fence_before();
+                warp_arrive(sm.o_free, lane);
+                warp_arrive(sm.freed[b], lane);
             }
-            prep_chunk<DK, DVT, F32>(sm, m, a, n, g, bt, wait, tmem, w, lane);
         }
     }
     if (wait.dead) flag_status(a.dev_status, KDA_DEV_TIMEOUT);
@@ -992,8 +986,10 @@ __global__ void __launch_bounds__(THREADS, 1) gdn_chunk_kernel(const GdnArgs a, 
     }
 }
 
-// [T][width] bf16 rows with a row stride; boxes of 64 rows.
-bool encode_rows(CUtensorMap* m, const void* base, long long width, long long stride, int T, int box)
+// ------------------------------------------------------------ launch
+
+// [T][width] bf16 rows with a row stride; boxes of 64 rows and `box` values.
+bool encode_rows(CUtensorMap* m, const void* base, long long width, long long stride, int T, int box, bool swizzle)
 {
     PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
     if (!enc) return false;
@@ -1002,54 +998,76 @@ bool encode_rows(CUtensorMap* m, const void* base, long long width, long long st
     const cuuint32_t boxes[2] = {(cuuint32_t)box, C};
     const cuuint32_t estr[2] = {1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, boxes, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, box == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int DK, int NW, bool F32> cudaError_t launch(const GdnArgs& a, int dv, cudaStream_t st)
+template <int DK, int DV, bool F32>
+cudaError_t launch_chain(const GdnArgs& a, const CUtensorMap& vmap, const Work& ws, cudaStream_t st)
 {
-    using S = Smem<DK, NW * 16, F32>;
-    // operand tiles on the swizzle's 1024-byte period, vectors on 16 bytes, barriers on 8
-    static_assert(offsetof(S, v) % 1024 == 0 && offsetof(S, tp) % 1024 == 0 && offsetof(S, st) % 1024 == 0 &&
-                  offsetof(S, ut) % 1024 == 0, "tiles");
-    static_assert(offsetof(S, x) % 16 == 0 && offsetof(S, f1) % 16 == 0 && offsetof(S, f2) % 16 == 0 &&
-                  offsetof(S, gh) % 16 == 0 && offsetof(S, gl) % 16 == 0 && offsetof(S, colk) % 16 == 0 &&
-                  offsetof(S, down) % 16 == 0 && offsetof(S, loaded) % 8 == 0, "vectors");
-    constexpr int smem = sizeof(Smem<DK, NW * 16, F32>);
+    using S = ChainSmem<DK, DV, F32>;
+    constexpr int smem = sizeof(S);
+    // operand tiles on the swizzle's 1024-byte period, barriers on 8
+    static_assert(offsetof(S, work) % 1024 == 0 && offsetof(S, v) % 128 == 0 && offsetof(S, loaded) % 8 == 0, "alignment");
     static_assert(smem <= 227 * 1024, "shared memory");
     static PerDeviceOnce once;
     cudaError_t e = once.run([](int) {
-        return cudaFuncSetAttribute(gdn_chunk_kernel<DK, NW, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        return cudaFuncSetAttribute(gdn_chain_kernel<DK, DV, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     });
     if (e != cudaSuccess) return e;
-    RowMaps maps;
-    if (!encode_rows(&maps.q, a.q, (long long)a.Hk * DK, a.qs, a.T, 64) ||
-        !encode_rows(&maps.k, a.k, (long long)a.Hk * DK, a.ks, a.T, 64) ||
-        !encode_rows(&maps.v, a.v, (long long)a.Hv * dv, a.vs, a.T, NW * 16))
-        return cudaErrorInvalidValue;
-    gdn_chunk_kernel<DK, NW, F32><<<a.N * a.Hv * (dv / (NW * 16)), THREADS, smem, st>>>(a, maps, dv);
+    gdn_chain_kernel<DK, DV, F32><<<a.N * a.Hv, CHAIN_THREADS, smem, st>>>(a, vmap, ws);
     return cudaGetLastError();
 }
 
-template <int DK> cudaError_t launch_dk(const GdnArgs& a, int dv, bool bf16, cudaStream_t st)
+template <int DK, bool F32> cudaError_t launch(const GdnArgs& a, int dv, cudaStream_t st)
 {
-    // Two chain warps a CTA where four would leave SMs without one, and where
-    // the fp32 outputs' low parts take the shared memory of the other two.
-    if (dv == 32 || (long long)a.N * a.Hv * (dv / 64) * 2 <= sm_count())
-        return bf16 ? launch<DK, 2, false>(a, dv, st) : launch<DK, 2, true>(a, dv, st);
-    if (bf16) return launch<DK, 4, false>(a, dv, st);
-    return launch<DK, DK == 128 ? 2 : 4, true>(a, dv, st);
+    using S = PrepSmem<DK, F32>;
+    using L = Slot<DK, F32>;
+    constexpr int smem = sizeof(S);
+    static_assert(offsetof(S, t_hi) % 128 == 0 && offsetof(S, fac) % 16 == 0 && offsetof(S, m) % 16 == 0 &&
+                  offsetof(S, xd) % 16 == 0 && offsetof(S, gh) % 16 == 0 &&
+                  offsetof(S, gl) % 16 == 0 && offsetof(S, colk) % 16 == 0 && offsetof(S, down) % 16 == 0 &&
+                  offsetof(S, loaded) % 8 == 0, "alignment");
+    static PerDeviceOnce once;
+    cudaError_t e = once.run([](int) {
+        return cudaFuncSetAttribute(gdn_prep_kernel<DK, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    });
+    if (e != cudaSuccess) return e;
+    RowMaps maps;
+    if (!encode_rows(&maps.q, a.q, (long long)a.Hk * DK, a.qs, a.T, 64, true) ||
+        !encode_rows(&maps.k, a.k, (long long)a.Hk * DK, a.ks, a.T, 64, true) ||
+        !encode_rows(&maps.v, a.v, (long long)a.Hv * dv, a.vs, a.T, dv, false))
+        return cudaErrorInvalidValue;
+    const long long slots = slot_count(a.N, a.T);
+    Work ws;
+    ws.kq = static_cast<unsigned char*>(a.workspace);
+    ws.v = ws.kq + slots * a.Hk * L::KQ;
+    gdn_prep_kernel<DK, F32><<<(unsigned)(slots * a.Hv), PREP, smem, st>>>(a, maps, ws);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (dv == 128) return launch_chain<DK, 128, F32>(a, maps.v, ws, st);
+    if (dv == 64) return launch_chain<DK, 64, F32>(a, maps.v, ws, st);
+    return launch_chain<DK, 32, F32>(a, maps.v, ws, st);
+}
+
+template <int DK> size_t slot_bytes(int Hk, int Hv, bool bf16)
+{
+    return (size_t)Hk * Slot<DK, false>::KQ + (size_t)Hv * (bf16 ? Slot<DK, false>::V : Slot<DK, true>::V);
 }
 
 }  // namespace
 
-size_t gdn_chunk_workspace_bytes(int, int, int, int, bool, int, int) { return 0; }
+size_t gdn_chunk_workspace_bytes(int Hk, int Hv, int dk, bool out_bf16, int N, int T)
+{
+    const size_t b = dk == 128 ? slot_bytes<128>(Hk, Hv, out_bf16) : dk == 64 ? slot_bytes<64>(Hk, Hv, out_bf16)
+                                                                             : slot_bytes<32>(Hk, Hv, out_bf16);
+    return (size_t)slot_count(N, T) * b;
+}
 
 cudaError_t launch_gdn_chunk(const GdnArgs& a, int dk, int dv, bool out_bf16, cudaStream_t st)
 {
-    if (dk == 128) return launch_dk<128>(a, dv, out_bf16, st);
-    if (dk == 64) return launch_dk<64>(a, dv, out_bf16, st);
-    return launch_dk<32>(a, dv, out_bf16, st);
+    if (dk == 128) return out_bf16 ? launch<128, false>(a, dv, st) : launch<128, true>(a, dv, st);
+    if (dk == 64) return out_bf16 ? launch<64, false>(a, dv, st) : launch<64, true>(a, dv, st);
+    return out_bf16 ? launch<32, false>(a, dv, st) : launch<32, true>(a, dv, st);
 }
 
 }  // namespace kda
