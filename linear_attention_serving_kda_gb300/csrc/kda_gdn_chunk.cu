@@ -162,21 +162,21 @@ struct RowMaps {
 };
 
 constexpr int PREP = 256;
+template <bool F32> constexpr int prep_ctas() { return F32 ? 2 : 3; }  // of an SM, by their shared memory
 
 template <int DK, bool F32> struct PrepSmem {
     using L = Slot<DK, F32>;
     static constexpr int PARTS = L::PARTS;
-    unsigned char kq[L::KQ];  // bf16 rows of k, then q; fp16 later
+    unsigned char kq[L::KQ];  // bf16 rows of k, then q; fp16 later; P T over q's
     union {
         struct {  // 64 x 64 fp16 tiles
-            unsigned char t_hi[8192], t_lo[8192], p_hi[8192], p_lo[F32 ? 8192 : 128];
-            unsigned char ts[PARTS][8192];  // diag(k's row factors / x) T
-            unsigned char tw[2][8192];      // diag(e^{G_C - G}) Ts
+            unsigned char t_hi[8192], t_lo[8192];  // T; then diag(e^{G_C - G}) Ts
+            unsigned char ts[PARTS][8192];         // Ts = diag(k's row factors / x) T
+            unsigned char p_hi[8192], p_lo[F32 ? 8192 : 128];
         };
-        struct {  // then what they give, as the slot holds it
-            unsigned char m[2][L::M], pt[PARTS][8192];
-        };
+        unsigned char m[2][L::M];  // then M^T
     };
+    unsigned char pt_lo[F32 ? 8192 : 128];
     Factors fac;
     alignas(16) float xd[C * XS];  // A's diagonal blocks, 16 x 16 each
     alignas(16) float eg[C], gh[C], gl[C], w[C];  // e^G, G / ln 2 in two words, e^{G_C - G}
@@ -184,7 +184,7 @@ template <int DK, bool F32> struct PrepSmem {
     alignas(16) float row[2 * C], colk[C], down[2 * C], sk[C];  // factors of A's and P's rows, of A's columns; of the stored rows
     uint64_t loaded, prod;
     uint32_t tmem;
-    int seq;
+    int begin, rows;
 };
 
 __device__ __forceinline__ void prep_sync() { __syncthreads(); }
@@ -327,9 +327,9 @@ template <int SIZE> struct Merge {
 };
 
 // One chunk's share of one value head.  Bound: latency (a dozen dependent
-// phases of a few hundred instructions each); two CTAs an SM fill each other's gaps.
+// phases of a few hundred instructions each); several CTAs an SM fill each other's gaps.
 template <int DK, bool F32>
-__global__ void __launch_bounds__(PREP, 2) gdn_prep_kernel(const GdnArgs a, const __grid_constant__ RowMaps maps, const Work ws)
+__global__ void __launch_bounds__(PREP, prep_ctas<F32>()) gdn_prep_kernel(const GdnArgs a, const __grid_constant__ RowMaps maps, const Work ws)
 {
     extern __shared__ __align__(1024) unsigned char dyn[];
     using S = PrepSmem<DK, F32>;
@@ -338,19 +338,20 @@ __global__ void __launch_bounds__(PREP, 2) gdn_prep_kernel(const GdnArgs a, cons
     const int t = threadIdx.x, w = t >> 5, lane = t & 31;
     const int h = blockIdx.x % a.Hv, rep = a.Hv / a.Hk, hk = h / rep;
     const int slot = blockIdx.x / a.Hv;
-    if (t == 0) sm.seq = -1;
+    if (t == 0) sm.begin = -1;
     __syncthreads();
-    // the last sequence whose slots start at or before this one
+    // the sequence that has this slot
     for (int s = t; s < a.N; s += PREP) {
         const int b = a.cu_seqlens[s], e = a.cu_seqlens[s + 1];
-        const int base = b / C + s;
-        if (b >= 0 && e > b && e <= a.T && slot >= base && slot < base + (e - b + C - 1) / C) atomicMax(&sm.seq, s);
+        const int c = slot - b / C - s;
+        if (b >= 0 && e > b && e <= a.T && c >= 0 && c < (e - b + C - 1) / C) {
+            sm.begin = b + c * C;
+            sm.rows = min(C, e - b - c * C);
+        }
     }
     __syncthreads();
-    const int seq = sm.seq;
-    if (seq < 0 || (a.slots && (a.slots[seq] < 0 || a.slots[seq] >= a.num_slots))) return;
-    const int begin = a.cu_seqlens[seq], end = a.cu_seqlens[seq + 1];
-    const int r0 = begin + (slot - begin / C - seq) * C, n = min(C, end - r0);
+    const int r0 = sm.begin, n = sm.rows;
+    if (r0 < 0) return;
 
     if (t == 0) {
         ptx::mbar_init(&sm.loaded, 1);
@@ -365,6 +366,29 @@ __global__ void __launch_bounds__(PREP, 2) gdn_prep_kernel(const GdnArgs a, cons
         }
     }
     if (w == 1) ptx::tmem_alloc(&sm.tmem, 128);
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = sm.tmem;
+    Waiter wait{false};
+    if (w == 0) {
+        wait(sm.loaded, 0);
+        if (lane == 0) {
+            // [K; Q] [K; Q]^T: k.k, q.k and, on the diagonal, both squared norms
+            const uint32_t kq = ptx::smem_u32(sm.kq);
+#pragma unroll
+            for (int kt = 0; kt < DK / 16; ++kt) {
+                const uint64_t d = ptx::desc_sw128(kq + (kt >> 2) * 16384 + (kt & 3) * 32);
+                ptx::mma_f16_ss(tmem, d, d, ptx::idesc_bf16(128, 128), kt > 0);
+            }
+            ptx::mma_commit(&sm.prod);
+        }
+        __syncwarp();
+    }
+    // a row of [K; Q] a lane (w & 3), against half of k's rows (w >> 2); the
+    // halves above the diagonal (w = 4 and 6) are left out
+    const int lr = (w & 3) * 32 + lane, r = lr & (C - 1), type = lr >> 6, s0 = (w >> 2) * 32;  // type 0: k, 1: q
+    const uint32_t at = tmem + ((uint32_t)((w & 3) * 32) << 16);
     if (w == 4) {
         // two rows a lane: gates and running sums
         const float ea = expf(a.A_log[h]) * 1.44269504088896341f, dt = a.dt_bias[h];
@@ -380,29 +404,6 @@ __global__ void __launch_bounds__(PREP, 2) gdn_prep_kernel(const GdnArgs a, cons
         sm.fac.beta[2 * lane + 1] = bt[1];
         scan_rows(sm, make_float2(g[0], g[1]), lane);
     }
-    ptx::tc_fence_before();
-    __syncthreads();
-    ptx::tc_fence_after();
-    const uint32_t tmem = sm.tmem;
-    Waiter wait{false};
-    wait(sm.loaded, 0);
-    if (w == 0) {
-        if (lane == 0) {
-            // [K; Q] [K; Q]^T: k.k, q.k and, on the diagonal, both squared norms
-            const uint32_t kq = ptx::smem_u32(sm.kq);
-#pragma unroll 1
-            for (int kt = 0; kt < DK / 16; ++kt) {
-                const uint64_t d = ptx::desc_sw128(kq + (kt >> 2) * 16384 + (kt & 3) * 32);
-                ptx::mma_f16_ss(tmem, d, d, ptx::idesc_bf16(128, 128), kt > 0);
-            }
-            ptx::mma_commit(&sm.prod);
-        }
-        __syncwarp();
-    }
-    // a row of [K; Q] a lane (w & 3), against half of k's rows (w >> 2); the
-    // halves above the diagonal (w = 4 and 6) are left out
-    const int lr = (w & 3) * 32 + lane, r = lr & (C - 1), type = lr >> 6, s0 = (w >> 2) * 32;  // type 0: k, 1: q
-    const uint32_t at = tmem + ((uint32_t)((w & 3) * 32) << 16);
     wait(sm.prod, 0);
     ptx::tc_fence_after();
     if (w == 0 || w >= 5) {
@@ -481,6 +482,7 @@ __global__ void __launch_bounds__(PREP, 2) gdn_prep_kernel(const GdnArgs a, cons
     if (w >= 4) {
         // meanwhile the rows themselves, and the largest of k's factors
         const int row = (w - 4) * 32 + lane;
+        wait(sm.loaded, 0);
         convert_row<DK>(sm.kq, row, sm.down[row], (row & (C - 1)) < n);
         if (w == 7) {
             float mx = fmaxf(sm.sk[lane], sm.sk[lane + 32]);
@@ -535,9 +537,14 @@ __global__ void __launch_bounds__(PREP, 2) gdn_prep_kernel(const GdnArgs a, cons
         invert_sync();  // every warp has read A21
         mg.store(sm, 32, 0, n0, mt, o, lane);
     }
+    ptx::fence_proxy_async_smem();
     prep_sync();
+    if (t == 0 && h % rep == 0) {
+        ptx::bulk_s2g(ws.kq + ((long long)slot * a.Hk + hk) * L::KQ, sm.kq, L::KQ);
+        ptx::bulk_commit();
+    }
     {
-        // Ts and Tw, sixteen values of a row a thread; zero above the diagonal
+        // Ts, and T times the decays to the chunk's end, sixteen values of a row a thread; zero above the diagonal
         const int rr = t >> 2, c0 = (t & 3) * 2;
         const float f = sm.sk[rr] / sm.fac.x, fw = f * sm.w[rr];
 #pragma unroll
@@ -556,8 +563,8 @@ __global__ void __launch_bounds__(PREP, 2) gdn_prep_kernel(const GdnArgs a, cons
             }
             *reinterpret_cast<uint4*>(sm.ts[0] + tile_at(rr, c)) = make_uint4(sh[0], sh[1], sh[2], sh[3]);
             if (F32) *reinterpret_cast<uint4*>(sm.ts[F32 ? 1 : 0] + tile_at(rr, c)) = make_uint4(sl[0], sl[1], sl[2], sl[3]);
-            *reinterpret_cast<uint4*>(sm.tw[0] + tile_at(rr, c)) = make_uint4(wh[0], wh[1], wh[2], wh[3]);
-            *reinterpret_cast<uint4*>(sm.tw[1] + tile_at(rr, c)) = make_uint4(wl[0], wl[1], wl[2], wl[3]);
+            *reinterpret_cast<uint4*>(sm.t_hi + tile_at(rr, c)) = make_uint4(wh[0], wh[1], wh[2], wh[3]);
+            *reinterpret_cast<uint4*>(sm.t_lo + tile_at(rr, c)) = make_uint4(wl[0], wl[1], wl[2], wl[3]);
         }
     }
     prep_sync();
@@ -573,30 +580,12 @@ __global__ void __launch_bounds__(PREP, 2) gdn_prep_kernel(const GdnArgs a, cons
             if (lo_tile) stsm(ptx::smem_u32(lo_tile) + o, lo);
         }
     };
-    float cm[8][4], cp[8][4];
+    float c[8][4];
+    auto clear = [&] {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) cm[i][j] = cp[i][j] = 0.f;
-    if (w * 16 < DK) {
-        // M^T: sixteen of dk's rows a warp, K'^T (exact) times Tw, high and low; row r of Tw meets columns s <= r
-        const uint32_t kb = ptx::smem_u32(sm.kq), th = ptx::smem_u32(sm.tw[0]), tl = ptx::smem_u32(sm.tw[1]);
-#pragma unroll
-        for (int kt = 0; kt < 4; ++kt) {
-            uint32_t x[4], f[4], e[4];
-            // left operand (dk, r) from rows r of k: transposed
-            ldsm_t(x, kb + kq_at(kt * 16 + brow, w * 2 + bcol));
-#pragma unroll
-            for (int q = 0; q <= kt; ++q) {
-                ldsm_t(f, th + tile_at(kt * 16 + arow, q * 2 + acol));
-                ldsm_t(e, tl + tile_at(kt * 16 + arow, q * 2 + acol));
-                mma(cm[2 * q], x, f[0], f[1]);
-                mma(cm[2 * q + 1], x, f[2], f[3]);
-                mma(cm[2 * q], x, e[0], e[1]);
-                mma(cm[2 * q + 1], x, e[2], e[3]);
-            }
-        }
-    }
+        for (int i = 0; i < 8; ++i) c[i][0] = c[i][1] = c[i][2] = c[i][3] = 0.f;
+    };
+    clear();
     if (w >= 4) {
         // P T: sixteen rows a warp
         const int mt = w - 4;
@@ -611,31 +600,53 @@ __global__ void __launch_bounds__(PREP, 2) gdn_prep_kernel(const GdnArgs a, cons
 #pragma unroll
             for (int q = 0; q <= kt; ++q) {
                 ldsm_t(f, tb[0] + tile_at(kt * 16 + arow, q * 2 + acol));
-                mma(cp[2 * q], x, f[0], f[1]);
-                mma(cp[2 * q + 1], x, f[2], f[3]);
+                mma(c[2 * q], x, f[0], f[1]);
+                mma(c[2 * q + 1], x, f[2], f[3]);
                 if (F32) {
                     ldsm_t(e, tb[1] + tile_at(kt * 16 + arow, q * 2 + acol));
-                    mma(cp[2 * q], y, f[0], f[1]);
-                    mma(cp[2 * q + 1], y, f[2], f[3]);
-                    mma(cp[2 * q], x, e[0], e[1]);
-                    mma(cp[2 * q + 1], x, e[2], e[3]);
+                    mma(c[2 * q], y, f[0], f[1]);
+                    mma(c[2 * q + 1], y, f[2], f[3]);
+                    mma(c[2 * q], x, e[0], e[1]);
+                    mma(c[2 * q + 1], x, e[2], e[3]);
                 }
+            }
+        }
+    } else if (t == 0) ptx::bulk_wait_read_all();  // [K; Q] is on its way: room for P T over q's rows
+    prep_sync();
+    if (w >= 4) store_tile(sm.kq + 8192, F32 ? sm.pt_lo : nullptr, (w - 4) * 16, c);
+    clear();
+    if (w * 16 < DK) {
+        // M^T: sixteen of dk's rows a warp, K'^T (exact) times T's high and low; row r of T meets columns s <= r
+        const uint32_t kb = ptx::smem_u32(sm.kq), th = ptx::smem_u32(sm.t_hi), tl = ptx::smem_u32(sm.t_lo);
+#pragma unroll
+        for (int kt = 0; kt < 4; ++kt) {
+            uint32_t x[4], f[4], e[4];
+            // left operand (dk, r) from rows r of k: transposed
+            ldsm_t(x, kb + kq_at(kt * 16 + brow, w * 2 + bcol));
+#pragma unroll
+            for (int q = 0; q <= kt; ++q) {
+                ldsm_t(f, th + tile_at(kt * 16 + arow, q * 2 + acol));
+                ldsm_t(e, tl + tile_at(kt * 16 + arow, q * 2 + acol));
+                mma(c[2 * q], x, f[0], f[1]);
+                mma(c[2 * q + 1], x, f[2], f[3]);
+                mma(c[2 * q], x, e[0], e[1]);
+                mma(c[2 * q + 1], x, e[2], e[3]);
             }
         }
     }
     prep_sync();  // the tiles read above make room
-    if (w * 16 < DK) store_tile(sm.m[0], sm.m[1], w * 16, cm);
-    if (w >= 4) store_tile(sm.pt[0], F32 ? sm.pt[F32 ? 1 : 0] : nullptr, (w - 4) * 16, cp);
+    if (w * 16 < DK) store_tile(sm.m[0], sm.m[1], w * 16, c);
     ptx::fence_proxy_async_smem();
     if (wait.dead) flag_status(a.dev_status, KDA_DEV_TIMEOUT);
     prep_sync();
     if (t == 0) {
         unsigned char* d = ws.v + ((long long)slot * a.Hv + h) * L::V;
-        ptx::bulk_s2g(d, sm.m, 2 * L::M + L::PARTS * 8192);
+        ptx::bulk_s2g(d, sm.m, 2 * L::M);
+        ptx::bulk_s2g(d + 2 * L::M, sm.kq + 8192, 8192);
+        if (F32) ptx::bulk_s2g(d + 2 * L::M + 8192, sm.pt_lo, 8192);
         ptx::bulk_s2g(d + 2 * L::M + L::PARTS * 8192, &sm.fac, sizeof(Factors));
-        if (h % rep == 0) ptx::bulk_s2g(ws.kq + ((long long)slot * a.Hk + hk) * L::KQ, sm.kq, L::KQ);
         ptx::bulk_commit();
-        ptx::bulk_wait_all();
+        ptx::bulk_wait_read_all();
     }
     if (w == 1) ptx::tmem_dealloc(tmem, 128);
 }
@@ -644,35 +655,59 @@ __global__ void __launch_bounds__(PREP, 2) gdn_prep_kernel(const GdnArgs a, cons
 
 // TMEM columns: the critical products (K S; then M^T R), S high and low, R high
 // and low as left operands (two fp16 a column), Q S, (P T) R
+// (the first of them as two halves, K S high and K S low)
 constexpr int TM_X = 0, TM_SH = 128, TM_SL = 192, TM_RH = 256, TM_RL = 288, TM_QS = 320, TM_PR = 384, TM_COLS = 512;
-constexpr int CHAIN_THREADS = 384;
+constexpr int CHAIN_THREADS = 640;
 
 template <int DK, int DV, bool F32> struct ChainSmem {
     using L = Slot<DK, F32>;
     unsigned char kq[2][L::KQ];
-    unsigned char work[2][(L::V + 1023) / 1024 * 1024];  // M^T, P T, factors
-    unsigned char v[2][C * DV * 2];                      // dense rows
+    unsigned char work[2][2 * L::M + L::PARTS * 8192];  // M^T, P T
+    unsigned char v[2][C * DV * 2];                     // dense rows
+    Factors fac[4];
     float f1[2][DV], f2[2][DV];  // the scales of S's and R's columns
+    float top[2][2][DV];         // the largest values of R's and S's halves of a column
     uint64_t loaded[2], freed[2];
-    uint64_t s_full, ks_full, r_full, su_full, o_full, o_free, f_full[2];
+    uint64_t sh_full, sl_full, ks_full, qs_full, rh_full, rl_full, su_full, o_full, o_free, f_full[2];
     uint32_t tmem;
     int found;
 };
 
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(a, fmaxf(b, c)); }
 
-// Packs N values two by two as fp16 high and low parts and stores them to N / 2 columns each.
-template <int N> __device__ __forceinline__ void store_split(uint32_t hi_at, uint32_t lo_at, const float (&x)[N])
+// Values two by two as fp16 high parts, N / 2 columns; and what those leave, as
+// low parts (the products with the high ones run meanwhile).
+template <int N> __device__ __forceinline__ void store_pairs(uint32_t at, const uint32_t (&v)[N])
 {
+    static_assert(N == 8 || N % 16 == 0, "columns");
+    if constexpr (N == 8) ptx::tmem_st8(at, v);
+    else {
 #pragma unroll
-    for (int b = 0; b < N; b += 32) {
-        uint32_t hi[16], lo[16];
+        for (int b = 0; b < N; b += 16) {
+            uint32_t w[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) split_h(x[b + 2 * i], x[b + 2 * i + 1], hi[i], lo[i]);
-        ptx::tmem_st16_async(hi_at + b / 2, hi);
-        ptx::tmem_st16_async(lo_at + b / 2, lo);
+            for (int i = 0; i < 16; ++i) w[i] = v[b + i];
+            ptx::tmem_st16_async(at + b, w);
+        }
+        ptx::tmem_wait_st();
     }
-    ptx::tmem_wait_st();
+}
+template <int N> __device__ __forceinline__ void store_high(uint32_t at, const float (&x)[N])
+{
+    uint32_t v[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) v[i] = pack_h(x[2 * i], x[2 * i + 1]);
+    store_pairs(at, v);
+}
+template <int N> __device__ __forceinline__ void store_low(uint32_t at, const float (&x)[N])
+{
+    uint32_t v[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+        const float2 h = unpack_h(pack_h(x[2 * i], x[2 * i + 1]));
+        v[i] = pack_h(x[2 * i] - h.x, x[2 * i + 1] - h.y);
+    }
+    store_pairs(at, v);
 }
 
 // The sequence of rank `rank` by length, longest first (ties: lowest index):
@@ -721,55 +756,70 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) gdn_chain_kernel(const GdnAr
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&sm.loaded[i], 1);
-            ptx::mbar_init(&sm.freed[i], 2 * NW);
+            ptx::mbar_init(&sm.freed[i], 2 * NW + 1);
             ptx::mbar_init(&sm.f_full[i], NW);
         }
-        ptx::mbar_init(&sm.s_full, NW);
-        ptx::mbar_init(&sm.ks_full, 1);
-        ptx::mbar_init(&sm.r_full, NW);
+        ptx::mbar_init(&sm.sh_full, 2 * NW);
+        ptx::mbar_init(&sm.sl_full, 2 * NW);
+        ptx::mbar_init(&sm.ks_full, 2);
+        ptx::mbar_init(&sm.qs_full, 1);
+        ptx::mbar_init(&sm.rh_full, 2 * NW);
+        ptx::mbar_init(&sm.rl_full, 2 * NW);
         ptx::mbar_init(&sm.su_full, 1);
         ptx::mbar_init(&sm.o_full, 1);
-        ptx::mbar_init(&sm.o_free, NW);
+        ptx::mbar_init(&sm.o_free, 2 * NW);
         ptx::fence_mbar_init();
     }
-    if (warp == 5) ptx::tmem_alloc(&sm.tmem, TM_COLS);
+    if (warp == 8) ptx::tmem_alloc(&sm.tmem, TM_COLS);
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = sm.tmem;
     Waiter wait{false};
 
-    // Registers: the launch gives every thread 168; the chain's warpgroup takes
-    // what the others leave (248 + 64 + 104 <= 3 * 168).
-    if (warp < 4) {
-        set_regs<true, 248>();
-        if (warp < NW) {
-            // column c of the state, scaled by g
-            const int c = warp * 32 + lane;
-            const uint32_t lanes = (uint32_t)(warp * 32) << 16, at = tmem + lanes;
-            float* state = a.state + ((size_t)state_slot * a.Hv + h) * DK * DV + c;
-            float s[DK], mx = 0.f, g, ig, rd = 1.f, ru = 1.f;
+    // Registers: the launch gives every thread 96; the chain's two warpgroups
+    // take what the others leave (2 * 144 + 64 + 2 * 64 <= 5 * 96).
+    if (warp < 8) {
+        set_regs<true, 144>();
+        if ((warp & 3) < NW) {
+            // column c of the state, scaled by g; of each product's columns (dk, then
+            // the chunk's rows) this warp has one half, its partner the other
+            constexpr int SK = DK / 2, RK = C / 2;
+            const int pair = warp & 3, half = warp >> 2, c = pair * 32 + lane;
+            const uint32_t at = tmem + ((uint32_t)(pair * 32) << 16);
+            float* state = a.state + ((size_t)state_slot * a.Hv + h) * DK * DV + (size_t)half * SK * DV + c;
+            // the larger of both halves' largest values
+            auto both = [&](int which, float x) {
+                sm.top[which][half][c] = x;
+                asm volatile("bar.sync %0, 64;" ::"r"(pair + 1) : "memory");
+                return fmaxf(x, sm.top[which][half ^ 1][c]);
+            };
+            float s[SK], mx = 0.f, g, ig, rd = 1.f, ru = 1.f;
 #pragma unroll
-            for (int i = 0; i < DK; ++i) s[i] = state[(size_t)i * DV];
+            for (int i = 0; i < SK; ++i) s[i] = state[(size_t)i * DV];
 #pragma unroll
-            for (int i = 0; i < DK; i += 2) mx = max3(mx, fabsf(s[i]), fabsf(s[i + 1]));
-            pow2_scale(mx, g, ig);
+            for (int i = 0; i < SK; i += 2) mx = max3(mx, fabsf(s[i]), fabsf(s[i + 1]));
+            pow2_scale(both(1, mx), g, ig);
 #pragma unroll
-            for (int i = 0; i < DK; ++i) s[i] *= g;
+            for (int i = 0; i < SK; ++i) s[i] *= g;
             for (int m = 0; m < chunks; ++m) {
                 const int b = m & 1, n = end - begin - m * C;
-                store_split<DK>(at + TM_SH, at + TM_SL, s);
+                if (m > 0) wait(sm.qs_full, m - 1);  // S's place is free
+                store_high<SK>(at + TM_SH + half * (SK / 2), s);
                 ptx::tc_fence_before();
-                warp_arrive(sm.s_full, lane);
+                warp_arrive(sm.sh_full, lane);
+                store_low<SK>(at + TM_SL + half * (SK / 2), s);
+                ptx::tc_fence_before();
+                warp_arrive(sm.sl_full, lane);
 
                 // R = beta V - beta e^G k.S, times rd
                 wait(sm.loaded[b], m >> 1);
-                const Factors& fac = *reinterpret_cast<const Factors*>(sm.work[b] + 2 * L::M + L::PARTS * 8192);
-                const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(sm.v[b]) + c;
-                float r[C];
+                const Factors& fac = sm.fac[m & 3];
+                const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(sm.v[b]) + half * RK * DV + c;
+                float r[RK];
 #pragma unroll
-                for (int i = 0; i < C; i += 4) {
-                    const float4 be = *reinterpret_cast<const float4*>(&fac.beta[i]);
+                for (int i = 0; i < RK; i += 4) {
+                    const float4 be = *reinterpret_cast<const float4*>(&fac.beta[half * RK + i]);
                     r[i] = be.x * (__bfloat162float(v[i * DV]) * rd);
                     r[i + 1] = be.y * (__bfloat162float(v[(i + 1) * DV]) * rd);
                     r[i + 2] = be.z * (__bfloat162float(v[(i + 2) * DV]) * rd);
@@ -777,7 +827,7 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) gdn_chain_kernel(const GdnAr
                 }
                 if (n < C)  // the copies took the next sequence's rows along
 #pragma unroll
-                    for (int i = 0; i < C; ++i) r[i] = i < n ? r[i] : 0.f;
+                    for (int i = 0; i < RK; ++i) r[i] = half * RK + i < n ? r[i] : 0.f;
                 const float last = fac.last, x = fac.x;
                 if (m > 0) wait(sm.o_full, m - 1);  // R's place is free
                 wait(sm.ks_full, m);
@@ -785,119 +835,122 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) gdn_chain_kernel(const GdnAr
                 const float fr = ig * rd;
                 mx = 0.f;
 #pragma unroll
-                for (int q = 0; q < C; q += 32) {
-                    float d[32];
-                    ptx::tmem_ld32(at + TM_X + q, d);
+                for (int q = 0; q < RK; q += 16) {
+                    float d[16], e[16];
+                    ptx::tmem_ld16(at + TM_X + half * RK + q, d);
+                    ptx::tmem_ld16(at + TM_X + C + half * RK + q, e);
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
-                        const float4 ek = *reinterpret_cast<const float4*>(&fac.ek[q + i]);
-                        r[q + i] = fmaf(-ek.x, d[i] * fr, r[q + i]);
-                        r[q + i + 1] = fmaf(-ek.y, d[i + 1] * fr, r[q + i + 1]);
-                        r[q + i + 2] = fmaf(-ek.z, d[i + 2] * fr, r[q + i + 2]);
-                        r[q + i + 3] = fmaf(-ek.w, d[i + 3] * fr, r[q + i + 3]);
-                        mx = max3(mx, max3(fabsf(r[q + i]), fabsf(r[q + i + 1]), fabsf(r[q + i + 2])), fabsf(r[q + i + 3]));
+                    for (int i = 0; i < 16; i += 4) {
+                        const float4 ek = *reinterpret_cast<const float4*>(&fac.ek[half * RK + q + i]);
+                        float* x = &r[q + i];
+                        x[0] = fmaf(-ek.x, (d[i] + e[i]) * fr, x[0]);
+                        x[1] = fmaf(-ek.y, (d[i + 1] + e[i + 1]) * fr, x[1]);
+                        x[2] = fmaf(-ek.z, (d[i + 2] + e[i + 2]) * fr, x[2]);
+                        x[3] = fmaf(-ek.w, (d[i + 3] + e[i + 3]) * fr, x[3]);
+                        mx = max3(mx, max3(fabsf(x[0]), fabsf(x[1]), fabsf(x[2])), fabsf(x[3]));
                     }
                 }
+                mx = both(0, mx);
                 // fp16 has room for a stale scale; a new one where the largest value has left [2^-6, 2^10)
                 if (__any_sync(0xffffffffu, mx != 0.f && !(mx >= 0x1p-6f && mx < 0x1p10f))) {
                     float down, up;
                     pow2_scale(mx * ru, down, up);
                     const float f = down * ru;
 #pragma unroll
-                    for (int i = 0; i < C; ++i) r[i] *= f;
+                    for (int i = 0; i < RK; ++i) r[i] *= f;
                     rd = down;
                     ru = up;
                 }
-                store_split<C>(at + TM_RH, at + TM_RL, r);
+                store_high<RK>(at + TM_RH + half * (RK / 2), r);
                 ptx::tc_fence_before();
-                warp_arrive(sm.r_full, lane);
-                sm.f1[b][c] = ig;
-                sm.f2[b][c] = ru * x;
-                warp_arrive(sm.f_full[b], lane);
+                warp_arrive(sm.rh_full, lane);
+                store_low<RK>(at + TM_RL + half * (RK / 2), r);
+                ptx::tc_fence_before();
+                warp_arrive(sm.rl_full, lane);
+                if (half == 0) {
+                    sm.f1[b][c] = ig;
+                    sm.f2[b][c] = ru * x;
+                    warp_arrive(sm.f_full[b], lane);
+                }
 
                 // S = e^{G_C} S + M^T R
 #pragma unroll
-                for (int i = 0; i < DK; ++i) s[i] *= last;
+                for (int i = 0; i < SK; ++i) s[i] *= last;
                 const float fs = (ru * x) * g;
                 wait(sm.su_full, m);
                 ptx::tc_fence_after();
                 mx = 0.f;
+                constexpr int W = SK < 32 ? SK : 32;
 #pragma unroll
-                for (int q = 0; q < DK; q += 32) {
-                    float d[32];
-                    ptx::tmem_ld32(at + TM_X + q, d);
+                for (int q = 0; q < SK; q += W) {
+                    float d[W];
+                    if constexpr (W == 32) ptx::tmem_ld32(at + TM_X + half * SK + q, d);
+                    else ptx::tmem_ld16(at + TM_X + half * SK + q, d);
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
+                    for (int i = 0; i < W; i += 2) {
                         s[q + i] = fmaf(fs, d[i], s[q + i]);
                         s[q + i + 1] = fmaf(fs, d[i + 1], s[q + i + 1]);
                         mx = max3(mx, fabsf(s[q + i]), fabsf(s[q + i + 1]));
                     }
                 }
+                mx = both(1, mx);
                 if (__any_sync(0xffffffffu, mx != 0.f && !(mx >= 0x1p-6f && mx < 0x1p10f))) {
                     float down, up;
                     pow2_scale(mx * ig, down, up);
                     const float f = down * ig;
 #pragma unroll
-                    for (int i = 0; i < DK; ++i) s[i] *= f;
+                    for (int i = 0; i < SK; ++i) s[i] *= f;
                     g = down;
                     ig = up;
                 }
                 warp_arrive(sm.freed[b], lane);
             }
 #pragma unroll
-            for (int i = 0; i < DK; ++i) state[(size_t)i * DV] = s[i] * ig;
+            for (int i = 0; i < SK; ++i) state[(size_t)i * DV] = s[i] * ig;
         }
-    } else if (warp < 8) {
+    } else if (warp < 12) {
         set_regs<false, 64>();
-        if (warp == 4) {
+        auto kq_step = [](int kt) { return (uint64_t)((kt >> 2) * (16384 >> 4) + (kt & 3) * 2); };
+        constexpr uint32_t id = ptx::idesc_f16(128, C), idm = ptx::idesc_f16(128, DK);
+        if (warp == 8) {
             const uint64_t policy = ptx::policy_evict_first();
             const long long slot0 = begin / C + seq;
             for (int m = 0; m < chunks; ++m) {
                 const int b = m & 1;
+                // a chunk's operands are free once its products are through; its factors
+                // are read a little longer, while its outputs are formed: a ring of four
                 if (m >= 2) wait(sm.freed[b], (m - 2) >> 1);
                 if (lane == 0) {
                     uint64_t* bar = &sm.loaded[b];
+                    const unsigned char* w = ws.v + ((slot0 + m) * a.Hv + h) * L::V;
                     ptx::mbar_arrive_expect_tx(bar, L::KQ + L::V + C * DV * 2);
                     ptx::bulk_g2s(sm.kq[b], ws.kq + ((slot0 + m) * a.Hk + h / (a.Hv / a.Hk)) * L::KQ, L::KQ, bar);
                     ptx::tma_load_2d(sm.v[b], &vmap, h * DV, begin + m * C, bar, policy);
-                    ptx::bulk_g2s_stream(sm.work[b], ws.v + ((slot0 + m) * a.Hv + h) * L::V, L::V, bar, policy);
+                    ptx::bulk_g2s_stream(&sm.fac[m & 3], w + sizeof(sm.work[0]), sizeof(Factors), bar, policy);
+                    ptx::bulk_g2s_stream(sm.work[b], w, sizeof(sm.work[0]), bar, policy);
                 }
                 __syncwarp();
             }
-        } else if (warp == 5) {
-            // the products, all from one thread: each commit covers what came before it
+        } else if (warp == 9 || warp == 10) {
+            // The critical products from two threads (one issues at half the
+            // tensor core's rate): K S of S's high parts and M^T R, K S of its low parts.
+            const bool first = warp == 9;
             for (int m = 0; m < chunks; ++m) {
                 const int b = m & 1;
                 wait(sm.loaded[b], m >> 1);
-                wait(sm.s_full, m);
+                wait(first ? sm.sh_full : sm.sl_full, m);
                 ptx::tc_fence_after();
-                const uint64_t k = ptx::desc_sw128(ptx::smem_u32(sm.kq[b])), q = k + (8192 >> 4);
-                const uint64_t mh = ptx::desc_sw128(ptx::smem_u32(sm.work[b])), ml = mh + (L::M >> 4), pt = ml + (L::M >> 4);
-                constexpr uint32_t id = ptx::idesc_f16(128, C), idm = ptx::idesc_f16(128, DK);
-                auto kq_step = [](int kt) { return (uint64_t)((kt >> 2) * (16384 >> 4) + (kt & 3) * 2); };
+                const uint64_t k = ptx::desc_sw128(ptx::smem_u32(sm.kq[b]));
+                const uint64_t mh = ptx::desc_sw128(ptx::smem_u32(sm.work[b])), ml = mh + (L::M >> 4);
                 if (lane == 0) {
+                    const uint32_t d = tmem + TM_X + (first ? 0 : C), s = tmem + (first ? TM_SH : TM_SL);
 #pragma unroll
-                    for (int kt = 0; kt < DK / 16; ++kt)
-                        ptx::mma_bf16_ts(tmem + TM_X, tmem + TM_SH + kt * 8, k + kq_step(kt), id, kt > 0);
-#pragma unroll
-                    for (int kt = 0; kt < DK / 16; ++kt)
-                        ptx::mma_bf16_ts(tmem + TM_X, tmem + TM_SL + kt * 8, k + kq_step(kt), id, 1);
+                    for (int kt = 0; kt < DK / 16; ++kt) ptx::mma_bf16_ts(d, s + kt * 8, k + kq_step(kt), id, kt > 0);
                     ptx::mma_commit(&sm.ks_full);
                 }
                 __syncwarp();
-                if (m > 0) wait(sm.o_free, m - 1);
-                ptx::tc_fence_after();
-                if (lane == 0) {
-#pragma unroll 1
-                    for (int kt = 0; kt < DK / 16; ++kt)
-                        ptx::mma_bf16_ts(tmem + TM_QS, tmem + TM_SH + kt * 8, q + kq_step(kt), id, kt > 0);
-                    if (F32)
-#pragma unroll 1
-                        for (int kt = 0; kt < DK / 16; ++kt)
-                            ptx::mma_bf16_ts(tmem + TM_QS, tmem + TM_SL + kt * 8, q + kq_step(kt), id, 1);
-                }
-                __syncwarp();
-                wait(sm.r_full, m);
+                if (!first) continue;
+                wait(sm.rh_full, m);
                 ptx::tc_fence_after();
                 if (lane == 0) {
 #pragma unroll
@@ -905,46 +958,85 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) gdn_chain_kernel(const GdnAr
                         ptx::mma_bf16_ts(tmem + TM_X, tmem + TM_RH + kt * 8, mh + kt * 2, idm, kt > 0);
 #pragma unroll
                     for (int kt = 0; kt < 4; ++kt)
-                        ptx::mma_bf16_ts(tmem + TM_X, tmem + TM_RL + kt * 8, mh + kt * 2, idm, 1);
+                        ptx::mma_bf16_ts(tmem + TM_X, tmem + TM_RH + kt * 8, ml + kt * 2, idm, 1);
+                }
+                __syncwarp();
+                wait(sm.rl_full, m);
+                ptx::tc_fence_after();
+                if (lane == 0) {
 #pragma unroll
                     for (int kt = 0; kt < 4; ++kt)
-                        ptx::mma_bf16_ts(tmem + TM_X, tmem + TM_RH + kt * 8, ml + kt * 2, idm, 1);
+                        ptx::mma_bf16_ts(tmem + TM_X, tmem + TM_RL + kt * 8, mh + kt * 2, idm, 1);
                     ptx::mma_commit(&sm.su_full);
-#pragma unroll 1
+                }
+                __syncwarp();
+            }
+        } else {
+            // the outputs' products
+            for (int m = 0; m < chunks; ++m) {
+                const int b = m & 1;
+                wait(sm.loaded[b], m >> 1);
+                wait(sm.sh_full, m);
+                if (F32) wait(sm.sl_full, m);
+                if (m > 0) wait(sm.o_free, m - 1);
+                ptx::tc_fence_after();
+                const uint64_t q = ptx::desc_sw128(ptx::smem_u32(sm.kq[b]) + 8192);
+                const uint64_t pt = ptx::desc_sw128(ptx::smem_u32(sm.work[b]) + 2 * L::M);
+                if (lane == 0) {
+#pragma unroll
+                    for (int kt = 0; kt < DK / 16; ++kt)
+                        ptx::mma_bf16_ts(tmem + TM_QS, tmem + TM_SH + kt * 8, q + kq_step(kt), id, kt > 0);
+                    if (F32)
+#pragma unroll
+                        for (int kt = 0; kt < DK / 16; ++kt)
+                            ptx::mma_bf16_ts(tmem + TM_QS, tmem + TM_SL + kt * 8, q + kq_step(kt), id, 1);
+                    ptx::mma_commit(&sm.qs_full);
+                }
+                __syncwarp();
+                wait(sm.rh_full, m);
+                if (F32) wait(sm.rl_full, m);
+                ptx::tc_fence_after();
+                if (lane == 0) {
+#pragma unroll
                     for (int kt = 0; kt < 4; ++kt)
                         ptx::mma_bf16_ts(tmem + TM_PR, tmem + TM_RH + kt * 8, pt + kt * 2, id, kt > 0);
                     if (F32)
-#pragma unroll 1
+#pragma unroll
                         for (int kt = 0; kt < 4; ++kt) {
                             ptx::mma_bf16_ts(tmem + TM_PR, tmem + TM_RL + kt * 8, pt + kt * 2, id, 1);
                             ptx::mma_bf16_ts(tmem + TM_PR, tmem + TM_RH + kt * 8, pt + (8192 >> 4) + kt * 2, id, 1);
                         }
                     ptx::mma_commit(&sm.o_full);
+                    ptx::mma_commit(&sm.freed[b]);
                 }
                 __syncwarp();
             }
         }
     } else {
-        set_regs<false, 104>();
-        if (warp - 8 < NW) {
-            // column c of the outputs: o_r = e1 q'.S + e2 (P T R)_r
-            const int w = warp - 8, c = w * 32 + lane;
+        set_regs<false, 64>();
+        if ((warp & 3) < NW) {
+            // column c of the outputs: o_r = e1 q'.S + e2 (P T R)_r, for half of the rows
+            const int w = warp & 3, c = w * 32 + lane, half = (warp - 12) >> 2;
             const uint32_t at = tmem + ((uint32_t)(w * 32) << 16);
             const size_t row_stride = (size_t)a.Hv * DV;
             for (int m = 0; m < chunks; ++m) {
                 const int b = m & 1, n = min(C, end - begin - m * C);
-                wait(sm.loaded[b], m >> 1);
                 wait(sm.f_full[b], m >> 1);
                 const float f1 = sm.f1[b][c], f2 = sm.f2[b][c];
-                const Factors& fac = *reinterpret_cast<const Factors*>(sm.work[b] + 2 * L::M + L::PARTS * 8192);
+                const Factors& fac = sm.fac[m & 3];
                 const size_t o0 = ((size_t)begin + (size_t)m * C) * row_stride + (size_t)h * DV;
                 wait(sm.o_full, m);
                 ptx::tc_fence_after();
-#pragma unroll 1
-                for (int i0 = 0; i0 < C; i0 += 16) {
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                    const int i0 = half * (C / 2) + z * 16;
                     float x[16], y[16];
                     ptx::tmem_ld16(at + TM_QS + i0, x);
                     ptx::tmem_ld16(at + TM_PR + i0, y);
+                    if (z == 1) {
+                        ptx::tc_fence_before();
+                        warp_arrive(sm.o_free, lane);
+                    }
 #pragma unroll
                     for (int i = 0; i < 16; i += 4) {
                         const float4 e1 = *reinterpret_cast<const float4*>(&fac.e1[i0 + i]);
@@ -971,16 +1063,13 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) gdn_chain_kernel(const GdnAr
                     }
                     __syncwarp();
                 }
-                ptx::tc_fence_before();
-                warp_arrive(sm.o_free, lane);
-                warp_arrive(sm.freed[b], lane);
             }
         }
     }
     if (wait.dead) flag_status(a.dev_status, KDA_DEV_TIMEOUT);
     ptx::tc_fence_before();
     __syncthreads();
-    if (warp == 5) {
+    if (warp == 8) {
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tmem, TM_COLS);
     }
@@ -1008,7 +1097,8 @@ cudaError_t launch_chain(const GdnArgs& a, const CUtensorMap& vmap, const Work& 
     using S = ChainSmem<DK, DV, F32>;
     constexpr int smem = sizeof(S);
     // operand tiles on the swizzle's 1024-byte period, barriers on 8
-    static_assert(offsetof(S, work) % 1024 == 0 && offsetof(S, v) % 128 == 0 && offsetof(S, loaded) % 8 == 0, "alignment");
+    static_assert(offsetof(S, work) % 1024 == 0 && offsetof(S, v) % 128 == 0 && offsetof(S, fac) % 16 == 0 && offsetof(S, loaded) % 8 == 0,
+                  "alignment");
     static_assert(smem <= 227 * 1024, "shared memory");
     static PerDeviceOnce once;
     cudaError_t e = once.run([](int) {
