@@ -138,7 +138,8 @@ struct Factors {
     float beta[C], ek[C];  // beta; beta e^G and k's row factor
     float e1[C], e2[C];    // scale, q's row factor, e^G (e1)
     float last, x;         // e^{G_C}; what M and P T still have to be multiplied by
-    float pad[30];
+    float top;             // M's largest value
+    float pad[29];
 };
 template <int DK, bool F32> struct Slot {
     static constexpr int HALVES = DK <= 64 ? 1 : DK / 64;  // 64-wide tiles a row spans (dk = 32: half of one)
@@ -164,27 +165,30 @@ struct RowMaps {
 constexpr int PREP = 256;
 template <bool F32> constexpr int prep_ctas() { return F32 ? 2 : 3; }  // of an SM, by their shared memory
 
-template <int DK, bool F32> struct PrepSmem {
+template <int DK, bool F32, int HEADS> struct PrepSmem {
     using L = Slot<DK, F32>;
     static constexpr int PARTS = L::PARTS;
     unsigned char kq[L::KQ];  // bf16 rows of k, then q; fp16 later; P T over q's
     union {
         struct {  // 64 x 64 fp16 tiles
             unsigned char t_hi[8192], t_lo[8192];  // T; then diag(e^{G_C - G}) Ts
-            unsigned char ts[PARTS][8192];         // Ts = diag(k's row factors / x) T
+            union {
+                unsigned char ts[PARTS][8192];  // Ts = diag(k's row factors / x) T
+                alignas(16) float xd[C * XS];   // before: A's diagonal blocks, 16 x 16 each
+            };
             unsigned char p_hi[8192], p_lo[F32 ? 8192 : 128];
         };
         unsigned char m[2][L::M];  // then M^T
     };
     unsigned char pt_lo[F32 ? 8192 : 128];
-    Factors fac;
-    alignas(16) float xd[C * XS];  // A's diagonal blocks, 16 x 16 each
-    alignas(16) float eg[C], gh[C], gl[C], w[C];  // e^G, G / ln 2 in two words, e^{G_C - G}
+    Factors fac[HEADS];
+    struct Gates {
+        alignas(16) float eg[C], gh[C], gl[C], w[C];  // e^G, G / ln 2 in two words, e^{G_C - G}
+    } gates[HEADS];
     alignas(16) float norm[2 * C];  // squared norms of k's and q's rows
     alignas(16) float row[2 * C], colk[C], down[2 * C], sk[C];  // factors of A's and P's rows, of A's columns; of the stored rows
     uint64_t loaded, prod;
     uint32_t tmem;
-    int begin, rows;
 };
 
 __device__ __forceinline__ void prep_sync() { __syncthreads(); }
@@ -203,7 +207,7 @@ __device__ __forceinline__ void dw_add(float& h, float& l, float oh, float ol)
 
 // One warp, rows 2 lane and 2 lane + 1 of a chunk: running sums of their log2
 // decays g (double word: differences of large sums keep their small part).
-template <class S> __device__ __forceinline__ void scan_rows(S& sm, float2 g, int lane)
+template <class S> __device__ __forceinline__ void scan_rows(S& gt, float2 g, float& last, int lane)
 {
     float h = g.x, l = 0.f;
     dw_add(h, l, g.y, 0.f);
@@ -216,12 +220,12 @@ template <class S> __device__ __forceinline__ void scan_rows(S& sm, float2 g, in
     float ph = __shfl_up_sync(0xffffffffu, h, 1), pl = __shfl_up_sync(0xffffffffu, l, 1);
     if (lane == 0) ph = pl = 0.f;
     dw_add(ph, pl, g.x, 0.f);  // the lane's first row
-    *reinterpret_cast<float2*>(&sm.gh[2 * lane]) = make_float2(ph, h);
-    *reinterpret_cast<float2*>(&sm.gl[2 * lane]) = make_float2(pl, l);
-    *reinterpret_cast<float2*>(&sm.eg[2 * lane]) = make_float2(exp2_sfu(ph + pl), exp2_sfu(h + l));
-    *reinterpret_cast<float2*>(&sm.w[2 * lane]) =
+    *reinterpret_cast<float2*>(&gt.gh[2 * lane]) = make_float2(ph, h);
+    *reinterpret_cast<float2*>(&gt.gl[2 * lane]) = make_float2(pl, l);
+    *reinterpret_cast<float2*>(&gt.eg[2 * lane]) = make_float2(exp2_sfu(ph + pl), exp2_sfu(h + l));
+    *reinterpret_cast<float2*>(&gt.w[2 * lane]) =
         make_float2(exp2_sfu((th - ph) + (tl - pl)), exp2_sfu((th - h) + (tl - l)));
-    if (lane == 0) sm.fac.last = exp2_sfu(th + tl);
+    if (lane == 0) last = exp2_sfu(th + tl);
 }
 
 // A row of [K; Q]: bf16 -> fp16 times a power of two, in place; zeros for a
@@ -326,31 +330,40 @@ template <int SIZE> struct Merge {
     }
 };
 
-// One chunk's share of one value head.  Bound: latency (a dozen dependent
-// phases of a few hundred instructions each); several CTAs an SM fill each other's gaps.
-template <int DK, bool F32>
-__global__ void __launch_bounds__(PREP, prep_ctas<F32>()) gdn_prep_kernel(const GdnArgs a, const __grid_constant__ RowMaps maps, const Work ws)
+// One chunk's share of HEADS value heads of one key head: the rows, their
+// products and norms once, then head by head.  Bound: latency (a dozen
+// dependent phases of a few hundred instructions each); several CTAs an SM fill
+// each other's gaps.
+template <int DK, bool F32, int HEADS>
+__global__ void __launch_bounds__(PREP, prep_ctas<F32>())
+gdn_prep_kernel(const GdnArgs a, const __grid_constant__ RowMaps maps, const Work ws)
 {
     extern __shared__ __align__(1024) unsigned char dyn[];
-    using S = PrepSmem<DK, F32>;
+    using S = PrepSmem<DK, F32, HEADS>;
     using L = Slot<DK, F32>;
     S& sm = *reinterpret_cast<S*>(dyn);
     const int t = threadIdx.x, w = t >> 5, lane = t & 31;
-    const int h = blockIdx.x % a.Hv, rep = a.Hv / a.Hk, hk = h / rep;
-    const int slot = blockIdx.x / a.Hv;
-    if (t == 0) sm.begin = -1;
-    __syncthreads();
-    // the sequence that has this slot
-    for (int s = t; s < a.N; s += PREP) {
-        const int b = a.cu_seqlens[s], e = a.cu_seqlens[s + 1];
+    const int groups = a.Hv / HEADS, h0 = blockIdx.x % groups * HEADS, rep = a.Hv / a.Hk, hk = h0 / rep;
+    const int slot = blockIdx.x / groups;
+    // Warps 4, 6: a head's gates.  Their parameters first, then (every warp for itself) the rows of this slot.
+    const int gate_head = w == 4 ? 0 : (w == 6 && HEADS == 2) ? 1 : -1;
+    float ea = 0.f, dt = 0.f;
+    if (gate_head >= 0) {
+        ea = a.A_log[h0 + gate_head];
+        dt = a.dt_bias[h0 + gate_head];
+    }
+    int r0 = -1, n = 0;
+    for (int s0 = 0; s0 < a.N && r0 < 0; s0 += 32) {
+        const int s = s0 + lane;
+        const int b = s < a.N ? a.cu_seqlens[s] : -1, e = s < a.N ? a.cu_seqlens[s + 1] : -1;
         const int c = slot - b / C - s;
-        if (b >= 0 && e > b && e <= a.T && c >= 0 && c < (e - b + C - 1) / C) {
-            sm.begin = b + c * C;
-            sm.rows = min(C, e - b - c * C);
+        const uint32_t hit = __ballot_sync(0xffffffffu, b >= 0 && e > b && e <= a.T && c >= 0 && c < (e - b + C - 1) / C);
+        if (hit) {
+            const int l = __ffs(hit) - 1;
+            r0 = __shfl_sync(0xffffffffu, b + c * C, l);
+            n = min(C, __shfl_sync(0xffffffffu, e, l) - r0);
         }
     }
-    __syncthreads();
-    const int r0 = sm.begin, n = sm.rows;
     if (r0 < 0) return;
 
     if (t == 0) {
@@ -366,6 +379,16 @@ __global__ void __launch_bounds__(PREP, prep_ctas<F32>()) gdn_prep_kernel(const 
         }
     }
     if (w == 1) ptx::tmem_alloc(&sm.tmem, 128);
+    float graw[2] = {0.f, 0.f}, braw[2] = {0.f, 0.f};
+    if (gate_head >= 0) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (2 * lane + i < n) {
+                const size_t at = (size_t)(r0 + 2 * lane + i) * a.Hv + h0 + gate_head;
+                graw[i] = ldv(static_cast<const __nv_bfloat16*>(a.a) + at);
+                braw[i] = ldv(static_cast<const __nv_bfloat16*>(a.b) + at);
+            }
+    }
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
@@ -385,25 +408,25 @@ __global__ void __launch_bounds__(PREP, prep_ctas<F32>()) gdn_prep_kernel(const 
         }
         __syncwarp();
     }
-    // a row of [K; Q] a lane (w & 3), against half of k's rows (w >> 2); the
-    // halves above the diagonal (w = 4 and 6) are left out
-    const int lr = (w & 3) * 32 + lane, r = lr & (C - 1), type = lr >> 6, s0 = (w >> 2) * 32;  // type 0: k, 1: q
-    const uint32_t at = tmem + ((uint32_t)((w & 3) * 32) << 16);
-    if (w == 4) {
-        // two rows a lane: gates and running sums
-        const float ea = expf(a.A_log[h]) * 1.44269504088896341f, dt = a.dt_bias[h];
+    if (gate_head >= 0) {
+        // two rows a lane; a padded row decays nothing and takes nothing
+        ea = expf(ea) * 1.44269504088896341f;
         float g[2] = {0.f, 0.f}, bt[2] = {0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < 2; ++i)
             if (2 * lane + i < n) {
-                const size_t at = (size_t)(r0 + 2 * lane + i) * a.Hv + h;
-                g[i] = gdn_log_alpha(ea, ldv(static_cast<const __nv_bfloat16*>(a.a) + at), dt);
-                bt[i] = sigmoidf_(ldv(static_cast<const __nv_bfloat16*>(a.b) + at));
+                g[i] = gdn_log_alpha(ea, graw[i], dt);
+                bt[i] = sigmoidf_(braw[i]);
             }
-        sm.fac.beta[2 * lane] = bt[0];
-        sm.fac.beta[2 * lane + 1] = bt[1];
-        scan_rows(sm, make_float2(g[0], g[1]), lane);
+        sm.fac[gate_head].beta[2 * lane] = bt[0];
+        sm.fac[gate_head].beta[2 * lane + 1] = bt[1];
+        if (lane == 0) sm.fac[gate_head].top = 0.f;
+        scan_rows(sm.gates[gate_head], make_float2(g[0], g[1]), sm.fac[gate_head].last, lane);
     }
+    // a row of [K; Q] a lane (w & 3), against half of k's rows (w >> 2); the
+    // halves above the diagonal (w = 4 and 6) are left out
+    const int lr = (w & 3) * 32 + lane, r = lr & (C - 1), type = lr >> 6, s0 = (w >> 2) * 32;  // type 0: k, 1: q
+    const uint32_t at = tmem + ((uint32_t)((w & 3) * 32) << 16);
     wait(sm.prod, 0);
     ptx::tc_fence_after();
     if (w == 0 || w >= 5) {
@@ -420,154 +443,6 @@ __global__ void __launch_bounds__(PREP, prep_ctas<F32>()) gdn_prep_kernel(const 
         sm.norm[lr] = y;
     }
     prep_sync();
-    if (w < 4) {
-        const float ss = sm.norm[lr];
-        float down, up;
-        pow2_scale_sqrt(ss, down, up);
-        // the factor that makes the stored row the (normalised) row; none for a padded one
-        const float nrm = r < n ? (a.l2 ? rsqrtf(ss + a.l2_eps) : 1.f) : 0.f, f = nrm * up;
-        sm.down[lr] = down;
-        if (type == 0) {
-            const float be = sm.fac.beta[r];
-            sm.sk[r] = f;
-            sm.fac.ek[r] = be * f * sm.eg[r];
-            sm.colk[r] = nrm;  // A comes from the raw rows' products
-            sm.row[r] = be * nrm;
-        } else {
-            sm.fac.e1[r] = a.scale * f * sm.eg[r];
-            sm.fac.e2[r] = a.scale * f;
-            sm.row[lr] = down;  // P is that of the stored rows
-        }
-    }
-    prep_sync();
-    if (w != 4 && w != 6) {
-        // the lane's row of A (beta_r |..| e^{G_r - G_s} k_r.k_s) or P, zero from the diagonal (or past it) on
-        const float rh = sm.gh[r], rl = sm.gl[r], rf = sm.row[lr];
-        const float* cf = type == 0 ? sm.colk : sm.down;
-        const int lim = r < n ? r + type : 0;
-        unsigned char* hi_tile = type == 0 ? sm.t_hi : sm.p_hi;
-        unsigned char* lo_tile = type == 0 ? sm.t_lo : sm.p_lo;
-#pragma unroll 2
-        for (int p = 0; p < 4; ++p) {
-            uint32_t hi[4], lo[4];
-            float v[8], d[8];
-            ptx::tmem_ld8(at + s0 + p * 8, d);
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-                const int s = s0 + p * 8 + z * 4;
-                const float4 ch = *reinterpret_cast<const float4*>(&sm.gh[s]);
-                const float4 cl = *reinterpret_cast<const float4*>(&sm.gl[s]);
-                const float4 c4 = *reinterpret_cast<const float4*>(&cf[s]);
-                const float h4[4] = {ch.x, ch.y, ch.z, ch.w}, l4[4] = {cl.x, cl.y, cl.z, cl.w}, f4[4] = {c4.x, c4.y, c4.z, c4.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float e = exp2_sfu((rh - h4[i]) + (rl - l4[i]));
-                    v[z * 4 + i] = s + i < lim ? (rf * f4[i]) * e * d[z * 4 + i] : 0.f;
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) split_h(v[2 * i], v[2 * i + 1], hi[i], lo[i]);
-            const int c = (s0 >> 3) + p;
-            *reinterpret_cast<uint4*>(hi_tile + tile_at(r, c)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            if (F32 || type == 0) *reinterpret_cast<uint4*>(lo_tile + tile_at(r, c)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            if (type == 0 && (r >> 4) == (c >> 1)) {
-                float* x = &sm.xd[r * XS + (c & 1) * 8];
-                *reinterpret_cast<float4*>(x) = make_float4(v[0], v[1], v[2], v[3]);
-                *reinterpret_cast<float4*>(x + 4) = make_float4(v[4], v[5], v[6], v[7]);
-            }
-        }
-    }
-    ptx::tc_fence_before();
-    prep_sync();
-    if (w >= 4) {
-        // meanwhile the rows themselves, and the largest of k's factors
-        const int row = (w - 4) * 32 + lane;
-        wait(sm.loaded, 0);
-        convert_row<DK>(sm.kq, row, sm.down[row], (row & (C - 1)) < n);
-        if (w == 7) {
-            float mx = fmaxf(sm.sk[lane], sm.sk[lane + 32]);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            float down, up;
-            pow2_scale(mx, down, up);
-            if (lane == 0) sm.fac.x = up;
-        }
-    } else {
-        {
-            // a diagonal block a warp: forward substitution, a column a lane (both
-            // halves of the warp: one stores the high parts, one the low)
-            const int d0 = w * 16, c = lane & 15;
-            float x[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                float acc = i == c ? 1.f : 0.f, acc2 = 0.f;
-#pragma unroll
-                for (int j = 0; j < i; j += 4) {
-                    const float4 f = *reinterpret_cast<const float4*>(&sm.xd[(d0 + i) * XS + j]);
-                    acc = fmaf(-f.x, x[j], acc);
-                    if (j + 1 < i) acc2 = fmaf(-f.y, x[j + 1], acc2);
-                    if (j + 2 < i) acc = fmaf(-f.z, x[j + 2], acc);
-                    if (j + 3 < i) acc2 = fmaf(-f.w, x[j + 3], acc2);
-                }
-                x[i] = acc + acc2;
-            }
-            unsigned char* tile = lane < 16 ? sm.t_hi : sm.t_lo;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const __half hi = __float2half_rn(x[i]);
-                const __half lo = __float2half_rn(x[i] - __half2float(hi));
-                *reinterpret_cast<__half*>(tile + tile_at(d0 + i, (d0 + c) >> 3) + (c & 7) * 2) = lane < 16 ? hi : lo;
-            }
-        }
-        invert_sync();
-        float o[2][4];
-        if (w < 2) {
-            const int j0 = w * 32, i0 = j0 + 16;
-            Merge<16> mg;
-            mg.first(sm, i0, j0, 0, lane);
-            mg.second(sm, i0, 0, o, lane);
-            __syncwarp();
-            mg.store(sm, i0, j0, 0, 0, o, lane);
-        }
-        invert_sync();
-        Merge<32> mg;
-        const int n0 = (w & 1) * 16, mt = w >> 1;
-        mg.first(sm, 32, 0, n0, lane);
-        mg.second(sm, 32, mt, o, lane);
-        invert_sync();  // every warp has read A21
-        mg.store(sm, 32, 0, n0, mt, o, lane);
-    }
-    ptx::fence_proxy_async_smem();
-    prep_sync();
-    if (t == 0 && h % rep == 0) {
-        ptx::bulk_s2g(ws.kq + ((long long)slot * a.Hk + hk) * L::KQ, sm.kq, L::KQ);
-        ptx::bulk_commit();
-    }
-    {
-        // Ts, and T times the decays to the chunk's end, sixteen values of a row a thread; zero above the diagonal
-        const int rr = t >> 2, c0 = (t & 3) * 2;
-        const float f = sm.sk[rr] / sm.fac.x, fw = f * sm.w[rr];
-#pragma unroll
-        for (int z = 0; z < 2; ++z) {
-            const int c = c0 + z;
-            const uint4 h4 = *reinterpret_cast<const uint4*>(sm.t_hi + tile_at(rr, c));
-            const uint4 l4 = *reinterpret_cast<const uint4*>(sm.t_lo + tile_at(rr, c));
-            const uint32_t hv[4] = {h4.x, h4.y, h4.z, h4.w}, lv[4] = {l4.x, l4.y, l4.z, l4.w};
-            uint32_t sh[4], sl[4], wh[4], wl[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 x = unpack_h(hv[i]), y = unpack_h(lv[i]);
-                const float u0 = c * 8 + 2 * i <= rr ? x.x + y.x : 0.f, u1 = c * 8 + 2 * i + 1 <= rr ? x.y + y.y : 0.f;
-                split_h(u0 * f, u1 * f, sh[i], sl[i]);
-                split_h(u0 * fw, u1 * fw, wh[i], wl[i]);
-            }
-            *reinterpret_cast<uint4*>(sm.ts[0] + tile_at(rr, c)) = make_uint4(sh[0], sh[1], sh[2], sh[3]);
-            if (F32) *reinterpret_cast<uint4*>(sm.ts[F32 ? 1 : 0] + tile_at(rr, c)) = make_uint4(sl[0], sl[1], sl[2], sl[3]);
-            *reinterpret_cast<uint4*>(sm.t_hi + tile_at(rr, c)) = make_uint4(wh[0], wh[1], wh[2], wh[3]);
-            *reinterpret_cast<uint4*>(sm.t_lo + tile_at(rr, c)) = make_uint4(wl[0], wl[1], wl[2], wl[3]);
-        }
-    }
-    prep_sync();
     const int arow = lane & 15, acol = lane >> 4, brow = (lane & 7) + ((lane >> 4) & 1) * 8, bcol = (lane >> 3) & 1;
     auto store_tile = [&](unsigned char* hi_tile, unsigned char* lo_tile, int row0, const float (&c)[8][4]) {
 #pragma unroll
@@ -580,74 +455,238 @@ __global__ void __launch_bounds__(PREP, prep_ctas<F32>()) gdn_prep_kernel(const 
             if (lo_tile) stsm(ptx::smem_u32(lo_tile) + o, lo);
         }
     };
-    float c[8][4];
-    auto clear = [&] {
+
+#pragma unroll 1
+    for (int j = 0; j < HEADS; ++j) {
+        const typename S::Gates& gt = sm.gates[j];
+        Factors& fac = sm.fac[j];
+        if (w < 4) {
+            const float ss = sm.norm[lr];
+            float down, up;
+            pow2_scale_sqrt(ss, down, up);
+            // the factor that makes the stored row the (normalised) row; none for a padded one
+            const float nrm = r < n ? (a.l2 ? rsqrtf(ss + a.l2_eps) : 1.f) : 0.f, f = nrm * up;
+            sm.down[lr] = down;
+            if (type == 0) {
+                const float be = fac.beta[r];
+                sm.sk[r] = f;
+                fac.ek[r] = be * f * gt.eg[r];
+                sm.colk[r] = nrm;  // A comes from the raw rows' products
+                sm.row[r] = be * nrm;
+            } else {
+                fac.e1[r] = a.scale * f * gt.eg[r];
+                fac.e2[r] = a.scale * f;
+                sm.row[lr] = down;  // P is that of the stored rows
+            }
+        }
+        if (j > 0 && t == 0) ptx::bulk_wait_read_all();  // the head before this one has left the tiles
+        prep_sync();
+        if (w != 4 && w != 6) {
+            // the lane's row of A (beta_r |..| e^{G_r - G_s} k_r.k_s) or P, zero from the diagonal (or past it) on
+            const float rh = gt.gh[r], rl = gt.gl[r], rf = sm.row[lr];
+            const float* cf = type == 0 ? sm.colk : sm.down;
+            const int lim = r < n ? r + type : 0;
+            unsigned char* hi_tile = type == 0 ? sm.t_hi : sm.p_hi;
+            unsigned char* lo_tile = type == 0 ? sm.t_lo : sm.p_lo;
+#pragma unroll 2
+            for (int p = 0; p < 4; ++p) {
+                uint32_t hi[4], lo[4];
+                float v[8], d[8];
+                ptx::tmem_ld8(at + s0 + p * 8, d);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) c[i][0] = c[i][1] = c[i][2] = c[i][3] = 0.f;
-    };
-    clear();
-    if (w >= 4) {
-        // P T: sixteen rows a warp
-        const int mt = w - 4;
-        const uint32_t pb[2] = {ptx::smem_u32(sm.p_hi), ptx::smem_u32(sm.p_lo)};
-        const uint32_t tb[2] = {ptx::smem_u32(sm.ts[0]), ptx::smem_u32(sm.ts[F32 ? 1 : 0])};
+                for (int z = 0; z < 2; ++z) {
+                    const int s = s0 + p * 8 + z * 4;
+                    const float4 ch = *reinterpret_cast<const float4*>(&gt.gh[s]);
+                    const float4 cl = *reinterpret_cast<const float4*>(&gt.gl[s]);
+                    const float4 c4 = *reinterpret_cast<const float4*>(&cf[s]);
+                    const float h4[4] = {ch.x, ch.y, ch.z, ch.w}, l4[4] = {cl.x, cl.y, cl.z, cl.w}, f4[4] = {c4.x, c4.y, c4.z, c4.w};
 #pragma unroll
-        for (int kt = 0; kt < 4; ++kt) {
-            if (kt > mt) break;  // P's columns up to its rows
-            uint32_t x[4], y[4], f[4], e[4];
-            ldsm(x, pb[0] + tile_at(mt * 16 + arow, kt * 2 + acol));
-            if (F32) ldsm(y, pb[1] + tile_at(mt * 16 + arow, kt * 2 + acol));
+                    for (int i = 0; i < 4; ++i) {
+                        const float e = exp2_sfu((rh - h4[i]) + (rl - l4[i]));
+                        v[z * 4 + i] = s + i < lim ? (rf * f4[i]) * e * d[z * 4 + i] : 0.f;
+                    }
+                }
 #pragma unroll
-            for (int q = 0; q <= kt; ++q) {
-                ldsm_t(f, tb[0] + tile_at(kt * 16 + arow, q * 2 + acol));
-                mma(c[2 * q], x, f[0], f[1]);
-                mma(c[2 * q + 1], x, f[2], f[3]);
-                if (F32) {
-                    ldsm_t(e, tb[1] + tile_at(kt * 16 + arow, q * 2 + acol));
-                    mma(c[2 * q], y, f[0], f[1]);
-                    mma(c[2 * q + 1], y, f[2], f[3]);
+                for (int i = 0; i < 4; ++i) split_h(v[2 * i], v[2 * i + 1], hi[i], lo[i]);
+                const int c = (s0 >> 3) + p;
+                *reinterpret_cast<uint4*>(hi_tile + tile_at(r, c)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                if (F32 || type == 0) *reinterpret_cast<uint4*>(lo_tile + tile_at(r, c)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                if (type == 0 && (r >> 4) == (c >> 1)) {
+                    float* x = &sm.xd[r * XS + (c & 1) * 8];
+                    *reinterpret_cast<float4*>(x) = make_float4(v[0], v[1], v[2], v[3]);
+                    *reinterpret_cast<float4*>(x + 4) = make_float4(v[4], v[5], v[6], v[7]);
+                }
+            }
+        }
+        ptx::tc_fence_before();
+        prep_sync();
+        if (w >= 4) {
+            // meanwhile the rows themselves, and the largest of k's factors
+            if (j == 0) {
+                const int row = (w - 4) * 32 + lane;
+                wait(sm.loaded, 0);
+                convert_row<DK>(sm.kq, row, sm.down[row], (row & (C - 1)) < n);
+                ptx::fence_proxy_async_smem();
+            }
+            if (w == 7) {
+                float mx = fmaxf(sm.sk[lane], sm.sk[lane + 32]);
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                float down, up;
+                pow2_scale(mx, down, up);
+                if (lane == 0) fac.x = up;
+            }
+        } else {
+            {
+                // a diagonal block a warp: forward substitution, a column a lane (both
+                // halves of the warp: one stores the high parts, one the low)
+                const int d0 = w * 16, c = lane & 15;
+                float x[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    float acc = i == c ? 1.f : 0.f, acc2 = 0.f;
+#pragma unroll
+                    for (int k = 0; k < i; k += 4) {
+                        const float4 f = *reinterpret_cast<const float4*>(&sm.xd[(d0 + i) * XS + k]);
+                        acc = fmaf(-f.x, x[k], acc);
+                        if (k + 1 < i) acc2 = fmaf(-f.y, x[k + 1], acc2);
+                        if (k + 2 < i) acc = fmaf(-f.z, x[k + 2], acc);
+                        if (k + 3 < i) acc2 = fmaf(-f.w, x[k + 3], acc2);
+                    }
+                    x[i] = acc + acc2;
+                }
+                unsigned char* tile = lane < 16 ? sm.t_hi : sm.t_lo;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const __half hi = __float2half_rn(x[i]);
+                    const __half lo = __float2half_rn(x[i] - __half2float(hi));
+                    *reinterpret_cast<__half*>(tile + tile_at(d0 + i, (d0 + c) >> 3) + (c & 7) * 2) = lane < 16 ? hi : lo;
+                }
+            }
+            invert_sync();
+            float o[2][4];
+            if (w < 2) {
+                const int j0 = w * 32, i0 = j0 + 16;
+                Merge<16> mg;
+                mg.first(sm, i0, j0, 0, lane);
+                mg.second(sm, i0, 0, o, lane);
+                __syncwarp();
+                mg.store(sm, i0, j0, 0, 0, o, lane);
+            }
+            invert_sync();
+            Merge<32> mg;
+            const int n0 = (w & 1) * 16, mt = w >> 1;
+            mg.first(sm, 32, 0, n0, lane);
+            mg.second(sm, 32, mt, o, lane);
+            invert_sync();  // every warp has read A21
+            mg.store(sm, 32, 0, n0, mt, o, lane);
+        }
+        prep_sync();
+        if (j == 0 && t == 0 && h0 % rep == 0) {
+            ptx::bulk_s2g(ws.kq + ((long long)slot * a.Hk + hk) * L::KQ, sm.kq, L::KQ);
+            ptx::bulk_commit();
+        }
+        {
+            // Ts, and T times the decays to the chunk's end, sixteen values of a row a thread; zero above the diagonal
+            const int rr = t >> 2, c0 = (t & 3) * 2;
+            const float f = sm.sk[rr] / fac.x, fw = f * gt.w[rr];
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+                const int c = c0 + z;
+                const uint4 h4 = *reinterpret_cast<const uint4*>(sm.t_hi + tile_at(rr, c));
+                const uint4 l4 = *reinterpret_cast<const uint4*>(sm.t_lo + tile_at(rr, c));
+                const uint32_t hv[4] = {h4.x, h4.y, h4.z, h4.w}, lv[4] = {l4.x, l4.y, l4.z, l4.w};
+                uint32_t sh[4], sl[4], wh[4], wl[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 x = unpack_h(hv[i]), y = unpack_h(lv[i]);
+                    const float u0 = c * 8 + 2 * i <= rr ? x.x + y.x : 0.f, u1 = c * 8 + 2 * i + 1 <= rr ? x.y + y.y : 0.f;
+                    split_h(u0 * f, u1 * f, sh[i], sl[i]);
+                    split_h(u0 * fw, u1 * fw, wh[i], wl[i]);
+                }
+                *reinterpret_cast<uint4*>(sm.ts[0] + tile_at(rr, c)) = make_uint4(sh[0], sh[1], sh[2], sh[3]);
+                if (F32) *reinterpret_cast<uint4*>(sm.ts[F32 ? 1 : 0] + tile_at(rr, c)) = make_uint4(sl[0], sl[1], sl[2], sl[3]);
+                *reinterpret_cast<uint4*>(sm.t_hi + tile_at(rr, c)) = make_uint4(wh[0], wh[1], wh[2], wh[3]);
+                *reinterpret_cast<uint4*>(sm.t_lo + tile_at(rr, c)) = make_uint4(wl[0], wl[1], wl[2], wl[3]);
+            }
+        }
+        prep_sync();
+        float c[8][4];
+        auto clear = [&] {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) c[i][0] = c[i][1] = c[i][2] = c[i][3] = 0.f;
+        };
+        clear();
+        if (w >= 4) {
+            // P T: sixteen rows a warp
+            const int mt = w - 4;
+            const uint32_t pb[2] = {ptx::smem_u32(sm.p_hi), ptx::smem_u32(sm.p_lo)};
+            const uint32_t tb[2] = {ptx::smem_u32(sm.ts[0]), ptx::smem_u32(sm.ts[F32 ? 1 : 0])};
+#pragma unroll
+            for (int kt = 0; kt < 4; ++kt) {
+                if (kt > mt) break;  // P's columns up to its rows
+                uint32_t x[4], y[4], f[4], e[4];
+                ldsm(x, pb[0] + tile_at(mt * 16 + arow, kt * 2 + acol));
+                if (F32) ldsm(y, pb[1] + tile_at(mt * 16 + arow, kt * 2 + acol));
+#pragma unroll
+                for (int q = 0; q <= kt; ++q) {
+                    ldsm_t(f, tb[0] + tile_at(kt * 16 + arow, q * 2 + acol));
+                    mma(c[2 * q], x, f[0], f[1]);
+                    mma(c[2 * q + 1], x, f[2], f[3]);
+                    if (F32) {
+                        ldsm_t(e, tb[1] + tile_at(kt * 16 + arow, q * 2 + acol));
+                        mma(c[2 * q], y, f[0], f[1]);
+                        mma(c[2 * q + 1], y, f[2], f[3]);
+                        mma(c[2 * q], x, e[0], e[1]);
+                        mma(c[2 * q + 1], x, e[2], e[3]);
+                    }
+                }
+            }
+        } else if (t == 0) ptx::bulk_wait_read_all();  // [K; Q] is on its way: room for P T over q's rows
+        prep_sync();
+        if (w >= 4) store_tile(sm.kq + 8192, F32 ? sm.pt_lo : nullptr, (w - 4) * 16, c);
+        clear();
+        if (w * 16 < DK) {
+            // M^T: sixteen of dk's rows a warp, K'^T (exact) times T's high and low; row r of T meets columns s <= r
+            const uint32_t kb = ptx::smem_u32(sm.kq), th = ptx::smem_u32(sm.t_hi), tl = ptx::smem_u32(sm.t_lo);
+#pragma unroll
+            for (int kt = 0; kt < 4; ++kt) {
+                uint32_t x[4], f[4], e[4];
+                // left operand (dk, r) from rows r of k: transposed
+                ldsm_t(x, kb + kq_at(kt * 16 + brow, w * 2 + bcol));
+#pragma unroll
+                for (int q = 0; q <= kt; ++q) {
+                    ldsm_t(f, th + tile_at(kt * 16 + arow, q * 2 + acol));
+                    ldsm_t(e, tl + tile_at(kt * 16 + arow, q * 2 + acol));
+                    mma(c[2 * q], x, f[0], f[1]);
+                    mma(c[2 * q + 1], x, f[2], f[3]);
                     mma(c[2 * q], x, e[0], e[1]);
                     mma(c[2 * q + 1], x, e[2], e[3]);
                 }
             }
+            float mx = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                mx = fmaxf(mx, fmaxf(fmaxf(fabsf(c[i][0]), fabsf(c[i][1])), fmaxf(fabsf(c[i][2]), fabsf(c[i][3]))));
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            if (lane == 0) atomicMax(reinterpret_cast<int*>(&fac.top), __float_as_int(mx));  // >= 0: ordered as integers
         }
-    } else if (t == 0) ptx::bulk_wait_read_all();  // [K; Q] is on its way: room for P T over q's rows
-    prep_sync();
-    if (w >= 4) store_tile(sm.kq + 8192, F32 ? sm.pt_lo : nullptr, (w - 4) * 16, c);
-    clear();
-    if (w * 16 < DK) {
-        // M^T: sixteen of dk's rows a warp, K'^T (exact) times T's high and low; row r of T meets columns s <= r
-        const uint32_t kb = ptx::smem_u32(sm.kq), th = ptx::smem_u32(sm.t_hi), tl = ptx::smem_u32(sm.t_lo);
-#pragma unroll
-        for (int kt = 0; kt < 4; ++kt) {
-            uint32_t x[4], f[4], e[4];
-            // left operand (dk, r) from rows r of k: transposed
-            ldsm_t(x, kb + kq_at(kt * 16 + brow, w * 2 + bcol));
-#pragma unroll
-            for (int q = 0; q <= kt; ++q) {
-                ldsm_t(f, th + tile_at(kt * 16 + arow, q * 2 + acol));
-                ldsm_t(e, tl + tile_at(kt * 16 + arow, q * 2 + acol));
-                mma(c[2 * q], x, f[0], f[1]);
-                mma(c[2 * q + 1], x, f[2], f[3]);
-                mma(c[2 * q], x, e[0], e[1]);
-                mma(c[2 * q + 1], x, e[2], e[3]);
-            }
+        prep_sync();  // the tiles read above make room
+        if (w * 16 < DK) store_tile(sm.m[0], sm.m[1], w * 16, c);
+        ptx::fence_proxy_async_smem();
+        prep_sync();
+        if (t == 0) {
+            unsigned char* d = ws.v + ((long long)slot * a.Hv + h0 + j) * L::V;
+            ptx::bulk_s2g(d, sm.m, 2 * L::M);
+            ptx::bulk_s2g(d + 2 * L::M, sm.kq + 8192, 8192);
+            if (F32) ptx::bulk_s2g(d + 2 * L::M + 8192, sm.pt_lo, 8192);
+            ptx::bulk_s2g(d + 2 * L::M + L::PARTS * 8192, &fac, sizeof(Factors));
+            ptx::bulk_commit();
         }
     }
-    prep_sync();  // the tiles read above make room
-    if (w * 16 < DK) store_tile(sm.m[0], sm.m[1], w * 16, c);
-    ptx::fence_proxy_async_smem();
     if (wait.dead) flag_status(a.dev_status, KDA_DEV_TIMEOUT);
-    prep_sync();
-    if (t == 0) {
-        unsigned char* d = ws.v + ((long long)slot * a.Hv + h) * L::V;
-        ptx::bulk_s2g(d, sm.m, 2 * L::M);
-        ptx::bulk_s2g(d + 2 * L::M, sm.kq + 8192, 8192);
-        if (F32) ptx::bulk_s2g(d + 2 * L::M + 8192, sm.pt_lo, 8192);
-        ptx::bulk_s2g(d + 2 * L::M + L::PARTS * 8192, &sm.fac, sizeof(Factors));
-        ptx::bulk_commit();
-        ptx::bulk_wait_read_all();
-    }
+    if (t == 0) ptx::bulk_wait_read_all();
     if (w == 1) ptx::tmem_dealloc(tmem, 128);
 }
 
@@ -794,12 +833,16 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) gdn_chain_kernel(const GdnAr
                 asm volatile("bar.sync %0, 64;" ::"r"(pair + 1) : "memory");
                 return fmaxf(x, sm.top[which][half ^ 1][c]);
             };
-            float s[SK], mx = 0.f, g, ig, rd = 1.f, ru = 1.f;
+            // A bound on the column's values (the same in both halves): while it stays
+            // below 2^14 in S's scale, fp16 has room; the exact value now and then
+            // and where it does not.
+            float s[SK], mx = 0.f, bound, g, ig, rd = 1.f, ru = 1.f;
 #pragma unroll
             for (int i = 0; i < SK; ++i) s[i] = state[(size_t)i * DV];
 #pragma unroll
             for (int i = 0; i < SK; i += 2) mx = max3(mx, fabsf(s[i]), fabsf(s[i + 1]));
-            pow2_scale(both(1, mx), g, ig);
+            bound = both(1, mx);
+            pow2_scale(bound, g, ig);
 #pragma unroll
             for (int i = 0; i < SK; ++i) s[i] *= g;
             for (int m = 0; m < chunks; ++m) {
@@ -828,7 +871,7 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) gdn_chain_kernel(const GdnAr
                 if (n < C)  // the copies took the next sequence's rows along
 #pragma unroll
                     for (int i = 0; i < RK; ++i) r[i] = half * RK + i < n ? r[i] : 0.f;
-                const float last = fac.last, x = fac.x;
+                const float last = fac.last, x = fac.x, top = fac.top;
                 if (m > 0) wait(sm.o_full, m - 1);  // R's place is free
                 wait(sm.ks_full, m);
                 ptx::tc_fence_after();
@@ -851,6 +894,7 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) gdn_chain_kernel(const GdnAr
                     }
                 }
                 mx = both(0, mx);
+                const float ru_was = ru;
                 // fp16 has room for a stale scale; a new one where the largest value has left [2^-6, 2^10)
                 if (__any_sync(0xffffffffu, mx != 0.f && !(mx >= 0x1p-6f && mx < 0x1p10f))) {
                     float down, up;
@@ -877,9 +921,11 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) gdn_chain_kernel(const GdnAr
 #pragma unroll
                 for (int i = 0; i < SK; ++i) s[i] *= last;
                 const float fs = (ru * x) * g;
+                bound = last * bound + (float)C * top * x * (mx * ru_was);
+                const bool exact = __any_sync(0xffffffffu, !(bound * g < 0x1p14f) || (bound != 0.f && bound * g < 0x1p-6f)) ||
+                                   (m & 15) == 15;
                 wait(sm.su_full, m);
                 ptx::tc_fence_after();
-                mx = 0.f;
                 constexpr int W = SK < 32 ? SK : 32;
 #pragma unroll
                 for (int q = 0; q < SK; q += W) {
@@ -887,16 +933,15 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) gdn_chain_kernel(const GdnAr
                     if constexpr (W == 32) ptx::tmem_ld32(at + TM_X + half * SK + q, d);
                     else ptx::tmem_ld16(at + TM_X + half * SK + q, d);
 #pragma unroll
-                    for (int i = 0; i < W; i += 2) {
-                        s[q + i] = fmaf(fs, d[i], s[q + i]);
-                        s[q + i + 1] = fmaf(fs, d[i + 1], s[q + i + 1]);
-                        mx = max3(mx, fabsf(s[q + i]), fabsf(s[q + i + 1]));
-                    }
+                    for (int i = 0; i < W; ++i) s[q + i] = fmaf(fs, d[i], s[q + i]);
                 }
-                mx = both(1, mx);
-                if (__any_sync(0xffffffffu, mx != 0.f && !(mx >= 0x1p-6f && mx < 0x1p10f))) {
+                if (exact) {
+                    mx = 0.f;
+#pragma unroll
+                    for (int i = 0; i < SK; i += 2) mx = max3(mx, fabsf(s[i]), fabsf(s[i + 1]));
+                    bound = both(1, mx) * ig;
                     float down, up;
-                    pow2_scale(mx * ig, down, up);
+                    pow2_scale(bound, down, up);
                     const float f = down * ig;
 #pragma unroll
                     for (int i = 0; i < SK; ++i) s[i] *= f;
@@ -1109,20 +1154,27 @@ cudaError_t launch_chain(const GdnArgs& a, const CUtensorMap& vmap, const Work& 
     return cudaGetLastError();
 }
 
-template <int DK, bool F32> cudaError_t launch(const GdnArgs& a, int dv, cudaStream_t st)
+template <int DK, bool F32, int HEADS>
+cudaError_t launch_prep(const GdnArgs& a, const RowMaps& maps, const Work& ws, long long slots, cudaStream_t st)
 {
-    using S = PrepSmem<DK, F32>;
-    using L = Slot<DK, F32>;
+    using S = PrepSmem<DK, F32, HEADS>;
     constexpr int smem = sizeof(S);
     static_assert(offsetof(S, t_hi) % 128 == 0 && offsetof(S, fac) % 16 == 0 && offsetof(S, m) % 16 == 0 &&
-                  offsetof(S, xd) % 16 == 0 && offsetof(S, gh) % 16 == 0 &&
-                  offsetof(S, gl) % 16 == 0 && offsetof(S, colk) % 16 == 0 && offsetof(S, down) % 16 == 0 &&
-                  offsetof(S, loaded) % 8 == 0, "alignment");
+                  offsetof(S, xd) % 16 == 0 && offsetof(S, gates) % 16 == 0 && offsetof(S, colk) % 16 == 0 &&
+                  offsetof(S, down) % 16 == 0 && offsetof(S, loaded) % 8 == 0, "alignment");
+    static_assert((smem + 1024) * prep_ctas<F32>() <= 228 * 1024, "shared memory");
     static PerDeviceOnce once;
-    cudaError_t e = once.run([](int) {
-        return cudaFuncSetAttribute(gdn_prep_kernel<DK, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = once.run([](int) {
+        return cudaFuncSetAttribute(gdn_prep_kernel<DK, F32, HEADS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     });
     if (e != cudaSuccess) return e;
+    gdn_prep_kernel<DK, F32, HEADS><<<(unsigned)(slots * (a.Hv / HEADS)), PREP, smem, st>>>(a, maps, ws);
+    return cudaGetLastError();
+}
+
+template <int DK, bool F32> cudaError_t launch(const GdnArgs& a, int dv, cudaStream_t st)
+{
+    using L = Slot<DK, F32>;
     RowMaps maps;
     if (!encode_rows(&maps.q, a.q, (long long)a.Hk * DK, a.qs, a.T, 64, true) ||
         !encode_rows(&maps.k, a.k, (long long)a.Hk * DK, a.ks, a.T, 64, true) ||
@@ -1132,8 +1184,9 @@ template <int DK, bool F32> cudaError_t launch(const GdnArgs& a, int dv, cudaStr
     Work ws;
     ws.kq = static_cast<unsigned char*>(a.workspace);
     ws.v = ws.kq + slots * a.Hk * L::KQ;
-    gdn_prep_kernel<DK, F32><<<(unsigned)(slots * a.Hv), PREP, smem, st>>>(a, maps, ws);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    const cudaError_t e = a.Hv / a.Hk % 2 == 0 ? launch_prep<DK, F32, 2>(a, maps, ws, slots, st)
+                                               : launch_prep<DK, F32, 1>(a, maps, ws, slots, st);
+    if (e != cudaSuccess) return e;
     if (dv == 128) return launch_chain<DK, 128, F32>(a, maps.v, ws, st);
     if (dv == 64) return launch_chain<DK, 64, F32>(a, maps.v, ws, st);
     return launch_chain<DK, 32, F32>(a, maps.v, ws, st);
