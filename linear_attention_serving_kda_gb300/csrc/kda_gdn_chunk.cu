@@ -67,6 +67,29 @@ __device__ __forceinline__ void stsm(uint32_t addr, const uint32_t (&r)[4])
                  "r"(r[2]), "r"(r[3])
                  : "memory");
 }
+// two fp32 operations an instruction
+__device__ __forceinline__ unsigned long long as_u64(float2 x) { return *reinterpret_cast<unsigned long long*>(&x); }
+__device__ __forceinline__ float2 as_f2(unsigned long long x) { return *reinterpret_cast<float2*>(&x); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    unsigned long long r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(as_u64(a)), "l"(as_u64(b)));
+    return as_f2(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(as_u64(a)), "l"(as_u64(b)));
+    return as_f2(r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(as_u64(a)), "l"(as_u64(b)), "l"(as_u64(c)));
+    return as_f2(r);
+}
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) { return fma2(b, make_float2(-1.f, -1.f), a); }
+__device__ __forceinline__ float2 both2(float x) { return make_float2(x, x); }
 __device__ __forceinline__ uint32_t pack_h(float x, float y)
 {
     const __half2 h = __floats2half2_rn(x, y);
@@ -77,8 +100,8 @@ __device__ __forceinline__ float2 unpack_h(uint32_t u) { return __half22float2(*
 __device__ __forceinline__ void split_h(float x, float y, uint32_t& hi, uint32_t& lo)
 {
     hi = pack_h(x, y);
-    const float2 f = unpack_h(hi);
-    lo = pack_h(x - f.x, y - f.y);
+    const float2 d = sub2(make_float2(x, y), unpack_h(hi));
+    lo = pack_h(d.x, d.y);
 }
 __device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
@@ -138,8 +161,8 @@ struct Factors {
     float beta[C], ek[C];  // beta; beta e^G and k's row factor
     float e1[C], e2[C];    // scale, q's row factor, e^G (e1)
     float last, x;         // e^{G_C}; what M and P T still have to be multiplied by
-    float top;             // M's largest value
-    float pad[29];
+    float top, ektop;      // the largest values of M and ek
+    float pad[28];
 };
 template <int DK, bool F32> struct Slot {
     static constexpr int HALVES = DK <= 64 ? 1 : DK / 64;  // 64-wide tiles a row spans (dk = 32: half of one)
@@ -171,12 +194,9 @@ template <int DK, bool F32, int HEADS> struct PrepSmem {
     unsigned char kq[L::KQ];  // bf16 rows of k, then q; fp16 later; P T over q's
     union {
         struct {  // 64 x 64 fp16 tiles
-            unsigned char t_hi[8192], t_lo[8192];  // T; then diag(e^{G_C - G}) Ts
-            union {
-                unsigned char ts[PARTS][8192];  // Ts = diag(k's row factors / x) T
-                alignas(16) float xd[C * XS];   // before: A's diagonal blocks, 16 x 16 each
-            };
+            unsigned char t_hi[8192], t_lo[8192];  // T; then with the rows' factors of M
             unsigned char p_hi[8192], p_lo[F32 ? 8192 : 128];
+            alignas(16) float xd[C * XS];          // A's diagonal blocks, 16 x 16 each
         };
         unsigned char m[2][L::M];  // then M^T
     };
@@ -186,7 +206,7 @@ template <int DK, bool F32, int HEADS> struct PrepSmem {
         alignas(16) float eg[C], gh[C], gl[C], w[C];  // e^G, G / ln 2 in two words, e^{G_C - G}
     } gates[HEADS];
     alignas(16) float norm[2 * C];  // squared norms of k's and q's rows
-    alignas(16) float row[2 * C], colk[C], down[2 * C], sk[C];  // factors of A's and P's rows, of A's columns; of the stored rows
+    alignas(16) float row[2 * C], col[2][C], down[2 * C], fm[C];  // factors of A's and P's rows, of their columns; of the stored rows; of M's
     uint64_t loaded, prod;
     uint32_t tmem;
 };
@@ -420,7 +440,7 @@ gdn_prep_kernel(const GdnArgs a, const __grid_constant__ RowMaps maps, const Wor
             }
         sm.fac[gate_head].beta[2 * lane] = bt[0];
         sm.fac[gate_head].beta[2 * lane + 1] = bt[1];
-        if (lane == 0) sm.fac[gate_head].top = 0.f;
+        if (lane == 0) sm.fac[gate_head].top = sm.fac[gate_head].ektop = 0.f;
         scan_rows(sm.gates[gate_head], make_float2(g[0], g[1]), sm.fac[gate_head].last, lane);
     }
     // a row of [K; Q] a lane (w & 3), against half of k's rows (w >> 2); the
@@ -462,21 +482,32 @@ gdn_prep_kernel(const GdnArgs a, const __grid_constant__ RowMaps maps, const Wor
         Factors& fac = sm.fac[j];
         if (w < 4) {
             const float ss = sm.norm[lr];
-            float down, up;
+            float down, up, x = 1.f, xi = 1.f;
             pow2_scale_sqrt(ss, down, up);
+            if (!a.l2) {
+                // k's row factors may be far from one: a power of two out of all of them
+                float mx = fmaxf(sm.norm[lane], sm.norm[lane + 32]);
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                pow2_scale_sqrt(mx, xi, x);
+            }
             // the factor that makes the stored row the (normalised) row; none for a padded one
             const float nrm = r < n ? (a.l2 ? rsqrtf(ss + a.l2_eps) : 1.f) : 0.f, f = nrm * up;
             sm.down[lr] = down;
             if (type == 0) {
                 const float be = fac.beta[r];
-                sm.sk[r] = f;
-                fac.ek[r] = be * f * gt.eg[r];
-                sm.colk[r] = nrm;  // A comes from the raw rows' products
+                const float ek = be * f * gt.eg[r];
+                fac.ek[r] = ek;
+                atomicMax(reinterpret_cast<int*>(&fac.ektop), __float_as_int(fabsf(ek)));  // >= 0: ordered as integers
+                sm.fm[r] = (f * xi) * gt.w[r];
+                sm.col[0][r] = nrm;               // A comes from the raw rows' products,
+                sm.col[1][r] = down * (f * xi);   // P is that of the stored rows, times what T's rows get
                 sm.row[r] = be * nrm;
+                if (t == 0) fac.x = x;
             } else {
                 fac.e1[r] = a.scale * f * gt.eg[r];
                 fac.e2[r] = a.scale * f;
-                sm.row[lr] = down;  // P is that of the stored rows
+                sm.row[lr] = down;
             }
         }
         if (j > 0 && t == 0) ptx::bulk_wait_read_all();  // the head before this one has left the tiles
@@ -484,7 +515,7 @@ gdn_prep_kernel(const GdnArgs a, const __grid_constant__ RowMaps maps, const Wor
         if (w != 4 && w != 6) {
             // the lane's row of A (beta_r |..| e^{G_r - G_s} k_r.k_s) or P, zero from the diagonal (or past it) on
             const float rh = gt.gh[r], rl = gt.gl[r], rf = sm.row[lr];
-            const float* cf = type == 0 ? sm.colk : sm.down;
+            const float* cf = sm.col[type];
             const int lim = r < n ? r + type : 0;
             unsigned char* hi_tile = type == 0 ? sm.t_hi : sm.p_hi;
             unsigned char* lo_tile = type == 0 ? sm.t_lo : sm.p_lo;
@@ -494,17 +525,16 @@ gdn_prep_kernel(const GdnArgs a, const __grid_constant__ RowMaps maps, const Wor
                 float v[8], d[8];
                 ptx::tmem_ld8(at + s0 + p * 8, d);
 #pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                    const int s = s0 + p * 8 + z * 4;
-                    const float4 ch = *reinterpret_cast<const float4*>(&gt.gh[s]);
-                    const float4 cl = *reinterpret_cast<const float4*>(&gt.gl[s]);
-                    const float4 c4 = *reinterpret_cast<const float4*>(&cf[s]);
-                    const float h4[4] = {ch.x, ch.y, ch.z, ch.w}, l4[4] = {cl.x, cl.y, cl.z, cl.w}, f4[4] = {c4.x, c4.y, c4.z, c4.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float e = exp2_sfu((rh - h4[i]) + (rl - l4[i]));
-                        v[z * 4 + i] = s + i < lim ? (rf * f4[i]) * e * d[z * 4 + i] : 0.f;
-                    }
+                for (int z = 0; z < 4; ++z) {
+                    const int s = s0 + p * 8 + z * 2;
+                    const float2 ch = *reinterpret_cast<const float2*>(&gt.gh[s]);
+                    const float2 cl = *reinterpret_cast<const float2*>(&gt.gl[s]);
+                    const float2 c2 = *reinterpret_cast<const float2*>(&cf[s]);
+                    const float2 e = add2(sub2(both2(rh), ch), sub2(both2(rl), cl));
+                    const float2 x = mul2(mul2(mul2(both2(rf), c2), make_float2(exp2_sfu(e.x), exp2_sfu(e.y))),
+                                          make_float2(d[2 * z], d[2 * z + 1]));
+                    v[2 * z] = s < lim ? x.x : 0.f;
+                    v[2 * z + 1] = s + 1 < lim ? x.y : 0.f;
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) split_h(v[2 * i], v[2 * i + 1], hi[i], lo[i]);
@@ -527,14 +557,6 @@ gdn_prep_kernel(const GdnArgs a, const __grid_constant__ RowMaps maps, const Wor
                 wait(sm.loaded, 0);
                 convert_row<DK>(sm.kq, row, sm.down[row], (row & (C - 1)) < n);
                 ptx::fence_proxy_async_smem();
-            }
-            if (w == 7) {
-                float mx = fmaxf(sm.sk[lane], sm.sk[lane + 32]);
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                float down, up;
-                pow2_scale(mx, down, up);
-                if (lane == 0) fac.x = up;
             }
         } else {
             {
@@ -586,31 +608,6 @@ gdn_prep_kernel(const GdnArgs a, const __grid_constant__ RowMaps maps, const Wor
             ptx::bulk_s2g(ws.kq + ((long long)slot * a.Hk + hk) * L::KQ, sm.kq, L::KQ);
             ptx::bulk_commit();
         }
-        {
-            // Ts, and T times the decays to the chunk's end, sixteen values of a row a thread; zero above the diagonal
-            const int rr = t >> 2, c0 = (t & 3) * 2;
-            const float f = sm.sk[rr] / fac.x, fw = f * gt.w[rr];
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-                const int c = c0 + z;
-                const uint4 h4 = *reinterpret_cast<const uint4*>(sm.t_hi + tile_at(rr, c));
-                const uint4 l4 = *reinterpret_cast<const uint4*>(sm.t_lo + tile_at(rr, c));
-                const uint32_t hv[4] = {h4.x, h4.y, h4.z, h4.w}, lv[4] = {l4.x, l4.y, l4.z, l4.w};
-                uint32_t sh[4], sl[4], wh[4], wl[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 x = unpack_h(hv[i]), y = unpack_h(lv[i]);
-                    const float u0 = c * 8 + 2 * i <= rr ? x.x + y.x : 0.f, u1 = c * 8 + 2 * i + 1 <= rr ? x.y + y.y : 0.f;
-                    split_h(u0 * f, u1 * f, sh[i], sl[i]);
-                    split_h(u0 * fw, u1 * fw, wh[i], wl[i]);
-                }
-                *reinterpret_cast<uint4*>(sm.ts[0] + tile_at(rr, c)) = make_uint4(sh[0], sh[1], sh[2], sh[3]);
-                if (F32) *reinterpret_cast<uint4*>(sm.ts[F32 ? 1 : 0] + tile_at(rr, c)) = make_uint4(sl[0], sl[1], sl[2], sl[3]);
-                *reinterpret_cast<uint4*>(sm.t_hi + tile_at(rr, c)) = make_uint4(wh[0], wh[1], wh[2], wh[3]);
-                *reinterpret_cast<uint4*>(sm.t_lo + tile_at(rr, c)) = make_uint4(wl[0], wl[1], wl[2], wl[3]);
-            }
-        }
-        prep_sync();
         float c[8][4];
         auto clear = [&] {
 #pragma unroll
@@ -618,10 +615,10 @@ gdn_prep_kernel(const GdnArgs a, const __grid_constant__ RowMaps maps, const Wor
         };
         clear();
         if (w >= 4) {
-            // P T: sixteen rows a warp
+            // P T (k's row factors are in P's columns): sixteen rows a warp
             const int mt = w - 4;
             const uint32_t pb[2] = {ptx::smem_u32(sm.p_hi), ptx::smem_u32(sm.p_lo)};
-            const uint32_t tb[2] = {ptx::smem_u32(sm.ts[0]), ptx::smem_u32(sm.ts[F32 ? 1 : 0])};
+            const uint32_t tb[2] = {ptx::smem_u32(sm.t_hi), ptx::smem_u32(sm.t_lo)};
 #pragma unroll
             for (int kt = 0; kt < 4; ++kt) {
                 if (kt > mt) break;  // P's columns up to its rows
@@ -645,6 +642,26 @@ gdn_prep_kernel(const GdnArgs a, const __grid_constant__ RowMaps maps, const Wor
         } else if (t == 0) ptx::bulk_wait_read_all();  // [K; Q] is on its way: room for P T over q's rows
         prep_sync();
         if (w >= 4) store_tile(sm.kq + 8192, F32 ? sm.pt_lo : nullptr, (w - 4) * 16, c);
+        // T with M's row factors, in pieces of eight values up to each diagonal block's end: 32 + 64 + 96 + 128
+#pragma unroll 1
+        for (int i = t; i < 320; i += PREP) {
+            const int kt = i < 32 ? 0 : i < 96 ? 1 : i < 192 ? 2 : 3, l = i - 16 * kt * (kt + 1);
+            const int rr = kt * 16 + l / (2 * kt + 2), pc = l % (2 * kt + 2);
+            const float f = sm.fm[rr];
+            uint4* hp = reinterpret_cast<uint4*>(sm.t_hi + tile_at(rr, pc));
+            uint4* lp = reinterpret_cast<uint4*>(sm.t_lo + tile_at(rr, pc));
+            const uint4 h4 = *hp, l4 = *lp;
+            const uint32_t hv[4] = {h4.x, h4.y, h4.z, h4.w}, lv[4] = {l4.x, l4.y, l4.z, l4.w};
+            uint32_t wh[4], wl[4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+                const float2 x = mul2(add2(unpack_h(hv[z]), unpack_h(lv[z])), both2(f));
+                split_h(x.x, x.y, wh[z], wl[z]);
+            }
+            *hp = make_uint4(wh[0], wh[1], wh[2], wh[3]);
+            *lp = make_uint4(wl[0], wl[1], wl[2], wl[3]);
+        }
+        prep_sync();
         clear();
         if (w * 16 < DK) {
             // M^T: sixteen of dk's rows a warp, K'^T (exact) times T's high and low; row r of T meets columns s <= r
@@ -670,7 +687,7 @@ gdn_prep_kernel(const GdnArgs a, const __grid_constant__ RowMaps maps, const Wor
                 mx = fmaxf(mx, fmaxf(fmaxf(fabsf(c[i][0]), fabsf(c[i][1])), fmaxf(fabsf(c[i][2]), fabsf(c[i][3]))));
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            if (lane == 0) atomicMax(reinterpret_cast<int*>(&fac.top), __float_as_int(mx));  // >= 0: ordered as integers
+            if (lane == 0) atomicMax(reinterpret_cast<int*>(&fac.top), __float_as_int(mx));
         }
         prep_sync();  // the tiles read above make room
         if (w * 16 < DK) store_tile(sm.m[0], sm.m[1], w * 16, c);
@@ -705,17 +722,17 @@ template <int DK, int DV, bool F32> struct ChainSmem {
     unsigned char v[2][C * DV * 2];                     // dense rows
     Factors fac[4];
     float f1[2][DV], f2[2][DV];  // the scales of S's and R's columns
-    float top[2][2][DV];         // the largest values of R's and S's halves of a column
+    float top[3][2][DV];         // the largest values of beta V's, R's and S's halves of a column
     uint64_t loaded[2], freed[2];
-    uint64_t sh_full, sl_full, ks_full, qs_full, rh_full, rl_full, su_full, o_full, o_free, f_full[2];
+    uint64_t s_full, ks_full, qs_full, rh_full, rl_full, su_full, o_full, o_free, f_full[2];
     uint32_t tmem;
     int found;
 };
 
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(a, fmaxf(b, c)); }
 
-// Values two by two as fp16 high parts, N / 2 columns; and what those leave, as
-// low parts (the products with the high ones run meanwhile).
+// Values two by two as fp16 high parts and what those leave as low parts, N / 2
+// columns each.
 template <int N> __device__ __forceinline__ void store_pairs(uint32_t at, const uint32_t (&v)[N])
 {
     static_assert(N == 8 || N % 16 == 0, "columns");
@@ -728,7 +745,15 @@ template <int N> __device__ __forceinline__ void store_pairs(uint32_t at, const 
             for (int i = 0; i < 16; ++i) w[i] = v[b + i];
             ptx::tmem_st16_async(at + b, w);
         }
-        ptx::tmem_wait_st();
+    }
+}
+template <int N> __device__ __forceinline__ void scale_all(float (&x)[N], float f)
+{
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+        const float2 y = mul2(make_float2(x[i], x[i + 1]), both2(f));
+        x[i] = y.x;
+        x[i + 1] = y.y;
     }
 }
 template <int N> __device__ __forceinline__ void store_high(uint32_t at, const float (&x)[N])
@@ -737,16 +762,31 @@ template <int N> __device__ __forceinline__ void store_high(uint32_t at, const f
 #pragma unroll
     for (int i = 0; i < N / 2; ++i) v[i] = pack_h(x[2 * i], x[2 * i + 1]);
     store_pairs(at, v);
+    ptx::tmem_wait_st();
 }
 template <int N> __device__ __forceinline__ void store_low(uint32_t at, const float (&x)[N])
 {
     uint32_t v[N / 2];
 #pragma unroll
     for (int i = 0; i < N / 2; ++i) {
-        const float2 h = unpack_h(pack_h(x[2 * i], x[2 * i + 1]));
-        v[i] = pack_h(x[2 * i] - h.x, x[2 * i + 1] - h.y);
+        uint32_t hi;
+        split_h(x[2 * i], x[2 * i + 1], hi, v[i]);
     }
     store_pairs(at, v);
+    ptx::tmem_wait_st();
+}
+template <int N> __device__ __forceinline__ void store_split(uint32_t hi_at, uint32_t lo_at, const float (&x)[N])
+{
+    constexpr int B = N < 32 ? N : 32;
+#pragma unroll
+    for (int b = 0; b < N; b += B) {
+        uint32_t hi[B / 2], lo[B / 2];
+#pragma unroll
+        for (int i = 0; i < B / 2; ++i) split_h(x[b + 2 * i], x[b + 2 * i + 1], hi[i], lo[i]);
+        store_pairs(hi_at + b / 2, hi);
+        store_pairs(lo_at + b / 2, lo);
+    }
+    ptx::tmem_wait_st();
 }
 
 // The sequence of rank `rank` by length, longest first (ties: lowest index):
@@ -798,8 +838,7 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) gdn_chain_kernel(const GdnAr
             ptx::mbar_init(&sm.freed[i], 2 * NW + 1);
             ptx::mbar_init(&sm.f_full[i], NW);
         }
-        ptx::mbar_init(&sm.sh_full, 2 * NW);
-        ptx::mbar_init(&sm.sl_full, 2 * NW);
+        ptx::mbar_init(&sm.s_full, 2 * NW);
         ptx::mbar_init(&sm.ks_full, 2);
         ptx::mbar_init(&sm.qs_full, 1);
         ptx::mbar_init(&sm.rh_full, 2 * NW);
@@ -836,24 +875,21 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) gdn_chain_kernel(const GdnAr
             // A bound on the column's values (the same in both halves): while it stays
             // below 2^14 in S's scale, fp16 has room; the exact value now and then
             // and where it does not.
-            float s[SK], mx = 0.f, bound, g, ig, rd = 1.f, ru = 1.f;
+            float s[SK], mx = 0.f, bound, g, ig;
 #pragma unroll
             for (int i = 0; i < SK; ++i) s[i] = state[(size_t)i * DV];
 #pragma unroll
             for (int i = 0; i < SK; i += 2) mx = max3(mx, fabsf(s[i]), fabsf(s[i + 1]));
-            bound = both(1, mx);
+            bound = both(2, mx);
             pow2_scale(bound, g, ig);
 #pragma unroll
             for (int i = 0; i < SK; ++i) s[i] *= g;
             for (int m = 0; m < chunks; ++m) {
                 const int b = m & 1, n = end - begin - m * C;
                 if (m > 0) wait(sm.qs_full, m - 1);  // S's place is free
-                store_high<SK>(at + TM_SH + half * (SK / 2), s);
+                store_split<SK>(at + TM_SH + half * (SK / 2), at + TM_SL + half * (SK / 2), s);
                 ptx::tc_fence_before();
-                warp_arrive(sm.sh_full, lane);
-                store_low<SK>(at + TM_SL + half * (SK / 2), s);
-                ptx::tc_fence_before();
-                warp_arrive(sm.sl_full, lane);
+                warp_arrive(sm.s_full, lane);
 
                 // R = beta V - beta e^G k.S, times rd
                 wait(sm.loaded[b], m >> 1);
@@ -861,49 +897,43 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) gdn_chain_kernel(const GdnAr
                 const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(sm.v[b]) + half * RK * DV + c;
                 float r[RK];
 #pragma unroll
-                for (int i = 0; i < RK; i += 4) {
-                    const float4 be = *reinterpret_cast<const float4*>(&fac.beta[half * RK + i]);
-                    r[i] = be.x * (__bfloat162float(v[i * DV]) * rd);
-                    r[i + 1] = be.y * (__bfloat162float(v[(i + 1) * DV]) * rd);
-                    r[i + 2] = be.z * (__bfloat162float(v[(i + 2) * DV]) * rd);
-                    r[i + 3] = be.w * (__bfloat162float(v[(i + 3) * DV]) * rd);
+                for (int i = 0; i < RK; i += 2) {
+                    const float2 be = *reinterpret_cast<const float2*>(&fac.beta[half * RK + i]);
+                    const float2 x = mul2(be, make_float2(__bfloat162float(v[i * DV]), __bfloat162float(v[(i + 1) * DV])));
+                    r[i] = x.x;
+                    r[i + 1] = x.y;
                 }
                 if (n < C)  // the copies took the next sequence's rows along
 #pragma unroll
                     for (int i = 0; i < RK; ++i) r[i] = half * RK + i < n ? r[i] : 0.f;
+                mx = 0.f;
+#pragma unroll
+                for (int i = 0; i < RK; i += 2) mx = max3(mx, fabsf(r[i]), fabsf(r[i + 1]));
+                // |k'| < 2, so |k'.S| <= 2 sqrt(dk) max |S|: R stays below 2^14 in the scale of this
+                // bound, and low parts do not mind how far below
+                float rd, ru;
+                pow2_scale(both(0, mx) + fac.ektop * (DK == 128 ? 23.f : DK == 64 ? 16.f : 12.f) * bound, rd, ru);
+                rd *= 0x1p13f;
+                ru *= 0x1p-13f;
+                scale_all(r, rd);
                 const float last = fac.last, x = fac.x, top = fac.top;
                 if (m > 0) wait(sm.o_full, m - 1);  // R's place is free
                 wait(sm.ks_full, m);
                 ptx::tc_fence_after();
                 const float fr = ig * rd;
-                mx = 0.f;
 #pragma unroll
                 for (int q = 0; q < RK; q += 16) {
                     float d[16], e[16];
                     ptx::tmem_ld16(at + TM_X + half * RK + q, d);
                     ptx::tmem_ld16(at + TM_X + C + half * RK + q, e);
 #pragma unroll
-                    for (int i = 0; i < 16; i += 4) {
-                        const float4 ek = *reinterpret_cast<const float4*>(&fac.ek[half * RK + q + i]);
-                        float* x = &r[q + i];
-                        x[0] = fmaf(-ek.x, (d[i] + e[i]) * fr, x[0]);
-                        x[1] = fmaf(-ek.y, (d[i + 1] + e[i + 1]) * fr, x[1]);
-                        x[2] = fmaf(-ek.z, (d[i + 2] + e[i + 2]) * fr, x[2]);
-                        x[3] = fmaf(-ek.w, (d[i + 3] + e[i + 3]) * fr, x[3]);
-                        mx = max3(mx, max3(fabsf(x[0]), fabsf(x[1]), fabsf(x[2])), fabsf(x[3]));
+                    for (int i = 0; i < 16; i += 2) {
+                        const float2 ek = *reinterpret_cast<const float2*>(&fac.ek[half * RK + q + i]);
+                        const float2 ks = mul2(add2(make_float2(d[i], d[i + 1]), make_float2(e[i], e[i + 1])), both2(-fr));
+                        const float2 x = fma2(ek, ks, make_float2(r[q + i], r[q + i + 1]));
+                        r[q + i] = x.x;
+                        r[q + i + 1] = x.y;
                     }
-                }
-                mx = both(0, mx);
-                const float ru_was = ru;
-                // fp16 has room for a stale scale; a new one where the largest value has left [2^-6, 2^10)
-                if (__any_sync(0xffffffffu, mx != 0.f && !(mx >= 0x1p-6f && mx < 0x1p10f))) {
-                    float down, up;
-                    pow2_scale(mx * ru, down, up);
-                    const float f = down * ru;
-#pragma unroll
-                    for (int i = 0; i < RK; ++i) r[i] *= f;
-                    rd = down;
-                    ru = up;
                 }
                 store_high<RK>(at + TM_RH + half * (RK / 2), r);
                 ptx::tc_fence_before();
@@ -918,10 +948,12 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) gdn_chain_kernel(const GdnAr
                 }
 
                 // S = e^{G_C} S + M^T R
-#pragma unroll
-                for (int i = 0; i < SK; ++i) s[i] *= last;
+                scale_all(s, last);
                 const float fs = (ru * x) * g;
-                bound = last * bound + (float)C * top * x * (mx * ru_was);
+                mx = 0.f;
+#pragma unroll
+                for (int i = 0; i < RK; i += 2) mx = max3(mx, fabsf(r[i]), fabsf(r[i + 1]));
+                bound = last * bound + (float)C * top * x * (both(1, mx) * ru);
                 const bool exact = __any_sync(0xffffffffu, !(bound * g < 0x1p14f) || (bound != 0.f && bound * g < 0x1p-6f)) ||
                                    (m & 15) == 15;
                 wait(sm.su_full, m);
@@ -933,18 +965,21 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) gdn_chain_kernel(const GdnAr
                     if constexpr (W == 32) ptx::tmem_ld32(at + TM_X + half * SK + q, d);
                     else ptx::tmem_ld16(at + TM_X + half * SK + q, d);
 #pragma unroll
-                    for (int i = 0; i < W; ++i) s[q + i] = fmaf(fs, d[i], s[q + i]);
+                    for (int i = 0; i < W; i += 2) {
+                        const float2 x = fma2(both2(fs), make_float2(d[i], d[i + 1]), make_float2(s[q + i], s[q + i + 1]));
+                        s[q + i] = x.x;
+                        s[q + i + 1] = x.y;
+                    }
                 }
                 if (exact) {
                     mx = 0.f;
 #pragma unroll
                     for (int i = 0; i < SK; i += 2) mx = max3(mx, fabsf(s[i]), fabsf(s[i + 1]));
-                    bound = both(1, mx) * ig;
+                    bound = both(2, mx) * ig;
                     float down, up;
                     pow2_scale(bound, down, up);
                     const float f = down * ig;
-#pragma unroll
-                    for (int i = 0; i < SK; ++i) s[i] *= f;
+                    scale_all(s, f);
                     g = down;
                     ig = up;
                 }
@@ -983,7 +1018,7 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) gdn_chain_kernel(const GdnAr
             for (int m = 0; m < chunks; ++m) {
                 const int b = m & 1;
                 wait(sm.loaded[b], m >> 1);
-                wait(first ? sm.sh_full : sm.sl_full, m);
+                wait(sm.s_full, m);
                 ptx::tc_fence_after();
                 const uint64_t k = ptx::desc_sw128(ptx::smem_u32(sm.kq[b]));
                 const uint64_t mh = ptx::desc_sw128(ptx::smem_u32(sm.work[b])), ml = mh + (L::M >> 4);
@@ -1017,13 +1052,12 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) gdn_chain_kernel(const GdnAr
                 __syncwarp();
             }
         } else {
-            // the outputs' products
+            // the outputs' products, each behind the critical ones of its kind
             for (int m = 0; m < chunks; ++m) {
                 const int b = m & 1;
-                wait(sm.loaded[b], m >> 1);
-                wait(sm.sh_full, m);
-                if (F32) wait(sm.sl_full, m);
                 if (m > 0) wait(sm.o_free, m - 1);
+                wait(sm.loaded[b], m >> 1);
+                wait(sm.ks_full, m);
                 ptx::tc_fence_after();
                 const uint64_t q = ptx::desc_sw128(ptx::smem_u32(sm.kq[b]) + 8192);
                 const uint64_t pt = ptx::desc_sw128(ptx::smem_u32(sm.work[b]) + 2 * L::M);
@@ -1038,8 +1072,7 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) gdn_chain_kernel(const GdnAr
                     ptx::mma_commit(&sm.qs_full);
                 }
                 __syncwarp();
-                wait(sm.rh_full, m);
-                if (F32) wait(sm.rl_full, m);
+                wait(sm.su_full, m);
                 ptx::tc_fence_after();
                 if (lane == 0) {
 #pragma unroll
@@ -1083,13 +1116,13 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) gdn_chain_kernel(const GdnAr
                         warp_arrive(sm.o_free, lane);
                     }
 #pragma unroll
-                    for (int i = 0; i < 16; i += 4) {
-                        const float4 e1 = *reinterpret_cast<const float4*>(&fac.e1[i0 + i]);
-                        const float4 e2 = *reinterpret_cast<const float4*>(&fac.e2[i0 + i]);
-                        x[i] = fmaf(e1.x, f1 * x[i], e2.x * (f2 * y[i]));
-                        x[i + 1] = fmaf(e1.y, f1 * x[i + 1], e2.y * (f2 * y[i + 1]));
-                        x[i + 2] = fmaf(e1.z, f1 * x[i + 2], e2.z * (f2 * y[i + 2]));
-                        x[i + 3] = fmaf(e1.w, f1 * x[i + 3], e2.w * (f2 * y[i + 3]));
+                    for (int i = 0; i < 16; i += 2) {
+                        const float2 e1 = *reinterpret_cast<const float2*>(&fac.e1[i0 + i]);
+                        const float2 e2 = *reinterpret_cast<const float2*>(&fac.e2[i0 + i]);
+                        const float2 o = fma2(e1, mul2(both2(f1), make_float2(x[i], x[i + 1])),
+                                              mul2(e2, mul2(both2(f2), make_float2(y[i], y[i + 1]))));
+                        x[i] = o.x;
+                        x[i + 1] = o.y;
                     }
                     if constexpr (F32) {
                         float* p = static_cast<float*>(a.out) + o0 + c + i0 * row_stride;
@@ -1160,7 +1193,7 @@ cudaError_t launch_prep(const GdnArgs& a, const RowMaps& maps, const Work& ws, l
     using S = PrepSmem<DK, F32, HEADS>;
     constexpr int smem = sizeof(S);
     static_assert(offsetof(S, t_hi) % 128 == 0 && offsetof(S, fac) % 16 == 0 && offsetof(S, m) % 16 == 0 &&
-                  offsetof(S, xd) % 16 == 0 && offsetof(S, gates) % 16 == 0 && offsetof(S, colk) % 16 == 0 &&
+                  offsetof(S, xd) % 16 == 0 && offsetof(S, gates) % 16 == 0 && offsetof(S, col) % 16 == 0 &&
                   offsetof(S, down) % 16 == 0 && offsetof(S, loaded) % 8 == 0, "alignment");
     static_assert((smem + 1024) * prep_ctas<F32>() <= 228 * 1024, "shared memory");
     static PerDeviceOnce once;
