@@ -76,34 +76,52 @@ struct ConvArgs {
     int32_t* dev_status;
 };
 
-// Each thread owns eight channels: K taps for each of them in registers and
-// the last K-1 rows beside them, so a tile of rows is read once.
+// Each thread owns eight channels: their K taps in registers, two channels to
+// a packed value, and the last K-1 rows beside them, so a tile of rows is read once.
 template <typename IO, int K> struct ConvLane {
-    float w[8][K];
-    float win[K][8];  // win[j]: the row j before the current one is win[K-1-j]
+    float2 w[K][4];
+    float2 win[K][4];  // win[K-1]: the current row, the ones before it below
     __device__ __forceinline__ void taps(const float* p, int c)
     {
+        float f[8 * K];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 2 * K; ++i) {
+            const float4 x = __ldg(reinterpret_cast<const float4*>(p + (size_t)c * K) + i);
+            f[4 * i] = x.x; f[4 * i + 1] = x.y; f[4 * i + 2] = x.z; f[4 * i + 3] = x.w;
+        }
 #pragma unroll
-            for (int j = 0; j < K; ++j) w[i][j] = p[(size_t)(c + i) * K + j];
+        for (int j = 0; j < K; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[j][i] = make_float2(f[2 * i * K + j], f[(2 * i + 1) * K + j]);
     }
-    // win[K-1] holds the current row: the row's outputs, then the window moves on
+    __device__ __forceinline__ void put(int j, const Vec8<IO>& v)
+    {
+        float x[8];
+        v.get(x);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) win[j][i] = make_float2(x[2 * i], x[2 * i + 1]);
+    }
+    // the outputs of the row in win[K-1]; then the window moves on
     __device__ __forceinline__ void step(Vec8<IO>& out)
     {
         float y[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float acc = 0.f;
+        for (int i = 0; i < 4; ++i) {
+            float2 acc = mul2(w[0][i], win[0][i]);
 #pragma unroll
-            for (int j = 0; j < K; ++j) acc = fmaf(w[i][j], win[j][i], acc);
-            y[i] = siluf_(acc);
+            for (int j = 1; j < K; ++j) acc = fma2(w[j][i], win[j][i], acc);
+            // x / (1 + e^-x)
+            const float2 e = mul2(acc, both2(-1.44269504088896341f));
+            const float2 d = add2(make_float2(exp2_sfu(e.x), exp2_sfu(e.y)), both2(1.f));
+            const float2 s = mul2(acc, make_float2(rcp_sfu(d.x), rcp_sfu(d.y)));
+            y[2 * i] = s.x;
+            y[2 * i + 1] = s.y;
         }
         out.set(y);
 #pragma unroll
         for (int j = 0; j + 1 < K; ++j)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) win[j][i] = win[j + 1][i];
+            for (int i = 0; i < 4; ++i) win[j][i] = win[j + 1][i];
     }
 };
 
@@ -173,7 +191,7 @@ template <typename IO, int K> __global__ void __launch_bounds__(CT) conv_varlen_
     ConvLane<IO, K> ln;
     ln.taps(a.w, c);
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j) hist[j].get(ln.win[j]);
+    for (int j = 0; j < K - 1; ++j) ln.put(j, hist[j]);
     if (r0 == b) {
         // the new state: the last K-1 rows of old state and sequence
         const int len = e - b;
@@ -191,48 +209,78 @@ template <typename IO, int K> __global__ void __launch_bounds__(CT) conv_varlen_
 #pragma unroll
         for (int j = 0; j < K - 1; ++j) nw[j].store(st + j * C + c);
     }
-    for (int r = r0; r < r1; r += CONV_AHEAD) {
+    const IO* xp = x + (size_t)r0 * C + c;
+    IO* yp = y + (size_t)r0 * C + c;
+    int left = r1 - r0;
+    for (; left >= CONV_AHEAD; left -= CONV_AHEAD, xp += CONV_AHEAD * C, yp += CONV_AHEAD * C) {
         Vec8<IO> in[CONV_AHEAD];
 #pragma unroll
-        for (int i = 0; i < CONV_AHEAD; ++i)
-            if (r + i < r1) in[i].load(x + (size_t)(r + i) * C + c);
+        for (int i = 0; i < CONV_AHEAD; ++i) in[i].load(xp + i * C);
 #pragma unroll
-        for (int i = 0; i < CONV_AHEAD; ++i)
-            if (r + i < r1) {
-                in[i].get(ln.win[K - 1]);
-                Vec8<IO> o;
-                ln.step(o);
-                o.store(y + (size_t)(r + i) * C + c);
-            }
+        for (int i = 0; i < CONV_AHEAD; ++i) {
+            ln.put(K - 1, in[i]);
+            Vec8<IO> o;
+            ln.step(o);
+            o.store(yp + i * C);
+        }
+    }
+#pragma unroll 1
+    for (; left > 0; --left, xp += C, yp += C) {
+        Vec8<IO> in, o;
+        in.load(xp);
+        ln.put(K - 1, in);
+        ln.step(o);
+        o.store(yp);
     }
 }
 
-// One row per sequence.
-template <typename IO, int K> __global__ void __launch_bounds__(CT) conv_decode_kernel(const ConvArgs a)
+// One row per sequence; a thread takes SEQS of them, so the taps are read once for all.
+template <typename IO, int K, int SEQS> __global__ void __launch_bounds__(CT) conv_decode_kernel(const ConvArgs a)
 {
-    const int seq = blockIdx.x;
     const int c = (blockIdx.y * CT + threadIdx.x) * 8;
-    const int slot = a.slots ? a.slots[seq] : seq;
-    if (slot >= a.num_slots) {
-        if (threadIdx.x == 0) flag_status(a.dev_status, KDA_DEV_BAD_SLOT);
-        return;
-    }
-    if (slot < 0 || c >= a.C) return;
+    if (c >= a.C) return;
     const size_t C = a.C;
-    IO* st = static_cast<IO*>(a.state) + (size_t)slot * (K - 1) * C;
-    Vec8<IO> v[K];
+    int slot[SEQS];
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j) v[j].load(st + j * C + c);
-    v[K - 1].load(static_cast<const IO*>(a.x) + (size_t)seq * C + c);
+    for (int q = 0; q < SEQS; ++q) {
+        const int seq = blockIdx.x * SEQS + q;
+        slot[q] = seq >= a.N ? -1 : a.slots ? a.slots[seq] : seq;
+        if (slot[q] >= a.num_slots) {
+            if (threadIdx.x == 0) flag_status(a.dev_status, KDA_DEV_BAD_SLOT);
+            slot[q] = -1;
+        }
+    }
     ConvLane<IO, K> ln;
+    Vec8<IO> v[SEQS][K];
+#pragma unroll
+    for (int q = 0; q < SEQS; ++q)
+        if (slot[q] >= 0) {
+            const IO* st = static_cast<const IO*>(a.state) + (size_t)slot[q] * (K - 1) * C + c;
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j) v[q][j].load(st + j * C);
+            v[q][K - 1].load(static_cast<const IO*>(a.x) + (size_t)(blockIdx.x * SEQS + q) * C + c);
+        }
     ln.taps(a.w, c);
 #pragma unroll
-    for (int j = 0; j < K; ++j) v[j].get(ln.win[j]);
-    Vec8<IO> o;
-    ln.step(o);
-    o.store(static_cast<IO*>(a.y) + (size_t)seq * C + c);
+    for (int q = 0; q < SEQS; ++q)
+        if (slot[q] >= 0) {
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j) v[j + 1].store(st + j * C + c);
+            for (int j = 0; j < K; ++j) ln.put(j, v[q][j]);
+            Vec8<IO> o;
+            ln.step(o);
+            o.store(static_cast<IO*>(a.y) + (size_t)(blockIdx.x * SEQS + q) * C + c);
+            IO* st = static_cast<IO*>(a.state) + (size_t)slot[q] * (K - 1) * C + c;
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j) v[q][j + 1].store(st + j * C);
+        }
+}
+
+template <typename IO, int K> void launch_conv_decode(const ConvArgs& a, int cols, cudaStream_t st)
+{
+    // several sequences a thread once there is a CTA for every SM
+    if ((long long)a.N * cols >= 4LL * sm_count())
+        conv_decode_kernel<IO, K, 4><<<dim3((a.N + 3) / 4, cols), CT, 0, st>>>(a);
+    else conv_decode_kernel<IO, K, 1><<<dim3(a.N, cols), CT, 0, st>>>(a);
 }
 
 template <typename IO> void launch_conv(const ConvArgs& a, int K, bool varlen, cudaStream_t st)
@@ -244,10 +292,9 @@ template <typename IO> void launch_conv(const ConvArgs& a, int K, bool varlen, c
         else if (K == 3) conv_varlen_kernel<IO, 3><<<g, CT, 0, st>>>(a);
         else conv_varlen_kernel<IO, 4><<<g, CT, 0, st>>>(a);
     } else {
-        const dim3 g(a.N, cols);
-        if (K == 2) conv_decode_kernel<IO, 2><<<g, CT, 0, st>>>(a);
-        else if (K == 3) conv_decode_kernel<IO, 3><<<g, CT, 0, st>>>(a);
-        else conv_decode_kernel<IO, 4><<<g, CT, 0, st>>>(a);
+        if (K == 2) launch_conv_decode<IO, 2>(a, cols, st);
+        else if (K == 3) launch_conv_decode<IO, 3>(a, cols, st);
+        else launch_conv_decode<IO, 4>(a, cols, st);
     }
 }
 

@@ -50,6 +50,12 @@ __device__ __forceinline__ float exp_sfu(float x)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(__fmul_rn(x, 1.44269504088896341f)));
     return y;
 }
+__device__ __forceinline__ float exp2_sfu(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 __device__ __forceinline__ float rcp_sfu(float x)
 {
     float y;
@@ -72,6 +78,32 @@ __device__ __forceinline__ float log_alpha(int gate_mode, float lb, float ea, fl
     if (gate_mode == KDA_GATE_SAFE) return lb * sigmoidf_(ea * x);
     return -ea * softplusf_(x);
 }
+
+// ------------------------------------------------------------ packed fp32
+
+// two fp32 operations an instruction
+__device__ __forceinline__ unsigned long long as_u64(float2 x) { return *reinterpret_cast<unsigned long long*>(&x); }
+__device__ __forceinline__ float2 as_f2(unsigned long long x) { return *reinterpret_cast<float2*>(&x); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    unsigned long long r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(as_u64(a)), "l"(as_u64(b)));
+    return as_f2(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(as_u64(a)), "l"(as_u64(b)));
+    return as_f2(r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(as_u64(a)), "l"(as_u64(b)), "l"(as_u64(c)));
+    return as_f2(r);
+}
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) { return fma2(b, make_float2(-1.f, -1.f), a); }
+__device__ __forceinline__ float2 both2(float x) { return make_float2(x, x); }
 
 // ------------------------------------------------------------ reductions
 

@@ -67,29 +67,6 @@ __device__ __forceinline__ void stsm(uint32_t addr, const uint32_t (&r)[4])
                  "r"(r[2]), "r"(r[3])
                  : "memory");
 }
-// two fp32 operations an instruction
-__device__ __forceinline__ unsigned long long as_u64(float2 x) { return *reinterpret_cast<unsigned long long*>(&x); }
-__device__ __forceinline__ float2 as_f2(unsigned long long x) { return *reinterpret_cast<float2*>(&x); }
-__device__ __forceinline__ float2 mul2(float2 a, float2 b)
-{
-    unsigned long long r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(as_u64(a)), "l"(as_u64(b)));
-    return as_f2(r);
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b)
-{
-    unsigned long long r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(as_u64(a)), "l"(as_u64(b)));
-    return as_f2(r);
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
-{
-    unsigned long long r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(as_u64(a)), "l"(as_u64(b)), "l"(as_u64(c)));
-    return as_f2(r);
-}
-__device__ __forceinline__ float2 sub2(float2 a, float2 b) { return fma2(b, make_float2(-1.f, -1.f), a); }
-__device__ __forceinline__ float2 both2(float x) { return make_float2(x, x); }
 __device__ __forceinline__ uint32_t pack_h(float x, float y)
 {
     const __half2 h = __floats2half2_rn(x, y);
@@ -128,13 +105,6 @@ __device__ __forceinline__ void pow2_scale_sqrt(float m, float& down, float& up)
     const int e = min(max((((int)(__float_as_uint(m) >> 23) & 255) + 1 - 128) >> 1, -60), 60);
     down = __uint_as_float((uint32_t)(127 - e) << 23);
     up = __uint_as_float((uint32_t)(127 + e) << 23);
-}
-
-__device__ __forceinline__ float exp2_sfu(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
 }
 
 // Bounded waits: after one that gives up the others only look once, and the

@@ -11,6 +11,7 @@ namespace {
 constexpr int ST = 256;             // threads of a CTA
 constexpr int PIECE = ST * 4 * 16;  // bytes one CTA moves at a time
 constexpr int LIST = 2048;          // pairs kept in shared memory at a time
+constexpr int RUN = 4;              // neighbouring pairs a CTA takes with a piece: a forked source is read once for them
 
 __device__ __forceinline__ bool test_bit(const uint32_t* m, int i) { return (m[i >> 5] >> (i & 31)) & 1u; }
 __device__ __forceinline__ void set_bit(uint32_t* m, int i) { atomicOr(m + (i >> 5), 1u << (i & 31)); }
@@ -48,9 +49,9 @@ struct PoolArgs {
     int32_t* dev_status;
 };
 
-// Items are (layer, piece of the slot, pair) with the pair running fastest:
-// neighbouring CTAs read the same piece of a forked source at about the same
-// time, so it leaves HBM once.
+// Items are (layer, piece of the slot, run of pairs) with the runs running
+// fastest: neighbouring CTAs read the same piece of a forked source at about
+// the same time, so it leaves HBM once.
 __global__ void __launch_bounds__(ST) slots_copy_kernel(const PoolArgs a)
 {
     extern __shared__ uint32_t maps[];  // three bit maps over the slots
@@ -86,21 +87,29 @@ __global__ void __launch_bounds__(ST) slots_copy_kernel(const PoolArgs a)
             pr = make_int2(s, d);
             return true;
         });
-        const long long items = pieces * a.layers * have;
+        const int runs = (have + RUN - 1) / RUN;
+        const long long items = pieces * a.layers * runs;
         for (long long w = blockIdx.x; w < items; w += gridDim.x) {
-            const int2 pr = list[w % have];
-            const long long rest = w / have;
+            const int first = (int)(w % runs) * RUN, last = min(first + RUN, have);
+            const long long rest = w / runs;
             char* base = a.pool + (rest / pieces) * a.layer_stride;
             const long long off = (rest % pieces) * PIECE + tid * 16;
-            const char* s = base + pr.x * a.slot_bytes;
-            char* d = base + pr.y * a.slot_bytes;
             uint4 v[4];
+            int held = -1;
+            for (int i = first; i < last; ++i) {
+                const int2 pr = list[i];
+                if (pr.x != held) {
+                    const char* s = base + pr.x * a.slot_bytes + off;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (off + j * ST * 16 < a.slot_bytes) v[j] = *reinterpret_cast<const uint4*>(s + off + j * ST * 16);
+                    for (int j = 0; j < 4; ++j)
+                        if (off + j * ST * 16 < a.slot_bytes) v[j] = *reinterpret_cast<const uint4*>(s + j * ST * 16);
+                    held = pr.x;
+                }
+                char* d = base + pr.y * a.slot_bytes + off;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (off + j * ST * 16 < a.slot_bytes) *reinterpret_cast<uint4*>(d + off + j * ST * 16) = v[j];
+                for (int j = 0; j < 4; ++j)
+                    if (off + j * ST * 16 < a.slot_bytes) *reinterpret_cast<uint4*>(d + j * ST * 16) = v[j];
+            }
         }
         __syncthreads();
     }
