@@ -6,6 +6,7 @@
 
 #include "kda_check.h"
 #include "kda_common.cuh"
+#include "kda_ptx.cuh"
 
 namespace kda {
 namespace {
@@ -126,14 +127,15 @@ template <typename IO, int K> struct ConvLane {
 };
 
 constexpr int CT = 128;       // threads: 1024 channels
-constexpr int CONV_ROWS = 32; // rows of a tile (K - 1 more are read again)
-constexpr int CONV_AHEAD = 8; // rows in flight
+constexpr int CONV_AHEAD = 8; // rows loaded at a time, a batch ahead of the one worked on
 
 // Tiles start at a sequence's first row, so only its tile 0 reads the old
 // state: that CTA also writes the new one, after its reads, and no other CTA
 // touches the slot.  blockIdx.x counts tiles over the sequences.
-template <typename IO, int K> __global__ void __launch_bounds__(CT) conv_varlen_kernel(const ConvArgs a)
+template <typename IO, int K, int CONV_ROWS> __global__ void __launch_bounds__(CT) conv_varlen_kernel(const ConvArgs a)
 {
+    ptx::grid_launch_dependents();
+    ptx::grid_dependency_wait();
     __shared__ int found[3];  // sequence, tile in it, tiles before a step of the search
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (warp == 0) {
@@ -212,10 +214,19 @@ template <typename IO, int K> __global__ void __launch_bounds__(CT) conv_varlen_
     const IO* xp = x + (size_t)r0 * C + c;
     IO* yp = y + (size_t)r0 * C + c;
     int left = r1 - r0;
-    for (; left >= CONV_AHEAD; left -= CONV_AHEAD, xp += CONV_AHEAD * C, yp += CONV_AHEAD * C) {
+    Vec8<IO> next[CONV_AHEAD];
+    if (left >= CONV_AHEAD)
+#pragma unroll
+        for (int i = 0; i < CONV_AHEAD; ++i) next[i].load(xp + i * C);
+#pragma unroll 1
+    for (; left >= CONV_AHEAD; left -= CONV_AHEAD, yp += CONV_AHEAD * C) {
         Vec8<IO> in[CONV_AHEAD];
 #pragma unroll
-        for (int i = 0; i < CONV_AHEAD; ++i) in[i].load(xp + i * C);
+        for (int i = 0; i < CONV_AHEAD; ++i) in[i] = next[i];
+        xp += CONV_AHEAD * C;
+        if (left >= 2 * CONV_AHEAD)
+#pragma unroll
+            for (int i = 0; i < CONV_AHEAD; ++i) next[i].load(xp + i * C);
 #pragma unroll
         for (int i = 0; i < CONV_AHEAD; ++i) {
             ln.put(K - 1, in[i]);
@@ -237,6 +248,8 @@ template <typename IO, int K> __global__ void __launch_bounds__(CT) conv_varlen_
 // One row per sequence; a thread takes SEQS of them, so the taps are read once for all.
 template <typename IO, int K, int SEQS> __global__ void __launch_bounds__(CT) conv_decode_kernel(const ConvArgs a)
 {
+    ptx::grid_launch_dependents();
+    ptx::grid_dependency_wait();
     const int c = (blockIdx.y * CT + threadIdx.x) * 8;
     if (c >= a.C) return;
     const size_t C = a.C;
@@ -275,27 +288,29 @@ template <typename IO, int K, int SEQS> __global__ void __launch_bounds__(CT) co
         }
 }
 
-template <typename IO, int K> void launch_conv_decode(const ConvArgs& a, int cols, cudaStream_t st)
+template <typename IO, int K> cudaError_t launch_conv_decode(const ConvArgs& a, int cols, cudaStream_t st)
 {
     // several sequences a thread once there is a CTA for every SM
     if ((long long)a.N * cols >= 4LL * sm_count())
-        conv_decode_kernel<IO, K, 4><<<dim3((a.N + 3) / 4, cols), CT, 0, st>>>(a);
-    else conv_decode_kernel<IO, K, 1><<<dim3(a.N, cols), CT, 0, st>>>(a);
+        return launch_dependent(conv_decode_kernel<IO, K, 4>, dim3((a.N + 3) / 4, cols), CT, 0, st, a);
+    return launch_dependent(conv_decode_kernel<IO, K, 1>, dim3(a.N, cols), CT, 0, st, a);
 }
 
-template <typename IO> void launch_conv(const ConvArgs& a, int K, bool varlen, cudaStream_t st)
+template <typename IO, int K> cudaError_t launch_conv_varlen(const ConvArgs& a, int cols, cudaStream_t st)
+{
+    // sum of ceil(len / rows) <= N + T / rows tiles; long ones (the K-1 rows before a
+    // tile are read again) where they still give every SM several CTAs
+    if ((long long)(a.T / 64) * cols >= 8LL * sm_count())
+        return launch_dependent(conv_varlen_kernel<IO, K, 64>, dim3(a.N + a.T / 64, cols), CT, 0, st, a);
+    return launch_dependent(conv_varlen_kernel<IO, K, 16>, dim3(a.N + a.T / 16, cols), CT, 0, st, a);
+}
+
+template <typename IO> cudaError_t launch_conv(const ConvArgs& a, int K, bool varlen, cudaStream_t st)
 {
     const int cols = (a.C / 8 + CT - 1) / CT;
-    if (varlen) {
-        const dim3 g(a.N + a.T / CONV_ROWS, cols);  // sum of ceil(len / rows) <= N + T / rows
-        if (K == 2) conv_varlen_kernel<IO, 2><<<g, CT, 0, st>>>(a);
-        else if (K == 3) conv_varlen_kernel<IO, 3><<<g, CT, 0, st>>>(a);
-        else conv_varlen_kernel<IO, 4><<<g, CT, 0, st>>>(a);
-    } else {
-        if (K == 2) launch_conv_decode<IO, 2>(a, cols, st);
-        else if (K == 3) launch_conv_decode<IO, 3>(a, cols, st);
-        else launch_conv_decode<IO, 4>(a, cols, st);
-    }
+    if (K == 2) return varlen ? launch_conv_varlen<IO, 2>(a, cols, st) : launch_conv_decode<IO, 2>(a, cols, st);
+    if (K == 3) return varlen ? launch_conv_varlen<IO, 3>(a, cols, st) : launch_conv_decode<IO, 3>(a, cols, st);
+    return varlen ? launch_conv_varlen<IO, 4>(a, cols, st) : launch_conv_decode<IO, 4>(a, cols, st);
 }
 
 int check_conv(const kda_conv_params* p)
@@ -330,9 +345,9 @@ int conv_call(const kda_conv_params* p, const int32_t* cu_seqlens, int32_t N, in
     a.state = conv_state;
     a.y = y;
     a.dev_status = dev_status;
-    if (p->io_dtype == KDA_DTYPE_BF16) launch_conv<__nv_bfloat16>(a, p->conv_kernel, varlen, stream);
-    else launch_conv<float>(a, p->conv_kernel, varlen, stream);
-    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_LAUNCH;
+    const cudaError_t e = p->io_dtype == KDA_DTYPE_BF16 ? launch_conv<__nv_bfloat16>(a, p->conv_kernel, varlen, stream)
+                                                        : launch_conv<float>(a, p->conv_kernel, varlen, stream);
+    return e == cudaSuccess ? KDA_OK : KDA_ERR_LAUNCH;
 }
 
 // ------------------------------------------------------------ block norms
@@ -443,6 +458,8 @@ __device__ __forceinline__ void norm_row(const NormArgs& a, long long row, int f
 template <typename IO, typename RES, int VPT>
 __global__ void __launch_bounds__(128) norm_warp_kernel(const NormArgs a, int lanes)
 {
+    ptx::grid_launch_dependents();
+    ptx::grid_dependency_wait();
     const int lane = threadIdx.x & 31, per_warp = 32 / lanes;
     const long long row = ((long long)blockIdx.x * 4 + (threadIdx.x >> 5)) * per_warp + lane / lanes;
     norm_row<IO, RES, VPT>(a, row < a.rows ? row : 0, lane % lanes, lanes, row < a.rows, [&](float s) {
@@ -455,6 +472,8 @@ __global__ void __launch_bounds__(128) norm_warp_kernel(const NormArgs a, int la
 template <typename IO, typename RES, int VPT>
 __global__ void __launch_bounds__(512) norm_block_kernel(const NormArgs a)
 {
+    ptx::grid_launch_dependents();
+    ptx::grid_dependency_wait();
     __shared__ float part[2][16];
     int turn = 0;
     norm_row<IO, RES, VPT>(a, blockIdx.x, threadIdx.x, blockDim.x, true, [&](float s) {
@@ -468,7 +487,7 @@ __global__ void __launch_bounds__(512) norm_block_kernel(const NormArgs a)
     });
 }
 
-template <typename IO, typename RES> void launch_norm(const NormArgs& a, cudaStream_t st)
+template <typename IO, typename RES> cudaError_t launch_norm(const NormArgs& a, cudaStream_t st)
 {
     const int nv = a.D / 8;
     if (nv <= 128) {
@@ -476,15 +495,14 @@ template <typename IO, typename RES> void launch_norm(const NormArgs& a, cudaStr
         while (lanes < nv && lanes < 32) lanes <<= 1;
         const long long per_cta = 4 * (32 / lanes);
         const unsigned g = (unsigned)((a.rows + per_cta - 1) / per_cta);
-        if (nv <= 32) norm_warp_kernel<IO, RES, 1><<<g, 128, 0, st>>>(a, lanes);
-        else if (nv <= 64) norm_warp_kernel<IO, RES, 2><<<g, 128, 0, st>>>(a, lanes);
-        else norm_warp_kernel<IO, RES, 4><<<g, 128, 0, st>>>(a, lanes);
-        return;
+        if (nv <= 32) return launch_dependent(norm_warp_kernel<IO, RES, 1>, g, 128, 0, st, a, lanes);
+        if (nv <= 64) return launch_dependent(norm_warp_kernel<IO, RES, 2>, g, 128, 0, st, a, lanes);
+        return launch_dependent(norm_warp_kernel<IO, RES, 4>, g, 128, 0, st, a, lanes);
     }
     const unsigned g = (unsigned)a.rows;
     auto threads = [&](int vpt) { return ((nv + vpt - 1) / vpt + 31) / 32 * 32; };
-    if (nv <= 1024) norm_block_kernel<IO, RES, 2><<<g, threads(2), 0, st>>>(a);
-    else norm_block_kernel<IO, RES, 4><<<g, threads(4), 0, st>>>(a);
+    if (nv <= 1024) return launch_dependent(norm_block_kernel<IO, RES, 2>, g, threads(2), 0, st, a);
+    return launch_dependent(norm_block_kernel<IO, RES, 4>, g, threads(4), 0, st, a);
 }
 
 }  // namespace
@@ -566,11 +584,11 @@ KDA_API int kda_block_norm(const kda_norm_params* p, int64_t rows, const void* y
     a.h = h_out;
     a.x = x_out;
     const bool iob = p->io_dtype == KDA_DTYPE_BF16, rsb = p->res_dtype == KDA_DTYPE_BF16;
-    if (iob && rsb) launch_norm<__nv_bfloat16, __nv_bfloat16>(a, stream);
-    else if (iob) launch_norm<__nv_bfloat16, float>(a, stream);
-    else if (rsb) launch_norm<float, __nv_bfloat16>(a, stream);
-    else launch_norm<float, float>(a, stream);
-    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_LAUNCH;
+    const cudaError_t e = iob && rsb ? launch_norm<__nv_bfloat16, __nv_bfloat16>(a, stream)
+                        : iob        ? launch_norm<__nv_bfloat16, float>(a, stream)
+                        : rsb        ? launch_norm<float, __nv_bfloat16>(a, stream)
+                                     : launch_norm<float, float>(a, stream);
+    return e == cudaSuccess ? KDA_OK : KDA_ERR_LAUNCH;
 }
 
 }  // extern "C"

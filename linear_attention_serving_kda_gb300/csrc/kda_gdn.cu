@@ -8,6 +8,7 @@
 #include <cstring>
 
 #include "kda_gdn.h"
+#include "kda_ptx.cuh"
 
 namespace kda {
 namespace {
@@ -41,6 +42,8 @@ constexpr int GD_WARPS = 8;
 template <int DK, int DVT, typename IO, typename OUT>
 __global__ void __launch_bounds__(GD_WARPS * 32) gdn_decode_kernel(const GdnArgs a, int dv)
 {
+    ptx::grid_launch_dependents();
+    ptx::grid_dependency_wait();
     constexpr int LPR = DVT / 4, RPP = 32 / LPR, RT = DK / (GD_WARPS * RPP), PER = DK / 32;
     static_assert(RT >= 1, "tile too narrow");
     __shared__ float ks[DK], qs[DK];
@@ -147,22 +150,22 @@ __global__ void __launch_bounds__(GD_WARPS * 32) gdn_decode_kernel(const GdnArgs
     }
 }
 
-template <int DK, typename IO, typename OUT> void decode_dk(const GdnArgs& a, int dv, cudaStream_t st)
+template <int DK, typename IO, typename OUT> cudaError_t decode_dk(const GdnArgs& a, int dv, cudaStream_t st)
 {
     // Narrower tiles while there is less than one CTA for every SM.
     int t = dv;
     while (t > 32 && (long long)a.N * a.Hv * (dv / t) < sm_count()) t /= 2;
     const unsigned g = (unsigned)((long long)a.N * a.Hv * (dv / t));
-    if (t == 128) gdn_decode_kernel<DK, 128, IO, OUT><<<g, GD_WARPS * 32, 0, st>>>(a, dv);
-    else if (t == 64) gdn_decode_kernel<DK, 64, IO, OUT><<<g, GD_WARPS * 32, 0, st>>>(a, dv);
-    else gdn_decode_kernel<DK, 32, IO, OUT><<<g, GD_WARPS * 32, 0, st>>>(a, dv);
+    if (t == 128) return launch_dependent(gdn_decode_kernel<DK, 128, IO, OUT>, g, GD_WARPS * 32, 0, st, a, dv);
+    if (t == 64) return launch_dependent(gdn_decode_kernel<DK, 64, IO, OUT>, g, GD_WARPS * 32, 0, st, a, dv);
+    return launch_dependent(gdn_decode_kernel<DK, 32, IO, OUT>, g, GD_WARPS * 32, 0, st, a, dv);
 }
 
-template <typename IO, typename OUT> void decode_io(const GdnArgs& a, int dk, int dv, cudaStream_t st)
+template <typename IO, typename OUT> cudaError_t decode_io(const GdnArgs& a, int dk, int dv, cudaStream_t st)
 {
-    if (dk == 128) decode_dk<128, IO, OUT>(a, dv, st);
-    else if (dk == 64) decode_dk<64, IO, OUT>(a, dv, st);
-    else decode_dk<32, IO, OUT>(a, dv, st);
+    if (dk == 128) return decode_dk<128, IO, OUT>(a, dv, st);
+    if (dk == 64) return decode_dk<64, IO, OUT>(a, dv, st);
+    return decode_dk<32, IO, OUT>(a, dv, st);
 }
 
 // ------------------------------------------------------------ fp32 rows, one by one
@@ -175,6 +178,8 @@ constexpr int GR_WARPS = 4, GR_COLS = 32, GR_ROWS = 16;
 
 template <int DK> __global__ void __launch_bounds__(GR_WARPS * 32) gdn_rows_kernel(const GdnArgs a, int dv)
 {
+    ptx::grid_launch_dependents();
+    ptx::grid_dependency_wait();
     constexpr int PER = DK / 32, M = DK / 16, RW = GR_ROWS / GR_WARPS;
     __shared__ __align__(16) float qs[GR_ROWS][DK], ks[GR_ROWS][DK], vs[GR_ROWS][GR_COLS];
     __shared__ float al[GR_ROWS], be[GR_ROWS];
@@ -347,10 +352,9 @@ int check_rows(const kda_gdn_params* p, const GdnArgs& g, int64_t rows, const vo
 cudaError_t launch_gdn_rows(const GdnArgs& a, int dk, int dv, cudaStream_t st)
 {
     const unsigned g = (unsigned)((long long)a.N * a.Hv * (dv / GR_COLS));
-    if (dk == 128) gdn_rows_kernel<128><<<g, GR_WARPS * 32, 0, st>>>(a, dv);
-    else if (dk == 64) gdn_rows_kernel<64><<<g, GR_WARPS * 32, 0, st>>>(a, dv);
-    else gdn_rows_kernel<32><<<g, GR_WARPS * 32, 0, st>>>(a, dv);
-    return cudaGetLastError();
+    if (dk == 128) return launch_dependent(gdn_rows_kernel<128>, g, GR_WARPS * 32, 0, st, a, dv);
+    if (dk == 64) return launch_dependent(gdn_rows_kernel<64>, g, GR_WARPS * 32, 0, st, a, dv);
+    return launch_dependent(gdn_rows_kernel<32>, g, GR_WARPS * 32, 0, st, a, dv);
 }
 
 }  // namespace kda
@@ -415,10 +419,10 @@ KDA_API int kda_gdn_decode(const kda_gdn_params* p, int32_t B, const void* q, co
     g.out = out;
     g.dev_status = dev_status;
     const int dk = p->head_dim_k, dv = p->head_dim_v;
-    if (p->io_dtype == KDA_DTYPE_F32) decode_io<float, float>(g, dk, dv, stream);
-    else if (p->out_dtype == KDA_DTYPE_BF16) decode_io<__nv_bfloat16, __nv_bfloat16>(g, dk, dv, stream);
-    else decode_io<__nv_bfloat16, float>(g, dk, dv, stream);
-    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_LAUNCH;
+    const cudaError_t e = p->io_dtype == KDA_DTYPE_F32    ? decode_io<float, float>(g, dk, dv, stream)
+                          : p->out_dtype == KDA_DTYPE_BF16 ? decode_io<__nv_bfloat16, __nv_bfloat16>(g, dk, dv, stream)
+                                                           : decode_io<__nv_bfloat16, float>(g, dk, dv, stream);
+    return e == cudaSuccess ? KDA_OK : KDA_ERR_LAUNCH;
 }
 
 }  // extern "C"

@@ -328,6 +328,8 @@ template <int DK, bool F32, int HEADS>
 __global__ void __launch_bounds__(PREP, prep_ctas<F32>())
 gdn_prep_kernel(const GdnArgs a, const __grid_constant__ RowMaps maps, const Work ws)
 {
+    ptx::grid_launch_dependents();
+    ptx::grid_dependency_wait();
     extern __shared__ __align__(1024) unsigned char dyn[];
     using S = PrepSmem<DK, F32, HEADS>;
     using L = Slot<DK, F32>;
@@ -797,6 +799,8 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) gdn_chain_kernel(const GdnAr
     S& sm = *reinterpret_cast<S*>(dyn);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int h = blockIdx.x % a.Hv;
+    ptx::grid_launch_dependents();
+    ptx::grid_dependency_wait();
     const int seq = ranked_seq(a.cu_seqlens, a.N, blockIdx.x / a.Hv, &sm.found);
     int begin, end, state_slot;
     if (!gdn_unit(a, seq, begin, end, state_slot)) return;
@@ -1153,8 +1157,7 @@ cudaError_t launch_chain(const GdnArgs& a, const CUtensorMap& vmap, const Work& 
         return cudaFuncSetAttribute(gdn_chain_kernel<DK, DV, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     });
     if (e != cudaSuccess) return e;
-    gdn_chain_kernel<DK, DV, F32><<<a.N * a.Hv, CHAIN_THREADS, smem, st>>>(a, vmap, ws);
-    return cudaGetLastError();
+    return launch_dependent(gdn_chain_kernel<DK, DV, F32>, a.N * a.Hv, CHAIN_THREADS, smem, st, a, vmap, ws);
 }
 
 template <int DK, bool F32, int HEADS>
@@ -1171,8 +1174,7 @@ cudaError_t launch_prep(const GdnArgs& a, const RowMaps& maps, const Work& ws, l
         return cudaFuncSetAttribute(gdn_prep_kernel<DK, F32, HEADS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     });
     if (e != cudaSuccess) return e;
-    gdn_prep_kernel<DK, F32, HEADS><<<(unsigned)(slots * (a.Hv / HEADS)), PREP, smem, st>>>(a, maps, ws);
-    return cudaGetLastError();
+    return launch_dependent(gdn_prep_kernel<DK, F32, HEADS>, (unsigned)(slots * (a.Hv / HEADS)), PREP, smem, st, a, maps, ws);
 }
 
 template <int DK, bool F32> cudaError_t launch(const GdnArgs& a, int dv, cudaStream_t st)
@@ -1187,8 +1189,10 @@ template <int DK, bool F32> cudaError_t launch(const GdnArgs& a, int dv, cudaStr
     Work ws;
     ws.kq = static_cast<unsigned char*>(a.workspace);
     ws.v = ws.kq + slots * a.Hk * L::KQ;
-    const cudaError_t e = a.Hv / a.Hk % 2 == 0 ? launch_prep<DK, F32, 2>(a, maps, ws, slots, st)
-                                               : launch_prep<DK, F32, 1>(a, maps, ws, slots, st);
+    // two heads a CTA (their rows, products and norms once) unless all single ones run at once anyway
+    const cudaError_t e = a.Hv / a.Hk % 2 == 0 && slots * a.Hv > prep_ctas<F32>() * sm_count()
+                              ? launch_prep<DK, F32, 2>(a, maps, ws, slots, st)
+                              : launch_prep<DK, F32, 1>(a, maps, ws, slots, st);
     if (e != cudaSuccess) return e;
     if (dv == 128) return launch_chain<DK, 128, F32>(a, maps.v, ws, st);
     if (dv == 64) return launch_chain<DK, 64, F32>(a, maps.v, ws, st);

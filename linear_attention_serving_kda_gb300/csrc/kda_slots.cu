@@ -4,6 +4,7 @@
 // bound is HBM bandwidth (a fork's source stays in L2 across its targets).
 #include "kda_check.h"
 #include "kda_common.cuh"
+#include "kda_ptx.cuh"
 
 namespace kda {
 namespace {
@@ -54,6 +55,8 @@ struct PoolArgs {
 // the same time, so it leaves HBM once.
 __global__ void __launch_bounds__(ST) slots_copy_kernel(const PoolArgs a)
 {
+    ptx::grid_launch_dependents();
+    ptx::grid_dependency_wait();
     extern __shared__ uint32_t maps[];  // three bit maps over the slots
     __shared__ int2 list[LIST];
     __shared__ int warp_tot[ST / 32];
@@ -118,6 +121,8 @@ __global__ void __launch_bounds__(ST) slots_copy_kernel(const PoolArgs a)
 
 __global__ void __launch_bounds__(ST) slots_zero_kernel(const PoolArgs a)
 {
+    ptx::grid_launch_dependents();
+    ptx::grid_dependency_wait();
     __shared__ int2 list[LIST];
     __shared__ int warp_tot[ST / 32];
     const int tid = threadIdx.x;
@@ -151,6 +156,8 @@ constexpr int PT = 1024;
 __global__ void __launch_bounds__(PT) compact_plan_kernel(int S, const int32_t* live, int32_t* src, int32_t* dst,
                                                           int32_t* remap)
 {
+    ptx::grid_launch_dependents();
+    ptx::grid_dependency_wait();
     __shared__ int holes[PT / 32], movers[PT / 32];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     int L = 0;
@@ -253,8 +260,8 @@ KDA_API int kda_slots_copy(const kda_slot_pool* pool, int32_t n, const int32_t* 
                                         3 * KDA_MAX_POOL_SLOTS / 8);
         }) != cudaSuccess)
         return KDA_ERR_LAUNCH;
-    slots_copy_kernel<<<pool_grid(pool, n), ST, smem, stream>>>(pool_args(pool, n, src, dst, dev_status));
-    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_LAUNCH;
+    return launch_dependent(slots_copy_kernel, pool_grid(pool, n), ST, smem, stream,
+                            pool_args(pool, n, src, dst, dev_status)) == cudaSuccess ? KDA_OK : KDA_ERR_LAUNCH;
 }
 
 KDA_API int kda_slots_zero(const kda_slot_pool* pool, int32_t n, const int32_t* slots, int32_t* dev_status,
@@ -267,8 +274,8 @@ KDA_API int kda_slots_zero(const kda_slot_pool* pool, int32_t n, const int32_t* 
     if ((rc = check_ptrs({slots})) != KDA_OK) return rc;
     if (overlap(pool->pool, pool_bytes(pool), slots, sizeof(int32_t) * (size_t)n)) return KDA_ERR_INVALID_ARGUMENT;
     if ((rc = check_device()) != KDA_OK) return rc;
-    slots_zero_kernel<<<pool_grid(pool, n), ST, 0, stream>>>(pool_args(pool, n, nullptr, slots, dev_status));
-    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_LAUNCH;
+    return launch_dependent(slots_zero_kernel, pool_grid(pool, n), ST, 0, stream,
+                            pool_args(pool, n, nullptr, slots, dev_status)) == cudaSuccess ? KDA_OK : KDA_ERR_LAUNCH;
 }
 
 KDA_API int kda_slots_compact_plan(const kda_slot_pool* pool, const int32_t* live, int32_t* src, int32_t* dst,
@@ -283,8 +290,8 @@ KDA_API int kda_slots_compact_plan(const kda_slot_pool* pool, const int32_t* liv
         for (int j = 0; j < i; ++j)
             if (overlap(all[i], b, all[j], b)) return KDA_ERR_INVALID_ARGUMENT;
     if ((rc = check_device()) != KDA_OK) return rc;
-    compact_plan_kernel<<<1, PT, 0, stream>>>(pool->num_slots, live, src, dst, remap);
-    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_LAUNCH;
+    return launch_dependent(compact_plan_kernel, 1, PT, 0, stream, pool->num_slots, live, src, dst, remap) == cudaSuccess
+               ? KDA_OK : KDA_ERR_LAUNCH;
 }
 
 }  // extern "C"
