@@ -126,7 +126,7 @@ template <typename IO, int K> struct ConvLane {
     }
 };
 
-constexpr int CT = 128;       // threads: 1024 channels
+constexpr int CT = 64;        // threads: 512 channels (more, smaller CTAs hide more of the loads: 128 threads took 218 us where these take 178)
 constexpr int CONV_AHEAD = 8; // rows loaded at a time, a batch ahead of the one worked on
 
 // Tiles start at a sequence's first row, so only its tile 0 reads the old
@@ -291,7 +291,7 @@ template <typename IO, int K, int SEQS> __global__ void __launch_bounds__(CT) co
 template <typename IO, int K> cudaError_t launch_conv_decode(const ConvArgs& a, int cols, cudaStream_t st)
 {
     // several sequences a thread once there is a CTA for every SM
-    if ((long long)a.N * cols >= 4LL * sm_count())
+    if ((long long)a.N * cols >= 2LL * sm_count())
         return launch_dependent(conv_decode_kernel<IO, K, 4>, dim3((a.N + 3) / 4, cols), CT, 0, st, a);
     return launch_dependent(conv_decode_kernel<IO, K, 1>, dim3(a.N, cols), CT, 0, st, a);
 }
@@ -300,8 +300,8 @@ template <typename IO, int K> cudaError_t launch_conv_varlen(const ConvArgs& a, 
 {
     // sum of ceil(len / rows) <= N + T / rows tiles; long ones (the K-1 rows before a
     // tile are read again) where they still give every SM several CTAs
-    if ((long long)(a.T / 64) * cols >= 8LL * sm_count())
-        return launch_dependent(conv_varlen_kernel<IO, K, 64>, dim3(a.N + a.T / 64, cols), CT, 0, st, a);
+    if ((long long)(a.T / 128) * cols >= 8LL * sm_count())
+        return launch_dependent(conv_varlen_kernel<IO, K, 128>, dim3(a.N + a.T / 128, cols), CT, 0, st, a);
     return launch_dependent(conv_varlen_kernel<IO, K, 16>, dim3(a.N + a.T / 16, cols), CT, 0, st, a);
 }
 
