@@ -136,8 +136,8 @@ def test_prefill_head_groups(cuda_lib, Hk, Hv, io):
 
 
 @pytest.mark.parametrize("heads", [1, 40])
-def test_prefill_both_cta_widths(cuda_lib, heads):
-    """Few chains take two chain warps a CTA, many take four: the same bits."""
+def test_prefill_one_head_as_among_many(cuda_lib, heads):
+    """A head's results do not depend on how many others the call has: the same bits."""
     c = Case([200, 90], Hk=heads, Hv=heads, seed=3)
     c.prefill(cuda_lib)
     c.check()
@@ -373,5 +373,118 @@ def test_two_calls_at_once(cuda_lib):
 def test_long_prompt(cuda_lib):
     """Many chunks of one sequence: errors do not pile up."""
     c = Case([4000], Hk=1, Hv=2, out="f32", seed=30)
+    c.prefill(cuda_lib)
+    c.check()
+
+
+def _beside(c):
+    """Whether a call of this case runs its chains beside prep (few chains, more slots than one wave of prep)."""
+    slots = c.T // 64 + c.N
+    return c.N * c.Hv * 2 < 152 and slots * c.Hv > (3 if c.out_t == "bf16" else 2) * 152
+
+
+@pytest.mark.parametrize("Hk,Hv,dk,dv,out,lens", [
+    (1, 8, 32, 32, "bf16", [4100]),
+    (2, 8, 32, 64, "f32", [0, 1500, 1, 700, 0, 130]),
+    (8, 8, 64, 32, "f32", [1800, 900]),
+    (3, 3, 32, 128, "bf16", [40, 9900]),
+    (4, 16, 128, 128, "bf16", [1100, 64, 65, 700]),
+])
+def test_prefill_chains_beside_prep(cuda_lib, Hk, Hv, dk, dv, out, lens):
+    slots = list(range(len(lens)))
+    if len(lens) > 3:
+        slots[3] = -1  # a padded sequence among them
+    c = Case(lens, Hk=Hk, Hv=Hv, dk=dk, dv=dv, out=out, seed=40 + dk, slots=slots)
+    assert _beside(c)
+    c.prefill(cuda_lib)
+    c.check()
+
+
+def test_prefill_beside_gives_the_bits_of_one_after_the_other(cuda_lib):
+    """The same rows as a call of their own (chains beside prep) and among
+    enough others that prep runs first: the same bits; and again on a
+    workspace full of ones."""
+    lens = [1400, 1100]
+    c = Case(lens, Hk=6, Hv=12, dk=64, dv=64, seed=50)
+    assert _beside(c)
+    c.prefill(cuda_lib)
+    want = c.g_out.tensor.clone(), c.g_state.tensor.clone()
+    c.reset()
+    p = c.params(cuda_lib)
+    need = cuda_lib.kda_gdn_prefill_workspace_bytes(p, 2, c.T)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    cuda_lib.check(cuda_lib.kda_gdn_prefill_varlen(p, c.cu, 2, c.T, c.q, c.k, c.v, c.a, c.b, None, c.g_state.tensor,
+                                                   c.g_out.tensor, ws, need, c.status))
+    torch.cuda.synchronize()
+    assert torch.equal(c.g_out.tensor, want[0]) and torch.equal(c.g_state.tensor, want[1])
+    many = Case(lens + [3] * 5, Hk=6, Hv=12, dk=64, dv=64, seed=51)
+    assert not _beside(many)
+    n = c.T
+    many.rows[:n].copy_(c.rows)
+    many.a[:n].copy_(c.a)
+    many.b[:n].copy_(c.b)
+    many.A_log, many.dt_bias = c.A_log, c.dt_bias
+    many.state0[:2].copy_(c.state0)
+    many.reset()
+    many.prefill(cuda_lib)
+    assert torch.equal(many.g_out.tensor[:n], want[0]) and torch.equal(many.g_state.tensor[:2], want[1])
+
+
+def test_beside_in_a_graph_and_twice_at_once(cuda_lib):
+    """Captured and replayed; and two such calls on two streams, a workspace each."""
+    cs = [Case([2600, 500], Hk=4, Hv=16, dk=32, dv=32, seed=60 + i) for i in range(2)]
+    assert _beside(cs[0])
+    for c in cs:
+        c.prefill(cuda_lib)
+    want = [(c.g_out.tensor.clone(), c.g_state.tensor.clone()) for c in cs]
+    p = cs[0].params(cuda_lib)
+    need = cuda_lib.kda_gdn_prefill_workspace_bytes(p, 2, 3100)
+    ws = [torch.empty(need, dtype=torch.uint8, device="cuda") for _ in cs]
+
+    def call(i, stream=None):
+        c = cs[i]
+        cuda_lib.check(cuda_lib.kda_gdn_prefill_varlen(c.params(cuda_lib), c.cu, 2, 3100, c.q, c.k, c.v, c.a, c.b, None,
+                                                       c.g_state.tensor, c.g_out.tensor, ws[i], need, c.status, stream))
+
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(0)
+    for _ in range(2):
+        cs[0].reset()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(cs[0].g_out.tensor, want[0][0]) and torch.equal(cs[0].g_state.tensor, want[0][1])
+    for c in cs:
+        c.reset()
+    torch.cuda.synchronize()
+    for i, s in enumerate([torch.cuda.Stream(), torch.cuda.Stream()]):
+        call(i, s)
+    torch.cuda.synchronize()
+    for c, (o, st) in zip(cs, want):
+        assert torch.equal(c.g_out.tensor, o) and torch.equal(c.g_state.tensor, st) and int(c.status.item()) == 0
+
+
+def test_back_to_back_calls_keep_their_order(cuda_lib):
+    """Calls right behind one another on a stream, each on the states and rows the one before left (their
+    kernels may start early, their memory accesses may not)."""
+    c = Case([1] * 4, Hk=2, Hv=4, seed=70)
+    for _ in range(20):
+        cuda_lib.check(cuda_lib.kda_gdn_decode(c.params(cuda_lib), 4, c.q, c.k, c.v, c.a, c.b, None, c.g_state.tensor,
+                                               c.g_out.tensor, c.status))
+    torch.cuda.synchronize()
+    got = c.g_state.tensor.clone()
+    c.reset()
+    for _ in range(20):
+        c.decode(cuda_lib)
+    assert torch.equal(got, c.g_state.tensor)
+
+
+@pytest.mark.parametrize("out,Hk,Hv,dk", [("f32", 8, 16, 32), ("bf16", 4, 16, 64), ("bf16", 5, 15, 32)])
+def test_prefill_many_heads_of_shared_keys(cuda_lib, out, Hk, Hv, dk):
+    """Enough chunk-heads that prep takes two heads of one key head together (an odd group: one), the sequences
+    enough that the chains run after it."""
+    c = Case([200, 0, 65, 700, 1, 64, 333, 128, 500, 130, 90, 640], Hk=Hk, Hv=Hv, dk=dk, dv=32, out=out, seed=80,
+             slots=[3, 0, 7, -1, 5, 1, 2, 11, 4, 6, 8, 9])
+    assert not _beside(c) and (c.T // 64 + c.N) * Hv > 3 * 152
     c.prefill(cuda_lib)
     c.check()
