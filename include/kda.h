@@ -348,11 +348,13 @@ typedef struct kda_gdn_params {
  * instance), gate logits a and beta logits b: dense [T][Hv], out: dense
  * [T][Hv][dv], rec_state: fp32 [num_slots][Hv][dk][dv], updated in place.  An empty
  * or skipped sequence leaves its state, and a skipped one its out rows, as
- * they were.  The non-negative slots of one call are distinct.  `out` overlaps
- * no input.
+ * they were.  The non-negative slots of one call are distinct.  `out`,
+ * the states and the workspace overlap no input and not each other.  A sequence
+ * whose cu_seqlens are bad is flagged and skipped; what such a call gives for
+ * the others is unspecified, within their own rows and slots.
  *   - bf16 rows run in chunks of 64 on the tensor cores.  The states keep fp32
  *     accuracy (every product that reaches them has operands split into
- *     bf16 high and low parts where one bf16 does not hold the value);
+ *     fp16 high and low parts where one fp16 does not hold the value);
  *     fp32 rows run row by row in fp32.
  *   - A prompt cut into several calls agrees with one uncut call to rounding.
  *   - Values up to 2^60 in magnitude keep that accuracy (operands are rescaled
@@ -383,7 +385,8 @@ KDA_API int kda_gdn_decode(const kda_gdn_params* p, int32_t B, const void* q, co
  * raw rows in return.  x and y: dense [rows][channels] of io_dtype, apart
  * (KDA_ERR_INVALID_ARGUMENT where they overlap).  A zero-length sequence
  * leaves its state, a skipped one its state and y rows.  The non-negative
- * slots of one call are distinct.
+ * slots of one call are distinct.  y and the states overlap no input and not
+ * each other; bad cu_seqlens as in kda_gdn_prefill_varlen.
  */
 typedef struct kda_conv_params {
     int32_t channels;         /* a multiple of 8, <= 2^20                       */

@@ -136,41 +136,13 @@ template <typename IO, int K, int CONV_ROWS> __global__ void __launch_bounds__(C
 {
     ptx::grid_launch_dependents();
     ptx::grid_dependency_wait();
-    __shared__ int found[3];  // sequence, tile in it, tiles before a step of the search
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (warp == 0) {
-        int before = 0, seq = -1, tile = 0;
-        bool bad = false;
-        for (int n0 = 0; n0 < a.N && seq < 0; n0 += 32) {
-            int tiles = 0;
-            if (n0 + lane < a.N) {
-                const int b = a.cu_seqlens[n0 + lane], e = a.cu_seqlens[n0 + lane + 1];
-                if (b < 0 || e < b || e > a.T) bad = true;
-                else tiles = (e - b + CONV_ROWS - 1) / CONV_ROWS;
-            }
-            int inc = tiles;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int up = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += up;
-            }
-            const bool mine = (int)blockIdx.x >= before + inc - tiles && (int)blockIdx.x < before + inc;
-            const uint32_t m = __ballot_sync(0xffffffffu, mine);
-            if (m) {
-                const int l = __ffs(m) - 1;
-                seq = n0 + l;
-                tile = __shfl_sync(0xffffffffu, (int)blockIdx.x - (before + inc - tiles), l);
-            }
-            before += __shfl_sync(0xffffffffu, inc, 31);
-        }
-        if (bad) flag_status(a.dev_status, KDA_DEV_BAD_SEQLENS);
-        if (lane == 0) {
-            found[0] = seq;
-            found[1] = tile;
-        }
+    const int tid = threadIdx.x;
+    if ((int)blockIdx.x < a.N && blockIdx.y == 0 && tid == 0) {  // as many CTAs as sequences, at least
+        const int f = a.cu_seqlens[blockIdx.x], l = a.cu_seqlens[blockIdx.x + 1];
+        if (f < 0 || l < f || l > a.T) flag_status(a.dev_status, KDA_DEV_BAD_SEQLENS);
     }
-    __syncthreads();
-    const int seq = found[0];
+    int b, e;
+    const int seq = find_tile<CONV_ROWS>(a.cu_seqlens, a.N, a.T, blockIdx.x, tid & 31, b, e);
     if (seq < 0) return;
     const int slot = a.slots ? a.slots[seq] : seq;
     if (slot >= a.num_slots) {
@@ -179,8 +151,7 @@ template <typename IO, int K, int CONV_ROWS> __global__ void __launch_bounds__(C
     }
     const int c = (blockIdx.y * CT + tid) * 8;
     if (slot < 0 || c >= a.C) return;
-    const int b = a.cu_seqlens[seq], e = a.cu_seqlens[seq + 1];
-    const int r0 = b + found[1] * CONV_ROWS, r1 = min(r0 + CONV_ROWS, e);
+    const int r0 = b + ((int)blockIdx.x - b / CONV_ROWS - seq) * CONV_ROWS, r1 = min(r0 + CONV_ROWS, e);
     const size_t C = a.C;
     const IO* x = static_cast<const IO*>(a.x);
     IO* y = static_cast<IO*>(a.y);
@@ -298,7 +269,7 @@ template <typename IO, int K> cudaError_t launch_conv_decode(const ConvArgs& a, 
 
 template <typename IO, int K> cudaError_t launch_conv_varlen(const ConvArgs& a, int cols, cudaStream_t st)
 {
-    // sum of ceil(len / rows) <= N + T / rows tiles; long ones (the K-1 rows before a
+    // long tiles (the K-1 rows before a
     // tile are read again) where they still give every SM several CTAs
     if ((long long)(a.T / 128) * cols >= 8LL * sm_count())
         return launch_dependent(conv_varlen_kernel<IO, K, 128>, dim3(a.N + a.T / 128, cols), CT, 0, st, a);
@@ -332,6 +303,12 @@ int conv_call(const kda_conv_params* p, const int32_t* cu_seqlens, int32_t N, in
     const size_t state = (size_t)p->num_slots * (p->conv_kernel - 1) * row;
     if (overlap(x, T * row, y, T * row) || overlap(conv_state, state, y, T * row) || overlap(conv_state, state, x, T * row))
         return KDA_ERR_INVALID_ARGUMENT;
+    const void* lists[3] = {p->conv_weight, cu_seqlens, slots};
+    const size_t size[3] = {row / io_size(p->io_dtype) * p->conv_kernel * sizeof(float), ((size_t)N + 1) * sizeof(int32_t),
+                            (size_t)N * sizeof(int32_t)};
+    for (int i = 0; i < 3; ++i)
+        if (overlap(y, T * row, lists[i], size[i]) || overlap(conv_state, state, lists[i], size[i]))
+            return KDA_ERR_INVALID_ARGUMENT;
     if ((rc = check_device()) != KDA_OK) return rc;
     ConvArgs a;
     a.C = p->channels;
@@ -518,7 +495,7 @@ KDA_API int kda_conv_varlen(const kda_conv_params* p, const int32_t* cu_seqlens,
 {
     int rc = check_conv(p);
     if (rc != KDA_OK) return rc;
-    if (N < 0 || T < 0) return KDA_ERR_INVALID_ARGUMENT;
+    if (N < 0 || T < 0 || (int64_t)N + T / 16 > INT32_MAX) return KDA_ERR_INVALID_ARGUMENT;
     if (N == 0 || T == 0) return KDA_OK;
     if ((rc = check_ptrs({cu_seqlens})) != KDA_OK) return rc;
     return conv_call(p, cu_seqlens, N, T, x, slots, conv_state, y, dev_status, true, stream);

@@ -105,6 +105,37 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
 __device__ __forceinline__ float2 sub2(float2 a, float2 b) { return fma2(b, make_float2(-1.f, -1.f), a); }
 __device__ __forceinline__ float2 both2(float x) { return make_float2(x, x); }
 
+// ------------------------------------------------------------ tiles of sequences
+
+// Tile c of R rows of a sequence that starts at row `begin` has the number
+// begin / R + seq + c: ascending sequences never share one, and there are at
+// most T / R + N.  One warp: the sequence of tile x with its rows, or -1 for a
+// number without one.  Only sequences within [0, T] are found.  A search of 32
+// sequences at a time: 8192 CTAs that each went through 4096 sequences in turn
+// would spend longer on that than on their rows.
+template <int R>
+__device__ __forceinline__ int find_tile(const int32_t* cu, int N, int T, int x, int lane, int& begin, int& end)
+{
+    int s0 = 0;
+    for (int n = (N + 31) / 32; n > 1;) {  // s0 / 32 + 0 .. n - 1: the blocks of 32 sequences left
+        const int step = (n + 31) / 32, s = s0 + lane * step * 32;
+        const bool below = lane * step < n && min(max(cu[min(s, N)], 0), T) / R + s <= x;
+        const int l = 31 - __clz(__ballot_sync(0xffffffffu, below) | 1u);
+        s0 += l * step * 32;
+        n = min(step, n - l * step);
+    }
+    const int s = s0 + lane;
+    begin = s < N ? cu[s] : -1;
+    end = s < N ? cu[s + 1] : -1;
+    const int c = x - begin / R - s;
+    const uint32_t hit = __ballot_sync(0xffffffffu, begin >= 0 && end > begin && end <= T && c >= 0 && c < (end - begin + R - 1) / R);
+    if (!hit) return -1;
+    const int l = __ffs(hit) - 1;
+    begin = __shfl_sync(0xffffffffu, begin, l);
+    end = __shfl_sync(0xffffffffu, end, l);
+    return s0 + l;
+}
+
 // ------------------------------------------------------------ reductions
 
 __device__ __forceinline__ float warp_sum(float x)

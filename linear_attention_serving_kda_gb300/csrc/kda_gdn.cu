@@ -326,10 +326,11 @@ void fill_gdn(GdnArgs& g, const kda_gdn_params* p)
     g.vs = p->v_row_stride ? p->v_row_stride : (long long)p->num_heads_v * p->head_dim_v;
 }
 
-// Pointers of a call over `rows` rows; `out` and the states overlap no input
-// and not each other.
-int check_rows(const kda_gdn_params* p, const GdnArgs& g, int64_t rows, const void* q, const void* k, const void* v,
-               const void* gate, const void* beta, const int32_t* slots, const float* rec_state, const void* out)
+// Pointers of a call over `rows` rows of N sequences; `out`, the states and
+// the workspace (`need` bytes of it) overlap no input and not each other.
+int check_rows(const kda_gdn_params* p, const GdnArgs& g, int64_t rows, int64_t N, const int32_t* cu_seqlens, const void* q,
+               const void* k, const void* v, const void* gate, const void* beta, const int32_t* slots,
+               const float* rec_state, const void* out, const void* workspace, size_t need)
 {
     int rc;
     if ((rc = check_ptrs({q, k, v, gate, beta, rec_state, out})) != KDA_OK || (rc = check_opt(slots)) != KDA_OK)
@@ -338,13 +339,17 @@ int check_rows(const kda_gdn_params* p, const GdnArgs& g, int64_t rows, const vo
                  vw = (size_t)p->num_heads_v * p->head_dim_v;
     const size_t nout = (size_t)rows * vw * io_size(p->out_dtype);
     const size_t nstate = (size_t)p->num_slots * vw * p->head_dim_k * sizeof(float);
-    const void* in[5] = {q, k, v, gate, beta};
-    const size_t size[5] = {((rows - 1) * g.qs + kw) * io, ((rows - 1) * g.ks + kw) * io, ((rows - 1) * g.vs + vw) * io,
-                            (size_t)rows * p->num_heads_v * io, (size_t)rows * p->num_heads_v * io};
-    for (int i = 0; i < 5; ++i)
-        if (overlap(out, nout, in[i], size[i]) || overlap(rec_state, nstate, in[i], size[i]))
+    const size_t heads = (size_t)p->num_heads_v * sizeof(float);
+    const void* in[9] = {q, k, v, gate, beta, cu_seqlens, slots, p->A_log, p->dt_bias};
+    const size_t size[9] = {((rows - 1) * g.qs + kw) * io, ((rows - 1) * g.ks + kw) * io, ((rows - 1) * g.vs + vw) * io,
+                            (size_t)rows * p->num_heads_v * io, (size_t)rows * p->num_heads_v * io,
+                            (size_t)(N + 1) * sizeof(int32_t), (size_t)N * sizeof(int32_t), heads, heads};
+    for (int i = 0; i < 9; ++i)
+        if (overlap(out, nout, in[i], size[i]) || overlap(rec_state, nstate, in[i], size[i]) ||
+            overlap(workspace, need, in[i], size[i]))
             return KDA_ERR_INVALID_ARGUMENT;
-    return overlap(out, nout, rec_state, nstate) ? KDA_ERR_INVALID_ARGUMENT : KDA_OK;
+    return overlap(out, nout, rec_state, nstate) || overlap(workspace, need, out, nout) ||
+                   overlap(workspace, need, rec_state, nstate) ? KDA_ERR_INVALID_ARGUMENT : KDA_OK;
 }
 
 }  // namespace
@@ -381,8 +386,8 @@ KDA_API int kda_gdn_prefill_varlen(const kda_gdn_params* p, const int32_t* cu_se
     GdnArgs g;
     fill_gdn(g, p);
     if ((rc = check_ptrs({cu_seqlens})) != KDA_OK) return rc;
-    if ((rc = check_rows(p, g, T, q, k, v, gate, beta, slots, rec_state, out)) != KDA_OK) return rc;
     const size_t need = kda_gdn_prefill_workspace_bytes(p, N, T);
+    if ((rc = check_rows(p, g, T, N, cu_seqlens, q, k, v, gate, beta, slots, rec_state, out, workspace, need)) != KDA_OK) return rc;
     if (need > 0 && (!workspace || ws_bytes < need || !aligned16(workspace))) return KDA_ERR_WORKSPACE;
     if ((rc = check_device()) != KDA_OK) return rc;
     g.N = N;
@@ -410,7 +415,7 @@ KDA_API int kda_gdn_decode(const kda_gdn_params* p, int32_t B, const void* q, co
     if (B == 0) return KDA_OK;
     GdnArgs g;
     fill_gdn(g, p);
-    if ((rc = check_rows(p, g, B, q, k, v, gate, beta, slots, rec_state, out)) != KDA_OK) return rc;
+    if ((rc = check_rows(p, g, B, B, nullptr, q, k, v, gate, beta, slots, rec_state, out, nullptr, 0)) != KDA_OK) return rc;
     if ((rc = check_device()) != KDA_OK) return rc;
     g.N = g.T = B;
     g.q = q; g.k = k; g.v = v; g.a = gate; g.b = beta;

@@ -28,12 +28,12 @@ struct GdnArgs {
     int32_t* dev_status;
 };
 
-// The log decay never has to go below this: e^-150 is zero in fp32, and sums
-// of it over a chunk stay far from the fp32 range (an infinite one would make
-// differences of running sums NaN).  NaN passes through.
+// The log decay never has to go below this: e^-150 is zero in fp32, 2^-150 too,
+// and sums of it over a chunk stay far from the fp32 range (an infinite one
+// would make differences of running sums NaN).  NaN passes through.
 constexpr float GDN_MIN_LOG = -150.0f;
 
-// ea: e^A_log of the head.
+// ea: e^A_log of the head (times log2 e: the result counts in powers of two).
 __device__ __forceinline__ float gdn_log_alpha(float ea, float a, float dt)
 {
     const float g = -ea * softplusf_(a + dt);

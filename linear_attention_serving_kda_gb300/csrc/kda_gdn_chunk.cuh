@@ -142,8 +142,7 @@ template <int DK, bool F32> struct Slot {
     static constexpr int V = 2 * M + PARTS * 8192 + (int)sizeof(Factors);
     static_assert(V % 128 == 0, "slots on the bulk copies' and the operand tiles' boundaries");
 };
-// Chunk c of a sequence that starts at row `begin` is slot begin / 64 + seq + c:
-// sequences never share one, and there are at most T / 64 + N.
+// A slot is a tile of find_tile: at most T / 64 + N.
 __host__ __device__ __forceinline__ long long slot_count(int N, int T) { return (long long)(T / C) + N; }
 
 struct Work {
@@ -365,6 +364,7 @@ __device__ __forceinline__ void prep_task(PrepSmem<DK, F32, HEADS>& sm, const Gd
         wait(sm.loaded, turn);
         if (lane == 0) {
             // [K; Q] [K; Q]^T: k.k, q.k and, on the diagonal, both squared norms
+            ptx::tc_fence_after();  // the team has read the task before this one
             const uint32_t kq = ptx::smem_u32(sm.kq);
 #pragma unroll
             for (int kt = 0; kt < DK / 16; ++kt) {
@@ -433,7 +433,7 @@ __device__ __forceinline__ void prep_task(PrepSmem<DK, F32, HEADS>& sm, const Gd
             pow2_scale_sqrt(ss, down, up);
             if (!a.l2) {
                 // k's row factors may be far from one: a power of two out of all of them
-                float mx = fmaxf(sm.norm[lane], sm.norm[lane + 32]);
+                float mx = fmaxf(lane < n ? sm.norm[lane] : 0.f, lane + 32 < n ? sm.norm[lane + 32] : 0.f);
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
                 pow2_scale_sqrt(mx, xi, x);
@@ -674,19 +674,10 @@ gdn_prep_kernel(const GdnArgs a, const __grid_constant__ RowMaps maps, const Wor
     S& sm = *reinterpret_cast<S*>(dyn);
     const int t = threadIdx.x, lane = t & 31, groups = a.Hv / HEADS, slot = blockIdx.x / groups;
     // every warp for itself: the rows of this slot
-    int r0 = -1, n = 0;
-    for (int s0 = 0; s0 < a.N && r0 < 0; s0 += 32) {
-        const int s = s0 + lane;
-        const int b = s < a.N ? a.cu_seqlens[s] : -1, e = s < a.N ? a.cu_seqlens[s + 1] : -1;
-        const int c = slot - b / C - s;
-        const uint32_t hit = __ballot_sync(0xffffffffu, b >= 0 && e > b && e <= a.T && c >= 0 && c < (e - b + C - 1) / C);
-        if (hit) {
-            const int l = __ffs(hit) - 1;
-            r0 = __shfl_sync(0xffffffffu, b + c * C, l);
-            n = min(C, __shfl_sync(0xffffffffu, e, l) - r0);
-        }
-    }
-    if (r0 < 0) return;
+    int begin, end;
+    const int seq = find_tile<C>(a.cu_seqlens, a.N, a.T, slot, lane, begin, end);
+    if (seq < 0) return;
+    const int r0 = begin + (slot - begin / C - seq) * C, n = min(C, end - r0);
     prep_setup(sm, t);
     __syncthreads();
     ptx::tc_fence_after();
@@ -780,10 +771,11 @@ template <int N> __device__ __forceinline__ void store_split(uint32_t hi_at, uin
 }
 
 // The sequence of rank `rank` by length, longest first (ties: lowest index):
-// long chains start first.  Up to one sequence a thread; more keep their order.
+// long chains start first.  More than RANKED sequences balance in any order and keep theirs.
+constexpr int RANKED = 128;
 __device__ __forceinline__ int ranked_seq(const int32_t* cu, int N, int rank, int* found)
 {
-    if (N > (int)blockDim.x || N == 1) return rank;
+    if (N > RANKED || N == 1) return rank;
     const int t = threadIdx.x;
     if (t == 0) *found = rank;
     __syncthreads();
@@ -944,7 +936,8 @@ __device__ __forceinline__ void chain_unit(unsigned char* dyn, const GdnArgs& a,
                 mx = 0.f;
 #pragma unroll
                 for (int i = 0; i < RK; i += 2) mx = max3(mx, fabsf(r[i]), fabsf(r[i + 1]));
-                bound = last * bound + (float)C * top * x * (both(1, mx) * ru);
+                // (a wait that gave up makes it infinite: both halves see that, and still take the same turns)
+                bound = last * bound + (float)C * top * x * (both(1, wait.dead ? __int_as_float(0x7f800000) : mx) * ru);
                 const bool exact = __any_sync(0xffffffffu, !(bound * g < 0x1p14f) || (bound != 0.f && bound * g < 0x1p-6f)) ||
                                    (m & 15) == 15;
                 wait(sm.su_full, m);

@@ -156,3 +156,20 @@ def test_struct_sizes():
     assert ctypes.sizeof(k.kda_conv_params) == 24
     assert ctypes.sizeof(k.kda_norm_params) == 32 + 16
     assert ctypes.sizeof(k.kda_slot_pool) == 32
+
+
+def test_lists_and_workspace_apart_from_what_is_written():
+    p = _gdn()
+    need = kda.kda_gdn_prefill_workspace_bytes(p, 2, 8)
+    assert _prefill(p, cu=ROWS["out"]) == INVALID and _prefill(p, slots=ROWS["rec_state"] + 64) == INVALID
+    assert _decode(p, slots=ROWS["out"]) == INVALID and _decode(_gdn(A_log=ROWS["out"])) == INVALID
+    for other in ("q", "gate", "out", "rec_state"):
+        assert _prefill(p, ws=ROWS[other], nws=need) == INVALID, other
+        assert _prefill(p, ws=ROWS[other] - need + 16, nws=need) == INVALID, other
+    conv = kda.ConvParams(channels=64, conv_kernel=4, conv_weight=addr(9), num_slots=3)
+    assert kda.kda_conv_varlen(conv, addr(4), 2, 8, addr(2), None, addr(3), addr(4), None, 0) == INVALID
+    assert kda.kda_conv_decode(conv, 2, addr(2), addr(3), addr(3), addr(4), None, 0) == INVALID
+    conv = kda.ConvParams(channels=64, conv_kernel=4, conv_weight=addr(4), num_slots=3)
+    assert kda.kda_conv_varlen(conv, addr(1), 2, 8, addr(2), None, addr(3), addr(4), None, 0) == INVALID
+    conv = kda.ConvParams(channels=64, conv_kernel=4, conv_weight=addr(9), num_slots=3)
+    assert kda.kda_conv_varlen(conv, addr(1), (1 << 31) - 1, 1 << 20, addr(2), None, addr(3), addr(4), None, 0) == INVALID

@@ -328,3 +328,10 @@ def test_layer_as_served(cuda_lib):
         # seven bf16 roundings in a row on the way to h, of which the branch is about a third of h
         assert P.rel(f(first), h[:T]) <= 7 * 2.0 ** -8
         assert P.rel(f(branch[i]), h[T]) <= 7 * 2.0 ** -8
+
+
+def test_conv_thousands_of_sequences(cuda_lib):
+    lens = np.random.default_rng(2).integers(0, 40, 2500)
+    c = Conv(lens.tolist(), 16, 3, "f32", 6, slots=np.random.default_rng(3).permutation(2500).tolist())
+    c.run(cuda_lib)
+    c.check()

@@ -488,3 +488,25 @@ def test_prefill_many_heads_of_shared_keys(cuda_lib, out, Hk, Hv, dk):
     assert not _beside(c) and (c.T // 64 + c.N) * Hv > 3 * 152
     c.prefill(cuda_lib)
     c.check()
+
+
+@pytest.mark.parametrize("huge", [2.0 ** 30, float("inf"), float("nan")])
+@pytest.mark.parametrize("l2", [False, True])
+def test_prefill_keys_of_the_next_sequence_do_not_matter(cuda_lib, l2, huge):
+    """A chunk's last rows come with the next sequence's first ones: whatever stands there changes no bit."""
+    c, clean = (Case([70, 30], Hk=2, Hv=2, seed=90, out="f32", l2=l2) for _ in range(2))
+    clean.prefill(cuda_lib)
+    clean.check()
+    c.k[70:90] *= huge
+    c.prefill(cuda_lib)
+    assert torch.equal(c.g_out.tensor[:70], clean.g_out.tensor[:70])
+    assert torch.equal(c.g_state.tensor[0], clean.g_state.tensor[0])
+
+
+@pytest.mark.parametrize("N", [33, 1100])
+def test_prefill_many_sequences(cuda_lib, N):
+    lens = np.random.default_rng(N).integers(0, 4, N)
+    lens[N // 2] = 140
+    c = Case(lens.tolist(), Hk=1, Hv=2, dk=32, dv=32, seed=91, slots=np.random.default_rng(1).permutation(N).tolist())
+    c.prefill(cuda_lib)
+    c.check()
