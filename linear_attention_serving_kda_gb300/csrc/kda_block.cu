@@ -131,8 +131,9 @@ constexpr int CONV_AHEAD = 8; // rows loaded at a time, a batch ahead of the one
 
 // Tiles start at a sequence's first row, so only its tile 0 reads the old
 // state: that CTA also writes the new one, after its reads, and no other CTA
-// touches the slot.  blockIdx.x counts tiles over the sequences.
-template <typename IO, int K, int CONV_ROWS> __global__ void __launch_bounds__(CT) conv_varlen_kernel(const ConvArgs a)
+// touches the slot.  blockIdx.x counts tiles over the sequences.  Six CTAs an SM: five
+// (174 registers) took 199 us where these take 178.
+template <typename IO, int K, int CONV_ROWS> __global__ void __launch_bounds__(CT, sizeof(IO) == 2 ? 6 : 1) conv_varlen_kernel(const ConvArgs a)
 {
     ptx::grid_launch_dependents();
     ptx::grid_dependency_wait();

@@ -21,7 +21,7 @@ size_t gdn_chunk_workspace_bytes(int Hk, int Hv, int dk, bool out_bf16, int N, i
 {
     const size_t b = dk == 128 ? slot_bytes<128>(Hk, Hv, out_bf16) : dk == 64 ? slot_bytes<64>(Hk, Hv, out_bf16)
                                                                              : slot_bytes<32>(Hk, Hv, out_bf16);
-    return (size_t)slot_count(N, T) * b;
+    return (size_t)slot_count(N, T) * b + sizeof(int);
 }
 
 cudaError_t launch_gdn_chunk(const GdnArgs& a, int dk, int dv, bool out_bf16, cudaStream_t st)

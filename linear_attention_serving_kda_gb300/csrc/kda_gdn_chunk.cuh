@@ -148,7 +148,9 @@ __host__ __device__ __forceinline__ long long slot_count(int N, int T) { return 
 struct Work {
     unsigned char* kq;  // [slot][Hk]
     unsigned char* v;   // [slot][Hv]
-    int* ready;         // [slot][Hv], where chains run beside prep: 1 once the slot is written
+    // where chains run beside prep: [slot][Hv], 1 once the slot is written; then the number of units taken
+    int* ready;
+    int* taken;
 };
 
 // ------------------------------------------------------------ prep
@@ -183,7 +185,7 @@ template <int DK, bool F32, int HEADS> struct PrepSmem {
     uint32_t tmem;
 };
 
-// Barriers of a team of prep warps, and of the four of them that invert T; a CTA has up to two teams.
+// Barriers of a team of prep warps, and of the four of them that invert T; a CTA has up to three teams.
 __device__ __forceinline__ void team_sync(int team) { asm volatile("bar.sync %0, 256;" ::"r"(1 + 2 * team) : "memory"); }
 __device__ __forceinline__ void invert_sync(int team) { asm volatile("bar.sync %0, 128;" ::"r"(2 + 2 * team) : "memory"); }
 
@@ -658,8 +660,6 @@ template <int DK, bool F32, int HEADS> __device__ __forceinline__ void prep_setu
         ptx::mbar_init(&sm.prod, 1);
         ptx::fence_mbar_init();
     }
-    if (t / 32 == 1) ptx::tmem_alloc(&sm.tmem, 128);
-    ptx::tc_fence_before();
 }
 
 // A task a CTA.
@@ -679,6 +679,8 @@ gdn_prep_kernel(const GdnArgs a, const __grid_constant__ RowMaps maps, const Wor
     if (seq < 0) return;
     const int r0 = begin + (slot - begin / C - seq) * C, n = min(C, end - r0);
     prep_setup(sm, t);
+    if (t / 32 == 1) ptx::tmem_alloc(&sm.tmem, 128);
+    ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
     Waiter wait{false};
@@ -696,6 +698,11 @@ gdn_prep_kernel(const GdnArgs a, const __grid_constant__ RowMaps maps, const Wor
 constexpr int TM_X = 0, TM_SH = 128, TM_SL = 192, TM_RH = 256, TM_RL = 288, TM_QS = 320, TM_PR = 384, TM_COLS = 512;
 constexpr int CHAIN_THREADS = 640;
 
+// A sequence's rows, its state and value head.
+struct Unit {
+    int seq, begin, end, slot, h;
+};
+
 template <int DK, int DV, bool F32> struct ChainSmem {
     using L = Slot<DK, F32>;
     unsigned char kq[2][L::KQ];
@@ -706,8 +713,8 @@ template <int DK, int DV, bool F32> struct ChainSmem {
     float top[3][2][DV];         // the largest values of beta V's, R's and S's halves of a column
     uint64_t loaded[2], freed[2];
     uint64_t s_full, ks_full, qs_full, rh_full, rl_full, su_full, o_full, o_free, f_full[2];
-    uint32_t tmem;
     int found;
+    Unit unit;
 };
 
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(a, fmaxf(b, c)); }
@@ -799,21 +806,31 @@ template <bool UP, int N> __device__ __forceinline__ void set_regs()
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// The chain of sequence rank unit / Hv and value head unit % Hv.  FLAGS: prep
-// runs beside it, and each slot's flag says when the slot is there.
-template <int DK, int DV, bool F32, bool FLAGS>
-__device__ __forceinline__ void chain_unit(unsigned char* dyn, const GdnArgs& a, const CUtensorMap& vmap, const Work& ws, int unit)
+// The chain's 640 threads.
+__device__ __forceinline__ void chain_sync() { asm volatile("bar.sync 7, 640;" ::: "memory"); }
+
+// What a CTA's chain units are.  One for each CTA:
+struct OneUnit {
+    static constexpr bool BESIDE = false;
+    Unit u;
+    template <class S> __device__ __forceinline__ bool next(S&, const GdnArgs&, const Work&, int turn, Unit& out)
+    {
+        out = u;
+        return turn == 0;
+    }
+};
+
+// The chains of one unit after the other.  The barriers' phases, the buffers
+// and TMEM go on from unit to unit: only `q`, the chunk's number among all of the
+// CTA's, counts for them.  tmem: all of it; freed here.
+template <int DK, int DV, bool F32, class Units>
+__device__ __forceinline__ void run_chains(unsigned char* dyn, const GdnArgs& a, const CUtensorMap& vmap, const Work& ws, uint32_t tmem, Units units)
 {
     constexpr int NW = DV / 32;
     using S = ChainSmem<DK, DV, F32>;
     using L = Slot<DK, F32>;
     S& sm = *reinterpret_cast<S*>(dyn);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int h = unit % a.Hv;
-    const int seq = ranked_seq(a.cu_seqlens, a.N, unit / a.Hv, &sm.found);
-    int begin, end, state_slot;
-    if (!gdn_unit(a, seq, begin, end, state_slot)) return;
-    const int chunks = (end - begin + C - 1) / C;
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
@@ -831,15 +848,15 @@ __device__ __forceinline__ void chain_unit(unsigned char* dyn, const GdnArgs& a,
         ptx::mbar_init(&sm.o_free, 2 * NW);
         ptx::fence_mbar_init();
     }
-    if (warp == 8) ptx::tmem_alloc(&sm.tmem, TM_COLS);
-    ptx::tc_fence_before();
-    __syncthreads();
-    ptx::tc_fence_after();
-    const uint32_t tmem = sm.tmem;
+    chain_sync();
     Waiter wait{false};
+    Unit u;
+    int q0 = 0;  // chunks of the units before
 
-    // Registers: the launch gives every thread 96; the chain's two warpgroups
-    // take what the others leave (2 * 144 + 64 + 2 * 64 <= 5 * 96).
+    // Registers: the launch gives every thread 96 (beside prep: 80, and there is a
+    // sixth warpgroup); the chain's two warpgroups take what the others leave
+    // (2 * 144 + 3 * 64 = 5 * 96; 2 * 144 + 3 * 56 + 24 = 6 * 80).
+    constexpr int FEW = Units::BESIDE ? 56 : 64;
     if (warp < 8) {
         set_regs<true, 144>();
         if ((warp & 3) < NW) {
@@ -848,296 +865,319 @@ __device__ __forceinline__ void chain_unit(unsigned char* dyn, const GdnArgs& a,
             constexpr int SK = DK / 2, RK = C / 2;
             const int pair = warp & 3, half = warp >> 2, c = pair * 32 + lane;
             const uint32_t at = tmem + ((uint32_t)(pair * 32) << 16);
-            float* state = a.state + ((size_t)state_slot * a.Hv + h) * DK * DV + (size_t)half * SK * DV + c;
             // the larger of both halves' largest values
             auto both = [&](int which, float x) {
                 sm.top[which][half][c] = x;
                 asm volatile("bar.sync %0, 64;" ::"r"(pair + 1) : "memory");
                 return fmaxf(x, sm.top[which][half ^ 1][c]);
             };
-            // A bound on the column's values (the same in both halves): while it stays
-            // below 2^14 in S's scale, fp16 has room; the exact value now and then
-            // and where it does not.
-            float s[SK], mx = 0.f, bound, g, ig;
+            for (int turn = 0; units.next(sm, a, ws, turn, u); ++turn) {
+                const int begin = u.begin, end = u.end, chunks = (end - begin + C - 1) / C;
+                float* state = a.state + ((size_t)u.slot * a.Hv + u.h) * DK * DV + (size_t)half * SK * DV + c;
+                // A bound on the column's values (the same in both halves): while it stays
+                // below 2^14 in S's scale, fp16 has room; the exact value now and then
+                // and where it does not.
+                float s[SK], mx = 0.f, bound, g, ig;
 #pragma unroll
-            for (int i = 0; i < SK; ++i) s[i] = state[(size_t)i * DV];
+                for (int i = 0; i < SK; ++i) s[i] = state[(size_t)i * DV];
 #pragma unroll
-            for (int i = 0; i < SK; i += 2) mx = max3(mx, fabsf(s[i]), fabsf(s[i + 1]));
-            bound = both(2, mx);
-            pow2_scale(bound, g, ig);
+                for (int i = 0; i < SK; i += 2) mx = max3(mx, fabsf(s[i]), fabsf(s[i + 1]));
+                bound = both(2, mx);
+                pow2_scale(bound, g, ig);
 #pragma unroll
-            for (int i = 0; i < SK; ++i) s[i] *= g;
-            for (int m = 0; m < chunks; ++m) {
-                const int b = m & 1, n = end - begin - m * C;
-                if (m > 0) wait(sm.qs_full, m - 1);  // S's place is free
-                store_split<SK>(at + TM_SH + half * (SK / 2), at + TM_SL + half * (SK / 2), s);
-                ptx::tc_fence_before();
-                warp_arrive(sm.s_full, lane);
+                for (int i = 0; i < SK; ++i) s[i] *= g;
+                for (int m = 0; m < chunks; ++m) {
+                    const int q = q0 + m, b = q & 1, n = end - begin - m * C;
+                    if (q > 0) wait(sm.qs_full, q - 1);  // S's place is free
+                    store_split<SK>(at + TM_SH + half * (SK / 2), at + TM_SL + half * (SK / 2), s);
+                    ptx::tc_fence_before();
+                    warp_arrive(sm.s_full, lane);
 
-                // R = beta V - beta e^G k.S, times rd
-                wait(sm.loaded[b], m >> 1);
-                const Factors& fac = sm.fac[m & 3];
-                const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(sm.v[b]) + half * RK * DV + c;
-                float r[RK];
+                    // R = beta V - beta e^G k.S, times rd
+                    wait(sm.loaded[b], q >> 1);
+                    const Factors& fac = sm.fac[q & 3];
+                    const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(sm.v[b]) + half * RK * DV + c;
+                    float r[RK];
 #pragma unroll
-                for (int i = 0; i < RK; i += 2) {
-                    const float2 be = *reinterpret_cast<const float2*>(&fac.beta[half * RK + i]);
-                    const float2 x = mul2(be, make_float2(__bfloat162float(v[i * DV]), __bfloat162float(v[(i + 1) * DV])));
-                    r[i] = x.x;
-                    r[i + 1] = x.y;
-                }
-                if (n < C)  // the copies took the next sequence's rows along
-#pragma unroll
-                    for (int i = 0; i < RK; ++i) r[i] = half * RK + i < n ? r[i] : 0.f;
-                mx = 0.f;
-#pragma unroll
-                for (int i = 0; i < RK; i += 2) mx = max3(mx, fabsf(r[i]), fabsf(r[i + 1]));
-                // |k'| < 2, so |k'.S| <= 2 sqrt(dk) max |S|: R stays below 2^14 in the scale of this
-                // bound, and low parts do not mind how far below
-                float rd, ru;
-                pow2_scale(both(0, mx) + fac.ektop * (DK == 128 ? 23.f : DK == 64 ? 16.f : 12.f) * bound, rd, ru);
-                rd *= 0x1p13f;
-                ru *= 0x1p-13f;
-                scale_all(r, rd);
-                const float last = fac.last, x = fac.x, top = fac.top;
-                if (m > 0) wait(sm.o_full, m - 1);  // R's place is free
-                wait(sm.ks_full, m);
-                ptx::tc_fence_after();
-                const float fr = ig * rd;
-#pragma unroll
-                for (int q = 0; q < RK; q += 16) {
-                    float d[16], e[16];
-                    ptx::tmem_ld16(at + TM_X + half * RK + q, d);
-                    ptx::tmem_ld16(at + TM_X + C + half * RK + q, e);
-#pragma unroll
-                    for (int i = 0; i < 16; i += 2) {
-                        const float2 ek = *reinterpret_cast<const float2*>(&fac.ek[half * RK + q + i]);
-                        const float2 ks = mul2(add2(make_float2(d[i], d[i + 1]), make_float2(e[i], e[i + 1])), both2(-fr));
-                        const float2 x = fma2(ek, ks, make_float2(r[q + i], r[q + i + 1]));
-                        r[q + i] = x.x;
-                        r[q + i + 1] = x.y;
+                    for (int i = 0; i < RK; i += 2) {
+                        const float2 be = *reinterpret_cast<const float2*>(&fac.beta[half * RK + i]);
+                        const float2 x = mul2(be, make_float2(__bfloat162float(v[i * DV]), __bfloat162float(v[(i + 1) * DV])));
+                        r[i] = x.x;
+                        r[i + 1] = x.y;
                     }
-                }
-                store_high<RK>(at + TM_RH + half * (RK / 2), r);
-                ptx::tc_fence_before();
-                warp_arrive(sm.rh_full, lane);
-                store_low<RK>(at + TM_RL + half * (RK / 2), r);
-                ptx::tc_fence_before();
-                warp_arrive(sm.rl_full, lane);
-                if (half == 0) {
-                    sm.f1[b][c] = ig;
-                    sm.f2[b][c] = ru * x;
-                    warp_arrive(sm.f_full[b], lane);
-                }
-
-                // S = e^{G_C} S + M^T R
-                scale_all(s, last);
-                const float fs = (ru * x) * g;
-                mx = 0.f;
+                    if (n < C)  // the copies took the next sequence's rows along
 #pragma unroll
-                for (int i = 0; i < RK; i += 2) mx = max3(mx, fabsf(r[i]), fabsf(r[i + 1]));
-                // (a wait that gave up makes it infinite: both halves see that, and still take the same turns)
-                bound = last * bound + (float)C * top * x * (both(1, wait.dead ? __int_as_float(0x7f800000) : mx) * ru);
-                const bool exact = __any_sync(0xffffffffu, !(bound * g < 0x1p14f) || (bound != 0.f && bound * g < 0x1p-6f)) ||
-                                   (m & 15) == 15;
-                wait(sm.su_full, m);
-                ptx::tc_fence_after();
-                constexpr int W = SK < 32 ? SK : 32;
-#pragma unroll
-                for (int q = 0; q < SK; q += W) {
-                    float d[W];
-                    if constexpr (W == 32) ptx::tmem_ld32(at + TM_X + half * SK + q, d);
-                    else ptx::tmem_ld16(at + TM_X + half * SK + q, d);
-#pragma unroll
-                    for (int i = 0; i < W; i += 2) {
-                        const float2 x = fma2(both2(fs), make_float2(d[i], d[i + 1]), make_float2(s[q + i], s[q + i + 1]));
-                        s[q + i] = x.x;
-                        s[q + i + 1] = x.y;
-                    }
-                }
-                if (exact) {
+                        for (int i = 0; i < RK; ++i) r[i] = half * RK + i < n ? r[i] : 0.f;
                     mx = 0.f;
 #pragma unroll
-                    for (int i = 0; i < SK; i += 2) mx = max3(mx, fabsf(s[i]), fabsf(s[i + 1]));
-                    bound = both(2, mx) * ig;
-                    float down, up;
-                    pow2_scale(bound, down, up);
-                    const float f = down * ig;
-                    scale_all(s, f);
-                    g = down;
-                    ig = up;
-                }
-                warp_arrive(sm.freed[b], lane);
-            }
+                    for (int i = 0; i < RK; i += 2) mx = max3(mx, fabsf(r[i]), fabsf(r[i + 1]));
+                    // |k'| < 2, so |k'.S| <= 2 sqrt(dk) max |S|: R stays below 2^14 in the scale of this
+                    // bound, and low parts do not mind how far below
+                    float rd, ru;
+                    pow2_scale(both(0, mx) + fac.ektop * (DK == 128 ? 23.f : DK == 64 ? 16.f : 12.f) * bound, rd, ru);
+                    rd *= 0x1p13f;
+                    ru *= 0x1p-13f;
+                    scale_all(r, rd);
+                    const float last = fac.last, x = fac.x, top = fac.top;
+                    if (q > 0) wait(sm.o_full, q - 1);  // R's place is free
+                    wait(sm.ks_full, q);
+                    ptx::tc_fence_after();
+                    const float fr = ig * rd;
 #pragma unroll
-            for (int i = 0; i < SK; ++i) state[(size_t)i * DV] = s[i] * ig;
-        }
+                    for (int z = 0; z < RK; z += 16) {
+                        float d[16], e[16];
+                        ptx::tmem_ld16(at + TM_X + half * RK + z, d);
+                        ptx::tmem_ld16(at + TM_X + C + half * RK + z, e);
+#pragma unroll
+                        for (int i = 0; i < 16; i += 2) {
+                            const float2 ek = *reinterpret_cast<const float2*>(&fac.ek[half * RK + z + i]);
+                            const float2 ks = mul2(add2(make_float2(d[i], d[i + 1]), make_float2(e[i], e[i + 1])), both2(-fr));
+                            const float2 x = fma2(ek, ks, make_float2(r[z + i], r[z + i + 1]));
+                            r[z + i] = x.x;
+                            r[z + i + 1] = x.y;
+                        }
+                    }
+                    store_high<RK>(at + TM_RH + half * (RK / 2), r);
+                    ptx::tc_fence_before();
+                    warp_arrive(sm.rh_full, lane);
+                    store_low<RK>(at + TM_RL + half * (RK / 2), r);
+                    ptx::tc_fence_before();
+                    warp_arrive(sm.rl_full, lane);
+                    if (half == 0) {
+                        sm.f1[b][c] = ig;
+                        sm.f2[b][c] = ru * x;
+                        warp_arrive(sm.f_full[b], lane);
+                    }
+
+                    // S = e^{G_C} S + M^T R
+                    scale_all(s, last);
+                    const float fs = (ru * x) * g;
+                    mx = 0.f;
+#pragma unroll
+                    for (int i = 0; i < RK; i += 2) mx = max3(mx, fabsf(r[i]), fabsf(r[i + 1]));
+                    // (a wait that gave up makes it infinite: both halves see that, and still take the same turns)
+                    bound = last * bound + (float)C * top * x * (both(1, wait.dead ? __int_as_float(0x7f800000) : mx) * ru);
+                    const bool exact = __any_sync(0xffffffffu, !(bound * g < 0x1p14f) || (bound != 0.f && bound * g < 0x1p-6f)) ||
+                                       (m & 15) == 15;
+                    wait(sm.su_full, q);
+                    ptx::tc_fence_after();
+                    constexpr int W = SK < 32 ? SK : 32;
+#pragma unroll
+                    for (int z = 0; z < SK; z += W) {
+                        float d[W];
+                        if constexpr (W == 32) ptx::tmem_ld32(at + TM_X + half * SK + z, d);
+                        else ptx::tmem_ld16(at + TM_X + half * SK + z, d);
+#pragma unroll
+                        for (int i = 0; i < W; i += 2) {
+                            const float2 x = fma2(both2(fs), make_float2(d[i], d[i + 1]), make_float2(s[z + i], s[z + i + 1]));
+                            s[z + i] = x.x;
+                            s[z + i + 1] = x.y;
+                        }
+                    }
+                    if (exact) {
+                        mx = 0.f;
+#pragma unroll
+                        for (int i = 0; i < SK; i += 2) mx = max3(mx, fabsf(s[i]), fabsf(s[i + 1]));
+                        bound = both(2, mx) * ig;
+                        float down, up;
+                        pow2_scale(bound, down, up);
+                        const float f = down * ig;
+                        scale_all(s, f);
+                        g = down;
+                        ig = up;
+                    }
+                    warp_arrive(sm.freed[b], lane);
+                }
+#pragma unroll
+                for (int i = 0; i < SK; ++i) state[(size_t)i * DV] = s[i] * ig;
+                q0 += chunks;
+            }
+        } else
+            for (int turn = 0; units.next(sm, a, ws, turn, u);) ++turn;
     } else if (warp < 12) {
-        set_regs<false, 64>();
+        set_regs<false, FEW>();
         auto kq_step = [](int kt) { return (uint64_t)((kt >> 2) * (16384 >> 4) + (kt & 3) * 2); };
         constexpr uint32_t id = ptx::idesc_f16(128, C), idm = ptx::idesc_f16(128, DK);
         if (warp == 8) {
             const uint64_t policy = ptx::policy_evict_first();
-            const long long slot0 = begin / C + seq;
-            for (int m = 0; m < chunks; ++m) {
-                const int b = m & 1;
-                // a chunk's operands are free once its products are through; its factors
-                // are read a little longer, while its outputs are formed: a ring of four
-                if (m >= 2) wait(sm.freed[b], (m - 2) >> 1);
-                if (FLAGS) {
-                    // this head's slot, and that of the key head's first, which brings [K; Q]
-                    const int* f = ws.ready + (slot0 + m) * a.Hv;
-                    const int lead = h / (a.Hv / a.Hk) * (a.Hv / a.Hk);
-                    if (!wait.dead && !(ptx::wait_flag_ge(f + lead, 1) && ptx::wait_flag_ge(f + h, 1))) wait.dead = true;
-                    ptx::fence_proxy_async_global();
+            for (int turn = 0; units.next(sm, a, ws, turn, u); ++turn) {
+                const int begin = u.begin, end = u.end, chunks = (end - begin + C - 1) / C;
+                const int h = u.h;
+                const long long slot0 = begin / C + u.seq;
+                for (int m = 0; m < chunks; ++m) {
+                    const int q = q0 + m, b = q & 1;
+                    // a chunk's operands are free once its products are through; its factors
+                    // are read a little longer, while its outputs are formed: a ring of four
+                    if (q >= 2) wait(sm.freed[b], (q - 2) >> 1);
+                    if (Units::BESIDE) {
+                        // this head's slot, and that of the key head's first, which brings [K; Q]
+                        const int* f = ws.ready + (slot0 + m) * a.Hv;
+                        const int lead = h / (a.Hv / a.Hk) * (a.Hv / a.Hk);
+                        if (!wait.dead && !(ptx::wait_flag_ge(f + lead, 1) && ptx::wait_flag_ge(f + h, 1))) wait.dead = true;
+                        ptx::fence_proxy_async_global();
+                    }
+                    if (lane == 0) {
+                        uint64_t* bar = &sm.loaded[b];
+                        const unsigned char* w = ws.v + ((slot0 + m) * a.Hv + h) * L::V;
+                        ptx::mbar_arrive_expect_tx(bar, L::KQ + L::V + C * DV * 2);
+                        ptx::bulk_g2s(sm.kq[b], ws.kq + ((slot0 + m) * a.Hk + h / (a.Hv / a.Hk)) * L::KQ, L::KQ, bar);
+                        ptx::tma_load_2d(sm.v[b], &vmap, h * DV, begin + m * C, bar, policy);
+                        ptx::bulk_g2s_stream(&sm.fac[q & 3], w + sizeof(sm.work[0]), sizeof(Factors), bar, policy);
+                        ptx::bulk_g2s_stream(sm.work[b], w, sizeof(sm.work[0]), bar, policy);
+                    }
+                    __syncwarp();
                 }
-                if (lane == 0) {
-                    uint64_t* bar = &sm.loaded[b];
-                    const unsigned char* w = ws.v + ((slot0 + m) * a.Hv + h) * L::V;
-                    ptx::mbar_arrive_expect_tx(bar, L::KQ + L::V + C * DV * 2);
-                    ptx::bulk_g2s(sm.kq[b], ws.kq + ((slot0 + m) * a.Hk + h / (a.Hv / a.Hk)) * L::KQ, L::KQ, bar);
-                    ptx::tma_load_2d(sm.v[b], &vmap, h * DV, begin + m * C, bar, policy);
-                    ptx::bulk_g2s_stream(&sm.fac[m & 3], w + sizeof(sm.work[0]), sizeof(Factors), bar, policy);
-                    ptx::bulk_g2s_stream(sm.work[b], w, sizeof(sm.work[0]), bar, policy);
-                }
-                __syncwarp();
+                q0 += chunks;
             }
         } else if (warp == 9 || warp == 10) {
             // The critical products from two threads (one issues at half the
             // tensor core's rate): K S of S's high parts and M^T R, K S of its low parts.
             const bool first = warp == 9;
-            for (int m = 0; m < chunks; ++m) {
-                const int b = m & 1;
-                wait(sm.loaded[b], m >> 1);
-                wait(sm.s_full, m);
-                ptx::tc_fence_after();
-                const uint64_t k = ptx::desc_sw128(ptx::smem_u32(sm.kq[b]));
-                const uint64_t mh = ptx::desc_sw128(ptx::smem_u32(sm.work[b])), ml = mh + (L::M >> 4);
-                if (lane == 0) {
-                    const uint32_t d = tmem + TM_X + (first ? 0 : C), s = tmem + (first ? TM_SH : TM_SL);
+            for (int turn = 0; units.next(sm, a, ws, turn, u); ++turn) {
+                const int chunks = (u.end - u.begin + C - 1) / C;
+                for (int m = 0; m < chunks; ++m) {
+                    const int q = q0 + m, b = q & 1;
+                    wait(sm.loaded[b], q >> 1);
+                    wait(sm.s_full, q);
+                    ptx::tc_fence_after();
+                    const uint64_t k = ptx::desc_sw128(ptx::smem_u32(sm.kq[b]));
+                    const uint64_t mh = ptx::desc_sw128(ptx::smem_u32(sm.work[b])), ml = mh + (L::M >> 4);
+                    if (lane == 0) {
+                        const uint32_t d = tmem + TM_X + (first ? 0 : C), s = tmem + (first ? TM_SH : TM_SL);
 #pragma unroll
-                    for (int kt = 0; kt < DK / 16; ++kt) ptx::mma_bf16_ts(d, s + kt * 8, k + kq_step(kt), id, kt > 0);
-                    ptx::mma_commit(&sm.ks_full);
+                        for (int kt = 0; kt < DK / 16; ++kt) ptx::mma_bf16_ts(d, s + kt * 8, k + kq_step(kt), id, kt > 0);
+                        ptx::mma_commit(&sm.ks_full);
+                    }
+                    __syncwarp();
+                    if (!first) continue;
+                    wait(sm.rh_full, q);
+                    ptx::tc_fence_after();
+                    if (lane == 0) {
+#pragma unroll
+                        for (int kt = 0; kt < 4; ++kt)
+                            ptx::mma_bf16_ts(tmem + TM_X, tmem + TM_RH + kt * 8, mh + kt * 2, idm, kt > 0);
+#pragma unroll
+                        for (int kt = 0; kt < 4; ++kt)
+                            ptx::mma_bf16_ts(tmem + TM_X, tmem + TM_RH + kt * 8, ml + kt * 2, idm, 1);
+                    }
+                    __syncwarp();
+                    wait(sm.rl_full, q);
+                    ptx::tc_fence_after();
+                    if (lane == 0) {
+#pragma unroll
+                        for (int kt = 0; kt < 4; ++kt)
+                            ptx::mma_bf16_ts(tmem + TM_X, tmem + TM_RL + kt * 8, mh + kt * 2, idm, 1);
+                        ptx::mma_commit(&sm.su_full);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
-                if (!first) continue;
-                wait(sm.rh_full, m);
-                ptx::tc_fence_after();
-                if (lane == 0) {
-#pragma unroll
-                    for (int kt = 0; kt < 4; ++kt)
-                        ptx::mma_bf16_ts(tmem + TM_X, tmem + TM_RH + kt * 8, mh + kt * 2, idm, kt > 0);
-#pragma unroll
-                    for (int kt = 0; kt < 4; ++kt)
-                        ptx::mma_bf16_ts(tmem + TM_X, tmem + TM_RH + kt * 8, ml + kt * 2, idm, 1);
-                }
-                __syncwarp();
-                wait(sm.rl_full, m);
-                ptx::tc_fence_after();
-                if (lane == 0) {
-#pragma unroll
-                    for (int kt = 0; kt < 4; ++kt)
-                        ptx::mma_bf16_ts(tmem + TM_X, tmem + TM_RL + kt * 8, mh + kt * 2, idm, 1);
-                    ptx::mma_commit(&sm.su_full);
-                }
-                __syncwarp();
+                q0 += chunks;
             }
         } else {
             // the outputs' products, each behind the critical ones of its kind
-            for (int m = 0; m < chunks; ++m) {
-                const int b = m & 1;
-                if (m > 0) wait(sm.o_free, m - 1);
-                wait(sm.loaded[b], m >> 1);
-                wait(sm.ks_full, m);
-                ptx::tc_fence_after();
-                const uint64_t q = ptx::desc_sw128(ptx::smem_u32(sm.kq[b]) + 8192);
-                const uint64_t pt = ptx::desc_sw128(ptx::smem_u32(sm.work[b]) + 2 * L::M);
-                if (lane == 0) {
-#pragma unroll
-                    for (int kt = 0; kt < DK / 16; ++kt)
-                        ptx::mma_bf16_ts(tmem + TM_QS, tmem + TM_SH + kt * 8, q + kq_step(kt), id, kt > 0);
-                    if (F32)
+            for (int turn = 0; units.next(sm, a, ws, turn, u); ++turn) {
+                const int chunks = (u.end - u.begin + C - 1) / C;
+                for (int m = 0; m < chunks; ++m) {
+                    const int q = q0 + m, b = q & 1;
+                    if (q > 0) wait(sm.o_free, q - 1);
+                    wait(sm.loaded[b], q >> 1);
+                    wait(sm.ks_full, q);
+                    ptx::tc_fence_after();
+                    const uint64_t qd = ptx::desc_sw128(ptx::smem_u32(sm.kq[b]) + 8192);
+                    const uint64_t pt = ptx::desc_sw128(ptx::smem_u32(sm.work[b]) + 2 * L::M);
+                    if (lane == 0) {
 #pragma unroll
                         for (int kt = 0; kt < DK / 16; ++kt)
-                            ptx::mma_bf16_ts(tmem + TM_QS, tmem + TM_SL + kt * 8, q + kq_step(kt), id, 1);
-                    ptx::mma_commit(&sm.qs_full);
-                }
-                __syncwarp();
-                wait(sm.su_full, m);
-                ptx::tc_fence_after();
-                if (lane == 0) {
+                            ptx::mma_bf16_ts(tmem + TM_QS, tmem + TM_SH + kt * 8, qd + kq_step(kt), id, kt > 0);
+                        if (F32)
 #pragma unroll
-                    for (int kt = 0; kt < 4; ++kt)
-                        ptx::mma_bf16_ts(tmem + TM_PR, tmem + TM_RH + kt * 8, pt + kt * 2, id, kt > 0);
-                    if (F32)
+                            for (int kt = 0; kt < DK / 16; ++kt)
+                                ptx::mma_bf16_ts(tmem + TM_QS, tmem + TM_SL + kt * 8, qd + kq_step(kt), id, 1);
+                        ptx::mma_commit(&sm.qs_full);
+                    }
+                    __syncwarp();
+                    wait(sm.su_full, q);
+                    ptx::tc_fence_after();
+                    if (lane == 0) {
 #pragma unroll
-                        for (int kt = 0; kt < 4; ++kt) {
-                            ptx::mma_bf16_ts(tmem + TM_PR, tmem + TM_RL + kt * 8, pt + kt * 2, id, 1);
-                            ptx::mma_bf16_ts(tmem + TM_PR, tmem + TM_RH + kt * 8, pt + (8192 >> 4) + kt * 2, id, 1);
-                        }
-                    ptx::mma_commit(&sm.o_full);
-                    ptx::mma_commit(&sm.freed[b]);
+                        for (int kt = 0; kt < 4; ++kt)
+                            ptx::mma_bf16_ts(tmem + TM_PR, tmem + TM_RH + kt * 8, pt + kt * 2, id, kt > 0);
+                        if (F32)
+#pragma unroll
+                            for (int kt = 0; kt < 4; ++kt) {
+                                ptx::mma_bf16_ts(tmem + TM_PR, tmem + TM_RL + kt * 8, pt + kt * 2, id, 1);
+                                ptx::mma_bf16_ts(tmem + TM_PR, tmem + TM_RH + kt * 8, pt + (8192 >> 4) + kt * 2, id, 1);
+                            }
+                        ptx::mma_commit(&sm.freed[b]);
+                        ptx::mma_commit(&sm.o_full);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
+                q0 += chunks;
             }
         }
     } else {
-        set_regs<false, 64>();
+        set_regs<false, FEW>();
         if ((warp & 3) < NW) {
             // column c of the outputs: o_r = e1 q'.S + e2 (P T R)_r, for half of the rows
             const int w = warp & 3, c = w * 32 + lane, half = (warp - 12) >> 2;
             const uint32_t at = tmem + ((uint32_t)(w * 32) << 16);
             const size_t row_stride = (size_t)a.Hv * DV;
-            for (int m = 0; m < chunks; ++m) {
-                const int b = m & 1, n = min(C, end - begin - m * C);
-                wait(sm.f_full[b], m >> 1);
-                const float f1 = sm.f1[b][c], f2 = sm.f2[b][c];
-                const Factors& fac = sm.fac[m & 3];
-                const size_t o0 = ((size_t)begin + (size_t)m * C) * row_stride + (size_t)h * DV;
-                wait(sm.o_full, m);
-                ptx::tc_fence_after();
+            for (int turn = 0; units.next(sm, a, ws, turn, u); ++turn) {
+                const int begin = u.begin, end = u.end, chunks = (end - begin + C - 1) / C;
+                for (int m = 0; m < chunks; ++m) {
+                    const int q = q0 + m, b = q & 1, n = min(C, end - begin - m * C);
+                    wait(sm.f_full[b], q >> 1);
+                    const float f1 = sm.f1[b][c], f2 = sm.f2[b][c];
+                    const Factors& fac = sm.fac[q & 3];
+                    const size_t o0 = ((size_t)begin + (size_t)m * C) * row_stride + (size_t)u.h * DV;
+                    wait(sm.o_full, q);
+                    ptx::tc_fence_after();
 #pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                    const int i0 = half * (C / 2) + z * 16;
-                    float x[16], y[16];
-                    ptx::tmem_ld16(at + TM_QS + i0, x);
-                    ptx::tmem_ld16(at + TM_PR + i0, y);
-                    if (z == 1) {
-                        ptx::tc_fence_before();
-                        warp_arrive(sm.o_free, lane);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 16; i += 2) {
-                        const float2 e1 = *reinterpret_cast<const float2*>(&fac.e1[i0 + i]);
-                        const float2 e2 = *reinterpret_cast<const float2*>(&fac.e2[i0 + i]);
-                        const float2 o = fma2(e1, mul2(both2(f1), make_float2(x[i], x[i + 1])),
-                                              mul2(e2, mul2(both2(f2), make_float2(y[i], y[i + 1]))));
-                        x[i] = o.x;
-                        x[i + 1] = o.y;
-                    }
-                    if constexpr (F32) {
-                        float* p = static_cast<float*>(a.out) + o0 + c + i0 * row_stride;
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (i0 + i < n) p[i * row_stride] = x[i];
-                    } else {
-                        // neighbouring lanes trade a value: even ones write two columns of row i, odd ones of row i + 1
-                        __nv_bfloat16* p = static_cast<__nv_bfloat16*>(a.out) + o0 + (c & ~1) + (i0 + (c & 1)) * row_stride;
+                    for (int z = 0; z < 2; ++z) {
+                        const int i0 = half * (C / 2) + z * 16;
+                        float x[16], y[16];
+                        ptx::tmem_ld16(at + TM_QS + i0, x);
+                        ptx::tmem_ld16(at + TM_PR + i0, y);
+                        if (z == 1) {
+                            ptx::tc_fence_before();
+                            warp_arrive(sm.o_free, lane);
+                        }
 #pragma unroll
                         for (int i = 0; i < 16; i += 2) {
-                            const float y1 = __shfl_xor_sync(0xffffffffu, (c & 1) ? x[i] : x[i + 1], 1);
-                            const __nv_bfloat162 o = (c & 1) ? __floats2bfloat162_rn(y1, x[i + 1]) : __floats2bfloat162_rn(x[i], y1);
-                            if (i0 + i + (c & 1) < n) *reinterpret_cast<__nv_bfloat162*>(p + i * row_stride) = o;
+                            const float2 e1 = *reinterpret_cast<const float2*>(&fac.e1[i0 + i]);
+                            const float2 e2 = *reinterpret_cast<const float2*>(&fac.e2[i0 + i]);
+                            const float2 o = fma2(e1, mul2(both2(f1), make_float2(x[i], x[i + 1])),
+                                                  mul2(e2, mul2(both2(f2), make_float2(y[i], y[i + 1]))));
+                            x[i] = o.x;
+                            x[i + 1] = o.y;
                         }
+                        if constexpr (F32) {
+                            float* p = static_cast<float*>(a.out) + o0 + c + i0 * row_stride;
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                if (i0 + i < n) p[i * row_stride] = x[i];
+                        } else {
+                            // neighbouring lanes trade a value: even ones write two columns of row i, odd ones of row i + 1
+                            __nv_bfloat16* p = static_cast<__nv_bfloat16*>(a.out) + o0 + (c & ~1) + (i0 + (c & 1)) * row_stride;
+#pragma unroll
+                            for (int i = 0; i < 16; i += 2) {
+                                const float y1 = __shfl_xor_sync(0xffffffffu, (c & 1) ? x[i] : x[i + 1], 1);
+                                const __nv_bfloat162 o = (c & 1) ? __floats2bfloat162_rn(y1, x[i + 1]) : __floats2bfloat162_rn(x[i], y1);
+                                if (i0 + i + (c & 1) < n) *reinterpret_cast<__nv_bfloat162*>(p + i * row_stride) = o;
+                            }
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
                 }
+                q0 += chunks;
             }
-        }
+        } else
+            for (int turn = 0; units.next(sm, a, ws, turn, u);) ++turn;
     }
     if (wait.dead) flag_status(a.dev_status, KDA_DEV_TIMEOUT);
     ptx::tc_fence_before();
-    __syncthreads();
+    chain_sync();
     if (warp == 8) {
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tmem, TM_COLS);
@@ -1150,94 +1190,221 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) gdn_chain_kernel(const GdnAr
     ptx::grid_launch_dependents();
     ptx::grid_dependency_wait();
     extern __shared__ __align__(1024) unsigned char dyn[];
-    chain_unit<DK, DV, F32, false>(dyn, a, vmap, ws, blockIdx.x);
+    OneUnit one;
+    Unit& u = one.u;
+    u.h = blockIdx.x % a.Hv;
+    u.seq = ranked_seq(a.cu_seqlens, a.N, blockIdx.x / a.Hv, &reinterpret_cast<ChainSmem<DK, DV, F32>*>(dyn)->found);
+    if (!gdn_unit(a, u.seq, u.begin, u.end, u.slot)) return;
+    __shared__ uint32_t tmem;
+    if (threadIdx.x / 32 == 8) ptx::tmem_alloc(&tmem, TM_COLS);
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    run_chains<DK, DV, F32>(dyn, a, vmap, ws, tmem, one);
 }
 
-// ------------------------------------------------------------ few chains
+// ------------------------------------------------------------ chains beside prep
 //
 // A few long chains leave most SMs idle, and would start only when all of prep
-// is done: one cooperative grid of a CTA an SM instead, the chains on its first
-// CTAs and two teams of prep on each of the others, in the order in which the chains
-// come to need the slots.  Prep waits for nobody, so the chains' waits end.
+// is done: one cooperative grid of a CTA an SM instead.  The first K CTAs start
+// with the longest chains, the others with prep, three teams of warps each, in the order in which
+// the chains come to need the slots; and whoever is done takes the next chain, longest
+// first.  Prep waits for nobody, so the chains' waits for its slots end.
+//
+// K: as many chains as are longer than the work of all chains spread over all SMs.
+// Those have to start before prep ends; were it fewer, one of them would end last
+// alone, were it more, prep would be slower for nothing.  At most half of the CTAs.
+constexpr int MERGED = 64;                    // sequences, two a lane
+constexpr int TEAMS = 3, BESIDE = TEAMS * PREP;  // threads
+static_assert(BESIDE >= CHAIN_THREADS, "roles");
 
-// Task p of the order (chunk 0 of every sequence, chunk 1 of every one that has
-// it, ..): its rows and slot; false past the last.  Up to 64 sequences, two a lane.
-__device__ __forceinline__ bool nth_chunk(const GdnArgs& a, int p, int lane, int& slot, int& r0, int& n)
+struct Plan {
+    int order[MERGED];  // the sequences, longest first; those nothing is to be done for last
+    int len[MERGED];    // chunks, by sequence
+    int chains, first;  // K; sequences among the chains that start first
+};
+
+// One warp.
+__device__ __forceinline__ void make_plan(Plan& p, const GdnArgs& a, int lane)
 {
-    int b[2], e[2], nc[2], most = 0;
+    int nc[2], total = 0;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int s = lane + 32 * i;
-        b[i] = s < a.N ? a.cu_seqlens[s] : 0;
-        e[i] = s < a.N ? a.cu_seqlens[s + 1] : 0;
-        nc[i] = b[i] >= 0 && e[i] > b[i] && e[i] <= a.T ? (e[i] - b[i] + C - 1) / C : 0;
-        most = max(most, nc[i]);
-    }
-    most = __reduce_max_sync(0xffffffffu, most);
-    auto before = [&](int c) { return __reduce_add_sync(0xffffffffu, min(nc[0], c) + min(nc[1], c)); };
-    if (p >= before(most)) return false;
-    int lo = 0, hi = most;  // before(lo) <= p < before(hi)
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (before(mid) <= p) lo = mid;
-        else hi = mid;
-    }
-    int k = p - before(lo);  // the k-th sequence with more than lo chunks
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint32_t has = __ballot_sync(0xffffffffu, nc[i] > lo);
-        const int cnt = __popc(has);
-        if (k < cnt) {
-            const int l = __fns(has, 0, k + 1);
-            const int bb = __shfl_sync(0xffffffffu, b[i], l), ee = __shfl_sync(0xffffffffu, e[i], l);
-            slot = bb / C + l + 32 * i + lo;
-            r0 = bb + lo * C;
-            n = min(C, ee - r0);
-            return true;
+        nc[i] = 0;
+        if (s < a.N) {
+            const int b = a.cu_seqlens[s], e = a.cu_seqlens[s + 1], slot = a.slots ? a.slots[s] : s;
+            if (b >= 0 && e > b && e <= a.T && slot >= 0 && slot < a.num_slots) nc[i] = (e - b + C - 1) / C;
         }
-        k -= cnt;
+        p.len[s] = nc[i];
+        total += nc[i];
     }
-    return false;
+    total = __reduce_add_sync(0xffffffffu, total);
+    __syncwarp();
+    int r[2] = {0, 0}, above = 0;
+    for (int k = 0; k < a.N; ++k) {
+        const int l = p.len[k];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) r[i] += l > nc[i] || (l == nc[i] && k < lane + 32 * i);
+        above += (long long)l * gridDim.x > (long long)total * a.Hv;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        if (lane + 32 * i < a.N) p.order[r[i]] = lane + 32 * i;
+    if (lane == 0) {
+        p.chains = (int)min((long long)above * a.Hv, (long long)gridDim.x / 2);
+        p.first = (p.chains + a.Hv - 1) / a.Hv;
+    }
 }
 
+// Prep's order: chunk 0 of the sequences whose chains start first, chunk 1 of
+// those of them that have one, ..; then the other sequences, longest first, one after the other.
+struct Order {
+    int b[2], e[2], nc[2], seq[2];  // of the sequences at places lane and lane + 32 of the plan's order
+    int first, most, total;         // of the ones that start first: how many, their most chunks, all their chunks
+    int ends[2];                    // running sums of the others' chunks
+    __device__ __forceinline__ int before(int c) const
+    {
+        return __reduce_add_sync(0xffffffffu, (lane() < first ? min(nc[0], c) : 0) + (lane() + 32 < first ? min(nc[1], c) : 0));
+    }
+    static __device__ __forceinline__ int lane() { return threadIdx.x & 31; }
+    __device__ __forceinline__ Order(const Plan& p, const GdnArgs& a) : first(p.first), most(0)
+    {
+        int run[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int at = lane() + 32 * i;
+            seq[i] = at < a.N ? p.order[at] : 0;
+            nc[i] = at < a.N ? p.len[seq[i]] : 0;
+            b[i] = a.cu_seqlens[seq[i]];
+            e[i] = a.cu_seqlens[seq[i] + 1];
+            if (at < first) most = max(most, nc[i]);
+            run[i] = at < first ? 0 : nc[i];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int up = __shfl_up_sync(0xffffffffu, run[i], o);
+                if (lane() >= o) run[i] += up;
+            }
+        }
+        ends[0] = run[0];
+        ends[1] = run[1] + __shfl_sync(0xffffffffu, run[0], 31);
+        most = __reduce_max_sync(0xffffffffu, most);
+        total = before(most);
+    }
+    // Task p: its slot and rows; false past the last.
+    __device__ __forceinline__ bool task(int p, int& slot, int& r0, int& n) const
+    {
+        int at = -1, c;
+        if (p < total) {
+            int lo = 0, hi = most;  // before(lo) <= p < before(hi)
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) / 2;
+                if (before(mid) <= p) lo = mid;
+                else hi = mid;
+            }
+            c = lo;
+            // longest first: the ones with more than c chunks are the first of the order
+            at = p - before(lo);
+        } else {
+            p -= total;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t past = __ballot_sync(0xffffffffu, ends[i] > p);
+                if (at < 0 && past) at = __ffs(past) - 1 + 32 * i;
+            }
+            if (at < 0) return false;
+            const int l = at & 31, end = __shfl_sync(0xffffffffu, at < 32 ? ends[0] : ends[1], l);
+            c = p - (end - __shfl_sync(0xffffffffu, at < 32 ? nc[0] : nc[1], l));
+        }
+        const int l = at & 31;
+        const int bb = __shfl_sync(0xffffffffu, at < 32 ? b[0] : b[1], l), ee = __shfl_sync(0xffffffffu, at < 32 ? e[0] : e[1], l);
+        slot = bb / C + __shfl_sync(0xffffffffu, at < 32 ? seq[0] : seq[1], l) + c;
+        r0 = bb + c * C;
+        n = min(C, ee - r0);
+        return true;
+    }
+};
+
+// Chain after chain, longest first: CTA i < K starts with chain i, the others are given out one by one.
+struct TakenUnits {
+    static constexpr bool BESIDE = true;
+    const Plan* plan;
+    template <class S> __device__ __forceinline__ bool next(S& sm, const GdnArgs& a, const Work& ws, int turn, Unit& out)
+    {
+        chain_sync();  // everyone is done with the unit before
+        if (threadIdx.x == 0) {
+            Unit& u = sm.unit;
+            int i = turn == 0 && (int)blockIdx.x < plan->chains ? (int)blockIdx.x : -1;
+            for (;; i = -1) {
+                if (i < 0) i = plan->chains + atomicAdd(ws.taken, 1);
+                if (i >= a.N * a.Hv) {
+                    u.seq = -1;
+                    break;
+                }
+                u.seq = plan->order[i / a.Hv];
+                u.h = i % a.Hv;
+                if (gdn_unit(a, u.seq, u.begin, u.end, u.slot)) break;
+            }
+        }
+        chain_sync();
+        out = sm.unit;
+        return out.seq >= 0;
+    }
+};
+
 template <int DK, int DV, bool F32, int HEADS>
-__global__ void __launch_bounds__(CHAIN_THREADS, 1)
+__global__ void __launch_bounds__(BESIDE, 1)
 gdn_beside_kernel(const GdnArgs a, const __grid_constant__ RowMaps maps, const Work ws)
 {
     extern __shared__ __align__(1024) unsigned char dyn[];
-    const int chains = a.N * a.Hv;
-    if (blockIdx.x < chains) {
-        chain_unit<DK, DV, F32, true>(dyn, a, maps.v, ws, blockIdx.x);
-        return;
-    }
-    using S = PrepSmem<DK, F32, HEADS>;
-    constexpr int STRIDE = (sizeof(S) + 1023) / 1024 * 1024;
-    const int team = threadIdx.x / PREP, t = threadIdx.x % PREP, lane = t & 31;
-    if (team >= 2) return;
-    S& sm = *reinterpret_cast<S*>(dyn + team * STRIDE);
-    prep_setup(sm, t);
-    team_sync(team);
+    __shared__ Plan plan;
+    __shared__ uint32_t tmem_at;
+    // one allocation a CTA: 128 columns for a team of prep, then all of them for chains
+    if (threadIdx.x < 32) make_plan(plan, a, threadIdx.x);
+    else if (threadIdx.x / 32 == 8) ptx::tmem_alloc(&tmem_at, TM_COLS);
+    ptx::tc_fence_before();
+    __syncthreads();
     ptx::tc_fence_after();
-    const uint32_t tmem = sm.tmem;
-    Waiter wait{false};
-    const int groups = a.Hv / HEADS, teams = (gridDim.x - chains) * 2;
-    int turn = 0;
-    for (long long i = (blockIdx.x - chains) * 2 + team;; i += teams, ++turn) {
-        int slot, r0, n;
-        if (!nth_chunk(a, (int)(i / groups), lane, slot, r0, n)) break;
-        const int h0 = (int)(i % groups) * HEADS;
-        prep_task<DK, F32, HEADS>(sm, a, maps, ws, slot, r0, n, h0, turn, team, tmem, wait, t);
-        if (t == 0) {
-            ptx::bulk_wait_all();
-            ptx::fence_proxy_async_global();
-            __threadfence();
+    const uint32_t tmem = tmem_at;
+    if ((int)blockIdx.x >= plan.chains) {
+        using S = PrepSmem<DK, F32, HEADS>;
+        constexpr int STRIDE = (sizeof(S) + 1023) / 1024 * 1024, TEAMS_HERE = prep_ctas<F32>();
+        const int team = threadIdx.x / PREP, t = threadIdx.x % PREP;
+        if (team < TEAMS_HERE) {
+            S& sm = *reinterpret_cast<S*>(dyn + team * STRIDE);
+            prep_setup(sm, t);
+            team_sync(team);
+            Waiter wait{false};
+            const Order order(plan, a);
+            const int groups = a.Hv / HEADS, teams = (gridDim.x - plan.chains) * TEAMS_HERE;
+            int turn = 0;
+            for (long long i = (blockIdx.x - plan.chains) * TEAMS_HERE + team;; i += teams, ++turn) {
+                int slot, r0, n;
+                if (!order.task((int)(i / groups), slot, r0, n)) break;
+                const int h0 = (int)(i % groups) * HEADS;
+                prep_task<DK, F32, HEADS>(sm, a, maps, ws, slot, r0, n, h0, turn, team, tmem + team * 128, wait, t);
+                if (t == 0) {
+                    ptx::bulk_wait_all();
+                    ptx::fence_proxy_async_global();
+                    __threadfence();
 #pragma unroll
-            for (int j = 0; j < HEADS; ++j) ptx::st_release_gpu(ws.ready + (long long)slot * a.Hv + h0 + j, 1);
+                    for (int j = 0; j < HEADS; ++j) ptx::st_release_gpu(ws.ready + (long long)slot * a.Hv + h0 + j, 1);
+                }
+                team_sync(team);
+            }
+            if (wait.dead) flag_status(a.dev_status, KDA_DEV_TIMEOUT);
+            if (t == 0) {
+                ptx::mbar_inval(&sm.loaded);
+                ptx::mbar_inval(&sm.prod);
+            }
+            ptx::fence_proxy_async_smem();  // the chains' copies come into the same memory
+            ptx::tc_fence_before();
         }
-        team_sync(team);
+        __syncthreads();
+        ptx::tc_fence_after();
     }
-    if (wait.dead) flag_status(a.dev_status, KDA_DEV_TIMEOUT);
-    if (t / 32 == 1) ptx::tmem_dealloc(tmem, 128);
+    if (threadIdx.x < CHAIN_THREADS) run_chains<DK, DV, F32>(dyn, a, maps.v, ws, tmem, TakenUnits{&plan});
+    else set_regs<false, 24>();
 }
 
 // ------------------------------------------------------------ launch
@@ -1293,18 +1460,18 @@ cudaError_t launch_prep(const GdnArgs& a, const RowMaps& maps, const Work& ws, l
 template <int DK, int DV, bool F32, int HEADS>
 cudaError_t launch_beside(const GdnArgs& a, const RowMaps& maps, const Work& ws, long long slots, cudaStream_t st)
 {
-    constexpr int prep = 2 * (int)((sizeof(PrepSmem<DK, F32, HEADS>) + 1023) / 1024 * 1024);
+    constexpr int prep = prep_ctas<F32>() * (int)((sizeof(PrepSmem<DK, F32, HEADS>) + 1023) / 1024 * 1024);
     constexpr int chain = (int)sizeof(ChainSmem<DK, DV, F32>), smem = prep > chain ? prep : chain;
-    static_assert(smem <= 227 * 1024, "shared memory");
+    static_assert(smem + sizeof(Plan) + 1024 <= 227 * 1024, "shared memory");
     static PerDeviceOnce once;
     cudaError_t e = once.run([](int) {
         return cudaFuncSetAttribute(gdn_beside_kernel<DK, DV, F32, HEADS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     });
     if (e != cudaSuccess) return e;
-    if ((e = cudaMemsetAsync(ws.ready, 0, slots * a.Hv * sizeof(int), st)) != cudaSuccess) return e;
+    if ((e = cudaMemsetAsync(ws.ready, 0, (slots * a.Hv + 1) * sizeof(int), st)) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = sm_count();
-    cfg.blockDim = CHAIN_THREADS;
+    cfg.blockDim = BESIDE;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr;
@@ -1319,10 +1486,7 @@ template <int DK, int DV, bool F32>
 cudaError_t launch_dv(const GdnArgs& a, const RowMaps& maps, const Work& ws, long long slots, cudaStream_t st)
 {
     const bool pairs = a.Hv / a.Hk % 2 == 0;
-    // Chains beside prep where they leave it more than half of the SMs and prep is
-    // more than one wave of CTAs (a 32768-row prompt of 32 heads 1.27 ms against
-    // 1.68 one after the other; 333 rows of 8 heads 36 us against 23)
-    if (a.N <= 64 && (long long)a.N * a.Hv * 2 < sm_count() && slots * a.Hv > prep_ctas<F32>() * sm_count())
+    if (a.N <= MERGED && slots * a.Hv > prep_ctas<F32>() * sm_count())
         return pairs ? launch_beside<DK, DV, F32, 2>(a, maps, ws, slots, st) : launch_beside<DK, DV, F32, 1>(a, maps, ws, slots, st);
     // two heads a CTA (their rows, products and norms once) unless all single ones run at once anyway
     const cudaError_t e = pairs && slots * a.Hv > prep_ctas<F32>() * sm_count() ? launch_prep<DK, F32, 2>(a, maps, ws, slots, st)
@@ -1343,6 +1507,7 @@ template <int DK, bool F32> cudaError_t launch(const GdnArgs& a, int dv, cudaStr
     ws.kq = static_cast<unsigned char*>(a.workspace);
     ws.v = ws.kq + slots * a.Hk * L::KQ;
     ws.ready = reinterpret_cast<int*>(ws.v + slots * a.Hv * L::V);
+    ws.taken = ws.ready + slots * a.Hv;
     if (dv == 128) return launch_dv<DK, 128, F32>(a, maps, ws, slots, st);
     if (dv == 64) return launch_dv<DK, 64, F32>(a, maps, ws, slots, st);
     return launch_dv<DK, 32, F32>(a, maps, ws, slots, st);

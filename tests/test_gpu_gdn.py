@@ -378,9 +378,9 @@ def test_long_prompt(cuda_lib):
 
 
 def _beside(c):
-    """Whether a call of this case runs its chains beside prep (few chains, more slots than one wave of prep)."""
+    """Whether a call of this case runs its chains beside prep (up to 64 sequences, more slots than one wave of prep)."""
     slots = c.T // 64 + c.N
-    return c.N * c.Hv * 2 < 152 and slots * c.Hv > (3 if c.out_t == "bf16" else 2) * 152
+    return c.N <= 64 and slots * c.Hv > (3 if c.out_t == "bf16" else 2) * 152
 
 
 @pytest.mark.parametrize("Hk,Hv,dk,dv,out,lens", [
@@ -402,7 +402,7 @@ def test_prefill_chains_beside_prep(cuda_lib, Hk, Hv, dk, dv, out, lens):
 
 def test_prefill_beside_gives_the_bits_of_one_after_the_other(cuda_lib):
     """The same rows as a call of their own (chains beside prep) and among
-    enough others that prep runs first: the same bits; and again on a
+    so many others that prep runs first: the same bits; and again on a
     workspace full of ones."""
     lens = [1400, 1100]
     c = Case(lens, Hk=6, Hv=12, dk=64, dv=64, seed=50)
@@ -417,7 +417,7 @@ def test_prefill_beside_gives_the_bits_of_one_after_the_other(cuda_lib):
                                                    c.g_out.tensor, ws, need, c.status))
     torch.cuda.synchronize()
     assert torch.equal(c.g_out.tensor, want[0]) and torch.equal(c.g_state.tensor, want[1])
-    many = Case(lens + [3] * 5, Hk=6, Hv=12, dk=64, dv=64, seed=51)
+    many = Case(lens + [1] * 63, Hk=6, Hv=12, dk=64, dv=64, seed=51)
     assert not _beside(many)
     n = c.T
     many.rows[:n].copy_(c.rows)
@@ -480,14 +480,38 @@ def test_back_to_back_calls_keep_their_order(cuda_lib):
 
 
 @pytest.mark.parametrize("out,Hk,Hv,dk", [("f32", 8, 16, 32), ("bf16", 4, 16, 64), ("bf16", 5, 15, 32)])
-def test_prefill_many_heads_of_shared_keys(cuda_lib, out, Hk, Hv, dk):
-    """Enough chunk-heads that prep takes two heads of one key head together (an odd group: one), the sequences
-    enough that the chains run after it."""
-    c = Case([200, 0, 65, 700, 1, 64, 333, 128, 500, 130, 90, 640], Hk=Hk, Hv=Hv, dk=dk, dv=32, out=out, seed=80,
-             slots=[3, 0, 7, -1, 5, 1, 2, 11, 4, 6, 8, 9])
-    assert not _beside(c) and (c.T // 64 + c.N) * Hv > 3 * 152
+@pytest.mark.parametrize("ones", [0, 60])
+def test_prefill_many_heads_of_shared_keys(cuda_lib, out, Hk, Hv, dk, ones):
+    """Enough chunk-heads that prep takes two heads of one key head together (an odd group: one); more chains
+    than SMs, odd and even ones, taken one after the other beside prep, or (many sequences) after it."""
+    lens = [200, 0, 65, 700, 1, 64, 333, 128, 500, 130, 90, 640]
+    c = Case(lens + [1] * ones, Hk=Hk, Hv=Hv, dk=dk, dv=32, out=out, seed=80,
+             slots=[3, 0, 7, -1, 5, 1, 2, 11, 4, 6, 8, 9] + list(range(12, 12 + ones)))
+    assert _beside(c) == (ones == 0) and (c.T // 64 + c.N) * Hv > 3 * 152
     c.prefill(cuda_lib)
     c.check()
+
+
+def test_prefill_many_chains_for_each_cta(cuda_lib):
+    r = np.random.default_rng(5)
+    c = Case(r.integers(0, 200, 64).tolist(), Hk=4, Hv=32, dk=32, dv=32, seed=81, num_slots=70,
+             slots=[int(s) if i % 9 else -1 for i, s in enumerate(r.permutation(70)[:64])])
+    assert _beside(c)
+    c.prefill(cuda_lib)
+    c.check()
+
+
+def test_prefill_beside_flags_bad_sequences_and_slots(cuda_lib):
+    c = Case([900, 60, 500, 1200], Hk=4, Hv=16, dk=32, dv=32, seed=82, slots=[2, 9, 1, 0], num_slots=4)
+    c.slots_h[1] = -1
+    assert _beside(c)
+    c.prefill(cuda_lib)
+    c.check(status=cuda_lib.KDA_DEV_BAD_SLOT)
+    c = Case([900, 60, 500, 1200], Hk=4, Hv=16, dk=32, dv=32, seed=82)
+    c.cu[4] = c.T + 1
+    c.prefill(cuda_lib)
+    assert int(c.status.item()) == cuda_lib.KDA_DEV_BAD_SEQLENS
+    assert torch.equal(c.g_state.tensor[3], c.state0[3]) and (c.g_out.tensor[1460:] == 7.0).all()
 
 
 @pytest.mark.parametrize("huge", [2.0 ** 30, float("inf"), float("nan")])
