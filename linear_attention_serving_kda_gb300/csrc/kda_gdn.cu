@@ -173,118 +173,148 @@ template <typename IO, typename OUT> cudaError_t decode_io(const GdnArgs& a, int
 // ------------------------------------------------------------ fp32 rows, one by one
 //
 // One CTA per (sequence, value head, 32 columns), the state in registers:
-// lane (part, column) of a warp holds a quarter of a column.  Rows are staged
-// sixteen at a time.  Bound: the chain of rows (two dot products across four
-// lanes each), not bandwidth: ROWS_NOTE.
+// lane (columns, part) of a warp holds an eighth of two columns, so that a value of k or q
+// from shared memory serves both (with a quarter of one column a lane those
+// reads were the bound: 982 us where these take 660).  As for single
+// tokens both of a row's dot products read the OLD state, so a row's
+// dependent steps are one product, two shuffles and the update.  Rows are
+// staged sixteen at a time, the next ones loaded meanwhile.  Bound: issue slots where
+// there are many chains (packed arithmetic: two values an instruction), a row's steps where there
+// are few, never bandwidth: 4096 rows of 8 sequences,
+// 32 heads of 128 x 128, take 660 us, 2048 rows of one sequence 569 us.
 constexpr int GR_WARPS = 4, GR_COLS = 32, GR_ROWS = 16;
 
 template <int DK> __global__ void __launch_bounds__(GR_WARPS * 32) gdn_rows_kernel(const GdnArgs a, int dv)
 {
-    ptx::grid_launch_dependents();
     ptx::grid_dependency_wait();
-    constexpr int PER = DK / 32, M = DK / 16, RW = GR_ROWS / GR_WARPS;
+    constexpr int PER = DK / 32, M = DK / 32, RW = GR_ROWS / GR_WARPS;
     __shared__ __align__(16) float qs[GR_ROWS][DK], ks[GR_ROWS][DK], vs[GR_ROWS][GR_COLS];
-    __shared__ float al[GR_ROWS], be[GR_ROWS];
+    __shared__ float al[GR_ROWS], be[GR_ROWS], qk[GR_ROWS];
     const int tiles = dv / GR_COLS;
-    const int tile = blockIdx.x % tiles, u = blockIdx.x / tiles, h = u % a.Hv, seq = u / a.Hv;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, part = lane >> 3, c = warp * 8 + (lane & 7);
+    const int tile = blockIdx.x % tiles, u = blockIdx.x / tiles, h = u % a.Hv;
+    __shared__ int found;
+    const int seq = ranked_seq(a.cu_seqlens, a.N, u / a.Hv, &found);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, part = lane & 7, c0 = warp * 8 + (lane >> 3) * 2, odd = lane & 1;
     int begin, end, slot;
     if (!gdn_unit(a, seq, begin, end, slot)) return;
     const int hk = h / (a.Hv / a.Hk);
-    float* S = a.state + ((size_t)slot * a.Hv + h) * DK * dv + tile * GR_COLS + c;
-    // the lane's rows of the state: 16 m + 4 part + 0..3
-    float s[M][4];
+    float* S = a.state + ((size_t)slot * a.Hv + h) * DK * dv + tile * GR_COLS + c0;
+    // of columns c0 and c0 + 1 the lane's rows of the state, 32 m + 4 part + 0..3, two by two
+    float2 s[2][M][2];
 #pragma unroll
     for (int m = 0; m < M; ++m)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[m][j] = S[(size_t)(16 * m + 4 * part + j) * dv];
+        for (int j = 0; j < 2; ++j) {
+            const float* p = S + (size_t)(32 * m + 4 * part + 2 * j) * dv;
+            const float2 x = *reinterpret_cast<const float2*>(p), y = *reinterpret_cast<const float2*>(p + dv);
+            s[0][m][j] = make_float2(x.x, y.x);
+            s[1][m][j] = make_float2(x.y, y.y);
+        }
     const float* q = static_cast<const float*>(a.q) + hk * DK + lane * PER;
     const float* k = static_cast<const float*>(a.k) + hk * DK + lane * PER;
-    const float* v = static_cast<const float*>(a.v) + h * dv + tile * GR_COLS;
-    float* out = static_cast<float*>(a.out) + (size_t)h * dv + tile * GR_COLS + c;
+    const float* v = static_cast<const float*>(a.v) + h * dv + tile * GR_COLS + lane;
+    float* out = static_cast<float*>(a.out) + (size_t)h * dv + tile * GR_COLS + c0 + odd;
     const float ea = expf(a.A_log[h]), dt = a.dt_bias[h];
 
-    for (int r0 = begin; r0 < end; r0 += GR_ROWS) {
-        const int n = min(GR_ROWS, end - r0);
-        float qr[RW][PER], kr[RW][PER];
+    // rows warp * RW .. of a batch to a warp
+    float qr[RW][PER], kr[RW][PER], vr[RW], gate = 0.f, beta = 0.f;
+    auto fetch = [&](int r0) {
 #pragma unroll
         for (int i = 0; i < RW; ++i) {
-            const int r = warp * RW + i;
-            if (r < n) {
-                load_n<float, PER>(q + (long long)(r0 + r) * a.qs, qr[i]);
-                load_n<float, PER>(k + (long long)(r0 + r) * a.ks, kr[i]);
+            const int r = r0 + warp * RW + i;
+            if (r < end) {
+                load_n<float, PER>(q + (long long)r * a.qs, qr[i]);
+                load_n<float, PER>(k + (long long)r * a.ks, kr[i]);
+                vr[i] = v[(long long)r * a.vs];
             }
         }
+        if (tid < GR_ROWS && r0 + tid < end) {
+            gate = static_cast<const float*>(a.a)[(size_t)(r0 + tid) * a.Hv + h];
+            beta = static_cast<const float*>(a.b)[(size_t)(r0 + tid) * a.Hv + h];
+        }
+    };
+    fetch(begin);
+    for (int r0 = begin; r0 < end; r0 += GR_ROWS) {
+        const int n = min(GR_ROWS, end - r0);
         __syncthreads();  // the rows staged before are done with
 #pragma unroll
         for (int i = 0; i < RW; ++i) {
             const int r = warp * RW + i;
             if (r >= n) continue;
+            float qq = 0.f, kk = 0.f, x = 0.f;
+#pragma unroll
+            for (int j = 0; j < PER; ++j) {
+                qq = fmaf(qr[i][j], qr[i][j], qq);
+                kk = fmaf(kr[i][j], kr[i][j], kk);
+                x = fmaf(qr[i][j], kr[i][j], x);
+            }
             float rq = 1.f, rk = 1.f;
             if (a.l2) {
-                float qq = 0.f, kk = 0.f;
-#pragma unroll
-                for (int j = 0; j < PER; ++j) {
-                    qq = fmaf(qr[i][j], qr[i][j], qq);
-                    kk = fmaf(kr[i][j], kr[i][j], kk);
-                }
                 rq = rsqrtf(warp_sum(qq) + a.l2_eps);
                 rk = rsqrtf(warp_sum(kk) + a.l2_eps);
             }
+            x = warp_sum(x);
+            if (lane == 0) qk[r] = x * rq * rk;
 #pragma unroll
             for (int j = 0; j < PER; ++j) {
                 qs[r][lane * PER + j] = qr[i][j] * rq;
                 ks[r][lane * PER + j] = kr[i][j] * rk;
             }
+            vs[r][lane] = vr[i];
         }
-        for (int i = tid; i < n * GR_COLS; i += GR_WARPS * 32)
-            vs[i / GR_COLS][i % GR_COLS] = v[(long long)(r0 + i / GR_COLS) * a.vs + i % GR_COLS];
         if (tid < n) {
-            const size_t gi = (size_t)(r0 + tid) * a.Hv + h;
-            al[tid] = expf(gdn_log_alpha(ea, static_cast<const float*>(a.a)[gi], dt));
-            be[tid] = sigmoidf_(static_cast<const float*>(a.b)[gi]);
+            al[tid] = expf(gdn_log_alpha(ea, gate, dt));
+            be[tid] = sigmoidf_(beta);
         }
         __syncthreads();
+        fetch(r0 + GR_ROWS);
         for (int r = 0; r < n; ++r) {
             const float alpha = al[r];
-            float d0 = 0.f, d1 = 0.f;
+            float2 x[2], y[2], kp[M][2];  // k.S and q.S of both columns
+#pragma unroll
+            for (int e = 0; e < 2; ++e) x[e] = y[e] = both2(0.f);
 #pragma unroll
             for (int m = 0; m < M; ++m) {
-                const float4 kv = *reinterpret_cast<const float4*>(&ks[r][16 * m + 4 * part]);
-                s[m][0] *= alpha; s[m][1] *= alpha; s[m][2] *= alpha; s[m][3] *= alpha;
-                d0 = fmaf(kv.x, s[m][0], d0);
-                d1 = fmaf(kv.y, s[m][1], d1);
-                d0 = fmaf(kv.z, s[m][2], d0);
-                d1 = fmaf(kv.w, s[m][3], d1);
-            }
-            float d = d0 + d1;
-            d += __shfl_xor_sync(0xffffffffu, d, 8);
-            d += __shfl_xor_sync(0xffffffffu, d, 16);
-            const float uu = be[r] * (vs[r][c] - d);
-            d0 = d1 = 0.f;
+                const float4 kv = *reinterpret_cast<const float4*>(&ks[r][32 * m + 4 * part]);
+                const float4 qv = *reinterpret_cast<const float4*>(&qs[r][32 * m + 4 * part]);
+                kp[m][0] = make_float2(kv.x, kv.y);
+                kp[m][1] = make_float2(kv.z, kv.w);
+                const float2 qp[2] = {make_float2(qv.x, qv.y), make_float2(qv.z, qv.w)};
 #pragma unroll
-            for (int m = 0; m < M; ++m) {
-                const float4 kv = *reinterpret_cast<const float4*>(&ks[r][16 * m + 4 * part]);
-                const float4 qv = *reinterpret_cast<const float4*>(&qs[r][16 * m + 4 * part]);
-                s[m][0] = fmaf(kv.x, uu, s[m][0]);
-                s[m][1] = fmaf(kv.y, uu, s[m][1]);
-                s[m][2] = fmaf(kv.z, uu, s[m][2]);
-                s[m][3] = fmaf(kv.w, uu, s[m][3]);
-                d0 = fmaf(qv.x, s[m][0], d0);
-                d1 = fmaf(qv.y, s[m][1], d1);
-                d0 = fmaf(qv.z, s[m][2], d0);
-                d1 = fmaf(qv.w, s[m][3], d1);
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        x[e] = fma2(kp[m][j], s[e][m][j], x[e]);
+                        y[e] = fma2(qp[j], s[e][m][j], y[e]);
+                    }
             }
-            float o = d0 + d1;
-            o += __shfl_xor_sync(0xffffffffu, o, 8);
-            o += __shfl_xor_sync(0xffffffffu, o, 16);
-            if (part == 0) out[(size_t)(r0 + r) * a.Hv * dv] = a.scale * o;
+            // over the eight parts: neighbours trade a column first, so that each lane ends with one column's sums
+            const float2 d0 = make_float2(x[0].x + x[0].y, y[0].x + y[0].y), d1 = make_float2(x[1].x + x[1].y, y[1].x + y[1].y);
+            const float2 mine = odd ? d1 : d0, other = odd ? d0 : d1;
+            float2 d = add2(mine, make_float2(__shfl_xor_sync(0xffffffffu, other.x, 1), __shfl_xor_sync(0xffffffffu, other.y, 1)));
+#pragma unroll
+            for (int o = 2; o < 8; o <<= 1)
+                d = add2(d, make_float2(__shfl_xor_sync(0xffffffffu, d.x, o), __shfl_xor_sync(0xffffffffu, d.y, o)));
+            const float uu = be[r] * (vs[r][c0 + odd] - alpha * d.x), theirs = __shfl_xor_sync(0xffffffffu, uu, 1);
+            const float2 u2[2] = {both2(odd ? theirs : uu), both2(odd ? uu : theirs)};
+#pragma unroll
+            for (int m = 0; m < M; ++m)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) s[e][m][j] = fma2(kp[m][j], u2[e], mul2(both2(alpha), s[e][m][j]));
+            if (part < 2) out[(size_t)(r0 + r) * a.Hv * dv] = a.scale * fmaf(qk[r], uu, alpha * d.y);
         }
     }
+    ptx::grid_launch_dependents();  // not before: the next call's CTAs would crowd the SMs that are free
 #pragma unroll
     for (int m = 0; m < M; ++m)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) S[(size_t)(16 * m + 4 * part + j) * dv] = s[m][j];
+        for (int j = 0; j < 2; ++j) {
+            float* p = S + (size_t)(32 * m + 4 * part + 2 * j) * dv;
+            *reinterpret_cast<float2*>(p) = make_float2(s[0][m][j].x, s[1][m][j].x);
+            *reinterpret_cast<float2*>(p + dv) = make_float2(s[0][m][j].y, s[1][m][j].y);
+        }
 }
 
 // ------------------------------------------------------------ checks

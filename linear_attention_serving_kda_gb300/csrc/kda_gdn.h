@@ -62,6 +62,28 @@ __device__ __forceinline__ bool gdn_unit(const GdnArgs& a, int seq, int& begin, 
     return slot >= 0 && end > begin;
 }
 
+// The sequence of rank `rank` by length, longest first (ties: lowest index):
+// long chains start first.  More than RANKED sequences balance in any order and keep theirs.
+constexpr int RANKED = 128;
+__device__ __forceinline__ int ranked_seq(const int32_t* cu, int N, int rank, int* found)
+{
+    if (N > RANKED || N == 1) return rank;
+    const int t = threadIdx.x;
+    if (t == 0) *found = rank;
+    __syncthreads();
+    if (t < N) {
+        const int len = cu[t + 1] - cu[t];
+        int r = 0;
+        for (int i = 0; i < N; ++i) {
+            const int l = cu[i + 1] - cu[i];
+            r += l > len || (l == len && i < t);
+        }
+        if (r == rank) *found = t;
+    }
+    __syncthreads();
+    return *found;
+}
+
 // The driver's encoder of tensor maps, null where it has none (kda_chunk.cu).
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 

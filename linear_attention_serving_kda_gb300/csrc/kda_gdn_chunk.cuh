@@ -777,28 +777,6 @@ template <int N> __device__ __forceinline__ void store_split(uint32_t hi_at, uin
     ptx::tmem_wait_st();
 }
 
-// The sequence of rank `rank` by length, longest first (ties: lowest index):
-// long chains start first.  More than RANKED sequences balance in any order and keep theirs.
-constexpr int RANKED = 128;
-__device__ __forceinline__ int ranked_seq(const int32_t* cu, int N, int rank, int* found)
-{
-    if (N > RANKED || N == 1) return rank;
-    const int t = threadIdx.x;
-    if (t == 0) *found = rank;
-    __syncthreads();
-    if (t < N) {
-        const int len = cu[t + 1] - cu[t];
-        int r = 0;
-        for (int i = 0; i < N; ++i) {
-            const int l = cu[i + 1] - cu[i];
-            r += l > len || (l == len && i < t);
-        }
-        if (r == rank) *found = t;
-    }
-    __syncthreads();
-    return *found;
-}
-
 // Sets the register count of the calling warpgroup's threads.
 template <bool UP, int N> __device__ __forceinline__ void set_regs()
 {
