@@ -363,8 +363,12 @@ typedef struct kda_gdn_params {
  *   - A NaN or an infinity in a row reaches no other sequence or head; in its
  *     own it may reach rows from its 64-row chunk's first on.
  *   - workspace: kda_gdn_prefill_workspace_bytes(p, N, T) bytes (may be NULL
- *     when that is 0); contents need no init.  Calls that may run at the same
- *     time take a workspace each.
+ *     when that is 0, for fp32 rows); it grows with
+ *     (T/64 + N) heads: 0.97 GB for 32768 rows, 16 key and 32 value heads of
+ *     128.  Contents need no init.  Calls that may run at the same time take a
+ *     workspace each.
+ *   - Long calls run as one cooperative grid of a CTA an SM; a call on a device
+ *     of which other work holds SMs waits for them.
  */
 KDA_API int kda_gdn_prefill_varlen(const kda_gdn_params* p, const int32_t* cu_seqlens, int32_t N, int32_t T,
                                    const void* q, const void* k, const void* v, const void* gate, const void* beta,

@@ -9,12 +9,21 @@
 // All exponents are differences that are <= 0.
 //
 // Only S goes from chunk to chunk, so the work is cut where S enters:
-//   - gdn_prep_kernel, one CTA per (chunk, value head), all at once: K and Q as
-//     operands, M and P T, into the workspace;
-//   - gdn_chain_kernel, one CTA per (sequence, value head): R and S' chunk
+//   - prep, a team of eight warps per (chunk, one or two value heads), all chunks at
+//     once: K and Q as operands, M and P T, into the workspace;
+//   - chains, one CTA per (sequence, value head): R and S' chunk
 //     after chunk, two dependent products each, and the outputs beside them.
 // The chain is what a long sequence's time is made of; with M in place of T the
-// updates U never appear on it.
+// updates U never appear on it.  Up to 64 sequences with work for more than a wave of
+// prep run as one grid, chains beside prep (gdn_beside_kernel); others as two kernels one
+// after the other.
+//
+// Bounds and figures (16 key and 32 value heads of 128 x 128, bf16 outputs).  Neither HBM
+// (a quarter of its time at most: rows 0.8 GB and workspace 2 GB for 32768 rows) nor the tensor cores
+// (24 % busy) but dependent steps: prep issues an instruction every other cycle and
+// else waits at its barriers, 322 us for 32768 rows with 24 warps an SM; a chunk of a chain takes 2.4 us,
+// of which the products are 1.0 and the rest the state's way between registers and
+// TMEM.  32768 rows as eight prompts 682 us, as one prompt 1250, which is its 512 chunks one after the other.
 //
 // Precision: the state keeps fp32 accuracy.  One decay per head leaves k and q
 // unscaled inside every product, so the rows' bf16 values are operands without
@@ -1462,12 +1471,16 @@ cudaError_t launch_beside(const GdnArgs& a, const RowMaps& maps, const Work& ws,
 template <int DK, int DV, bool F32>
 cudaError_t launch_dv(const GdnArgs& a, const RowMaps& maps, const Work& ws, long long slots, cudaStream_t st)
 {
-    const bool pairs = a.Hv / a.Hk % 2 == 0;
-    if (a.N <= MERGED && slots * a.Hv > prep_ctas<F32>() * sm_count())
+    // Two heads a team (their rows, products and norms once): 32768 rows as eight prompts take
+    // 682 us, 783 with one; one prompt 1250 and 1238.
+    const bool pairs = a.Hv / a.Hk % 2 == 0, waves = slots * a.Hv > prep_ctas<F32>() * sm_count();
+    // Chains beside prep where prep is more than one wave of CTAs: 32768 rows of 32 heads take
+    // 682 us as eight prompts of mixed lengths (847 one after the other), 1250 as one (1640),
+    // 662 as sixteen (637); 7001 rows of 12 heads 114 (137); but 333 rows of 8 heads 40 us, 23 one after the other.
+    if (a.N <= MERGED && waves)
         return pairs ? launch_beside<DK, DV, F32, 2>(a, maps, ws, slots, st) : launch_beside<DK, DV, F32, 1>(a, maps, ws, slots, st);
-    // two heads a CTA (their rows, products and norms once) unless all single ones run at once anyway
-    const cudaError_t e = pairs && slots * a.Hv > prep_ctas<F32>() * sm_count() ? launch_prep<DK, F32, 2>(a, maps, ws, slots, st)
-                                                                              : launch_prep<DK, F32, 1>(a, maps, ws, slots, st);
+    // (in one wave all single heads run at once)
+    const cudaError_t e = pairs && waves ? launch_prep<DK, F32, 2>(a, maps, ws, slots, st) : launch_prep<DK, F32, 1>(a, maps, ws, slots, st);
     return e != cudaSuccess ? e : launch_chain<DK, DV, F32>(a, maps.v, ws, st);
 }
 
