@@ -15,7 +15,7 @@ from .kda import (  # noqa: F401
     kda_prefill_workspace_bytes, kda_verify_log_bytes, kda_verify_window,
     load, status_string,
     # the gated delta rule with one decay per head, and what stands around it
-    KDA_MAX_POOL_SLOTS, KDA_NORM_GATE_NONE, KDA_NORM_GATE_SIGMOID, KDA_NORM_GATE_SILU, ConvParams, GdnParams,
+    KDA_MAX_POOL_SLOTS, KDA_MAX_ROWS, KDA_NORM_GATE_NONE, KDA_NORM_GATE_SIGMOID, KDA_NORM_GATE_SILU, ConvParams, GdnParams,
     NormParams, SlotPool, kda_block_norm, kda_conv_decode, kda_conv_varlen, kda_gdn_decode,
     kda_gdn_prefill_varlen, kda_gdn_prefill_workspace_bytes, kda_slots_compact_plan, kda_slots_copy,
     kda_slots_zero,

@@ -413,7 +413,8 @@ KDA_API int kda_gdn_prefill_varlen(const kda_gdn_params* p, const int32_t* cu_se
 {
     int rc = check_gdn(p);
     if (rc != KDA_OK) return rc;
-    if (N < 0 || T < 0 || ((int64_t)T / 64 + 4 * (int64_t)N) * p->num_heads_v > INT32_MAX) return KDA_ERR_INVALID_ARGUMENT;
+    if (N < 0 || T < 0 || T > KDA_MAX_ROWS || ((int64_t)T / 64 + 4 * (int64_t)N) * p->num_heads_v > INT32_MAX)
+        return KDA_ERR_INVALID_ARGUMENT;
     if (N == 0 || T == 0) return KDA_OK;
     GdnArgs g;
     fill_gdn(g, p);

@@ -38,6 +38,7 @@ KDA_NORM_GATE_NONE = 0
 KDA_NORM_GATE_SIGMOID = 1
 KDA_NORM_GATE_SILU = 2
 KDA_MAX_POOL_SLOTS = 262144
+KDA_MAX_ROWS = 2147483000
 
 
 class kda_params(ctypes.Structure):

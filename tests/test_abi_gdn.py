@@ -173,3 +173,12 @@ def test_lists_and_workspace_apart_from_what_is_written():
     assert kda.kda_conv_varlen(conv, addr(1), 2, 8, addr(2), None, addr(3), addr(4), None, 0) == INVALID
     conv = kda.ConvParams(channels=64, conv_kernel=4, conv_weight=addr(9), num_slots=3)
     assert kda.kda_conv_varlen(conv, addr(1), (1 << 31) - 1, 1 << 20, addr(2), None, addr(3), addr(4), None, 0) == INVALID
+
+
+def test_row_counts_past_the_index_range():
+    rows = (1 << 31) - 1
+    assert _prefill(_gdn(num_heads_k=1, num_heads_v=1, head_dim_k=32, head_dim_v=32), N=1, T=rows) == INVALID
+    conv = kda.ConvParams(channels=8, conv_kernel=2, conv_weight=addr(9), num_slots=3)
+    far = 1 << 50
+    assert kda.kda_conv_varlen(conv, addr(1), 1, rows, far, None, addr(3), 2 * far, None, 0) == INVALID
+    assert kda.kda_conv_decode(conv, rows, far, None, addr(3), 2 * far, None, 0) == INVALID

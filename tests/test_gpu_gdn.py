@@ -534,3 +534,22 @@ def test_prefill_many_sequences(cuda_lib, N):
     c = Case(lens.tolist(), Hk=1, Hv=2, dk=32, dv=32, seed=91, slots=np.random.default_rng(1).permutation(N).tolist())
     c.prefill(cuda_lib)
     c.check()
+
+
+@pytest.mark.parametrize("Hv,rows", [(2, 200), (16, 2600)])
+def test_prefill_bad_gates_stay_in_their_sequence_and_head(cuda_lib, Hv, rows):
+    """A NaN or infinite gate logit ends in its own sequence's rows and state, and leaves no wait behind."""
+    bad, clean = (Case([rows, 70, 130], Hk=2, Hv=Hv, dk=32, dv=32, seed=95) for _ in range(2))
+    assert _beside(bad) == (Hv == 16)
+    clean.prefill(cuda_lib)
+    bad.a[30, 1] = float("nan")
+    bad.b[rows + 3, 0] = float("nan")
+    bad.a[rows + 75, 1] = float("-inf")   # no decay at all: finite
+    bad.prefill(cuda_lib)
+    same = torch.ones(bad.T, Hv, dtype=torch.bool, device="cuda")
+    same[:rows, 1] = same[rows:rows + 70, 0] = same[rows + 70:, 1] = False
+    assert torch.equal(bad.g_out.tensor[same], clean.g_out.tensor[same])
+    assert torch.equal(bad.g_state.tensor[0, 0], clean.g_state.tensor[0, 0])
+    assert torch.equal(bad.g_state.tensor[1, 1:], clean.g_state.tensor[1, 1:])
+    assert bad.g_state.tensor[0, 1].isnan().all() and bad.g_out.tensor[rows + 70:].isfinite().all()
+    assert int(bad.status.item()) == 0
