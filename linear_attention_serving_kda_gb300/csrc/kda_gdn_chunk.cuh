@@ -124,7 +124,7 @@ struct Waiter {
     bool dead;
     __device__ __forceinline__ void operator()(uint64_t& bar, int phase)
     {
-        if (!ptx::mbar_wait_short(&bar, phase & 1, dead ? 1u : 1u << 22)) dead = true;
+        if (!ptx::mbar_wait_short(&bar, phase & 1, dead ? 1u : 1u << 26)) dead = true;
     }
 };
 
@@ -142,8 +142,8 @@ struct Factors {
     float beta[C], ek[C];  // beta; beta e^G and k's row factor
     float e1[C], e2[C];    // scale, q's row factor, e^G (e1)
     float last, x;         // e^{G_C}; what M and P T still have to be multiplied by
-    float top, ektop;      // the largest values of M and ek
-    float pad[28];
+    float ektop;           // the largest value of ek
+    float pad[29];
 };
 template <int DK, bool F32> struct Slot {
     static constexpr int HALVES = DK <= 64 ? 1 : DK / 64;  // 64-wide tiles a row spans (dk = 32: half of one)
@@ -398,7 +398,7 @@ __device__ __forceinline__ void prep_task(PrepSmem<DK, F32, HEADS>& sm, const Gd
             }
         sm.fac[gate_head].beta[2 * lane] = bt[0];
         sm.fac[gate_head].beta[2 * lane + 1] = bt[1];
-        if (lane == 0) sm.fac[gate_head].top = sm.fac[gate_head].ektop = 0.f;
+        if (lane == 0) sm.fac[gate_head].ektop = 0.f;
         scan_rows(sm.gates[gate_head], make_float2(g[0], g[1]), sm.fac[gate_head].last, lane);
     }
     // a row of [K; Q] a lane (w & 3), against half of k's rows (w >> 2); the
@@ -434,20 +434,25 @@ __device__ __forceinline__ void prep_task(PrepSmem<DK, F32, HEADS>& sm, const Gd
         }
     };
 
+    float x = 1.f, xi = 1.f;
 #pragma unroll 1
     for (int j = 0; j < HEADS; ++j) {
         const typename S::Gates& gt = sm.gates[j];
         Factors& fac = sm.fac[j];
         if (w < 4) {
             const float ss = sm.norm[lr];
-            float down, up, x = 1.f, xi = 1.f;
+            float down, up;
             pow2_scale_sqrt(ss, down, up);
-            if (!a.l2) {
-                // k's row factors may be far from one: a power of two out of all of them
-                float mx = fmaxf(lane < n ? sm.norm[lane] : 0.f, lane + 32 < n ? sm.norm[lane + 32] : 0.f);
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                pow2_scale_sqrt(mx, xi, x);
+            if (j == 0) {
+                // k's row factors may all be far from one (no normalisation, or rows that are small
+                // next to its eps): a power of two out of all of them
+                auto square = [&](int row) {
+                    const float y = sm.norm[row];
+                    return row < n ? (a.l2 ? y / (y + a.l2_eps) : y) : 0.f;
+                };
+                const float mx = __uint_as_float(__reduce_max_sync(
+                    0xffffffffu, max(__float_as_uint(square(lane)), __float_as_uint(square(lane + 32)))));
+                if (mx > 0.f) pow2_scale_sqrt(mx, xi, x);
             }
             // the factor that makes the stored row the (normalised) row; none for a padded one
             const float nrm = r < n ? (a.l2 ? rsqrtf(ss + a.l2_eps) : 1.f) : 0.f, f = nrm * up;
@@ -639,13 +644,6 @@ __device__ __forceinline__ void prep_task(PrepSmem<DK, F32, HEADS>& sm, const Gd
                     mma(c[2 * q + 1], x, e[2], e[3]);
                 }
             }
-            float mx = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                mx = fmaxf(mx, fmaxf(fmaxf(fabsf(c[i][0]), fabsf(c[i][1])), fmaxf(fabsf(c[i][2]), fabsf(c[i][3]))));
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            if (lane == 0) atomicMax(reinterpret_cast<int*>(&fac.top), __float_as_int(mx));
         }
         team_sync(team);  // the tiles read above make room
         if (w * 16 < DK) store_tile(sm.m[0], sm.m[1], w * 16, c);
@@ -719,7 +717,7 @@ template <int DK, int DV, bool F32> struct ChainSmem {
     unsigned char v[2][C * DV * 2];                     // dense rows
     Factors fac[4];
     float f1[2][DV], f2[2][DV];  // the scales of S's and R's columns
-    float top[3][2][DV];         // the largest values of beta V's, R's and S's halves of a column
+    float top[2][2][DV];         // the largest values of beta V's and S's halves of a column
     uint64_t loaded[2], freed[2];
     uint64_t s_full, ks_full, qs_full, rh_full, rl_full, su_full, o_full, o_free, f_full[2];
     int found;
@@ -852,31 +850,42 @@ __device__ __forceinline__ void run_chains(unsigned char* dyn, const GdnArgs& a,
             constexpr int SK = DK / 2, RK = C / 2;
             const int pair = warp & 3, half = warp >> 2, c = pair * 32 + lane;
             const uint32_t at = tmem + ((uint32_t)(pair * 32) << 16);
-            // the larger of both halves' largest values
+            // the larger of both halves' largest values (each in its place by now)
             auto both = [&](int which, float x) {
-                sm.top[which][half][c] = x;
                 asm volatile("bar.sync %0, 64;" ::"r"(pair + 1) : "memory");
                 return fmaxf(x, sm.top[which][half ^ 1][c]);
             };
             for (int turn = 0; units.next(sm, a, ws, turn, u); ++turn) {
                 const int begin = u.begin, end = u.end, chunks = (end - begin + C - 1) / C;
                 float* state = a.state + ((size_t)u.slot * a.Hv + u.h) * DK * DV + (size_t)half * SK * DV + c;
-                // A bound on the column's values (the same in both halves): while it stays
-                // below 2^14 in S's scale, fp16 has room; the exact value now and then
-                // and where it does not.
-                float s[SK], mx = 0.f, bound, g, ig;
+                // s is S times g, the power of two of the column that brings its largest
+                // value near one for the fp16 operands.  Decays of many orders of magnitude a chunk are
+                // ordinary, and a value that has become much smaller than one would lose digits of its low part:
+                // so every chunk looks at the largest value again, and changes g where it is off.
+                float s[SK], g = 1.f, ig = 1.f;
 #pragma unroll
                 for (int i = 0; i < SK; ++i) s[i] = state[(size_t)i * DV];
-#pragma unroll
-                for (int i = 0; i < SK; i += 2) mx = max3(mx, fabsf(s[i]), fabsf(s[i + 1]));
-                bound = both(2, mx);
-                pow2_scale(bound, g, ig);
-#pragma unroll
-                for (int i = 0; i < SK; ++i) s[i] *= g;
                 for (int m = 0; m < chunks; ++m) {
                     const int q = q0 + m, b = q & 1, n = end - begin - m * C;
                     if (q > 0) wait(sm.qs_full, q - 1);  // S's place is free
+                    float most = 0.f, mx = 0.f;
+#pragma unroll
+                    for (int i = 0; i < SK; i += 2) most = max3(most, fabsf(s[i]), fabsf(s[i + 1]));
+                    // stored before the other half's largest value is known, and again where g was off
+                    sm.top[1][half][c] = most;
                     store_split<SK>(at + TM_SH + half * (SK / 2), at + TM_SL + half * (SK / 2), s);
+                    most = both(1, most);
+                    const bool off = !(most >= 0.125f && most < 0x1p14f) && most != 0.f;
+                    if (__any_sync(0xffffffffu, off)) {
+                        float down, up;
+                        pow2_scale(off ? most * ig : ig, down, up);
+                        const float f = down * ig;
+                        scale_all(s, f);
+                        most *= f;
+                        g = down;
+                        ig = up;
+                        store_split<SK>(at + TM_SH + half * (SK / 2), at + TM_SL + half * (SK / 2), s);
+                    }
                     ptx::tc_fence_before();
                     warp_arrive(sm.s_full, lane);
 
@@ -895,17 +904,17 @@ __device__ __forceinline__ void run_chains(unsigned char* dyn, const GdnArgs& a,
                     if (n < C)  // the copies took the next sequence's rows along
 #pragma unroll
                         for (int i = 0; i < RK; ++i) r[i] = half * RK + i < n ? r[i] : 0.f;
-                    mx = 0.f;
 #pragma unroll
                     for (int i = 0; i < RK; i += 2) mx = max3(mx, fabsf(r[i]), fabsf(r[i + 1]));
+                    sm.top[0][half][c] = mx;
                     // |k'| < 2, so |k'.S| <= 2 sqrt(dk) max |S|: R stays below 2^14 in the scale of this
                     // bound, and low parts do not mind how far below
                     float rd, ru;
-                    pow2_scale(both(0, mx) + fac.ektop * (DK == 128 ? 23.f : DK == 64 ? 16.f : 12.f) * bound, rd, ru);
+                    pow2_scale(both(0, mx) + fac.ektop * (DK == 128 ? 23.f : DK == 64 ? 16.f : 12.f) * (most * ig), rd, ru);
                     rd *= 0x1p13f;
                     ru *= 0x1p-13f;
                     scale_all(r, rd);
-                    const float last = fac.last, x = fac.x, top = fac.top;
+                    const float last = fac.last, x = fac.x;
                     if (q > 0) wait(sm.o_full, q - 1);  // R's place is free
                     wait(sm.ks_full, q);
                     ptx::tc_fence_after();
@@ -939,13 +948,6 @@ __device__ __forceinline__ void run_chains(unsigned char* dyn, const GdnArgs& a,
                     // S = e^{G_C} S + M^T R
                     scale_all(s, last);
                     const float fs = (ru * x) * g;
-                    mx = 0.f;
-#pragma unroll
-                    for (int i = 0; i < RK; i += 2) mx = max3(mx, fabsf(r[i]), fabsf(r[i + 1]));
-                    // (a wait that gave up makes it infinite: both halves see that, and still take the same turns)
-                    bound = last * bound + (float)C * top * x * (both(1, wait.dead ? __int_as_float(0x7f800000) : mx) * ru);
-                    const bool exact = __any_sync(0xffffffffu, !(bound * g < 0x1p14f) || (bound != 0.f && bound * g < 0x1p-6f)) ||
-                                       (m & 15) == 15;
                     wait(sm.su_full, q);
                     ptx::tc_fence_after();
                     constexpr int W = SK < 32 ? SK : 32;
@@ -960,18 +962,6 @@ __device__ __forceinline__ void run_chains(unsigned char* dyn, const GdnArgs& a,
                             s[z + i] = x.x;
                             s[z + i + 1] = x.y;
                         }
-                    }
-                    if (exact) {
-                        mx = 0.f;
-#pragma unroll
-                        for (int i = 0; i < SK; i += 2) mx = max3(mx, fabsf(s[i]), fabsf(s[i + 1]));
-                        bound = both(2, mx) * ig;
-                        float down, up;
-                        pow2_scale(bound, down, up);
-                        const float f = down * ig;
-                        scale_all(s, f);
-                        g = down;
-                        ig = up;
                     }
                     warp_arrive(sm.freed[b], lane);
                 }

@@ -553,3 +553,23 @@ def test_prefill_bad_gates_stay_in_their_sequence_and_head(cuda_lib, Hv, rows):
     assert torch.equal(bad.g_state.tensor[1, 1:], clean.g_state.tensor[1, 1:])
     assert bad.g_state.tensor[0, 1].isnan().all() and bad.g_out.tensor[rows + 70:].isfinite().all()
     assert int(bad.status.item()) == 0
+
+
+@pytest.mark.parametrize("lens,Hk,Hv,dk,dv,seed,kw", [
+    ([436], 8, 16, 128, 64, 739419993, dict(gate=3.0)),
+    ([300], 2, 4, 64, 128, 96, dict(beta=4.0)),
+    ([521], 4, 8, 32, 128, 1023189493, dict(l2=False)),
+    ([200, 130], 2, 2, 128, 128, 97, dict(l2=False, gate=2.0)),
+])
+@pytest.mark.parametrize("spread", [1e-6, 2.0 ** -40])
+def test_prefill_rows_far_below_the_state_they_meet(cuda_lib, lens, Hk, Hv, dk, dv, seed, kw, spread):
+    """Rows of another magnitude than the state decay it by many orders to theirs (and, normalised, are small
+    next to the norm's eps): the small state that is left has all its digits.
+
+    Tolerance: a row of T R is a sum of up to 64 terms, each off by 2^-22 of the largest.  Errors of either sign
+    add up to 8 * 2^-22, half of STATE; but the 64 rows of a chunk on 32 dims are never independent, each is
+    corrected along the ones before it, and errors of one sign add up to 64 * 2^-22 = 2^-16."""
+    c = Case(lens, Hk=Hk, Hv=Hv, dk=dk, dv=dv, seed=seed, out="f32", spread=spread, **kw)
+    c.prefill(cuda_lib)
+    tol = 2.0 ** -16 if dk < 64 else STATE
+    c.check(tol_out=tol, tol_state=tol)
