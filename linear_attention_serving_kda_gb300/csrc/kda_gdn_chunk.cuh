@@ -21,16 +21,16 @@
 // Bounds and figures (16 key and 32 value heads of 128 x 128, bf16 outputs).  Neither HBM
 // (a quarter of its time at most: rows 0.8 GB and workspace 2 GB for 32768 rows) nor the tensor cores
 // (24 % busy) but dependent steps: prep issues an instruction every other cycle and
-// else waits at its barriers, 322 us for 32768 rows with 24 warps an SM; a chunk of a chain takes 2.4 us,
+// else waits at its barriers, 322 us for 32768 rows with 24 warps an SM; a chunk of a chain takes 2.5 us,
 // of which the products are 1.0 and the rest the state's way between registers and
-// TMEM.  32768 rows as eight prompts 682 us, as one prompt 1250, which is its 512 chunks one after the other.
+// TMEM.  32768 rows as eight prompts 688 us, as one prompt 1293, which is its 512 chunks one after the other.
 //
 // Precision: the state keeps fp32 accuracy.  One decay per head leaves k and q
 // unscaled inside every product, so the rows' bf16 values are operands without
 // loss: prep rescales each row by a power of two to a norm in [1, 2) and stores
 // it as fp16 (exact down to 2^-17).  Every other operand that reaches the state
 // (S, R, T, M) is two fp16 values, high and low, about 22 bits; S and R are
-// scaled by a power of two per column so that the low part stays in fp16's range.  P, P T
+// scaled by a power of two per column and chunk, M by one per chunk, so that the low part stays in fp16's range.  P, P T
 // and the outputs' reading of S and R keep the high part only where the outputs
 // are bf16 (11 bits against their 8).
 #pragma once
@@ -1462,11 +1462,11 @@ template <int DK, int DV, bool F32>
 cudaError_t launch_dv(const GdnArgs& a, const RowMaps& maps, const Work& ws, long long slots, cudaStream_t st)
 {
     // Two heads a team (their rows, products and norms once): 32768 rows as eight prompts take
-    // 682 us, 783 with one; one prompt 1250 and 1238.
+    // 688 us, 801 with one; one prompt 1293 and 1284.
     const bool pairs = a.Hv / a.Hk % 2 == 0, waves = slots * a.Hv > prep_ctas<F32>() * sm_count();
     // Chains beside prep where prep is more than one wave of CTAs: 32768 rows of 32 heads take
-    // 682 us as eight prompts of mixed lengths (847 one after the other), 1250 as one (1640),
-    // 662 as sixteen (637); 7001 rows of 12 heads 114 (137); but 333 rows of 8 heads 40 us, 23 one after the other.
+    // 688 us as eight prompts of mixed lengths (852 one after the other), 1293 as one (1631),
+    // 675 as sixteen (644); 7001 rows of 12 heads 115 (138); but 333 rows of 8 heads 41 us, 24 one after the other.
     if (a.N <= MERGED && waves)
         return pairs ? launch_beside<DK, DV, F32, 2>(a, maps, ws, slots, st) : launch_beside<DK, DV, F32, 1>(a, maps, ws, slots, st);
     // (in one wave all single heads run at once)
