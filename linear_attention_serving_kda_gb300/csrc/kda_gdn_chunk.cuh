@@ -6,7 +6,11 @@
 //     R    = diag(beta) V - diag(beta e^G) K S           (U = T R: the rule's updates)
 //     S'   = e^{G_C} S + M^T R,   M = T^T diag(e^{G_C - G}) K
 //     O    = diag(e^G) Q S + (P T) R,   P_rs = e^{G_r - G_s} q_r.k_s  (s <= r)
-// All exponents are differences that are <= 0.
+// All exponents are differences that are <= 0.  The key rows' factors (powers of two,
+// the norm) stay out of T, M and P: with k_r = f_r k'_r, |k'_r| in [1, 2), and F = diag(f),
+//     F A F^-1 has the entries beta_r f_r^2 e^{G_r - G_s} k'_r.k'_s,  F R takes R's place,
+// and M, P and K S have K' in K's place: no entry of F T F^-1 exceeds 4 while beta |k|^2 <= 2, whatever
+// the rows' magnitudes.  Below, A, T, M, P and R are those.
 //
 // Only S goes from chunk to chunk, so the work is cut where S enters:
 //   - prep, a team of eight warps per (chunk, one or two value heads), all chunks at
@@ -30,7 +34,7 @@
 // loss: prep rescales each row by a power of two to a norm in [1, 2) and stores
 // it as fp16 (exact down to 2^-17).  Every other operand that reaches the state
 // (S, R, T, M) is two fp16 values, high and low, about 22 bits; S and R are
-// scaled by a power of two per column and chunk, M by one per chunk, so that the low part stays in fp16's range.  P, P T
+// scaled by a power of two per column and chunk, so that the low part stays in fp16's range.  P, P T
 // and the outputs' reading of S and R keep the high part only where the outputs
 // are bf16 (11 bits against their 8).
 #pragma once
@@ -139,11 +143,11 @@ __device__ __forceinline__ void warp_arrive(uint64_t& bar, int lane)
 // What prep leaves for a chunk: [K; Q] for each key head, and for each value head
 // M^T (dk rows over the chunk's rows, high and low), P T (high; and low), and the factors.
 struct Factors {
-    float beta[C], ek[C];  // beta; beta e^G and k's row factor
+    float beta[C], ek[C];  // beta f; beta f^2 e^G
     float e1[C], e2[C];    // scale, q's row factor, e^G (e1)
-    float last, x;         // e^{G_C}; what M and P T still have to be multiplied by
+    float last;            // e^{G_C}
     float ektop;           // the largest value of ek
-    float pad[29];
+    float pad[30];
 };
 template <int DK, bool F32> struct Slot {
     static constexpr int HALVES = DK <= 64 ? 1 : DK / 64;  // 64-wide tiles a row spans (dk = 32: half of one)
@@ -189,7 +193,7 @@ template <int DK, bool F32, int HEADS> struct PrepSmem {
         alignas(16) float eg[C], gh[C], gl[C], w[C];  // e^G, G / ln 2 in two words, e^{G_C - G}
     } gates[HEADS];
     alignas(16) float norm[2 * C];  // squared norms of k's and q's rows
-    alignas(16) float row[2 * C], col[2][C], down[2 * C], fm[C];  // factors of A's and P's rows, of their columns; of the stored rows; of M's
+    alignas(16) float row[2 * C], down[2 * C];  // factors of A's and P's rows; of the stored rows, k's of A's and P's columns
     uint64_t loaded, prod;
     uint32_t tmem;
 };
@@ -434,7 +438,6 @@ __device__ __forceinline__ void prep_task(PrepSmem<DK, F32, HEADS>& sm, const Gd
         }
     };
 
-    float x = 1.f, xi = 1.f;
 #pragma unroll 1
     for (int j = 0; j < HEADS; ++j) {
         const typename S::Gates& gt = sm.gates[j];
@@ -443,30 +446,15 @@ __device__ __forceinline__ void prep_task(PrepSmem<DK, F32, HEADS>& sm, const Gd
             const float ss = sm.norm[lr];
             float down, up;
             pow2_scale_sqrt(ss, down, up);
-            if (j == 0) {
-                // k's row factors may all be far from one (no normalisation, or rows that are small
-                // next to its eps): a power of two out of all of them
-                auto square = [&](int row) {
-                    const float y = sm.norm[row];
-                    return row < n ? (a.l2 ? y / (y + a.l2_eps) : y) : 0.f;
-                };
-                const float mx = __uint_as_float(__reduce_max_sync(
-                    0xffffffffu, max(__float_as_uint(square(lane)), __float_as_uint(square(lane + 32)))));
-                if (mx > 0.f) pow2_scale_sqrt(mx, xi, x);
-            }
-            // the factor that makes the stored row the (normalised) row; none for a padded one
+            // f: what makes the stored row the (normalised) row; none for a padded one
             const float nrm = r < n ? (a.l2 ? rsqrtf(ss + a.l2_eps) : 1.f) : 0.f, f = nrm * up;
             sm.down[lr] = down;
             if (type == 0) {
-                const float be = fac.beta[r];
-                const float ek = be * f * gt.eg[r];
+                const float be = fac.beta[r], ek = be * f * f * gt.eg[r];
+                fac.beta[r] = be * f;
                 fac.ek[r] = ek;
                 atomicMax(reinterpret_cast<int*>(&fac.ektop), __float_as_int(fabsf(ek)));  // >= 0: ordered as integers
-                sm.fm[r] = (f * xi) * gt.w[r];
-                sm.col[0][r] = nrm;               // A comes from the raw rows' products,
-                sm.col[1][r] = down * (f * xi);   // P is that of the stored rows, times what T's rows get
-                sm.row[r] = be * nrm;
-                if (t == 0) fac.x = x;
+                sm.row[r] = be * nrm * f;  // from the raw rows' products, with their columns' down
             } else {
                 fac.e1[r] = a.scale * f * gt.eg[r];
                 fac.e2[r] = a.scale * f;
@@ -478,7 +466,6 @@ __device__ __forceinline__ void prep_task(PrepSmem<DK, F32, HEADS>& sm, const Gd
         if (w != 4 && w != 6) {
             // the lane's row of A (beta_r |..| e^{G_r - G_s} k_r.k_s) or P, zero from the diagonal (or past it) on
             const float rh = gt.gh[r], rl = gt.gl[r], rf = sm.row[lr];
-            const float* cf = sm.col[type];
             const int lim = r < n ? r + type : 0;
             unsigned char* hi_tile = type == 0 ? sm.t_hi : sm.p_hi;
             unsigned char* lo_tile = type == 0 ? sm.t_lo : sm.p_lo;
@@ -492,7 +479,7 @@ __device__ __forceinline__ void prep_task(PrepSmem<DK, F32, HEADS>& sm, const Gd
                     const int s = s0 + p * 8 + z * 2;
                     const float2 ch = *reinterpret_cast<const float2*>(&gt.gh[s]);
                     const float2 cl = *reinterpret_cast<const float2*>(&gt.gl[s]);
-                    const float2 c2 = *reinterpret_cast<const float2*>(&cf[s]);
+                    const float2 c2 = *reinterpret_cast<const float2*>(&sm.down[s]);
                     const float2 e = add2(sub2(both2(rh), ch), sub2(both2(rl), cl));
                     const float2 x = mul2(mul2(mul2(both2(rf), c2), make_float2(exp2_sfu(e.x), exp2_sfu(e.y))),
                                           make_float2(d[2 * z], d[2 * z + 1]));
@@ -578,7 +565,7 @@ __device__ __forceinline__ void prep_task(PrepSmem<DK, F32, HEADS>& sm, const Gd
         };
         clear();
         if (w >= 4) {
-            // P T (k's row factors are in P's columns): sixteen rows a warp
+            // P T: sixteen rows a warp
             const int mt = w - 4;
             const uint32_t pb[2] = {ptx::smem_u32(sm.p_hi), ptx::smem_u32(sm.p_lo)};
             const uint32_t tb[2] = {ptx::smem_u32(sm.t_hi), ptx::smem_u32(sm.t_lo)};
@@ -605,12 +592,12 @@ __device__ __forceinline__ void prep_task(PrepSmem<DK, F32, HEADS>& sm, const Gd
         } else if (t == 0) ptx::bulk_wait_read_all();  // [K; Q] is on its way: room for P T over q's rows
         team_sync(team);
         if (w >= 4) store_tile(sm.kq + 8192, F32 ? sm.pt_lo : nullptr, (w - 4) * 16, c);
-        // T with M's row factors, in pieces of eight values up to each diagonal block's end: 32 + 64 + 96 + 128
+        // T with M's row factors e^{G_C - G}, in pieces of eight values up to each diagonal block's end: 32 + 64 + 96 + 128
 #pragma unroll 1
         for (int i = t; i < 320; i += PREP) {
             const int kt = i < 32 ? 0 : i < 96 ? 1 : i < 192 ? 2 : 3, l = i - 16 * kt * (kt + 1);
             const int rr = kt * 16 + l / (2 * kt + 2), pc = l % (2 * kt + 2);
-            const float f = sm.fm[rr];
+            const float f = gt.w[rr];
             uint4* hp = reinterpret_cast<uint4*>(sm.t_hi + tile_at(rr, pc));
             uint4* lp = reinterpret_cast<uint4*>(sm.t_lo + tile_at(rr, pc));
             const uint4 h4 = *hp, l4 = *lp;
@@ -914,7 +901,7 @@ __device__ __forceinline__ void run_chains(unsigned char* dyn, const GdnArgs& a,
                     rd *= 0x1p13f;
                     ru *= 0x1p-13f;
                     scale_all(r, rd);
-                    const float last = fac.last, x = fac.x;
+                    const float last = fac.last;
                     if (q > 0) wait(sm.o_full, q - 1);  // R's place is free
                     wait(sm.ks_full, q);
                     ptx::tc_fence_after();
@@ -941,13 +928,13 @@ __device__ __forceinline__ void run_chains(unsigned char* dyn, const GdnArgs& a,
                     warp_arrive(sm.rl_full, lane);
                     if (half == 0) {
                         sm.f1[b][c] = ig;
-                        sm.f2[b][c] = ru * x;
+                        sm.f2[b][c] = ru;
                         warp_arrive(sm.f_full[b], lane);
                     }
 
                     // S = e^{G_C} S + M^T R
                     scale_all(s, last);
-                    const float fs = (ru * x) * g;
+                    const float fs = ru * g;
                     wait(sm.su_full, q);
                     ptx::tc_fence_after();
                     constexpr int W = SK < 32 ? SK : 32;
@@ -1422,7 +1409,7 @@ cudaError_t launch_prep(const GdnArgs& a, const RowMaps& maps, const Work& ws, l
     using S = PrepSmem<DK, F32, HEADS>;
     constexpr int smem = sizeof(S);
     static_assert(offsetof(S, t_hi) % 128 == 0 && offsetof(S, fac) % 16 == 0 && offsetof(S, m) % 16 == 0 &&
-                  offsetof(S, xd) % 16 == 0 && offsetof(S, gates) % 16 == 0 && offsetof(S, col) % 16 == 0 &&
+                  offsetof(S, xd) % 16 == 0 && offsetof(S, gates) % 16 == 0 &&
                   offsetof(S, down) % 16 == 0 && offsetof(S, loaded) % 8 == 0, "alignment");
     static_assert((smem + 1024) * prep_ctas<F32>() <= 228 * 1024, "shared memory");
     static PerDeviceOnce once;

@@ -573,3 +573,15 @@ def test_prefill_rows_far_below_the_state_they_meet(cuda_lib, lens, Hk, Hv, dk, 
     c.prefill(cuda_lib)
     tol = 2.0 ** -16 if dk < 64 else STATE
     c.check(tol_out=tol, tol_state=tol)
+
+
+@pytest.mark.parametrize("Hv,dk", [(2, 128), (4, 64)])
+def test_prefill_keys_of_all_magnitudes(cuda_lib, Hv, dk):
+    """Without the norm, keys from 2^-12 to 2^12 side by side, their beta |k|^2 up to one: T as it stands would
+    have entries of 2^24 and more."""
+    c = Case([200, 90], Hk=2, Hv=Hv, dk=dk, dv=64, seed=98, out="f32", l2=False)
+    e = torch.from_numpy(np.random.default_rng(98).integers(-12, 13, (c.T, 1))).cuda()
+    c.k.copy_(torch.ldexp(c.k.float(), e))
+    c.b.copy_((-2 * math.log(2.0)) * e.clamp(min=0) + c.b.float().clamp(max=0))
+    c.prefill(cuda_lib)
+    c.check()
