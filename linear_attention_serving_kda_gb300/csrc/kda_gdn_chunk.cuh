@@ -901,7 +901,6 @@ __device__ __forceinline__ void run_chains(unsigned char* dyn, const GdnArgs& a,
                     rd *= 0x1p13f;
                     ru *= 0x1p-13f;
                     scale_all(r, rd);
-                    const float last = fac.last;
                     if (q > 0) wait(sm.o_full, q - 1);  // R's place is free
                     wait(sm.ks_full, q);
                     ptx::tc_fence_after();
@@ -933,7 +932,7 @@ __device__ __forceinline__ void run_chains(unsigned char* dyn, const GdnArgs& a,
                     }
 
                     // S = e^{G_C} S + M^T R
-                    scale_all(s, last);
+                    scale_all(s, fac.last);
                     const float fs = ru * g;
                     wait(sm.su_full, q);
                     ptx::tc_fence_after();
