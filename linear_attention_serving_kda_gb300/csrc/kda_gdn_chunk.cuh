@@ -27,7 +27,7 @@
 // (24 % busy) but dependent steps: prep issues an instruction every other cycle and
 // else waits at its barriers, 322 us for 32768 rows with 24 warps an SM; a chunk of a chain takes 2.5 us,
 // of which the products are 1.0 and the rest the state's way between registers and
-// TMEM.  32768 rows as eight prompts 688 us, as one prompt 1293, which is its 512 chunks one after the other.
+// TMEM.  32768 rows as eight prompts 699 us, as one prompt 1317, which is its 512 chunks one after the other.
 //
 // Precision: the state keeps fp32 accuracy.  One decay per head leaves k and q
 // unscaled inside every product, so the rows' bf16 values are operands without
@@ -996,7 +996,7 @@ __device__ __forceinline__ void run_chains(unsigned char* dyn, const GdnArgs& a,
             // The critical products from two warps: K S of S's high parts and M^T R, K S of
             // its low parts.  The warps stay whole and one lane of each issues: from a branch of
             // that lane's own every operand is moved over first, and a long prompt
-            // takes 1316 us where it takes 1245 like this.
+            // takes 5 % longer.
             const bool first = warp == 9;
             const uint32_t leader = ptx::elect_one();
             for (int turn = 0; units.next(sm, a, ws, turn, u); ++turn) {
@@ -1448,11 +1448,11 @@ template <int DK, int DV, bool F32>
 cudaError_t launch_dv(const GdnArgs& a, const RowMaps& maps, const Work& ws, long long slots, cudaStream_t st)
 {
     // Two heads a team (their rows, products and norms once): 32768 rows as eight prompts take
-    // 688 us, 801 with one; one prompt 1293 and 1284.
+    // 699 us, 785 with one; one prompt 1317 and 1310.
     const bool pairs = a.Hv / a.Hk % 2 == 0, waves = slots * a.Hv > prep_ctas<F32>() * sm_count();
     // Chains beside prep where prep is more than one wave of CTAs: 32768 rows of 32 heads take
-    // 688 us as eight prompts of mixed lengths (852 one after the other), 1293 as one (1631),
-    // 675 as sixteen (644); 7001 rows of 12 heads 115 (138); but 333 rows of 8 heads 41 us, 24 one after the other.
+    // 699 us as eight prompts of mixed lengths (840 one after the other), 1317 as one (1625),
+    // 675 as sixteen (632); 7001 rows of 12 heads 115 (137); but 333 rows of 8 heads 41 us, 24 one after the other.
     if (a.N <= MERGED && waves)
         return pairs ? launch_beside<DK, DV, F32, 2>(a, maps, ws, slots, st) : launch_beside<DK, DV, F32, 1>(a, maps, ws, slots, st);
     // (in one wave all single heads run at once)
