@@ -358,6 +358,8 @@ typedef struct kda_gdn_params {
  *     fp16 high and low parts where one fp16 does not hold the value);
  *     fp32 rows run row by row in fp32.
  *   - A prompt cut into several calls agrees with one uncut call to rounding.
+ *     A chunk that leaves a state more than 2^12 below the one it met keeps
+ *     about 2^-34 of the old one in place of 2^-21 of the new one.
  *   - Values up to 2^60 in magnitude keep that accuracy (operands are rescaled
  *     by powers of two within 2^+-60).  With l2_norm = 0 keys are expected to
  *     satisfy beta |k|^2 <= 2, beyond which the rule itself grows without bound.

@@ -143,7 +143,7 @@ __device__ __forceinline__ void warp_arrive(uint64_t& bar, int lane)
 // What prep leaves for a chunk: [K; Q] for each key head, and for each value head
 // M^T (dk rows over the chunk's rows, high and low), P T (high; and low), and the factors.
 struct Factors {
-    float beta[C], ek[C];  // beta f; beta f^2 e^G
+    float beta[C], ek[C];  // beta f D; beta f^2 e^G D
     float e1[C], e2[C];    // scale, q's row factor, e^G (e1)
     float last;            // e^{G_C}
     float ektop;           // the largest value of ek
@@ -193,7 +193,7 @@ template <int DK, bool F32, int HEADS> struct PrepSmem {
         alignas(16) float eg[C], gh[C], gl[C], w[C];  // e^G, G / ln 2 in two words, e^{G_C - G}
     } gates[HEADS];
     alignas(16) float norm[2 * C];  // squared norms of k's and q's rows
-    alignas(16) float row[2 * C], down[2 * C];  // factors of A's and P's rows; of the stored rows, k's of A's and P's columns
+    alignas(16) float inv[C], row[2 * C], down[2 * C];  // factors of A's and P's rows; of the stored rows, k's of A's and P's columns
     uint64_t loaded, prod;
     uint32_t tmem;
 };
@@ -450,11 +450,16 @@ __device__ __forceinline__ void prep_task(PrepSmem<DK, F32, HEADS>& sm, const Gd
             const float nrm = r < n ? (a.l2 ? rsqrtf(ss + a.l2_eps) : 1.f) : 0.f, f = nrm * up;
             sm.down[lr] = down;
             if (type == 0) {
-                const float be = fac.beta[r], ek = be * f * f * gt.eg[r];
+                // R's rows times D: a power of two near e^{G_C - G}, so that rows which the chunk's end
+                // has forgotten do not set the scale of those it has not; M's and P T's columns take
+                // 1 / D, at most 2^12 for P T's sake (its entries stay below 2^14)
+                const float dd = __uint_as_float(__float_as_uint(fminf(fmaxf(gt.w[r], 0x1p-12f), 1.f)) & 0x7f800000u);
+                const float be = fac.beta[r] * dd, ek = be * f * f * gt.eg[r];
+                sm.inv[r] = __uint_as_float((254u << 23) - __float_as_uint(dd));
                 fac.beta[r] = be * f;
                 fac.ek[r] = ek;
                 atomicMax(reinterpret_cast<int*>(&fac.ektop), __float_as_int(fabsf(ek)));  // >= 0: ordered as integers
-                sm.row[r] = be * nrm * f;  // from the raw rows' products, with their columns' down
+                sm.row[r] = be * sm.inv[r] * nrm * f;  // from the raw rows' products, with their columns' down
             } else {
                 fac.e1[r] = a.scale * f * gt.eg[r];
                 fac.e2[r] = a.scale * f;
@@ -591,7 +596,14 @@ __device__ __forceinline__ void prep_task(PrepSmem<DK, F32, HEADS>& sm, const Gd
             }
         } else if (t == 0) ptx::bulk_wait_read_all();  // [K; Q] is on its way: room for P T over q's rows
         team_sync(team);
-        if (w >= 4) store_tile(sm.kq + 8192, F32 ? sm.pt_lo : nullptr, (w - 4) * 16, c);
+        if (w >= 4) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float2 v = *reinterpret_cast<const float2*>(&sm.inv[i * 8 + (lane & 3) * 2]);
+                c[i][0] *= v.x; c[i][1] *= v.y; c[i][2] *= v.x; c[i][3] *= v.y;
+            }
+            store_tile(sm.kq + 8192, F32 ? sm.pt_lo : nullptr, (w - 4) * 16, c);
+        }
         // T with M's row factors e^{G_C - G}, in pieces of eight values up to each diagonal block's end: 32 + 64 + 96 + 128
 #pragma unroll 1
         for (int i = t; i < 320; i += PREP) {
@@ -605,7 +617,7 @@ __device__ __forceinline__ void prep_task(PrepSmem<DK, F32, HEADS>& sm, const Gd
             uint32_t wh[4], wl[4];
 #pragma unroll
             for (int z = 0; z < 4; ++z) {
-                const float2 x = mul2(add2(unpack_h(hv[z]), unpack_h(lv[z])), both2(f));
+                const float2 x = mul2(mul2(add2(unpack_h(hv[z]), unpack_h(lv[z])), both2(f)), *reinterpret_cast<const float2*>(&sm.inv[pc * 8 + 2 * z]));
                 split_h(x.x, x.y, wh[z], wl[z]);
             }
             *hp = make_uint4(wh[0], wh[1], wh[2], wh[3]);
