@@ -354,9 +354,9 @@ typedef struct kda_gdn_params {
  * whose cu_seqlens are bad is flagged and skipped; what such a call gives for
  * the others is unspecified, within their own rows and slots.
  *   - bf16 rows run in chunks of 64 on the tensor cores.  The states keep fp32
- *     accuracy (every product that reaches them has operands split into
- *     fp16 high and low parts where one fp16 does not hold the value);
- *     fp32 rows run row by row in fp32.
+ *     accuracy, and so do the outputs up to their rounding to out_dtype (every
+ *     product has operands split into fp16 high and low parts where one fp16
+ *     does not hold the value); fp32 rows run row by row in fp32.
  *   - A prompt cut into several calls agrees with one uncut call to rounding.
  *     A chunk that leaves a state more than 2^12 below the one it met keeps
  *     about 2^-34 of the old one in place of 2^-21 of the new one.
@@ -367,8 +367,8 @@ typedef struct kda_gdn_params {
  *     own it may reach rows from its 64-row chunk's first on.
  *   - workspace: kda_gdn_prefill_workspace_bytes(p, N, T) bytes (may be NULL
  *     when that is 0, for fp32 rows); it grows with
- *     (T/64 + N) heads: 0.97 GB for 32768 rows, 16 key and 32 value heads of
- *     128.  Contents need no init.  Calls that may run at the same time take a
+ *     (T/64 + N) heads: 1.10 GB for 32768 rows, 16 key and 32 value heads of
+ *     128, whatever the out_dtype.  Contents need no init.  Calls that may run at the same time take a
  *     workspace each.
  *   - Long calls run as one cooperative grid of a CTA an SM; a call on a device
  *     of which other work holds SMs waits for them.

@@ -403,7 +403,7 @@ extern "C" {
 KDA_API size_t kda_gdn_prefill_workspace_bytes(const kda_gdn_params* p, int32_t N, int32_t T)
 {
     if (check_gdn(p) != KDA_OK || N <= 0 || T <= 0 || p->io_dtype != KDA_DTYPE_BF16) return 0;
-    return gdn_chunk_workspace_bytes(p->num_heads_k, p->num_heads_v, p->head_dim_k, p->out_dtype == KDA_DTYPE_BF16, N, T);
+    return gdn_chunk_workspace_bytes(p->num_heads_k, p->num_heads_v, p->head_dim_k, N, T);
 }
 
 KDA_API int kda_gdn_prefill_varlen(const kda_gdn_params* p, const int32_t* cu_seqlens, int32_t N, int32_t T,

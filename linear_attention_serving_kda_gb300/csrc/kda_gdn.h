@@ -90,6 +90,6 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 // Prefill row by row (fp32 rows), and in chunks on the tensor cores (bf16 rows).
 cudaError_t launch_gdn_rows(const GdnArgs& a, int dk, int dv, cudaStream_t st);
 cudaError_t launch_gdn_chunk(const GdnArgs& a, int dk, int dv, bool out_bf16, cudaStream_t st);
-size_t gdn_chunk_workspace_bytes(int Hk, int Hv, int dk, bool out_bf16, int N, int T);
+size_t gdn_chunk_workspace_bytes(int Hk, int Hv, int dk, int N, int T);
 
 }  // namespace kda

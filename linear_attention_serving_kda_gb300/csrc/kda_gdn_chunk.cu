@@ -10,17 +10,16 @@ cudaError_t launch_gdn_chunk_64(const GdnArgs& a, int dv, bool out_bf16, cudaStr
 
 namespace {
 
-template <int DK> size_t slot_bytes(int Hk, int Hv, bool bf16)
+template <int DK> size_t slot_bytes(int Hk, int Hv)
 {
-    return (size_t)Hk * Slot<DK, false>::KQ + (size_t)Hv * ((bf16 ? Slot<DK, false>::V : Slot<DK, true>::V) + sizeof(int));
+    return (size_t)Hk * Slot<DK>::KQ + (size_t)Hv * (Slot<DK>::V + sizeof(int));
 }
 
 }  // namespace
 
-size_t gdn_chunk_workspace_bytes(int Hk, int Hv, int dk, bool out_bf16, int N, int T)
+size_t gdn_chunk_workspace_bytes(int Hk, int Hv, int dk, int N, int T)
 {
-    const size_t b = dk == 128 ? slot_bytes<128>(Hk, Hv, out_bf16) : dk == 64 ? slot_bytes<64>(Hk, Hv, out_bf16)
-                                                                             : slot_bytes<32>(Hk, Hv, out_bf16);
+    const size_t b = dk == 128 ? slot_bytes<128>(Hk, Hv) : dk == 64 ? slot_bytes<64>(Hk, Hv) : slot_bytes<32>(Hk, Hv);
     return (size_t)slot_count(N, T) * b + sizeof(int);
 }
 

@@ -27,16 +27,17 @@
 // (24 % busy) but dependent steps: prep issues an instruction every other cycle and
 // else waits at its barriers, 322 us for 32768 rows with 24 warps an SM; a chunk of a chain takes 2.5 us,
 // of which the products are 1.0 and the rest the state's way between registers and
-// TMEM.  32768 rows as eight prompts 699 us, as one prompt 1317, which is its 512 chunks one after the other.
+// TMEM.  32768 rows as eight prompts 737 us, as one prompt 1350, which is its 512 chunks one after the other.
 //
 // Precision: the state keeps fp32 accuracy.  One decay per head leaves k and q
 // unscaled inside every product, so the rows' bf16 values are operands without
 // loss: prep rescales each row by a power of two to a norm in [1, 2) and stores
-// it as fp16 (exact down to 2^-17).  Every other operand that reaches the state
-// (S, R, T, M) is two fp16 values, high and low, about 22 bits; S and R are
-// scaled by a power of two per column and chunk, so that the low part stays in fp16's range.  P, P T
-// and the outputs' reading of S and R keep the high part only where the outputs
-// are bf16 (11 bits against their 8).
+// it as fp16 (exact down to 2^-17).  Every other operand
+// (S, R, T, M, P, P T) is two fp16 values, high and low, about 22 bits; S and R are
+// scaled by a power of two per column and chunk, so that the low part stays in fp16's range.
+// That holds for bf16 outputs too: on nearly equal keys an output is a small difference of
+// large products, and high parts alone (eight prompts 705 us in place of 737, one 1324 in place
+// of 1350) put 3 % of such outputs more than a bf16 step and 1e-3 of their RMS off.
 #pragma once
 
 #include <cstddef>
@@ -52,7 +53,9 @@ namespace kda {
 namespace {
 
 constexpr int C = 64;
-constexpr int XS = 20;  // row stride of the fp32 diagonal blocks
+// Float index of 16-byte piece `p` of row r of A's fp32 diagonal blocks: rows of 16 values,
+// pieces permuted so that eight rows' same piece lie in distinct banks.
+__device__ __forceinline__ int diag_at(int r, int p) { return r * 16 + ((p ^ (r >> 1)) & 3) * 4; }
 
 // ------------------------------------------------------------ fragments
 
@@ -141,7 +144,7 @@ __device__ __forceinline__ void warp_arrive(uint64_t& bar, int lane)
 // ------------------------------------------------------------ workspace
 
 // What prep leaves for a chunk: [K; Q] for each key head, and for each value head
-// M^T (dk rows over the chunk's rows, high and low), P T (high; and low), and the factors.
+// M^T (dk rows over the chunk's rows) and P T, high and low each, and the factors.
 struct Factors {
     float beta[C], ek[C];  // beta f D; beta f^2 e^G D
     float e1[C], e2[C];    // scale, q's row factor, e^G (e1)
@@ -149,10 +152,10 @@ struct Factors {
     float ektop;           // the largest value of ek
     float pad[30];
 };
-template <int DK, bool F32> struct Slot {
+template <int DK> struct Slot {
     static constexpr int HALVES = DK <= 64 ? 1 : DK / 64;  // 64-wide tiles a row spans (dk = 32: half of one)
-    static constexpr int KQ = HALVES * 16384, M = DK * 128, PARTS = F32 ? 2 : 1;
-    static constexpr int V = 2 * M + PARTS * 8192 + (int)sizeof(Factors);
+    static constexpr int KQ = HALVES * 16384, M = DK * 128;
+    static constexpr int V = 2 * M + 2 * 8192 + (int)sizeof(Factors);
     static_assert(V % 128 == 0, "slots on the bulk copies' and the operand tiles' boundaries");
 };
 // A slot is a tile of find_tile: at most T / 64 + N.
@@ -173,21 +176,27 @@ struct RowMaps {
 };
 
 constexpr int PREP = 256;
-template <bool F32> constexpr int prep_ctas() { return F32 ? 2 : 3; }  // of an SM, by their shared memory
+constexpr int PREP_CTAS = 3;  // of an SM, by their shared memory
 
-template <int DK, bool F32, int HEADS> struct PrepSmem {
-    using L = Slot<DK, F32>;
-    static constexpr int PARTS = L::PARTS;
+template <int DK, int HEADS> struct PrepSmem {
+    using L = Slot<DK>;
     unsigned char kq[L::KQ];  // bf16 rows of k, then q; fp16 later; P T over q's
     union {
         struct {  // 64 x 64 fp16 tiles
             unsigned char t_hi[8192], t_lo[8192];  // T; then with the rows' factors of M
-            unsigned char p_hi[8192], p_lo[F32 ? 8192 : 128];
-            alignas(16) float xd[C * XS];          // A's diagonal blocks, 16 x 16 each
+            unsigned char p_hi[8192], p_lo[8192];
         };
         unsigned char m[2][L::M];  // then M^T
     };
-    unsigned char pt_lo[F32 ? 8192 : 128];
+    alignas(16) float xd[C * 16];  // A's diagonal blocks, 16 x 16 each
+    // P T: high parts over q's first 64 values, low ones over its last where it has 128, else where P's were
+    __device__ __forceinline__ unsigned char* pt_hi() { return kq + 8192; }
+    __device__ __forceinline__ unsigned char* pt_lo()
+    {
+        static_assert(DK == 128 || 2 * L::M <= 16384, "M^T over P's low parts");
+        if constexpr (DK == 128) return kq + 16384 + 8192;
+        else return p_lo;
+    }
     Factors fac[HEADS];
     struct Gates {
         alignas(16) float eg[C], gh[C], gl[C], w[C];  // e^G, G / ln 2 in two words, e^{G_C - G}
@@ -342,12 +351,12 @@ template <int SIZE> struct Merge {
 // by head.  Bound: latency (a dozen dependent phases of a few hundred
 // instructions each); several teams an SM fill each other's gaps.  Task `turn` of
 // its team.
-template <int DK, bool F32, int HEADS>
-__device__ __forceinline__ void prep_task(PrepSmem<DK, F32, HEADS>& sm, const GdnArgs& a, const RowMaps& maps, const Work& ws,
+template <int DK, int HEADS>
+__device__ __forceinline__ void prep_task(PrepSmem<DK, HEADS>& sm, const GdnArgs& a, const RowMaps& maps, const Work& ws,
                                           int slot, int r0, int n, int h0, int turn, int team, uint32_t tmem, Waiter& wait, int t)
 {
-    using S = PrepSmem<DK, F32, HEADS>;
-    using L = Slot<DK, F32>;
+    using S = PrepSmem<DK, HEADS>;
+    using L = Slot<DK>;
     const int w = t >> 5, lane = t & 31, rep = a.Hv / a.Hk, hk = h0 / rep;
     if (t == 0) {
         ptx::mbar_arrive_expect_tx(&sm.loaded, L::KQ);
@@ -434,7 +443,7 @@ __device__ __forceinline__ void prep_task(PrepSmem<DK, F32, HEADS>& sm, const Gd
             for (int i = 0; i < 4; ++i) split_h(c[2 * q + (i >> 1)][2 * (i & 1)], c[2 * q + (i >> 1)][2 * (i & 1) + 1], hi[i], lo[i]);
             const uint32_t o = tile_at(row0 + arow, q * 2 + acol);
             stsm(ptx::smem_u32(hi_tile) + o, hi);
-            if (lo_tile) stsm(ptx::smem_u32(lo_tile) + o, lo);
+            stsm(ptx::smem_u32(lo_tile) + o, lo);
         }
     };
 
@@ -495,11 +504,10 @@ __device__ __forceinline__ void prep_task(PrepSmem<DK, F32, HEADS>& sm, const Gd
                 for (int i = 0; i < 4; ++i) split_h(v[2 * i], v[2 * i + 1], hi[i], lo[i]);
                 const int c = (s0 >> 3) + p;
                 *reinterpret_cast<uint4*>(hi_tile + tile_at(r, c)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                if (F32 || type == 0) *reinterpret_cast<uint4*>(lo_tile + tile_at(r, c)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                *reinterpret_cast<uint4*>(lo_tile + tile_at(r, c)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 if (type == 0 && (r >> 4) == (c >> 1)) {
-                    float* x = &sm.xd[r * XS + (c & 1) * 8];
-                    *reinterpret_cast<float4*>(x) = make_float4(v[0], v[1], v[2], v[3]);
-                    *reinterpret_cast<float4*>(x + 4) = make_float4(v[4], v[5], v[6], v[7]);
+                    *reinterpret_cast<float4*>(&sm.xd[diag_at(r, (c & 1) * 2)]) = make_float4(v[0], v[1], v[2], v[3]);
+                    *reinterpret_cast<float4*>(&sm.xd[diag_at(r, (c & 1) * 2 + 1)]) = make_float4(v[4], v[5], v[6], v[7]);
                 }
             }
         }
@@ -524,7 +532,7 @@ __device__ __forceinline__ void prep_task(PrepSmem<DK, F32, HEADS>& sm, const Gd
                     float acc = i == c ? 1.f : 0.f, acc2 = 0.f;
 #pragma unroll
                     for (int k = 0; k < i; k += 4) {
-                        const float4 f = *reinterpret_cast<const float4*>(&sm.xd[(d0 + i) * XS + k]);
+                        const float4 f = *reinterpret_cast<const float4*>(&sm.xd[diag_at(d0 + i, k >> 2)]);
                         acc = fmaf(-f.x, x[k], acc);
                         if (k + 1 < i) acc2 = fmaf(-f.y, x[k + 1], acc2);
                         if (k + 2 < i) acc = fmaf(-f.z, x[k + 2], acc);
@@ -579,19 +587,17 @@ __device__ __forceinline__ void prep_task(PrepSmem<DK, F32, HEADS>& sm, const Gd
                 if (kt > mt) break;  // P's columns up to its rows
                 uint32_t x[4], y[4], f[4], e[4];
                 ldsm(x, pb[0] + tile_at(mt * 16 + arow, kt * 2 + acol));
-                if (F32) ldsm(y, pb[1] + tile_at(mt * 16 + arow, kt * 2 + acol));
+                ldsm(y, pb[1] + tile_at(mt * 16 + arow, kt * 2 + acol));
 #pragma unroll
                 for (int q = 0; q <= kt; ++q) {
                     ldsm_t(f, tb[0] + tile_at(kt * 16 + arow, q * 2 + acol));
                     mma(c[2 * q], x, f[0], f[1]);
                     mma(c[2 * q + 1], x, f[2], f[3]);
-                    if (F32) {
-                        ldsm_t(e, tb[1] + tile_at(kt * 16 + arow, q * 2 + acol));
-                        mma(c[2 * q], y, f[0], f[1]);
-                        mma(c[2 * q + 1], y, f[2], f[3]);
-                        mma(c[2 * q], x, e[0], e[1]);
-                        mma(c[2 * q + 1], x, e[2], e[3]);
-                    }
+                    ldsm_t(e, tb[1] + tile_at(kt * 16 + arow, q * 2 + acol));
+                    mma(c[2 * q], y, f[0], f[1]);
+                    mma(c[2 * q + 1], y, f[2], f[3]);
+                    mma(c[2 * q], x, e[0], e[1]);
+                    mma(c[2 * q + 1], x, e[2], e[3]);
                 }
             }
         } else if (t == 0) ptx::bulk_wait_read_all();  // [K; Q] is on its way: room for P T over q's rows
@@ -602,7 +608,7 @@ __device__ __forceinline__ void prep_task(PrepSmem<DK, F32, HEADS>& sm, const Gd
                 const float2 v = *reinterpret_cast<const float2*>(&sm.inv[i * 8 + (lane & 3) * 2]);
                 c[i][0] *= v.x; c[i][1] *= v.y; c[i][2] *= v.x; c[i][3] *= v.y;
             }
-            store_tile(sm.kq + 8192, F32 ? sm.pt_lo : nullptr, (w - 4) * 16, c);
+            store_tile(sm.pt_hi(), sm.pt_lo(), (w - 4) * 16, c);
         }
         // T with M's row factors e^{G_C - G}, in pieces of eight values up to each diagonal block's end: 32 + 64 + 96 + 128
 #pragma unroll 1
@@ -651,15 +657,15 @@ __device__ __forceinline__ void prep_task(PrepSmem<DK, F32, HEADS>& sm, const Gd
         if (t == 0) {
             unsigned char* d = ws.v + ((long long)slot * a.Hv + h0 + j) * L::V;
             ptx::bulk_s2g(d, sm.m, 2 * L::M);
-            ptx::bulk_s2g(d + 2 * L::M, sm.kq + 8192, 8192);
-            if (F32) ptx::bulk_s2g(d + 2 * L::M + 8192, sm.pt_lo, 8192);
-            ptx::bulk_s2g(d + 2 * L::M + L::PARTS * 8192, &fac, sizeof(Factors));
+            ptx::bulk_s2g(d + 2 * L::M, sm.pt_hi(), 8192);
+            ptx::bulk_s2g(d + 2 * L::M + 8192, sm.pt_lo(), 8192);
+            ptx::bulk_s2g(d + 2 * L::M + 2 * 8192, &fac, sizeof(Factors));
             ptx::bulk_commit();
         }
     }
 }
 
-template <int DK, bool F32, int HEADS> __device__ __forceinline__ void prep_setup(PrepSmem<DK, F32, HEADS>& sm, int t)
+template <int DK, int HEADS> __device__ __forceinline__ void prep_setup(PrepSmem<DK, HEADS>& sm, int t)
 {
     if (t == 0) {
         ptx::mbar_init(&sm.loaded, 1);
@@ -669,14 +675,14 @@ template <int DK, bool F32, int HEADS> __device__ __forceinline__ void prep_setu
 }
 
 // A task a CTA.
-template <int DK, bool F32, int HEADS>
-__global__ void __launch_bounds__(PREP, prep_ctas<F32>())
+template <int DK, int HEADS>
+__global__ void __launch_bounds__(PREP, PREP_CTAS)
 gdn_prep_kernel(const GdnArgs a, const __grid_constant__ RowMaps maps, const Work ws)
 {
     ptx::grid_launch_dependents();
     ptx::grid_dependency_wait();
     extern __shared__ __align__(1024) unsigned char dyn[];
-    using S = PrepSmem<DK, F32, HEADS>;
+    using S = PrepSmem<DK, HEADS>;
     S& sm = *reinterpret_cast<S*>(dyn);
     const int t = threadIdx.x, lane = t & 31, groups = a.Hv / HEADS, slot = blockIdx.x / groups;
     // every warp for itself: the rows of this slot
@@ -690,7 +696,7 @@ gdn_prep_kernel(const GdnArgs a, const __grid_constant__ RowMaps maps, const Wor
     __syncthreads();
     ptx::tc_fence_after();
     Waiter wait{false};
-    prep_task<DK, F32, HEADS>(sm, a, maps, ws, slot, r0, n, blockIdx.x % groups * HEADS, 0, 0, sm.tmem, wait, t);
+    prep_task<DK, HEADS>(sm, a, maps, ws, slot, r0, n, blockIdx.x % groups * HEADS, 0, 0, sm.tmem, wait, t);
     if (wait.dead) flag_status(a.dev_status, KDA_DEV_TIMEOUT);
     if (t == 0) ptx::bulk_wait_read_all();
     if (t / 32 == 1) ptx::tmem_dealloc(sm.tmem, 128);
@@ -709,10 +715,10 @@ struct Unit {
     int seq, begin, end, slot, h;
 };
 
-template <int DK, int DV, bool F32> struct ChainSmem {
-    using L = Slot<DK, F32>;
+template <int DK, int DV> struct ChainSmem {
+    using L = Slot<DK>;
     unsigned char kq[2][L::KQ];
-    unsigned char work[2][2 * L::M + L::PARTS * 8192];  // M^T, P T
+    unsigned char work[2][2 * L::M + 2 * 8192];       // M^T, P T
     unsigned char v[2][C * DV * 2];                     // dense rows
     Factors fac[4];
     float f1[2][DV], f2[2][DV];  // the scales of S's and R's columns
@@ -807,12 +813,12 @@ struct OneUnit {
 // The chains of one unit after the other.  The barriers' phases, the buffers
 // and TMEM go on from unit to unit: only `q`, the chunk's number among all of the
 // CTA's, counts for them.  tmem: all of it; freed here.
-template <int DK, int DV, bool F32, class Units>
+template <int DK, int DV, bool OUT32, class Units>
 __device__ __forceinline__ void run_chains(unsigned char* dyn, const GdnArgs& a, const CUtensorMap& vmap, const Work& ws, uint32_t tmem, Units units)
 {
     constexpr int NW = DV / 32;
-    using S = ChainSmem<DK, DV, F32>;
-    using L = Slot<DK, F32>;
+    using S = ChainSmem<DK, DV>;
+    using L = Slot<DK>;
     S& sm = *reinterpret_cast<S*>(dyn);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -1065,10 +1071,9 @@ __device__ __forceinline__ void run_chains(unsigned char* dyn, const GdnArgs& a,
 #pragma unroll
                     for (int kt = 0; kt < DK / 16; ++kt)
                         ptx::mma_ts_if(leader, tmem + TM_QS, tmem + TM_SH + kt * 8, qd + kq_step(kt), id, kt > 0);
-                    if (F32)
 #pragma unroll
-                        for (int kt = 0; kt < DK / 16; ++kt)
-                            ptx::mma_ts_if(leader, tmem + TM_QS, tmem + TM_SL + kt * 8, qd + kq_step(kt), id, 1);
+                    for (int kt = 0; kt < DK / 16; ++kt)
+                        ptx::mma_ts_if(leader, tmem + TM_QS, tmem + TM_SL + kt * 8, qd + kq_step(kt), id, 1);
                     ptx::mma_commit_if(leader, &sm.qs_full);
                     __syncwarp();
                     wait(sm.su_full, q);
@@ -1077,12 +1082,11 @@ __device__ __forceinline__ void run_chains(unsigned char* dyn, const GdnArgs& a,
 #pragma unroll
                     for (int kt = 0; kt < 4; ++kt)
                         ptx::mma_ts_if(leader, tmem + TM_PR, tmem + TM_RH + kt * 8, pt + kt * 2, id, kt > 0);
-                    if (F32)
 #pragma unroll
-                        for (int kt = 0; kt < 4; ++kt) {
-                            ptx::mma_ts_if(leader, tmem + TM_PR, tmem + TM_RL + kt * 8, pt + kt * 2, id, 1);
-                            ptx::mma_ts_if(leader, tmem + TM_PR, tmem + TM_RH + kt * 8, pt + (8192 >> 4) + kt * 2, id, 1);
-                        }
+                    for (int kt = 0; kt < 4; ++kt) {
+                        ptx::mma_ts_if(leader, tmem + TM_PR, tmem + TM_RL + kt * 8, pt + kt * 2, id, 1);
+                        ptx::mma_ts_if(leader, tmem + TM_PR, tmem + TM_RH + kt * 8, pt + (8192 >> 4) + kt * 2, id, 1);
+                    }
                     ptx::mma_commit_if(leader, &sm.freed[b]);
                     ptx::mma_commit_if(leader, &sm.o_full);
                     __syncwarp();
@@ -1126,7 +1130,7 @@ __device__ __forceinline__ void run_chains(unsigned char* dyn, const GdnArgs& a,
                             x[i] = o.x;
                             x[i + 1] = o.y;
                         }
-                        if constexpr (F32) {
+                        if constexpr (OUT32) {
                             float* p = static_cast<float*>(a.out) + o0 + c + i0 * row_stride;
 #pragma unroll
                             for (int i = 0; i < 16; ++i)
@@ -1158,7 +1162,7 @@ __device__ __forceinline__ void run_chains(unsigned char* dyn, const GdnArgs& a,
     }
 }
 
-template <int DK, int DV, bool F32>
+template <int DK, int DV, bool OUT32>
 __global__ void __launch_bounds__(CHAIN_THREADS, 1) gdn_chain_kernel(const GdnArgs a, const __grid_constant__ CUtensorMap vmap, const Work ws)
 {
     ptx::grid_launch_dependents();
@@ -1167,14 +1171,14 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) gdn_chain_kernel(const GdnAr
     OneUnit one;
     Unit& u = one.u;
     u.h = blockIdx.x % a.Hv;
-    u.seq = ranked_seq(a.cu_seqlens, a.N, blockIdx.x / a.Hv, &reinterpret_cast<ChainSmem<DK, DV, F32>*>(dyn)->found);
+    u.seq = ranked_seq(a.cu_seqlens, a.N, blockIdx.x / a.Hv, &reinterpret_cast<ChainSmem<DK, DV>*>(dyn)->found);
     if (!gdn_unit(a, u.seq, u.begin, u.end, u.slot)) return;
     __shared__ uint32_t tmem;
     if (threadIdx.x / 32 == 8) ptx::tmem_alloc(&tmem, TM_COLS);
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
-    run_chains<DK, DV, F32>(dyn, a, vmap, ws, tmem, one);
+    run_chains<DK, DV, OUT32>(dyn, a, vmap, ws, tmem, one);
 }
 
 // ------------------------------------------------------------ chains beside prep
@@ -1189,7 +1193,7 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) gdn_chain_kernel(const GdnAr
 // Those have to start before prep ends; were it fewer, one of them would end last
 // alone, were it more, prep would be slower for nothing.  At most half of the CTAs.
 constexpr int MERGED = 64;                    // sequences, two a lane
-constexpr int TEAMS = 3, BESIDE = TEAMS * PREP;  // threads
+constexpr int BESIDE = PREP_CTAS * PREP;  // threads: as many teams of prep as CTAs of it fit on an SM
 static_assert(BESIDE >= CHAIN_THREADS, "roles");
 
 struct Plan {
@@ -1326,7 +1330,7 @@ struct TakenUnits {
     }
 };
 
-template <int DK, int DV, bool F32, int HEADS>
+template <int DK, int DV, bool OUT32, int HEADS>
 __global__ void __launch_bounds__(BESIDE, 1)
 gdn_beside_kernel(const GdnArgs a, const __grid_constant__ RowMaps maps, const Work ws)
 {
@@ -1341,43 +1345,41 @@ gdn_beside_kernel(const GdnArgs a, const __grid_constant__ RowMaps maps, const W
     ptx::tc_fence_after();
     const uint32_t tmem = tmem_at;
     if ((int)blockIdx.x >= plan.chains) {
-        using S = PrepSmem<DK, F32, HEADS>;
-        constexpr int STRIDE = (sizeof(S) + 1023) / 1024 * 1024, TEAMS_HERE = prep_ctas<F32>();
+        using S = PrepSmem<DK, HEADS>;
+        constexpr int STRIDE = (sizeof(S) + 1023) / 1024 * 1024;
         const int team = threadIdx.x / PREP, t = threadIdx.x % PREP;
-        if (team < TEAMS_HERE) {
-            S& sm = *reinterpret_cast<S*>(dyn + team * STRIDE);
-            prep_setup(sm, t);
-            team_sync(team);
-            Waiter wait{false};
-            const Order order(plan, a);
-            const int groups = a.Hv / HEADS, teams = (gridDim.x - plan.chains) * TEAMS_HERE;
-            int turn = 0;
-            for (long long i = (blockIdx.x - plan.chains) * TEAMS_HERE + team;; i += teams, ++turn) {
-                int slot, r0, n;
-                if (!order.task((int)(i / groups), slot, r0, n)) break;
-                const int h0 = (int)(i % groups) * HEADS;
-                prep_task<DK, F32, HEADS>(sm, a, maps, ws, slot, r0, n, h0, turn, team, tmem + team * 128, wait, t);
-                if (t == 0) {
-                    ptx::bulk_wait_all();
-                    ptx::fence_proxy_async_global();
-                    __threadfence();
-#pragma unroll
-                    for (int j = 0; j < HEADS; ++j) ptx::st_release_gpu(ws.ready + (long long)slot * a.Hv + h0 + j, 1);
-                }
-                team_sync(team);
-            }
-            if (wait.dead) flag_status(a.dev_status, KDA_DEV_TIMEOUT);
+        S& sm = *reinterpret_cast<S*>(dyn + team * STRIDE);
+        prep_setup(sm, t);
+        team_sync(team);
+        Waiter wait{false};
+        const Order order(plan, a);
+        const int groups = a.Hv / HEADS, teams = (gridDim.x - plan.chains) * PREP_CTAS;
+        int turn = 0;
+        for (long long i = (blockIdx.x - plan.chains) * PREP_CTAS + team;; i += teams, ++turn) {
+            int slot, r0, n;
+            if (!order.task((int)(i / groups), slot, r0, n)) break;
+            const int h0 = (int)(i % groups) * HEADS;
+            prep_task<DK, HEADS>(sm, a, maps, ws, slot, r0, n, h0, turn, team, tmem + team * 128, wait, t);
             if (t == 0) {
-                ptx::mbar_inval(&sm.loaded);
-                ptx::mbar_inval(&sm.prod);
+                ptx::bulk_wait_all();
+                ptx::fence_proxy_async_global();
+                __threadfence();
+#pragma unroll
+                for (int j = 0; j < HEADS; ++j) ptx::st_release_gpu(ws.ready + (long long)slot * a.Hv + h0 + j, 1);
             }
-            ptx::fence_proxy_async_smem();  // the chains' copies come into the same memory
-            ptx::tc_fence_before();
+            team_sync(team);
         }
+        if (wait.dead) flag_status(a.dev_status, KDA_DEV_TIMEOUT);
+        if (t == 0) {
+            ptx::mbar_inval(&sm.loaded);
+            ptx::mbar_inval(&sm.prod);
+        }
+        ptx::fence_proxy_async_smem();  // the chains' copies come into the same memory
+        ptx::tc_fence_before();
         __syncthreads();
         ptx::tc_fence_after();
     }
-    if (threadIdx.x < CHAIN_THREADS) run_chains<DK, DV, F32>(dyn, a, maps.v, ws, tmem, TakenUnits{&plan});
+    if (threadIdx.x < CHAIN_THREADS) run_chains<DK, DV, OUT32>(dyn, a, maps.v, ws, tmem, TakenUnits{&plan});
     else set_regs<false, 24>();
 }
 
@@ -1397,10 +1399,10 @@ bool encode_rows(CUtensorMap* m, const void* base, long long width, long long st
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int DK, int DV, bool F32>
+template <int DK, int DV, bool OUT32>
 cudaError_t launch_chain(const GdnArgs& a, const CUtensorMap& vmap, const Work& ws, cudaStream_t st)
 {
-    using S = ChainSmem<DK, DV, F32>;
+    using S = ChainSmem<DK, DV>;
     constexpr int smem = sizeof(S);
     // operand tiles on the swizzle's 1024-byte period, barriers on 8
     static_assert(offsetof(S, work) % 1024 == 0 && offsetof(S, v) % 128 == 0 && offsetof(S, fac) % 16 == 0 && offsetof(S, loaded) % 8 == 0,
@@ -1408,38 +1410,38 @@ cudaError_t launch_chain(const GdnArgs& a, const CUtensorMap& vmap, const Work& 
     static_assert(smem <= 227 * 1024, "shared memory");
     static PerDeviceOnce once;
     cudaError_t e = once.run([](int) {
-        return cudaFuncSetAttribute(gdn_chain_kernel<DK, DV, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        return cudaFuncSetAttribute(gdn_chain_kernel<DK, DV, OUT32>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     });
     if (e != cudaSuccess) return e;
-    return launch_dependent(gdn_chain_kernel<DK, DV, F32>, a.N * a.Hv, CHAIN_THREADS, smem, st, a, vmap, ws);
+    return launch_dependent(gdn_chain_kernel<DK, DV, OUT32>, a.N * a.Hv, CHAIN_THREADS, smem, st, a, vmap, ws);
 }
 
-template <int DK, bool F32, int HEADS>
+template <int DK, int HEADS>
 cudaError_t launch_prep(const GdnArgs& a, const RowMaps& maps, const Work& ws, long long slots, cudaStream_t st)
 {
-    using S = PrepSmem<DK, F32, HEADS>;
+    using S = PrepSmem<DK, HEADS>;
     constexpr int smem = sizeof(S);
     static_assert(offsetof(S, t_hi) % 128 == 0 && offsetof(S, fac) % 16 == 0 && offsetof(S, m) % 16 == 0 &&
                   offsetof(S, xd) % 16 == 0 && offsetof(S, gates) % 16 == 0 &&
                   offsetof(S, down) % 16 == 0 && offsetof(S, loaded) % 8 == 0, "alignment");
-    static_assert((smem + 1024) * prep_ctas<F32>() <= 228 * 1024, "shared memory");
+    static_assert((smem + 1024) * PREP_CTAS <= 228 * 1024, "shared memory");
     static PerDeviceOnce once;
     const cudaError_t e = once.run([](int) {
-        return cudaFuncSetAttribute(gdn_prep_kernel<DK, F32, HEADS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        return cudaFuncSetAttribute(gdn_prep_kernel<DK, HEADS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     });
     if (e != cudaSuccess) return e;
-    return launch_dependent(gdn_prep_kernel<DK, F32, HEADS>, (unsigned)(slots * (a.Hv / HEADS)), PREP, smem, st, a, maps, ws);
+    return launch_dependent(gdn_prep_kernel<DK, HEADS>, (unsigned)(slots * (a.Hv / HEADS)), PREP, smem, st, a, maps, ws);
 }
 
-template <int DK, int DV, bool F32, int HEADS>
+template <int DK, int DV, bool OUT32, int HEADS>
 cudaError_t launch_beside(const GdnArgs& a, const RowMaps& maps, const Work& ws, long long slots, cudaStream_t st)
 {
-    constexpr int prep = prep_ctas<F32>() * (int)((sizeof(PrepSmem<DK, F32, HEADS>) + 1023) / 1024 * 1024);
-    constexpr int chain = (int)sizeof(ChainSmem<DK, DV, F32>), smem = prep > chain ? prep : chain;
+    constexpr int prep = PREP_CTAS * (int)((sizeof(PrepSmem<DK, HEADS>) + 1023) / 1024 * 1024);
+    constexpr int chain = (int)sizeof(ChainSmem<DK, DV>), smem = prep > chain ? prep : chain;
     static_assert(smem + sizeof(Plan) + 1024 <= 227 * 1024, "shared memory");
     static PerDeviceOnce once;
     cudaError_t e = once.run([](int) {
-        return cudaFuncSetAttribute(gdn_beside_kernel<DK, DV, F32, HEADS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        return cudaFuncSetAttribute(gdn_beside_kernel<DK, DV, OUT32, HEADS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     });
     if (e != cudaSuccess) return e;
     if ((e = cudaMemsetAsync(ws.ready, 0, (slots * a.Hv + 1) * sizeof(int), st)) != cudaSuccess) return e;
@@ -1453,28 +1455,28 @@ cudaError_t launch_beside(const GdnArgs& a, const RowMaps& maps, const Work& ws,
     attr.val.cooperative = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, gdn_beside_kernel<DK, DV, F32, HEADS>, a, maps, ws);
+    return cudaLaunchKernelEx(&cfg, gdn_beside_kernel<DK, DV, OUT32, HEADS>, a, maps, ws);
 }
 
-template <int DK, int DV, bool F32>
+template <int DK, int DV, bool OUT32>
 cudaError_t launch_dv(const GdnArgs& a, const RowMaps& maps, const Work& ws, long long slots, cudaStream_t st)
 {
     // Two heads a team (their rows, products and norms once): 32768 rows as eight prompts take
     // 699 us, 785 with one; one prompt 1317 and 1310.
-    const bool pairs = a.Hv / a.Hk % 2 == 0, waves = slots * a.Hv > prep_ctas<F32>() * sm_count();
+    const bool pairs = a.Hv / a.Hk % 2 == 0, waves = slots * a.Hv > PREP_CTAS * sm_count();
     // Chains beside prep where prep is more than one wave of CTAs: 32768 rows of 32 heads take
     // 699 us as eight prompts of mixed lengths (840 one after the other), 1317 as one (1625),
     // 675 as sixteen (632); 7001 rows of 12 heads 115 (137); but 333 rows of 8 heads 41 us, 24 one after the other.
     if (a.N <= MERGED && waves)
-        return pairs ? launch_beside<DK, DV, F32, 2>(a, maps, ws, slots, st) : launch_beside<DK, DV, F32, 1>(a, maps, ws, slots, st);
+        return pairs ? launch_beside<DK, DV, OUT32, 2>(a, maps, ws, slots, st) : launch_beside<DK, DV, OUT32, 1>(a, maps, ws, slots, st);
     // (in one wave all single heads run at once)
-    const cudaError_t e = pairs && waves ? launch_prep<DK, F32, 2>(a, maps, ws, slots, st) : launch_prep<DK, F32, 1>(a, maps, ws, slots, st);
-    return e != cudaSuccess ? e : launch_chain<DK, DV, F32>(a, maps.v, ws, st);
+    const cudaError_t e = pairs && waves ? launch_prep<DK, 2>(a, maps, ws, slots, st) : launch_prep<DK, 1>(a, maps, ws, slots, st);
+    return e != cudaSuccess ? e : launch_chain<DK, DV, OUT32>(a, maps.v, ws, st);
 }
 
-template <int DK, bool F32> cudaError_t launch(const GdnArgs& a, int dv, cudaStream_t st)
+template <int DK, bool OUT32> cudaError_t launch(const GdnArgs& a, int dv, cudaStream_t st)
 {
-    using L = Slot<DK, F32>;
+    using L = Slot<DK>;
     RowMaps maps;
     if (!encode_rows(&maps.q, a.q, (long long)a.Hk * DK, a.qs, a.T, 64, true) ||
         !encode_rows(&maps.k, a.k, (long long)a.Hk * DK, a.ks, a.T, 64, true) ||
@@ -1486,9 +1488,9 @@ template <int DK, bool F32> cudaError_t launch(const GdnArgs& a, int dv, cudaStr
     ws.v = ws.kq + slots * a.Hk * L::KQ;
     ws.ready = reinterpret_cast<int*>(ws.v + slots * a.Hv * L::V);
     ws.taken = ws.ready + slots * a.Hv;
-    if (dv == 128) return launch_dv<DK, 128, F32>(a, maps, ws, slots, st);
-    if (dv == 64) return launch_dv<DK, 64, F32>(a, maps, ws, slots, st);
-    return launch_dv<DK, 32, F32>(a, maps, ws, slots, st);
+    if (dv == 128) return launch_dv<DK, 128, OUT32>(a, maps, ws, slots, st);
+    if (dv == 64) return launch_dv<DK, 64, OUT32>(a, maps, ws, slots, st);
+    return launch_dv<DK, 32, OUT32>(a, maps, ws, slots, st);
 }
 
 }  // namespace
