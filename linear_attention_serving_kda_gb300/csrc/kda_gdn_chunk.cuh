@@ -913,16 +913,17 @@ __device__ __forceinline__ void run_chains(unsigned char* dyn, const GdnArgs& a,
                     for (int i = 0; i < RK; i += 2) mx = max3(mx, fabsf(r[i]), fabsf(r[i + 1]));
                     sm.top[0][half][c] = mx;
                     // |k'| < 2, so |k'.S| <= 2 sqrt(dk) max |S|: R stays below 2^14 in the scale of this
-                    // bound, and low parts do not mind how far below
+                    // bound, and low parts do not mind how far below; 2^-60 of S at least, so that ig rd is finite
                     float rd, ru;
-                    pow2_scale(both(0, mx) + fac.ektop * (DK == 128 ? 23.f : DK == 64 ? 16.f : 12.f) * (most * ig), rd, ru);
+                    pow2_scale(fmaxf(both(0, mx) + fac.ektop * (DK == 128 ? 23.f : DK == 64 ? 16.f : 12.f) * (most * ig),
+                                     0x1p-60f * (most * ig)), rd, ru);
                     rd *= 0x1p13f;
                     ru *= 0x1p-13f;
                     scale_all(r, rd);
                     if (q > 0) wait(sm.o_full, q - 1);  // R's place is free
                     wait(sm.ks_full, q);
                     ptx::tc_fence_after();
-                    const float fr = ig * rd;
+                    const float fr = most == 0.f ? 0.f : ig * rd;  // an S of zeros may have any ig
 #pragma unroll
                     for (int z = 0; z < RK; z += 16) {
                         float d[16], e[16];

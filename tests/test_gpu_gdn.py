@@ -585,3 +585,22 @@ def test_prefill_keys_of_all_magnitudes(cuda_lib, Hv, dk):
     c.b.copy_((-2 * math.log(2.0)) * e.clamp(min=0) + c.b.float().clamp(max=0))
     c.prefill(cuda_lib)
     c.check()
+
+
+@pytest.mark.parametrize("lens,Hv,dk", [([64], 1, 128), ([200, 70], 2, 64), ([100, 3], 4, 32)])
+@pytest.mark.parametrize("kind", ["zeros", "zeros after a reset", "one small row"])
+@pytest.mark.parametrize("l2", [False, True])
+def test_prefill_rows_of_zeros_on_a_large_state(cuda_lib, lens, Hv, dk, kind, l2):
+    """Rows that give next to nothing (2^-120 of the keys, no values) on states near 2^58: what the rows' scale
+    and the state's make together has to stay finite."""
+    c = Case(lens, Hk=1, Hv=Hv, dk=dk, dv=32, seed=99, out="f32", l2=l2, gate=-30.0)
+    c.state0 *= 2.0 ** 59
+    c.rows.zero_()
+    if kind == "zeros after a reset":
+        c.a[65:66] = 1e30  # the state is all zeros from there on, its last scale still there
+    if kind == "one small row":
+        c.v[1:2] = 2.0 ** -60
+        c.k[1:2, 3] = 1.0
+    c.reset()
+    c.prefill(cuda_lib)
+    c.check()
