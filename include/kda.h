@@ -323,7 +323,7 @@ KDA_API int kda_commit_verify(const kda_params* p, int32_t B, int32_t W, const i
  *     S = alpha S + k u^T,  u = beta (v - alpha S^T k),  o = scale S^T q
  * (rows arrive after their convolution).  The state is fp32 [dk][dv].
  * ------------------------------------------------------------------------ */
-#define KDA_MAX_ROWS 2147483000  /* rows of one call of the rule or the convolution */
+#define KDA_MAX_ROWS 2147483000  /* rows of one call of the rule or the convolution; the latter's N + T / 16 too */
 typedef struct kda_gdn_params {
     int32_t num_heads_k;   /* Hk >= 1                                           */
     int32_t num_heads_v;   /* Hv, a multiple of Hk, <= 1024                     */

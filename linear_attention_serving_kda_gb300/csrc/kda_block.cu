@@ -501,7 +501,8 @@ KDA_API int kda_conv_varlen(const kda_conv_params* p, const int32_t* cu_seqlens,
 {
     int rc = check_conv(p);
     if (rc != KDA_OK) return rc;
-    if (N < 0 || T < 0 || T > KDA_MAX_ROWS || (int64_t)N + T / 16 > INT32_MAX) return KDA_ERR_INVALID_ARGUMENT;
+    // tiles are counted by index, and the search for one looks up to 31 sequences past the last
+    if (N < 0 || T < 0 || T > KDA_MAX_ROWS || (int64_t)N + T / 16 > KDA_MAX_ROWS) return KDA_ERR_INVALID_ARGUMENT;
     if (N == 0 || T == 0) return KDA_OK;
     if ((rc = check_ptrs({cu_seqlens})) != KDA_OK) return rc;
     return conv_call(p, cu_seqlens, N, T, x, slots, conv_state, y, dev_status, true, stream);

@@ -182,3 +182,13 @@ def test_row_counts_past_the_index_range():
     far = 1 << 50
     assert kda.kda_conv_varlen(conv, addr(1), 1, rows, far, None, addr(3), 2 * far, None, 0) == INVALID
     assert kda.kda_conv_decode(conv, rows, far, None, addr(3), 2 * far, None, 0) == INVALID
+
+
+def test_sequence_counts_past_the_index_range():
+    """The search for a row tile counts in blocks of 32 sequences: counts within 31 of the index range's end wrapped."""
+    conv = kda.ConvParams(channels=8, conv_kernel=2, conv_weight=addr(9), num_slots=3)
+    far = 1 << 50
+    for N in ((1 << 31) - 1, (1 << 31) - 31, kda.KDA_MAX_ROWS + 1):
+        assert kda.kda_conv_varlen(conv, far, N, 8, addr(2), None, addr(3), addr(4), None, 0) == INVALID
+        assert _prefill(_gdn(num_heads_k=1, num_heads_v=1), N=N, T=8, cu=far) == INVALID
+    assert kda.kda_conv_varlen(conv, far, kda.KDA_MAX_ROWS, 16, addr(2), None, addr(3), addr(4), None, 0) == INVALID
