@@ -371,7 +371,8 @@ typedef struct kda_gdn_params {
  *     128, whatever the out_dtype.  Contents need no init.  Calls that may run at the same time take a
  *     workspace each.
  *   - Long calls run as one cooperative grid of a CTA an SM; a call on a device
- *     of which other work holds SMs waits for them.
+ *     of which other work holds SMs waits for them.  On a stream of a green
+ *     context with a part of the SMs they run as two kernels, with the same bits.
  */
 KDA_API int kda_gdn_prefill_varlen(const kda_gdn_params* p, const int32_t* cu_seqlens, int32_t N, int32_t T,
                                    const void* q, const void* k, const void* v, const void* gate, const void* beta,

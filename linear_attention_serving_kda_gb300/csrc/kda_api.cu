@@ -7,6 +7,10 @@
 // GenAI PR #2843, author's review reply).
 #include <cmath>
 #include <cstring>
+#include <mutex>
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
 
 #include "kda_check.h"
 #include "kda_common.cuh"
@@ -94,6 +98,27 @@ int kda::sm_count()
     if (n == 0 && cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess)
         count[dev].store(n, std::memory_order_relaxed);
     return n;
+}
+
+int kda::stream_sm_count(cudaStream_t stream)
+{
+    static PFN_cuStreamGetGreenCtx_v12040 green_of = nullptr;
+    static PFN_cuGreenCtxGetDevResource_v12040 resource_of = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        auto find = [](const char* name) {
+            void* ptr = nullptr;
+            cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+            return cudaGetDriverEntryPointByVersion(name, &ptr, 12040, cudaEnableDefault, &q) == cudaSuccess &&
+                   q == cudaDriverEntryPointSuccess ? ptr : nullptr;
+        };
+        green_of = reinterpret_cast<PFN_cuStreamGetGreenCtx_v12040>(find("cuStreamGetGreenCtx"));
+        resource_of = reinterpret_cast<PFN_cuGreenCtxGetDevResource_v12040>(find("cuGreenCtxGetDevResource"));
+    });
+    CUgreenCtx g = nullptr;
+    if (!green_of || !resource_of || green_of(stream, &g) != CUDA_SUCCESS || !g) return sm_count();
+    CUdevResource r;
+    return resource_of(g, &r, CU_DEV_RESOURCE_TYPE_SM) == CUDA_SUCCESS ? (int)r.sm.smCount : 0;
 }
 
 extern "C" {

@@ -54,5 +54,8 @@ inline cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, dim3 block,
 int check_device();
 // SMs of the current device, 0 when it cannot be asked.
 int sm_count();
+// SMs that kernels on the stream may use: fewer than the device's where the stream belongs to a partition of it
+// (a green context).
+int stream_sm_count(cudaStream_t stream);
 
 }  // namespace kda

@@ -1468,7 +1468,9 @@ cudaError_t launch_dv(const GdnArgs& a, const RowMaps& maps, const Work& ws, lon
     // Chains beside prep where prep is more than one wave of CTAs: 32768 rows of 32 heads take
     // 699 us as eight prompts of mixed lengths (840 one after the other), 1317 as one (1625),
     // 675 as sixteen (632); 7001 rows of 12 heads 115 (137); but 333 rows of 8 heads 41 us, 24 one after the other.
-    if (a.N <= MERGED && waves)
+    // That grid's chains wait for prep on other SMs, so all of its CTAs have to be resident: on a stream of a
+    // partition of the device one after the other, with the same bits.
+    if (a.N <= MERGED && waves && stream_sm_count(st) >= sm_count())
         return pairs ? launch_beside<DK, DV, OUT32, 2>(a, maps, ws, slots, st) : launch_beside<DK, DV, OUT32, 1>(a, maps, ws, slots, st);
     // (in one wave all single heads run at once)
     const cudaError_t e = pairs && waves ? launch_prep<DK, 2>(a, maps, ws, slots, st) : launch_prep<DK, 1>(a, maps, ws, slots, st);

@@ -604,3 +604,21 @@ def test_prefill_rows_of_zeros_on_a_large_state(cuda_lib, lens, Hv, dk, kind, l2
     c.reset()
     c.prefill(cuda_lib)
     c.check()
+
+
+def test_prefill_on_a_part_of_the_device(cuda_lib):
+    """A long call on a stream that may use a part of the SMs only: no grid that needs them all, the same bits."""
+    from tests.green import stream_on_part
+
+    c = Case([1100, 64, 65, 700], Hk=4, Hv=16, seed=100)
+    assert _beside(c)
+    c.prefill(cuda_lib)
+    c.check()
+    want = c.g_out.tensor.clone(), c.g_state.tensor.clone()
+    c.reset()
+    torch.cuda.synchronize()
+    with stream_on_part(32) as (cu, stream, sms):
+        assert sms < torch.cuda.get_device_properties(0).multi_processor_count
+        c.prefill(cuda_lib, stream=stream.value)
+        assert cu.cuStreamSynchronize(stream) == 0
+    assert torch.equal(c.g_out.tensor, want[0]) and torch.equal(c.g_state.tensor, want[1]) and int(c.status.item()) == 0
