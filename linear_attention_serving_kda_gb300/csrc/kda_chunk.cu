@@ -64,6 +64,7 @@
 
 #include <mutex>
 
+#include "kda_check.h"
 #include "kda_common.cuh"
 #include "kda_internal.h"
 #include "kda_ptx.cuh"
@@ -1994,7 +1995,7 @@ cudaError_t launch_chunk(int io_bf16, const ChunkArgs& a, cudaStream_t st)
         cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, chk::kda_chunk_split_kernel<false>, chk::NT,
                                                       chk::SMEM_BYTES);
         const int nc = a.N * a.H;
-        if (per_sm >= 1 && 2 * nc <= sms) {
+        if (per_sm >= 1 && 2 * nc <= sms && stream_sm_count(st) >= sms) {
             chk::SplitArgs sp;
             const size_t flags = ((size_t)nc * (chk::SPLIT_RING + 1) * sizeof(int) + 1023) & ~size_t(1023);
             sp.ready = reinterpret_cast<int*>(a.split_ws);
@@ -2033,7 +2034,7 @@ cudaError_t launch_chunk(int io_bf16, const ChunkArgs& a, cudaStream_t st)
             else chk::kda_split_outputs_kernel<false><<<dim3(gx, nc), chk::NT, 0, st>>>(a, sp);
             return cudaGetLastError();
         }
-        // too few SMs for producers beside the chains: the fused kernel below
+        // too few SMs for producers beside the chains, or a stream that may not use them all: the fused kernel below
     }
     if (a.schedule) chk::kda_chunk_schedule_kernel<<<1, 256, 0, st>>>(a.cu_seqlens, a.N, a.nsplit, a.schedule);
     const dim3 grid(a.N * a.H);

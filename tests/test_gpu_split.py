@@ -172,3 +172,23 @@ def test_chain_flag_wait_runs_out_and_reports(cuda_lib):
     # the context is still usable: the normal call gives the fused kernel's bits
     pp, ff = _both(wl)
     assert torch.equal(pp.out[:wl.T], ff.out[:wl.T]) and torch.equal(pp.rec_state, ff.rec_state)
+
+
+def test_split_shapes_on_a_part_of_the_device(cuda_lib):
+    """On a stream that may use a part of the SMs only, the fused kernel takes the call: the same bits."""
+    from tests.green import stream_on_part
+
+    wl = W.make_workload("split_part", 2900, [1500, 300], H=4, d=128, K=4, io_dtype=W.BF16, gate_mode=W.SAFE,
+                         lower_bound=-5.0, out_gate=True, init_state="random")
+    whole, part = DeviceCase(wl), DeviceCase(wl)
+    assert K.kda_prefill_workspace_bytes(whole.params(), wl.N, wl.T) > 2**20, "not the split path"
+    K.check(whole.prefill())
+    torch.cuda.synchronize()
+    with stream_on_part(32) as (cu, stream, sms):
+        assert sms < torch.cuda.get_device_properties(0).multi_processor_count
+        K.check(part.prefill(stream=stream.value))
+        assert cu.cuStreamSynchronize(stream) == 0
+    assert int(part.dev_status.item()) == 0
+    for name in ("rec_state", "conv_state"):
+        assert torch.equal(getattr(part, name), getattr(whole, name))
+    assert torch.equal(part.out[:wl.T], whole.out[:wl.T])
