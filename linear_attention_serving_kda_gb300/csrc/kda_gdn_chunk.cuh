@@ -10,7 +10,8 @@
 // the norm) stay out of T, M and P: with k_r = f_r k'_r, |k'_r| in [1, 2), and F = diag(f),
 //     F A F^-1 has the entries beta_r f_r^2 e^{G_r - G_s} k'_r.k'_s,  F R takes R's place,
 // and M, P and K S have K' in K's place: no entry of F T F^-1 exceeds 4 while beta |k|^2 <= 2, whatever
-// the rows' magnitudes.  Below, A, T, M, P and R are those.
+// the rows' magnitudes.  Most of the decays stay out of T likewise (D in prep_task: 8 in place of 4).
+// Below, A, T, M, P and R are those.
 //
 // Only S goes from chunk to chunk, so the work is cut where S enters:
 //   - prep, a team of eight warps per (chunk, one or two value heads), all chunks at
@@ -202,7 +203,8 @@ template <int DK, int HEADS> struct PrepSmem {
         alignas(16) float eg[C], gh[C], gl[C], w[C];  // e^G, G / ln 2 in two words, e^{G_C - G}
     } gates[HEADS];
     alignas(16) float norm[2 * C];  // squared norms of k's and q's rows
-    alignas(16) float inv[C], row[2 * C], down[2 * C];  // factors of A's and P's rows; of the stored rows, k's of A's and P's columns
+    alignas(16) float row[2 * C], col[C];     // factors of A's and P's rows and columns
+    alignas(16) float down[2 * C], wd[C];     // of the stored rows; e^{G_C - G} / D
     uint64_t loaded, prod;
     uint32_t tmem;
 };
@@ -459,16 +461,19 @@ __device__ __forceinline__ void prep_task(PrepSmem<DK, HEADS>& sm, const GdnArgs
             const float nrm = r < n ? (a.l2 ? rsqrtf(ss + a.l2_eps) : 1.f) : 0.f, f = nrm * up;
             sm.down[lr] = down;
             if (type == 0) {
-                // R's rows times D: a power of two near e^{G_C - G}, so that rows which the chunk's end
-                // has forgotten do not set the scale of those it has not; M's and P T's columns take
-                // 1 / D, at most 2^12 for P T's sake (its entries stay below 2^14)
+                // D R takes R's place, D a power of two near e^{G_C - G}, so that rows which the chunk's end
+                // has forgotten do not set the scale of those it has not; and D T D^-1, M D^-1 and P D^-1 those
+                // of T, M and P: with T's decays left in it, its small entries (and what M made of them, divided by D)
+                // would be at fp16's smallest step.  D >= 2^-12 for P's sake (its entries stay below 2^14)
                 const float dd = __uint_as_float(__float_as_uint(fminf(fmaxf(gt.w[r], 0x1p-12f), 1.f)) & 0x7f800000u);
                 const float be = fac.beta[r] * dd, ek = be * f * f * gt.eg[r];
-                sm.inv[r] = __uint_as_float((254u << 23) - __float_as_uint(dd));
+                const float inv = __uint_as_float((254u << 23) - __float_as_uint(dd));
+                sm.col[r] = down * inv;
+                sm.wd[r] = gt.w[r] * inv;
                 fac.beta[r] = be * f;
                 fac.ek[r] = ek;
                 atomicMax(reinterpret_cast<int*>(&fac.ektop), __float_as_int(fabsf(ek)));  // >= 0: ordered as integers
-                sm.row[r] = be * sm.inv[r] * nrm * f;  // from the raw rows' products, with their columns' down
+                sm.row[r] = be * nrm * f;  // from the raw rows' products, with their columns' down
             } else {
                 fac.e1[r] = a.scale * f * gt.eg[r];
                 fac.e2[r] = a.scale * f;
@@ -493,10 +498,11 @@ __device__ __forceinline__ void prep_task(PrepSmem<DK, HEADS>& sm, const GdnArgs
                     const int s = s0 + p * 8 + z * 2;
                     const float2 ch = *reinterpret_cast<const float2*>(&gt.gh[s]);
                     const float2 cl = *reinterpret_cast<const float2*>(&gt.gl[s]);
-                    const float2 c2 = *reinterpret_cast<const float2*>(&sm.down[s]);
+                    const float2 c2 = *reinterpret_cast<const float2*>(&sm.col[s]);
                     const float2 e = add2(sub2(both2(rh), ch), sub2(both2(rl), cl));
-                    const float2 x = mul2(mul2(mul2(both2(rf), c2), make_float2(exp2_sfu(e.x), exp2_sfu(e.y))),
-                                          make_float2(d[2 * z], d[2 * z + 1]));
+                    // (rf c2 may be infinite, of rows of zeros say)
+                    const float2 x = mul2(mul2(both2(rf), make_float2(exp2_sfu(e.x), exp2_sfu(e.y))),
+                                          mul2(c2, make_float2(d[2 * z], d[2 * z + 1])));
                     v[2 * z] = s < lim ? x.x : 0.f;
                     v[2 * z + 1] = s + 1 < lim ? x.y : 0.f;
                 }
@@ -602,20 +608,13 @@ __device__ __forceinline__ void prep_task(PrepSmem<DK, HEADS>& sm, const GdnArgs
             }
         } else if (t == 0) ptx::bulk_wait_read_all();  // [K; Q] is on its way: room for P T over q's rows
         team_sync(team);
-        if (w >= 4) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float2 v = *reinterpret_cast<const float2*>(&sm.inv[i * 8 + (lane & 3) * 2]);
-                c[i][0] *= v.x; c[i][1] *= v.y; c[i][2] *= v.x; c[i][3] *= v.y;
-            }
-            store_tile(sm.pt_hi(), sm.pt_lo(), (w - 4) * 16, c);
-        }
-        // T with M's row factors e^{G_C - G}, in pieces of eight values up to each diagonal block's end: 32 + 64 + 96 + 128
+        if (w >= 4) store_tile(sm.pt_hi(), sm.pt_lo(), (w - 4) * 16, c);
+        // T with M's row factors, in pieces of eight values up to each diagonal block's end: 32 + 64 + 96 + 128
 #pragma unroll 1
         for (int i = t; i < 320; i += PREP) {
             const int kt = i < 32 ? 0 : i < 96 ? 1 : i < 192 ? 2 : 3, l = i - 16 * kt * (kt + 1);
             const int rr = kt * 16 + l / (2 * kt + 2), pc = l % (2 * kt + 2);
-            const float f = gt.w[rr];
+            const float f = sm.wd[rr];
             uint4* hp = reinterpret_cast<uint4*>(sm.t_hi + tile_at(rr, pc));
             uint4* lp = reinterpret_cast<uint4*>(sm.t_lo + tile_at(rr, pc));
             const uint4 h4 = *hp, l4 = *lp;
@@ -623,7 +622,7 @@ __device__ __forceinline__ void prep_task(PrepSmem<DK, HEADS>& sm, const GdnArgs
             uint32_t wh[4], wl[4];
 #pragma unroll
             for (int z = 0; z < 4; ++z) {
-                const float2 x = mul2(mul2(add2(unpack_h(hv[z]), unpack_h(lv[z])), both2(f)), *reinterpret_cast<const float2*>(&sm.inv[pc * 8 + 2 * z]));
+                const float2 x = mul2(add2(unpack_h(hv[z]), unpack_h(lv[z])), both2(f));
                 split_h(x.x, x.y, wh[z], wl[z]);
             }
             *hp = make_uint4(wh[0], wh[1], wh[2], wh[3]);
@@ -1424,7 +1423,7 @@ cudaError_t launch_prep(const GdnArgs& a, const RowMaps& maps, const Work& ws, l
     constexpr int smem = sizeof(S);
     static_assert(offsetof(S, t_hi) % 128 == 0 && offsetof(S, fac) % 16 == 0 && offsetof(S, m) % 16 == 0 &&
                   offsetof(S, xd) % 16 == 0 && offsetof(S, gates) % 16 == 0 &&
-                  offsetof(S, down) % 16 == 0 && offsetof(S, loaded) % 8 == 0, "alignment");
+                  offsetof(S, col) % 16 == 0 && offsetof(S, loaded) % 8 == 0, "alignment");
     static_assert((smem + 1024) * PREP_CTAS <= 228 * 1024, "shared memory");
     static PerDeviceOnce once;
     const cudaError_t e = once.run([](int) {

@@ -622,3 +622,35 @@ def test_prefill_on_a_part_of_the_device(cuda_lib):
         c.prefill(cuda_lib, stream=stream.value)
         assert cu.cuStreamSynchronize(stream) == 0
     assert torch.equal(c.g_out.tensor, want[0]) and torch.equal(c.g_state.tensor, want[1]) and int(c.status.item()) == 0
+
+
+@pytest.mark.parametrize("fall", [16, 20])
+@pytest.mark.parametrize("dk,dv", [(128, 128), (64, 32), (32, 64)])
+def test_prefill_state_far_below_the_one_a_chunk_met(cuda_lib, dk, dv, fall):
+    """One chunk whose decays leave a state 2^fall below the one it met.
+
+    Tolerance: T is kept with D on either side, D >= 2^-12 the rows' decay to the chunk's end, so that its entries
+    are off by 2^-25 (fp16's smallest half step) at most; the chunk's first rows meet them with D R, 2^(fall - 12)
+    times the new state, and up to 64 of them add up, of either sign: 2^(fall - 37) * 8 of the new state, beside STATE."""
+    c = Case([64, 64], Hk=2, Hv=2, dk=dk, dv=dv, seed=110 + fall, out="f32")
+    c.A_log.zero_()
+    c.a.zero_()
+    c.dt_bias.fill_(math.log(math.expm1(fall * math.log(2.0) / 64)))
+    c.state0 *= 2.0 ** fall / 0.1
+    c.reset()
+    c.prefill(cuda_lib)
+    tol = 2.0 ** (fall - 34) + STATE
+    c.check(tol_out=tol, tol_state=tol)
+
+
+@pytest.mark.parametrize("l2", [False, True])
+@pytest.mark.parametrize("spread", [1.0, 2.0 ** -40])
+def test_prefill_rows_of_zeros_among_strong_decays(cuda_lib, l2, spread):
+    """Rows of zeros (whose scale is the largest there is) that the chunk's end has forgotten, between others."""
+    c = Case([150, 64], Hk=2, Hv=2, dk=64, dv=64, seed=101, out="f32", l2=l2, gate=1.0, dt=0.0, spread=spread)
+    c.state0 *= spread
+    c.rows[::3] = 0
+    c.rows[64:100] = 0
+    c.reset()
+    c.prefill(cuda_lib)
+    c.check()
