@@ -258,7 +258,7 @@ def test_prefill_nan_stays_in_its_sequence_and_head(cuda_lib):
     assert a[10, 0].isnan().all() and a[80:, 0, 5].isnan().all()
 
 
-def test_prefill_many_sequences(cuda_lib):
+def test_prefill_more_sequences_than_threads(cuda_lib):
     """More sequences than threads of a CTA: they keep their order."""
     r = np.random.default_rng(1)
     lens = r.integers(0, 6, 300).tolist()
