@@ -335,3 +335,51 @@ def test_conv_thousands_of_sequences(cuda_lib):
     c = Conv(lens.tolist(), 16, 3, "f32", 6, slots=np.random.default_rng(3).permutation(2500).tolist())
     c.run(cuda_lib)
     c.check()
+
+
+def _conv64(c):
+    """The definition in 64 bits on the GPU, for cases that take too long on the host."""
+    x, w, state = c.x.double(), c.w.double(), c.state0.double()
+    y, t = torch.full_like(x, float("nan")), 0
+    for ln, s in zip(c.lens, c.slots_h):
+        if s >= 0 and ln:
+            full = torch.cat([state[s], x[t:t + ln]])
+            acc = sum(full[j:j + ln] * w[:, j] for j in range(c.K))
+            y[t:t + ln] = acc * torch.sigmoid(acc)
+            state[s] = full[ln:]
+        t += ln
+    return y, state
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("K", [2, 3, 4])
+def test_conv_long_tiles(cuda_lib, K, io):
+    """Enough rows for tiles of 128: lengths around a tile's and around its batches of eight rows, every row by
+    itself, and the bits of the same rows in calls that are too short for such tiles."""
+    lens = [6000, 127, 128, 129, 0, 255, 257, 1, 130, 5000, 137, 12, 4999, 2900]
+    slots = [3, 0, 7, 5, 1, 2, 4, 6, -1, 9, 8, 11, 10, 12]
+    c = Conv(lens, 4104, K, io, 50 + K, slots=slots, num_slots=14)
+    cols, sms = -(-c.C // 512), torch.cuda.get_device_properties(0).multi_processor_count
+    assert c.T // 128 * cols >= 8 * sms
+    c.run(cuda_lib)
+    y, st = _conv64(c)
+    got, real = c.y.tensor.double(), ~y[:, 0].isnan()
+    # a row's values may all be small: half a step of its own, or of a hundredth of the RMS row
+    err, ref = (got - y)[real].norm(dim=1), y[real].norm(dim=1)
+    assert (err <= TOL[io] * ref.clamp(min=float(ref.square().mean().sqrt()) / 100)).all()
+    assert (got[~real] == 7.0).all()
+    assert torch.equal(c.state.tensor.double(), st)
+    assert int(c.status) == 0 and c.y.intact() and c.state.intact()
+    # the same in calls of a few sequences, long ones in two pieces
+    want_y, want_state = c.y.tensor.clone(), c.state.tensor.clone()
+    c.state.tensor.copy_(c.state0)
+    c.y.tensor.fill_(7.0)
+    t = 0
+    for ln, s in zip(lens, slots):
+        for n in ([ln // 2, ln - ln // 2] if ln > 3000 else [ln]):
+            assert n // 128 * cols < 8 * sms
+            cuda_lib.check(cuda_lib.kda_conv_varlen(c.params(cuda_lib), _i32(0, n), 1, n, c.x[t:], _i32(s), c.state.tensor,
+                                                    c.y.tensor[t:], c.status))
+            t += n
+    torch.cuda.synchronize()
+    assert torch.equal(c.y.tensor, want_y) and torch.equal(c.state.tensor, want_state)
