@@ -192,3 +192,32 @@ def test_sequence_counts_past_the_index_range():
         assert kda.kda_conv_varlen(conv, far, N, 8, addr(2), None, addr(3), addr(4), None, 0) == INVALID
         assert _prefill(_gdn(num_heads_k=1, num_heads_v=1), N=N, T=8, cu=far) == INVALID
     assert kda.kda_conv_varlen(conv, far, kda.KDA_MAX_ROWS, 16, addr(2), None, addr(3), addr(4), None, 0) == INVALID
+
+
+def test_struct_layouts_as_c_sees_them(tmp_path):
+    """Sizes and offsets of every parameter structure from a C program built against the header."""
+    import os
+    import shutil
+    import subprocess
+
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if cc is None:
+        pytest.skip("no C compiler")
+    k = kda.kda
+    structs = [k.kda_params, k.kda_gdn_params, k.kda_conv_params, k.kda_norm_params, k.kda_slot_pool]
+    lines, want = [], []
+    for s in structs:
+        lines.append(f'printf("%zu\\n", sizeof({s.__name__}));')
+        want.append(ctypes.sizeof(s))
+        for f, _ in s._fields_:
+            lines.append(f'printf("%zu\\n", offsetof({s.__name__}, {f}));')
+            want.append(getattr(s, f).offset)
+    src = tmp_path / "layout.c"
+    src.write_text('#include <stddef.h>\n#include <stdio.h>\n#include "kda.h"\nint main(void)\n{\n' + "\n".join(lines) + "\nreturn 0;\n}\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(kbuild._nvcc())))
+    exe = tmp_path / "layout"
+    subprocess.run([cc, "-std=c11", "-I", os.path.join(root, "include"), "-I", os.path.join(cuda, "include"), str(src), "-o", str(exe)],
+                   check=True)
+    got = subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.split()
+    assert [int(x) for x in got] == want
