@@ -383,3 +383,100 @@ def test_conv_long_tiles(cuda_lib, K, io):
             t += n
     torch.cuda.synchronize()
     assert torch.equal(c.y.tensor, want_y) and torch.equal(c.state.tensor, want_state)
+
+
+def test_conv_rows_behind_the_last_sequence(cuda_lib):
+    c = Conv([40, 3, 70], 64, 4, "bf16", 7)
+    cuda_lib.check(cuda_lib.kda_conv_varlen(c.params(cuda_lib), c.cu, 2, c.T, c.x, None, c.state.tensor, c.y.tensor, c.status))
+    torch.cuda.synchronize()
+    y, _ = P.conv(c.lens, _f(c.x), _f(c.w), _f(c.state0), c.slots_h)
+    assert P.rel(_f(c.y.tensor[:43]), y[:43]) <= TOL["bf16"] and (c.y.tensor[43:] == 7.0).all()
+    assert torch.equal(c.state.tensor[2], c.state0[2]) and int(c.status) == 0
+
+
+def test_largest_pool(cuda_lib):
+    """As many slots as a pool may have: copy, zero, and the plan and moves of a compaction."""
+    S, n = cuda_lib.KDA_MAX_POOL_SLOTS, 4
+    t, pool = _pool(cuda_lib, 2, S, n)
+    before, status = t.tensor.clone(), _i32(0)
+    cuda_lib.check(cuda_lib.kda_slots_copy(pool, 5, _i32(S - 1, S - 1, S, 0, 7), _i32(S - 2, 1, 3, S - 3, S - 4), status))
+    cuda_lib.check(cuda_lib.kda_slots_zero(pool, 2, _i32(S - 1, S - 5), status))
+    torch.cuda.synchronize()
+    want = _copied(before, S, n, [(S - 1, S - 2), (S - 1, 1), (0, S - 3), (7, S - 4)])
+    for s in (S - 1, S - 5):
+        want[:, s * n:(s + 1) * n] = 0
+    assert torch.equal(t.tensor, want) and t.intact() and int(status) == cuda_lib.KDA_DEV_BAD_SLOT
+    live = np.random.default_rng(9).random(S) < 0.4
+    src, dst, remap = (Guarded((S,), torch.int32, "cuda") for _ in range(3))
+    lv = torch.from_numpy(live.astype(np.int32)).cuda()
+    cuda_lib.check(cuda_lib.kda_slots_compact_plan(pool, lv, src.tensor, dst.tensor, remap.tensor))
+    cuda_lib.check(cuda_lib.kda_slots_copy(pool, S, src.tensor, dst.tensor, None))
+    torch.cuda.synchronize()
+    moves, where = P.compact_plan(live)
+    assert remap.tensor.tolist() == where and src.tensor[:len(moves)].tolist() == [m[0] for m in moves]
+    m = torch.tensor(moves, device="cuda")
+    got = want.view(2, S, n).clone()
+    got[:, m[:, 1]] = want.view(2, S, n)[:, m[:, 0]]
+    assert torch.equal(t.tensor, got.view(2, S * n)) and all(x.intact() for x in (t, src, dst, remap))
+
+
+def test_layer_captured(cuda_lib):
+    """A layer's calls one behind the other in a captured graph (kernels that may start early, a memory set and a
+    grid of all SMs between them): replayed twice, the eager calls' bits."""
+    r = np.random.default_rng(12)
+    bf = torch.bfloat16
+    Hk, Hv, d, K, N = 4, 16, 64, 4, 2
+    C, lens = (2 * Hk + Hv) * d, [1500, 700]
+    T = sum(lens)
+    t = lambda *s, sd=1.0: torch.from_numpy(r.standard_normal(s) * sd).cuda()  # noqa: E731
+    x, z, a, b = t(T, C).to(bf), t(T, Hv * d).to(bf), t(T, Hv).to(bf), t(T, Hv).to(bf)
+    conv_w, A_log, dt = t(C, K, sd=0.5).float(), t(Hv, sd=0.3).float(), t(Hv).float() - 3
+    S = 4
+    conv0, rec0 = t(S, K - 1, C).to(bf), t(S, Hv, d, d, sd=0.1).float()
+    conv_state, rec, xn, y = conv0.clone(), rec0.clone(), torch.empty_like(x), torch.empty_like(x)
+    o, on = (torch.empty(T, Hv, d, dtype=bf, device="cuda") for _ in range(2))
+    cu, slots, status = _i32(0, lens[0], T), _i32(2, 0), _i32(0)
+    kda = cuda_lib
+    cp = kda.ConvParams(channels=C, conv_kernel=K, conv_weight=conv_w, num_slots=S)
+    gp = kda.GdnParams(Hk, Hv, d, d, A_log, dt, scale=d ** -0.5, num_slots=S, q_row_stride=C, k_row_stride=C, v_row_stride=C)
+    need = kda.kda_gdn_prefill_workspace_bytes(gp, N, T)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    pools = [kda.SlotPool(pool=p, num_layers=1, num_slots=S, slot_bytes=n, layer_stride_bytes=S * n)
+             for p, n in ((conv_state, (K - 1) * C * 2), (rec, Hv * d * d * 4))]
+    src, dst, gone, next_rows = _i32(2, 0), _i32(1, 3), _i32(2), _i32(1, 3)
+    assert (T // 64 + N) * Hv > 3 * torch.cuda.get_device_properties(0).multi_processor_count
+
+    def calls():
+        kda.check(kda.kda_block_norm(kda.NormParams(dim=C, post_norm=False), T, x, None, None, None, xn))
+        kda.check(kda.kda_conv_varlen(cp, cu, N, T, xn, slots, conv_state, y, status))
+        q, k, v = y[:, :Hk * d], y[:, Hk * d:2 * Hk * d], y[:, 2 * Hk * d:]
+        kda.check(kda.kda_gdn_prefill_varlen(gp, cu, N, T, q, k, v, a, b, slots, rec, o, ws, need, status))
+        kda.check(kda.kda_block_norm(kda.NormParams(dim=d, gate_act=kda.KDA_NORM_GATE_SILU), T * Hv, o, z, None, None, on))
+        for p in pools:  # fork both sequences, free one, then a token of the copies
+            kda.check(kda.kda_slots_copy(p, 2, src, dst, status))
+            kda.check(kda.kda_slots_zero(p, 1, gone, status))
+        kda.check(kda.kda_conv_decode(cp, N, xn, next_rows, conv_state, y, status))
+        kda.check(kda.kda_gdn_decode(gp, N, q, k, v, a, b, next_rows, rec, o, status))
+
+    outs = (xn, y, o, on, conv_state, rec)
+
+    def reset():
+        conv_state.copy_(conv0)
+        rec.copy_(rec0)
+        for buf in (xn, y, o, on):
+            buf.fill_(7.0)
+
+    reset()
+    calls()
+    torch.cuda.synchronize()
+    want = [buf.clone() for buf in outs]
+    assert int(status) == 0 and all(w.isfinite().all() for w in want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls()
+    for _ in range(2):
+        reset()
+        graph.replay()
+        torch.cuda.synchronize()
+        for got, w in zip(outs, want):
+            assert torch.equal(got, w)

@@ -101,3 +101,31 @@ def test_the_rows_bound_sees_one_wrong_row():
     assert P.rel(got, out) < 2.0 ** -8 + 2.0 ** -10
     err, ref = np.linalg.norm(got - out, axis=-1), np.linalg.norm(out, axis=-1)
     assert (err > 2.0 ** -8 * ref + 2.0 ** -14 * np.sqrt((ref ** 2).mean())).sum() == 1
+
+
+@pytest.mark.parametrize("N", [129, 300])
+def test_fp32_rows_of_many_sequences(cuda_lib, N):
+    """More sequences than are put in order by their lengths."""
+    lens = np.random.default_rng(N).integers(0, 6, N)
+    lens[N // 2] = 140
+    c = Case(lens.tolist(), Hk=1, Hv=2, dk=64, dv=32, io="f32", out="f32", seed=92, slots=np.random.default_rng(2).permutation(N).tolist())
+    c.prefill(cuda_lib)
+    check_rows(c)
+
+
+@pytest.mark.parametrize("io,Hv,first", [("bf16", 2, 70), ("bf16", 16, 2600), ("f32", 2, 70)])
+def test_rows_behind_the_last_sequence(cuda_lib, io, Hv, first):
+    """A call over more rows than its sequences have: the rows behind them, and everyone else's state, stay."""
+    c = Case([first, 30, 41], Hk=2, Hv=Hv, dk=64, dv=32, io=io, out="f32", seed=160)
+    c.N = 2
+    assert beside(c) == (Hv == 16)
+    p = c.params(cuda_lib)
+    need = cuda_lib.kda_gdn_prefill_workspace_bytes(p, 2, c.T)
+    ws = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
+    cuda_lib.check(cuda_lib.kda_gdn_prefill_varlen(p, c.cu, 2, c.T, c.q, c.k, c.v, c.a, c.b, None, c.g_state.tensor,
+                                                   c.g_out.tensor, ws, need, c.status))
+    torch.cuda.synchronize()
+    out, _ = c.want()
+    n = first + 30
+    assert (c.g_out.tensor[n:] == 7.0).all() and torch.equal(c.g_state.tensor[2], c.state0[2])
+    assert P.rel(c.g_out.tensor[:n].double().cpu().numpy(), out[:n]) <= 2.0 ** -18 and int(c.status.item()) == 0
