@@ -368,7 +368,8 @@ typedef struct kda_gdn_params {
  *   - workspace: kda_gdn_prefill_workspace_bytes(p, N, T) bytes (may be NULL
  *     when that is 0, for fp32 rows); it grows with
  *     (T/64 + N) heads: 1.10 GB for 32768 rows, 16 key and 32 value heads of
- *     128, whatever the out_dtype.  Contents need no init.  Calls that may run at the same time take a
+ *     128, whatever the out_dtype.  A long prompt cut into several calls needs
+ *     no more of it than the longest of them.  Contents need no init.  Calls that may run at the same time take a
  *     workspace each.
  *   - Long calls run as one cooperative grid of a CTA an SM; a call on a device
  *     of which other work holds SMs waits for them.  On a stream of a green
@@ -424,7 +425,8 @@ KDA_API int kda_conv_decode(const kda_conv_params* p, int32_t B, const void* x, 
  *   nullable, not both.  An output may be the very buffer of an input of its
  *   type (row for row in place); any other overlap with an input or with the
  *   other output is KDA_ERR_INVALID_ARGUMENT.  A row of infinities or NaN
- *   gives NaN in that row alone.
+ *   gives NaN in that row alone.  The sums of squares have fp32's range: values
+ *   up to 2^56 in magnitude, and down to 2^-50 where norm_eps is 0.
  */
 #define KDA_NORM_GATE_NONE 0
 #define KDA_NORM_GATE_SIGMOID 1

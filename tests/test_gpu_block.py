@@ -480,3 +480,21 @@ def test_layer_captured(cuda_lib):
         torch.cuda.synchronize()
         for got, w in zip(outs, want):
             assert torch.equal(got, w)
+
+
+@pytest.mark.parametrize("D", [24, 512, 16384])
+@pytest.mark.parametrize("e", [56, -50])
+def test_block_norm_ends_of_the_range(cuda_lib, D, e):
+    """The largest and smallest values whose squares the sums hold, in every place and in one alone, without eps."""
+    y = torch.zeros(3, D, device="cuda")
+    y[0] = 2.0 ** e
+    y[1, D - 1] = -2.0 ** e
+    y[2] = torch.ldexp(torch.rand(D, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda") + 0.5, torch.tensor(e - 1))
+    F32 = cuda_lib.KDA_DTYPE_F32
+    h, x = torch.empty_like(y), torch.empty_like(y)
+    p = cuda_lib.NormParams(dim=D, norm_eps=0.0, io_dtype=F32, res_dtype=F32)
+    cuda_lib.check(cuda_lib.kda_block_norm(p, 3, y, None, None, h, x))
+    torch.cuda.synchronize()
+    eh, ex = P.block_norm(_f(y), None, 0, None, 1.0, True, 1.0, 1.0, 0.0)
+    for r in range(3):
+        assert P.rel(_f(h[r]), eh[r]) <= TOL["f32"] and P.rel(_f(x[r]), ex[r]) <= TOL["f32"]
