@@ -134,7 +134,7 @@ constexpr int CONV_AHEAD = 8; // rows loaded at a time, a batch ahead of the one
 // Tiles start at a sequence's first row, so only its tile 0 reads the old
 // state: that CTA also writes the new one, after its reads, and no other CTA
 // touches the slot.  blockIdx.x counts tiles over the sequences.  Six CTAs an SM: five
-// (174 registers) took 199 us where these take 178.
+// (174 registers) took 199 us where these take 178, though four bf16 taps spill 48 bytes of loads for it.
 template <typename IO, int K, int CONV_ROWS> __global__ void __launch_bounds__(CT, sizeof(IO) == 2 ? 6 : 1) conv_varlen_kernel(const ConvArgs a)
 {
     ptx::grid_launch_dependents();
@@ -274,8 +274,8 @@ template <typename IO, int K> cudaError_t launch_conv_decode(const ConvArgs& a, 
 template <typename IO, int K> cudaError_t launch_conv_varlen(const ConvArgs& a, int cols, cudaStream_t st)
 {
     // long tiles (the K-1 rows before a tile and the taps are read again for each) where they
-    // still give every SM several CTAs: 32768 rows of 8192 channels 176 us, 218 with short ones;
-    // 333 rows 7.9 us with short ones, 21 with long ones
+    // still give every SM eight CTAs: 32768 rows of 8192 channels 176 us, 218 with short ones;
+    // 333 rows 7.9 us with short ones, 21 with long ones.  Nothing between the two lengths was tried
     if ((long long)(a.T / 128) * cols >= 8LL * sm_count())
         return launch_dependent(conv_varlen_kernel<IO, K, 128>, dim3(a.N + a.T / 128, cols), CT, 0, st, a);
     return launch_dependent(conv_varlen_kernel<IO, K, 16>, dim3(a.N + a.T / 16, cols), CT, 0, st, a);

@@ -23,12 +23,14 @@
 // prep run as one grid, chains beside prep (gdn_beside_kernel); others as two kernels one
 // after the other.
 //
-// Bounds and figures (16 key and 32 value heads of 128 x 128, bf16 outputs).  Neither HBM
-// (a quarter of its time at most: rows 0.8 GB and workspace 2 GB for 32768 rows) nor the tensor cores
-// (24 % busy) but dependent steps: prep issues an instruction every other cycle and
-// else waits at its barriers, 322 us for 32768 rows with 24 warps an SM; a chunk of a chain takes 2.5 us,
+// Bounds and figures (16 key and 32 value heads of 128 x 128, bf16 outputs, 32768 rows).  Dependent
+// steps first: prep issues an instruction every other cycle and else waits at its barriers,
+// 330 us with 24 warps an SM; a chunk of a chain takes 2.6 us,
 // of which the products are 1.0 and the rest the state's way between registers and
-// TMEM.  32768 rows as eight prompts 737 us, as one prompt 1350, which is its 512 chunks one after the other.
+// TMEM.  Eight prompts 725 us, one prompt 1350, which is its 512 chunks one after the other.  HBM next:
+// rows of 0.8 GB, and a workspace of 1.1 GB written once and read 1.25 times, are 3.3 GB at most, 480 us at the
+// copy rate: two thirds of the eight prompts' time, a third of the one's.  The tensor cores are 28 % busy.
+// (The beside kernels run at their 80 registers and spill up to 150 bytes of loads a thread.)
 //
 // Precision: the state keeps fp32 accuracy.  One decay per head leaves k and q
 // unscaled inside every product, so the rows' bf16 values are operands without
@@ -37,7 +39,7 @@
 // (S, R, T, M, P, P T) is two fp16 values, high and low, about 22 bits; S and R are
 // scaled by a power of two per column and chunk, so that the low part stays in fp16's range.
 // That holds for bf16 outputs too: on nearly equal keys an output is a small difference of
-// large products, and high parts alone (eight prompts 705 us in place of 737, one 1324 in place
+// large products, and high parts alone (eight prompts 705 us in place of 725, one 1324 in place
 // of 1350) put 3 % of such outputs more than a bf16 step and 1e-3 of their RMS off.
 #pragma once
 
@@ -520,7 +522,7 @@ __device__ __forceinline__ void prep_task(PrepSmem<DK, HEADS>& sm, const GdnArgs
         ptx::tc_fence_before();
         team_sync(team);
         if (w >= 4) {
-            // meanwhile the rows themselves, and the largest of k's factors
+            // meanwhile the rows themselves
             if (j == 0) {
                 const int row = (w - 4) * 32 + lane;
                 wait(sm.loaded, turn);
@@ -1462,11 +1464,16 @@ template <int DK, int DV, bool OUT32>
 cudaError_t launch_dv(const GdnArgs& a, const RowMaps& maps, const Work& ws, long long slots, cudaStream_t st)
 {
     // Two heads a team (their rows, products and norms once): 32768 rows as eight prompts take
-    // 699 us, 785 with one; one prompt 1317 and 1310.
+    // 725 us, 840 with one; one prompt 1350 and 1333.
     const bool pairs = a.Hv / a.Hk % 2 == 0, waves = slots * a.Hv > PREP_CTAS * sm_count();
-    // Chains beside prep where prep is more than one wave of CTAs: 32768 rows of 32 heads take
-    // 699 us as eight prompts of mixed lengths (840 one after the other), 1317 as one (1625),
-    // 675 as sixteen (632); 7001 rows of 12 heads 115 (137); but 333 rows of 8 heads 41 us, 24 one after the other.
+    // Chains beside prep where prep is more than one wave of CTAs, in us (in brackets: one after the
+    // other).  32768 rows of 32 heads: one prompt 1350 (1683); mixed lengths of 8 prompts 725 (881), 12 709 (789),
+    // 16 707 (670), 32 741 (703), 64 803 (777); equal ones of 2 693 (1014), 4 912 (689), 8 734 (698), 16 744 (711),
+    // 64 775 (762).  Of 4 heads: mixed lengths of 4 to 64 prompts 533 to 130 (555 to 158), equal ones of 16 128 (148),
+    // 24 178 (124), 32 164 (109), 64 120 (119).  8192 rows of 12 heads: mixed lengths of 8 120 (126), 24 94 (97), 32 95
+    // (89), 64 111 (106).  333 rows of 8 heads, not a wave: 42 (24).  So it gains where some chains are longer than the
+    // others or there are few of them, up to a third, and loses some 5 % where there are several equal ones for every
+    // SM and up to a third where there is about one: the lengths are on the device, where this choice cannot see them.
     // That grid's chains wait for prep on other SMs, so all of its CTAs have to be resident: on a stream of a
     // partition of the device one after the other, with the same bits.
     if (a.N <= MERGED && waves && stream_sm_count(st) >= sm_count())

@@ -3,7 +3,7 @@
 // Pure data movement: a copied slot is read once and written once, so the
 // bound is HBM bandwidth.  A fork's source is read once for each RUN of targets, from
 // HBM once: seven copies of 24 layers of 2 MiB 70 us, 5.7 TB/s of what the copy has to move.
-// 107 moves of 24 layers of 48 KiB with their plan 30 us, 5.1 TB/s, seven of them the plan and the second launch.
+// 66 moves of 24 layers of 48 KiB with their plan 30 us, 5.1 TB/s, seven of the 30 the plan and the second launch.
 #include "kda_check.h"
 #include "kda_common.cuh"
 #include "kda_ptx.cuh"
