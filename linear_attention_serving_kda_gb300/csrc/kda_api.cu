@@ -7,8 +7,6 @@
 // GenAI PR #2843, author's review reply).
 #include <cmath>
 #include <cstring>
-#include <mutex>
-
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -71,6 +69,25 @@ size_t log_float_bytes(const kda_params* p, int32_t B, int32_t W)
 
 }  // namespace
 
+// A function of the driver's by name, null where it has none.
+static void* driver_function(const char* name, unsigned version)
+{
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+    return cudaGetDriverEntryPointByVersion(name, &ptr, version, cudaEnableDefault, &q) == cudaSuccess &&
+           q == cudaDriverEntryPointSuccess ? ptr : nullptr;
+}
+
+// A thread whose first CUDA call is one of ours has no current context, which
+// the driver's own calls (tensor maps, a stream's resources) need: the runtime
+// binds one at its first launch, and here at cudaSetDevice.
+static bool bind_context(int dev)
+{
+    static const auto current = reinterpret_cast<PFN_cuCtxGetCurrent_v4000>(driver_function("cuCtxGetCurrent", 4000));
+    CUcontext c = nullptr;
+    return (current && current(&c) == CUDA_SUCCESS && c) || cudaSetDevice(dev) == cudaSuccess;
+}
+
 // The library is built for sm_103a only; remember the answer per device
 // (the set-up object records only a successful check; -1 marks another GPU).
 int kda::check_device()
@@ -85,7 +102,7 @@ int kda::check_device()
         if (r == cudaSuccess) ok[d].store((major == 10 && minor == 3) ? 1 : -1, std::memory_order_relaxed);
         return r;
     });
-    if (e != cudaSuccess || cudaGetDevice(&dev) != cudaSuccess) return KDA_ERR_DEVICE;
+    if (e != cudaSuccess || cudaGetDevice(&dev) != cudaSuccess || !bind_context(dev)) return KDA_ERR_DEVICE;
     return ok[dev].load(std::memory_order_relaxed) == 1 ? KDA_OK : KDA_ERR_DEVICE;
 }
 
@@ -102,21 +119,13 @@ int kda::sm_count()
 
 int kda::stream_sm_count(cudaStream_t stream)
 {
-    static PFN_cuStreamGetGreenCtx_v12040 green_of = nullptr;
-    static PFN_cuGreenCtxGetDevResource_v12040 resource_of = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        auto find = [](const char* name) {
-            void* ptr = nullptr;
-            cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-            return cudaGetDriverEntryPointByVersion(name, &ptr, 12040, cudaEnableDefault, &q) == cudaSuccess &&
-                   q == cudaDriverEntryPointSuccess ? ptr : nullptr;
-        };
-        green_of = reinterpret_cast<PFN_cuStreamGetGreenCtx_v12040>(find("cuStreamGetGreenCtx"));
-        resource_of = reinterpret_cast<PFN_cuGreenCtxGetDevResource_v12040>(find("cuGreenCtxGetDevResource"));
-    });
+    static const auto green_of = reinterpret_cast<PFN_cuStreamGetGreenCtx_v12040>(driver_function("cuStreamGetGreenCtx", 12040));
+    static const auto resource_of =
+        reinterpret_cast<PFN_cuGreenCtxGetDevResource_v12040>(driver_function("cuGreenCtxGetDevResource", 12040));
     CUgreenCtx g = nullptr;
-    if (!green_of || !resource_of || green_of(stream, &g) != CUDA_SUCCESS || !g) return sm_count();
+    if (!green_of || !resource_of) return sm_count();  // a driver without such streams
+    if (green_of(stream, &g) != CUDA_SUCCESS) return 0;  // no answer: take none for granted
+    if (!g) return sm_count();
     CUdevResource r;
     return resource_of(g, &r, CU_DEV_RESOURCE_TYPE_SM) == CUDA_SUCCESS ? (int)r.sm.smCount : 0;
 }

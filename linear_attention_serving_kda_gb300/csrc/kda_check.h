@@ -55,7 +55,7 @@ int check_device();
 // SMs of the current device, 0 when it cannot be asked.
 int sm_count();
 // SMs that kernels on the stream may use: fewer than the device's where the stream belongs to a partition of it
-// (a green context).
+// (a green context), 0 where the driver does not say.
 int stream_sm_count(cudaStream_t stream);
 
 }  // namespace kda

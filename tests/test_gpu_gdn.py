@@ -654,3 +654,27 @@ def test_prefill_rows_of_zeros_among_strong_decays(cuda_lib, l2, spread):
     c.reset()
     c.prefill(cuda_lib)
     c.check()
+
+
+@pytest.mark.parametrize("lens", [[90, 41], [1100, 64, 65, 700]])
+def test_calls_from_another_thread(cuda_lib, lens):
+    """A thread whose first CUDA call this is: the same bits."""
+    import threading
+
+    c = Case(lens, Hk=4, Hv=16, seed=102)
+    c.prefill(cuda_lib)
+    want = c.g_out.tensor.clone(), c.g_state.tensor.clone()
+    c.reset()
+    p = c.params(cuda_lib)
+    need = cuda_lib.kda_gdn_prefill_workspace_bytes(p, c.N, c.T)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    stream = torch.cuda.current_stream().cuda_stream
+    torch.cuda.synchronize()
+    rc = []
+    t = threading.Thread(target=lambda: rc.append(cuda_lib.kda_gdn_prefill_varlen(
+        p, c.cu, c.N, c.T, c.q, c.k, c.v, c.a, c.b, None, c.g_state.tensor, c.g_out.tensor, ws, need, c.status, stream)))
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    assert rc == [cuda_lib.KDA_OK] and int(c.status.item()) == 0
+    assert torch.equal(c.g_out.tensor, want[0]) and torch.equal(c.g_state.tensor, want[1])

@@ -220,3 +220,25 @@ def test_prefill_then_decode(cuda_lib, oracle_mod, T):
     assert_close(np.concatenate([to_np(o) for o in outs]), ref["out"][T:], "decoded rows")
     assert_close(to_np(pre.rec_state), ref["rec_state"], "final state")
     assert np.array_equal(to_np(pre.conv_state), ref["conv_state"].astype(np.float32))
+
+
+@pytest.mark.parametrize("lens,H", [([100, 37], 2), ([1500, 300], 4)])
+def test_prefill_from_another_thread(cuda_lib, lens, H):
+    """A thread whose first CUDA call is the prefill (fused kernel; split path): the same bits."""
+    import threading
+
+    wl = W.make_workload("thread", 77, lens, H=H, d=128, K=4, io_dtype=W.BF16, gate_mode=W.SAFE, lower_bound=-5.0,
+                         out_gate=True, init_state="random")
+    here, there = DeviceCase(wl), DeviceCase(wl)
+    K.check(here.prefill())
+    need = K.kda_prefill_workspace_bytes(there.params(), wl.N, wl.T)
+    there.workspace = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
+    stream = torch.cuda.current_stream().cuda_stream
+    torch.cuda.synchronize()
+    rc = []
+    t = threading.Thread(target=lambda: rc.append(there.prefill(stream=stream)))
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    assert rc == [K.KDA_OK] and int(there.dev_status.item()) == 0
+    assert torch.equal(there.out[:wl.T], here.out[:wl.T]) and torch.equal(there.rec_state, here.rec_state)
