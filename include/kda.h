@@ -360,6 +360,8 @@ typedef struct kda_gdn_params {
  *   - A prompt cut into several calls agrees with one uncut call to rounding.
  *     A chunk that leaves a state more than 2^12 below the one it met keeps
  *     about 2^-34 of the old one in place of 2^-21 of the new one.
+ *     Nearly equal keys without decays, whose corrections undo one another, cost
+ *     up to 2^-15 of the state as beta |k|^2 comes near 2 (2^-16 near 1).
  *   - Values up to 2^60 in magnitude keep that accuracy (operands are rescaled
  *     by powers of two within 2^+-60).  With l2_norm = 0 keys are expected to
  *     satisfy beta |k|^2 <= 2, beyond which the rule itself grows without bound.

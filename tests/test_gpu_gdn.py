@@ -678,3 +678,17 @@ def test_calls_from_another_thread(cuda_lib, lens):
     torch.cuda.synchronize()
     assert rc == [cuda_lib.KDA_OK] and int(c.status.item()) == 0
     assert torch.equal(c.g_out.tensor, want[0]) and torch.equal(c.g_state.tensor, want[1])
+
+
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 32), (32, 128)])
+def test_prefill_nearly_equal_keys_of_the_largest_norm(cuda_lib, dk, dv):
+    """Nearly equal keys of beta |k|^2 near 2, hardly any decay: every correction turns the last one around.
+
+    Tolerance: T's entries alternate around +-2 along 64 rows, so the sums that make M and S' are of 64 terms of
+    one size and either sign, each 2^-22 of 2 off: 2^-15."""
+    c = Case([150, 64], Hk=1, Hv=2, dk=dk, dv=dv, seed=103, out="f32", l2=False, gate=-10.0, beta=9.0)
+    c.k[:] = c.k[:1] + 0.05 * c.k
+    k = c.k.float()
+    c.k.copy_(k / k.norm(dim=-1, keepdim=True) * 1.4)
+    c.prefill(cuda_lib)
+    c.check(tol_out=2.0 ** -15, tol_state=2.0 ** -15)
