@@ -85,6 +85,7 @@ extern "C" {
 #define KDA_DEV_BAD_SLOT 2     /* slots[b] >= num_slots */
 #define KDA_DEV_BAD_ACCEPTED 4 /* accepted[b] outside [0, W] */
 #define KDA_DEV_TIMEOUT 8      /* a bounded on-chip wait gave up; the unit was skipped */
+#define KDA_DEV_BAD_PAGE 16    /* a page number in use is negative or >= num_pages */
 
 #define KDA_DTYPE_F32 0
 #define KDA_DTYPE_BF16 1
@@ -486,6 +487,178 @@ KDA_API int kda_slots_zero(const kda_slot_pool* pool, int32_t n, const int32_t* 
  */
 KDA_API int kda_slots_compact_plan(const kda_slot_pool* pool, const int32_t* live, int32_t* src, int32_t* dst,
                                    int32_t* remap, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Softmax attention over a paged cache of keys and values, for the layers
+ * that hybrid models put between the recurrent ones: rotary positions, the
+ * append of new rows to the cache, the attention of a chunk of new rows and
+ * of single tokens.  The conventions at the top hold for these calls too.
+ * None of the source pages has these operators in this form.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Rotary positions.  Pair i < rotary_dim / 2 of a head turns by the angle
+ * position * f_i; f_i (radians per position), from the base and the scaling
+ * for contexts longer than the trained `length`:
+ *   f_i = base^(-2 i / rotary_dim), then
+ *   NONE    f_i
+ *   LINEAR  f_i / factor
+ *   BASE    f_i of the base  base * factor^(rotary_dim / (rotary_dim - 2))
+ *   RAMP    f_i (1 - r_i) + r_i f_i / factor, r_i rising from 0 to 1 over the pairs
+ *           from floor(d(fast)) to ceil(d(slow)), d(b) = rotary_dim
+ *           ln(length / (2 pi b)) / (2 ln base): the pair that makes b turns over length
+ *   SMOOTH  f_i k_i + (1 - k_i) f_i / factor, k_i rising from 0 to 1 with the pair's
+ *           turns over length, length f_i / (2 pi), from slow to fast
+ */
+#define KDA_ROPE_SCALE_NONE 0
+#define KDA_ROPE_SCALE_LINEAR 1
+#define KDA_ROPE_SCALE_BASE 2
+#define KDA_ROPE_SCALE_RAMP 3
+#define KDA_ROPE_SCALE_SMOOTH 4
+typedef struct kda_rope_scaling {
+    double base;   /* > 1 (10000)                                               */
+    double factor; /* > 0; not read with NONE                                   */
+    double length; /* > 0, RAMP and SMOOTH                                      */
+    double fast;   /* turns over length: fast > slow > 0, RAMP (32, 1) and      */
+    double slow;   /*   SMOOTH (4, 1)                                           */
+    int32_t kind;  /* KDA_ROPE_SCALE_*                                          */
+} kda_rope_scaling;
+
+/*
+ * The angles of rotary_dim / 2 pairs as the kernels take them, into HOST
+ * memory (the caller copies them to the device once): turns[i] =
+ * frac(f_i / (2 pi)) * 2^64.  A position times that, modulo 2^64, is the
+ * angle's fraction of a turn, exactly: far positions lose nothing.
+ *   radians: HOST, nullable; rotary_dim / 2 finite angles in place of
+ *            base^(-2 i / rotary_dim), for any other scheme (kind BASE then
+ *            gives KDA_ERR_INVALID_ARGUMENT).
+ * rotary_dim: even, 2 .. KDA_ROPE_MAX_DIM.  Touches no GPU.
+ */
+#define KDA_ROPE_MAX_DIM 512
+KDA_API int kda_rope_turns(const kda_rope_scaling* s, int32_t rotary_dim, const double* radians, uint64_t* turns);
+
+/*
+ * Rotation of the heads of `rows` rows: with c = a cos, s = a sin of a pair's
+ * angle (a = rope_amplitude), pair (x1, x2) becomes (x1 c - x2 s, x2 c + x1 s).
+ * Pair i is the channels (i, i + rotary_dim / 2) of its head (HALF) or
+ * (2 i, 2 i + 1) (PAIRS); channels from rotary_dim on stay as they are.
+ * transpose = 1 turns the other way: the gradient of the rotation.
+ *   positions: device int32 [rows]; a row with a negative one is skipped.
+ *   x, y: [rows][num_heads][head_dim] of io_dtype with a row stride each; y may
+ *         be x itself (with the same stride), any other overlap is
+ *         KDA_ERR_INVALID_ARGUMENT.  q and k heads that follow one another in
+ *         a row take one call.
+ */
+#define KDA_ROPE_HALF 0
+#define KDA_ROPE_PAIRS 1
+typedef struct kda_rope_params {
+    int32_t num_heads;          /* >= 1                                         */
+    int32_t head_dim;           /* a multiple of 16, <= KDA_ROPE_MAX_DIM        */
+    int32_t io_dtype;           /* x and y: KDA_DTYPE_F32 / _BF16               */
+    int32_t rotary_dim;         /* even, 2 .. head_dim                          */
+    int32_t rope_layout;        /* KDA_ROPE_HALF / _PAIRS                       */
+    int32_t transpose;          /* 0 or 1                                       */
+    float rope_amplitude;       /* finite (1.0)                                 */
+    int64_t x_row_stride;       /* elements; 0: dense; at least dense, and a    */
+    int64_t y_row_stride;       /*   multiple of 16 bytes                       */
+    const uint64_t* rope_turns; /* device [rotary_dim / 2], from kda_rope_turns */
+} kda_rope_params;
+KDA_API int kda_rope(const kda_rope_params* p, int64_t rows, const int32_t* positions, const void* x, void* y,
+                     cudaStream_t stream);
+
+/*
+ * A layer's heads and its cache.  Keys and values lie in pages of page_size
+ * tokens: token t of sequence s is place t mod page_size of page
+ * pages[s][t / page_size] (device int32 [N][pages_per_seq]); several sequences
+ * may share a page.  k_cache and v_cache: num_pages pages each, with the same
+ * strides between pages, tokens and key heads, so that either order of
+ * tokens and heads, and pools of several layers or of keys and values side
+ * by side, fit (a page is a slot of kda_slots_copy then: copies of shared pages).
+ * Table entries past a sequence's tokens are not read.
+ */
+typedef struct kda_paged_params {
+    int32_t num_heads_q;          /* Hq, a multiple of Hkv                      */
+    int32_t num_heads_kv;         /* Hkv >= 1; query head h reads key head h / (Hq / Hkv); Hq <= 1024 */
+    int32_t head_dim;             /* D in {32, 64, 128, 256}                    */
+    int32_t io_dtype;             /* rows, cache and out: KDA_DTYPE_F32 / _BF16 */
+    int32_t page_size;            /* 16, 32, 64, 128, 256, 512 or 1024          */
+    int32_t num_pages;            /* >= 1                                       */
+    int32_t pages_per_seq;        /* >= 1; times page_size <= KDA_MAX_ROWS      */
+    int32_t causal;               /* attention: 1, or 0 (every row sees every token) */
+    int32_t window;               /* attention: 0, or with causal = 1 the tokens a row sees, its own the last */
+    int32_t rotary_dim;           /* append: 0, or as in kda_rope_params        */
+    int32_t rope_layout;          /* append                                     */
+    float rope_amplitude;         /* append                                     */
+    float scale;                  /* attention: of q.k; finite, > 0             */
+    int64_t cache_page_stride;    /* elements; 0: dense [page][token][head][D]; */
+    int64_t cache_token_stride;   /*   multiples of 16 bytes, no two places of  */
+    int64_t cache_head_stride;    /*   a page and no two pages overlapping      */
+    int64_t q_in_row_stride;      /* elements from a row to the next; 0: dense; */
+    int64_t k_row_stride;         /*   multiples of 16 bytes.  Append: q_in, k, v, */
+    int64_t v_row_stride;         /*   and q (q_out); attention: q              */
+    int64_t q_row_stride;
+    const uint64_t* rope_turns;   /* append: device [rotary_dim / 2]            */
+} kda_paged_params;
+
+/*
+ * Writes new rows' keys, rotated, and values to the cache, and their rotated
+ * queries to q_out.  Sequence s owns rows cu_seqlens[s] .. cu_seqlens[s+1]-1
+ * (decode: row s), which are its last tokens: kv_lens[s] (device int32 [N])
+ * counts its tokens with them.  The r-th of n rows is token kv_lens[s] - n + r.
+ *   kv_lens[s] < 0: padding, the sequence is skipped.  kv_lens[s] above
+ *       pages_per_seq * page_size: flagged (KDA_DEV_BAD_SEQLENS), skipped.  A row
+ *       before token 0 (more rows than kv_lens[s]): flagged, the row skipped.
+ *   A page that is negative or >= num_pages: flagged (KDA_DEV_BAD_PAGE), the row skipped.
+ *   positions: device int32 [T], nullable: the positions that rows turn to
+ *       (default: their token).
+ *   k: [T][Hkv][D], v: [T][Hkv][D], q: [T][Hq][D], nullable with q_out; q_out may
+ *       be q itself (with the same stride), other overlaps of what is written
+ *       with an input are KDA_ERR_INVALID_ARGUMENT.  rotary_dim = 0: no rotation.
+ * Rows of one call go to distinct places of the cache.
+ */
+KDA_API int kda_paged_append_varlen(const kda_paged_params* p, const int32_t* cu_seqlens, int32_t N, int32_t T,
+                                    const int32_t* kv_lens, const int32_t* pages, const int32_t* positions,
+                                    const void* q, const void* k, const void* v, void* q_out, void* k_cache,
+                                    void* v_cache, int32_t* dev_status, cudaStream_t stream);
+/* One row per sequence. */
+KDA_API int kda_paged_append_decode(const kda_paged_params* p, int32_t B, const int32_t* kv_lens, const int32_t* pages,
+                                    const int32_t* positions, const void* q, const void* k, const void* v, void* q_out,
+                                    void* k_cache, void* v_cache, int32_t* dev_status, cudaStream_t stream);
+
+/*
+ * Attention of new rows over their sequences' cached tokens (their own
+ * appended before): with p the token of a row (as in the append),
+ *     o = sum_j w_j v_j / sum_j w_j,  w_j = e^(scale q.k_j)
+ * over tokens j <= p (causal), j > p - window (window > 0), or all
+ * j < kv_lens[s] (causal = 0).  A row that sees none gives o = 0.
+ *   out: dense [T][Hq][D]; lse: fp32 [T][Hq], nullable: log sum_j w_j (-inf for
+ *       a row that sees none), for joining with attention over other tokens.
+ *   A sequence with kv_lens[s] < 0 is skipped; above pages_per_seq *
+ *       page_size, or with bad cu_seqlens, it is flagged (KDA_DEV_BAD_SEQLENS)
+ *       and skipped; out and lse keep what they held.
+ *   A page that is negative or >= num_pages hides its tokens, as if they were not
+ *       there, and is flagged (KDA_DEV_BAD_PAGE).  Pages wholly before the
+ *       window are not read.
+ *   Products take the rows' type and sum in fp32; weights are fp32 and, for bf16
+ *       rows of a chunk, rounded to bf16 where they meet the values (single tokens:
+ *       in two bf16 parts).
+ *   Whatever lies in the cache's places past a sequence's tokens has no
+ *       effect.  A NaN or an infinity in a query or key reaches rows that
+ *       see it, in a value also rows of the same chunk that do not.
+ *   workspace: kda_paged_attn_workspace_bytes(p, N, T) (decode: kda_paged_attn_
+ *       decode_workspace_bytes(p, B)) bytes, contents need no init.  Calls that
+ *       may run at the same time take a workspace each.
+ */
+KDA_API int kda_paged_attn_varlen(const kda_paged_params* p, const int32_t* cu_seqlens, int32_t N, int32_t T,
+                                  const int32_t* kv_lens, const int32_t* pages, const void* q, const void* k_cache,
+                                  const void* v_cache, void* out, float* lse, void* workspace, size_t ws_bytes,
+                                  int32_t* dev_status, cudaStream_t stream);
+KDA_API size_t kda_paged_attn_workspace_bytes(const kda_paged_params* p, int32_t N, int32_t T);
+/* One row per sequence, its newest token (causal or not gives the same). */
+KDA_API int kda_paged_attn_decode(const kda_paged_params* p, int32_t B, const int32_t* kv_lens, const int32_t* pages,
+                                  const void* q, const void* k_cache, const void* v_cache, void* out, float* lse,
+                                  void* workspace, size_t ws_bytes, int32_t* dev_status, cudaStream_t stream);
+KDA_API size_t kda_paged_attn_decode_workspace_bytes(const kda_paged_params* p, int32_t B);
 
 /* Human-readable name of a return code. */
 KDA_API const char* kda_status_string(int status);

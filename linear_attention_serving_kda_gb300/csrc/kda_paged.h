@@ -1,0 +1,65 @@
+// kda_paged.h -- what the kernels of softmax attention over a paged cache share.
+#pragma once
+
+#include <cudaTypedefs.h>
+
+#include "kda_check.h"
+#include "kda_common.cuh"
+
+namespace kda {
+
+struct PagedArgs {
+    int Hq, Hkv, G, D, N, T;
+    int page_shift, num_pages, width;  // width: entries of a sequence's row of `pages`
+    int causal, window;
+    float scale;
+    long long page_stride, token_stride, head_stride, q_stride;  // elements
+    const int32_t* cu_seqlens;  // null: sequence s owns row s
+    const int32_t* kv_lens;
+    const int32_t* pages;
+    const void* q;
+    const void* k;
+    const void* v;
+    void* out;
+    float* lse;
+    void* workspace;
+    int32_t* dev_status;
+};
+
+// Tokens that a row of the table can name.
+__device__ __forceinline__ long long paged_capacity(const PagedArgs& a) { return (long long)a.width << a.page_shift; }
+
+// The rows begin .. end - 1 of sequence s and its tokens, checked; false when it is skipped (with
+// the fault in *fault).
+__device__ __forceinline__ bool paged_seq(const PagedArgs& a, int s, int& begin, int& end, int& kv, int* fault)
+{
+    begin = s;
+    end = s + 1;
+    if (a.cu_seqlens) {
+        begin = a.cu_seqlens[s];
+        end = a.cu_seqlens[s + 1];
+        if (begin < 0 || end < begin || end > a.T) {
+            *fault |= KDA_DEV_BAD_SEQLENS;
+            return false;
+        }
+    }
+    kv = a.kv_lens[s];
+    if (kv > paged_capacity(a)) {
+        *fault |= KDA_DEV_BAD_SEQLENS;
+        return false;
+    }
+    return kv >= 0 && end > begin;
+}
+
+// Attention of chunks: fp32 rows and bf16 rows; of single tokens: bf16 rows (fp32 ones run as chunks).
+cudaError_t launch_paged_f32(const PagedArgs& a, cudaStream_t st);
+size_t paged_f32_workspace_bytes(const PagedArgs& a);
+cudaError_t launch_paged_bf16(const PagedArgs& a, cudaStream_t st);
+size_t paged_bf16_workspace_bytes(const PagedArgs& a);
+cudaError_t launch_paged_token(const PagedArgs& a, cudaStream_t st);
+size_t paged_token_workspace_bytes(const PagedArgs& a);
+
+// The driver's encoder of tensor maps, null where it has none (kda_chunk.cu).
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
+
+}  // namespace kda

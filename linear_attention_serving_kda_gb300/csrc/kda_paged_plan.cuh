@@ -1,0 +1,239 @@
+// kda_paged_plan.cuh -- how the rows of an attention call are cut into work, and
+// how the parts of a long row's tokens are joined.
+//
+// The rows of a sequence that share a key head (its tokens times the G query heads of the
+// group, token after token) are cut into tiles; a tile's tokens are those that any of its rows
+// sees.  One CTA takes all of a tile's tokens where there are tiles enough; few rows over many tokens are
+// cut along the tokens as well, into items of about half a CTA's share of the whole, and
+// joined afterwards.  Only the GPU knows the lengths, so a kernel of one CTA writes the items, longest first.
+#pragma once
+
+#include "kda_paged.h"
+#include "kda_ptx.cuh"
+
+namespace kda {
+namespace paged {
+
+struct Item {
+    int begin, seq;         // first row of the sequence; its number
+    int row0, rows;         // rows of the tile, counted over tokens and heads of the group
+    int pos0;               // token of the sequence's first row
+    int k0, k1;             // tokens of this item; k0 starts a page or a tile of one
+    int part;               // -1: the whole tile, else where its sums go
+};
+struct Joined {
+    int begin, row0, rows, part, parts;
+};
+struct Head {
+    int items, joined, parts, pad;
+};
+
+struct Plan {
+    int rows;      // of a tile
+    int keys;      // of a tile
+    int ctas;      // that share the work
+    int max_items, max_joined, max_parts;
+    int part_rows; // rows kept of a part
+    Head* head;
+    Item* items;
+    Joined* joined;
+    float* o;      // [parts][Hkv][part_rows][D], not divided by the weights' sum
+    float2* ml;    // [parts][Hkv][part_rows]: largest score (in powers of two), sum of the weights
+};
+
+constexpr int LEAST = 2;  // key tiles of an item, at least
+
+inline size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+
+// Bounds and places in the workspace.  A tile cut into parts has more than one item's length L of key
+// tiles, so it has at most 2 cost / L parts, and L >= total / (2 ctas): 4 ctas parts over all key heads.
+inline size_t lay_out(Plan& p, const PagedArgs& a, int rows, int keys, int ctas)
+{
+    p.rows = rows;
+    p.keys = keys;
+    p.ctas = ctas;
+    const int64_t tiles = ((int64_t)a.T * a.G + rows - 1) / rows + std::min(a.N, a.T);
+    p.max_parts = 4 * ctas / a.Hkv + 2;
+    p.max_joined = p.max_parts / 2 + 1;
+    p.max_items = (int)(tiles + p.max_parts);
+    p.part_rows = (int)std::min<int64_t>(rows, (int64_t)a.T * a.G);
+    unsigned char* w = static_cast<unsigned char*>(a.workspace);
+    size_t at = 0;
+    const auto take = [&](size_t n) {
+        unsigned char* x = w ? w + at : nullptr;
+        at += align256(n);
+        return x;
+    };
+    p.head = reinterpret_cast<Head*>(take(sizeof(Head)));
+    p.items = reinterpret_cast<Item*>(take(sizeof(Item) * (size_t)p.max_items));
+    p.joined = reinterpret_cast<Joined*>(take(sizeof(Joined) * (size_t)p.max_joined));
+    const size_t part = (size_t)p.max_parts * a.Hkv * p.part_rows;
+    p.ml = reinterpret_cast<float2*>(take(part * sizeof(float2)));
+    p.o = reinterpret_cast<float*>(take(part * a.D * sizeof(float)));
+    return at;
+}
+
+// Tokens that rows row0 .. row0 + rows - 1 see: [lo, hi), lo down to the start of a page or of a tile of `keys` in it.
+__device__ __forceinline__ void span(const PagedArgs& a, int keys, int pos0, int kv, int row0, int rows, int& lo, int& hi)
+{
+    lo = 0;
+    hi = kv;
+    if (!a.causal) return;
+    const long long p0 = (long long)pos0 + row0 / a.G, p1 = (long long)pos0 + (row0 + rows - 1) / a.G;
+    hi = (int)max(0ll, min((long long)kv, p1 + 1));
+    if (a.window) {
+        const int unit = min(keys, 1 << a.page_shift);
+        lo = (int)min((long long)hi, max(0ll, p0 - a.window + 1)) & ~(unit - 1);
+    }
+}
+
+constexpr int PT = 1024;
+constexpr int BUCKETS = 512;
+
+// f(begin, seq, row0, rows, pos0, lo, hi) for every tile, by one thread each.  Few sequences: the CTA takes the tiles
+// of one after the other; many: a warp each.
+template <class F> __device__ void each_tile(const PagedArgs& a, const Plan& p, int* fault, F&& f)
+{
+    const int lane = threadIdx.x & 31;
+    const bool wide = a.N <= 16;
+    const int team = wide ? PT : 32, who = wide ? threadIdx.x : lane, step = wide ? 1 : PT / 32;
+    // sequences first .. first + 31 * step are looked up at a time, one by each lane
+    for (long long first = wide ? 0 : threadIdx.x >> 5; first < a.N; first += 32 * step) {
+        int begin = 0, end = 0, kv = 0, ok = 0;
+        const long long mine = first + (long long)lane * step;
+        if (mine < a.N) ok = paged_seq(a, (int)mine, begin, end, kv, fault);
+        uint32_t left = __ballot_sync(0xffffffffu, ok);
+        while (left) {
+            const int l = __ffs(left) - 1;
+            left &= left - 1;
+            const int b = __shfl_sync(0xffffffffu, begin, l), n = __shfl_sync(0xffffffffu, end, l) - b, t = __shfl_sync(0xffffffffu, kv, l);
+            const int all = n * a.G;
+            for (long long r = (long long)who * p.rows; r < all; r += (long long)team * p.rows) {
+                const int rows = min(p.rows, all - (int)r);
+                int lo, hi;
+                span(a, p.keys, t - n, t, (int)r, rows, lo, hi);
+                f(b, (int)(first + (long long)l * step), (int)r, rows, t - n, lo, hi);
+            }
+        }
+    }
+}
+
+__global__ void __launch_bounds__(PT) plan_kernel(const PagedArgs a, const Plan p)
+{
+    ptx::grid_launch_dependents();
+    ptx::grid_dependency_wait();
+    __shared__ unsigned long long total;
+    __shared__ int longest, bucket[BUCKETS], njoined, nparts, sums[PT / 32], all_faults;
+    const int tid = threadIdx.x;
+    if (tid == 0) {
+        total = 0;
+        longest = njoined = nparts = all_faults = 0;
+    }
+    for (int i = tid; i < BUCKETS; i += PT) bucket[i] = 0;
+    __syncthreads();
+    const auto cost = [&](int lo, int hi) { return max(1, (hi - lo + p.keys - 1) / p.keys); };
+    {
+        long long sum = 0;
+        int most = 0, fault = 0;
+        each_tile(a, p, &fault, [&](int, int, int, int, int, int lo, int hi) {
+            const int c = cost(lo, hi);
+            sum += c;
+            most = max(most, c);
+        });
+        if (fault) atomicOr(&all_faults, fault);
+        if (sum) {
+            atomicAdd(&total, (unsigned long long)sum);
+            atomicMax(&longest, most);
+        }
+    }
+    __syncthreads();
+    if (tid == 0 && all_faults) flag_status(a.dev_status, all_faults);
+    const unsigned long long share = total * a.Hkv / (2u * p.ctas) + 1;
+    const int L = (int)min((unsigned long long)INT32_MAX, max((unsigned long long)LEAST, share));
+    const int top = min(L, longest);
+    const auto bucket_of = [&](int c) { return (int)((long long)(top - min(c, top)) * (BUCKETS - 1) / max(top, 1)); };
+    int dummy = 0;
+    each_tile(a, p, &dummy, [&](int, int, int, int, int, int lo, int hi) {
+        const int c = cost(lo, hi), parts = (c + L - 1) / L;
+        atomicAdd(&bucket[bucket_of((c + parts - 1) / parts)], parts);
+    });
+    __syncthreads();
+    // where each bucket begins
+    int mine = tid < BUCKETS ? bucket[tid] : 0, before = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, before, o);
+        if ((tid & 31) >= o) before += x;
+    }
+    if ((tid & 31) == 31) sums[tid >> 5] = before;
+    __syncthreads();
+    for (int w = 0; w < (tid >> 5); ++w) before += sums[w];
+    if (tid == BUCKETS - 1) p.head->items = before;
+    if (tid < BUCKETS) bucket[tid] = before - mine;
+    __syncthreads();
+    each_tile(a, p, &dummy, [&](int begin, int seq, int row0, int rows, int pos0, int lo, int hi) {
+        const int c = cost(lo, hi), parts = (c + L - 1) / L, each = (c + parts - 1) / parts;
+        const int at = atomicAdd(&bucket[bucket_of(each)], parts);
+        int part = -1;
+        if (parts > 1) {
+            part = atomicAdd(&nparts, parts);
+            p.joined[atomicAdd(&njoined, 1)] = {begin, row0, rows, part, parts};
+        }
+        for (int i = 0; i < parts; ++i) {
+            // part i's key tiles: c * i / parts and on, none of them empty
+            const int t0 = (int)((long long)c * i / parts), t1 = (int)((long long)c * (i + 1) / parts);
+            Item it;
+            it.begin = begin; it.seq = seq; it.row0 = row0; it.rows = rows; it.pos0 = pos0;
+            it.k0 = lo + t0 * p.keys;
+            it.k1 = min(hi, lo + t1 * p.keys);
+            it.part = parts > 1 ? part + i : -1;
+            p.items[at + i] = it;
+        }
+    });
+    __syncthreads();
+    if (tid == 0) {
+        p.head->joined = njoined;
+        p.head->parts = nparts;
+    }
+}
+
+// Rows whose tokens were cut into parts: a warp a row, its lanes over the head's channels.
+constexpr int JT = 256;
+template <typename IO, int D> __global__ void __launch_bounds__(JT) join_kernel(const PagedArgs a, const Plan p)
+{
+    ptx::grid_launch_dependents();
+    ptx::grid_dependency_wait();
+    constexpr int PER = D / 32;
+    const int lane = threadIdx.x & 31;
+    const long long rows = (long long)p.head->joined * a.Hkv * p.part_rows;
+    for (long long i = (long long)blockIdx.x * (JT / 32) + (threadIdx.x >> 5); i < rows; i += (long long)gridDim.x * (JT / 32)) {
+        const int r = (int)(i % p.part_rows), h = (int)(i / p.part_rows % a.Hkv);
+        const Joined j = p.joined[i / p.part_rows / a.Hkv];
+        if (r >= j.rows) continue;
+        const size_t first = ((size_t)j.part * a.Hkv + h) * p.part_rows + r, step = (size_t)a.Hkv * p.part_rows;
+        float m = -INFINITY;
+        for (int s = lane; s < j.parts; s += 32) m = fmaxf(m, p.ml[first + s * step].x);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float base = m == -INFINITY ? 0.f : m;
+        float l = 0.f, o[PER] = {};
+#pragma unroll 4
+        for (int s = 0; s < j.parts; ++s) {
+            const float2 ml = p.ml[first + s * step];
+            const float f = exp2f(ml.x - base);
+            l += f * ml.y;
+            const float* x = p.o + (first + s * step) * D;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) o[e] = fmaf(f, x[e * 32 + lane], o[e]);
+        }
+        const int f = j.row0 + r, head = h * a.G + f % a.G;
+        const size_t row = (size_t)(j.begin + f / a.G) * a.Hq + head;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) stv(static_cast<IO*>(a.out) + row * D + e * 32 + lane, l == 0.f ? 0.f : o[e] * inv);
+        if (a.lse && lane == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+    }
+}
+
+}  // namespace paged
+}  // namespace kda

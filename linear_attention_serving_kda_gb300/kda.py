@@ -26,6 +26,7 @@ KDA_DEV_BAD_SEQLENS = 1
 KDA_DEV_BAD_SLOT = 2
 KDA_DEV_BAD_ACCEPTED = 4
 KDA_DEV_TIMEOUT = 8
+KDA_DEV_BAD_PAGE = 16
 KDA_ACT_EXP = 0
 KDA_ACT_RCP = 1
 KDA_ACT_SIGMOID = 2
@@ -39,6 +40,14 @@ KDA_NORM_GATE_SIGMOID = 1
 KDA_NORM_GATE_SILU = 2
 KDA_MAX_POOL_SLOTS = 262144
 KDA_MAX_ROWS = 2147483000
+KDA_ROPE_SCALE_NONE = 0
+KDA_ROPE_SCALE_LINEAR = 1
+KDA_ROPE_SCALE_BASE = 2
+KDA_ROPE_SCALE_RAMP = 3
+KDA_ROPE_SCALE_SMOOTH = 4
+KDA_ROPE_HALF = 0
+KDA_ROPE_PAIRS = 1
+KDA_ROPE_MAX_DIM = 512
 
 
 class kda_params(ctypes.Structure):
@@ -87,6 +96,34 @@ class kda_slot_pool(ctypes.Structure):
     ]
 
 
+class kda_rope_scaling(ctypes.Structure):
+    _fields_ = [
+        ("base", ctypes.c_double), ("factor", ctypes.c_double), ("length", ctypes.c_double),
+        ("fast", ctypes.c_double), ("slow", ctypes.c_double), ("kind", ctypes.c_int32),
+    ]
+
+
+class kda_rope_params(ctypes.Structure):
+    _fields_ = [
+        ("num_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("io_dtype", ctypes.c_int32),
+        ("rotary_dim", ctypes.c_int32), ("rope_layout", ctypes.c_int32), ("transpose", ctypes.c_int32),
+        ("rope_amplitude", ctypes.c_float), ("x_row_stride", ctypes.c_int64), ("y_row_stride", ctypes.c_int64),
+        ("rope_turns", ctypes.c_void_p),
+    ]
+
+
+class kda_paged_params(ctypes.Structure):
+    _fields_ = [
+        ("num_heads_q", ctypes.c_int32), ("num_heads_kv", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+        ("io_dtype", ctypes.c_int32), ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+        ("pages_per_seq", ctypes.c_int32), ("causal", ctypes.c_int32), ("window", ctypes.c_int32),
+        ("rotary_dim", ctypes.c_int32), ("rope_layout", ctypes.c_int32), ("rope_amplitude", ctypes.c_float),
+        ("scale", ctypes.c_float), ("cache_page_stride", ctypes.c_int64), ("cache_token_stride", ctypes.c_int64),
+        ("cache_head_stride", ctypes.c_int64), ("q_in_row_stride", ctypes.c_int64), ("k_row_stride", ctypes.c_int64),
+        ("v_row_stride", ctypes.c_int64), ("q_row_stride", ctypes.c_int64), ("rope_turns", ctypes.c_void_p),
+    ]
+
+
 _VP = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _SIG = {
@@ -121,6 +158,16 @@ _SIG = {
     "kda_slots_copy": (ctypes.c_int, [ctypes.POINTER(kda_slot_pool), _I32] + [_VP] * 4),
     "kda_slots_zero": (ctypes.c_int, [ctypes.POINTER(kda_slot_pool), _I32] + [_VP] * 3),
     "kda_slots_compact_plan": (ctypes.c_int, [ctypes.POINTER(kda_slot_pool)] + [_VP] * 5),
+    "kda_rope_turns": (ctypes.c_int, [ctypes.POINTER(kda_rope_scaling), _I32, _VP, _VP]),
+    "kda_rope": (ctypes.c_int, [ctypes.POINTER(kda_rope_params), ctypes.c_int64] + [_VP] * 4),
+    "kda_paged_append_varlen": (ctypes.c_int, [ctypes.POINTER(kda_paged_params), _VP, _I32, _I32] + [_VP] * 11),
+    "kda_paged_append_decode": (ctypes.c_int, [ctypes.POINTER(kda_paged_params), _I32] + [_VP] * 11),
+    "kda_paged_attn_varlen": (ctypes.c_int, [ctypes.POINTER(kda_paged_params), _VP, _I32, _I32] + [_VP] * 8 +
+                              [ctypes.c_size_t, _VP, _VP]),
+    "kda_paged_attn_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(kda_paged_params), _I32, _I32]),
+    "kda_paged_attn_decode": (ctypes.c_int, [ctypes.POINTER(kda_paged_params), _I32] + [_VP] * 8 +
+                              [ctypes.c_size_t, _VP, _VP]),
+    "kda_paged_attn_decode_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(kda_paged_params), _I32]),
     "kda_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "kda_abi_version": (ctypes.c_int, []),
 }
@@ -271,6 +318,82 @@ class SlotPool:
     def c_struct(self) -> kda_slot_pool:
         return kda_slot_pool(pool=_ptr(self.pool), layer_stride_bytes=self.layer_stride_bytes,
                              slot_bytes=self.slot_bytes, num_layers=self.num_layers, num_slots=self.num_slots)
+
+
+@dataclass
+class RopeScaling:
+    """Angles of rotary positions and their scaling for long contexts (kda_rope_scaling)."""
+
+    kind: int = KDA_ROPE_SCALE_NONE
+    base: float = 10000.0
+    factor: float = 1.0
+    length: float = 4096.0
+    fast: float = 32.0
+    slow: float = 1.0
+
+    def c_struct(self) -> kda_rope_scaling:
+        return kda_rope_scaling(base=self.base, factor=self.factor, length=self.length, fast=self.fast, slow=self.slow,
+                                kind=self.kind)
+
+
+@dataclass
+class RopeParams:
+    """Rotation of the heads of rows (kda_rope_params)."""
+
+    num_heads: int
+    head_dim: int
+    rotary_dim: int
+    rope_turns: object
+    rope_layout: int = KDA_ROPE_HALF
+    rope_amplitude: float = 1.0
+    transpose: bool = False
+    io_dtype: int = KDA_DTYPE_BF16
+    x_row_stride: int = 0
+    y_row_stride: int = 0
+
+    def c_struct(self) -> kda_rope_params:
+        return kda_rope_params(
+            num_heads=self.num_heads, head_dim=self.head_dim, io_dtype=self.io_dtype, rotary_dim=self.rotary_dim,
+            rope_layout=self.rope_layout, transpose=int(self.transpose), rope_amplitude=self.rope_amplitude,
+            x_row_stride=self.x_row_stride, y_row_stride=self.y_row_stride, rope_turns=_ptr(self.rope_turns))
+
+
+@dataclass
+class PagedParams:
+    """Heads of softmax attention and their paged cache (kda_paged_params)."""
+
+    num_heads_q: int
+    num_heads_kv: int
+    head_dim: int
+    page_size: int
+    num_pages: int
+    pages_per_seq: int
+    io_dtype: int = KDA_DTYPE_BF16
+    causal: bool = True
+    window: int = 0
+    scale: float = 1.0
+    rotary_dim: int = 0
+    rope_layout: int = KDA_ROPE_HALF
+    rope_amplitude: float = 1.0
+    rope_turns: object = None
+    cache_page_stride: int = 0
+    cache_token_stride: int = 0
+    cache_head_stride: int = 0
+    q_in_row_stride: int = 0
+    k_row_stride: int = 0
+    v_row_stride: int = 0
+    q_row_stride: int = 0
+
+    def c_struct(self) -> kda_paged_params:
+        return kda_paged_params(
+            num_heads_q=self.num_heads_q, num_heads_kv=self.num_heads_kv, head_dim=self.head_dim,
+            io_dtype=self.io_dtype, page_size=self.page_size, num_pages=self.num_pages,
+            pages_per_seq=self.pages_per_seq, causal=int(self.causal), window=self.window, rotary_dim=self.rotary_dim,
+            rope_layout=self.rope_layout, rope_amplitude=self.rope_amplitude, scale=self.scale,
+            cache_page_stride=self.cache_page_stride, cache_token_stride=self.cache_token_stride,
+            cache_head_stride=self.cache_head_stride, q_in_row_stride=self.q_in_row_stride,
+            k_row_stride=self.k_row_stride, v_row_stride=self.v_row_stride, q_row_stride=self.q_row_stride,
+            rope_turns=_ptr(self.rope_turns))
 
 
 def _ptr(t):
@@ -439,6 +562,57 @@ def kda_slots_compact_plan(pool: SlotPool, live, src, dst, remap, stream=None) -
     """The moves (for kda_slots_copy) that close the holes of a pool."""
     return load().kda_slots_compact_plan(ctypes.byref(pool.c_struct()), _ptr(live), _ptr(src), _ptr(dst), _ptr(remap),
                                          _stream(stream))
+
+
+def kda_rope_turns(scaling: RopeScaling, rotary_dim: int, radians, turns) -> int:
+    """Angles of rotary_dim / 2 pairs per position, as the kernels take them, into a host tensor of 64-bit integers
+    (radians: a host tensor of doubles, or None)."""
+    return load().kda_rope_turns(ctypes.byref(scaling.c_struct()), rotary_dim, _ptr(radians), _ptr(turns))
+
+
+def kda_rope(params: RopeParams, rows: int, positions, x, y, stream=None) -> int:
+    """Rotary positions on the heads of rows, or the gradient of that."""
+    return load().kda_rope(ctypes.byref(params.c_struct()), rows, _ptr(positions), _ptr(x), _ptr(y), _stream(stream))
+
+
+def kda_paged_append_varlen(params: PagedParams, cu_seqlens, N: int, T: int, kv_lens, pages, positions, q, k, v, q_out,
+                            k_cache, v_cache, dev_status=None, stream=None) -> int:
+    """Prompt rows' rotated keys and values into the paged cache, their rotated queries to q_out."""
+    return load().kda_paged_append_varlen(
+        ctypes.byref(params.c_struct()), _ptr(cu_seqlens), N, T, _ptr(kv_lens), _ptr(pages), _ptr(positions), _ptr(q),
+        _ptr(k), _ptr(v), _ptr(q_out), _ptr(k_cache), _ptr(v_cache), _ptr(dev_status), _stream(stream))
+
+
+def kda_paged_append_decode(params: PagedParams, B: int, kv_lens, pages, positions, q, k, v, q_out, k_cache, v_cache,
+                            dev_status=None, stream=None) -> int:
+    """The same for one row per sequence."""
+    return load().kda_paged_append_decode(
+        ctypes.byref(params.c_struct()), B, _ptr(kv_lens), _ptr(pages), _ptr(positions), _ptr(q), _ptr(k), _ptr(v),
+        _ptr(q_out), _ptr(k_cache), _ptr(v_cache), _ptr(dev_status), _stream(stream))
+
+
+def kda_paged_attn_workspace_bytes(params: PagedParams, N: int, T: int) -> int:
+    return load().kda_paged_attn_workspace_bytes(ctypes.byref(params.c_struct()), N, T)
+
+
+def kda_paged_attn_varlen(params: PagedParams, cu_seqlens, N: int, T: int, kv_lens, pages, q, k_cache, v_cache, out,
+                          lse=None, workspace=None, ws_bytes: int = 0, dev_status=None, stream=None) -> int:
+    """Attention of chunks of new rows over their sequences' pages."""
+    return load().kda_paged_attn_varlen(
+        ctypes.byref(params.c_struct()), _ptr(cu_seqlens), N, T, _ptr(kv_lens), _ptr(pages), _ptr(q), _ptr(k_cache),
+        _ptr(v_cache), _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes, _ptr(dev_status), _stream(stream))
+
+
+def kda_paged_attn_decode_workspace_bytes(params: PagedParams, B: int) -> int:
+    return load().kda_paged_attn_decode_workspace_bytes(ctypes.byref(params.c_struct()), B)
+
+
+def kda_paged_attn_decode(params: PagedParams, B: int, kv_lens, pages, q, k_cache, v_cache, out, lse=None,
+                          workspace=None, ws_bytes: int = 0, dev_status=None, stream=None) -> int:
+    """Attention of one new row per sequence over its pages."""
+    return load().kda_paged_attn_decode(
+        ctypes.byref(params.c_struct()), B, _ptr(kv_lens), _ptr(pages), _ptr(q), _ptr(k_cache), _ptr(v_cache),
+        _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes, _ptr(dev_status), _stream(stream))
 
 
 class Prepared:
