@@ -1,0 +1,479 @@
+// kda_paged_bf16.cu -- attention of chunks of bf16 rows over a paged cache on the tensor cores.
+//
+// A CTA holds one or two tiles of 128 rows (tokens times the heads that share a key head) and goes through its
+// tokens KEYS at a time:
+//     S = Q K^T            tcgen05, Q and K from shared memory, S in TMEM
+//     W = 2^(c S - m)      a thread a row: c = scale log2 e, m the row's running maximum of c S
+//     O = O + W V          tcgen05, W (bf16) from TMEM where S lay, V from shared memory, O in TMEM
+// m lags behind the true maximum by up to 2^8 (the weights stay within fp32 and bf16 by far), so
+// that O is rarely rescaled; the sum of the weights is fp32, of the weights before their rounding.
+// The two tiles' products and exponentials alternate: while one tile's scores are exponentiated, the tensor
+// cores work for the other; with one tile, two steps of it do.
+#include <cuda.h>
+
+#include "kda_paged_plan.cuh"
+
+namespace kda {
+namespace {
+
+using namespace paged;
+
+constexpr int THREADS = 384;  // two softmax warpgroups, a warp that issues products, one that loads, two without work
+constexpr uint32_t WAIT = 1u << 22;
+constexpr float LAG = 8.f;
+
+template <int DP> struct Shape {
+    static constexpr int TILES = DP == 256 ? 1 : 2;    // tiles of 128 rows: TMEM holds 512 columns, O takes DP of them a tile
+    static constexpr int KEYS = DP == 256 ? 64 : 128;
+    static constexpr int BLOCKS = DP / 64;             // 128-byte pieces of a row
+    static constexpr int SLOT = KEYS * DP * 2;
+    static constexpr int SLOTS = DP == 64 ? 8 : 5;
+    static constexpr int Q = TILES * 128 * DP * 2;
+    struct Smem {
+        unsigned char q[Q];
+        unsigned char ring[SLOTS * SLOT];
+        uint64_t full[SLOTS], empty[SLOTS], scores[2], weights[2], product[2], rows[2], taken[2], drained;
+        uint32_t hidden[8], tmem, dead;
+    };
+};
+
+// Shared-memory descriptor of a matrix whose rows (of the product's inner dimension) hold 64 values of the outer one in
+// 128 swizzled bytes: `lead` bytes from a block of 64 outer values to the next.
+__device__ __forceinline__ uint64_t desc_outer_sw128(uint32_t saddr, uint32_t lead)
+{
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)(lead >> 4) << 16;
+    d |= (uint64_t)(1024 >> 4) << 32;  // eight inner values on
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+
+__device__ __forceinline__ void mma_ss_if(uint32_t leader, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, int x, int y, int z, int w, uint64_t* bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+            ptx::smem_u32(dst)),
+        "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w), "r"(ptx::smem_u32(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+// the n lowest bits, none for n <= 0, all for n >= 32
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Steps of an item: with two tiles, step s is tile s & 1 over tokens s >> 1; with one, tokens s.  Step s uses S's
+// buffer s & 1.  Everyone counts the phases of every barrier alike from the items themselves.
+struct Work {
+    Item it;
+    int h, n, tiles, steps;  // key head, tiles of tokens, tiles of rows
+};
+
+template <int DP> __device__ __forceinline__ Work work_of(const PagedArgs& a, const Plan& p, int x)
+{
+    Work w;
+    w.it = p.items[x / a.Hkv];
+    w.h = x % a.Hkv;
+    w.n = (w.it.k1 - w.it.k0 + Shape<DP>::KEYS - 1) / Shape<DP>::KEYS;
+    w.tiles = w.it.rows > 128 ? 2 : 1;
+    w.steps = w.n * w.tiles;
+    return w;
+}
+
+template <int DP, int D> __global__ void __launch_bounds__(THREADS, 1)
+paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap)
+{
+    using L = Shape<DP>;
+    constexpr int KEYS = L::KEYS, BLOCKS = L::BLOCKS, SLOT = L::SLOT, SLOTS = L::SLOTS;
+    extern __shared__ __align__(1024) unsigned char raw[];
+    auto& s = *reinterpret_cast<typename L::Smem*>(raw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    ptx::grid_launch_dependents();
+    if (tid == 0) {
+        for (int i = 0; i < SLOTS; ++i) {
+            ptx::mbar_init(&s.full[i], 1);
+            ptx::mbar_init(&s.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&s.scores[i], 1);
+            ptx::mbar_init(&s.product[i], 1);
+            ptx::mbar_init(&s.weights[i], 4);
+            ptx::mbar_init(&s.rows[i], 4);
+            ptx::mbar_init(&s.taken[i], 4);
+        }
+        ptx::mbar_init(&s.drained, 1);
+        s.dead = 0;
+        ptx::fence_mbar_init();
+        ptx::fence_proxy_async_smem();
+    }
+    if (warp == 8) ptx::tmem_alloc(&s.tmem, 512);
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&s.tmem);
+    ptx::grid_dependency_wait();
+    const int items = p.head->items * a.Hkv;
+    // A wait that runs out ends the CTA's work: every role leaves its loop at its next wait.
+    const auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (ptx::mbar_wait(bar, parity & 1, WAIT) && !*reinterpret_cast<volatile uint32_t*>(&s.dead)) return true;
+        *reinterpret_cast<volatile uint32_t*>(&s.dead) = 1;
+        return false;
+    };
+    constexpr uint32_t O0 = 256;  // S: columns 0 .. 2 KEYS - 1, O behind
+
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if (warp == 9) {
+            // ---- loads: keys and values in the order in which the products meet them
+            uint32_t use = 0, kt = 0;
+            bool ok = true;
+            const int box = min(KEYS, 1 << a.page_shift), boxes = KEYS / box;
+            for (int x = blockIdx.x; x < items && ok; x += gridDim.x) {
+                const Work w = work_of<DP>(a, p, x);
+                const int ahead = w.tiles == 1 ? 2 : 1;
+                const auto load = [&](const CUtensorMap* map, int j, bool keys) {
+                    const int slot = use % SLOTS, t0 = w.it.k0 + j * KEYS, t = t0 + lane % boxes * box, blk = lane / boxes;
+                    int page = 0;
+                    const bool mine = blk < BLOCKS && t < w.it.k1;
+                    if (mine) page = a.pages[(long long)w.it.seq * a.width + (t >> a.page_shift)];
+                    const bool gone = mine && (page < 0 || page >= a.num_pages);
+                    const uint32_t all = __ballot_sync(0xffffffffu, mine);
+                    uint32_t hide = __ballot_sync(0xffffffffu, gone && blk == 0);
+                    if (!(ok = wait(&s.empty[slot], (use / SLOTS) & 1 ^ 1))) return;
+                    if (lane == 0) {
+                        if (keys) {
+                            s.hidden[kt & 7] = hide;
+                            if (hide) flag_status(a.dev_status, KDA_DEV_BAD_PAGE);
+                        }
+                        ptx::mbar_arrive_expect_tx(&s.full[slot], __popc(all) * box * 128);
+                    }
+                    __syncwarp();
+                    if (mine) {
+                        unsigned char* dst = s.ring + slot * SLOT + blk * (KEYS * 128) + lane % boxes * box * 128;
+                        tma_load_4d(dst, map, blk * 64, t & ((1 << a.page_shift) - 1), w.h, gone ? -1 : page, &s.full[slot]);
+                    }
+                    if (keys) ++kt;
+                    ++use;
+                };
+                for (int j = 0; j < min(ahead, w.n) && ok; ++j) load(&kmap, j, true);
+                for (int j = 0; j < w.n && ok; ++j) {
+                    load(&vmap, j, false);
+                    if (ok && j + ahead < w.n) load(&kmap, j + ahead, true);
+                }
+            }
+            // a CTA that gave up: what is on its way has to land first
+            if (!ok)
+                for (uint32_t u = use > SLOTS ? use - SLOTS : 0; u < use; ++u) ptx::mbar_wait(&s.full[u % SLOTS], (u / SLOTS) & 1, WAIT);
+        } else if (warp == 8) {
+            // ---- products
+            const uint32_t leader = ptx::elect_one();
+            constexpr uint32_t ID_S = ptx::idesc_bf16(128, KEYS), ID_O = ptx::idesc_bf16(128, DP) | (1u << 16);  // V: inner dimension by rows
+            uint32_t use = 0, wcount[2] = {0, 0}, qcount[2] = {0, 0};
+            bool ok = true;
+            const uint32_t qa = ptx::smem_u32(s.q), ring = ptx::smem_u32(s.ring);
+            for (int x = blockIdx.x; x < items && ok; x += gridDim.x) {
+                const Work w = work_of<DP>(a, p, x);
+                if (w.n == 0) continue;
+                const int ahead = w.tiles == 1 ? 2 : 1;
+                // uses of the ring: keys of tile j, values of tile j
+                const auto key_use = [&](int j) { return use + (j < ahead ? j : 2 * j - ahead + 1); };
+                const auto value_use = [&](int j) { return use + (j < w.n - ahead ? ahead + 2 * j : w.n + j); };
+                const auto scores = [&](int st) {
+                    const int t = w.tiles == 2 ? st & 1 : 0, j = w.tiles == 2 ? st >> 1 : st, b = st & 1;
+                    const uint32_t u = key_use(j);
+                    if (t == 0 && !(ok = wait(&s.full[u % SLOTS], u / SLOTS))) return;
+                    if (j == 0 && !(ok = wait(&s.rows[t], qcount[t]))) return;
+                    ptx::tc_fence_after();
+                    const uint64_t da = ptx::desc_sw128(qa + t * (128 * DP * 2)), db = ptx::desc_sw128(ring + u % SLOTS * SLOT);
+#pragma unroll
+                    for (int k = 0; k < DP / 16; ++k)
+                        mma_ss_if(leader, tmem + b * KEYS, da + ((k / 4) * (128 * 128) + (k % 4) * 32) / 16,
+                                  db + ((k / 4) * (KEYS * 128) + (k % 4) * 32) / 16, ID_S, k > 0);
+                    ptx::mma_commit_if(leader, &s.scores[b]);
+                    if (t == w.tiles - 1) ptx::mma_commit_if(leader, &s.empty[u % SLOTS]);
+                };
+                const auto values = [&](int st) {
+                    const int t = w.tiles == 2 ? st & 1 : 0, j = w.tiles == 2 ? st >> 1 : st, b = st & 1;
+                    const uint32_t u = value_use(j);
+                    if (t == 0) {
+                        if (!(ok = wait(&s.full[u % SLOTS], u / SLOTS))) return;
+                        const int have = w.it.k1 - w.it.k0 - j * KEYS;
+                        if (have < KEYS) {  // what lies behind the tokens may be anything: zeros, whose weights are zero
+                            for (int i = lane; i < (KEYS - have) * 8 * BLOCKS; i += 32) {
+                                const int r = have + i / 8 % (KEYS - have), blk = i / (8 * (KEYS - have));
+                                *reinterpret_cast<uint4*>(s.ring + u % SLOTS * SLOT + blk * (KEYS * 128) + r * 128 + i % 8 * 16) = make_uint4(0, 0, 0, 0);
+                            }
+                            ptx::fence_proxy_async_smem();
+                            __syncwarp();
+                        }
+                    }
+                    if (j == 0 && !(ok = wait(&s.taken[t], qcount[t] + 1))) return;  // O of the item before is read
+                    if (!(ok = wait(&s.weights[b], wcount[b]))) return;
+                    ++wcount[b];
+                    ptx::tc_fence_after();
+                    const uint64_t db = desc_outer_sw128(ring + u % SLOTS * SLOT, KEYS * 128);
+#pragma unroll
+                    for (int k = 0; k < KEYS / 16; ++k)
+                        ptx::mma_ts_if(leader, tmem + O0 + t * DP, tmem + b * KEYS + k * 8, db + k * 2048 / 16, ID_O, j > 0 || k > 0);
+                    ptx::mma_commit_if(leader, &s.product[b]);
+                    if (t == w.tiles - 1) ptx::mma_commit_if(leader, &s.empty[u % SLOTS]);
+                };
+                scores(0);
+                if (ok && w.steps > 1) scores(1);
+                for (int st = 0; st < w.steps && ok; ++st) {
+                    values(st);
+                    if (ok && st + 2 < w.steps) scores(st + 2);
+                }
+                use += 2 * w.n;
+                for (int t = 0; t < w.tiles; ++t) ++qcount[t];
+            }
+            // nothing may be on its way when TMEM is freed
+            ptx::mma_commit_if(leader, &s.drained);
+            ptx::mbar_wait(&s.drained, 0, WAIT);
+        }
+    } else {
+        // ---- a thread a row: exponentials, rescaling, outputs
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        const int t = warp >> 2, r = tid & 127;  // tile, row of it
+        const uint32_t tl = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes
+        const float c = a.scale * 1.4426950408889634f;
+        uint32_t scount[2] = {0, 0}, pcount[2] = {0, 0}, kt = 0;
+        bool ok = true;
+        for (int x = blockIdx.x; x < items && ok; x += gridDim.x) {
+            if (t >= L::TILES) break;
+            const Work w = work_of<DP>(a, p, x);
+            const int row = t * 128 + r;
+            const bool mine = t < w.tiles;
+            const bool live = mine && t * 128 + (warp & 3) * 32 < w.it.rows;  // the warp has rows
+            const int f = w.it.row0 + min(row, w.it.rows - 1), tok = f / a.G, head = w.h * a.G + f % a.G;
+            float m = -INFINITY, sum = 0.f;
+            if (mine && w.n > 0) {
+                // the tile's rows to shared memory: 16-byte pieces, permuted within eight rows as the descriptor expects
+                constexpr int PIECES = DP / 8;
+                for (int i = lane; i < 32 * PIECES; i += 32) {
+                    const int rr = (warp & 3) * 32 + i / PIECES, e = i % PIECES, ff = w.it.row0 + t * 128 + rr;
+                    uint4 q = make_uint4(0, 0, 0, 0);
+                    if (t * 128 + rr < w.it.rows && e * 8 < D)
+                        q = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + (w.it.begin + ff / a.G) * a.q_stride +
+                                                            (long long)(w.h * a.G + ff % a.G) * D + e * 8);
+                    *reinterpret_cast<uint4*>(s.q + t * (128 * DP * 2) + e / 8 * (128 * 128) + rr * 128 + ((e % 8) ^ (rr & 7)) * 16) = q;
+                }
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&s.rows[t]);
+                const int pos = w.it.pos0 + tok;
+                const int hi = a.causal ? min(w.it.k1, pos + 1) : w.it.k1;
+                const int lo = a.window ? (int)max(0ll, (long long)pos - a.window + 1) : 0;
+                for (int st = w.tiles == 2 ? t : 0; st < w.steps; st += w.tiles) {
+                    const int j = w.tiles == 2 ? st >> 1 : st, b = st & 1, k0 = w.it.k0 + j * KEYS;
+                    if (!(ok = wait(&s.scores[b], scount[b]))) break;
+                    ++scount[b];
+                    ptx::tc_fence_after();
+                    if (live) {
+                        float v[KEYS];
+                        if constexpr (KEYS == 128) ptx::tmem_ld128(tl + b * KEYS, v);
+                        else ptx::tmem_ld64(tl + b * KEYS, v);
+                        const uint32_t hide = *reinterpret_cast<volatile uint32_t*>(&s.hidden[(kt + j) & 7]);
+                        if (__any_sync(0xffffffffu, k0 + KEYS > hi || k0 < lo) || hide) {
+                            const int box_shift = min(a.page_shift, KEYS == 128 ? 7 : 6);
+#pragma unroll
+                            for (int i = 0; i < KEYS; i += 32) {
+                                uint32_t seen = low_bits(hi - k0 - i) & ~low_bits(lo - k0 - i);
+                                if ((hide >> (i >> box_shift)) & 1) seen &= 0xffff0000u;
+                                if ((hide >> ((i + 16) >> box_shift)) & 1) seen &= 0x0000ffffu;
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) v[i + e] = (seen >> e) & 1 ? v[i + e] : -INFINITY;
+                            }
+                        }
+                        float mx[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) mx[i] = fmaxf(v[2 * i], v[2 * i + 1]);
+#pragma unroll
+                        for (int i = 8; i < KEYS; i += 8)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], v[i + 2 * e], v[i + 2 * e + 1]);
+                        const float most = c * fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                        const bool grow = most > m + LAG || (m == -INFINITY && most > m);
+                        if (__any_sync(0xffffffffu, grow)) {
+                            const float next = grow ? most : m, fac = grow ? exp2_sfu(m - next) : 1.f;
+                            sum *= fac;
+                            if (j > 0) {
+                                // with one tile the step before's product may still run (with two it had to end before these scores began)
+                                if (w.tiles == 1 && !(ok = wait(&s.product[b ^ 1], pcount[b ^ 1] + (st - 1) / 2))) break;
+                                ptx::tc_fence_after();
+#pragma unroll 1
+                                for (int e = 0; e < DP; e += 32) {
+                                    float o[32];
+                                    ptx::tmem_ld32(tl + O0 + t * DP + e, o);
+#pragma unroll
+                                    for (int i = 0; i < 32; ++i) o[i] *= fac;
+                                    ptx::tmem_st32(tl + O0 + t * DP + e, o);
+                                }
+                            }
+                            m = next;
+                        }
+                        const float2 c2 = both2(c), base = both2(m == -INFINITY ? 0.f : -m);
+                        float2 part[2] = {both2(0.f), both2(0.f)};
+#pragma unroll
+                        for (int i = 0; i < KEYS; i += 32) {
+                            uint32_t packed[16];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                float2 y = fma2(make_float2(v[i + 2 * e], v[i + 2 * e + 1]), c2, base);
+                                y.x = exp2_sfu(y.x);
+                                y.y = exp2_sfu(y.y);
+                                part[e & 1] = add2(part[e & 1], y);
+                                packed[e] = pack_bf16(y.x, y.y);
+                            }
+                            ptx::tmem_st16_async(tl + b * KEYS + i / 2, packed);
+                        }
+                        part[0] = add2(part[0], part[1]);
+                        sum += part[0].x + part[0].y;
+                        ptx::tmem_wait_st();
+                    }
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(&s.weights[b]);
+                }
+            }
+            if (!ok) break;
+            kt += w.n;
+            if (mine) {
+                if (w.n > 0) {
+                    const int last = w.tiles == 2 ? w.steps - 2 + t : w.steps - 1, b = last & 1;
+                    if (!(ok = wait(&s.product[b], pcount[b] + last / 2))) break;
+                    ptx::tc_fence_after();
+                }
+                if (live) {
+                    const bool whole = w.it.part < 0, has = row < w.it.rows;
+                    const float inv = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+                    const size_t at = ((size_t)(w.it.begin + tok)) * a.Hq + head;
+                    const size_t slot = ((size_t)max(w.it.part, 0) * a.Hkv + w.h) * p.part_rows + row;
+#pragma unroll 1
+                    for (int e = 0; e < D; e += 32) {
+                        float o[32];
+                        if (w.n > 0) {
+                            ptx::tmem_ld32(tl + O0 + t * DP + e, o);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] = 0.f;
+                        }
+                        if (!has) continue;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = sum == 0.f ? 0.f : o[i] * inv;
+                        if (whole) {
+                            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at * D + e);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                dst[i] = make_uint4(pack_bf16(o[8 * i], o[8 * i + 1]), pack_bf16(o[8 * i + 2], o[8 * i + 3]),
+                                                    pack_bf16(o[8 * i + 4], o[8 * i + 5]), pack_bf16(o[8 * i + 6], o[8 * i + 7]));
+                        } else {
+                            float4* dst = reinterpret_cast<float4*>(p.o + slot * D + e);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                        }
+                    }
+                    if (has) {
+                        if (!whole) p.ml[slot] = make_float2(m, sum);
+                        else if (a.lse) a.lse[at] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994531f;
+                    }
+                }
+                if (w.n > 0) {
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(&s.taken[t]);
+                }
+            }
+            for (int b = 0; b < 2; ++b) pcount[b] += w.tiles == 2 ? w.n : (w.n + 1 - b) / 2;
+            scount[0] = pcount[0];
+            scount[1] = pcount[1];
+            // the other warpgroup, without rows in this item, may not run ahead over phases of barriers that it did not wait for
+            if (L::TILES == 2 && w.tiles == 1) {
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                ok = !*reinterpret_cast<volatile uint32_t*>(&s.dead);
+            }
+        }
+        if (!ok && L::TILES == 2) asm volatile("bar.arrive 1, 256;" ::: "memory");
+        if (!ok && lane == 0) flag_status(a.dev_status, KDA_DEV_TIMEOUT);
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 8) ptx::tmem_dealloc(tmem, 512);
+}
+
+// [num_pages][Hkv][page_size][D] by the cache's strides; boxes of a page's (or a tile's) tokens and 64 channels of one head.
+bool encode_cache(CUtensorMap* m, const void* base, const PagedArgs& a, int keys)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t P = (cuuint64_t)1 << a.page_shift;
+    const cuuint64_t dims[4] = {(cuuint64_t)a.D, P, (cuuint64_t)a.Hkv, (cuuint64_t)a.num_pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)a.token_stride * 2, (cuuint64_t)a.head_stride * 2, (cuuint64_t)a.page_stride * 2};
+    const cuuint32_t box[4] = {64, (cuuint32_t)std::min<cuuint64_t>(P, keys), 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int DP, int D> cudaError_t launch(const PagedArgs& a, cudaStream_t st)
+{
+    using L = Shape<DP>;
+    constexpr int smem = sizeof(typename L::Smem);
+    static_assert(smem <= 227 * 1024, "shared memory");
+    static_assert(offsetof(typename L::Smem, ring) % 1024 == 0 && L::SLOT % 1024 == 0 && offsetof(typename L::Smem, full) % 8 == 0, "alignment");
+    static PerDeviceOnce once;
+    cudaError_t e = once.run([](int) {
+        return cudaFuncSetAttribute(paged_bf16_kernel<DP, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    });
+    if (e != cudaSuccess) return e;
+    CUtensorMap km, vm;
+    if (!encode_cache(&km, a.k, a, L::KEYS) || !encode_cache(&vm, a.v, a, L::KEYS)) return cudaErrorInvalidValue;
+    const int ctas = sm_count();
+    if (ctas <= 0) return cudaErrorInvalidDevice;
+    Plan p;
+    lay_out(p, a, 128 * L::TILES, L::KEYS, 152);
+    e = launch_dependent(plan_kernel, 1, PT, 0, st, a, p);
+    if (e == cudaSuccess) e = launch_dependent(paged_bf16_kernel<DP, D>, ctas, THREADS, smem, st, a, p, km, vm);
+    if (e == cudaSuccess) e = launch_dependent(join_kernel<__nv_bfloat16, D>, 304, JT, 0, st, a, p);
+    return e;
+}
+
+}  // namespace
+
+size_t paged_bf16_workspace_bytes(const PagedArgs& a)
+{
+    Plan p;
+    return a.D == 256 ? lay_out(p, a, 128, 64, 152) : lay_out(p, a, 256, 128, 152);
+}
+
+cudaError_t launch_paged_bf16(const PagedArgs& a, cudaStream_t st)
+{
+    switch (a.D) {
+    case 32: return launch<64, 32>(a, st);
+    case 64: return launch<64, 64>(a, st);
+    case 128: return launch<128, 128>(a, st);
+    default: return launch<256, 256>(a, st);
+    }
+}
+
+}  // namespace kda

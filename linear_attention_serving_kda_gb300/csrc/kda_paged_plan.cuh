@@ -118,7 +118,7 @@ template <class F> __device__ void each_tile(const PagedArgs& a, const Plan& p, 
     }
 }
 
-__global__ void __launch_bounds__(PT) plan_kernel(const PagedArgs a, const Plan p)
+static __global__ void __launch_bounds__(PT) plan_kernel(const PagedArgs a, const Plan p)
 {
     ptx::grid_launch_dependents();
     ptx::grid_dependency_wait();
