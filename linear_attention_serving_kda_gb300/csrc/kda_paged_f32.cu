@@ -228,7 +228,5 @@ size_t paged_f32_workspace_bytes(const PagedArgs& a)
 }
 
 cudaError_t launch_paged_f32(const PagedArgs& a, cudaStream_t st) { return launch_io<float>(a, st); }
-size_t paged_token_workspace_bytes(const PagedArgs& a) { return paged_f32_workspace_bytes(a); }
-cudaError_t launch_paged_token(const PagedArgs& a, cudaStream_t st) { return launch_io<__nv_bfloat16>(a, st); }
 
 }  // namespace kda

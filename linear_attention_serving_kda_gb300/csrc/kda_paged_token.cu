@@ -1,0 +1,549 @@
+// kda_paged_token.cu -- attention of single bf16 rows over a paged cache.
+//
+// Every cached value is read once for the G query heads that share it, so HBM bandwidth is the bound: a row's
+// products are a handful a byte.  All that matters is that every SM keeps loading until the last byte: the tiles of 64
+// tokens of all (sequence, key head) pairs form one line, and each of CTAS CTAs takes an equal stretch of it, whatever the
+// lengths.  A pair within one stretch is written out; one that stretches cut leaves a part in the workspace for each
+// of them, and token_join_kernel adds the parts.
+// A warp loads (tensor copies, a ring of tiles); eight warps, in two teams that take the tiles in turn, hold 16 tokens of a tile
+// each: scores and values by mma.sync with up to 16 heads as rows (a tcgen05 tile would have 128 of them, nearly all empty), weights
+// in two bf16 parts, running maximum and sum of each warp by itself, joined at the pair's end.
+#include <cuda.h>
+
+#include "kda_paged.h"
+#include "kda_ptx.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int CTAS = 152;     // one an SM
+constexpr int KEYS = 64;      // tokens of a tile
+constexpr int ROWS = 16;      // heads of a unit
+constexpr int WARPS = 8;      // consumers
+constexpr int TT = 32 * (WARPS + 1);
+constexpr int KNOWN = 1024;   // sequences whose lengths a CTA keeps
+constexpr uint32_t WAIT = 1u << 22;
+constexpr float LAG = 8.f;
+
+// What the stretches leave for token_join_kernel.
+struct Cut {
+    long long line;            // tiles in all
+    int seq, unit, last;       // the unit that begins in this stretch and ends in that of CTA `last`; seq < 0: none
+    int pad;
+};
+struct TokenWork {
+    Cut* cut;                  // [CTAS]
+    float2* ml;                // [CTAS][2][ROWS]: largest score (in powers of two) and sum of the weights;
+    float* o;                  // [CTAS][2][ROWS][D]   0: of a unit that began before, 1: of the one that goes on
+};
+
+size_t lay_out(TokenWork& w, const PagedArgs& a)
+{
+    unsigned char* p = static_cast<unsigned char*>(a.workspace);
+    size_t at = 0;
+    const auto take = [&](size_t n) {
+        unsigned char* x = p ? p + at : nullptr;
+        at += (n + 255) / 256 * 256;
+        return x;
+    };
+    w.cut = reinterpret_cast<Cut*>(take(sizeof(Cut) * CTAS));
+    w.ml = reinterpret_cast<float2*>(take(sizeof(float2) * CTAS * 2 * ROWS));
+    w.o = reinterpret_cast<float*>(take(sizeof(float) * CTAS * 2 * ROWS * (size_t)a.D));
+    return at;
+}
+
+template <int D> struct Token {
+    static constexpr int DP = D < 64 ? 64 : D, BLOCKS = DP / 64;
+    static constexpr int HALF = KEYS * DP * 2, STAGE = 2 * HALF;  // keys, then values
+    static constexpr int STAGES = D == 256 ? 3 : D == 128 ? 6 : 8;
+    static constexpr int CH = D == 256 ? 16 : 32;
+    struct Smem {
+        unsigned char ring[STAGES * STAGE];
+        unsigned char q[2][ROWS * D * 2];
+        float o[WARPS][ROWS * (CH + 4)];  // CH channels of every warp's sums at a time
+        float2 ml[WARPS][ROWS];
+        uint64_t full[STAGES], empty[STAGES], qfull[2], qempty[2];
+        int kv[KNOWN];                    // lengths from the stretch's first sequence on, -1: skipped
+        long long sum[TT / 32];
+        uint32_t hidden[STAGES];
+        int first, dead;
+        long long offset;
+    };
+};
+
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, int x, int y, int z, int w, uint64_t* bar, uint64_t policy)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(
+            ptx::smem_u32(dst)),
+        "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w), "r"(ptx::smem_u32(bar)), "l"(policy)
+        : "memory");
+}
+
+// Tokens lo .. kv - 1 are seen; tiles count from lo's page (or tile within a page) on.
+struct Span {
+    int lo, start, n;
+    __device__ __forceinline__ Span(const PagedArgs& a, int kv)
+    {
+        lo = a.window && kv > a.window ? kv - a.window : 0;
+        start = lo & ~(min(KEYS, 1 << a.page_shift) - 1);
+        n = kv < 0 ? 0 : max(1, (kv - start + KEYS - 1) / KEYS);
+    }
+};
+
+__device__ __forceinline__ int length_of(const PagedArgs& a, int s, int* fault)
+{
+    int begin, end, kv;
+    return paged_seq(a, s, begin, end, kv, fault) ? kv : -1;
+}
+
+__device__ __forceinline__ long long stretch(long long line, int c) { return line * c / CTAS; }
+__device__ __forceinline__ int owner(long long line, long long x) { return (int)(((x + 1) * CTAS + line - 1) / line) - 1; }
+
+// A CTA's walk along its stretch, unit after unit.
+struct Walk {
+    int s, kv, u;            // sequence, its tokens, unit within it (key head, block of heads)
+    int lo, start, n;        // as in Span
+    int t0, t1;              // tiles of the unit in this stretch
+    long long left;          // tiles of the stretch from t0 on
+};
+
+template <class S> __device__ __forceinline__ void enter(const PagedArgs& a, const S& sm, Walk& w)
+{
+    while (true) {  // sequences without tokens are passed over; one with tokens follows while tiles are left
+        const int i = w.s - sm.first;
+        int f = 0;
+        if (w.s >= a.N) {  // lengths that changed under the call
+            w.left = w.kv = 0;
+            break;
+        }
+        w.kv = i < KNOWN ? sm.kv[i] : length_of(a, w.s, &f);
+        if (w.kv >= 0) break;
+        ++w.s;
+    }
+    const Span x(a, w.kv);
+    w.lo = x.lo;
+    w.start = x.start;
+    w.n = x.n;
+}
+template <class S> __device__ __forceinline__ void begin_walk(const PagedArgs& a, const S& sm, Walk& w, long long tiles)
+{
+    w.s = sm.first;
+    w.left = tiles;
+    if (tiles <= 0) return;
+    enter(a, sm, w);
+    w.u = (int)(sm.offset / w.n);
+    w.t0 = (int)(sm.offset % w.n);
+    w.t1 = (int)min((long long)w.n, w.t0 + w.left);
+}
+template <class S> __device__ __forceinline__ void next_unit(const PagedArgs& a, const S& sm, Walk& w, int units)
+{
+    w.left -= w.t1 - w.t0;
+    if (w.left <= 0) return;
+    if (++w.u == units) {
+        w.u = 0;
+        ++w.s;
+        enter(a, sm, w);
+    }
+    w.t0 = 0;
+    w.t1 = (int)min((long long)w.n, w.left);
+}
+
+template <int D> __global__ void __launch_bounds__(TT, 1)
+paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap)
+{
+    using L = Token<D>;
+    constexpr int STAGES = L::STAGES, BLOCKS = L::BLOCKS;
+    extern __shared__ __align__(1024) unsigned char raw[];
+    auto& s = *reinterpret_cast<typename L::Smem*>(raw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, blocks = (a.G + ROWS - 1) / ROWS, units = a.Hkv * blocks;
+    ptx::grid_launch_dependents();
+    if (tid == 0) {
+        for (int i = 0; i < STAGES; ++i) {
+            ptx::mbar_init(&s.full[i], 1);
+            ptx::mbar_init(&s.empty[i], WARPS / 2);
+        }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&s.qfull[i], 1);
+            ptx::mbar_init(&s.qempty[i], WARPS);
+        }
+        s.dead = 0;
+        ptx::fence_mbar_init();
+    }
+    for (int i = tid; i < 2 * ROWS * D / 8; i += TT) reinterpret_cast<uint4*>(s.q)[i] = make_uint4(0, 0, 0, 0);  // rows without a head stay zero
+    ptx::fence_proxy_async_smem();
+    ptx::grid_dependency_wait();
+
+    // ---- the stretch: tiles before each thread's run of sequences, then the sequence in which the stretch begins
+    const int per = (a.N + TT - 1) / TT, s0 = min(tid * per, a.N), s1 = min(s0 + per, a.N);
+    long long mine = 0;
+    int fault = 0;
+    for (int i = s0; i < s1; ++i) mine += Span(a, length_of(a, i, &fault)).n;
+    if (blockIdx.x == 0 && fault) flag_status(a.dev_status, fault);
+    long long before = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += x;
+    }
+    if (lane == 31) s.sum[warp] = before;
+    if (tid == 0) s.first = a.N;
+    __syncthreads();
+    long long line = 0;
+    for (int w = 0; w < TT / 32; ++w) {
+        if (w < warp) before += s.sum[w];
+        line += s.sum[w];
+    }
+    before -= mine;
+    line *= units;
+    before *= units;
+    const long long x0 = stretch(line, blockIdx.x), x1 = stretch(line, blockIdx.x + 1);
+    if (x0 < x1 && before <= x0 && x0 < before + mine * units) {
+        int i = s0, f = 0;
+        for (;; ++i) {
+            const int n = Span(a, length_of(a, i, &f)).n;
+            if (x0 < before + (long long)n * units) break;
+            before += (long long)n * units;
+        }
+        s.first = i;
+        s.offset = x0 - before;
+    }
+    __syncthreads();
+    for (int i = tid; i < KNOWN; i += TT) {
+        int f = 0;
+        s.kv[i] = s.first + i < a.N ? length_of(a, s.first + i, &f) : -1;
+    }
+    __syncthreads();
+    const auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (ptx::mbar_wait(bar, parity & 1, WAIT) && !*reinterpret_cast<volatile int*>(&s.dead)) return true;
+        *reinterpret_cast<volatile int*>(&s.dead) = 1;
+        return false;
+    };
+    Walk w;
+    begin_walk(a, s, w, x1 - x0);
+    bool ok = true;
+    if (warp == WARPS) {
+        // ---- loads
+        const uint64_t once = ptx::policy_evict_first();
+        const int box = min(KEYS, 1 << a.page_shift), boxes = KEYS / box;
+        uint32_t use = 0, unit = 0;
+        for (; w.left > 0 && ok; next_unit(a, s, w, units), ++unit) {
+            const int h = w.u / blocks, g0 = w.u % blocks * ROWS, rows = min(ROWS, a.G - g0);
+            if (!(ok = wait(&s.qempty[unit & 1], (unit >> 1) + 1))) break;
+            if (lane == 0) {
+                ptx::mbar_arrive_expect_tx(&s.qfull[unit & 1], rows * D * 2);
+                ptx::bulk_g2s(s.q[unit & 1], static_cast<const __nv_bfloat16*>(a.q) + w.s * a.q_stride + (long long)(h * a.G + g0) * D, rows * D * 2,
+                              &s.qfull[unit & 1]);
+            }
+            for (int t = w.t0; t < w.t1; ++t, ++use) {
+                const int stage = use % STAGES, k0 = w.start + t * KEYS, tok = k0 + lane % boxes * box;
+                const bool in = tok < w.kv;
+                int page = 0;
+                if (in) page = a.pages[(long long)w.s * a.width + (tok >> a.page_shift)];
+                const bool gone = in && (page < 0 || page >= a.num_pages);
+                const uint32_t hide = __ballot_sync(0xffffffffu, gone && lane < boxes);
+                const int n = __popc(__ballot_sync(0xffffffffu, in && lane < boxes));
+                if (!(ok = wait(&s.empty[stage], use / STAGES + 1))) break;
+                if (lane == 0) {
+                    s.hidden[stage] = hide;
+                    if (hide) flag_status(a.dev_status, KDA_DEV_BAD_PAGE);
+                    ptx::mbar_arrive_expect_tx(&s.full[stage], n * box * 128 * BLOCKS * 2);
+                }
+                __syncwarp();
+                // lanes over the boxes of keys and values; each lane holds the page of box lane % boxes
+                for (int i = lane; i < 2 * BLOCKS * boxes; i += 32) {
+                    const int blk = i / boxes % BLOCKS, half = i / (boxes * BLOCKS);
+                    if (in)
+                        tma_load_4d(s.ring + stage * L::STAGE + half * L::HALF + blk * (KEYS * 128) + lane % boxes * box * 128, half ? &vmap : &kmap,
+                                    blk * 64, tok & ((1 << a.page_shift) - 1), h, gone ? -1 : page, &s.full[stage], once);
+                }
+            }
+        }
+        if (!ok) {  // what is on its way has to land first
+            for (uint32_t u = use > STAGES ? use - STAGES : 0; u < use; ++u) ptx::mbar_wait(&s.full[u % STAGES], (u / STAGES) & 1, WAIT);
+            for (uint32_t u = unit > 1 ? unit - 1 : 0; u <= unit; ++u) ptx::mbar_wait(&s.qfull[u & 1], (u >> 1) & 1, 1u << 12);
+        }
+    } else {
+        const int team = warp >> 2, k16 = (warp & 3) * 16;  // this warp's tokens of a tile
+        const float c = a.scale * 1.4426950408889634f;
+        uint32_t use = 0, unit = 0;
+        const uint32_t ring = ptx::smem_u32(s.ring);
+        if (tid == 0) work.cut[blockIdx.x].seq = -1;
+        // (a wait that ran out: the warps go on without waiting and without tiles, so that they still meet at the barriers)
+        for (; w.left > 0; next_unit(a, s, w, units), ++unit) {
+            const int h = w.u / blocks, g0 = w.u % blocks * ROWS, rows = min(ROWS, a.G - g0);
+            ok = ok && wait(&s.qfull[unit & 1], unit >> 1);
+            const uint32_t qbase = ptx::smem_u32(s.q[unit & 1]) + (lane & 15) * (D * 2) + (lane >> 4) * 16;
+            constexpr bool KEEP = D <= 128;  // wider rows come from shared memory each time: registers
+            uint32_t qf[KEEP ? D / 16 : 1][4];
+            if constexpr (KEEP) {
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) ldsm(qf[k], qbase + k * 32);
+            }
+            float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+            for (int t = w.t0; t < w.t1; ++t, ++use) {
+                if ((use & 1) != (uint32_t)team) continue;
+                const int stage = use % STAGES, k0 = w.start + t * KEYS + k16;
+                if (!ok || !(ok = wait(&s.full[stage], use / STAGES))) continue;
+                const uint32_t hide = *reinterpret_cast<volatile uint32_t*>(&s.hidden[stage]);
+                const uint32_t kb = ring + stage * L::STAGE, vb = kb + L::HALF;
+                const int box_shift = min(a.page_shift, 6);
+                const bool gone = (hide >> (k16 >> box_shift)) & 1;
+                const bool part = k0 + 16 > w.kv || k0 < w.lo || gone;
+                if (part) {
+                    // values of places that the row does not see, whatever lies there: zeros
+                    unsigned char* v = s.ring + stage * L::STAGE + L::HALF + k16 * 128;
+                    for (int i = lane; i < 16 * 8 * BLOCKS; i += 32) {
+                        const int r = i / 8 % 16, blk = i / 128;
+                        if (k0 + r >= w.kv || k0 + r < w.lo || gone) *reinterpret_cast<uint4*>(v + blk * (KEYS * 128) + r * 128 + i % 8 * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                float sc[2][4] = {};
+                {
+                    const int r = k16 + (lane & 7) + ((lane >> 4) & 1) * 8, ch = (lane >> 3) & 1;
+                    const uint32_t row = kb + r * 128;
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        uint32_t b[4];
+                        ldsm(b, row + (k / 4) * (KEYS * 128) + ((((k % 4) * 2 + ch) ^ (r & 7)) << 4));
+                        if constexpr (KEEP) {
+                            mma16816(sc[0], qf[k], b[0], b[1]);
+                            mma16816(sc[1], qf[k], b[2], b[3]);
+                        } else {
+                            uint32_t q[4];
+                            ldsm(q, qbase + k * 32);
+                            mma16816(sc[0], q, b[0], b[1]);
+                            mma16816(sc[1], q, b[2], b[3]);
+                        }
+                    }
+                }
+                if (part) {
+#pragma unroll
+                    for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int tok = k0 + nb * 8 + (lane & 3) * 2 + (e & 1);
+                            if (gone || tok >= w.kv || tok < w.lo) sc[nb][e] = -INFINITY;
+                        }
+                }
+                float top[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) top[i] = c * fmaxf(fmaxf(sc[0][2 * i], sc[0][2 * i + 1]), fmaxf(sc[1][2 * i], sc[1][2 * i + 1]));
+                if (__any_sync(0xffffffffu, top[0] > m[0] + LAG || top[1] > m[1] + LAG)) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float x = top[i];
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+                        const float next = fmaxf(m[i], x), f = next == -INFINITY ? 1.f : exp2_sfu(m[i] - next);
+                        m[i] = next;
+                        l[i] *= f;
+#pragma unroll
+                        for (int j = 0; j < D / 8; ++j) {
+                            o[j][2 * i] *= f;
+                            o[j][2 * i + 1] *= f;
+                        }
+                    }
+                }
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float base = m[i] == -INFINITY ? 0.f : m[i];
+                        const float x = exp2_sfu(fmaf(sc[nb][2 * i], c, -base)), y = exp2_sfu(fmaf(sc[nb][2 * i + 1], c, -base));
+                        l[i] += x + y;
+                        const uint32_t p = pack_bf16(x, y);
+                        hi[2 * nb + i] = p;
+                        lo[2 * nb + i] = pack_bf16(x - __uint_as_float(p << 16), y - __uint_as_float(p & 0xffff0000u));
+                    }
+                {
+                    const int r = k16 + (lane & 7) + ((lane >> 3) & 1) * 8, ch = lane >> 4;
+                    const uint32_t row = vb + r * 128;
+#pragma unroll
+                    for (int j = 0; j < D / 16; ++j) {
+                        uint32_t b[4];
+                        ldsm_t(b, row + (j / 4) * (KEYS * 128) + ((((j % 4) * 2 + ch) ^ (r & 7)) << 4));
+                        mma16816(o[2 * j], hi, b[0], b[1]);
+                        mma16816(o[2 * j + 1], hi, b[2], b[3]);
+                        mma16816(o[2 * j], lo, b[0], b[1]);
+                        mma16816(o[2 * j + 1], lo, b[2], b[3]);
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&s.empty[stage]);
+            }
+            // ---- the eight warps' sums together
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+                l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+                if ((lane & 3) == 0) s.ml[warp][lane / 4 + 8 * i] = make_float2(m[i], l[i]);
+            }
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&s.qempty[unit & 1]);
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            float f[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float top = -INFINITY;
+                for (int x = 0; x < WARPS; ++x) top = fmaxf(top, s.ml[x][lane / 4 + 8 * i].x);
+                f[i] = m[i] == -INFINITY ? 0.f : exp2_sfu(m[i] - top);
+            }
+            // two of CH channels of a row at a time, by a thread each
+            constexpr int CH = L::CH;
+            const int row = tid / (CH / 2), ch = tid % (CH / 2) * 2;
+            const bool in = row < rows && !*reinterpret_cast<volatile int*>(&s.dead);
+            float top = -INFINITY, sum = 0.f;
+            for (int x = 0; x < WARPS; ++x) top = fmaxf(top, s.ml[x][row % ROWS].x);
+            for (int x = 0; x < WARPS; ++x) sum += top == -INFINITY ? 0.f : s.ml[x][row % ROWS].y * exp2_sfu(s.ml[x][row % ROWS].x - top);
+            const bool whole = w.t0 == 0 && w.t1 == w.n;
+            const int slot = w.t0 == 0 ? 1 : 0;
+            const size_t head = (size_t)w.s * a.Hq + h * a.G + g0 + row, cell = ((size_t)blockIdx.x * 2 + slot) * ROWS + row;
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+            for (int e = 0; e < D; e += CH) {
+#pragma unroll
+                for (int j = 0; j < CH / 8; ++j)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        *reinterpret_cast<float2*>(&s.o[warp][(lane / 4 + 8 * i) * (CH + 4) + j * 8 + (lane & 3) * 2]) =
+                            make_float2(o[e / 8 + j][2 * i] * f[i], o[e / 8 + j][2 * i + 1] * f[i]);
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                float2 y = make_float2(0.f, 0.f);
+                if (row < ROWS)
+#pragma unroll
+                    for (int x = 0; x < WARPS; ++x) y = add2(y, *reinterpret_cast<const float2*>(&s.o[x][row * (CH + 4) + ch]));
+                if (in) {
+                    if (whole) *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + head * D + e + ch) =
+                        sum == 0.f ? 0u : pack_bf16(y.x * inv, y.y * inv);
+                    else *reinterpret_cast<float2*>(work.o + cell * D + e + ch) = y;
+                }
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+            }
+            if (in && ch == 0) {
+                if (!whole) work.ml[cell] = make_float2(top, sum);
+                else if (a.lse) a.lse[head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+            }
+            if (w.t0 == 0 && !whole && tid == 0) {
+                const long long last = x1 - 1 + (w.n - w.t1);  // the unit's last tile in the line
+                work.cut[blockIdx.x] = {line, w.s, w.u, owner(line, last), 0};
+            }
+        }
+        if (!ok && lane == 0) flag_status(a.dev_status, KDA_DEV_TIMEOUT);
+    }
+    __syncthreads();
+}
+
+// The parts of the unit that begins in stretch blockIdx.x and goes on: a thread two channels of a row.
+template <int D> __global__ void __launch_bounds__(ROWS * D / 2 > 1024 ? 1024 : ROWS * D / 2) token_join_kernel(const PagedArgs a, const TokenWork work)
+{
+    ptx::grid_launch_dependents();
+    ptx::grid_dependency_wait();
+    const Cut cut = work.cut[blockIdx.x];
+    if (cut.seq < 0) return;
+    const int blocks = (a.G + ROWS - 1) / ROWS, h = cut.unit / blocks, g0 = cut.unit % blocks * ROWS, rows = min(ROWS, a.G - g0);
+    for (int i = threadIdx.x; i < rows * (D / 2); i += blockDim.x) {
+        const int row = i / (D / 2), ch = i % (D / 2) * 2;
+        const auto cell = [&](int c) { return ((size_t)c * 2 + (c == (int)blockIdx.x)) * ROWS + row; };
+        const auto used = [&](int c) { return stretch(cut.line, c) < stretch(cut.line, c + 1); };
+        float top = -INFINITY;
+        for (int c = blockIdx.x; c <= cut.last; ++c)
+            if (used(c)) top = fmaxf(top, work.ml[cell(c)].x);
+        const float base = top == -INFINITY ? 0.f : top;
+        float sum = 0.f;
+        float2 y = make_float2(0.f, 0.f);
+#pragma unroll 4
+        for (int c = blockIdx.x; c <= cut.last; ++c) {
+            if (!used(c)) continue;
+            const float2 ml = work.ml[cell(c)];
+            const float f = exp2f(ml.x - base);
+            sum += f * ml.y;
+            y = fma2(both2(f), *reinterpret_cast<const float2*>(work.o + cell(c) * D + ch), y);
+        }
+        const size_t head = (size_t)cut.seq * a.Hq + h * a.G + g0 + row;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + head * D + ch) = sum == 0.f ? 0u : pack_bf16(y.x * inv, y.y * inv);
+        if (a.lse && ch == 0) a.lse[head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+    }
+}
+
+bool encode_cache(CUtensorMap* m, const void* base, const PagedArgs& a)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t P = (cuuint64_t)1 << a.page_shift;
+    const cuuint64_t dims[4] = {(cuuint64_t)a.D, P, (cuuint64_t)a.Hkv, (cuuint64_t)a.num_pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)a.token_stride * 2, (cuuint64_t)a.head_stride * 2, (cuuint64_t)a.page_stride * 2};
+    const cuuint32_t box[4] = {64, (cuuint32_t)std::min<cuuint64_t>(P, KEYS), 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D> cudaError_t launch(const PagedArgs& a, cudaStream_t st)
+{
+    using L = Token<D>;
+    constexpr int smem = sizeof(typename L::Smem);
+    static_assert(smem <= 227 * 1024, "shared memory");
+    static_assert(L::HALF % 1024 == 0 && offsetof(typename L::Smem, q) % 16 == 0 && offsetof(typename L::Smem, full) % 8 == 0, "alignment");
+    static PerDeviceOnce once;
+    cudaError_t e = once.run([](int) { return cudaFuncSetAttribute(paged_token_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
+    if (e != cudaSuccess) return e;
+    CUtensorMap km, vm;
+    if (!encode_cache(&km, a.k, a) || !encode_cache(&vm, a.v, a)) return cudaErrorInvalidValue;
+    TokenWork w;
+    lay_out(w, a);
+    e = launch_dependent(paged_token_kernel<D>, CTAS, TT, smem, st, a, w, km, vm);
+    constexpr int jt = ROWS * D / 2 > 1024 ? 1024 : ROWS * D / 2;
+    if (e == cudaSuccess) e = launch_dependent(token_join_kernel<D>, CTAS, jt, 0, st, a, w);
+    return e;
+}
+
+}  // namespace
+
+size_t paged_token_workspace_bytes(const PagedArgs& a)
+{
+    TokenWork w;
+    return lay_out(w, a);
+}
+
+cudaError_t launch_paged_token(const PagedArgs& a, cudaStream_t st)
+{
+    switch (a.D) {
+    case 32: return launch<32>(a, st);
+    case 64: return launch<64>(a, st);
+    case 128: return launch<128>(a, st);
+    default: return launch<256>(a, st);
+    }
+}
+
+}  // namespace kda
