@@ -35,6 +35,7 @@ __device__ __forceinline__ bool paged_seq(const PagedArgs& a, int s, int& begin,
 {
     begin = s;
     end = s + 1;
+    kv = a.kv_lens[s];
     if (a.cu_seqlens) {
         begin = a.cu_seqlens[s];
         end = a.cu_seqlens[s + 1];
@@ -43,7 +44,6 @@ __device__ __forceinline__ bool paged_seq(const PagedArgs& a, int s, int& begin,
             return false;
         }
     }
-    kv = a.kv_lens[s];
     if (kv > paged_capacity(a)) {
         *fault |= KDA_DEV_BAD_SEQLENS;
         return false;

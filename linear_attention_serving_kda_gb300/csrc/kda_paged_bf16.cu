@@ -18,8 +18,8 @@ namespace {
 
 using namespace paged;
 
-constexpr int THREADS = 384;  // two softmax warpgroups, a warp that issues products, one that loads, two without work
-constexpr uint32_t WAIT = 1u << 22;
+constexpr int THREADS = 384;  // two softmax warpgroups, a warp that issues products, one that loads keys and values, two that load rows
+constexpr uint32_t WAIT = 1u << 20;
 constexpr float LAG = 8.f;
 
 template <int DP> struct Shape {
@@ -32,32 +32,48 @@ template <int DP> struct Shape {
     struct Smem {
         unsigned char q[Q];
         unsigned char ring[SLOTS * SLOT];
-        uint64_t full[SLOTS], empty[SLOTS], scores[2], weights[2], product[2], rows[2], taken[2], drained;
-        uint32_t hidden[8], tmem, dead;
+        uint64_t full[SLOTS], empty[SLOTS], scores[2], weights[2], product[2], rows[2], free[2], taken[2], drained;
+        uint32_t hidden[8], tmem;
     };
 };
 
-// Shared-memory descriptor of a matrix whose rows (of the product's inner dimension) hold 64 values of the outer one in
-// 128 swizzled bytes: `lead` bytes from a block of 64 outer values to the next.
-__device__ __forceinline__ uint64_t desc_outer_sw128(uint32_t saddr, uint32_t lead)
-{
-    uint64_t d = 0;
-    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
-    d |= (uint64_t)(lead >> 4) << 16;
-    d |= (uint64_t)(1024 >> 4) << 32;  // eight inner values on
-    d |= (uint64_t)1 << 46;
-    d |= (uint64_t)2 << 61;
-    return d;
-}
+// Shared-memory descriptors of operands in 128-byte rows with the 128-byte swizzle, lower words (the upper one is
+// the same for all: eight rows are 1024 bytes).  A slice of 16 inner values lies 32 bytes on within 64 of them for rows along
+// the inner dimension (Q, K), 16 rows on for rows along the outer one (V; `lead` bytes from 64 outer values to the next).
+constexpr uint32_t DESC_HI = (1024 >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_inner(uint32_t saddr) { return (saddr >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_outer(uint32_t saddr, uint32_t lead) { return (saddr >> 4) | ((lead >> 4) << 16); }
 
-__device__ __forceinline__ void mma_ss_if(uint32_t leader, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate)
+// D (TMEM) (+)= A B^T; one thread issues.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate)
 {
     asm volatile(
-        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
-        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
+        "{\n .reg .pred p;\n .reg .b64 x, y;\n setp.ne.b32 p, %4, 0;\n mov.b64 x, {%1, %5};\n mov.b64 y, {%2, %5};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(DESC_HI)
         : "memory");
 }
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b64 y;\n setp.ne.b32 p, %4, 0;\n mov.b64 y, {%2, %5};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(DESC_HI)
+        : "memory");
+}
+
+// A place in the ring of SLOTS tiles and the parity of its use.
+template <int SLOTS> struct Place {
+    uint32_t slot = 0, phase = 0;
+    __device__ __forceinline__ void on(uint32_t n)
+    {
+        slot += n;
+        if (slot >= SLOTS) {
+            slot -= SLOTS;
+            phase ^= 1;
+        }
+    }
+};
 
 __device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, int x, int y, int z, int w, uint64_t* bar)
 {
@@ -119,26 +135,22 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
             ptx::mbar_init(&s.scores[i], 1);
             ptx::mbar_init(&s.product[i], 1);
             ptx::mbar_init(&s.weights[i], 4);
-            ptx::mbar_init(&s.rows[i], 4);
+            ptx::mbar_init(&s.rows[i], 2);
+            ptx::mbar_init(&s.free[i], 1);
             ptx::mbar_init(&s.taken[i], 4);
         }
         ptx::mbar_init(&s.drained, 1);
-        s.dead = 0;
         ptx::fence_mbar_init();
         ptx::fence_proxy_async_smem();
     }
     if (warp == 8) ptx::tmem_alloc(&s.tmem, 512);
     __syncthreads();
     ptx::tc_fence_after();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&s.tmem);
+    constexpr uint32_t tmem = 0;  // all 512 columns: they begin at 0 (a constant keeps the products' operands out of registers)
     ptx::grid_dependency_wait();
     const int items = p.head->items * a.Hkv;
-    // A wait that runs out ends the CTA's work: every role leaves its loop at its next wait.
-    const auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (ptx::mbar_wait(bar, parity & 1, WAIT) && !*reinterpret_cast<volatile uint32_t*>(&s.dead)) return true;
-        *reinterpret_cast<volatile uint32_t*>(&s.dead) = 1;
-        return false;
-    };
+    // A wait that runs out ends its role's work (and with it, one by one, the others').
+    const auto wait = [&](uint64_t* bar, uint32_t parity) { return ptx::mbar_wait(bar, parity & 1, WAIT); };
     constexpr uint32_t O0 = 256;  // S: columns 0 .. 2 KEYS - 1, O behind
 
     if (warp >= 8) {
@@ -184,71 +196,143 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
             // a CTA that gave up: what is on its way has to land first
             if (!ok)
                 for (uint32_t u = use > SLOTS ? use - SLOTS : 0; u < use; ++u) ptx::mbar_wait(&s.full[u % SLOTS], (u / SLOTS) & 1, WAIT);
-        } else if (warp == 8) {
-            // ---- products
-            const uint32_t leader = ptx::elect_one();
-            constexpr uint32_t ID_S = ptx::idesc_bf16(128, KEYS), ID_O = ptx::idesc_bf16(128, DP) | (1u << 16);  // V: inner dimension by rows
-            uint32_t use = 0, wcount[2] = {0, 0}, qcount[2] = {0, 0};
+        } else if (warp >= 10) {
+            // ---- rows: half of each tile by either warp, 16-byte pieces permuted within eight rows as the descriptor expects
+            constexpr int PIECES = DP / 8, AT_ONCE = 32 / PIECES;  // rows that a warp's 32 pieces make
+            const int e = lane % PIECES, r0 = (warp & 1) * 64 + lane / PIECES;
+            const int dt = AT_ONCE / a.G, dg = AT_ONCE % a.G;
+            uint32_t count[2] = {0, 0};
             bool ok = true;
-            const uint32_t qa = ptx::smem_u32(s.q), ring = ptx::smem_u32(s.ring);
             for (int x = blockIdx.x; x < items && ok; x += gridDim.x) {
                 const Work w = work_of<DP>(a, p, x);
                 if (w.n == 0) continue;
-                const int ahead = w.tiles == 1 ? 2 : 1;
-                // uses of the ring: keys of tile j, values of tile j
-                const auto key_use = [&](int j) { return use + (j < ahead ? j : 2 * j - ahead + 1); };
-                const auto value_use = [&](int j) { return use + (j < w.n - ahead ? ahead + 2 * j : w.n + j); };
-                const auto scores = [&](int st) {
-                    const int t = w.tiles == 2 ? st & 1 : 0, j = w.tiles == 2 ? st >> 1 : st, b = st & 1;
-                    const uint32_t u = key_use(j);
-                    if (t == 0 && !(ok = wait(&s.full[u % SLOTS], u / SLOTS))) return;
-                    if (j == 0 && !(ok = wait(&s.rows[t], qcount[t]))) return;
-                    ptx::tc_fence_after();
-                    const uint64_t da = ptx::desc_sw128(qa + t * (128 * DP * 2)), db = ptx::desc_sw128(ring + u % SLOTS * SLOT);
 #pragma unroll
-                    for (int k = 0; k < DP / 16; ++k)
-                        mma_ss_if(leader, tmem + b * KEYS, da + ((k / 4) * (128 * 128) + (k % 4) * 32) / 16,
-                                  db + ((k / 4) * (KEYS * 128) + (k % 4) * 32) / 16, ID_S, k > 0);
-                    ptx::mma_commit_if(leader, &s.scores[b]);
-                    if (t == w.tiles - 1) ptx::mma_commit_if(leader, &s.empty[u % SLOTS]);
+                for (int t = 0; t < L::TILES; ++t) {
+                    if (t >= w.tiles) break;
+                    if (!(ok = wait(&s.free[t], count[t] + 1))) break;  // the scores of the item before are done
+                    ++count[t];
+                    const int f = w.it.row0 + t * 128 + r0;
+                    int g = f % a.G;
+                    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (w.it.begin + f / a.G) * a.q_stride + (long long)w.h * a.G * D + e * 8;
+                    unsigned char* dst = s.q + t * (128 * DP * 2) + e / 8 * (128 * 128);
+#pragma unroll 4
+                    for (int r = r0; r < r0 / 64 * 64 + 64; r += AT_ONCE) {
+                        const bool in = t * 128 + r < w.it.rows && e * 8 < D;
+                        ptx::cp_async16(dst + r * 128 + ((e % 8) ^ (r & 7)) * 16, in ? q + (long long)g * D : static_cast<const __nv_bfloat16*>(a.q), in ? 16 : 0);
+                        g += dg;
+                        q += dt * a.q_stride;
+                        if (g >= a.G) {
+                            g -= a.G;
+                            q += a.q_stride;
+                        }
+                    }
+                    ptx::cp_async_commit();
+                }
+#pragma unroll
+                for (int t = 0; t < L::TILES; ++t) {
+                    if (t >= w.tiles || !ok) break;
+                    if (t == 0 && w.tiles == 2) ptx::cp_async_wait_prev();
+                    else ptx::cp_async_wait_all();
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(&s.rows[t]);
+                }
+            }
+            ptx::cp_async_wait_all();
+        } else if (warp == 8) {
+            // ---- products
+            const bool leader = ptx::elect_one();
+            constexpr uint32_t ID_S = ptx::idesc_bf16(128, KEYS), ID_O = ptx::idesc_bf16(128, DP) | (1u << 16);  // V: inner dimension by rows
+            constexpr uint32_t STEP = SLOT / 16;
+            const uint32_t qd = desc_inner(ptx::smem_u32(s.q)), kd = desc_inner(ptx::smem_u32(s.ring)),
+                           vd = desc_outer(ptx::smem_u32(s.ring), KEYS * 128);
+            Place<SLOTS> first;
+            uint32_t wcount[2] = {0, 0}, qcount[2] = {0, 0};
+            bool ok = true;
+            for (int x = blockIdx.x; x < items && ok; x += gridDim.x) {
+                const Work w = work_of<DP>(a, p, x);
+                if (w.n == 0) continue;
+                const bool two = w.tiles == 2;
+                // the ring holds K0 (K1, with one tile) V0 K1 (K2) V1 ...
+                Place<SLOTS> kp = first, vp = first;
+                vp.on(two ? 1 : min(2, w.n));
+                int kj = 0, vj = 0;  // the tiles at kp and vp
+                const auto scores = [&](int t, int b) {  // of row tile t over the keys at kp, into buffer b
+                    if (t == 0 && !wait(&s.full[kp.slot], kp.phase)) return false;
+                    if (kj == 0 && !wait(&s.rows[t], t ? qcount[1] : qcount[0])) return false;
+                    ptx::tc_fence_after();
+                    if (leader) {
+                        const uint32_t da = qd + t * (128 * DP * 2 / 16), db = kd + kp.slot * STEP;
+#pragma unroll
+                        for (int k = 0; k < DP / 16; ++k)
+                            mma_ss(tmem + b * KEYS, da + ((k / 4) * (128 * 128) + (k % 4) * 32) / 16, db + ((k / 4) * (KEYS * 128) + (k % 4) * 32) / 16, ID_S, k > 0);
+                        ptx::mma_commit(&s.scores[b]);
+                        if (t == 1 || !two) ptx::mma_commit(&s.empty[kp.slot]);
+                        if (kj == w.n - 1) ptx::mma_commit(&s.free[t]);
+                    }
+                    __syncwarp();
+                    if (t == 1 || !two) {
+                        kp.on(!two && kj == 0 ? 1 : 2);
+                        ++kj;
+                    }
+                    return true;
                 };
-                const auto values = [&](int st) {
-                    const int t = w.tiles == 2 ? st & 1 : 0, j = w.tiles == 2 ? st >> 1 : st, b = st & 1;
-                    const uint32_t u = value_use(j);
+                const auto values = [&](int t, int b) {  // of row tile t over the values at vp, weights in buffer b
                     if (t == 0) {
-                        if (!(ok = wait(&s.full[u % SLOTS], u / SLOTS))) return;
-                        const int have = w.it.k1 - w.it.k0 - j * KEYS;
+                        if (!wait(&s.full[vp.slot], vp.phase)) return false;
+                        const int have = w.it.k1 - w.it.k0 - vj * KEYS;
                         if (have < KEYS) {  // what lies behind the tokens may be anything: zeros, whose weights are zero
                             for (int i = lane; i < (KEYS - have) * 8 * BLOCKS; i += 32) {
                                 const int r = have + i / 8 % (KEYS - have), blk = i / (8 * (KEYS - have));
-                                *reinterpret_cast<uint4*>(s.ring + u % SLOTS * SLOT + blk * (KEYS * 128) + r * 128 + i % 8 * 16) = make_uint4(0, 0, 0, 0);
+                                *reinterpret_cast<uint4*>(s.ring + vp.slot * SLOT + blk * (KEYS * 128) + r * 128 + i % 8 * 16) = make_uint4(0, 0, 0, 0);
                             }
                             ptx::fence_proxy_async_smem();
                             __syncwarp();
                         }
                     }
-                    if (j == 0 && !(ok = wait(&s.taken[t], qcount[t] + 1))) return;  // O of the item before is read
-                    if (!(ok = wait(&s.weights[b], wcount[b]))) return;
-                    ++wcount[b];
+                    if (vj == 0 && !wait(&s.taken[t], (t ? qcount[1] : qcount[0]) + 1)) return false;  // O of the item before is read
+                    if (!wait(&s.weights[b], b ? wcount[1] : wcount[0])) return false;
+                    ++(b ? wcount[1] : wcount[0]);
                     ptx::tc_fence_after();
-                    const uint64_t db = desc_outer_sw128(ring + u % SLOTS * SLOT, KEYS * 128);
+                    if (leader) {
+                        const uint32_t db = vd + vp.slot * STEP;
 #pragma unroll
-                    for (int k = 0; k < KEYS / 16; ++k)
-                        ptx::mma_ts_if(leader, tmem + O0 + t * DP, tmem + b * KEYS + k * 8, db + k * 2048 / 16, ID_O, j > 0 || k > 0);
-                    ptx::mma_commit_if(leader, &s.product[b]);
-                    if (t == w.tiles - 1) ptx::mma_commit_if(leader, &s.empty[u % SLOTS]);
+                        for (int k = 0; k < KEYS / 16; ++k)
+                            mma_ts(tmem + O0 + t * DP, tmem + b * KEYS + k * 8, db + k * 2048 / 16, ID_O, k > 0 || vj > 0);
+                        ptx::mma_commit(&s.product[b]);
+                        if (t == 1 || !two) ptx::mma_commit(&s.empty[vp.slot]);
+                    }
+                    __syncwarp();
+                    if (t == 1 || !two) {
+                        vp.on(!two && vj == w.n - 2 ? 1 : 2);
+                        ++vj;
+                    }
+                    return true;
                 };
-                scores(0);
-                if (ok && w.steps > 1) scores(1);
-                for (int st = 0; st < w.steps && ok; ++st) {
-                    values(st);
-                    if (ok && st + 2 < w.steps) scores(st + 2);
-                }
-                use += 2 * w.n;
-                for (int t = 0; t < w.tiles; ++t) ++qcount[t];
+                ok = scores(0, 0);
+                if (two) ok = ok && scores(1, 1);
+                else if (w.n > 1) ok = ok && scores(0, 1);
+                if (two)
+                    for (int j = 0; j < w.n && ok; ++j) {
+                        ok = values(0, 0);
+                        if (j + 1 < w.n) ok = ok && scores(0, 0);
+                        ok = ok && values(1, 1);
+                        if (j + 1 < w.n) ok = ok && scores(1, 1);
+                    }
+                else
+                    for (int j = 0; j < w.n && ok; ++j) {
+                        ok = values(0, j & 1);
+                        if (j + 2 < w.n) ok = ok && scores(0, j & 1);
+                    }
+                const uint32_t end = first.slot + 2 * w.n;
+                first.slot = end % SLOTS;
+                first.phase ^= end / SLOTS & 1;
+                ++qcount[0];
+                qcount[1] += two;
             }
             // nothing may be on its way when TMEM is freed
-            ptx::mma_commit_if(leader, &s.drained);
+            if (leader) ptx::mma_commit(&s.drained);
+            __syncwarp();
             ptx::mbar_wait(&s.drained, 0, WAIT);
         }
     } else {
@@ -268,19 +352,6 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
             const int f = w.it.row0 + min(row, w.it.rows - 1), tok = f / a.G, head = w.h * a.G + f % a.G;
             float m = -INFINITY, sum = 0.f;
             if (mine && w.n > 0) {
-                // the tile's rows to shared memory: 16-byte pieces, permuted within eight rows as the descriptor expects
-                constexpr int PIECES = DP / 8;
-                for (int i = lane; i < 32 * PIECES; i += 32) {
-                    const int rr = (warp & 3) * 32 + i / PIECES, e = i % PIECES, ff = w.it.row0 + t * 128 + rr;
-                    uint4 q = make_uint4(0, 0, 0, 0);
-                    if (t * 128 + rr < w.it.rows && e * 8 < D)
-                        q = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + (w.it.begin + ff / a.G) * a.q_stride +
-                                                            (long long)(w.h * a.G + ff % a.G) * D + e * 8);
-                    *reinterpret_cast<uint4*>(s.q + t * (128 * DP * 2) + e / 8 * (128 * 128) + rr * 128 + ((e % 8) ^ (rr & 7)) * 16) = q;
-                }
-                ptx::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(&s.rows[t]);
                 const int pos = w.it.pos0 + tok;
                 const int hi = a.causal ? min(w.it.k1, pos + 1) : w.it.k1;
                 const int lo = a.window ? (int)max(0ll, (long long)pos - a.window + 1) : 0;
@@ -410,7 +481,6 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
             // the other warpgroup, without rows in this item, may not run ahead over phases of barriers that it did not wait for
             if (L::TILES == 2 && w.tiles == 1) {
                 asm volatile("bar.sync 1, 256;" ::: "memory");
-                ok = !*reinterpret_cast<volatile uint32_t*>(&s.dead);
             }
         }
         if (!ok && L::TILES == 2) asm volatile("bar.arrive 1, 256;" ::: "memory");
@@ -454,7 +524,7 @@ template <int DP, int D> cudaError_t launch(const PagedArgs& a, cudaStream_t st)
     lay_out(p, a, 128 * L::TILES, L::KEYS, 152);
     e = launch_dependent(plan_kernel, 1, PT, 0, st, a, p);
     if (e == cudaSuccess) e = launch_dependent(paged_bf16_kernel<DP, D>, ctas, THREADS, smem, st, a, p, km, vm);
-    if (e == cudaSuccess) e = launch_dependent(join_kernel<__nv_bfloat16, D>, 304, JT, 0, st, a, p);
+    if (e == cudaSuccess) e = launch_join<__nv_bfloat16, D>(a, p, st);
     return e;
 }
 

@@ -201,7 +201,7 @@ template <typename IO, int D, int R> cudaError_t launch(const PagedArgs& a, cuda
     lay_out(p, a, R, L::KEYS, ctas);
     e = launch_dependent(plan_kernel, 1, PT, 0, st, a, p);
     if (e == cudaSuccess) e = launch_dependent(paged_f32_kernel<IO, D, R>, ctas, FT, smem, st, a, p);
-    if (e == cudaSuccess) e = launch_dependent(join_kernel<IO, D>, 304, JT, 0, st, a, p);
+    if (e == cudaSuccess) e = launch_join<IO, D>(a, p, st);
     return e;
 }
 

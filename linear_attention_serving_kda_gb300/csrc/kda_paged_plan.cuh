@@ -167,7 +167,10 @@ static __global__ void __launch_bounds__(PT) plan_kernel(const PagedArgs a, cons
     }
     if ((tid & 31) == 31) sums[tid >> 5] = before;
     __syncthreads();
-    for (int w = 0; w < (tid >> 5); ++w) before += sums[w];
+    int below = (tid & 31) < (tid >> 5) ? sums[tid & 31] : 0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) below += __shfl_xor_sync(0xffffffffu, below, o);
+    before += below;
     if (tid == BUCKETS - 1) p.head->items = before;
     if (tid < BUCKETS) bucket[tid] = before - mine;
     __syncthreads();
@@ -197,42 +200,84 @@ static __global__ void __launch_bounds__(PT) plan_kernel(const PagedArgs a, cons
     }
 }
 
-// Rows whose tokens were cut into parts: a warp a row, its lanes over the head's channels.
+// A warp joins the parts of one row: part s has its maximum and sum at ml(s) and its D values at o(s), both
+// null for a part without any.  Returns the sum and the maximum, and in y the lane's D / 32 neighbouring values, not divided.
+template <int D, class ML, class O> __device__ __forceinline__ float2 join_row(int parts, ML&& ml, O&& o, float (&y)[D / 32])
+{
+    constexpr int PER = D / 32;
+    const int lane = threadIdx.x & 31;
+    float m = -INFINITY, l = 0.f;
+    for (int s = lane; s < parts; s += 32)
+        if (const float2* x = ml(s)) m = fmaxf(m, x->x);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) y[e] = 0.f;
+    for (int s0 = 0; s0 < parts; s0 += 32) {
+        float f = 0.f;
+        const float2* x = s0 + lane < parts ? ml(s0 + lane) : nullptr;
+        if (x) {
+            f = exp2f(x->x - base);
+            l += f * x->y;
+        }
+        const int n = min(32, parts - s0);
+#pragma unroll 4
+        for (int s = 0; s < n; ++s) {
+            const float g = __shfl_sync(0xffffffffu, f, s);
+            const float* v = o(s0 + s);
+            if (!v) continue;
+            if constexpr (PER >= 4) {
+#pragma unroll
+                for (int e = 0; e < PER; e += 4) {
+                    const float4 z = *reinterpret_cast<const float4*>(v + lane * PER + e);
+                    y[e] = fmaf(g, z.x, y[e]);
+                    y[e + 1] = fmaf(g, z.y, y[e + 1]);
+                    y[e + 2] = fmaf(g, z.z, y[e + 2]);
+                    y[e + 3] = fmaf(g, z.w, y[e + 3]);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < PER; ++e) y[e] = fmaf(g, v[lane * PER + e], y[e]);
+            }
+        }
+    }
+    return make_float2(m, warp_sum(l));
+}
+// The joined row to out and lse (row: of [T][Hq]).
+template <typename IO, int D> __device__ __forceinline__ void write_row(const PagedArgs& a, size_t row, float2 ml, const float (&y)[D / 32])
+{
+    constexpr int PER = D / 32;
+    const int lane = threadIdx.x & 31;
+    const float inv = ml.y == 0.f ? 0.f : 1.f / ml.y;
+    IO* out = static_cast<IO*>(a.out) + row * D + lane * PER;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) stv(out + e, ml.y == 0.f ? 0.f : y[e] * inv);
+    if (a.lse && lane == 0) a.lse[row] = ml.y == 0.f ? -INFINITY : (ml.x + log2f(ml.y)) * 0.69314718055994531f;
+}
+
+// Rows whose tokens were cut into parts: a warp a row.
 constexpr int JT = 256;
 template <typename IO, int D> __global__ void __launch_bounds__(JT) join_kernel(const PagedArgs a, const Plan p)
 {
     ptx::grid_launch_dependents();
     ptx::grid_dependency_wait();
-    constexpr int PER = D / 32;
-    const int lane = threadIdx.x & 31;
-    const long long rows = (long long)p.head->joined * a.Hkv * p.part_rows;
-    for (long long i = (long long)blockIdx.x * (JT / 32) + (threadIdx.x >> 5); i < rows; i += (long long)gridDim.x * (JT / 32)) {
-        const int r = (int)(i % p.part_rows), h = (int)(i / p.part_rows % a.Hkv);
-        const Joined j = p.joined[i / p.part_rows / a.Hkv];
+    const int rows = p.head->joined * a.Hkv * p.part_rows;
+    for (int i = blockIdx.x * (JT / 32) + (threadIdx.x >> 5); i < rows; i += gridDim.x * (JT / 32)) {
+        const int r = i % p.part_rows, th = i / p.part_rows, h = th % a.Hkv;
+        const Joined j = p.joined[th / a.Hkv];
         if (r >= j.rows) continue;
         const size_t first = ((size_t)j.part * a.Hkv + h) * p.part_rows + r, step = (size_t)a.Hkv * p.part_rows;
-        float m = -INFINITY;
-        for (int s = lane; s < j.parts; s += 32) m = fmaxf(m, p.ml[first + s * step].x);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const float base = m == -INFINITY ? 0.f : m;
-        float l = 0.f, o[PER] = {};
-#pragma unroll 4
-        for (int s = 0; s < j.parts; ++s) {
-            const float2 ml = p.ml[first + s * step];
-            const float f = exp2f(ml.x - base);
-            l += f * ml.y;
-            const float* x = p.o + (first + s * step) * D;
-#pragma unroll
-            for (int e = 0; e < PER; ++e) o[e] = fmaf(f, x[e * 32 + lane], o[e]);
-        }
-        const int f = j.row0 + r, head = h * a.G + f % a.G;
-        const size_t row = (size_t)(j.begin + f / a.G) * a.Hq + head;
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-        for (int e = 0; e < PER; ++e) stv(static_cast<IO*>(a.out) + row * D + e * 32 + lane, l == 0.f ? 0.f : o[e] * inv);
-        if (a.lse && lane == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+        float y[D / 32];
+        const float2 ml = join_row<D>(j.parts, [&](int s) { return p.ml + first + s * step; }, [&](int s) { return p.o + (first + s * step) * D; }, y);
+        const int f = j.row0 + r;
+        write_row<IO, D>(a, (size_t)(j.begin + f / a.G) * a.Hq + h * a.G + f % a.G, ml, y);
     }
+}
+template <typename IO, int D> cudaError_t launch_join(const PagedArgs& a, const Plan& p, cudaStream_t st)
+{
+    const int64_t most = ((int64_t)p.max_joined * a.Hkv * p.part_rows + JT / 32 - 1) / (JT / 32);
+    return launch_dependent(join_kernel<IO, D>, (unsigned)std::min<int64_t>(most, 152 * 8), JT, 0, st, a, p);
 }
 
 }  // namespace paged

@@ -10,7 +10,7 @@
 // in two bf16 parts, running maximum and sum of each warp by itself, joined at the pair's end.
 #include <cuda.h>
 
-#include "kda_paged.h"
+#include "kda_paged_plan.cuh"
 #include "kda_ptx.cuh"
 
 namespace kda {
@@ -463,37 +463,22 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
     __syncthreads();
 }
 
-// The parts of the unit that begins in stretch blockIdx.x and goes on: a thread two channels of a row.
-template <int D> __global__ void __launch_bounds__(ROWS * D / 2 > 1024 ? 1024 : ROWS * D / 2) token_join_kernel(const PagedArgs a, const TokenWork work)
+// The parts of the unit that begins in stretch blockIdx.x and goes on: a warp a row.
+template <int D> __global__ void __launch_bounds__(32 * ROWS) token_join_kernel(const PagedArgs a, const TokenWork work)
 {
     ptx::grid_launch_dependents();
     ptx::grid_dependency_wait();
     const Cut cut = work.cut[blockIdx.x];
     if (cut.seq < 0) return;
-    const int blocks = (a.G + ROWS - 1) / ROWS, h = cut.unit / blocks, g0 = cut.unit % blocks * ROWS, rows = min(ROWS, a.G - g0);
-    for (int i = threadIdx.x; i < rows * (D / 2); i += blockDim.x) {
-        const int row = i / (D / 2), ch = i % (D / 2) * 2;
-        const auto cell = [&](int c) { return ((size_t)c * 2 + (c == (int)blockIdx.x)) * ROWS + row; };
-        const auto used = [&](int c) { return stretch(cut.line, c) < stretch(cut.line, c + 1); };
-        float top = -INFINITY;
-        for (int c = blockIdx.x; c <= cut.last; ++c)
-            if (used(c)) top = fmaxf(top, work.ml[cell(c)].x);
-        const float base = top == -INFINITY ? 0.f : top;
-        float sum = 0.f;
-        float2 y = make_float2(0.f, 0.f);
-#pragma unroll 4
-        for (int c = blockIdx.x; c <= cut.last; ++c) {
-            if (!used(c)) continue;
-            const float2 ml = work.ml[cell(c)];
-            const float f = exp2f(ml.x - base);
-            sum += f * ml.y;
-            y = fma2(both2(f), *reinterpret_cast<const float2*>(work.o + cell(c) * D + ch), y);
-        }
-        const size_t head = (size_t)cut.seq * a.Hq + h * a.G + g0 + row;
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + head * D + ch) = sum == 0.f ? 0u : pack_bf16(y.x * inv, y.y * inv);
-        if (a.lse && ch == 0) a.lse[head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
-    }
+    const int blocks = (a.G + ROWS - 1) / ROWS, h = cut.unit / blocks, g0 = cut.unit % blocks * ROWS, row = threadIdx.x >> 5;
+    if (g0 + row >= a.G) return;
+    // stretches without a tile (fewer tiles than stretches) left nothing
+    const auto used = [&](int s) { return stretch(cut.line, blockIdx.x + s) < stretch(cut.line, blockIdx.x + s + 1); };
+    const auto cell = [&](int s) { return ((size_t)(blockIdx.x + s) * 2 + (s == 0)) * ROWS + row; };
+    float y[D / 32];
+    const float2 ml = paged::join_row<D>(cut.last - (int)blockIdx.x + 1, [&](int s) { return used(s) ? work.ml + cell(s) : nullptr; },
+                                         [&](int s) { return used(s) ? work.o + cell(s) * D : nullptr; }, y);
+    paged::write_row<__nv_bfloat16, D>(a, (size_t)cut.seq * a.Hq + h * a.G + g0 + row, ml, y);
 }
 
 bool encode_cache(CUtensorMap* m, const void* base, const PagedArgs& a)
@@ -523,8 +508,7 @@ template <int D> cudaError_t launch(const PagedArgs& a, cudaStream_t st)
     TokenWork w;
     lay_out(w, a);
     e = launch_dependent(paged_token_kernel<D>, CTAS, TT, smem, st, a, w, km, vm);
-    constexpr int jt = ROWS * D / 2 > 1024 ? 1024 : ROWS * D / 2;
-    if (e == cudaSuccess) e = launch_dependent(token_join_kernel<D>, CTAS, jt, 0, st, a, w);
+    if (e == cudaSuccess) e = launch_dependent(token_join_kernel<D>, CTAS, 32 * std::min(ROWS, a.G), 0, st, a, w);
     return e;
 }
 
