@@ -19,6 +19,7 @@ namespace {
 using namespace paged;
 
 constexpr int THREADS = 384;  // two softmax warpgroups, a warp that issues products, one that loads keys and values, two that load rows
+constexpr int CTAS = 152;  // one an SM
 constexpr uint32_t WAIT = 1u << 20;
 constexpr float LAG = 8.f;
 
@@ -29,11 +30,14 @@ template <int DP> struct Shape {
     static constexpr int SLOT = KEYS * DP * 2;
     static constexpr int SLOTS = DP == 64 ? 8 : 5;
     static constexpr int Q = TILES * 128 * DP * 2;
+    static constexpr int OUT = 128 * DP * 2 / SLOT;    // slots that a tile's outputs pass through, COLS channels in each
+    static constexpr int COLS = SLOT / 256;
     struct Smem {
         unsigned char q[Q];
         unsigned char ring[SLOTS * SLOT];
         uint64_t full[SLOTS], empty[SLOTS], scores[2], weights[2], product[2], rows[2], free[2], taken[2], drained;
         uint32_t hidden[8], tmem;
+        Start start;
     };
 };
 
@@ -99,23 +103,21 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     return r;
 }
 
-// Steps of an item: with two tiles, step s is tile s & 1 over tokens s >> 1; with one, tokens s.  Step s uses S's
-// buffer s & 1.  Everyone counts the phases of every barrier alike from the items themselves.
-struct Work {
-    Item it;
-    int h, n, tiles, steps;  // key head, tiles of tokens, tiles of rows
+// Steps of a piece of a unit: with two tiles of rows, step s is tile s & 1 over key tile s >> 1; with one, key tile s.  Step
+// s uses S's buffer s & 1.  Everyone counts the phases of every barrier alike from the pieces themselves.
+struct Work : Walk {
+    int tiles, count, steps, k0, k1;  // tiles of rows, key tiles, steps, tokens
+    bool staged;                      // the outputs leave through slots of the ring
+    __device__ __forceinline__ void derive(int keys)
+    {
+        tiles = rows > 128 ? 2 : 1;
+        count = t1 - t0;
+        steps = count * tiles;
+        k0 = lo + t0 * keys;
+        k1 = min(hi, lo + t1 * keys);
+        staged = whole() && count > 0;
+    }
 };
-
-template <int DP> __device__ __forceinline__ Work work_of(const PagedArgs& a, const Plan& p, int x)
-{
-    Work w;
-    w.it = p.items[x / a.Hkv];
-    w.h = x % a.Hkv;
-    w.n = (w.it.k1 - w.it.k0 + Shape<DP>::KEYS - 1) / Shape<DP>::KEYS;
-    w.tiles = w.it.rows > 128 ? 2 : 1;
-    w.steps = w.n * w.tiles;
-    return w;
-}
 
 template <int DP, int D> __global__ void __launch_bounds__(THREADS, 1)
 paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap)
@@ -148,7 +150,8 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
     ptx::tc_fence_after();
     constexpr uint32_t tmem = 0;  // all 512 columns: they begin at 0 (a constant keeps the products' operands out of registers)
     ptx::grid_dependency_wait();
-    const int items = p.head->items * a.Hkv;
+    find_start<THREADS / 32>(a, p, s.start);
+    if (tid == 0) p.cut[blockIdx.x].rows = 0;
     // A wait that runs out ends its role's work (and with it, one by one, the others').
     const auto wait = [&](uint64_t* bar, uint32_t parity) { return ptx::mbar_wait(bar, parity & 1, WAIT); };
     constexpr uint32_t O0 = 256;  // S: columns 0 .. 2 KEYS - 1, O behind
@@ -160,14 +163,16 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
             uint32_t use = 0, kt = 0;
             bool ok = true;
             const int box = min(KEYS, 1 << a.page_shift), boxes = KEYS / box;
-            for (int x = blockIdx.x; x < items && ok; x += gridDim.x) {
-                const Work w = work_of<DP>(a, p, x);
+            Work w;
+            for (w.begin_at(a, p, s.start); w.left > 0 && ok; w.next(a, p)) {
+                if (!w.act) continue;
+                w.derive(KEYS);
                 const int ahead = w.tiles == 1 ? 2 : 1;
                 const auto load = [&](const CUtensorMap* map, int j, bool keys) {
-                    const int slot = use % SLOTS, t0 = w.it.k0 + j * KEYS, t = t0 + lane % boxes * box, blk = lane / boxes;
+                    const int slot = use % SLOTS, t0 = w.k0 + j * KEYS, t = t0 + lane % boxes * box, blk = lane / boxes;
                     int page = 0;
-                    const bool mine = blk < BLOCKS && t < w.it.k1;
-                    if (mine) page = a.pages[(long long)w.it.seq * a.width + (t >> a.page_shift)];
+                    const bool mine = blk < BLOCKS && t < w.k1;
+                    if (mine) page = a.pages[(long long)w.seq * a.width + (t >> a.page_shift)];
                     const bool gone = mine && (page < 0 || page >= a.num_pages);
                     const uint32_t all = __ballot_sync(0xffffffffu, mine);
                     uint32_t hide = __ballot_sync(0xffffffffu, gone && blk == 0);
@@ -182,16 +187,21 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
                     __syncwarp();
                     if (mine) {
                         unsigned char* dst = s.ring + slot * SLOT + blk * (KEYS * 128) + lane % boxes * box * 128;
-                        tma_load_4d(dst, map, blk * 64, t & ((1 << a.page_shift) - 1), w.h, gone ? -1 : page, &s.full[slot]);
+                        tma_load_4d(dst, map, blk * 64, t & ((1 << a.page_shift) - 1), w.head, gone ? -1 : page, &s.full[slot]);
                     }
                     if (keys) ++kt;
                     ++use;
                 };
-                for (int j = 0; j < min(ahead, w.n) && ok; ++j) load(&kmap, j, true);
-                for (int j = 0; j < w.n && ok; ++j) {
+                for (int j = 0; j < min(ahead, w.count) && ok; ++j) load(&kmap, j, true);
+                for (int j = 0; j < w.count && ok; ++j) {
                     load(&vmap, j, false);
-                    if (ok && j + ahead < w.n) load(&kmap, j + ahead, true);
+                    if (ok && j + ahead < w.count) load(&kmap, j + ahead, true);
                 }
+                if (w.staged)  // slots for the outputs
+                    for (int i = 0; i < w.tiles * L::OUT && ok; ++i, ++use) {
+                        if (!(ok = wait(&s.empty[use % SLOTS], use / SLOTS + 1))) break;
+                        if (lane == 0) ptx::mbar_arrive(&s.full[use % SLOTS]);
+                    }
             }
             // a CTA that gave up: what is on its way has to land first
             if (!ok)
@@ -203,21 +213,22 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
             const int dt = AT_ONCE / a.G, dg = AT_ONCE % a.G;
             uint32_t count[2] = {0, 0};
             bool ok = true;
-            for (int x = blockIdx.x; x < items && ok; x += gridDim.x) {
-                const Work w = work_of<DP>(a, p, x);
-                if (w.n == 0) continue;
+            Work w;
+            for (w.begin_at(a, p, s.start); w.left > 0 && ok; w.next(a, p)) {
+                if (!w.act || w.n == 0) continue;
+                w.derive(KEYS);
 #pragma unroll
                 for (int t = 0; t < L::TILES; ++t) {
                     if (t >= w.tiles) break;
                     if (!(ok = wait(&s.free[t], count[t] + 1))) break;  // the scores of the item before are done
                     ++count[t];
-                    const int f = w.it.row0 + t * 128 + r0;
+                    const int f = w.row0 + t * 128 + r0;
                     int g = f % a.G;
-                    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (w.it.begin + f / a.G) * a.q_stride + (long long)w.h * a.G * D + e * 8;
+                    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (w.begin + f / a.G) * a.q_stride + (long long)w.head * a.G * D + e * 8;
                     unsigned char* dst = s.q + t * (128 * DP * 2) + e / 8 * (128 * 128);
 #pragma unroll 4
                     for (int r = r0; r < r0 / 64 * 64 + 64; r += AT_ONCE) {
-                        const bool in = t * 128 + r < w.it.rows && e * 8 < D;
+                        const bool in = t * 128 + r < w.rows && e * 8 < D;
                         ptx::cp_async16(dst + r * 128 + ((e % 8) ^ (r & 7)) * 16, in ? q + (long long)g * D : static_cast<const __nv_bfloat16*>(a.q), in ? 16 : 0);
                         g += dg;
                         q += dt * a.q_stride;
@@ -249,13 +260,14 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
             Place<SLOTS> first;
             uint32_t wcount[2] = {0, 0}, qcount[2] = {0, 0};
             bool ok = true;
-            for (int x = blockIdx.x; x < items && ok; x += gridDim.x) {
-                const Work w = work_of<DP>(a, p, x);
-                if (w.n == 0) continue;
+            Work w;
+            for (w.begin_at(a, p, s.start); w.left > 0 && ok; w.next(a, p)) {
+                if (!w.act || w.n == 0) continue;
+                w.derive(KEYS);
                 const bool two = w.tiles == 2;
                 // the ring holds K0 (K1, with one tile) V0 K1 (K2) V1 ...
                 Place<SLOTS> kp = first, vp = first;
-                vp.on(two ? 1 : min(2, w.n));
+                vp.on(two ? 1 : min(2, w.count));
                 int kj = 0, vj = 0;  // the tiles at kp and vp
                 const auto scores = [&](int t, int b) {  // of row tile t over the keys at kp, into buffer b
                     if (t == 0 && !wait(&s.full[kp.slot], kp.phase)) return false;
@@ -268,7 +280,7 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
                             mma_ss(tmem + b * KEYS, da + ((k / 4) * (128 * 128) + (k % 4) * 32) / 16, db + ((k / 4) * (KEYS * 128) + (k % 4) * 32) / 16, ID_S, k > 0);
                         ptx::mma_commit(&s.scores[b]);
                         if (t == 1 || !two) ptx::mma_commit(&s.empty[kp.slot]);
-                        if (kj == w.n - 1) ptx::mma_commit(&s.free[t]);
+                        if (kj == w.count - 1) ptx::mma_commit(&s.free[t]);
                     }
                     __syncwarp();
                     if (t == 1 || !two) {
@@ -280,7 +292,7 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
                 const auto values = [&](int t, int b) {  // of row tile t over the values at vp, weights in buffer b
                     if (t == 0) {
                         if (!wait(&s.full[vp.slot], vp.phase)) return false;
-                        const int have = w.it.k1 - w.it.k0 - vj * KEYS;
+                        const int have = w.k1 - w.k0 - vj * KEYS;
                         if (have < KEYS) {  // what lies behind the tokens may be anything: zeros, whose weights are zero
                             for (int i = lane; i < (KEYS - have) * 8 * BLOCKS; i += 32) {
                                 const int r = have + i / 8 % (KEYS - have), blk = i / (8 * (KEYS - have));
@@ -304,27 +316,27 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
                     }
                     __syncwarp();
                     if (t == 1 || !two) {
-                        vp.on(!two && vj == w.n - 2 ? 1 : 2);
+                        vp.on(!two && vj == w.count - 2 ? 1 : 2);
                         ++vj;
                     }
                     return true;
                 };
                 ok = scores(0, 0);
                 if (two) ok = ok && scores(1, 1);
-                else if (w.n > 1) ok = ok && scores(0, 1);
+                else if (w.count > 1) ok = ok && scores(0, 1);
                 if (two)
-                    for (int j = 0; j < w.n && ok; ++j) {
+                    for (int j = 0; j < w.count && ok; ++j) {
                         ok = values(0, 0);
-                        if (j + 1 < w.n) ok = ok && scores(0, 0);
+                        if (j + 1 < w.count) ok = ok && scores(0, 0);
                         ok = ok && values(1, 1);
-                        if (j + 1 < w.n) ok = ok && scores(1, 1);
+                        if (j + 1 < w.count) ok = ok && scores(1, 1);
                     }
                 else
-                    for (int j = 0; j < w.n && ok; ++j) {
+                    for (int j = 0; j < w.count && ok; ++j) {
                         ok = values(0, j & 1);
-                        if (j + 2 < w.n) ok = ok && scores(0, j & 1);
+                        if (j + 2 < w.count) ok = ok && scores(0, j & 1);
                     }
-                const uint32_t end = first.slot + 2 * w.n;
+                const uint32_t end = first.slot + 2 * w.count + (w.staged ? w.tiles * L::OUT : 0);
                 first.slot = end % SLOTS;
                 first.phase ^= end / SLOTS & 1;
                 ++qcount[0];
@@ -336,31 +348,34 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
             ptx::mbar_wait(&s.drained, 0, WAIT);
         }
     } else {
-        // ---- a thread a row: exponentials, rescaling, outputs
+        // ---- a thread a row: exponentials, rescaling, outputs.  (After a wait that ran out a warp goes on without waits
+        // and stores, so that it still meets the others at the named barriers.)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         const int t = warp >> 2, r = tid & 127;  // tile, row of it
         const uint32_t tl = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes
         const float c = a.scale * 1.4426950408889634f;
-        uint32_t scount[2] = {0, 0}, pcount[2] = {0, 0}, kt = 0;
+        uint32_t scount[2] = {0, 0}, pcount[2] = {0, 0}, kt = 0, use = 0;
         bool ok = true;
-        for (int x = blockIdx.x; x < items && ok; x += gridDim.x) {
+        Work w;
+        for (w.begin_at(a, p, s.start); w.left > 0; w.next(a, p)) {
             if (t >= L::TILES) break;
-            const Work w = work_of<DP>(a, p, x);
+            if (!w.act) continue;
+            w.derive(KEYS);
             const int row = t * 128 + r;
             const bool mine = t < w.tiles;
-            const bool live = mine && t * 128 + (warp & 3) * 32 < w.it.rows;  // the warp has rows
-            const int f = w.it.row0 + min(row, w.it.rows - 1), tok = f / a.G, head = w.h * a.G + f % a.G;
+            const bool live = mine && t * 128 + (warp & 3) * 32 < w.rows;  // the warp has rows
+            const int f = w.row0 + min(row, w.rows - 1), tok = f / a.G, head = w.head * a.G + f % a.G;
             float m = -INFINITY, sum = 0.f;
-            if (mine && w.n > 0) {
-                const int pos = w.it.pos0 + tok;
-                const int hi = a.causal ? min(w.it.k1, pos + 1) : w.it.k1;
+            if (mine && w.count > 0) {
+                const int pos = w.pos0() + tok;
+                const int hi = a.causal ? min(w.k1, pos + 1) : w.k1;
                 const int lo = a.window ? (int)max(0ll, (long long)pos - a.window + 1) : 0;
                 for (int st = w.tiles == 2 ? t : 0; st < w.steps; st += w.tiles) {
-                    const int j = w.tiles == 2 ? st >> 1 : st, b = st & 1, k0 = w.it.k0 + j * KEYS;
-                    if (!(ok = wait(&s.scores[b], scount[b]))) break;
+                    const int j = w.tiles == 2 ? st >> 1 : st, b = st & 1, k0 = w.k0 + j * KEYS;
+                    ok = ok && wait(&s.scores[b], scount[b]);
                     ++scount[b];
                     ptx::tc_fence_after();
-                    if (live) {
+                    if (live && ok) {
                         float v[KEYS];
                         if constexpr (KEYS == 128) ptx::tmem_ld128(tl + b * KEYS, v);
                         else ptx::tmem_ld64(tl + b * KEYS, v);
@@ -390,7 +405,7 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
                             sum *= fac;
                             if (j > 0) {
                                 // with one tile the step before's product may still run (with two it had to end before these scores began)
-                                if (w.tiles == 1 && !(ok = wait(&s.product[b ^ 1], pcount[b ^ 1] + (st - 1) / 2))) break;
+                                if (w.tiles == 1) ok = wait(&s.product[b ^ 1], pcount[b ^ 1] + (st - 1) / 2);
                                 ptx::tc_fence_after();
 #pragma unroll 1
                                 for (int e = 0; e < DP; e += 32) {
@@ -427,55 +442,104 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
                     if (lane == 0) ptx::mbar_arrive(&s.weights[b]);
                 }
             }
-            if (!ok) break;
-            kt += w.n;
+            kt += w.count;
             if (mine) {
-                if (w.n > 0) {
+                if (w.count > 0) {
                     const int last = w.tiles == 2 ? w.steps - 2 + t : w.steps - 1, b = last & 1;
-                    if (!(ok = wait(&s.product[b], pcount[b] + last / 2))) break;
+                    ok = ok && wait(&s.product[b], pcount[b] + last / 2);
                     ptx::tc_fence_after();
                 }
-                if (live) {
-                    const bool whole = w.it.part < 0, has = row < w.it.rows;
-                    const float inv = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
-                    const size_t at = ((size_t)(w.it.begin + tok)) * a.Hq + head;
-                    const size_t slot = ((size_t)max(w.it.part, 0) * a.Hkv + w.h) * p.part_rows + row;
+                const bool has = row < w.rows && ok;
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                const size_t cell = (size_t)blockIdx.x * 2 + (w.t0 == 0);
+                if (w.staged) {
+                    // a thread's row into the slot, 16-byte pieces permuted within eight rows; then whole rows out
+                    use += 2 * w.count + t * L::OUT;
+                    constexpr int COLS = L::COLS, PIECES = COLS / 8, AT_ONCE = 128 / PIECES;
+                    const int dt = AT_ONCE / a.G, dg = AT_ONCE % a.G;
 #pragma unroll 1
-                    for (int e = 0; e < D; e += 32) {
-                        float o[32];
-                        if (w.n > 0) {
-                            ptx::tmem_ld32(tl + O0 + t * DP + e, o);
-                        } else {
+                    for (int i = 0; i < L::OUT; ++i, ++use) {
+                        unsigned char* slot = s.ring + use % SLOTS * SLOT;
+                        ok = ok && wait(&s.full[use % SLOTS], use / SLOTS);
+                        if (live && ok) {
+#pragma unroll 1
+                            for (int e = 0; e < COLS; e += 32) {
+                                float o[32];
+                                ptx::tmem_ld32(tl + O0 + t * DP + i * COLS + e, o);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] = 0.f;
+                                for (int k = 0; k < 32; ++k) o[k] = sum == 0.f ? 0.f : o[k] * inv;
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    *reinterpret_cast<uint4*>(slot + r * (COLS * 2) + ((e / 8 + k) ^ (r & 7)) * 16) =
+                                        make_uint4(pack_bf16(o[8 * k], o[8 * k + 1]), pack_bf16(o[8 * k + 2], o[8 * k + 3]),
+                                                   pack_bf16(o[8 * k + 4], o[8 * k + 5]), pack_bf16(o[8 * k + 6], o[8 * k + 7]));
+                            }
                         }
-                        if (!has) continue;
+                        if (i == L::OUT - 1) {  // O may be overwritten
+                            ptx::tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) ptx::mbar_arrive(&s.taken[t]);
+                        }
+                        asm volatile("bar.sync %0, 128;" ::"r"(2 + t) : "memory");
+                        const int e = r % PIECES, f0 = w.row0 + t * 128 + r / PIECES;
+                        int g = f0 % a.G;
+                        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + ((size_t)(w.begin + f0 / a.G) * a.Hq + w.head * a.G) * D + i * COLS + e * 8;
+#pragma unroll 4
+                        for (int rr = r / PIECES; rr < 128; rr += AT_ONCE) {
+                            if (ok && t * 128 + rr < w.rows && i * COLS + e * 8 < D)
+                                *reinterpret_cast<uint4*>(out + (size_t)g * D) = *reinterpret_cast<const uint4*>(slot + rr * (COLS * 2) + (e ^ (rr & 7)) * 16);
+                            g += dg;
+                            out += (size_t)dt * a.Hq * D;
+                            if (g >= a.G) {
+                                g -= a.G;
+                                out += (size_t)a.Hq * D;
+                            }
+                        }
+                        ptx::fence_proxy_async_smem();
+                        asm volatile("bar.sync %0, 128;" ::"r"(2 + t) : "memory");
+                        if (r == 0) ptx::mbar_arrive(&s.empty[use % SLOTS]);
+                    }
+                    use += (w.tiles - 1 - t) * L::OUT;
+                } else {
+                    if (live) {
+#pragma unroll 1
+                        for (int e = 0; e < D; e += 32) {
+                            float o[32];
+                            if (w.count > 0) {
+                                ptx::tmem_ld32(tl + O0 + t * DP + e, o);
+                            } else {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = sum == 0.f ? 0.f : o[i] * inv;
-                        if (whole) {
-                            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at * D + e);
+                                for (int i = 0; i < 32; ++i) o[i] = 0.f;
+                            }
+                            if (!has) continue;
+                            if (w.count > 0) {
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                dst[i] = make_uint4(pack_bf16(o[8 * i], o[8 * i + 1]), pack_bf16(o[8 * i + 2], o[8 * i + 3]),
-                                                    pack_bf16(o[8 * i + 4], o[8 * i + 5]), pack_bf16(o[8 * i + 6], o[8 * i + 7]));
-                        } else {
-                            float4* dst = reinterpret_cast<float4*>(p.o + slot * D + e);
+                                for (int i = 0; i < 8; ++i)
+                                    p.o[(cell * (D / 4) + e / 4 + i) * p.part_rows + row] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                            } else {  // rows that see nothing
+                                uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + ((size_t)(w.begin + tok) * a.Hq + head) * D + e);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                                for (int i = 0; i < 4; ++i) dst[i] = make_uint4(0, 0, 0, 0);
+                            }
                         }
                     }
-                    if (has) {
-                        if (!whole) p.ml[slot] = make_float2(m, sum);
-                        else if (a.lse) a.lse[at] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994531f;
+                    if (w.count > 0) {
+                        ptx::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(&s.taken[t]);
+                        use += 2 * w.count;
                     }
                 }
-                if (w.n > 0) {
-                    ptx::tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(&s.taken[t]);
+                if (live && has) {
+                    if (!w.whole()) p.ml[cell * p.part_rows + row] = make_float2(m, sum);
+                    else if (a.lse) a.lse[(size_t)(w.begin + tok) * a.Hq + head] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994531f;
                 }
+            } else {
+                use += 2 * w.count + (w.staged ? w.tiles * L::OUT : 0);
             }
-            for (int b = 0; b < 2; ++b) pcount[b] += w.tiles == 2 ? w.n : (w.n + 1 - b) / 2;
+            if (tid == 0 && ok && w.t0 == 0 && !w.whole())
+                p.cut[blockIdx.x] = {s.start.line, w.begin, w.row0, w.rows, w.head, owner(s.start.line, w.end() - 1, p.ctas)};
+            for (int b = 0; b < 2; ++b) pcount[b] += w.tiles == 2 ? w.count : (w.count + 1 - b) / 2;
             scount[0] = pcount[0];
             scount[1] = pcount[1];
             // the other warpgroup, without rows in this item, may not run ahead over phases of barriers that it did not wait for
@@ -483,7 +547,6 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
                 asm volatile("bar.sync 1, 256;" ::: "memory");
             }
         }
-        if (!ok && L::TILES == 2) asm volatile("bar.arrive 1, 256;" ::: "memory");
         if (!ok && lane == 0) flag_status(a.dev_status, KDA_DEV_TIMEOUT);
     }
     ptx::tc_fence_before();
@@ -518,12 +581,9 @@ template <int DP, int D> cudaError_t launch(const PagedArgs& a, cudaStream_t st)
     if (e != cudaSuccess) return e;
     CUtensorMap km, vm;
     if (!encode_cache(&km, a.k, a, L::KEYS) || !encode_cache(&vm, a.v, a, L::KEYS)) return cudaErrorInvalidValue;
-    const int ctas = sm_count();
-    if (ctas <= 0) return cudaErrorInvalidDevice;
     Plan p;
-    lay_out(p, a, 128 * L::TILES, L::KEYS, 152);
-    e = launch_dependent(plan_kernel, 1, PT, 0, st, a, p);
-    if (e == cudaSuccess) e = launch_dependent(paged_bf16_kernel<DP, D>, ctas, THREADS, smem, st, a, p, km, vm);
+    lay_out(p, a, 128 * L::TILES, L::KEYS, CTAS);
+    e = launch_dependent(paged_bf16_kernel<DP, D>, CTAS, THREADS, smem, st, a, p, km, vm);
     if (e == cudaSuccess) e = launch_join<__nv_bfloat16, D>(a, p, st);
     return e;
 }
@@ -533,7 +593,7 @@ template <int DP, int D> cudaError_t launch(const PagedArgs& a, cudaStream_t st)
 size_t paged_bf16_workspace_bytes(const PagedArgs& a)
 {
     Plan p;
-    return a.D == 256 ? lay_out(p, a, 128, 64, 152) : lay_out(p, a, 256, 128, 152);
+    return a.D == 256 ? lay_out(p, a, 128, 64, CTAS) : lay_out(p, a, 256, 128, CTAS);
 }
 
 cudaError_t launch_paged_bf16(const PagedArgs& a, cudaStream_t st)

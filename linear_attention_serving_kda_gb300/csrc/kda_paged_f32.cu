@@ -12,6 +12,7 @@ namespace {
 using namespace paged;
 
 constexpr int FT = 256;
+constexpr int CTAS = 304;  // two an SM
 
 template <int D, int R> struct F32 {
     static constexpr int KEYS = D == 256 ? 32 : 64;
@@ -39,10 +40,13 @@ template <typename IO, int D, int R> __global__ void __launch_bounds__(FT) paged
     auto& s = *reinterpret_cast<typename L::Smem*>(raw);
     const int tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
     const float c = a.scale * 1.4426950408889634f;
-    const int n = p.head->items * a.Hkv;
-    for (int x = blockIdx.x; x < n; x += gridDim.x) {
-        const Item it = p.items[x / a.Hkv];
-        const int h = x % a.Hkv;
+    __shared__ Start start;
+    find_start<FT / 32>(a, p, start);
+    if (tid == 0) p.cut[blockIdx.x].rows = 0;
+    Walk it;
+    for (it.begin_at(a, p, start); it.left > 0; it.next(a, p)) {
+        if (!it.act) continue;
+        const int h = it.head, first = it.lo + it.t0 * KEYS, last = min(it.hi, it.lo + it.t1 * KEYS);
         __syncthreads();
         for (int i = tid; i < R * (D / 4); i += FT) {
             const int r = i / (D / 4), e = i % (D / 4), f = it.row0 + r;
@@ -57,18 +61,18 @@ template <typename IO, int D, int R> __global__ void __launch_bounds__(FT) paged
         for (int i = 0; i < RI; ++i) {
             m[i] = -INFINITY;
             l[i] = 0.f;
-            pos[i] = it.pos0 + (it.row0 + ty + 16 * i) / a.G;
+            pos[i] = it.pos0() + (it.row0 + ty + 16 * i) / a.G;
 #pragma unroll
             for (int d = 0; d < DI; ++d)
 #pragma unroll
                 for (int e = 0; e < DW; ++e) o[i][d][e] = 0.f;
         }
-        for (int k0 = it.k0; k0 < it.k1; k0 += KEYS) {
+        for (int k0 = first; k0 < last; k0 += KEYS) {
             __syncthreads();  // the tile before is done with
             if (tid < KEYS) {
                 const int t = k0 + tid;
                 long long at = -1;
-                if (t < it.k1) {
+                if (t < last) {
                     const int page = a.pages[(long long)it.seq * a.width + (t >> a.page_shift)];
                     if (page < 0 || page >= a.num_pages) flag_status(a.dev_status, KDA_DEV_BAD_PAGE);
                     else at = page * a.page_stride + (t & ((1 << a.page_shift) - 1)) * a.token_stride + h * a.head_stride;
@@ -164,8 +168,8 @@ template <typename IO, int D, int R> __global__ void __launch_bounds__(FT) paged
             const int r = ty + 16 * i, f = it.row0 + r;
             if (r >= it.rows) continue;
             const size_t row = (size_t)(it.begin + f / a.G) * a.Hq + h * a.G + f % a.G;
-            const size_t slot = ((size_t)max(it.part, 0) * a.Hkv + h) * p.part_rows + r;
-            const bool whole = it.part < 0;
+            const size_t cell = (size_t)blockIdx.x * 2 + (it.t0 == 0);
+            const bool whole = it.whole();
             const float inv = !whole ? 1.f : l[i] == 0.f ? 0.f : 1.f / l[i];
 #pragma unroll
             for (int d = 0; d < DI; ++d)
@@ -173,13 +177,14 @@ template <typename IO, int D, int R> __global__ void __launch_bounds__(FT) paged
                 for (int e = 0; e < DW; ++e) {
                     const float y = l[i] == 0.f ? 0.f : o[i][d][e] * inv;
                     if (whole) stv(static_cast<IO*>(a.out) + row * D + d * 64 + tx * DW + e, y);
-                    else p.o[slot * D + d * 64 + tx * DW + e] = y;
+                    else reinterpret_cast<float*>(p.o + (cell * (D / 4) + (d * 64 + tx * DW + e) / 4) * p.part_rows + r)[(tx * DW + e) % 4] = y;
                 }
             if (tx == 0) {
-                if (!whole) p.ml[slot] = make_float2(m[i], l[i]);
+                if (!whole) p.ml[cell * p.part_rows + r] = make_float2(m[i], l[i]);
                 else if (a.lse) a.lse[row] = l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * 0.69314718055994531f;
             }
         }
+        if (tid == 0 && it.t0 == 0 && !it.whole()) p.cut[blockIdx.x] = {start.line, it.begin, it.row0, it.rows, h, owner(start.line, it.end() - 1, p.ctas)};
     }
 }
 
@@ -197,10 +202,8 @@ template <typename IO, int D, int R> cudaError_t launch(const PagedArgs& a, cuda
     });
     if (e != cudaSuccess) return e;
     Plan p;
-    const int ctas = 304;
-    lay_out(p, a, R, L::KEYS, ctas);
-    e = launch_dependent(plan_kernel, 1, PT, 0, st, a, p);
-    if (e == cudaSuccess) e = launch_dependent(paged_f32_kernel<IO, D, R>, ctas, FT, smem, st, a, p);
+    lay_out(p, a, R, L::KEYS, CTAS);
+    e = launch_dependent(paged_f32_kernel<IO, D, R>, CTAS, FT, smem, st, a, p);
     if (e == cudaSuccess) e = launch_join<IO, D>(a, p, st);
     return e;
 }
@@ -224,7 +227,7 @@ template <typename IO> cudaError_t launch_io(const PagedArgs& a, cudaStream_t st
 size_t paged_f32_workspace_bytes(const PagedArgs& a)
 {
     Plan p;
-    return lay_out(p, a, tile_rows(a), a.D == 256 ? 32 : 64, 304);
+    return lay_out(p, a, tile_rows(a), a.D == 256 ? 32 : 64, CTAS);
 }
 
 cudaError_t launch_paged_f32(const PagedArgs& a, cudaStream_t st) { return launch_io<float>(a, st); }

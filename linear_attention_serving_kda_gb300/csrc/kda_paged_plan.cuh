@@ -1,11 +1,13 @@
-// kda_paged_plan.cuh -- how the rows of an attention call are cut into work, and
-// how the parts of a long row's tokens are joined.
+// kda_paged_plan.cuh -- how the rows of an attention call are shared out among CTAs, and how the parts of a
+// row's tokens are joined.
 //
-// The rows of a sequence that share a key head (its tokens times the G query heads of the
-// group, token after token) are cut into tiles; a tile's tokens are those that any of its rows
-// sees.  One CTA takes all of a tile's tokens where there are tiles enough; few rows over many tokens are
-// cut along the tokens as well, into items of about half a CTA's share of the whole, and
-// joined afterwards.  Only the GPU knows the lengths, so a kernel of one CTA writes the items, longest first.
+// The rows of a sequence that share a key head (its tokens times the G query heads of the group, token after
+// token) are cut into tiles of rows; a tile sees the tokens that any of its rows sees, cut into tiles of keys.  A
+// (tile of rows, key head) is a unit; the key tiles of all units form one line (with UNIT places more a unit, for what a unit
+// costs besides), and each CTA takes an equal stretch of it, whatever the lengths.  A unit within one stretch
+// is written out; one that stretches cut leaves a part in the workspace for each, which join_kernel adds: at most two parts a CTA.
+// Only the GPU knows the lengths: every CTA counts the line and finds where its stretch begins by itself (two
+// passes over the sequences by all warps, a microsecond or two; a kernel of its own in front took 8 to 18).
 #pragma once
 
 #include "kda_paged.h"
@@ -14,64 +16,50 @@
 namespace kda {
 namespace paged {
 
-struct Item {
-    int begin, seq;         // first row of the sequence; its number
-    int row0, rows;         // rows of the tile, counted over tokens and heads of the group
-    int pos0;               // token of the sequence's first row
-    int k0, k1;             // tokens of this item; k0 starts a page or a tile of one
-    int part;               // -1: the whole tile, else where its sums go
+constexpr int UNIT = 3;
+
+struct Start {
+    long long line;            // places in all
+    int seq, row0, head, at;   // first unit of the CTA's stretch, and where in it the stretch begins
 };
-struct Joined {
-    int begin, row0, rows, part, parts;
-};
-struct Head {
-    int items, joined, parts, pad;
+struct Cut {
+    long long line;
+    int begin, row0, rows, head, last;  // the unit that begins in a stretch and ends in that of CTA `last`; rows 0: none
 };
 
 struct Plan {
-    int rows;      // of a tile
-    int keys;      // of a tile
-    int ctas;      // that share the work
-    int max_items, max_joined, max_parts;
-    int part_rows; // rows kept of a part
-    Head* head;
-    Item* items;
-    Joined* joined;
-    float* o;      // [parts][Hkv][part_rows][D], not divided by the weights' sum
-    float2* ml;    // [parts][Hkv][part_rows]: largest score (in powers of two), sum of the weights
+    int rows;       // of a tile
+    int keys;       // of a tile
+    int ctas;
+    int part_rows;  // rows kept of a part
+    Cut* cut;           // [ctas]
+    float2* ml;         // [ctas][2][part_rows]: largest score (in powers of two), sum of the weights;
+    float4* o;          // [ctas][2][D / 4][part_rows], not divided.  0: of a unit that began before, 1: of one that goes on
 };
 
-constexpr int LEAST = 2;  // key tiles of an item, at least
-
-inline size_t align256(size_t x) { return (x + 255) / 256 * 256; }
-
-// Bounds and places in the workspace.  A tile cut into parts has more than one item's length L of key
-// tiles, so it has at most 2 cost / L parts, and L >= total / (2 ctas): 4 ctas parts over all key heads.
 inline size_t lay_out(Plan& p, const PagedArgs& a, int rows, int keys, int ctas)
 {
     p.rows = rows;
     p.keys = keys;
     p.ctas = ctas;
-    const int64_t tiles = ((int64_t)a.T * a.G + rows - 1) / rows + std::min(a.N, a.T);
-    p.max_parts = 4 * ctas / a.Hkv + 2;
-    p.max_joined = p.max_parts / 2 + 1;
-    p.max_items = (int)(tiles + p.max_parts);
     p.part_rows = (int)std::min<int64_t>(rows, (int64_t)a.T * a.G);
     unsigned char* w = static_cast<unsigned char*>(a.workspace);
     size_t at = 0;
     const auto take = [&](size_t n) {
         unsigned char* x = w ? w + at : nullptr;
-        at += align256(n);
+        at += (n + 255) / 256 * 256;
         return x;
     };
-    p.head = reinterpret_cast<Head*>(take(sizeof(Head)));
-    p.items = reinterpret_cast<Item*>(take(sizeof(Item) * (size_t)p.max_items));
-    p.joined = reinterpret_cast<Joined*>(take(sizeof(Joined) * (size_t)p.max_joined));
-    const size_t part = (size_t)p.max_parts * a.Hkv * p.part_rows;
+    p.cut = reinterpret_cast<Cut*>(take(sizeof(Cut) * ctas));
+    const size_t part = (size_t)ctas * 2 * p.part_rows;
     p.ml = reinterpret_cast<float2*>(take(part * sizeof(float2)));
-    p.o = reinterpret_cast<float*>(take(part * a.D * sizeof(float)));
+    p.o = reinterpret_cast<float4*>(take(part * a.D * sizeof(float)));
     return at;
 }
+
+// First place of CTA c's stretch, and the CTA that has place x.
+__device__ __forceinline__ long long stretch(long long line, int c, int ctas) { return line * c / ctas; }
+__device__ __forceinline__ int owner(long long line, long long x, int ctas) { return (int)(((x + 1) * ctas + line - 1) / line) - 1; }
 
 // Tokens that rows row0 .. row0 + rows - 1 see: [lo, hi), lo down to the start of a page or of a tile of `keys` in it.
 __device__ __forceinline__ void span(const PagedArgs& a, int keys, int pos0, int kv, int row0, int rows, int& lo, int& hi)
@@ -87,197 +75,248 @@ __device__ __forceinline__ void span(const PagedArgs& a, int keys, int pos0, int
     }
 }
 
-constexpr int PT = 1024;
-constexpr int BUCKETS = 512;
+// A walk along a stretch, piece of a unit after piece of a unit.
+struct Walk {
+    int seq, begin, kv;         // sequence, its first row, its tokens in the cache
+    int tokens, all;            // its rows, and times G
+    int row0, rows, head;       // the unit
+    int lo, hi, n;              // its tokens (lo may lie before the first that is seen) and key tiles
+    int t0, t1;                 // the piece's key tiles
+    bool act;                   // the piece has something to do
+    int from;                   // the piece's first place in the unit
+    long long left, x;          // places of the stretch from there on, and places before the unit
 
-// f(begin, seq, row0, rows, pos0, lo, hi) for every tile, by one thread each.  Few sequences: the CTA takes the tiles
-// of one after the other; many: a warp each.
-template <class F> __device__ void each_tile(const PagedArgs& a, const Plan& p, int* fault, F&& f)
-{
-    const int lane = threadIdx.x & 31;
-    const bool wide = a.N <= 16;
-    const int team = wide ? PT : 32, who = wide ? threadIdx.x : lane, step = wide ? 1 : PT / 32;
-    // sequences first .. first + 31 * step are looked up at a time, one by each lane
-    for (long long first = wide ? 0 : threadIdx.x >> 5; first < a.N; first += 32 * step) {
-        int begin = 0, end = 0, kv = 0, ok = 0;
-        const long long mine = first + (long long)lane * step;
-        if (mine < a.N) ok = paged_seq(a, (int)mine, begin, end, kv, fault);
-        uint32_t left = __ballot_sync(0xffffffffu, ok);
-        while (left) {
-            const int l = __ffs(left) - 1;
-            left &= left - 1;
-            const int b = __shfl_sync(0xffffffffu, begin, l), n = __shfl_sync(0xffffffffu, end, l) - b, t = __shfl_sync(0xffffffffu, kv, l);
-            const int all = n * a.G;
-            for (long long r = (long long)who * p.rows; r < all; r += (long long)team * p.rows) {
-                const int rows = min(p.rows, all - (int)r);
-                int lo, hi;
-                span(a, p.keys, t - n, t, (int)r, rows, lo, hi);
-                f(b, (int)(first + (long long)l * step), (int)r, rows, t - n, lo, hi);
-            }
-        }
-    }
-}
+    __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == n; }
+    __device__ __forceinline__ int pos0() const { return kv - tokens; }
+    __device__ __forceinline__ long long end() const { return x + n + UNIT; }
 
-static __global__ void __launch_bounds__(PT) plan_kernel(const PagedArgs a, const Plan p)
-{
-    ptx::grid_launch_dependents();
-    ptx::grid_dependency_wait();
-    __shared__ unsigned long long total;
-    __shared__ int longest, bucket[BUCKETS], njoined, nparts, sums[PT / 32], all_faults;
-    const int tid = threadIdx.x;
-    if (tid == 0) {
-        total = 0;
-        longest = njoined = nparts = all_faults = 0;
-    }
-    for (int i = tid; i < BUCKETS; i += PT) bucket[i] = 0;
-    __syncthreads();
-    const auto cost = [&](int lo, int hi) { return max(1, (hi - lo + p.keys - 1) / p.keys); };
+    // the sequence, or the first behind it, that has rows
+    __device__ __forceinline__ void enter(const PagedArgs& a)
     {
-        long long sum = 0;
-        int most = 0, fault = 0;
-        each_tile(a, p, &fault, [&](int, int, int, int, int, int lo, int hi) {
-            const int c = cost(lo, hi);
-            sum += c;
-            most = max(most, c);
-        });
-        if (fault) atomicOr(&all_faults, fault);
-        if (sum) {
-            atomicAdd(&total, (unsigned long long)sum);
-            atomicMax(&longest, most);
-        }
-    }
-    __syncthreads();
-    if (tid == 0 && all_faults) flag_status(a.dev_status, all_faults);
-    const unsigned long long share = total * a.Hkv / (2u * p.ctas) + 1;
-    const int L = (int)min((unsigned long long)INT32_MAX, max((unsigned long long)LEAST, share));
-    const int top = min(L, longest);
-    const auto bucket_of = [&](int c) { return (int)((long long)(top - min(c, top)) * (BUCKETS - 1) / max(top, 1)); };
-    int dummy = 0;
-    each_tile(a, p, &dummy, [&](int, int, int, int, int, int lo, int hi) {
-        const int c = cost(lo, hi), parts = (c + L - 1) / L;
-        atomicAdd(&bucket[bucket_of((c + parts - 1) / parts)], parts);
-    });
-    __syncthreads();
-    // where each bucket begins
-    int mine = tid < BUCKETS ? bucket[tid] : 0, before = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, before, o);
-        if ((tid & 31) >= o) before += x;
-    }
-    if ((tid & 31) == 31) sums[tid >> 5] = before;
-    __syncthreads();
-    int below = (tid & 31) < (tid >> 5) ? sums[tid & 31] : 0;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) below += __shfl_xor_sync(0xffffffffu, below, o);
-    before += below;
-    if (tid == BUCKETS - 1) p.head->items = before;
-    if (tid < BUCKETS) bucket[tid] = before - mine;
-    __syncthreads();
-    each_tile(a, p, &dummy, [&](int begin, int seq, int row0, int rows, int pos0, int lo, int hi) {
-        const int c = cost(lo, hi), parts = (c + L - 1) / L, each = (c + parts - 1) / parts;
-        const int at = atomicAdd(&bucket[bucket_of(each)], parts);
-        int part = -1;
-        if (parts > 1) {
-            part = atomicAdd(&nparts, parts);
-            p.joined[atomicAdd(&njoined, 1)] = {begin, row0, rows, part, parts};
-        }
-        for (int i = 0; i < parts; ++i) {
-            // part i's key tiles: c * i / parts and on, none of them empty
-            const int t0 = (int)((long long)c * i / parts), t1 = (int)((long long)c * (i + 1) / parts);
-            Item it;
-            it.begin = begin; it.seq = seq; it.row0 = row0; it.rows = rows; it.pos0 = pos0;
-            it.k0 = lo + t0 * p.keys;
-            it.k1 = min(hi, lo + t1 * p.keys);
-            it.part = parts > 1 ? part + i : -1;
-            p.items[at + i] = it;
-        }
-    });
-    __syncthreads();
-    if (tid == 0) {
-        p.head->joined = njoined;
-        p.head->parts = nparts;
-    }
-}
-
-// A warp joins the parts of one row: part s has its maximum and sum at ml(s) and its D values at o(s), both
-// null for a part without any.  Returns the sum and the maximum, and in y the lane's D / 32 neighbouring values, not divided.
-template <int D, class ML, class O> __device__ __forceinline__ float2 join_row(int parts, ML&& ml, O&& o, float (&y)[D / 32])
-{
-    constexpr int PER = D / 32;
-    const int lane = threadIdx.x & 31;
-    float m = -INFINITY, l = 0.f;
-    for (int s = lane; s < parts; s += 32)
-        if (const float2* x = ml(s)) m = fmaxf(m, x->x);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    const float base = m == -INFINITY ? 0.f : m;
-#pragma unroll
-    for (int e = 0; e < PER; ++e) y[e] = 0.f;
-    for (int s0 = 0; s0 < parts; s0 += 32) {
-        float f = 0.f;
-        const float2* x = s0 + lane < parts ? ml(s0 + lane) : nullptr;
-        if (x) {
-            f = exp2f(x->x - base);
-            l += f * x->y;
-        }
-        const int n = min(32, parts - s0);
-#pragma unroll 4
-        for (int s = 0; s < n; ++s) {
-            const float g = __shfl_sync(0xffffffffu, f, s);
-            const float* v = o(s0 + s);
-            if (!v) continue;
-            if constexpr (PER >= 4) {
-#pragma unroll
-                for (int e = 0; e < PER; e += 4) {
-                    const float4 z = *reinterpret_cast<const float4*>(v + lane * PER + e);
-                    y[e] = fmaf(g, z.x, y[e]);
-                    y[e + 1] = fmaf(g, z.y, y[e + 1]);
-                    y[e + 2] = fmaf(g, z.z, y[e + 2]);
-                    y[e + 3] = fmaf(g, z.w, y[e + 3]);
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < PER; ++e) y[e] = fmaf(g, v[lane * PER + e], y[e]);
+        int e, f = 0;
+        for (; seq < a.N; ++seq)
+            if (paged_seq(a, seq, begin, e, kv, &f)) {
+                tokens = e - begin;
+                all = tokens * a.G;
+                return;
             }
-        }
+        left = 0;  // lengths that changed under the call
+        all = 0;
+        kv = begin = tokens = 0;
     }
-    return make_float2(m, warp_sum(l));
-}
-// The joined row to out and lse (row: of [T][Hq]).
-template <typename IO, int D> __device__ __forceinline__ void write_row(const PagedArgs& a, size_t row, float2 ml, const float (&y)[D / 32])
+    __device__ __forceinline__ void unit(const PagedArgs& a, const Plan& p)
+    {
+        rows = min(p.rows, all - row0);
+        span(a, p.keys, pos0(), kv, row0, rows, lo, hi);
+        n = (hi - lo + p.keys - 1) / p.keys;
+    }
+    __device__ __forceinline__ void piece()
+    {
+        const int to = (int)min((long long)n + UNIT, from + left);
+        t0 = max(from - UNIT, 0);
+        t1 = max(to - UNIT, 0);
+        act = t1 > t0 || (n == 0 && from == 0);
+    }
+    __device__ __forceinline__ void begin_at(const PagedArgs& a, const Plan& p, const Start& s)
+    {
+        x = stretch(s.line, blockIdx.x, p.ctas);
+        left = stretch(s.line, blockIdx.x + 1, p.ctas) - x;
+        if (left <= 0) return;
+        seq = s.seq;
+        row0 = s.row0;
+        head = s.head;
+        from = s.at;
+        x -= from;
+        enter(a);
+        if (left <= 0) return;
+        unit(a, p);
+        piece();
+    }
+    __device__ __forceinline__ void next(const PagedArgs& a, const Plan& p)
+    {
+        left -= min((long long)n + UNIT, from + left) - from;
+        if (left <= 0) return;
+        x += n + UNIT;
+        from = 0;
+        if (++head == a.Hkv) {
+            head = 0;
+            row0 += p.rows;
+            if (row0 >= all) {
+                row0 = 0;
+                ++seq;
+                enter(a);
+                if (left <= 0) return;
+            }
+            unit(a, p);
+        }
+        piece();
+    }
+};
+
+// Places of a tile of rows of one key head.
+__device__ __forceinline__ int places(const PagedArgs& a, const Plan& p, int pos0, int kv, int row0, int rows)
 {
-    constexpr int PER = D / 32;
-    const int lane = threadIdx.x & 31;
-    const float inv = ml.y == 0.f ? 0.f : 1.f / ml.y;
-    IO* out = static_cast<IO*>(a.out) + row * D + lane * PER;
-#pragma unroll
-    for (int e = 0; e < PER; ++e) stv(out + e, ml.y == 0.f ? 0.f : y[e] * inv);
-    if (a.lse && lane == 0) a.lse[row] = ml.y == 0.f ? -INFINITY : (ml.x + log2f(ml.y)) * 0.69314718055994531f;
+    int lo, hi;
+    span(a, p.keys, pos0, kv, row0, rows, lo, hi);
+    return (hi - lo + p.keys - 1) / p.keys + UNIT;
 }
 
-// Rows whose tokens were cut into parts: a warp a row.
+// Where this CTA's stretch begins, by all its WARPS warps (each a run of sequences).  Ends with a barrier.
+template <int WARPS> __device__ void find_start(const PagedArgs& a, const Plan& p, Start& out)
+{
+    __shared__ long long sums[WARPS];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int per = (int)(((long long)a.N + WARPS - 1) / WARPS);
+    const int s0 = (int)min((long long)a.N, (long long)warp * per), s1 = min(a.N, s0 + per);
+    int fault = 0;
+    // places of the sequences base + lane, over all key heads
+    const auto count = [&](int base, int& begin, int& n, int& kv) {
+        int end = 0;
+        begin = n = kv = 0;
+        if (base + lane < s1 && paged_seq(a, base + lane, begin, end, kv, &fault)) n = end - begin;
+        const long long all = (long long)n * a.G;
+        long long sum = 0;
+        const bool few = all <= 4ll * p.rows;
+        if (few)
+            for (int r = 0; r < all; r += p.rows) sum += places(a, p, kv - n, kv, r, (int)min((long long)p.rows, all - r));
+        for (uint32_t left = __ballot_sync(0xffffffffu, !few); left; left &= left - 1) {  // many tiles: by all lanes
+            const int l = __ffs(left) - 1, nn = __shfl_sync(0xffffffffu, n, l), k = __shfl_sync(0xffffffffu, kv, l);
+            const long long aa = (long long)nn * a.G;
+            long long x = 0;
+            for (long long r = (long long)lane * p.rows; r < aa; r += 32ll * p.rows) x += places(a, p, k - nn, k, (int)r, (int)min((long long)p.rows, aa - r));
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+            if (lane == l) sum = x;
+        }
+        return sum * a.Hkv;
+    };
+    const auto scan = [&](long long x) {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        return x;
+    };
+    int begin, n, kv;
+    long long mine = 0;
+    for (int base = s0; base < s1; base += 32) mine += count(base, begin, n, kv);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    if (lane == 0) sums[warp] = mine;
+    if (blockIdx.x == 0 && fault) flag_status(a.dev_status, fault);
+    __syncthreads();
+    long long line = 0, before = 0;
+    for (int w = 0; w < WARPS; ++w) {
+        if (w < warp) before += sums[w];
+        line += sums[w];
+    }
+    const long long x = stretch(line, blockIdx.x, p.ctas);
+    if (threadIdx.x == 0) out.line = line;
+    if (x >= before && x < before + mine) {
+        for (int base = s0; base < s1; base += 32) {
+            const long long c = count(base, begin, n, kv), upto = before + scan(c);
+            const uint32_t hit = __ballot_sync(0xffffffffu, x < upto);
+            if (!hit) {
+                before = __shfl_sync(0xffffffffu, upto, 31);
+                continue;
+            }
+            const int l = __ffs(hit) - 1;
+            long long at = x - __shfl_sync(0xffffffffu, upto - c, l);  // within the sequence
+            const int nn = __shfl_sync(0xffffffffu, n, l), k = __shfl_sync(0xffffffffu, kv, l);
+            const long long all = (long long)nn * a.G;
+            for (long long r0 = 0; r0 < all; r0 += 32ll * p.rows) {
+                const long long r = r0 + (long long)lane * p.rows;
+                const int cost = r < all ? places(a, p, k - nn, k, (int)r, (int)min((long long)p.rows, all - r)) : 0;
+                const long long t = scan((long long)cost * a.Hkv);
+                const uint32_t in = __ballot_sync(0xffffffffu, at < t);
+                if (!in) {
+                    at -= __shfl_sync(0xffffffffu, t, 31);
+                    continue;
+                }
+                if (lane == __ffs(in) - 1) {
+                    at -= t - (long long)cost * a.Hkv;
+                    out.seq = base + l;
+                    out.row0 = (int)r;
+                    out.head = (int)(at / cost);
+                    out.at = (int)(at % cost);
+                }
+                break;
+            }
+            break;
+        }
+    }
+    __syncthreads();
+}
+
+// The parts of the unit that begins in stretch blockIdx.x and goes on: a CTA 32 rows, a lane a row, a warp four
+// channels at a time (as the parts lie), and the rows turned in shared memory.
 constexpr int JT = 256;
 template <typename IO, int D> __global__ void __launch_bounds__(JT) join_kernel(const PagedArgs a, const Plan p)
 {
     ptx::grid_launch_dependents();
     ptx::grid_dependency_wait();
-    const int rows = p.head->joined * a.Hkv * p.part_rows;
-    for (int i = blockIdx.x * (JT / 32) + (threadIdx.x >> 5); i < rows; i += gridDim.x * (JT / 32)) {
-        const int r = i % p.part_rows, th = i / p.part_rows, h = th % a.Hkv;
-        const Joined j = p.joined[th / a.Hkv];
-        if (r >= j.rows) continue;
-        const size_t first = ((size_t)j.part * a.Hkv + h) * p.part_rows + r, step = (size_t)a.Hkv * p.part_rows;
-        float y[D / 32];
-        const float2 ml = join_row<D>(j.parts, [&](int s) { return p.ml + first + s * step; }, [&](int s) { return p.o + (first + s * step) * D; }, y);
-        const int f = j.row0 + r;
-        write_row<IO, D>(a, (size_t)(j.begin + f / a.G) * a.Hq + h * a.G + f % a.G, ml, y);
+    __shared__ float4 turned[32][D / 4 + 1];
+    const int c0 = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = blockIdx.y * 32 + lane;
+    const Cut cut = p.cut[c0];
+    if (blockIdx.y * 32 >= cut.rows) return;
+    // stretches without a place (fewer places than stretches) left nothing
+    const auto used = [&](int s) { return stretch(cut.line, c0 + s, p.ctas) < stretch(cut.line, c0 + s + 1, p.ctas); };
+    const auto cell = [&](int s) { return (size_t)(c0 + s) * 2 + (s == 0); };
+    const int parts = cut.last - c0 + 1;
+    const bool in = r < cut.rows;
+    float m = -INFINITY, l = 0.f;
+#pragma unroll 4
+    for (int s = 0; s < parts; ++s)
+        if (in && used(s)) {
+            const float2 x = p.ml[cell(s) * p.part_rows + r];
+            const float next = fmaxf(m, x.x);
+            if (next != -INFINITY) l = l * exp2f(m - next) + x.y * exp2f(x.x - next);
+            m = next;
+        }
+    const float base = m == -INFINITY ? 0.f : m, inv = l == 0.f ? 0.f : 1.f / l;
+    constexpr int GROUPS = D / 4, EACH = GROUPS < 8 ? 1 : GROUPS / 8;
+    float4 y[EACH];
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+    for (int s = 0; s < parts; ++s)
+        if (in && used(s)) {
+            const float f = exp2f(p.ml[cell(s) * p.part_rows + r].x - base);
+#pragma unroll
+            for (int i = 0; i < EACH; ++i) {
+                const float4 z = p.o[(cell(s) * GROUPS + warp * EACH + i) * p.part_rows + r];
+                y[i].x = fmaf(f, z.x, y[i].x);
+                y[i].y = fmaf(f, z.y, y[i].y);
+                y[i].z = fmaf(f, z.z, y[i].z);
+                y[i].w = fmaf(f, z.w, y[i].w);
+            }
+        }
+#pragma unroll
+    for (int i = 0; i < EACH; ++i)
+        turned[lane][warp * EACH + i] = l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(y[i].x * inv, y[i].y * inv, y[i].z * inv, y[i].w * inv);
+    const auto row_of = [&](int rr) {
+        const int f = cut.row0 + blockIdx.y * 32 + rr;
+        return (size_t)(cut.begin + f / a.G) * a.Hq + cut.head * a.G + f % a.G;
+    };
+    if (a.lse && warp == 0 && in) a.lse[row_of(lane)] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+    __syncthreads();
+    for (int rr = warp; rr < 32 && blockIdx.y * 32 + rr < cut.rows; rr += JT / 32) {
+        IO* out = static_cast<IO*>(a.out) + row_of(rr) * D;
+        for (int i = lane; i < GROUPS; i += 32) {
+            const float4 z = turned[rr][i];
+            if constexpr (sizeof(IO) == 4) {
+                reinterpret_cast<float4*>(out)[i] = z;
+            } else {
+                const __nv_bfloat162 lo = __floats2bfloat162_rn(z.x, z.y), hi = __floats2bfloat162_rn(z.z, z.w);
+                reinterpret_cast<uint2*>(out)[i] = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+            }
+        }
     }
 }
 template <typename IO, int D> cudaError_t launch_join(const PagedArgs& a, const Plan& p, cudaStream_t st)
 {
-    const int64_t most = ((int64_t)p.max_joined * a.Hkv * p.part_rows + JT / 32 - 1) / (JT / 32);
-    return launch_dependent(join_kernel<IO, D>, (unsigned)std::min<int64_t>(most, 152 * 8), JT, 0, st, a, p);
+    return launch_dependent(join_kernel<IO, D>, dim3(p.ctas, (p.part_rows + 31) / 32), JT, 0, st, a, p);
 }
 
 }  // namespace paged

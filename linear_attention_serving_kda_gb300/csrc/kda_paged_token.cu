@@ -10,7 +10,7 @@
 // in two bf16 parts, running maximum and sum of each warp by itself, joined at the pair's end.
 #include <cuda.h>
 
-#include "kda_paged_plan.cuh"
+#include "kda_paged.h"
 #include "kda_ptx.cuh"
 
 namespace kda {
@@ -463,6 +463,62 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
     __syncthreads();
 }
 
+// A warp joins the parts of one row: part s has its maximum and sum at ml(s) and its D values at o(s), both
+// null for a part without any.  Returns the sum and the maximum, and in y the lane's D / 32 neighbouring values, not divided.
+template <int D, class ML, class O> __device__ __forceinline__ float2 join_row(int parts, ML&& ml, O&& o, float (&y)[D / 32])
+{
+    constexpr int PER = D / 32;
+    const int lane = threadIdx.x & 31;
+    float m = -INFINITY, l = 0.f;
+    for (int s = lane; s < parts; s += 32)
+        if (const float2* x = ml(s)) m = fmaxf(m, x->x);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) y[e] = 0.f;
+    for (int s0 = 0; s0 < parts; s0 += 32) {
+        float f = 0.f;
+        const float2* x = s0 + lane < parts ? ml(s0 + lane) : nullptr;
+        if (x) {
+            f = exp2f(x->x - base);
+            l += f * x->y;
+        }
+        const int n = min(32, parts - s0);
+#pragma unroll 4
+        for (int s = 0; s < n; ++s) {
+            const float g = __shfl_sync(0xffffffffu, f, s);
+            const float* v = o(s0 + s);
+            if (!v) continue;
+            if constexpr (PER >= 4) {
+#pragma unroll
+                for (int e = 0; e < PER; e += 4) {
+                    const float4 z = *reinterpret_cast<const float4*>(v + lane * PER + e);
+                    y[e] = fmaf(g, z.x, y[e]);
+                    y[e + 1] = fmaf(g, z.y, y[e + 1]);
+                    y[e + 2] = fmaf(g, z.z, y[e + 2]);
+                    y[e + 3] = fmaf(g, z.w, y[e + 3]);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < PER; ++e) y[e] = fmaf(g, v[lane * PER + e], y[e]);
+            }
+        }
+    }
+    return make_float2(m, warp_sum(l));
+}
+// The joined row to out and lse (row: of [T][Hq]).
+template <typename IO, int D> __device__ __forceinline__ void write_row(const PagedArgs& a, size_t row, float2 ml, const float (&y)[D / 32])
+{
+    constexpr int PER = D / 32;
+    const int lane = threadIdx.x & 31;
+    const float inv = ml.y == 0.f ? 0.f : 1.f / ml.y;
+    IO* out = static_cast<IO*>(a.out) + row * D + lane * PER;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) stv(out + e, ml.y == 0.f ? 0.f : y[e] * inv);
+    if (a.lse && lane == 0) a.lse[row] = ml.y == 0.f ? -INFINITY : (ml.x + log2f(ml.y)) * 0.69314718055994531f;
+}
+
 // The parts of the unit that begins in stretch blockIdx.x and goes on: a warp a row.
 template <int D> __global__ void __launch_bounds__(32 * ROWS) token_join_kernel(const PagedArgs a, const TokenWork work)
 {
@@ -476,9 +532,9 @@ template <int D> __global__ void __launch_bounds__(32 * ROWS) token_join_kernel(
     const auto used = [&](int s) { return stretch(cut.line, blockIdx.x + s) < stretch(cut.line, blockIdx.x + s + 1); };
     const auto cell = [&](int s) { return ((size_t)(blockIdx.x + s) * 2 + (s == 0)) * ROWS + row; };
     float y[D / 32];
-    const float2 ml = paged::join_row<D>(cut.last - (int)blockIdx.x + 1, [&](int s) { return used(s) ? work.ml + cell(s) : nullptr; },
+    const float2 ml = join_row<D>(cut.last - (int)blockIdx.x + 1, [&](int s) { return used(s) ? work.ml + cell(s) : nullptr; },
                                          [&](int s) { return used(s) ? work.o + cell(s) * D : nullptr; }, y);
-    paged::write_row<__nv_bfloat16, D>(a, (size_t)cut.seq * a.Hq + h * a.G + g0 + row, ml, y);
+    write_row<__nv_bfloat16, D>(a, (size_t)cut.seq * a.Hq + h * a.G + g0 + row, ml, y);
 }
 
 bool encode_cache(CUtensorMap* m, const void* base, const PagedArgs& a)
