@@ -153,7 +153,7 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
     find_start<THREADS / 32>(a, p, s.start);
     if (tid == 0) p.cut[blockIdx.x].rows = 0;
     // A wait that runs out ends its role's work (and with it, one by one, the others').
-    const auto wait = [&](uint64_t* bar, uint32_t parity) { return ptx::mbar_wait(bar, parity & 1, WAIT); };
+    const auto wait = [&](uint64_t* bar, uint32_t parity) { return ptx::mbar_wait_short(bar, parity & 1, WAIT); };
     constexpr uint32_t O0 = 256;  // S: columns 0 .. 2 KEYS - 1, O behind
 
     if (warp >= 8) {
@@ -268,74 +268,107 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
                 // the ring holds K0 (K1, with one tile) V0 K1 (K2) V1 ...
                 Place<SLOTS> kp = first, vp = first;
                 vp.on(two ? 1 : min(2, w.count));
-                int kj = 0, vj = 0;  // the tiles at kp and vp
-                const auto scores = [&](int t, int b) {  // of row tile t over the keys at kp, into buffer b
-                    if (t == 0 && !wait(&s.full[kp.slot], kp.phase)) return false;
-                    if (kj == 0 && !wait(&s.rows[t], t ? qcount[1] : qcount[0])) return false;
-                    ptx::tc_fence_after();
-                    if (leader) {
-                        const uint32_t da = qd + t * (128 * DP * 2 / 16), db = kd + kp.slot * STEP;
+                // scores of row tile t over the keys at kp into buffer b, products of the weights there with the values at vp: by the leader.
+                // Between a tile's weights and its next scores nothing is waited for: every instruction there is time without products.
+                const auto scores = [&](int t, int b) {
+                    const uint32_t da = qd + t * (128 * DP * 2 / 16), db = kd + kp.slot * STEP;
 #pragma unroll
-                        for (int k = 0; k < DP / 16; ++k)
-                            mma_ss(tmem + b * KEYS, da + ((k / 4) * (128 * 128) + (k % 4) * 32) / 16, db + ((k / 4) * (KEYS * 128) + (k % 4) * 32) / 16, ID_S, k > 0);
-                        ptx::mma_commit(&s.scores[b]);
-                        if (t == 1 || !two) ptx::mma_commit(&s.empty[kp.slot]);
-                        if (kj == w.count - 1) ptx::mma_commit(&s.free[t]);
-                    }
-                    __syncwarp();
-                    if (t == 1 || !two) {
-                        kp.on(!two && kj == 0 ? 1 : 2);
-                        ++kj;
+                    for (int k = 0; k < DP / 16; ++k)
+                        mma_ss(tmem + b * KEYS, da + ((k / 4) * (128 * 128) + (k % 4) * 32) / 16, db + ((k / 4) * (KEYS * 128) + (k % 4) * 32) / 16, ID_S, k > 0);
+                    ptx::mma_commit(&s.scores[b]);
+                };
+                const auto values = [&](int t, int b, int j) {
+                    const uint32_t db = vd + vp.slot * STEP;
+#pragma unroll
+                    for (int k = 0; k < KEYS / 16; ++k)
+                        mma_ts(tmem + O0 + t * DP, tmem + b * KEYS + k * 8, db + k * 2048 / 16, ID_O, k > 0 || j > 0);
+                };
+                const auto values_here = [&](int j) {
+                    if (!wait(&s.full[vp.slot], vp.phase)) return false;
+                    const int have = w.k1 - w.k0 - j * KEYS;
+                    if (have < KEYS) {  // what lies behind the tokens may be anything: zeros, whose weights are zero
+                        for (int i = lane; i < (KEYS - have) * 8 * BLOCKS; i += 32) {
+                            const int r = have + i / 8 % (KEYS - have), blk = i / (8 * (KEYS - have));
+                            *reinterpret_cast<uint4*>(s.ring + vp.slot * SLOT + blk * (KEYS * 128) + r * 128 + i % 8 * 16) = make_uint4(0, 0, 0, 0);
+                        }
+                        ptx::fence_proxy_async_smem();
+                        __syncwarp();
                     }
                     return true;
                 };
-                const auto values = [&](int t, int b) {  // of row tile t over the values at vp, weights in buffer b
-                    if (t == 0) {
-                        if (!wait(&s.full[vp.slot], vp.phase)) return false;
-                        const int have = w.k1 - w.k0 - vj * KEYS;
-                        if (have < KEYS) {  // what lies behind the tokens may be anything: zeros, whose weights are zero
-                            for (int i = lane; i < (KEYS - have) * 8 * BLOCKS; i += 32) {
-                                const int r = have + i / 8 % (KEYS - have), blk = i / (8 * (KEYS - have));
-                                *reinterpret_cast<uint4*>(s.ring + vp.slot * SLOT + blk * (KEYS * 128) + r * 128 + i % 8 * 16) = make_uint4(0, 0, 0, 0);
-                            }
-                            ptx::fence_proxy_async_smem();
-                            __syncwarp();
+                if (two) {
+                    ok = wait(&s.full[kp.slot], kp.phase) && wait(&s.rows[0], qcount[0]);
+                    if (ok && leader) scores(0, 0);
+                    ok = ok && wait(&s.rows[1], qcount[1]);
+                    if (ok && leader) {
+                        scores(1, 1);
+                        ptx::mma_commit(&s.empty[kp.slot]);
+                        if (w.count == 1) {
+                            ptx::mma_commit(&s.free[0]);
+                            ptx::mma_commit(&s.free[1]);
                         }
                     }
-                    if (vj == 0 && !wait(&s.taken[t], (t ? qcount[1] : qcount[0]) + 1)) return false;  // O of the item before is read
-                    if (!wait(&s.weights[b], b ? wcount[1] : wcount[0])) return false;
-                    ++(b ? wcount[1] : wcount[0]);
-                    ptx::tc_fence_after();
-                    if (leader) {
-                        const uint32_t db = vd + vp.slot * STEP;
-#pragma unroll
-                        for (int k = 0; k < KEYS / 16; ++k)
-                            mma_ts(tmem + O0 + t * DP, tmem + b * KEYS + k * 8, db + k * 2048 / 16, ID_O, k > 0 || vj > 0);
-                        ptx::mma_commit(&s.product[b]);
-                        if (t == 1 || !two) ptx::mma_commit(&s.empty[vp.slot]);
-                    }
                     __syncwarp();
-                    if (t == 1 || !two) {
-                        vp.on(!two && vj == w.count - 2 ? 1 : 2);
-                        ++vj;
-                    }
-                    return true;
-                };
-                ok = scores(0, 0);
-                if (two) ok = ok && scores(1, 1);
-                else if (w.count > 1) ok = ok && scores(0, 1);
-                if (two)
+                    kp.on(2);
                     for (int j = 0; j < w.count && ok; ++j) {
-                        ok = values(0, 0);
-                        if (j + 1 < w.count) ok = ok && scores(0, 0);
-                        ok = ok && values(1, 1);
-                        if (j + 1 < w.count) ok = ok && scores(1, 1);
+                        const bool more = j + 1 < w.count;
+                        ok = values_here(j) && (!more || wait(&s.full[kp.slot], kp.phase));
+                        if (j == 0) ok = ok && wait(&s.taken[0], qcount[0] + 1) && wait(&s.taken[1], qcount[1] + 1);  // O of the unit before is read
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            ok = ok && wait(&s.weights[t], wcount[t]);
+                            ++wcount[t];
+                            ptx::tc_fence_after();
+                            if (ok && leader) {
+                                values(t, t, j);
+                                if (more) {
+                                    scores(t, t);
+                                    if (t == 1) ptx::mma_commit(&s.empty[kp.slot]);
+                                    if (j + 2 == w.count) ptx::mma_commit(&s.free[t]);
+                                } else {
+                                    ptx::mma_commit(&s.product[t]);
+                                }
+                                if (t == 1) ptx::mma_commit(&s.empty[vp.slot]);
+                            }
+                            __syncwarp();
+                        }
+                        kp.on(2);
+                        vp.on(2);
                     }
-                else
+                } else {
+                    ok = wait(&s.rows[0], qcount[0]);
+                    for (int j = 0; j < min(2, w.count) && ok; ++j) {
+                        ok = wait(&s.full[kp.slot], kp.phase);
+                        if (ok && leader) {
+                            scores(0, j);
+                            ptx::mma_commit(&s.empty[kp.slot]);
+                            if (j + 1 == w.count) ptx::mma_commit(&s.free[0]);
+                        }
+                        __syncwarp();
+                        kp.on(j == 0 ? 1 : 2);
+                    }
                     for (int j = 0; j < w.count && ok; ++j) {
-                        ok = values(0, j & 1);
-                        if (j + 2 < w.count) ok = ok && scores(0, j & 1);
+                        const bool more = j + 2 < w.count;
+                        const int b = j & 1;
+                        ok = values_here(j) && (!more || wait(&s.full[kp.slot], kp.phase));
+                        if (j == 0) ok = ok && wait(&s.taken[0], qcount[0] + 1);
+                        ok = ok && wait(&s.weights[b], b ? wcount[1]++ : wcount[0]++);
+                        ptx::tc_fence_after();
+                        if (ok && leader) {
+                            values(0, b, j);
+                            ptx::mma_commit(&s.product[b]);
+                            if (more) {
+                                scores(0, b);
+                                ptx::mma_commit(&s.empty[kp.slot]);
+                                if (j + 3 == w.count) ptx::mma_commit(&s.free[0]);
+                            }
+                            ptx::mma_commit(&s.empty[vp.slot]);
+                        }
+                        __syncwarp();
+                        kp.on(2);
+                        vp.on(j == w.count - 2 ? 1 : 2);
                     }
+                }
                 const uint32_t end = first.slot + 2 * w.count + (w.staged ? w.tiles * L::OUT : 0);
                 first.slot = end % SLOTS;
                 first.phase ^= end / SLOTS & 1;
@@ -354,7 +387,7 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
         const int t = warp >> 2, r = tid & 127;  // tile, row of it
         const uint32_t tl = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes
         const float c = a.scale * 1.4426950408889634f;
-        uint32_t scount[2] = {0, 0}, pcount[2] = {0, 0}, kt = 0, use = 0;
+        uint32_t scount[2] = {0, 0}, sbase[2] = {0, 0}, pcount[2] = {0, 0}, kt = 0, use = 0;
         bool ok = true;
         Work w;
         for (w.begin_at(a, p, s.start); w.left > 0; w.next(a, p)) {
@@ -445,8 +478,8 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
             kt += w.count;
             if (mine) {
                 if (w.count > 0) {
-                    const int last = w.tiles == 2 ? w.steps - 2 + t : w.steps - 1, b = last & 1;
-                    ok = ok && wait(&s.product[b], pcount[b] + last / 2);
+                    const int last = w.steps - 1, b = w.tiles == 2 ? t : last & 1;
+                    ok = ok && wait(&s.product[b], w.tiles == 2 ? pcount[b] : pcount[b] + last / 2);
                     ptx::tc_fence_after();
                 }
                 const bool has = row < w.rows && ok;
@@ -539,9 +572,10 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
             }
             if (tid == 0 && ok && w.t0 == 0 && !w.whole())
                 p.cut[blockIdx.x] = {s.start.line, w.begin, w.row0, w.rows, w.head, owner(s.start.line, w.end() - 1, p.ctas)};
-            for (int b = 0; b < 2; ++b) pcount[b] += w.tiles == 2 ? w.count : (w.count + 1 - b) / 2;
-            scount[0] = pcount[0];
-            scount[1] = pcount[1];
+            for (int b = 0; b < 2; ++b) {
+                scount[b] = sbase[b] += w.tiles == 2 ? w.count : (w.count + 1 - b) / 2;
+                pcount[b] += w.tiles == 2 ? min(w.count, 1) : (w.count + 1 - b) / 2;
+            }
             // the other warpgroup, without rows in this item, may not run ahead over phases of barriers that it did not wait for
             if (L::TILES == 2 && w.tiles == 1) {
                 asm volatile("bar.sync 1, 256;" ::: "memory");
