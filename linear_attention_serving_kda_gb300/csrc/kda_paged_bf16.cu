@@ -153,7 +153,7 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
     find_start<THREADS / 32>(a, p, s.start);
     if (tid == 0) p.cut[blockIdx.x].rows = 0;
     // A wait that runs out ends its role's work (and with it, one by one, the others').
-    const auto wait = [&](uint64_t* bar, uint32_t parity) { return ptx::mbar_wait_short(bar, parity & 1, WAIT); };
+    const auto wait = [&](uint64_t* bar, uint32_t parity) { return ptx::mbar_wait(bar, parity & 1, WAIT); };
     constexpr uint32_t O0 = 256;  // S: columns 0 .. 2 KEYS - 1, O behind
 
     if (warp >= 8) {
@@ -321,6 +321,7 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
                             ptx::tc_fence_after();
                             if (ok && leader) {
                                 values(t, t, j);
+                                if (t == 1) ptx::mma_commit(&s.empty[vp.slot]);
                                 if (more) {
                                     scores(t, t);
                                     if (t == 1) ptx::mma_commit(&s.empty[kp.slot]);
@@ -328,7 +329,6 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
                                 } else {
                                     ptx::mma_commit(&s.product[t]);
                                 }
-                                if (t == 1) ptx::mma_commit(&s.empty[vp.slot]);
                             }
                             __syncwarp();
                         }
@@ -350,21 +350,28 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
                     for (int j = 0; j < w.count && ok; ++j) {
                         const bool more = j + 2 < w.count;
                         const int b = j & 1;
-                        ok = values_here(j) && (!more || wait(&s.full[kp.slot], kp.phase));
+                        ok = values_here(j);
                         if (j == 0) ok = ok && wait(&s.taken[0], qcount[0] + 1);
+                        const bool there = __all_sync(0xffffffffu, more && ptx::mbar_test(&s.full[kp.slot], kp.phase));
                         ok = ok && wait(&s.weights[b], b ? wcount[1]++ : wcount[0]++);
                         ptx::tc_fence_after();
+                        const auto next = [&] {
+                            scores(0, b);
+                            ptx::mma_commit(&s.empty[kp.slot]);
+                            if (j + 3 == w.count) ptx::mma_commit(&s.free[0]);
+                        };
                         if (ok && leader) {
                             values(0, b, j);
                             ptx::mma_commit(&s.product[b]);
-                            if (more) {
-                                scores(0, b);
-                                ptx::mma_commit(&s.empty[kp.slot]);
-                                if (j + 3 == w.count) ptx::mma_commit(&s.free[0]);
-                            }
                             ptx::mma_commit(&s.empty[vp.slot]);
+                            if (there) next();
                         }
                         __syncwarp();
+                        if (more && !there) {  // keys that are not there yet do not hold up the product
+                            ok = ok && wait(&s.full[kp.slot], kp.phase);
+                            if (ok && leader) next();
+                            __syncwarp();
+                        }
                         kp.on(2);
                         vp.on(j == w.count - 2 ? 1 : 2);
                     }
@@ -409,28 +416,36 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
                     ++scount[b];
                     ptx::tc_fence_after();
                     if (live && ok) {
-                        float v[KEYS];
-                        if constexpr (KEYS == 128) ptx::tmem_ld128(tl + b * KEYS, v);
-                        else ptx::tmem_ld64(tl + b * KEYS, v);
+                        // 64 scores at a time: the first ones' maximum while the second ones come
+                        float v[KEYS], mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                        auto& v0 = *reinterpret_cast<float(*)[64]>(v);
+                        auto& v1 = *reinterpret_cast<float(*)[64]>(v + (KEYS - 64));
                         const uint32_t hide = *reinterpret_cast<volatile uint32_t*>(&s.hidden[(kt + j) & 7]);
-                        if (__any_sync(0xffffffffu, k0 + KEYS > hi || k0 < lo) || hide) {
-                            const int box_shift = min(a.page_shift, KEYS == 128 ? 7 : 6);
+                        const bool masked = __any_sync(0xffffffffu, k0 + KEYS > hi || k0 < lo) || hide;
+                        const int box_shift = min(a.page_shift, KEYS == 128 ? 7 : 6);
+                        const auto look = [&](int from) {
+                            if (masked)
 #pragma unroll
-                            for (int i = 0; i < KEYS; i += 32) {
-                                uint32_t seen = low_bits(hi - k0 - i) & ~low_bits(lo - k0 - i);
-                                if ((hide >> (i >> box_shift)) & 1) seen &= 0xffff0000u;
-                                if ((hide >> ((i + 16) >> box_shift)) & 1) seen &= 0x0000ffffu;
+                                for (int i = from; i < from + 64; i += 32) {
+                                    uint32_t seen = low_bits(hi - k0 - i) & ~low_bits(lo - k0 - i);
+                                    if ((hide >> (i >> box_shift)) & 1) seen &= 0xffff0000u;
+                                    if ((hide >> ((i + 16) >> box_shift)) & 1) seen &= 0x0000ffffu;
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) v[i + e] = (seen >> e) & 1 ? v[i + e] : -INFINITY;
-                            }
+                                    for (int e = 0; e < 32; ++e) v[i + e] = (seen >> e) & 1 ? v[i + e] : -INFINITY;
+                                }
+#pragma unroll
+                            for (int i = from; i < from + 64; i += 8)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], v[i + 2 * e], v[i + 2 * e + 1]);
+                        };
+                        ptx::tmem_ld64_async(tl + b * KEYS, v0);
+                        ptx::tmem_wait_ld64(v0);
+                        if constexpr (KEYS == 128) ptx::tmem_ld64_async(tl + b * KEYS + 64, v1);
+                        look(0);
+                        if constexpr (KEYS == 128) {
+                            ptx::tmem_wait_ld64(v1);
+                            look(64);
                         }
-                        float mx[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) mx[i] = fmaxf(v[2 * i], v[2 * i + 1]);
-#pragma unroll
-                        for (int i = 8; i < KEYS; i += 8)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], v[i + 2 * e], v[i + 2 * e + 1]);
                         const float most = c * fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                         const bool grow = most > m + LAG || (m == -INFINITY && most > m);
                         if (__any_sync(0xffffffffu, grow)) {
