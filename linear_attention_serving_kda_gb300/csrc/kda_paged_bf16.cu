@@ -66,6 +66,14 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint3
         : "memory");
 }
 
+// The first lane's value, which the compiler then knows to be the warp's: operands of products come from uniform registers,
+// and moving each one there by itself was most of the time that issuing them took.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ void commit_to(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
 // A place in the ring of SLOTS tiles and the parity of its use.
 template <int SLOTS> struct Place {
     uint32_t slot = 0, phase = 0;
@@ -270,18 +278,26 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
                 vp.on(two ? 1 : min(2, w.count));
                 // scores of row tile t over the keys at kp into buffer b, products of the weights there with the values at vp: by the leader.
                 // Between a tile's weights and its next scores nothing is waited for: every instruction there is time without products.
+                uint32_t db, ebar, dv, vbar;  // operands and barriers of the slots at kp and vp
+                const auto at_keys = [&] {
+                    db = uniform(kd + kp.slot * STEP);
+                    ebar = uniform(ptx::smem_u32(&s.empty[kp.slot]));
+                };
+                const auto at_values = [&] {
+                    dv = uniform(vd + vp.slot * STEP);
+                    vbar = uniform(ptx::smem_u32(&s.empty[vp.slot]));
+                };
                 const auto scores = [&](int t, int b) {
-                    const uint32_t da = qd + t * (128 * DP * 2 / 16), db = kd + kp.slot * STEP;
+                    const uint32_t da = qd + t * (128 * DP * 2 / 16);
 #pragma unroll
                     for (int k = 0; k < DP / 16; ++k)
                         mma_ss(tmem + b * KEYS, da + ((k / 4) * (128 * 128) + (k % 4) * 32) / 16, db + ((k / 4) * (KEYS * 128) + (k % 4) * 32) / 16, ID_S, k > 0);
                     ptx::mma_commit(&s.scores[b]);
                 };
                 const auto values = [&](int t, int b, int j) {
-                    const uint32_t db = vd + vp.slot * STEP;
 #pragma unroll
                     for (int k = 0; k < KEYS / 16; ++k)
-                        mma_ts(tmem + O0 + t * DP, tmem + b * KEYS + k * 8, db + k * 2048 / 16, ID_O, k > 0 || j > 0);
+                        mma_ts(tmem + O0 + t * DP, tmem + b * KEYS + k * 8, dv + k * 2048 / 16, ID_O, k > 0 || j > 0);
                 };
                 const auto values_here = [&](int j) {
                     if (!wait(&s.full[vp.slot], vp.phase)) return false;
@@ -296,13 +312,15 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
                     }
                     return true;
                 };
+                at_keys();
                 if (two) {
                     ok = wait(&s.full[kp.slot], kp.phase) && wait(&s.rows[0], qcount[0]);
                     if (ok && leader) scores(0, 0);
+                    __syncwarp();
                     ok = ok && wait(&s.rows[1], qcount[1]);
                     if (ok && leader) {
                         scores(1, 1);
-                        ptx::mma_commit(&s.empty[kp.slot]);
+                        commit_to(ebar);
                         if (w.count == 1) {
                             ptx::mma_commit(&s.free[0]);
                             ptx::mma_commit(&s.free[1]);
@@ -312,6 +330,8 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
                     kp.on(2);
                     for (int j = 0; j < w.count && ok; ++j) {
                         const bool more = j + 1 < w.count;
+                        at_keys();
+                        at_values();
                         ok = values_here(j) && (!more || wait(&s.full[kp.slot], kp.phase));
                         if (j == 0) ok = ok && wait(&s.taken[0], qcount[0] + 1) && wait(&s.taken[1], qcount[1] + 1);  // O of the unit before is read
 #pragma unroll
@@ -321,10 +341,10 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
                             ptx::tc_fence_after();
                             if (ok && leader) {
                                 values(t, t, j);
-                                if (t == 1) ptx::mma_commit(&s.empty[vp.slot]);
+                                if (t == 1) commit_to(vbar);
                                 if (more) {
                                     scores(t, t);
-                                    if (t == 1) ptx::mma_commit(&s.empty[kp.slot]);
+                                    if (t == 1) commit_to(ebar);
                                     if (j + 2 == w.count) ptx::mma_commit(&s.free[t]);
                                 } else {
                                     ptx::mma_commit(&s.product[t]);
@@ -338,10 +358,11 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
                 } else {
                     ok = wait(&s.rows[0], qcount[0]);
                     for (int j = 0; j < min(2, w.count) && ok; ++j) {
+                        at_keys();
                         ok = wait(&s.full[kp.slot], kp.phase);
                         if (ok && leader) {
                             scores(0, j);
-                            ptx::mma_commit(&s.empty[kp.slot]);
+                            commit_to(ebar);
                             if (j + 1 == w.count) ptx::mma_commit(&s.free[0]);
                         }
                         __syncwarp();
@@ -350,6 +371,8 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
                     for (int j = 0; j < w.count && ok; ++j) {
                         const bool more = j + 2 < w.count;
                         const int b = j & 1;
+                        at_keys();
+                        at_values();
                         ok = values_here(j);
                         if (j == 0) ok = ok && wait(&s.taken[0], qcount[0] + 1);
                         const bool there = __all_sync(0xffffffffu, more && ptx::mbar_test(&s.full[kp.slot], kp.phase));
@@ -357,13 +380,13 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
                         ptx::tc_fence_after();
                         const auto next = [&] {
                             scores(0, b);
-                            ptx::mma_commit(&s.empty[kp.slot]);
+                            commit_to(ebar);
                             if (j + 3 == w.count) ptx::mma_commit(&s.free[0]);
                         };
                         if (ok && leader) {
                             values(0, b, j);
                             ptx::mma_commit(&s.product[b]);
-                            ptx::mma_commit(&s.empty[vp.slot]);
+                            commit_to(vbar);
                             if (there) next();
                         }
                         __syncwarp();
