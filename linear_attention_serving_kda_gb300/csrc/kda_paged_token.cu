@@ -1,12 +1,12 @@
 // kda_paged_token.cu -- attention of single bf16 rows over a paged cache.
 //
 // Every cached value is read once for the G query heads that share it, so HBM bandwidth is the bound: a row's
-// products are a handful a byte.  All that matters is that every SM keeps loading until the last byte: the tiles of 64
-// tokens of all (sequence, key head) pairs form one line, and each of CTAS CTAs takes an equal stretch of it, whatever the
+// products are a handful a byte.  All that matters is that every SM keeps loading until the last byte: the tiles
+// of all (sequence, key head) pairs form one line, and each of CTAS CTAs takes an equal stretch of it, whatever the
 // lengths.  A pair within one stretch is written out; one that stretches cut leaves a part in the workspace for each
 // of them, and token_join_kernel adds the parts.
-// A warp loads (tensor copies, a ring of tiles); eight warps, in two teams that take the tiles in turn, hold 16 tokens of a tile
-// each: scores and values by mma.sync with up to 16 heads as rows (a tcgen05 tile would have 128 of them, nearly all empty), weights
+// A warp loads (tensor copies, a ring of tiles); teams of warps that take the tiles in turn hold 16 tokens of a tile
+// a warp: scores and values by mma.sync with up to 16 heads as rows (a tcgen05 tile would have 128 of them, nearly all empty), weights
 // in two bf16 parts, running maximum and sum of each warp by itself, joined at the pair's end.
 #include <cuda.h>
 
@@ -17,10 +17,7 @@ namespace kda {
 namespace {
 
 constexpr int CTAS = 152;     // one an SM
-constexpr int KEYS = 64;      // tokens of a tile
 constexpr int ROWS = 16;      // heads of a unit
-constexpr int WARPS = 8;      // consumers
-constexpr int TT = 32 * (WARPS + 1);
 constexpr int KNOWN = 1024;   // sequences whose lengths a CTA keeps
 constexpr uint32_t WAIT = 1u << 22;
 constexpr float LAG = 8.f;
@@ -52,11 +49,17 @@ size_t lay_out(TokenWork& w, const PagedArgs& a)
     return at;
 }
 
+// Teams of TEAM warps, 16 tokens of a tile each, take the tiles in turn.  A stage of the ring belongs to one team (their
+// number divides the stages'), so that whoever waits for a stage has waited for each of its uses: parities tell two apart, not three.
 template <int D> struct Token {
     static constexpr int DP = D < 64 ? 64 : D, BLOCKS = DP / 64;
+    static constexpr int TEAM = D == 256 ? 2 : 4, TEAMS = D == 256 ? 3 : 2, WARPS = TEAM * TEAMS;
+    static constexpr int THREADS = 32 * (WARPS + 1);
+    static constexpr int KEYS = 16 * TEAM;                        // tokens of a tile
     static constexpr int HALF = KEYS * DP * 2, STAGE = 2 * HALF;  // keys, then values
-    static constexpr int STAGES = D == 256 ? 3 : D == 128 ? 6 : 8;
+    static constexpr int STAGES = D >= 128 ? 6 : 8;
     static constexpr int CH = D == 256 ? 16 : 32;
+    static_assert(STAGES % TEAMS == 0, "a stage belongs to one team");
     struct Smem {
         unsigned char ring[STAGES * STAGE];
         unsigned char q[2][ROWS * D * 2];
@@ -64,7 +67,7 @@ template <int D> struct Token {
         float2 ml[WARPS][ROWS];
         uint64_t full[STAGES], empty[STAGES], qfull[2], qempty[2];
         int kv[KNOWN];                    // lengths from the stretch's first sequence on, -1: skipped
-        long long sum[TT / 32];
+        long long sum[WARPS + 1];
         uint32_t hidden[STAGES];
         int first, dead;
         long long offset;
@@ -103,7 +106,7 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, int x, 
 }
 
 // Tokens lo .. kv - 1 are seen; tiles count from lo's page (or tile within a page) on.
-struct Span {
+template <int KEYS> struct Span {
     int lo, start, n;
     __device__ __forceinline__ Span(const PagedArgs& a, int kv)
     {
@@ -130,7 +133,7 @@ struct Walk {
     long long left;          // tiles of the stretch from t0 on
 };
 
-template <class S> __device__ __forceinline__ void enter(const PagedArgs& a, const S& sm, Walk& w)
+template <int KEYS, class S> __device__ __forceinline__ void enter(const PagedArgs& a, const S& sm, Walk& w)
 {
     while (true) {  // sequences without tokens are passed over; one with tokens follows while tiles are left
         const int i = w.s - sm.first;
@@ -143,39 +146,39 @@ template <class S> __device__ __forceinline__ void enter(const PagedArgs& a, con
         if (w.kv >= 0) break;
         ++w.s;
     }
-    const Span x(a, w.kv);
+    const Span<KEYS> x(a, w.kv);
     w.lo = x.lo;
     w.start = x.start;
     w.n = x.n;
 }
-template <class S> __device__ __forceinline__ void begin_walk(const PagedArgs& a, const S& sm, Walk& w, long long tiles)
+template <int KEYS, class S> __device__ __forceinline__ void begin_walk(const PagedArgs& a, const S& sm, Walk& w, long long tiles)
 {
     w.s = sm.first;
     w.left = tiles;
     if (tiles <= 0) return;
-    enter(a, sm, w);
+    enter<KEYS>(a, sm, w);
     w.u = (int)(sm.offset / w.n);
     w.t0 = (int)(sm.offset % w.n);
     w.t1 = (int)min((long long)w.n, w.t0 + w.left);
 }
-template <class S> __device__ __forceinline__ void next_unit(const PagedArgs& a, const S& sm, Walk& w, int units)
+template <int KEYS, class S> __device__ __forceinline__ void next_unit(const PagedArgs& a, const S& sm, Walk& w, int units)
 {
     w.left -= w.t1 - w.t0;
     if (w.left <= 0) return;
     if (++w.u == units) {
         w.u = 0;
         ++w.s;
-        enter(a, sm, w);
+        enter<KEYS>(a, sm, w);
     }
     w.t0 = 0;
     w.t1 = (int)min((long long)w.n, w.left);
 }
 
-template <int D> __global__ void __launch_bounds__(TT, 1)
+template <int D> __global__ void __launch_bounds__(Token<D>::THREADS, 1)
 paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap)
 {
     using L = Token<D>;
-    constexpr int STAGES = L::STAGES, BLOCKS = L::BLOCKS;
+    constexpr int STAGES = L::STAGES, BLOCKS = L::BLOCKS, KEYS = L::KEYS, WARPS = L::WARPS, TEAM = L::TEAM, TT = L::THREADS;
     extern __shared__ __align__(1024) unsigned char raw[];
     auto& s = *reinterpret_cast<typename L::Smem*>(raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, blocks = (a.G + ROWS - 1) / ROWS, units = a.Hkv * blocks;
@@ -183,7 +186,7 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
     if (tid == 0) {
         for (int i = 0; i < STAGES; ++i) {
             ptx::mbar_init(&s.full[i], 1);
-            ptx::mbar_init(&s.empty[i], WARPS / 2);
+            ptx::mbar_init(&s.empty[i], TEAM);
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&s.qfull[i], 1);
@@ -200,7 +203,7 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
     const int per = (a.N + TT - 1) / TT, s0 = min(tid * per, a.N), s1 = min(s0 + per, a.N);
     long long mine = 0;
     int fault = 0;
-    for (int i = s0; i < s1; ++i) mine += Span(a, length_of(a, i, &fault)).n;
+    for (int i = s0; i < s1; ++i) mine += Span<KEYS>(a, length_of(a, i, &fault)).n;
     if (blockIdx.x == 0 && fault) flag_status(a.dev_status, fault);
     long long before = mine;
 #pragma unroll
@@ -223,7 +226,7 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
     if (x0 < x1 && before <= x0 && x0 < before + mine * units) {
         int i = s0, f = 0;
         for (;; ++i) {
-            const int n = Span(a, length_of(a, i, &f)).n;
+            const int n = Span<KEYS>(a, length_of(a, i, &f)).n;
             if (x0 < before + (long long)n * units) break;
             before += (long long)n * units;
         }
@@ -242,14 +245,14 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
         return false;
     };
     Walk w;
-    begin_walk(a, s, w, x1 - x0);
+    begin_walk<KEYS>(a, s, w, x1 - x0);
     bool ok = true;
     if (warp == WARPS) {
         // ---- loads
         const uint64_t once = ptx::policy_evict_first();
         const int box = min(KEYS, 1 << a.page_shift), boxes = KEYS / box;
         uint32_t use = 0, unit = 0;
-        for (; w.left > 0 && ok; next_unit(a, s, w, units), ++unit) {
+        for (; w.left > 0 && ok; next_unit<KEYS>(a, s, w, units), ++unit) {
             const int h = w.u / blocks, g0 = w.u % blocks * ROWS, rows = min(ROWS, a.G - g0);
             if (!(ok = wait(&s.qempty[unit & 1], (unit >> 1) + 1))) break;
             if (lane == 0) {
@@ -286,13 +289,13 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
             for (uint32_t u = unit > 1 ? unit - 1 : 0; u <= unit; ++u) ptx::mbar_wait(&s.qfull[u & 1], (u >> 1) & 1, 1u << 12);
         }
     } else {
-        const int team = warp >> 2, k16 = (warp & 3) * 16;  // this warp's tokens of a tile
+        const int team = warp / TEAM, k16 = warp % TEAM * 16;  // this warp's tokens of a tile
         const float c = a.scale * 1.4426950408889634f;
         uint32_t use = 0, unit = 0;
         const uint32_t ring = ptx::smem_u32(s.ring);
         if (tid == 0) work.cut[blockIdx.x].seq = -1;
         // (a wait that ran out: the warps go on without waiting and without tiles, so that they still meet at the barriers)
-        for (; w.left > 0; next_unit(a, s, w, units), ++unit) {
+        for (; w.left > 0; next_unit<KEYS>(a, s, w, units), ++unit) {
             const int h = w.u / blocks, g0 = w.u % blocks * ROWS, rows = min(ROWS, a.G - g0);
             ok = ok && wait(&s.qfull[unit & 1], unit >> 1);
             const uint32_t qbase = ptx::smem_u32(s.q[unit & 1]) + (lane & 15) * (D * 2) + (lane >> 4) * 16;
@@ -308,12 +311,12 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
             for (int t = w.t0; t < w.t1; ++t, ++use) {
-                if ((use & 1) != (uint32_t)team) continue;
+                if (use % L::TEAMS != (uint32_t)team) continue;
                 const int stage = use % STAGES, k0 = w.start + t * KEYS + k16;
                 if (!ok || !(ok = wait(&s.full[stage], use / STAGES))) continue;
                 const uint32_t hide = *reinterpret_cast<volatile uint32_t*>(&s.hidden[stage]);
                 const uint32_t kb = ring + stage * L::STAGE, vb = kb + L::HALF;
-                const int box_shift = min(a.page_shift, 6);
+                const int box_shift = min(a.page_shift, KEYS == 64 ? 6 : 5);
                 const bool gone = (hide >> (k16 >> box_shift)) & 1;
                 const bool part = k0 + 16 > w.kv || k0 < w.lo || gone;
                 if (part) {
@@ -401,7 +404,7 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(&s.empty[stage]);
             }
-            // ---- the eight warps' sums together
+            // ---- the warps' sums together
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
@@ -410,7 +413,7 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
             }
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&s.qempty[unit & 1]);
-            asm volatile("bar.sync 1, 256;" ::: "memory");
+            asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory");
             float f[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -420,7 +423,7 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
             }
             // two of CH channels of a row at a time, by a thread each
             constexpr int CH = L::CH;
-            const int row = tid / (CH / 2), ch = tid % (CH / 2) * 2;
+            const int row = tid / (CH / 2), ch = tid % (CH / 2) * 2;  // (threads past the last row have none)
             const bool in = row < rows && !*reinterpret_cast<volatile int*>(&s.dead);
             float top = -INFINITY, sum = 0.f;
             for (int x = 0; x < WARPS; ++x) top = fmaxf(top, s.ml[x][row % ROWS].x);
@@ -437,7 +440,7 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
                     for (int i = 0; i < 2; ++i)
                         *reinterpret_cast<float2*>(&s.o[warp][(lane / 4 + 8 * i) * (CH + 4) + j * 8 + (lane & 3) * 2]) =
                             make_float2(o[e / 8 + j][2 * i] * f[i], o[e / 8 + j][2 * i + 1] * f[i]);
-                asm volatile("bar.sync 1, 256;" ::: "memory");
+                asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory");
                 float2 y = make_float2(0.f, 0.f);
                 if (row < ROWS)
 #pragma unroll
@@ -447,7 +450,7 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
                         sum == 0.f ? 0u : pack_bf16(y.x * inv, y.y * inv);
                     else *reinterpret_cast<float2*>(work.o + cell * D + e + ch) = y;
                 }
-                asm volatile("bar.sync 1, 256;" ::: "memory");
+                asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory");
             }
             if (in && ch == 0) {
                 if (!whole) work.ml[cell] = make_float2(top, sum);
@@ -537,14 +540,14 @@ template <int D> __global__ void __launch_bounds__(32 * ROWS) token_join_kernel(
     write_row<__nv_bfloat16, D>(a, (size_t)cut.seq * a.Hq + h * a.G + g0 + row, ml, y);
 }
 
-bool encode_cache(CUtensorMap* m, const void* base, const PagedArgs& a)
+bool encode_cache(CUtensorMap* m, const void* base, const PagedArgs& a, int keys)
 {
     PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
     if (!enc) return false;
     const cuuint64_t P = (cuuint64_t)1 << a.page_shift;
     const cuuint64_t dims[4] = {(cuuint64_t)a.D, P, (cuuint64_t)a.Hkv, (cuuint64_t)a.num_pages};
     const cuuint64_t strides[3] = {(cuuint64_t)a.token_stride * 2, (cuuint64_t)a.head_stride * 2, (cuuint64_t)a.page_stride * 2};
-    const cuuint32_t box[4] = {64, (cuuint32_t)std::min<cuuint64_t>(P, KEYS), 1, 1};
+    const cuuint32_t box[4] = {64, (cuuint32_t)std::min<cuuint64_t>(P, keys), 1, 1};
     const cuuint32_t estr[4] = {1, 1, 1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -560,10 +563,10 @@ template <int D> cudaError_t launch(const PagedArgs& a, cudaStream_t st)
     cudaError_t e = once.run([](int) { return cudaFuncSetAttribute(paged_token_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
     if (e != cudaSuccess) return e;
     CUtensorMap km, vm;
-    if (!encode_cache(&km, a.k, a) || !encode_cache(&vm, a.v, a)) return cudaErrorInvalidValue;
+    if (!encode_cache(&km, a.k, a, L::KEYS) || !encode_cache(&vm, a.v, a, L::KEYS)) return cudaErrorInvalidValue;
     TokenWork w;
     lay_out(w, a);
-    e = launch_dependent(paged_token_kernel<D>, CTAS, TT, smem, st, a, w, km, vm);
+    e = launch_dependent(paged_token_kernel<D>, CTAS, L::THREADS, smem, st, a, w, km, vm);
     if (e == cudaSuccess) e = launch_dependent(token_join_kernel<D>, CTAS, 32 * std::min(ROWS, a.G), 0, st, a, w);
     return e;
 }

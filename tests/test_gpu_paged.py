@@ -613,6 +613,17 @@ def test_token_many_sequences(cuda_lib, N):
     Attn(Cache([1] * N, kv, Hkv=1, G=2, D=32), cuda_lib, decode=True).run().check()
 
 
+@pytest.mark.parametrize("D", [32, 64, 128, 256])
+def test_token_every_row_of_a_long_batch(cuda_lib, D):
+    """Rings of tiles that wrap many times, at every width: each batch position against the same sequence by itself."""
+    c = Cache([1] * 40, [700 + 211 * i for i in range(40)], Hkv=2, G=3, D=D, page=32)
+    a = Attn(c, cuda_lib, decode=True).run()
+    first = a.out.tensor.clone()
+    for _ in range(20):
+        assert torch.equal(a.run().out.tensor, first)
+    a.check()
+
+
 def test_token_large_scores(cuda_lib):
     for io in ("bf16", "f32"):
         Attn(Cache([1] * 3, [700, 1500, 40], D=128, io=io, spread=30.0), cuda_lib, decode=True).run().check()
