@@ -17,8 +17,7 @@ namespace kda {
 namespace {
 
 constexpr int CTAS = 152;     // one an SM
-constexpr int ROWS = 16;      // heads of a unit
-constexpr int KNOWN = 1024;   // sequences whose lengths a CTA keeps
+constexpr int KNOWN = 512;    // sequences whose lengths a CTA keeps
 constexpr uint32_t WAIT = 1u << 22;
 constexpr float LAG = 8.f;
 
@@ -30,12 +29,16 @@ struct Cut {
 };
 struct TokenWork {
     Cut* cut;                  // [CTAS]
-    float2* ml;                // [CTAS][2][ROWS]: largest score (in powers of two) and sum of the weights;
-    float* o;                  // [CTAS][2][ROWS][D]   0: of a unit that began before, 1: of the one that goes on
+    float2* ml;                // [CTAS][2][rows]: largest score (in powers of two) and sum of the weights;
+    float* o;                  // [CTAS][2][rows][D]   0: of a unit that began before, 1: of the one that goes on
 };
+
+// Heads of a unit: eight (a column block of a product) or sixteen.
+int unit_rows(const PagedArgs& a) { return a.G <= 8 ? 8 : 16; }
 
 size_t lay_out(TokenWork& w, const PagedArgs& a)
 {
+    const size_t rows = unit_rows(a);
     unsigned char* p = static_cast<unsigned char*>(a.workspace);
     size_t at = 0;
     const auto take = [&](size_t n) {
@@ -44,25 +47,26 @@ size_t lay_out(TokenWork& w, const PagedArgs& a)
         return x;
     };
     w.cut = reinterpret_cast<Cut*>(take(sizeof(Cut) * CTAS));
-    w.ml = reinterpret_cast<float2*>(take(sizeof(float2) * CTAS * 2 * ROWS));
-    w.o = reinterpret_cast<float*>(take(sizeof(float) * CTAS * 2 * ROWS * (size_t)a.D));
+    w.ml = reinterpret_cast<float2*>(take(sizeof(float2) * CTAS * 2 * rows));
+    w.o = reinterpret_cast<float*>(take(sizeof(float) * CTAS * 2 * rows * (size_t)a.D));
     return at;
 }
 
 // Teams of TEAM warps, 16 tokens of a tile each, take the tiles in turn.  A stage of the ring belongs to one team (their
 // number divides the stages'), so that whoever waits for a stage has waited for each of its uses: parities tell two apart, not three.
-template <int D> struct Token {
+template <int D, int HB> struct Token {
     static constexpr int DP = D < 64 ? 64 : D, BLOCKS = DP / 64;
-    static constexpr int TEAM = D == 256 ? 2 : 4, TEAMS = D == 256 ? 3 : 2, WARPS = TEAM * TEAMS;
+    static constexpr int ROWS = 8 * HB;
+    static constexpr int TEAM = D == 256 ? 2 : 4, WARPS = HB == 1 ? 12 : D == 256 ? 6 : 8, TEAMS = WARPS / TEAM;  // as registers allow
     static constexpr int THREADS = 32 * (WARPS + 1);
     static constexpr int KEYS = 16 * TEAM;                        // tokens of a tile
     static constexpr int HALF = KEYS * DP * 2, STAGE = 2 * HALF;  // keys, then values
-    static constexpr int STAGES = D >= 128 ? 6 : 8;
-    static constexpr int CH = D == 256 ? 16 : 32;
+    static constexpr int STAGES = D >= 128 ? 6 : 12;
+    static constexpr int CH = 32, QS = D * 2 + 16;                // bytes of a row of q: eight rows in distinct banks
     static_assert(STAGES % TEAMS == 0, "a stage belongs to one team");
     struct Smem {
         unsigned char ring[STAGES * STAGE];
-        unsigned char q[2][ROWS * D * 2];
+        unsigned char q[2][ROWS * QS];
         float o[WARPS][ROWS * (CH + 4)];  // CH channels of every warp's sums at a time
         float2 ml[WARPS][ROWS];
         uint64_t full[STAGES], empty[STAGES], qfull[2], qempty[2];
@@ -89,6 +93,13 @@ __device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t addr)
 {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+// An 8 x 8 block of 16-bit values, turned.
+__device__ __forceinline__ uint32_t turn8(uint32_t x)
+{
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
 }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 {
@@ -174,11 +185,11 @@ template <int KEYS, class S> __device__ __forceinline__ void next_unit(const Pag
     w.t1 = (int)min((long long)w.n, w.left);
 }
 
-template <int D> __global__ void __launch_bounds__(Token<D>::THREADS, 1)
+template <int D, int HB> __global__ void __launch_bounds__(Token<D, HB>::THREADS, 1)
 paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap)
 {
-    using L = Token<D>;
-    constexpr int STAGES = L::STAGES, BLOCKS = L::BLOCKS, KEYS = L::KEYS, WARPS = L::WARPS, TEAM = L::TEAM, TT = L::THREADS;
+    using L = Token<D, HB>;
+    constexpr int ROWS = L::ROWS, STAGES = L::STAGES, BLOCKS = L::BLOCKS, KEYS = L::KEYS, WARPS = L::WARPS, TEAM = L::TEAM, TT = L::THREADS;
     extern __shared__ __align__(1024) unsigned char raw[];
     auto& s = *reinterpret_cast<typename L::Smem*>(raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, blocks = (a.G + ROWS - 1) / ROWS, units = a.Hkv * blocks;
@@ -195,7 +206,7 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
         s.dead = 0;
         ptx::fence_mbar_init();
     }
-    for (int i = tid; i < 2 * ROWS * D / 8; i += TT) reinterpret_cast<uint4*>(s.q)[i] = make_uint4(0, 0, 0, 0);  // rows without a head stay zero
+    for (int i = tid; i < (int)sizeof(s.q) / 16; i += TT) reinterpret_cast<uint4*>(s.q)[i] = make_uint4(0, 0, 0, 0);  // rows without a head stay zero
     ptx::fence_proxy_async_smem();
     ptx::grid_dependency_wait();
 
@@ -255,11 +266,11 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
         for (; w.left > 0 && ok; next_unit<KEYS>(a, s, w, units), ++unit) {
             const int h = w.u / blocks, g0 = w.u % blocks * ROWS, rows = min(ROWS, a.G - g0);
             if (!(ok = wait(&s.qempty[unit & 1], (unit >> 1) + 1))) break;
-            if (lane == 0) {
-                ptx::mbar_arrive_expect_tx(&s.qfull[unit & 1], rows * D * 2);
-                ptx::bulk_g2s(s.q[unit & 1], static_cast<const __nv_bfloat16*>(a.q) + w.s * a.q_stride + (long long)(h * a.G + g0) * D, rows * D * 2,
-                              &s.qfull[unit & 1]);
-            }
+            if (lane == 0) ptx::mbar_arrive_expect_tx(&s.qfull[unit & 1], rows * D * 2);
+            __syncwarp();
+            if (lane < rows)
+                ptx::bulk_g2s(s.q[unit & 1] + lane * L::QS, static_cast<const __nv_bfloat16*>(a.q) + w.s * a.q_stride + (long long)(h * a.G + g0 + lane) * D,
+                              D * 2, &s.qfull[unit & 1]);
             for (int t = w.t0; t < w.t1; ++t, ++use) {
                 const int stage = use % STAGES, k0 = w.start + t * KEYS, tok = k0 + lane % boxes * box;
                 const bool in = tok < w.kv;
@@ -298,18 +309,26 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
         for (; w.left > 0; next_unit<KEYS>(a, s, w, units), ++unit) {
             const int h = w.u / blocks, g0 = w.u % blocks * ROWS, rows = min(ROWS, a.G - g0);
             ok = ok && wait(&s.qfull[unit & 1], unit >> 1);
-            const uint32_t qbase = ptx::smem_u32(s.q[unit & 1]) + (lane & 15) * (D * 2) + (lane >> 4) * 16;
-            constexpr bool KEEP = D <= 128;  // wider rows come from shared memory each time: registers
-            uint32_t qf[KEEP ? D / 16 : 1][4];
+            // tokens are the products' rows, heads their columns: S^T = K Q^T, O^T += V^T W^T
+            const uint32_t qbase = ptx::smem_u32(s.q[unit & 1]) + (lane & 7) * L::QS + (lane >> 3) * 16;
+            constexpr bool KEEP = D * HB <= 128;  // more than that comes from shared memory each time: registers
+            uint32_t qf[HB][KEEP ? D / 32 : 1][4];
             if constexpr (KEEP) {
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) ldsm(qf[k], qbase + k * 32);
+                for (int b = 0; b < HB; ++b)
+#pragma unroll
+                    for (int k = 0; k < D / 32; ++k) ldsm(qf[b][k], qbase + b * 8 * L::QS + k * 64);
             }
-            float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+            float o[HB][D / 16][4], m[HB][2], l[HB][2];  // of this lane's two heads (a block)
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i)
+            for (int b = 0; b < HB; ++b) {
+                m[b][0] = m[b][1] = -INFINITY;
+                l[b][0] = l[b][1] = 0.f;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+                for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[b][i][e] = 0.f;
+            }
             for (int t = w.t0; t < w.t1; ++t, ++use) {
                 if (use % L::TEAMS != (uint32_t)team) continue;
                 const int stage = use % STAGES, k0 = w.start + t * KEYS + k16;
@@ -329,76 +348,86 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
                     ptx::fence_proxy_async_smem();
                     __syncwarp();
                 }
-                float sc[2][4] = {};
+                float sc[2][HB][4] = {};  // even and odd steps apart: half the latency
                 {
-                    const int r = k16 + (lane & 7) + ((lane >> 4) & 1) * 8, ch = (lane >> 3) & 1;
+                    const int r = k16 + (lane & 15), ch = lane >> 4;
                     const uint32_t row = kb + r * 128;
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        uint32_t b[4];
-                        ldsm(b, row + (k / 4) * (KEYS * 128) + ((((k % 4) * 2 + ch) ^ (r & 7)) << 4));
-                        if constexpr (KEEP) {
-                            mma16816(sc[0], qf[k], b[0], b[1]);
-                            mma16816(sc[1], qf[k], b[2], b[3]);
-                        } else {
+                    for (int k = 0; k < D / 32; ++k) {
+                        uint32_t x[2][4];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) ldsm(x[i], row + (k / 2) * (KEYS * 128) + (((k % 2 * 4 + i * 2 + ch) ^ (r & 7)) << 4));
+#pragma unroll
+                        for (int b = 0; b < HB; ++b) {
                             uint32_t q[4];
-                            ldsm(q, qbase + k * 32);
-                            mma16816(sc[0], q, b[0], b[1]);
-                            mma16816(sc[1], q, b[2], b[3]);
+                            if constexpr (!KEEP) ldsm(q, qbase + b * 8 * L::QS + k * 64);
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                if constexpr (KEEP) mma16816(sc[i][b], x[i], qf[b][k][2 * i], qf[b][k][2 * i + 1]);
+                                else mma16816(sc[i][b], x[i], q[2 * i], q[2 * i + 1]);
+                            }
                         }
                     }
                 }
-                if (part) {
+                bool grow = false;
+                float top[HB][2];
 #pragma unroll
-                    for (int nb = 0; nb < 2; ++nb)
+                for (int b = 0; b < HB; ++b) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int tok = k0 + nb * 8 + (lane & 3) * 2 + (e & 1);
-                            if (gone || tok >= w.kv || tok < w.lo) sc[nb][e] = -INFINITY;
-                        }
-                }
-                float top[2];
+                    for (int e = 0; e < 4; ++e) {
+                        sc[0][b][e] += sc[1][b][e];
+                        const int tok = k0 + lane / 4 + (e & 2) * 4;
+                        if (part && (gone || tok >= w.kv || tok < w.lo)) sc[0][b][e] = -INFINITY;
+                    }
 #pragma unroll
-                for (int i = 0; i < 2; ++i) top[i] = c * fmaxf(fmaxf(sc[0][2 * i], sc[0][2 * i + 1]), fmaxf(sc[1][2 * i], sc[1][2 * i + 1]));
-                if (__any_sync(0xffffffffu, top[0] > m[0] + LAG || top[1] > m[1] + LAG)) {
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        float x = top[i];
-                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-                        const float next = fmaxf(m[i], x), f = next == -INFINITY ? 1.f : exp2_sfu(m[i] - next);
-                        m[i] = next;
-                        l[i] *= f;
-#pragma unroll
-                        for (int j = 0; j < D / 8; ++j) {
-                            o[j][2 * i] *= f;
-                            o[j][2 * i + 1] *= f;
-                        }
+                    for (int e = 0; e < 2; ++e) {
+                        top[b][e] = c * fmaxf(sc[0][b][e], sc[0][b][e + 2]);
+                        grow |= top[b][e] > m[b][e] + LAG;
                     }
                 }
-                uint32_t hi[4], lo[4];
+                if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-                for (int nb = 0; nb < 2; ++nb)
+                    for (int b = 0; b < HB; ++b)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float base = m[i] == -INFINITY ? 0.f : m[i];
-                        const float x = exp2_sfu(fmaf(sc[nb][2 * i], c, -base)), y = exp2_sfu(fmaf(sc[nb][2 * i + 1], c, -base));
-                        l[i] += x + y;
+                        for (int e = 0; e < 2; ++e) {
+                            float x = top[b][e];
+#pragma unroll
+                            for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+                            const float next = fmaxf(m[b][e], x), f = next == -INFINITY ? 1.f : exp2_sfu(m[b][e] - next);
+                            m[b][e] = next;
+                            l[b][e] *= f;
+#pragma unroll
+                            for (int j = 0; j < D / 16; ++j) {
+                                o[b][j][e] *= f;
+                                o[b][j][e + 2] *= f;
+                            }
+                        }
+                }
+                uint32_t hi[HB][2], lo[HB][2];
+#pragma unroll
+                for (int b = 0; b < HB; ++b) {
+                    const float base0 = m[b][0] == -INFINITY ? 0.f : m[b][0], base1 = m[b][1] == -INFINITY ? 0.f : m[b][1];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {  // tokens lane / 4, and eight on
+                        const float x = exp2_sfu(fmaf(sc[0][b][2 * i], c, -base0)), y = exp2_sfu(fmaf(sc[0][b][2 * i + 1], c, -base1));
+                        l[b][0] += x;
+                        l[b][1] += y;
                         const uint32_t p = pack_bf16(x, y);
-                        hi[2 * nb + i] = p;
-                        lo[2 * nb + i] = pack_bf16(x - __uint_as_float(p << 16), y - __uint_as_float(p & 0xffff0000u));
+                        hi[b][i] = turn8(p);
+                        lo[b][i] = turn8(pack_bf16(x - __uint_as_float(p << 16), y - __uint_as_float(p & 0xffff0000u)));
                     }
+                }
                 {
-                    const int r = k16 + (lane & 7) + ((lane >> 3) & 1) * 8, ch = lane >> 4;
+                    const int r = k16 + (lane & 7) + (lane >> 4) * 8, ch = (lane >> 3) & 1;
                     const uint32_t row = vb + r * 128;
 #pragma unroll
                     for (int j = 0; j < D / 16; ++j) {
-                        uint32_t b[4];
-                        ldsm_t(b, row + (j / 4) * (KEYS * 128) + ((((j % 4) * 2 + ch) ^ (r & 7)) << 4));
-                        mma16816(o[2 * j], hi, b[0], b[1]);
-                        mma16816(o[2 * j + 1], hi, b[2], b[3]);
-                        mma16816(o[2 * j], lo, b[0], b[1]);
-                        mma16816(o[2 * j + 1], lo, b[2], b[3]);
+                        uint32_t x[4];
+                        ldsm_t(x, row + (j / 4) * (KEYS * 128) + ((((j % 4) * 2 + ch) ^ (r & 7)) << 4));
+#pragma unroll
+                        for (int b = 0; b < HB; ++b) mma16816(o[b][j], x, hi[b][0], hi[b][1]);
+#pragma unroll
+                        for (int b = 0; b < HB; ++b) mma16816(o[b][j], x, lo[b][0], lo[b][1]);
                     }
                 }
                 __syncwarp();
@@ -406,21 +435,25 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
             }
             // ---- the warps' sums together
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-                l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-                if ((lane & 3) == 0) s.ml[warp][lane / 4 + 8 * i] = make_float2(m[i], l[i]);
-            }
+            for (int b = 0; b < HB; ++b)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) l[b][e] += __shfl_xor_sync(0xffffffffu, l[b][e], d);
+                    if (lane < 4) s.ml[warp][b * 8 + lane * 2 + e] = make_float2(m[b][e], l[b][e]);
+                }
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&s.qempty[unit & 1]);
             asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory");
-            float f[2];
+            float f[HB][2];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                float top = -INFINITY;
-                for (int x = 0; x < WARPS; ++x) top = fmaxf(top, s.ml[x][lane / 4 + 8 * i].x);
-                f[i] = m[i] == -INFINITY ? 0.f : exp2_sfu(m[i] - top);
-            }
+            for (int b = 0; b < HB; ++b)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float top = -INFINITY;
+                    for (int x = 0; x < WARPS; ++x) top = fmaxf(top, s.ml[x][b * 8 + (lane & 3) * 2 + e].x);
+                    f[b][e] = m[b][e] == -INFINITY ? 0.f : exp2_sfu(m[b][e] - top);
+                }
             // two of CH channels of a row at a time, by a thread each
             constexpr int CH = L::CH;
             const int row = tid / (CH / 2), ch = tid % (CH / 2) * 2;  // (threads past the last row have none)
@@ -435,11 +468,12 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
 #pragma unroll
             for (int e = 0; e < D; e += CH) {
 #pragma unroll
-                for (int j = 0; j < CH / 8; ++j)
+                for (int b = 0; b < HB; ++b)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        *reinterpret_cast<float2*>(&s.o[warp][(lane / 4 + 8 * i) * (CH + 4) + j * 8 + (lane & 3) * 2]) =
-                            make_float2(o[e / 8 + j][2 * i] * f[i], o[e / 8 + j][2 * i + 1] * f[i]);
+                    for (int j = 0; j < CH / 16; ++j)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            s.o[warp][(b * 8 + (lane & 3) * 2 + (i & 1)) * (CH + 4) + j * 16 + lane / 4 + (i & 2) * 4] = o[b][e / 16 + j][i] * f[b][i & 1];
                 asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory");
                 float2 y = make_float2(0.f, 0.f);
                 if (row < ROWS)
@@ -523,7 +557,7 @@ template <typename IO, int D> __device__ __forceinline__ void write_row(const Pa
 }
 
 // The parts of the unit that begins in stretch blockIdx.x and goes on: a warp a row.
-template <int D> __global__ void __launch_bounds__(32 * ROWS) token_join_kernel(const PagedArgs a, const TokenWork work)
+template <int D, int ROWS> __global__ void __launch_bounds__(32 * ROWS) token_join_kernel(const PagedArgs a, const TokenWork work)
 {
     ptx::grid_launch_dependents();
     ptx::grid_dependency_wait();
@@ -553,22 +587,27 @@ bool encode_cache(CUtensorMap* m, const void* base, const PagedArgs& a, int keys
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D> cudaError_t launch(const PagedArgs& a, cudaStream_t st)
+template <int D, int HB> cudaError_t launch(const PagedArgs& a, cudaStream_t st)
 {
-    using L = Token<D>;
+    using L = Token<D, HB>;
     constexpr int smem = sizeof(typename L::Smem);
     static_assert(smem <= 227 * 1024, "shared memory");
     static_assert(L::HALF % 1024 == 0 && offsetof(typename L::Smem, q) % 16 == 0 && offsetof(typename L::Smem, full) % 8 == 0, "alignment");
     static PerDeviceOnce once;
-    cudaError_t e = once.run([](int) { return cudaFuncSetAttribute(paged_token_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
+    cudaError_t e = once.run([](int) { return cudaFuncSetAttribute(paged_token_kernel<D, HB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
     if (e != cudaSuccess) return e;
     CUtensorMap km, vm;
     if (!encode_cache(&km, a.k, a, L::KEYS) || !encode_cache(&vm, a.v, a, L::KEYS)) return cudaErrorInvalidValue;
     TokenWork w;
     lay_out(w, a);
-    e = launch_dependent(paged_token_kernel<D>, CTAS, L::THREADS, smem, st, a, w, km, vm);
-    if (e == cudaSuccess) e = launch_dependent(token_join_kernel<D>, CTAS, 32 * std::min(ROWS, a.G), 0, st, a, w);
+    e = launch_dependent(paged_token_kernel<D, HB>, CTAS, L::THREADS, smem, st, a, w, km, vm);
+    if (e == cudaSuccess) e = launch_dependent(token_join_kernel<D, L::ROWS>, CTAS, 32 * std::min(L::ROWS, a.G), 0, st, a, w);
     return e;
+}
+
+template <int D> cudaError_t launch_heads(const PagedArgs& a, cudaStream_t st)
+{
+    return unit_rows(a) == 8 ? launch<D, 1>(a, st) : launch<D, 2>(a, st);
 }
 
 }  // namespace
@@ -582,10 +621,10 @@ size_t paged_token_workspace_bytes(const PagedArgs& a)
 cudaError_t launch_paged_token(const PagedArgs& a, cudaStream_t st)
 {
     switch (a.D) {
-    case 32: return launch<32>(a, st);
-    case 64: return launch<64>(a, st);
-    case 128: return launch<128>(a, st);
-    default: return launch<256>(a, st);
+    case 32: return launch_heads<32>(a, st);
+    case 64: return launch_heads<64>(a, st);
+    case 128: return launch_heads<128>(a, st);
+    default: return launch_heads<256>(a, st);
     }
 }
 
