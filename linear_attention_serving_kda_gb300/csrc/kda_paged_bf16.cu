@@ -153,6 +153,10 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
         ptx::fence_mbar_init();
         ptx::fence_proxy_async_smem();
     }
+    if (tid == 32) {  // the maps are the launch's own arguments: no need to wait for them
+        ptx::prefetch_map(&kmap);
+        ptx::prefetch_map(&vmap);
+    }
     if (warp == 8) ptx::tmem_alloc(&s.tmem, 512);
     __syncthreads();
     ptx::tc_fence_after();

@@ -207,6 +207,10 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
         ptx::fence_mbar_init();
     }
     for (int i = tid; i < (int)sizeof(s.q) / 16; i += TT) reinterpret_cast<uint4*>(s.q)[i] = make_uint4(0, 0, 0, 0);  // rows without a head stay zero
+    if (tid == 32) {  // the maps are the launch's own arguments: no need to wait for them
+        ptx::prefetch_map(&kmap);
+        ptx::prefetch_map(&vmap);
+    }
     ptx::fence_proxy_async_smem();
     ptx::grid_dependency_wait();
 

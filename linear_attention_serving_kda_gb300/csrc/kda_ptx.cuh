@@ -127,6 +127,9 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const void* tmap, int x, 
         : "memory");
 }
 
+// Brings a tensor map near before the first copy with it.
+__device__ __forceinline__ void prefetch_map(const void* tmap) { asm volatile("prefetch.tensormap [%0];" ::"l"(tmap) : "memory"); }
+
 // 1-D bulk copy shared -> global in the current bulk group (16-byte aligned
 // addresses, size a multiple of 16).
 __device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t bytes)
