@@ -107,12 +107,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-__device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, int x, int y, int z, int w, uint64_t* bar, uint64_t policy)
+__device__ __forceinline__ void tma_load_5d(void* dst, const void* tmap, int x, int y, int z, int w, int v, uint64_t* bar, uint64_t policy)
 {
     asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(
             ptx::smem_u32(dst)),
-        "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w), "r"(ptx::smem_u32(bar)), "l"(policy)
+        "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(ptx::smem_u32(bar)), "l"(policy)
         : "memory");
 }
 
@@ -290,13 +290,10 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
                     ptx::mbar_arrive_expect_tx(&s.full[stage], n * box * 128 * BLOCKS * 2);
                 }
                 __syncwarp();
-                // lanes over the boxes of keys and values; each lane holds the page of box lane % boxes
-                for (int i = lane; i < 2 * BLOCKS * boxes; i += 32) {
-                    const int blk = i / boxes % BLOCKS, half = i / (boxes * BLOCKS);
-                    if (in)
-                        tma_load_4d(s.ring + stage * L::STAGE + half * L::HALF + blk * (KEYS * 128) + lane % boxes * box * 128, half ? &vmap : &kmap,
-                                    blk * 64, tok & ((1 << a.page_shift) - 1), h, gone ? -1 : page, &s.full[stage], once);
-                }
+                // a copy a page of keys and of values; each lane holds the page of box lane % boxes
+                if (lane < 2 * boxes && in)
+                    tma_load_5d(s.ring + stage * L::STAGE + lane / boxes * L::HALF + lane % boxes * box * (L::DP * 2), lane < boxes ? &kmap : &vmap, 0,
+                                tok & ((1 << a.page_shift) - 1), 0, h, gone ? -1 : page, &s.full[stage], once);
             }
         }
         if (!ok) {  // what is on its way has to land first
@@ -338,29 +335,30 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
                 const int stage = use % STAGES, k0 = w.start + t * KEYS + k16;
                 if (!ok || !(ok = wait(&s.full[stage], use / STAGES))) continue;
                 const uint32_t hide = *reinterpret_cast<volatile uint32_t*>(&s.hidden[stage]);
-                const uint32_t kb = ring + stage * L::STAGE, vb = kb + L::HALF;
-                const int box_shift = min(a.page_shift, KEYS == 64 ? 6 : 5);
+                // a box holds its tokens' first 64 channels, then the next 64 ...
+                const int box_shift = min(a.page_shift, KEYS == 64 ? 6 : 5), blk_bytes = 128 << box_shift;
+                const uint32_t kb = ring + stage * L::STAGE + (k16 >> box_shift) * (blk_bytes * BLOCKS) + (k16 & ((1 << box_shift) - 1)) * 128, vb = kb + L::HALF;
                 const bool gone = (hide >> (k16 >> box_shift)) & 1;
                 const bool part = k0 + 16 > w.kv || k0 < w.lo || gone;
                 if (part) {
                     // values of places that the row does not see, whatever lies there: zeros
-                    unsigned char* v = s.ring + stage * L::STAGE + L::HALF + k16 * 128;
+                    unsigned char* v = s.ring + (vb - ring);
                     for (int i = lane; i < 16 * 8 * BLOCKS; i += 32) {
                         const int r = i / 8 % 16, blk = i / 128;
-                        if (k0 + r >= w.kv || k0 + r < w.lo || gone) *reinterpret_cast<uint4*>(v + blk * (KEYS * 128) + r * 128 + i % 8 * 16) = make_uint4(0, 0, 0, 0);
+                        if (k0 + r >= w.kv || k0 + r < w.lo || gone) *reinterpret_cast<uint4*>(v + blk * blk_bytes + r * 128 + i % 8 * 16) = make_uint4(0, 0, 0, 0);
                     }
                     ptx::fence_proxy_async_smem();
                     __syncwarp();
                 }
                 float sc[2][HB][4] = {};  // even and odd steps apart: half the latency
                 {
-                    const int r = k16 + (lane & 15), ch = lane >> 4;
+                    const int r = lane & 15, ch = lane >> 4;
                     const uint32_t row = kb + r * 128;
 #pragma unroll
                     for (int k = 0; k < D / 32; ++k) {
                         uint32_t x[2][4];
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) ldsm(x[i], row + (k / 2) * (KEYS * 128) + (((k % 2 * 4 + i * 2 + ch) ^ (r & 7)) << 4));
+                        for (int i = 0; i < 2; ++i) ldsm(x[i], row + (k / 2) * blk_bytes + (((k % 2 * 4 + i * 2 + ch) ^ (r & 7)) << 4));
 #pragma unroll
                         for (int b = 0; b < HB; ++b) {
                             uint32_t q[4];
@@ -422,12 +420,12 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
                     }
                 }
                 {
-                    const int r = k16 + (lane & 7) + (lane >> 4) * 8, ch = (lane >> 3) & 1;
+                    const int r = (lane & 7) + (lane >> 4) * 8, ch = (lane >> 3) & 1;
                     const uint32_t row = vb + r * 128;
 #pragma unroll
                     for (int j = 0; j < D / 16; ++j) {
                         uint32_t x[4];
-                        ldsm_t(x, row + (j / 4) * (KEYS * 128) + ((((j % 4) * 2 + ch) ^ (r & 7)) << 4));
+                        ldsm_t(x, row + (j / 4) * blk_bytes + ((((j % 4) * 2 + ch) ^ (r & 7)) << 4));
 #pragma unroll
                         for (int b = 0; b < HB; ++b) mma16816(o[b][j], x, hi[b][0], hi[b][1]);
 #pragma unroll
@@ -578,16 +576,17 @@ template <int D, int ROWS> __global__ void __launch_bounds__(32 * ROWS) token_jo
     write_row<__nv_bfloat16, D>(a, (size_t)cut.seq * a.Hq + h * a.G + g0 + row, ml, y);
 }
 
+// [num_pages][Hkv][D / 64][page_size][64] by the cache's strides; boxes of a page's (or a tile's) tokens and all channels of one head.
 bool encode_cache(CUtensorMap* m, const void* base, const PagedArgs& a, int keys)
 {
     PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
     if (!enc) return false;
-    const cuuint64_t P = (cuuint64_t)1 << a.page_shift;
-    const cuuint64_t dims[4] = {(cuuint64_t)a.D, P, (cuuint64_t)a.Hkv, (cuuint64_t)a.num_pages};
-    const cuuint64_t strides[3] = {(cuuint64_t)a.token_stride * 2, (cuuint64_t)a.head_stride * 2, (cuuint64_t)a.page_stride * 2};
-    const cuuint32_t box[4] = {64, (cuuint32_t)std::min<cuuint64_t>(P, keys), 1, 1};
-    const cuuint32_t estr[4] = {1, 1, 1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+    const cuuint64_t P = (cuuint64_t)1 << a.page_shift, blocks = a.D < 64 ? 1 : a.D / 64;
+    const cuuint64_t dims[5] = {(cuuint64_t)std::min(a.D, 64), P, blocks, (cuuint64_t)a.Hkv, (cuuint64_t)a.num_pages};
+    const cuuint64_t strides[4] = {(cuuint64_t)a.token_stride * 2, 128, (cuuint64_t)a.head_stride * 2, (cuuint64_t)a.page_stride * 2};
+    const cuuint32_t box[5] = {64, (cuuint32_t)std::min<cuuint64_t>(P, keys), (cuuint32_t)blocks, 1, 1};
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
