@@ -640,8 +640,8 @@ KDA_API int kda_paged_append_decode(const kda_paged_params* p, int32_t B, const 
  *       there, and is flagged (KDA_DEV_BAD_PAGE).  Pages wholly before the
  *       window are not read.
  *   Products take the rows' type and sum in fp32; weights are fp32 and, for bf16
- *       rows of a chunk, rounded to bf16 where they meet the values (single tokens:
- *       in two bf16 parts).
+ *       rows of a chunk, rounded to bf16 where they meet the values (single tokens
+ *       of up to 16 heads a key head: in two bf16 parts).
  *   Whatever lies in the cache's places past a sequence's tokens has no
  *       effect.  A NaN or an infinity in a query or key reaches rows that
  *       see it, in a value also rows of the same chunk that do not.

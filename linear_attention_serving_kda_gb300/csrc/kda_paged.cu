@@ -483,7 +483,8 @@ size_t attn_workspace(const kda_paged_params* p, int32_t N, int32_t T, bool toke
     fill_paged(a, p);
     a.N = N;
     a.T = T;
-    return p->io_dtype == KDA_DTYPE_F32 ? paged_f32_workspace_bytes(a) : token ? paged_token_workspace_bytes(a) : paged_bf16_workspace_bytes(a);
+    const bool f32 = p->io_dtype == KDA_DTYPE_F32;
+    return token && paged_token_wanted(a, f32) ? paged_token_workspace_bytes(a) : f32 ? paged_f32_workspace_bytes(a) : paged_bf16_workspace_bytes(a);
 }
 
 int attend(const kda_paged_params* p, const int32_t* cu_seqlens, int32_t N, int32_t T, const int32_t* kv_lens, const int32_t* pages,
@@ -518,7 +519,9 @@ int attend(const kda_paged_params* p, const int32_t* cu_seqlens, int32_t N, int3
     a.lse = lse;
     a.workspace = workspace;
     a.dev_status = dev_status;
-    const cudaError_t e = io == 4 ? launch_paged_f32(a, stream) : token ? launch_paged_token(a, stream) : launch_paged_bf16(a, stream);
+    const cudaError_t e = token && paged_token_wanted(a, io == 4) ? launch_paged_token(a, io == 4, stream)
+                          : io == 4                               ? launch_paged_f32(a, stream)
+                                                                  : launch_paged_bf16(a, stream);
     return e == cudaSuccess ? KDA_OK : KDA_ERR_LAUNCH;
 }
 

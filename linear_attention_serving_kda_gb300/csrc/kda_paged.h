@@ -51,13 +51,14 @@ __device__ __forceinline__ bool paged_seq(const PagedArgs& a, int s, int& begin,
     return kv >= 0 && end > begin;
 }
 
-// Attention of chunks: fp32 rows and bf16 rows; of single tokens: bf16 rows (fp32 ones run as chunks).
+// Attention of chunks: fp32 rows, bf16 rows; of single tokens, where `wanted`.
 cudaError_t launch_paged_f32(const PagedArgs& a, cudaStream_t st);
 size_t paged_f32_workspace_bytes(const PagedArgs& a);
 cudaError_t launch_paged_bf16(const PagedArgs& a, cudaStream_t st);
 size_t paged_bf16_workspace_bytes(const PagedArgs& a);
-cudaError_t launch_paged_token(const PagedArgs& a, cudaStream_t st);
+cudaError_t launch_paged_token(const PagedArgs& a, bool f32, cudaStream_t st);
 size_t paged_token_workspace_bytes(const PagedArgs& a);
+bool paged_token_wanted(const PagedArgs& a, bool f32);
 
 // The driver's encoder of tensor maps, null where it has none (kda_chunk.cu).
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();

@@ -54,21 +54,24 @@ size_t lay_out(TokenWork& w, const PagedArgs& a)
 
 // Teams of TEAM warps, 16 tokens of a tile each, take the tiles in turn.  A stage of the ring belongs to one team (their
 // number divides the stages'), so that whoever waits for a stage has waited for each of its uses: parities tell two apart, not three.
-template <int D, int HB> struct Token {
-    static constexpr int DP = D < 64 ? 64 : D, BLOCKS = DP / 64;
+template <typename IO, int D, int HB> struct Token {
+    static constexpr int SIZE = sizeof(IO), WIDE = 128 / SIZE;   // values of 128 bytes
+    static constexpr int DP = D < WIDE ? WIDE : D, BLOCKS = DP / WIDE;
     static constexpr int ROWS = 8 * HB;
-    static constexpr int TEAM = D == 256 ? 2 : 4, WARPS = HB == 1 ? 12 : D == 256 ? 6 : 8, TEAMS = WARPS / TEAM;  // as registers allow
+    static constexpr int TEAM = D * SIZE == 1024 ? 1 : D * SIZE == 512 ? 2 : 4;
+    static constexpr int WARPS = TEAM == 1 ? 6 : HB == 1 ? 12 : TEAM == 2 ? 6 : 8, TEAMS = WARPS / TEAM;  // as registers allow
     static constexpr int THREADS = 32 * (WARPS + 1);
-    static constexpr int KEYS = 16 * TEAM;                        // tokens of a tile
-    static constexpr int HALF = KEYS * DP * 2, STAGE = 2 * HALF;  // keys, then values
-    static constexpr int STAGES = D >= 128 ? 6 : 12;
-    static constexpr int CH = 32, QS = D * 2 + 16;                // bytes of a row of q: eight rows in distinct banks
+    static constexpr int KEYS = 16 * TEAM;                         // tokens of a tile
+    static constexpr int HALF = KEYS * DP * SIZE, STAGE = 2 * HALF;  // keys, then values
+    static constexpr int STAGES = STAGE <= 16384 ? 12 : 6;
+    static constexpr int CH = 32, QS = D * SIZE + 16;              // bytes of a row of q: eight rows in distinct banks
     static_assert(STAGES % TEAMS == 0, "a stage belongs to one team");
     struct Smem {
         unsigned char ring[STAGES * STAGE];
         unsigned char q[2][ROWS * QS];
         float o[WARPS][ROWS * (CH + 4)];  // CH channels of every warp's sums at a time
         float2 ml[WARPS][ROWS];
+        float w[SIZE == 4 ? WARPS : 1][16 * 8];  // fp32 rows: weights of 16 tokens and eight heads
         uint64_t full[STAGES], empty[STAGES], qfull[2], qempty[2];
         int kv[KNOWN];                    // lengths from the stretch's first sequence on, -1: skipped
         long long sum[WARPS + 1];
@@ -185,10 +188,11 @@ template <int KEYS, class S> __device__ __forceinline__ void next_unit(const Pag
     w.t1 = (int)min((long long)w.n, w.left);
 }
 
-template <int D, int HB> __global__ void __launch_bounds__(Token<D, HB>::THREADS, 1)
+template <typename IO, int D, int HB> __global__ void __launch_bounds__(Token<IO, D, HB>::THREADS, 1)
 paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap)
 {
-    using L = Token<D, HB>;
+    using L = Token<IO, D, HB>;
+    constexpr bool F32 = sizeof(IO) == 4;
     constexpr int ROWS = L::ROWS, STAGES = L::STAGES, BLOCKS = L::BLOCKS, KEYS = L::KEYS, WARPS = L::WARPS, TEAM = L::TEAM, TT = L::THREADS;
     extern __shared__ __align__(1024) unsigned char raw[];
     auto& s = *reinterpret_cast<typename L::Smem*>(raw);
@@ -270,11 +274,11 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
         for (; w.left > 0 && ok; next_unit<KEYS>(a, s, w, units), ++unit) {
             const int h = w.u / blocks, g0 = w.u % blocks * ROWS, rows = min(ROWS, a.G - g0);
             if (!(ok = wait(&s.qempty[unit & 1], (unit >> 1) + 1))) break;
-            if (lane == 0) ptx::mbar_arrive_expect_tx(&s.qfull[unit & 1], rows * D * 2);
+            if (lane == 0) ptx::mbar_arrive_expect_tx(&s.qfull[unit & 1], rows * D * L::SIZE);
             __syncwarp();
             if (lane < rows)
-                ptx::bulk_g2s(s.q[unit & 1] + lane * L::QS, static_cast<const __nv_bfloat16*>(a.q) + w.s * a.q_stride + (long long)(h * a.G + g0 + lane) * D,
-                              D * 2, &s.qfull[unit & 1]);
+                ptx::bulk_g2s(s.q[unit & 1] + lane * L::QS, static_cast<const IO*>(a.q) + w.s * a.q_stride + (long long)(h * a.G + g0 + lane) * D,
+                              D * L::SIZE, &s.qfull[unit & 1]);
             for (int t = w.t0; t < w.t1; ++t, ++use) {
                 const int stage = use % STAGES, k0 = w.start + t * KEYS, tok = k0 + lane % boxes * box;
                 const bool in = tok < w.kv;
@@ -292,7 +296,7 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
                 __syncwarp();
                 // a copy a page of keys and of values; each lane holds the page of box lane % boxes
                 if (lane < 2 * boxes && in)
-                    tma_load_5d(s.ring + stage * L::STAGE + lane / boxes * L::HALF + lane % boxes * box * (L::DP * 2), lane < boxes ? &kmap : &vmap, 0,
+                    tma_load_5d(s.ring + stage * L::STAGE + lane / boxes * L::HALF + lane % boxes * box * (L::DP * L::SIZE), lane < boxes ? &kmap : &vmap, 0,
                                 tok & ((1 << a.page_shift) - 1), 0, h, gone ? -1 : page, &s.full[stage], once);
             }
         }
@@ -312,7 +316,7 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
             ok = ok && wait(&s.qfull[unit & 1], unit >> 1);
             // tokens are the products' rows, heads their columns: S^T = K Q^T, O^T += V^T W^T
             const uint32_t qbase = ptx::smem_u32(s.q[unit & 1]) + (lane & 7) * L::QS + (lane >> 3) * 16;
-            constexpr bool KEEP = D * HB <= 128;  // more than that comes from shared memory each time: registers
+            constexpr bool KEEP = !F32 && D * HB <= 128;  // more than that comes from shared memory each time: registers
             uint32_t qf[HB][KEEP ? D / 32 : 1][4];
             if constexpr (KEEP) {
 #pragma unroll
@@ -320,7 +324,19 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
 #pragma unroll
                     for (int k = 0; k < D / 32; ++k) ldsm(qf[b][k], qbase + b * 8 * L::QS + k * 64);
             }
-            float o[HB][D / 16][4], m[HB][2], l[HB][2];  // of this lane's two heads (a block)
+            float o[F32 ? 1 : HB][F32 ? 1 : D / 16][4], m[HB][2], l[HB][2];  // of this lane's two heads (a block)
+            // fp32 rows: all eight heads, D / 32 channels a lane
+            constexpr int PER = D / 32;
+            float of[F32 ? 8 : 1][F32 ? PER : 1], mf[F32 ? 8 : 1], lf[F32 ? 8 : 1];
+            if constexpr (F32) {
+#pragma unroll
+                for (int g = 0; g < 8; ++g) {
+                    mf[g] = -INFINITY;
+                    lf[g] = 0.f;
+#pragma unroll
+                    for (int i = 0; i < PER; ++i) of[g][i] = 0.f;
+                }
+            }
 #pragma unroll
             for (int b = 0; b < HB; ++b) {
                 m[b][0] = m[b][1] = -INFINITY;
@@ -328,7 +344,8 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) o[b][i][e] = 0.f;
+                    for (int e = 0; e < 4; ++e)
+                        if constexpr (!F32) o[b][i][e] = 0.f;
             }
             for (int t = w.t0; t < w.t1; ++t, ++use) {
                 if (use % L::TEAMS != (uint32_t)team) continue;
@@ -336,7 +353,7 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
                 if (!ok || !(ok = wait(&s.full[stage], use / STAGES))) continue;
                 const uint32_t hide = *reinterpret_cast<volatile uint32_t*>(&s.hidden[stage]);
                 // a box holds its tokens' first 64 channels, then the next 64 ...
-                const int box_shift = min(a.page_shift, KEYS == 64 ? 6 : 5), blk_bytes = 128 << box_shift;
+                const int box_shift = min(a.page_shift, KEYS == 64 ? 6 : KEYS == 32 ? 5 : 4), blk_bytes = 128 << box_shift;
                 const uint32_t kb = ring + stage * L::STAGE + (k16 >> box_shift) * (blk_bytes * BLOCKS) + (k16 & ((1 << box_shift) - 1)) * 128, vb = kb + L::HALF;
                 const bool gone = (hide >> (k16 >> box_shift)) & 1;
                 const bool part = k0 + 16 > w.kv || k0 < w.lo || gone;
@@ -350,6 +367,80 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
                     ptx::fence_proxy_async_smem();
                     __syncwarp();
                 }
+                if constexpr (F32) {
+                    // scores: two lanes a token, half of every 32 channels each
+                    const int tk = lane >> 1, half = lane & 1, tok = k0 + tk;
+                    const unsigned char* kr = s.ring + (kb - ring) + tk * 128;
+                    const unsigned char* qr = s.q[unit & 1];
+                    float sc[8] = {};
+#pragma unroll 4
+                    for (int i = 0; i < D / 8; ++i) {
+                        const int ch = half * 4 + i % 4, blk = i / 4;
+                        const float4 k = *reinterpret_cast<const float4*>(kr + blk * blk_bytes + ((ch ^ (tk & 7)) << 4));
+#pragma unroll
+                        for (int g = 0; g < 8; ++g)
+                            if (g < rows) {
+                                const float4 q = *reinterpret_cast<const float4*>(qr + g * L::QS + blk * 128 + ch * 16);
+                                sc[g] = fmaf(q.w, k.w, fmaf(q.z, k.z, fmaf(q.y, k.y, fmaf(q.x, k.x, sc[g]))));
+                            }
+                    }
+                    const bool seen = !(part && (gone || tok >= w.kv || tok < w.lo));
+                    bool grow = false;
+#pragma unroll
+                    for (int g = 0; g < 8; ++g)
+                        if (g < rows) {
+                            sc[g] += __shfl_xor_sync(0xffffffffu, sc[g], 1);
+                            sc[g] = seen ? c * sc[g] : -INFINITY;
+                            grow |= sc[g] > mf[g] + LAG;
+                        }
+                    if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                        for (int g = 0; g < 8; ++g)
+                            if (g < rows) {
+                                float x = sc[g];
+#pragma unroll
+                                for (int d = 2; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+                                const float next = fmaxf(mf[g], x), f = next == -INFINITY ? 1.f : exp2_sfu(mf[g] - next);
+                                mf[g] = next;
+                                lf[g] *= f;
+#pragma unroll
+                                for (int i = 0; i < PER; ++i) of[g][i] *= f;
+                            }
+                    }
+                    float* wr = s.w[warp];
+#pragma unroll
+                    for (int g = 0; g < 8; ++g)
+                        if (g < rows) {
+                            const float x = exp2_sfu(sc[g] - (mf[g] == -INFINITY ? 0.f : mf[g]));
+                            if (half == 0) {
+                                lf[g] += x;
+                                wr[tk * 8 + g] = x;
+                            }
+                        }
+                    __syncwarp();
+                    const unsigned char* vr = s.ring + (vb - ring);
+#pragma unroll 4
+                    for (int t16 = 0; t16 < 16; ++t16) {
+                        float v[PER];
+                        if constexpr (PER >= 4) {
+#pragma unroll
+                            for (int i = 0; i < PER; i += 4)
+                                *reinterpret_cast<float4*>(v + i) = *reinterpret_cast<const float4*>(vr + (i + lane / 8) * blk_bytes + t16 * 128 + ((lane % 8 ^ (t16 & 7)) << 4));
+                        } else {
+                            const int at = lane * PER;
+#pragma unroll
+                            for (int i = 0; i < PER; ++i)
+                                v[i] = *reinterpret_cast<const float*>(vr + at / 32 * blk_bytes + t16 * 128 + ((at % 32 / 4 ^ (t16 & 7)) << 4) + (at % 4 + i) * 4);
+                        }
+                        const float4 w0 = *reinterpret_cast<const float4*>(wr + t16 * 8), w1 = *reinterpret_cast<const float4*>(wr + t16 * 8 + 4);
+                        const float ww[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+                        for (int g = 0; g < 8; ++g)
+                            if (g < rows)
+#pragma unroll
+                                for (int i = 0; i < PER; ++i) of[g][i] = fmaf(ww[g], v[i], of[g][i]);
+                    }
+                } else {
                 float sc[2][HB][4] = {};  // even and odd steps apart: half the latency
                 {
                     const int r = lane & 15, ch = lane >> 4;
@@ -432,10 +523,18 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
                         for (int b = 0; b < HB; ++b) mma16816(o[b][j], x, lo[b][0], lo[b][1]);
                     }
                 }
+                }
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(&s.empty[stage]);
             }
             // ---- the warps' sums together
+            if constexpr (F32) {
+#pragma unroll
+                for (int g = 0; g < 8; ++g) {
+                    lf[g] = warp_sum(lf[g]);
+                    if (lane == 0) s.ml[warp][g] = make_float2(mf[g], lf[g]);
+                }
+            } else {
 #pragma unroll
             for (int b = 0; b < HB; ++b)
 #pragma unroll
@@ -444,9 +543,19 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
                     for (int d = 4; d < 32; d <<= 1) l[b][e] += __shfl_xor_sync(0xffffffffu, l[b][e], d);
                     if (lane < 4) s.ml[warp][b * 8 + lane * 2 + e] = make_float2(m[b][e], l[b][e]);
                 }
+            }
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&s.qempty[unit & 1]);
             asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory");
+            float ff[F32 ? 8 : 1];
+            if constexpr (F32) {
+#pragma unroll
+                for (int g = 0; g < 8; ++g) {
+                    float top = -INFINITY;
+                    for (int x = 0; x < WARPS; ++x) top = fmaxf(top, s.ml[x][g].x);
+                    ff[g] = mf[g] == -INFINITY ? 0.f : exp2_sfu(mf[g] - top);
+                }
+            }
             float f[HB][2];
 #pragma unroll
             for (int b = 0; b < HB; ++b)
@@ -469,6 +578,15 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
             for (int e = 0; e < D; e += CH) {
+                if constexpr (F32) {
+#pragma unroll
+                    for (int i = 0; i < PER; ++i) {
+                        const int at = PER >= 4 ? i / 4 * 128 + lane * 4 + i % 4 : lane * PER + i;
+                        if (at / CH == e / CH)
+#pragma unroll
+                            for (int g = 0; g < 8; ++g) s.o[warp][g * (CH + 4) + at % CH] = of[g][i] * ff[g];
+                    }
+                } else {
 #pragma unroll
                 for (int b = 0; b < HB; ++b)
 #pragma unroll
@@ -476,13 +594,16 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             s.o[warp][(b * 8 + (lane & 3) * 2 + (i & 1)) * (CH + 4) + j * 16 + lane / 4 + (i & 2) * 4] = o[b][e / 16 + j][i] * f[b][i & 1];
+                }
                 asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory");
                 float2 y = make_float2(0.f, 0.f);
                 if (row < ROWS)
 #pragma unroll
                     for (int x = 0; x < WARPS; ++x) y = add2(y, *reinterpret_cast<const float2*>(&s.o[x][row * (CH + 4) + ch]));
                 if (in) {
-                    if (whole) *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + head * D + e + ch) =
+                    if (whole && F32) *reinterpret_cast<float2*>(static_cast<float*>(a.out) + head * D + e + ch) =
+                        sum == 0.f ? make_float2(0.f, 0.f) : make_float2(y.x * inv, y.y * inv);
+                    else if (whole) *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + head * D + e + ch) =
                         sum == 0.f ? 0u : pack_bf16(y.x * inv, y.y * inv);
                     else *reinterpret_cast<float2*>(work.o + cell * D + e + ch) = y;
                 }
@@ -559,7 +680,7 @@ template <typename IO, int D> __device__ __forceinline__ void write_row(const Pa
 }
 
 // The parts of the unit that begins in stretch blockIdx.x and goes on: a warp a row.
-template <int D, int ROWS> __global__ void __launch_bounds__(32 * ROWS) token_join_kernel(const PagedArgs a, const TokenWork work)
+template <typename IO, int D, int ROWS> __global__ void __launch_bounds__(32 * ROWS) token_join_kernel(const PagedArgs a, const TokenWork work)
 {
     ptx::grid_launch_dependents();
     ptx::grid_dependency_wait();
@@ -573,47 +694,52 @@ template <int D, int ROWS> __global__ void __launch_bounds__(32 * ROWS) token_jo
     float y[D / 32];
     const float2 ml = join_row<D>(cut.last - (int)blockIdx.x + 1, [&](int s) { return used(s) ? work.ml + cell(s) : nullptr; },
                                          [&](int s) { return used(s) ? work.o + cell(s) * D : nullptr; }, y);
-    write_row<__nv_bfloat16, D>(a, (size_t)cut.seq * a.Hq + h * a.G + g0 + row, ml, y);
+    write_row<IO, D>(a, (size_t)cut.seq * a.Hq + h * a.G + g0 + row, ml, y);
 }
 
-// [num_pages][Hkv][D / 64][page_size][64] by the cache's strides; boxes of a page's (or a tile's) tokens and all channels of one head.
-bool encode_cache(CUtensorMap* m, const void* base, const PagedArgs& a, int keys)
+// [num_pages][Hkv][D / 64][page_size][64] (fp32: 32 values, 128 bytes either way) by the cache's strides; boxes of a page's (or a tile's) tokens and all channels of one head.
+bool encode_cache(CUtensorMap* m, const void* base, const PagedArgs& a, int keys, int size)
 {
     PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
     if (!enc) return false;
-    const cuuint64_t P = (cuuint64_t)1 << a.page_shift, blocks = a.D < 64 ? 1 : a.D / 64;
-    const cuuint64_t dims[5] = {(cuuint64_t)std::min(a.D, 64), P, blocks, (cuuint64_t)a.Hkv, (cuuint64_t)a.num_pages};
-    const cuuint64_t strides[4] = {(cuuint64_t)a.token_stride * 2, 128, (cuuint64_t)a.head_stride * 2, (cuuint64_t)a.page_stride * 2};
-    const cuuint32_t box[5] = {64, (cuuint32_t)std::min<cuuint64_t>(P, keys), (cuuint32_t)blocks, 1, 1};
+    const cuuint64_t P = (cuuint64_t)1 << a.page_shift, wide = 128 / size, blocks = std::max<cuuint64_t>(1, a.D / wide);
+    const cuuint64_t dims[5] = {std::min<cuuint64_t>(a.D, wide), P, blocks, (cuuint64_t)a.Hkv, (cuuint64_t)a.num_pages};
+    const cuuint64_t strides[4] = {(cuuint64_t)a.token_stride * size, 128, (cuuint64_t)a.head_stride * size, (cuuint64_t)a.page_stride * size};
+    const cuuint32_t box[5] = {(cuuint32_t)wide, (cuuint32_t)std::min<cuuint64_t>(P, keys), (cuuint32_t)blocks, 1, 1};
     const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+    return enc(m, size == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int HB> cudaError_t launch(const PagedArgs& a, cudaStream_t st)
+template <typename IO, int D, int HB> cudaError_t launch(const PagedArgs& a, cudaStream_t st)
 {
-    using L = Token<D, HB>;
+    using L = Token<IO, D, HB>;
     constexpr int smem = sizeof(typename L::Smem);
     static_assert(smem <= 227 * 1024, "shared memory");
     static_assert(L::HALF % 1024 == 0 && offsetof(typename L::Smem, q) % 16 == 0 && offsetof(typename L::Smem, full) % 8 == 0, "alignment");
     static PerDeviceOnce once;
-    cudaError_t e = once.run([](int) { return cudaFuncSetAttribute(paged_token_kernel<D, HB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
+    cudaError_t e = once.run([](int) { return cudaFuncSetAttribute(paged_token_kernel<IO, D, HB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
     if (e != cudaSuccess) return e;
     CUtensorMap km, vm;
-    if (!encode_cache(&km, a.k, a, L::KEYS) || !encode_cache(&vm, a.v, a, L::KEYS)) return cudaErrorInvalidValue;
+    if (!encode_cache(&km, a.k, a, L::KEYS, L::SIZE) || !encode_cache(&vm, a.v, a, L::KEYS, L::SIZE)) return cudaErrorInvalidValue;
     TokenWork w;
     lay_out(w, a);
-    e = launch_dependent(paged_token_kernel<D, HB>, CTAS, L::THREADS, smem, st, a, w, km, vm);
-    if (e == cudaSuccess) e = launch_dependent(token_join_kernel<D, L::ROWS>, CTAS, 32 * std::min(L::ROWS, a.G), 0, st, a, w);
+    e = launch_dependent(paged_token_kernel<IO, D, HB>, CTAS, L::THREADS, smem, st, a, w, km, vm);
+    if (e == cudaSuccess) e = launch_dependent(token_join_kernel<IO, D, L::ROWS>, CTAS, 32 * std::min(L::ROWS, a.G), 0, st, a, w);
     return e;
 }
 
-template <int D> cudaError_t launch_heads(const PagedArgs& a, cudaStream_t st)
+template <int D> cudaError_t launch_heads(const PagedArgs& a, bool f32, cudaStream_t st)
 {
-    return unit_rows(a) == 8 ? launch<D, 1>(a, st) : launch<D, 2>(a, st);
+    if (f32) return launch<float, D, 1>(a, st);
+    return unit_rows(a) == 8 ? launch<__nv_bfloat16, D, 1>(a, st) : launch<__nv_bfloat16, D, 2>(a, st);
 }
 
 }  // namespace
+
+// A unit holds the heads of a group up to these: more of them would read the cache again for each, and take the kernels for
+// chunks, whose tiles hold up to 256 rows (64 sequences of 8192 tokens, four key heads of 32 query heads: 195 us there, 355 here).
+bool paged_token_wanted(const PagedArgs& a, bool f32) { return a.G <= (f32 ? 8 : 16); }
 
 size_t paged_token_workspace_bytes(const PagedArgs& a)
 {
@@ -621,13 +747,13 @@ size_t paged_token_workspace_bytes(const PagedArgs& a)
     return lay_out(w, a);
 }
 
-cudaError_t launch_paged_token(const PagedArgs& a, cudaStream_t st)
+cudaError_t launch_paged_token(const PagedArgs& a, bool f32, cudaStream_t st)
 {
     switch (a.D) {
-    case 32: return launch_heads<32>(a, st);
-    case 64: return launch_heads<64>(a, st);
-    case 128: return launch_heads<128>(a, st);
-    default: return launch_heads<256>(a, st);
+    case 32: return launch_heads<32>(a, f32, st);
+    case 64: return launch_heads<64>(a, f32, st);
+    case 128: return launch_heads<128>(a, f32, st);
+    default: return launch_heads<256>(a, f32, st);
     }
 }
 
