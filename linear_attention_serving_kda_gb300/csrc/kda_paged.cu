@@ -143,7 +143,9 @@ template <typename IO, int V> struct Unit {
 };
 
 constexpr int RT = 512;    // most threads of a CTA
-constexpr int RAHEAD = 4;  // heads whose loads are in flight together
+// Heads whose loads a thread has in flight together: more take registers from other CTAs (append of 32768 rows of 48 heads of
+// 128: 146 us with one, 129 with two, 148 with four; rotation of 40 heads: 106 with two, 99 with four).
+constexpr int RAHEAD = 4, AAHEAD = 2;
 
 struct RopeArgs {
     int H, D, units, groups, rows_per_cta;
@@ -268,10 +270,10 @@ template <typename IO, int V> __global__ void __launch_bounds__(RT) append_kerne
         flat.turned = false;
         flat.at = 2 * V * u;
         flat.second = flat.at + V;
-        Piece<IO, V> x[RAHEAD][2];
+        Piece<IO, V> x[AAHEAD][2];
         auto fetch = [&](int h0) {
 #pragma unroll
-            for (int j = 0; j < RAHEAD; ++j) {
+            for (int j = 0; j < AAHEAD; ++j) {
                 const int h = h0 + j * a.groups;
                 if (h >= H) continue;
                 const IO* src = h < a.heads_q           ? static_cast<const IO*>(p.q) + row * a.qis + (long long)h * D
@@ -286,7 +288,7 @@ template <typename IO, int V> __global__ void __launch_bounds__(RT) append_kerne
         w.angles(a.turn, u, angle[r]);
         for (int h0 = g; h0 < H;) {
 #pragma unroll
-            for (int j = 0; j < RAHEAD; ++j) {
+            for (int j = 0; j < AAHEAD; ++j) {
                 const int h = h0 + j * a.groups;
                 if (h >= H) continue;
                 const bool value = h >= a.heads_q + p.Hkv;
@@ -297,7 +299,7 @@ template <typename IO, int V> __global__ void __launch_bounds__(RT) append_kerne
                 x[j][0].store(dst + (value ? flat.at : w.at));
                 x[j][1].store(dst + (value ? flat.second : w.second));
             }
-            h0 += RAHEAD * a.groups;
+            h0 += AAHEAD * a.groups;
             if (h0 < H) fetch(h0);
         }
     }

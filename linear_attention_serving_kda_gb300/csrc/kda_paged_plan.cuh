@@ -256,7 +256,9 @@ template <typename IO, int D> __global__ void __launch_bounds__(JT) join_kernel(
 {
     ptx::grid_launch_dependents();
     ptx::grid_dependency_wait();
+    constexpr int AT_ONCE = 32;  // parts whose maxima and sums are held together
     __shared__ float4 turned[32][D / 4 + 1];
+    __shared__ float2 held[AT_ONCE][32];
     const int c0 = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = blockIdx.y * 32 + lane;
     const Cut cut = p.cut[c0];
     if (blockIdx.y * 32 >= cut.rows) return;
@@ -265,33 +267,40 @@ template <typename IO, int D> __global__ void __launch_bounds__(JT) join_kernel(
     const auto cell = [&](int s) { return (size_t)(c0 + s) * 2 + (s == 0); };
     const int parts = cut.last - c0 + 1;
     const bool in = r < cut.rows;
-    float m = -INFINITY, l = 0.f;
-#pragma unroll 4
-    for (int s = 0; s < parts; ++s)
-        if (in && used(s)) {
-            const float2 x = p.ml[cell(s) * p.part_rows + r];
-            const float next = fmaxf(m, x.x);
-            if (next != -INFINITY) l = l * exp2f(m - next) + x.y * exp2f(x.x - next);
-            m = next;
-        }
-    const float base = m == -INFINITY ? 0.f : m, inv = l == 0.f ? 0.f : 1.f / l;
     constexpr int GROUPS = D / 4, EACH = GROUPS < 8 ? 1 : GROUPS / 8;
+    float m = -INFINITY, l = 0.f;
     float4 y[EACH];
 #pragma unroll
     for (int i = 0; i < EACH; ++i) y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-    for (int s = 0; s < parts; ++s)
-        if (in && used(s)) {
-            const float f = exp2f(p.ml[cell(s) * p.part_rows + r].x - base);
+    for (int s0 = 0; s0 < parts; s0 += AT_ONCE) {
+        const int n = min(AT_ONCE, parts - s0);
+        __syncthreads();
+        for (int s = warp; s < n; s += JT / 32) held[s][lane] = in && used(s0 + s) ? p.ml[cell(s0 + s) * p.part_rows + r] : make_float2(-INFINITY, 0.f);
+        __syncthreads();
+        float next = m;
+        for (int s = 0; s < n; ++s) next = fmaxf(next, held[s][lane].x);
+        const float base = next == -INFINITY ? 0.f : next, f0 = exp2f(m - base);
+        m = next;
+        l *= f0;
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) y[i] = make_float4(y[i].x * f0, y[i].y * f0, y[i].z * f0, y[i].w * f0);
+#pragma unroll 4
+        for (int s = 0; s < n; ++s) {
+            const float2 x = held[s][lane];
+            if (x.x == -INFINITY) continue;  // a part that saw nothing, or none
+            const float f = exp2f(x.x - base);
+            l += f * x.y;
 #pragma unroll
             for (int i = 0; i < EACH; ++i) {
-                const float4 z = p.o[(cell(s) * GROUPS + warp * EACH + i) * p.part_rows + r];
+                const float4 z = p.o[(cell(s0 + s) * GROUPS + warp * EACH + i) * p.part_rows + r];
                 y[i].x = fmaf(f, z.x, y[i].x);
                 y[i].y = fmaf(f, z.y, y[i].y);
                 y[i].z = fmaf(f, z.z, y[i].z);
                 y[i].w = fmaf(f, z.w, y[i].w);
             }
         }
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
     for (int i = 0; i < EACH; ++i)
         turned[lane][warp * EACH + i] = l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(y[i].x * inv, y[i].y * inv, y[i].z * inv, y[i].w * inv);
