@@ -64,7 +64,8 @@ template <typename IO, int D, int HB> struct Token {
     static constexpr int KEYS = 16 * TEAM;                         // tokens of a tile
     static constexpr int HALF = KEYS * DP * SIZE, STAGE = 2 * HALF;  // keys, then values
     static constexpr int STAGES = STAGE <= 16384 ? 12 : 6;
-    static constexpr int CH = 32, QS = D * SIZE + 16;              // bytes of a row of q: eight rows in distinct banks
+    static constexpr int CH = D == 128 && HB == 1 && SIZE == 2 ? 64 : 32;  // as shared memory allows
+    static constexpr int QS = D * SIZE + 16;                       // bytes of a row of q: eight rows in distinct banks
     static_assert(STAGES % TEAMS == 0, "a stage belongs to one team");
     struct Smem {
         unsigned char ring[STAGES * STAGE];
@@ -222,7 +223,11 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
     const int per = (a.N + TT - 1) / TT, s0 = min(tid * per, a.N), s1 = min(s0 + per, a.N);
     long long mine = 0;
     int fault = 0;
-    for (int i = s0; i < s1; ++i) mine += Span<KEYS>(a, length_of(a, i, &fault)).n;
+    int known = -1;
+    for (int i = s0; i < s1; ++i) {
+        known = length_of(a, i, &fault);
+        mine += Span<KEYS>(a, known).n;
+    }
     if (blockIdx.x == 0 && fault) flag_status(a.dev_status, fault);
     long long before = mine;
 #pragma unroll
@@ -255,8 +260,9 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
     __syncthreads();
     for (int i = tid; i < KNOWN; i += TT) {
         int f = 0;
-        s.kv[i] = s.first + i < a.N ? length_of(a, s.first + i, &f) : -1;
+        if (per > 1 || s.first + i >= a.N) s.kv[i] = s.first + i < a.N ? length_of(a, s.first + i, &f) : -1;
     }
+    if (per == 1 && tid < a.N && tid >= s.first && tid - s.first < KNOWN) s.kv[tid - s.first] = known;  // a sequence a thread: it is at hand
     __syncthreads();
     const auto wait = [&](uint64_t* bar, uint32_t parity) {
         if (ptx::mbar_wait(bar, parity & 1, WAIT) && !*reinterpret_cast<volatile int*>(&s.dead)) return true;
@@ -645,7 +651,7 @@ template <int D, class ML, class O> __device__ __forceinline__ float2 join_row(i
             l += f * x->y;
         }
         const int n = min(32, parts - s0);
-#pragma unroll 4
+#pragma unroll 8
         for (int s = 0; s < n; ++s) {
             const float g = __shfl_sync(0xffffffffu, f, s);
             const float* v = o(s0 + s);
