@@ -26,6 +26,7 @@ constexpr float LAG = 8.f;
 template <int DP> struct Shape {
     static constexpr int TILES = DP == 256 ? 1 : 2;    // tiles of 128 rows: TMEM holds 512 columns, O takes DP of them a tile
     static constexpr int KEYS = DP == 256 ? 64 : 128;
+    static constexpr int UNIT = DP == 256 ? 7 : 3;
     static constexpr int BLOCKS = DP / 64;             // 128-byte pieces of a row
     static constexpr int SLOT = KEYS * DP * 2;
     static constexpr int SLOTS = DP == 64 ? 8 : 5;
@@ -613,7 +614,7 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
                 use += 2 * w.count + (w.staged ? w.tiles * L::OUT : 0);
             }
             if (tid == 0 && ok && w.t0 == 0 && !w.whole())
-                p.cut[blockIdx.x] = {s.start.line, w.begin, w.row0, w.rows, w.head, owner(s.start.line, w.end() - 1, p.ctas)};
+                p.cut[blockIdx.x] = {s.start.line, w.begin, w.row0, w.rows, w.head, owner(s.start.line, w.end(p) - 1, p.ctas)};
             for (int b = 0; b < 2; ++b) {
                 scount[b] = sbase[b] += w.tiles == 2 ? w.count : (w.count + 1 - b) / 2;
                 pcount[b] += w.tiles == 2 ? min(w.count, 1) : (w.count + 1 - b) / 2;
@@ -658,7 +659,7 @@ template <int DP, int D> cudaError_t launch(const PagedArgs& a, cudaStream_t st)
     CUtensorMap km, vm;
     if (!encode_cache(&km, a.k, a, L::KEYS) || !encode_cache(&vm, a.v, a, L::KEYS)) return cudaErrorInvalidValue;
     Plan p;
-    lay_out(p, a, 128 * L::TILES, L::KEYS, CTAS);
+    lay_out(p, a, 128 * L::TILES, L::KEYS, CTAS, L::UNIT);
     e = launch_dependent(paged_bf16_kernel<DP, D>, CTAS, THREADS, smem, st, a, p, km, vm);
     if (e == cudaSuccess) e = launch_join<__nv_bfloat16, D>(a, p, st);
     return e;
@@ -669,7 +670,7 @@ template <int DP, int D> cudaError_t launch(const PagedArgs& a, cudaStream_t st)
 size_t paged_bf16_workspace_bytes(const PagedArgs& a)
 {
     Plan p;
-    return a.D == 256 ? lay_out(p, a, 128, 64, CTAS) : lay_out(p, a, 256, 128, CTAS);
+    return a.D == 256 ? lay_out(p, a, 128, 64, CTAS, 0) : lay_out(p, a, 256, 128, CTAS, 0);
 }
 
 cudaError_t launch_paged_bf16(const PagedArgs& a, cudaStream_t st)

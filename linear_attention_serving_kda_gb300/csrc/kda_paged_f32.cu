@@ -13,6 +13,7 @@ namespace {
 using namespace paged;
 
 constexpr int FT = 256;
+constexpr int UNIT = 1;
 constexpr int ctas_of(int D) { return D == 256 ? 152 : 304; }  // one or two an SM, as shared memory allows
 
 template <int D, int R> struct F32 {
@@ -191,7 +192,7 @@ template <int D, int R> __global__ void __launch_bounds__(FT, D == 256 ? 1 : 2) 
                 else if (a.lse) a.lse[row] = none ? -INFINITY : (m[i] + log2f(l[i])) * 0.69314718055994531f;
             }
         }
-        if (tid == 0 && it.t0 == 0 && !it.whole()) p.cut[blockIdx.x] = {start.line, it.begin, it.row0, it.rows, h, owner(start.line, it.end() - 1, p.ctas)};
+        if (tid == 0 && it.t0 == 0 && !it.whole()) p.cut[blockIdx.x] = {start.line, it.begin, it.row0, it.rows, h, owner(start.line, it.end(p) - 1, p.ctas)};
     }
     ptx::cp_async_wait_all();
 }
@@ -210,7 +211,7 @@ template <int D, int R> cudaError_t launch(const PagedArgs& a, cudaStream_t st)
     });
     if (e != cudaSuccess) return e;
     Plan p;
-    lay_out(p, a, R, L::KEYS, ctas_of(D));
+    lay_out(p, a, R, L::KEYS, ctas_of(D), UNIT);
     e = launch_dependent(paged_f32_kernel<D, R>, ctas_of(D), FT, smem, st, a, p);
     if (e == cudaSuccess) e = launch_join<float, D>(a, p, st);
     return e;
@@ -226,7 +227,7 @@ template <int D> cudaError_t launch_rows(const PagedArgs& a, cudaStream_t st)
 size_t paged_f32_workspace_bytes(const PagedArgs& a)
 {
     Plan p;
-    return lay_out(p, a, tile_rows(a), a.D == 256 ? 32 : 64, ctas_of(a.D));
+    return lay_out(p, a, tile_rows(a), a.D == 256 ? 32 : 64, ctas_of(a.D), 0);
 }
 
 cudaError_t launch_paged_f32(const PagedArgs& a, cudaStream_t st)

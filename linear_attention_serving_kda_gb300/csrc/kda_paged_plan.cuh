@@ -3,7 +3,7 @@
 //
 // The rows of a sequence that share a key head (its tokens times the G query heads of the group, token after
 // token) are cut into tiles of rows; a tile sees the tokens that any of its rows sees, cut into tiles of keys.  A
-// (tile of rows, key head) is a unit; the key tiles of all units form one line (with UNIT places more a unit, for what a unit
+// (tile of rows, key head) is a unit; the key tiles of all units form one line (with `unit` places more a unit, for what a unit
 // costs besides), and each CTA takes an equal stretch of it, whatever the lengths.  A unit within one stretch
 // is written out; one that stretches cut leaves a part in the workspace for each, which join_kernel adds: at most two parts a CTA.
 // Only the GPU knows the lengths: every CTA counts the line and finds where its stretch begins by itself (two
@@ -15,8 +15,6 @@
 
 namespace kda {
 namespace paged {
-
-constexpr int UNIT = 3;
 
 struct Start {
     long long line;            // places in all
@@ -31,14 +29,16 @@ struct Plan {
     int rows;       // of a tile
     int keys;       // of a tile
     int ctas;
+    int unit;       // places of a unit besides its key tiles
     int part_rows;  // rows kept of a part
     Cut* cut;           // [ctas]
     float2* ml;         // [ctas][2][part_rows]: largest score (in powers of two), sum of the weights;
     float4* o;          // [ctas][2][D / 4][part_rows], not divided.  0: of a unit that began before, 1: of one that goes on
 };
 
-inline size_t lay_out(Plan& p, const PagedArgs& a, int rows, int keys, int ctas)
+inline size_t lay_out(Plan& p, const PagedArgs& a, int rows, int keys, int ctas, int unit)
 {
+    p.unit = unit;
     p.rows = rows;
     p.keys = keys;
     p.ctas = ctas;
@@ -88,7 +88,7 @@ struct Walk {
 
     __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == n; }
     __device__ __forceinline__ int pos0() const { return kv - tokens; }
-    __device__ __forceinline__ long long end() const { return x + n + UNIT; }
+    __device__ __forceinline__ long long end(const Plan& p) const { return x + n + p.unit; }
 
     // the sequence, or the first behind it, that has rows
     __device__ __forceinline__ void enter(const PagedArgs& a)
@@ -110,11 +110,11 @@ struct Walk {
         span(a, p.keys, pos0(), kv, row0, rows, lo, hi);
         n = (hi - lo + p.keys - 1) / p.keys;
     }
-    __device__ __forceinline__ void piece()
+    __device__ __forceinline__ void piece(const Plan& p)
     {
-        const int to = (int)min((long long)n + UNIT, from + left);
-        t0 = max(from - UNIT, 0);
-        t1 = max(to - UNIT, 0);
+        const int to = (int)min((long long)n + p.unit, from + left);
+        t0 = max(from - p.unit, 0);
+        t1 = max(to - p.unit, 0);
         act = t1 > t0 || (n == 0 && from == 0);
     }
     __device__ __forceinline__ void begin_at(const PagedArgs& a, const Plan& p, const Start& s)
@@ -130,13 +130,13 @@ struct Walk {
         enter(a);
         if (left <= 0) return;
         unit(a, p);
-        piece();
+        piece(p);
     }
     __device__ __forceinline__ void next(const PagedArgs& a, const Plan& p)
     {
-        left -= min((long long)n + UNIT, from + left) - from;
+        left -= min((long long)n + p.unit, from + left) - from;
         if (left <= 0) return;
-        x += n + UNIT;
+        x += n + p.unit;
         from = 0;
         if (++head == a.Hkv) {
             head = 0;
@@ -149,7 +149,7 @@ struct Walk {
             }
             unit(a, p);
         }
-        piece();
+        piece(p);
     }
 };
 
@@ -158,7 +158,7 @@ __device__ __forceinline__ int places(const PagedArgs& a, const Plan& p, int pos
 {
     int lo, hi;
     span(a, p.keys, pos0, kv, row0, rows, lo, hi);
-    return (hi - lo + p.keys - 1) / p.keys + UNIT;
+    return (hi - lo + p.keys - 1) / p.keys + p.unit;
 }
 
 // Where this CTA's stretch begins, by all its WARPS warps (each a run of sequences).  Ends with a barrier.
