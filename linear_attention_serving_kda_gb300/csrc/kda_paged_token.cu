@@ -64,9 +64,10 @@ template <typename IO, int D, int HB> struct Token {
     static constexpr int KEYS = 16 * TEAM;                         // tokens of a tile
     static constexpr int HALF = KEYS * DP * SIZE, STAGE = 2 * HALF;  // keys, then values
     static constexpr int STAGES = STAGE <= 16384 ? 12 : 6;
-    static constexpr int CH = D == 128 && HB == 1 && SIZE == 2 ? 64 : 32;  // as shared memory allows
+    static constexpr int CH = D == 128 && HB == 1 && SIZE == 2 ? 64 : WARPS * 2 < ROWS ? 16 : 32;  // as shared memory and threads allow
     static constexpr int QS = D * SIZE + 16;                       // bytes of a row of q: eight rows in distinct banks
     static_assert(STAGES % TEAMS == 0, "a stage belongs to one team");
+    static_assert(WARPS * 32 >= ROWS * CH / 2, "two channels a thread");
     struct Smem {
         unsigned char ring[STAGES * STAGE];
         unsigned char q[2][ROWS * QS];

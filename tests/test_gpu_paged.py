@@ -580,6 +580,14 @@ def test_token_head_groups(cuda_lib, Hkv, G, io):
     Attn(c, cuda_lib, decode=True, lse=G % 2 == 0).run().check()
 
 
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [32, 64, 128, 256])
+@pytest.mark.parametrize("G", [8, 9, 16])
+def test_token_every_head_of_a_unit(cuda_lib, G, D, io):
+    c = Cache([1] * 4, [200, 3, 500, 130], Hkv=2, G=G, D=D, io=io)
+    Attn(c, cuda_lib, decode=True).run().check()
+
+
 @pytest.mark.parametrize("io,D", [("bf16", 128), ("bf16", 256), ("bf16", 32), ("f32", 64)])
 @pytest.mark.parametrize("window", [1, 15, 100, 1000])
 def test_token_window(cuda_lib, window, io, D):
