@@ -388,6 +388,9 @@ void fill_paged(PagedArgs& a, const kda_paged_params* p)
     a.Hq = p->num_heads_q;
     a.Hkv = p->num_heads_kv;
     a.G = a.Hq / a.Hkv;
+    const int bits = log2i(a.G);
+    a.g_mul = (uint32_t)(((uint64_t)1 << (31 + bits)) / a.G + 1);
+    a.g_shift = 31 + bits;
     a.D = p->head_dim;
     a.page_shift = log2i(p->page_size);
     a.num_pages = p->num_pages;

@@ -10,6 +10,8 @@ namespace kda {
 
 struct PagedArgs {
     int Hq, Hkv, G, D, N, T;
+    uint32_t g_mul;  // with g_shift: division by G (group_of)
+    int g_shift;
     int page_shift, num_pages, width;  // width: entries of a sequence's row of `pages`
     int causal, window;
     float scale;
@@ -25,6 +27,10 @@ struct PagedArgs {
     void* workspace;
     int32_t* dev_status;
 };
+
+// n / G for 0 <= n < 2^31, as n M / 2^(31 + s) with 2^(s - 1) < G <= 2^s and M = floor(2^(31 + s) / G) + 1: M G is above
+// 2^(31 + s) by at most G <= 2^s, which makes less than n 2^s / (G 2^(31 + s)) < 1 / G of difference, too little to reach the next quotient.
+__device__ __forceinline__ int group_of(const PagedArgs& a, int n) { return (int)(((uint64_t)(uint32_t)n * a.g_mul) >> a.g_shift); }
 
 // Tokens that a row of the table can name.
 __device__ __forceinline__ long long paged_capacity(const PagedArgs& a) { return (long long)a.width << a.page_shift; }

@@ -18,7 +18,7 @@ namespace {
 
 using namespace paged;
 
-constexpr int THREADS = 384;  // two softmax warpgroups, a warp that issues products, one that loads keys and values, two that load rows
+constexpr int THREADS = 384;  // two softmax warpgroups, a warp that issues products, one that loads keys and values, two that load rows and store outputs
 constexpr int CTAS = 152;  // one an SM
 constexpr uint32_t WAIT = 1u << 20;
 constexpr float LAG = 8.f;
@@ -36,7 +36,7 @@ template <int DP> struct Shape {
     struct Smem {
         unsigned char q[Q];
         unsigned char ring[SLOTS * SLOT];
-        uint64_t full[SLOTS], empty[SLOTS], scores[2], weights[2], product[2], rows[2], free[2], taken[2], drained;
+        uint64_t full[SLOTS], empty[SLOTS], scores[2], weights[2], product[2], rows[2], free[2], taken[2], ready[2], drained;
         uint32_t hidden[8], tmem;
         Start start;
     };
@@ -97,6 +97,16 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, int x, 
         : "memory");
 }
 
+__device__ __forceinline__ void tma_store_3d(const void* tmap, int x, int y, int z, const void* src)
+{
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(tmap), "r"(x), "r"(y), "r"(z),
+                 "r"(ptx::smem_u32(src))
+                 : "memory");
+}
+
+// A tile's rows as whole tokens of all the group's heads: a box of the output.
+__host__ __device__ inline bool whole_tokens(int G) { return (G & (G - 1)) == 0 && G <= 128; }
+
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
     float r;
@@ -129,7 +139,8 @@ struct Work : Walk {
 };
 
 template <int DP, int D> __global__ void __launch_bounds__(THREADS, 1)
-paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap)
+paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                  const __grid_constant__ CUtensorMap omap)
 {
     using L = Shape<DP>;
     constexpr int KEYS = L::KEYS, BLOCKS = L::BLOCKS, SLOT = L::SLOT, SLOTS = L::SLOTS;
@@ -149,6 +160,7 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
             ptx::mbar_init(&s.rows[i], 2);
             ptx::mbar_init(&s.free[i], 1);
             ptx::mbar_init(&s.taken[i], 4);
+            ptx::mbar_init(&s.ready[i], 4);
         }
         ptx::mbar_init(&s.drained, 1);
         ptx::fence_mbar_init();
@@ -157,6 +169,7 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
     if (tid == 32) {  // the maps are the launch's own arguments: no need to wait for them
         ptx::prefetch_map(&kmap);
         ptx::prefetch_map(&vmap);
+        ptx::prefetch_map(&omap);
     }
     if (warp == 8) ptx::tmem_alloc(&s.tmem, 512);
     __syncthreads();
@@ -220,12 +233,56 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
             if (!ok)
                 for (uint32_t u = use > SLOTS ? use - SLOTS : 0; u < use; ++u) ptx::mbar_wait(&s.full[u % SLOTS], (u / SLOTS) & 1, WAIT);
         } else if (warp >= 10) {
-            // ---- rows: half of each tile by either warp, 16-byte pieces permuted within eight rows as the descriptor expects
+            // ---- rows: half of each tile by either warp, 16-byte pieces permuted within eight rows as the descriptor expects;
+            // and the outputs of the unit before from the ring's slots, the first slot by one warp, the second by the other
             constexpr int PIECES = DP / 8, AT_ONCE = 32 / PIECES;  // rows that a warp's 32 pieces make
-            const int e = lane % PIECES, r0 = (warp & 1) * 64 + lane / PIECES;
-            const int dt = AT_ONCE / a.G, dg = AT_ONCE % a.G;
-            uint32_t count[2] = {0, 0};
+            const int me = warp & 1, e = lane % PIECES, r0 = me * 64 + lane / PIECES;
+            const int dt = group_of(a, AT_ONCE), dg = AT_ONCE - dt * a.G;
+            uint32_t count[2] = {0, 0}, stored = 0, use = 0;
             bool ok = true;
+            // slot `me` of a unit that leaves through the ring
+            struct {
+                bool any = false;
+                int begin, row0, rows, head;
+                uint32_t use;
+            } out;
+            const auto store = [&] {
+                if (!out.any || !ok) return;
+                out.any = false;
+                constexpr int COLS = L::COLS, PC = COLS / 8, ROWS_AT_ONCE = 32 / PC;
+                const int t = L::OUT == 1 ? me : 0, col = L::OUT == 1 ? 0 : me * COLS, c8 = lane % PC;
+                if (!(ok = wait(&s.ready[me], stored++))) return;
+                const unsigned char* slot = s.ring + out.use % SLOTS * SLOT;
+                const int last = min(128, out.rows - t * 128);
+                if (last == 128 && whole_tokens(a.G)) {
+                    if (lane == 0) {
+                        for (int b = 0; b < COLS / 64; ++b)
+                            tma_store_3d(&omap, col + b * 64, out.head * a.G, out.begin + group_of(a, out.row0 + t * 128), slot + b * (128 * 128));
+                        ptx::bulk_commit();
+                        ptx::bulk_wait_read_all();
+                        ptx::mbar_arrive(&s.empty[out.use % SLOTS]);
+                    }
+                    __syncwarp();
+                    return;
+                }
+                const int ot = group_of(a, ROWS_AT_ONCE), og = ROWS_AT_ONCE - ot * a.G, f0 = out.row0 + t * 128 + lane / PC, tok0 = group_of(a, f0);
+                int g = f0 - tok0 * a.G;
+                __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + ((size_t)(out.begin + tok0) * a.Hq + out.head * a.G) * D + col + c8 * 8;
+#pragma unroll 8
+                for (int rr = lane / PC; rr < last; rr += ROWS_AT_ONCE) {
+                    const uint4 x = *reinterpret_cast<const uint4*>(slot + c8 / 8 * (128 * 128) + rr * 128 + ((c8 ^ rr) & 7) * 16);
+                    if (col + c8 * 8 < D) *reinterpret_cast<uint4*>(dst + (size_t)g * D) = x;
+                    g += og;
+                    dst += (size_t)ot * a.Hq * D;
+                    if (g >= a.G) {
+                        g -= a.G;
+                        dst += (size_t)a.Hq * D;
+                    }
+                }
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&s.empty[out.use % SLOTS]);
+            };
             Work w;
             for (w.begin_at(a, p, s.start); w.left > 0 && ok; w.next(a, p)) {
                 if (!w.act || w.n == 0) continue;
@@ -233,11 +290,11 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
 #pragma unroll
                 for (int t = 0; t < L::TILES; ++t) {
                     if (t >= w.tiles) break;
-                    if (!(ok = wait(&s.free[t], count[t] + 1))) break;  // the scores of the item before are done
+                    if (!(ok = wait(&s.free[t], count[t] + 1))) break;  // the scores of the unit before are done
                     ++count[t];
-                    const int f = w.row0 + t * 128 + r0;
-                    int g = f % a.G;
-                    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (w.begin + f / a.G) * a.q_stride + (long long)w.head * a.G * D + e * 8;
+                    const int f = w.row0 + t * 128 + r0, tok = group_of(a, f);
+                    int g = f - tok * a.G;
+                    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (w.begin + tok) * a.q_stride + (long long)w.head * a.G * D + e * 8;
                     unsigned char* dst = s.q + t * (128 * DP * 2) + e / 8 * (128 * 128);
 #pragma unroll 4
                     for (int r = r0; r < r0 / 64 * 64 + 64; r += AT_ONCE) {
@@ -261,8 +318,21 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(&s.rows[t]);
                 }
+                store();  // of the unit before: these rows went first
+                use += 2 * w.count;
+                if (w.staged) {
+                    out.any = me < w.tiles * L::OUT;
+                    out.begin = w.begin;
+                    out.row0 = w.row0;
+                    out.rows = w.rows;
+                    out.head = w.head;
+                    out.use = use + me;
+                    use += w.tiles * L::OUT;
+                }
             }
+            store();
             ptx::cp_async_wait_all();
+            ptx::bulk_wait_all();
         } else if (warp == 8) {
             // ---- products
             const bool leader = ptx::elect_one();
@@ -432,7 +502,7 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
             const int row = t * 128 + r;
             const bool mine = t < w.tiles;
             const bool live = mine && t * 128 + (warp & 3) * 32 < w.rows;  // the warp has rows
-            const int f = w.row0 + min(row, w.rows - 1), tok = f / a.G, head = w.head * a.G + f % a.G;
+            const int f = w.row0 + min(row, w.rows - 1), tok = group_of(a, f), head = w.head * a.G + f - tok * a.G;
             float m = -INFINITY, sum = 0.f;
             if (mine && w.count > 0) {
                 const int pos = w.pos0() + tok;
@@ -529,10 +599,9 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
                 const float inv = sum == 0.f ? 0.f : 1.f / sum;
                 const size_t cell = (size_t)blockIdx.x * 2 + (w.t0 == 0);
                 if (w.staged) {
-                    // a thread's row into the slot, 16-byte pieces permuted within eight rows; then whole rows out
+                    // a thread's row into the slot, 16-byte pieces permuted within eight rows; whole rows leave from there
                     use += 2 * w.count + t * L::OUT;
-                    constexpr int COLS = L::COLS, PIECES = COLS / 8, AT_ONCE = 128 / PIECES;
-                    const int dt = AT_ONCE / a.G, dg = AT_ONCE % a.G;
+                    constexpr int COLS = L::COLS;
 #pragma unroll 1
                     for (int i = 0; i < L::OUT; ++i, ++use) {
                         unsigned char* slot = s.ring + use % SLOTS * SLOT;
@@ -546,34 +615,18 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
                                 for (int k = 0; k < 32; ++k) o[k] = sum == 0.f ? 0.f : o[k] * inv;
 #pragma unroll
                                 for (int k = 0; k < 4; ++k)
-                                    *reinterpret_cast<uint4*>(slot + r * (COLS * 2) + ((e / 8 + k) ^ (r & 7)) * 16) =
+                                    *reinterpret_cast<uint4*>(slot + e / 64 * (128 * 128) + r * 128 + ((e % 64 / 8 + k) ^ (r & 7)) * 16) =
                                         make_uint4(pack_bf16(o[8 * k], o[8 * k + 1]), pack_bf16(o[8 * k + 2], o[8 * k + 3]),
                                                    pack_bf16(o[8 * k + 4], o[8 * k + 5]), pack_bf16(o[8 * k + 6], o[8 * k + 7]));
                             }
                         }
-                        if (i == L::OUT - 1) {  // O may be overwritten
-                            ptx::tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) ptx::mbar_arrive(&s.taken[t]);
-                        }
-                        asm volatile("bar.sync %0, 128;" ::"r"(2 + t) : "memory");
-                        const int e = r % PIECES, f0 = w.row0 + t * 128 + r / PIECES;
-                        int g = f0 % a.G;
-                        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + ((size_t)(w.begin + f0 / a.G) * a.Hq + w.head * a.G) * D + i * COLS + e * 8;
-#pragma unroll 4
-                        for (int rr = r / PIECES; rr < 128; rr += AT_ONCE) {
-                            if (ok && t * 128 + rr < w.rows && i * COLS + e * 8 < D)
-                                *reinterpret_cast<uint4*>(out + (size_t)g * D) = *reinterpret_cast<const uint4*>(slot + rr * (COLS * 2) + (e ^ (rr & 7)) * 16);
-                            g += dg;
-                            out += (size_t)dt * a.Hq * D;
-                            if (g >= a.G) {
-                                g -= a.G;
-                                out += (size_t)a.Hq * D;
-                            }
-                        }
+                        ptx::tc_fence_before();
                         ptx::fence_proxy_async_smem();
-                        asm volatile("bar.sync %0, 128;" ::"r"(2 + t) : "memory");
-                        if (r == 0) ptx::mbar_arrive(&s.empty[use % SLOTS]);
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (i == L::OUT - 1) ptx::mbar_arrive(&s.taken[t]);  // O may be overwritten
+                            if (ok) ptx::mbar_arrive(&s.ready[L::OUT == 1 ? t : i]);
+                        }
                     }
                     use += (w.tiles - 1 - t) * L::OUT;
                 } else {
@@ -645,6 +698,20 @@ bool encode_cache(CUtensorMap* m, const void* base, const PagedArgs& a, int keys
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// [T][Hq][D]; boxes of 128 / G tokens of a group's heads and 64 channels.
+bool encode_out(CUtensorMap* m, const PagedArgs& a)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)a.D, (cuuint64_t)a.Hq, (cuuint64_t)a.T};
+    const cuuint64_t strides[2] = {(cuuint64_t)a.D * 2, (cuuint64_t)a.Hq * a.D * 2};
+    const int G = whole_tokens(a.G) ? a.G : 1;  // (not used otherwise)
+    const cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)(128 / G)};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.out, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int DP, int D> cudaError_t launch(const PagedArgs& a, cudaStream_t st)
 {
     using L = Shape<DP>;
@@ -656,11 +723,11 @@ template <int DP, int D> cudaError_t launch(const PagedArgs& a, cudaStream_t st)
         return cudaFuncSetAttribute(paged_bf16_kernel<DP, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     });
     if (e != cudaSuccess) return e;
-    CUtensorMap km, vm;
-    if (!encode_cache(&km, a.k, a, L::KEYS) || !encode_cache(&vm, a.v, a, L::KEYS)) return cudaErrorInvalidValue;
+    CUtensorMap km, vm, om;
+    if (!encode_cache(&km, a.k, a, L::KEYS) || !encode_cache(&vm, a.v, a, L::KEYS) || !encode_out(&om, a)) return cudaErrorInvalidValue;
     Plan p;
     lay_out(p, a, 128 * L::TILES, L::KEYS, CTAS, L::UNIT);
-    e = launch_dependent(paged_bf16_kernel<DP, D>, CTAS, THREADS, smem, st, a, p, km, vm);
+    e = launch_dependent(paged_bf16_kernel<DP, D>, CTAS, THREADS, smem, st, a, p, km, vm, om);
     if (e == cudaSuccess) e = launch_join<__nv_bfloat16, D>(a, p, st);
     return e;
 }

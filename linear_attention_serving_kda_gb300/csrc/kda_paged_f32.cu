@@ -47,8 +47,9 @@ template <int D, int R> __global__ void __launch_bounds__(FT, D == 256 ? 1 : 2) 
         for (int i = tid; i < R * (D / 4); i += FT) {
             const int r = i / (D / 4), e = i % (D / 4), f = it.row0 + r;
             const bool in = r < it.rows;
+            const int tok = group_of(a, f);
             ptx::cp_async16(s.q + r * QS + 4 * e,
-                            static_cast<const float*>(a.q) + (in ? (it.begin + f / a.G) * a.q_stride + (long long)(h * a.G + f % a.G) * D + 4 * e : 0), in ? 16 : 0);
+                            static_cast<const float*>(a.q) + (in ? (it.begin + tok) * a.q_stride + (long long)(h * a.G + f - tok * a.G) * D + 4 * e : 0), in ? 16 : 0);
         }
         float m[RI], l[RI];
         float2 o[RI][DI][DW / 2];
@@ -57,7 +58,7 @@ template <int D, int R> __global__ void __launch_bounds__(FT, D == 256 ? 1 : 2) 
         for (int i = 0; i < RI; ++i) {
             m[i] = -INFINITY;
             l[i] = 0.f;
-            pos[i] = it.pos0() + (it.row0 + ty + 16 * i) / a.G;
+            pos[i] = it.pos0() + group_of(a, it.row0 + ty + 16 * i);
 #pragma unroll
             for (int d = 0; d < DI; ++d)
 #pragma unroll
@@ -172,9 +173,9 @@ template <int D, int R> __global__ void __launch_bounds__(FT, D == 256 ? 1 : 2) 
         for (int i = 0; i < RI; ++i) {
 #pragma unroll
             for (int x2 = 8; x2 > 0; x2 >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], x2);
-            const int r = ty + 16 * i, f = it.row0 + r;
+            const int r = ty + 16 * i, f = it.row0 + r, tok = group_of(a, f);
             if (r >= it.rows) continue;
-            const size_t row = (size_t)(it.begin + f / a.G) * a.Hq + h * a.G + f % a.G;
+            const size_t row = (size_t)(it.begin + tok) * a.Hq + h * a.G + f - tok * a.G;
             const size_t cell = (size_t)blockIdx.x * 2 + (it.t0 == 0);
             const bool whole = it.whole(), none = l[i] == 0.f;
             const float2 inv = both2(!whole ? 1.f : none ? 0.f : 1.f / l[i]);

@@ -27,7 +27,8 @@ struct Cut {
 
 struct Plan {
     int rows;       // of a tile
-    int keys;       // of a tile
+    int keys;       // of a tile, a power of two
+    int key_shift;
     int ctas;
     int unit;       // places of a unit besides its key tiles
     int part_rows;  // rows kept of a part
@@ -41,6 +42,7 @@ inline size_t lay_out(Plan& p, const PagedArgs& a, int rows, int keys, int ctas,
     p.unit = unit;
     p.rows = rows;
     p.keys = keys;
+    for (p.key_shift = 0; (1 << p.key_shift) < keys;) ++p.key_shift;
     p.ctas = ctas;
     p.part_rows = (int)std::min<int64_t>(rows, (int64_t)a.T * a.G);
     unsigned char* w = static_cast<unsigned char*>(a.workspace);
@@ -67,7 +69,7 @@ __device__ __forceinline__ void span(const PagedArgs& a, int keys, int pos0, int
     lo = 0;
     hi = kv;
     if (!a.causal) return;
-    const long long p0 = (long long)pos0 + row0 / a.G, p1 = (long long)pos0 + (row0 + rows - 1) / a.G;
+    const long long p0 = (long long)pos0 + group_of(a, row0), p1 = (long long)pos0 + group_of(a, row0 + rows - 1);
     hi = (int)max(0ll, min((long long)kv, p1 + 1));
     if (a.window) {
         const int unit = min(keys, 1 << a.page_shift);
@@ -108,7 +110,7 @@ struct Walk {
     {
         rows = min(p.rows, all - row0);
         span(a, p.keys, pos0(), kv, row0, rows, lo, hi);
-        n = (hi - lo + p.keys - 1) / p.keys;
+        n = (hi - lo + p.keys - 1) >> p.key_shift;
     }
     __device__ __forceinline__ void piece(const Plan& p)
     {
@@ -158,7 +160,7 @@ __device__ __forceinline__ int places(const PagedArgs& a, const Plan& p, int pos
 {
     int lo, hi;
     span(a, p.keys, pos0, kv, row0, rows, lo, hi);
-    return (hi - lo + p.keys - 1) / p.keys + p.unit;
+    return ((hi - lo + p.keys - 1) >> p.key_shift) + p.unit;
 }
 
 // Where this CTA's stretch begins, by all its WARPS warps (each a run of sequences).  Ends with a barrier.
@@ -305,8 +307,8 @@ template <typename IO, int D> __global__ void __launch_bounds__(JT) join_kernel(
     for (int i = 0; i < EACH; ++i)
         turned[lane][warp * EACH + i] = l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(y[i].x * inv, y[i].y * inv, y[i].z * inv, y[i].w * inv);
     const auto row_of = [&](int rr) {
-        const int f = cut.row0 + blockIdx.y * 32 + rr;
-        return (size_t)(cut.begin + f / a.G) * a.Hq + cut.head * a.G + f % a.G;
+        const int f = cut.row0 + blockIdx.y * 32 + rr, tok = group_of(a, f);
+        return (size_t)(cut.begin + tok) * a.Hq + cut.head * a.G + f - tok * a.G;
     };
     if (a.lse && warp == 0 && in) a.lse[row_of(lane)] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
     __syncthreads();
