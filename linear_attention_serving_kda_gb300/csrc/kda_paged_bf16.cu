@@ -97,6 +97,13 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, int x, 
         : "memory");
 }
 
+__device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, int x, int y, int z, uint64_t* bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(ptx::smem_u32(dst)),
+        "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(ptx::smem_u32(bar))
+        : "memory");
+}
 __device__ __forceinline__ void tma_store_3d(const void* tmap, int x, int y, int z, const void* src)
 {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(tmap), "r"(x), "r"(y), "r"(z),
@@ -104,7 +111,7 @@ __device__ __forceinline__ void tma_store_3d(const void* tmap, int x, int y, int
                  : "memory");
 }
 
-// A tile's rows as whole tokens of all the group's heads: a box of the output.
+// A tile's rows as whole tokens of all the group's heads: a box of the queries and of the output.
 __host__ __device__ inline bool whole_tokens(int G) { return (G & (G - 1)) == 0 && G <= 128; }
 
 __device__ __forceinline__ float max3(float a, float b, float c)
@@ -140,7 +147,7 @@ struct Work : Walk {
 
 template <int DP, int D> __global__ void __launch_bounds__(THREADS, 1)
 paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                  const __grid_constant__ CUtensorMap omap)
+                  const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap omap)
 {
     using L = Shape<DP>;
     constexpr int KEYS = L::KEYS, BLOCKS = L::BLOCKS, SLOT = L::SLOT, SLOTS = L::SLOTS;
@@ -157,7 +164,7 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
             ptx::mbar_init(&s.scores[i], 1);
             ptx::mbar_init(&s.product[i], 1);
             ptx::mbar_init(&s.weights[i], 4);
-            ptx::mbar_init(&s.rows[i], 2);
+            ptx::mbar_init(&s.rows[i], whole_tokens(a.G) ? 1 : 2);
             ptx::mbar_init(&s.free[i], 1);
             ptx::mbar_init(&s.taken[i], 4);
             ptx::mbar_init(&s.ready[i], 4);
@@ -169,6 +176,7 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
     if (tid == 32) {  // the maps are the launch's own arguments: no need to wait for them
         ptx::prefetch_map(&kmap);
         ptx::prefetch_map(&vmap);
+        ptx::prefetch_map(&qmap);
         ptx::prefetch_map(&omap);
     }
     if (warp == 8) ptx::tmem_alloc(&s.tmem, 512);
@@ -233,8 +241,9 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
             if (!ok)
                 for (uint32_t u = use > SLOTS ? use - SLOTS : 0; u < use; ++u) ptx::mbar_wait(&s.full[u % SLOTS], (u / SLOTS) & 1, WAIT);
         } else if (warp >= 10) {
-            // ---- rows: half of each tile by either warp, 16-byte pieces permuted within eight rows as the descriptor expects;
-            // and the outputs of the unit before from the ring's slots, the first slot by one warp, the second by the other
+            // ---- rows: a tensor copy, or (tiles that cut tokens) half of each tile by either warp, 16-byte pieces permuted within
+            // eight rows as the descriptor expects; and the outputs of the unit before from the ring's slots, the first slot by one warp,
+            // the second by the other.  (Pieces by threads take 3 us a unit, copies nothing that shows: 64 prompts of 333 rows 202 -> 190 us.)
             constexpr int PIECES = DP / 8, AT_ONCE = 32 / PIECES;  // rows that a warp's 32 pieces make
             const int me = warp & 1, e = lane % PIECES, r0 = me * 64 + lane / PIECES;
             const int dt = group_of(a, AT_ONCE), dg = AT_ONCE - dt * a.G;
@@ -289,13 +298,23 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
                 w.derive(KEYS);
 #pragma unroll
                 for (int t = 0; t < L::TILES; ++t) {
-                    if (t >= w.tiles) break;
+                    if (t >= w.tiles || (whole_tokens(a.G) && me == 1)) break;
                     if (!(ok = wait(&s.free[t], count[t] + 1))) break;  // the scores of the unit before are done
                     ++count[t];
+                    unsigned char* base = s.q + t * (128 * DP * 2);
+                    if (whole_tokens(a.G)) {
+                        if (lane == 0) {
+                            ptx::mbar_arrive_expect_tx(&s.rows[t], 128 * DP * 2);
+                            for (int b = 0; b < BLOCKS; ++b)
+                                tma_load_3d(base + b * (128 * 128), &qmap, b * 64, w.head * a.G, w.begin + group_of(a, w.row0 + t * 128), &s.rows[t]);
+                        }
+                        __syncwarp();
+                        continue;
+                    }
                     const int f = w.row0 + t * 128 + r0, tok = group_of(a, f);
                     int g = f - tok * a.G;
                     const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (w.begin + tok) * a.q_stride + (long long)w.head * a.G * D + e * 8;
-                    unsigned char* dst = s.q + t * (128 * DP * 2) + e / 8 * (128 * 128);
+                    unsigned char* dst = base + e / 8 * (128 * 128);
 #pragma unroll 4
                     for (int r = r0; r < r0 / 64 * 64 + 64; r += AT_ONCE) {
                         const bool in = t * 128 + r < w.rows && e * 8 < D;
@@ -308,12 +327,7 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
                         }
                     }
                     ptx::cp_async_commit();
-                }
-#pragma unroll
-                for (int t = 0; t < L::TILES; ++t) {
-                    if (t >= w.tiles || !ok) break;
-                    if (t == 0 && w.tiles == 2) ptx::cp_async_wait_prev();
-                    else ptx::cp_async_wait_all();
+                    ptx::cp_async_wait_all();
                     ptx::fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(&s.rows[t]);
@@ -331,8 +345,11 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
                 }
             }
             store();
-            ptx::cp_async_wait_all();
             ptx::bulk_wait_all();
+            // what is on its way has to land first
+            if (!ok && whole_tokens(a.G) && me == 0)
+                for (int t = 0; t < L::TILES; ++t)
+                    if (count[t]) ptx::mbar_wait(&s.rows[t], (count[t] - 1) & 1, WAIT);
         } else if (warp == 8) {
             // ---- products
             const bool leader = ptx::elect_one();
@@ -698,18 +715,18 @@ bool encode_cache(CUtensorMap* m, const void* base, const PagedArgs& a, int keys
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// [T][Hq][D]; boxes of 128 / G tokens of a group's heads and 64 channels.
-bool encode_out(CUtensorMap* m, const PagedArgs& a)
+// [T][Hq][D] rows; boxes of 128 / G tokens of a group's heads and 64 channels.
+bool encode_rows(CUtensorMap* m, const void* base, long long stride, const PagedArgs& a)
 {
     PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
     if (!enc) return false;
     const cuuint64_t dims[3] = {(cuuint64_t)a.D, (cuuint64_t)a.Hq, (cuuint64_t)a.T};
-    const cuuint64_t strides[2] = {(cuuint64_t)a.D * 2, (cuuint64_t)a.Hq * a.D * 2};
+    const cuuint64_t strides[2] = {(cuuint64_t)a.D * 2, (cuuint64_t)stride * 2};
     const int G = whole_tokens(a.G) ? a.G : 1;  // (not used otherwise)
     const cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)(128 / G)};
     const cuuint32_t estr[3] = {1, 1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.out, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int DP, int D> cudaError_t launch(const PagedArgs& a, cudaStream_t st)
@@ -723,11 +740,13 @@ template <int DP, int D> cudaError_t launch(const PagedArgs& a, cudaStream_t st)
         return cudaFuncSetAttribute(paged_bf16_kernel<DP, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     });
     if (e != cudaSuccess) return e;
-    CUtensorMap km, vm, om;
-    if (!encode_cache(&km, a.k, a, L::KEYS) || !encode_cache(&vm, a.v, a, L::KEYS) || !encode_out(&om, a)) return cudaErrorInvalidValue;
+    CUtensorMap km, vm, qm, om;
+    if (!encode_cache(&km, a.k, a, L::KEYS) || !encode_cache(&vm, a.v, a, L::KEYS) ||
+        !encode_rows(&qm, a.q, a.q_stride, a) || !encode_rows(&om, a.out, (long long)a.Hq * a.D, a))
+        return cudaErrorInvalidValue;
     Plan p;
     lay_out(p, a, 128 * L::TILES, L::KEYS, CTAS, L::UNIT);
-    e = launch_dependent(paged_bf16_kernel<DP, D>, CTAS, THREADS, smem, st, a, p, km, vm, om);
+    e = launch_dependent(paged_bf16_kernel<DP, D>, CTAS, THREADS, smem, st, a, p, km, vm, qm, om);
     if (e == cudaSuccess) e = launch_join<__nv_bfloat16, D>(a, p, st);
     return e;
 }
