@@ -26,7 +26,7 @@ constexpr float LAG = 8.f;
 template <int DP> struct Shape {
     static constexpr int TILES = DP == 256 ? 1 : 2;    // tiles of 128 rows: TMEM holds 512 columns, O takes DP of them a tile
     static constexpr int KEYS = DP == 256 ? 64 : 128;
-    static constexpr int UNIT = DP == 256 ? 7 : 3;
+    static constexpr int UNIT = DP == 256 ? 3 : 2;
     static constexpr int BLOCKS = DP / 64;             // 128-byte pieces of a row
     static constexpr int SLOT = KEYS * DP * 2;
     static constexpr int SLOTS = DP == 64 ? 8 : 5;
@@ -395,10 +395,11 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
                     if (!wait(&s.full[vp.slot], vp.phase)) return false;
                     const int have = w.k1 - w.k0 - j * KEYS;
                     if (have < KEYS) {  // what lies behind the tokens may be anything: zeros, whose weights are zero
-                        for (int i = lane; i < (KEYS - have) * 8 * BLOCKS; i += 32) {
-                            const int r = have + i / 8 % (KEYS - have), blk = i / (8 * (KEYS - have));
-                            *reinterpret_cast<uint4*>(s.ring + vp.slot * SLOT + blk * (KEYS * 128) + r * 128 + i % 8 * 16) = make_uint4(0, 0, 0, 0);
-                        }
+                        // (a linear fill of each block's last rows: with a division a piece it took 5500 cycles, the next unit's start)
+#pragma unroll
+                        for (int blk = 0; blk < BLOCKS; ++blk)
+                            for (int at = have * 128 + lane * 16; at < KEYS * 128; at += 512)
+                                *reinterpret_cast<uint4*>(s.ring + vp.slot * SLOT + blk * (KEYS * 128) + at) = make_uint4(0, 0, 0, 0);
                         ptx::fence_proxy_async_smem();
                         __syncwarp();
                     }
