@@ -198,7 +198,7 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
             bool ok = true;
             const int box = min(KEYS, 1 << a.page_shift), boxes = KEYS / box;
             Work w;
-            for (w.begin_at(a, p, s.start); w.left > 0 && ok; w.next(a, p)) {
+            for (w.start(p, s.start); ok && w.step(a, p);) {
                 if (!w.act) continue;
                 w.derive(KEYS);
                 const int ahead = w.tiles == 1 ? 2 : 1;
@@ -293,7 +293,7 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
                 if (lane == 0) ptx::mbar_arrive(&s.empty[out.use % SLOTS]);
             };
             Work w;
-            for (w.begin_at(a, p, s.start); w.left > 0 && ok; w.next(a, p)) {
+            for (w.start(p, s.start); ok && w.step(a, p);) {
                 if (!w.act || w.n == 0) continue;
                 w.derive(KEYS);
 #pragma unroll
@@ -361,7 +361,7 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
             uint32_t wcount[2] = {0, 0}, qcount[2] = {0, 0};
             bool ok = true;
             Work w;
-            for (w.begin_at(a, p, s.start); w.left > 0 && ok; w.next(a, p)) {
+            for (w.start(p, s.start); ok && w.step(a, p);) {
                 if (!w.act || w.n == 0) continue;
                 w.derive(KEYS);
                 const bool two = w.tiles == 2;
@@ -513,7 +513,7 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
         uint32_t scount[2] = {0, 0}, sbase[2] = {0, 0}, pcount[2] = {0, 0}, kt = 0, use = 0;
         bool ok = true;
         Work w;
-        for (w.begin_at(a, p, s.start); w.left > 0; w.next(a, p)) {
+        for (w.start(p, s.start); w.step(a, p);) {
             if (t >= L::TILES) break;
             if (!w.act) continue;
             w.derive(KEYS);
@@ -525,7 +525,7 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
             if (mine && w.count > 0) {
                 const int pos = w.pos0() + tok;
                 const int hi = a.causal ? min(w.k1, pos + 1) : w.k1;
-                const int lo = a.window ? (int)max(0ll, (long long)pos - a.window + 1) : 0;
+                const int lo = a.window && pos >= a.window ? pos - a.window + 1 : 0;
                 for (int st = w.tiles == 2 ? t : 0; st < w.steps; st += w.tiles) {
                     const int j = w.tiles == 2 ? st >> 1 : st, b = st & 1, k0 = w.k0 + j * KEYS;
                     ok = ok && wait(&s.scores[b], scount[b]);
@@ -546,6 +546,7 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
                                     uint32_t seen = low_bits(hi - k0 - i) & ~low_bits(lo - k0 - i);
                                     if ((hide >> (i >> box_shift)) & 1) seen &= 0xffff0000u;
                                     if ((hide >> ((i + 16) >> box_shift)) & 1) seen &= 0x0000ffffu;
+                                    if (__all_sync(0xffffffffu, seen == 0xffffffffu)) continue;
 #pragma unroll
                                     for (int e = 0; e < 32; ++e) v[i + e] = (seen >> e) & 1 ? v[i + e] : -INFINITY;
                                 }

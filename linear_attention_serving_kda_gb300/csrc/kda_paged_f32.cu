@@ -40,7 +40,7 @@ template <int D, int R> __global__ void __launch_bounds__(FT, D == 256 ? 1 : 2) 
     find_start<FT / 32>(a, p, start);
     if (tid == 0) p.cut[blockIdx.x].rows = 0;
     Walk it;
-    for (it.begin_at(a, p, start); it.left > 0; it.next(a, p)) {
+    for (it.start(p, start); it.step(a, p);) {
         if (!it.act) continue;
         const int h = it.head, first = it.lo + it.t0 * KEYS, last = min(it.hi, it.lo + it.t1 * KEYS);
         __syncthreads();

@@ -69,12 +69,9 @@ __device__ __forceinline__ void span(const PagedArgs& a, int keys, int pos0, int
     lo = 0;
     hi = kv;
     if (!a.causal) return;
-    const long long p0 = (long long)pos0 + group_of(a, row0), p1 = (long long)pos0 + group_of(a, row0 + rows - 1);
-    hi = (int)max(0ll, min((long long)kv, p1 + 1));
-    if (a.window) {
-        const int unit = min(keys, 1 << a.page_shift);
-        lo = (int)min((long long)hi, max(0ll, p0 - a.window + 1)) & ~(unit - 1);
-    }
+    const int p0 = pos0 + group_of(a, row0), p1 = pos0 + group_of(a, row0 + rows - 1);
+    hi = max(0, min(kv, p1 + 1));
+    if (a.window) lo = min(hi, p0 >= a.window ? p0 - a.window + 1 : 0) & ~(min(keys, 1 << a.page_shift) - 1);
 }
 
 // A walk along a stretch, piece of a unit after piece of a unit.
@@ -119,39 +116,51 @@ struct Walk {
         t1 = max(to - p.unit, 0);
         act = t1 > t0 || (n == 0 && from == 0);
     }
-    __device__ __forceinline__ void begin_at(const PagedArgs& a, const Plan& p, const Start& s)
+    bool begun, new_seq, new_unit;
+    __device__ __forceinline__ void start(const Plan& p, const Start& s)
     {
         x = stretch(s.line, blockIdx.x, p.ctas);
         left = stretch(s.line, blockIdx.x + 1, p.ctas) - x;
-        if (left <= 0) return;
         seq = s.seq;
         row0 = s.row0;
         head = s.head;
         from = s.at;
         x -= from;
-        enter(a);
-        if (left <= 0) return;
-        unit(a, p);
-        piece(p);
+        begun = false;
+        new_seq = new_unit = true;
     }
-    __device__ __forceinline__ void next(const PagedArgs& a, const Plan& p)
+    // On to the next piece; false: the stretch is at its end.  (The one place where each step is taken: several roles of a
+    // kernel have it each, and their code shares an instruction cache that units of a tile or two run out of.)
+    __device__ __forceinline__ bool step(const PagedArgs& a, const Plan& p)
     {
-        left -= min((long long)n + p.unit, from + left) - from;
-        if (left <= 0) return;
-        x += n + p.unit;
-        from = 0;
-        if (++head == a.Hkv) {
-            head = 0;
-            row0 += p.rows;
-            if (row0 >= all) {
-                row0 = 0;
-                ++seq;
-                enter(a);
-                if (left <= 0) return;
+        if (begun) {
+            left -= min((long long)n + p.unit, from + left) - from;
+            x += n + p.unit;
+            from = 0;
+            if (++head == a.Hkv) {
+                head = 0;
+                row0 += p.rows;
+                new_unit = true;
+                if (row0 >= all) {
+                    row0 = 0;
+                    ++seq;
+                    new_seq = true;
+                }
             }
+        }
+        begun = true;
+        if (left <= 0) return false;
+        if (new_seq) {
+            enter(a);
+            new_seq = false;
+            if (left <= 0) return false;
+        }
+        if (new_unit) {
             unit(a, p);
+            new_unit = false;
         }
         piece(p);
+        return true;
     }
 };
 
