@@ -589,7 +589,7 @@ typedef struct kda_paged_params {
     int32_t rotary_dim;           /* append: 0, or as in kda_rope_params        */
     int32_t rope_layout;          /* append                                     */
     float rope_amplitude;         /* append                                     */
-    float scale;                  /* attention: of q.k; finite, > 0             */
+    float scale;                  /* attention: of q.k; > 0, < 2^127            */
     int64_t cache_page_stride;    /* elements; 0: dense [page][token][head][D]; */
     int64_t cache_token_stride;   /*   multiples of 16 bytes, no two places of  */
     int64_t cache_head_stride;    /*   a page and no two pages overlapping      */
@@ -608,6 +608,7 @@ typedef struct kda_paged_params {
  *   kv_lens[s] < 0: padding, the sequence is skipped.  kv_lens[s] above
  *       pages_per_seq * page_size: flagged (KDA_DEV_BAD_SEQLENS), skipped.  A row
  *       before token 0 (more rows than kv_lens[s]): flagged, the row skipped.
+ *       Bad cu_seqlens as in kda_gdn_prefill_varlen.
  *   A page that is negative or >= num_pages: flagged (KDA_DEV_BAD_PAGE), the row skipped.
  *   positions: device int32 [T], nullable: the positions that rows turn to
  *       (default: their token).
@@ -635,7 +636,8 @@ KDA_API int kda_paged_append_decode(const kda_paged_params* p, int32_t B, const 
  *       a row that sees none), for joining with attention over other tokens.
  *   A sequence with kv_lens[s] < 0 is skipped; above pages_per_seq *
  *       page_size, or with bad cu_seqlens, it is flagged (KDA_DEV_BAD_SEQLENS)
- *       and skipped; out and lse keep what they held.
+ *       and skipped; its out and lse keep what they held (bad cu_seqlens: what
+ *       the call gives for the others is unspecified, within their own rows).
  *   A page that is negative or >= num_pages hides its tokens, as if they were not
  *       there, and is flagged (KDA_DEV_BAD_PAGE).  Pages wholly before the
  *       window are not read.

@@ -370,7 +370,7 @@ int check_attn(const kda_paged_params* p)
 {
     const int rc = check_paged(p);
     if (rc != KDA_OK) return rc;
-    if (!(std::isfinite(p->scale) && p->scale > 0.0f)) return KDA_ERR_INVALID_ARGUMENT;
+    if (!(p->scale > 0.0f && std::isfinite(p->scale * 1.4426950408889634f))) return KDA_ERR_INVALID_ARGUMENT;  // (the kernels count in powers of two)
     if ((p->causal != 0 && p->causal != 1) || p->window < 0 || (p->window > 0 && !p->causal)) return KDA_ERR_INVALID_ARGUMENT;
     return KDA_OK;
 }

@@ -130,7 +130,7 @@ def test_paged_params(kw, rc):
 
 
 @pytest.mark.parametrize("kw,rc", [
-    (dict(scale=0.0), INVALID), (dict(scale=-1.0), INVALID), (dict(scale=NAN), INVALID), (dict(scale=INF), INVALID), (dict(causal=2), INVALID),
+    (dict(scale=0.0), INVALID), (dict(scale=-1.0), INVALID), (dict(scale=NAN), INVALID), (dict(scale=INF), INVALID), (dict(scale=3e38), INVALID), (dict(causal=2), INVALID),
     (dict(window=-1), INVALID), (dict(window=4, causal=False), INVALID),
 ])
 def test_attn_params(kw, rc):
