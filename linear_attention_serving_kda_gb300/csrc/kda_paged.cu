@@ -2,7 +2,11 @@
 // entry points of the attention over it (kernels: kda_paged_*.cu).
 //
 // The rotation and the append read and write every value once; HBM bandwidth
-// bounds both, and the latency of one pass where rows are few.
+// bounds both, and the latency of one pass where rows are few.  A thread holds
+// one place of a pair (16 bytes of either half) and goes through the heads with
+// it, so that a sine and cosine serve a row's heads.  Measured: rotation of 32768
+// rows of 40 heads of 128, bf16, 99 us, 6.8 TB/s (the copy rate); append of 32768
+// rows of 48 heads 123 us, 6.6 TB/s; 64 rows of single tokens 2.8 and 4.3 us.
 #include <cmath>
 #include <cstring>
 
@@ -144,7 +148,8 @@ template <typename IO, int V> struct Unit {
 
 constexpr int RT = 512;    // most threads of a CTA
 // Heads whose loads a thread has in flight together: more take registers from other CTAs (append of 32768 rows of 48 heads of
-// 128: 146 us with one, 129 with two, 148 with four; rotation of 40 heads: 106 with two, 99 with four).
+// 128: 144 us with one, 130 with two, 136 with three, 149 with four, and of single tokens of 64 sequences 4.2, 4.3, 4.4 and 3.5 us,
+// of 200 4.3, 4.4, 4.5 and 6.2; rotation of 40 heads: 106 with two, 99 with four).
 constexpr int RAHEAD = 4, AAHEAD = 2;
 
 struct RopeArgs {
