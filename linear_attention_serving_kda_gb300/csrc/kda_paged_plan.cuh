@@ -298,7 +298,7 @@ template <typename IO, int D> __global__ void __launch_bounds__(JT) join_kernel(
 #pragma unroll 4
         for (int s = 0; s < n; ++s) {
             const float2 x = held[s][lane];
-            if (x.x == -INFINITY) continue;  // a part that saw nothing, or none
+            if (x.y == 0.f) continue;  // a part that saw nothing, or none (one that met only NaN has no maximum either, but its sum)
             const float f = exp2f(x.x - base);
             l += f * x.y;
 #pragma unroll

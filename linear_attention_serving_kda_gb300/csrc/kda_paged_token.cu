@@ -581,7 +581,8 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
             const bool in = row < rows && !*reinterpret_cast<volatile int*>(&s.dead);
             float top = -INFINITY, sum = 0.f;
             for (int x = 0; x < WARPS; ++x) top = fmaxf(top, s.ml[x][row % ROWS].x);
-            for (int x = 0; x < WARPS; ++x) sum += top == -INFINITY ? 0.f : s.ml[x][row % ROWS].y * exp2_sfu(s.ml[x][row % ROWS].x - top);
+            const float base = top == -INFINITY ? 0.f : top;  // (warps that met only NaN have no maximum, but their sum)
+            for (int x = 0; x < WARPS; ++x) sum += s.ml[x][row % ROWS].y * exp2_sfu(s.ml[x][row % ROWS].x - base);
             const bool whole = w.t0 == 0 && w.t1 == w.n;
             const int slot = w.t0 == 0 ? 1 : 0;
             const size_t head = (size_t)w.s * a.Hq + h * a.G + g0 + row, cell = ((size_t)blockIdx.x * 2 + slot) * ROWS + row;

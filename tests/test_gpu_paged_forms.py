@@ -267,3 +267,35 @@ def test_rope_matches_the_append(cuda_lib):
             assert torch.equal(c.views[0][int(c.table[s, t // 16]), t % 16], y[row, c.Hq:])
             row += 1
     assert np.allclose(P.radians(128)[0], 1.0) and _f(v).size
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("decode", [False, True])
+def test_nan_in_a_query_or_in_many_keys_is_not_lost(cuda_lib, decode, io):
+    # a short sequence is one unit within a stretch, a long one is cut into parts, some of which meet nothing but NaN
+    n = [1, 1, 1] if decode else [30, 5, 20]
+    c = Cache(n, [40, 9000, 60], D=64, page=64, io=io)
+    a = Attn(c, cuda_lib, decode=decode).run()
+    clean, lse = a.out.tensor.clone(), a.lse.tensor.clone()
+    ends = np.cumsum(n)
+    q = a.q.clone()
+    rows = [0, int(ends[0])]  # of the short and of the long sequence
+    for r in rows:
+        a.q[r, 2 * 64:3 * 64] = float("nan")  # head 2
+    a.run()
+    hit = torch.zeros_like(clean, dtype=torch.bool)
+    for r in rows:
+        hit[r, 2] = True
+    hit[c.T:] = False
+    same = ~hit
+    assert torch.isnan(a.out.tensor[hit]).all() and torch.isnan(a.lse.tensor[hit[..., 0]]).all()
+    assert torch.equal(a.out.tensor[same], clean[same]) and torch.equal(a.lse.tensor[same[..., 0]], lse[same[..., 0]])
+    a.q.copy_(q)
+    pg = torch.from_numpy(c.table[1][10:70].astype(np.int64)).cuda()
+    c.views[0][pg, :, 1] = float("nan")  # keys of tokens 640 to 4479, key head 1
+    a.run()
+    hit[:] = False
+    hit[int(ends[0]):int(ends[1]), c.G:2 * c.G] = True
+    same = ~hit
+    assert torch.isnan(a.out.tensor[hit]).all() and torch.isnan(a.lse.tensor[hit[..., 0]]).all()
+    assert torch.equal(a.out.tensor[same], clean[same]) and torch.equal(a.lse.tensor[same[..., 0]], lse[same[..., 0]])
