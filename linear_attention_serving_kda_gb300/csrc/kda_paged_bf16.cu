@@ -11,7 +11,7 @@
 // cores work for the other; with one tile, two steps of it do.
 // The weights are rounded to bf16 (2^-8 of each at most, with either sign: their sum is off by less than the outputs' own rounding).
 // What bounds it: for long chunks of wide heads the products, and the power that they draw.  8192 rows of 32 heads of 128 run
-// at 1590 TFLOP/s without a mask (1515 when called without a pause), at 1440 with one; the library's plain product reaches 1908.  32 heads
+// at 1590 TFLOP/s without a mask (1515 when called without a pause), at 1440 with one; the library's plain product reaches 1908.  16 heads
 // of 256 run at 1140 to 1230: with one tile of rows every key and value is loaded from L2 once a 128 rows.  Heads of 64 do half
 // the products a score and stop at 950, at the way of a row's scores through its thread (not at the exponential unit: polynomials in place of
 // a quarter of them, 846).  A unit costs 10 us besides where prompts are short, mostly waiting for instructions.
