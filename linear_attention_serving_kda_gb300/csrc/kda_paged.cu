@@ -5,8 +5,8 @@
 // bounds both, and the latency of one pass where rows are few.  A thread holds
 // one place of a pair (16 bytes of either half) and goes through the heads with
 // it, so that a sine and cosine serve a row's heads.  Measured: rotation of 32768
-// rows of 40 heads of 128, bf16, 99 us, 6.8 TB/s (the copy rate); append of 32768
-// rows of 48 heads 123 us, 6.6 TB/s; 64 rows of single tokens 2.8 and 4.3 us.
+// rows of 40 heads of 128, bf16, 98 us, 6.8 TB/s (the copy rate); append of 32768
+// rows of 48 heads 120 us, 6.7 TB/s; 64 rows of single tokens 2.9 and 4.3 us.
 #include <cmath>
 #include <cstring>
 
@@ -317,15 +317,17 @@ int piece_of(int rd, int io_bf16)
     return rd % 8 == 0 ? 4 : 1;
 }
 
-// Threads for each row and unit (`groups`), rows of a CTA and its threads: a head a thread until the GPU is
-// full, then up to MAXPER heads, which share their angles.
+// Threads for each row and unit (`groups`), rows of a CTA and its threads: a head a thread until half of the GPU's threads
+// are taken, then up to eight heads, which share their angles (2000 rows of 40 heads of 128: 10.4 us where all threads were to be taken first,
+// 8.5 so; a quarter: 7.9, but 7001 rows of 12 fp32 heads of 64 9.0 in place of 7.7).  CTAs of 128 threads or a row: 8192 fp32 rows of 16 heads
+// of 128 23.1 us with 256, 19.3 with 128, 19.3 with 64, append of 32768 rows 129, 127 and 138.
 void split_rows(long long rows, int heads, int units, int max_rows, int& groups, int& rows_per_cta, int& threads)
 {
     const long long all = rows * heads * units;
-    int per = (int)std::min<long long>(8, std::max<long long>(1, all / (152 * 2048)));
+    int per = (int)std::min<long long>(8, std::max<long long>(1, all / (152 * 1024)));
     while ((long long)((heads + per - 1) / per) * units > RT && per < heads) ++per;
     groups = (heads + per - 1) / per;
-    rows_per_cta = std::min(std::max(1, 256 / (groups * units)), max_rows);
+    rows_per_cta = std::min(std::max(1, 128 / (groups * units)), max_rows);
     threads = std::min(RT, (rows_per_cta * groups * units + 31) / 32 * 32);
 }
 
