@@ -46,7 +46,9 @@ template <int D, int R> __global__ void __launch_bounds__(FT, D == 256 ? 1 : 2) 
         if (!it.act) continue;
         const int h = it.head, first = it.lo + it.t0 * KEYS, last = min(it.hi, it.lo + it.t1 * KEYS);
         __syncthreads();
-        for (int i = tid; i < R * (D / 4); i += FT) {
+        // A piece without tokens loads no rows: nothing would wait for them before the next piece's rows go to the same place,
+        // and of two asynchronous copies to one place either may land last.
+        for (int i = tid; first < last && i < R * (D / 4); i += FT) {
             const int r = i / (D / 4), e = i % (D / 4), f = it.row0 + r;
             const bool in = r < it.rows;
             const int tok = group_of(a, f);

@@ -299,3 +299,16 @@ def test_nan_in_a_query_or_in_many_keys_is_not_lost(cuda_lib, decode, io):
     same = ~hit
     assert torch.isnan(a.out.tensor[hit]).all() and torch.isnan(a.lse.tensor[hit[..., 0]]).all()
     assert torch.equal(a.out.tensor[same], clean[same]) and torch.equal(a.lse.tensor[same[..., 0]], lse[same[..., 0]])
+
+
+@pytest.mark.parametrize("D", [64, 256])
+def test_rows_without_tokens_between_rows_with_some(cuda_lib, D):
+    """Far more units than CTAs, so that each takes rows that see nothing and rows that see something in turn: sequences
+    without tokens, and with more rows than tokens, among ordinary ones."""
+    r = np.random.default_rng(D)
+    lens = [int(r.integers(1, 4)) for _ in range(2400)]
+    kv = [0 if i % 2 else int(n + r.integers(0, 30)) for i, n in enumerate(lens)]
+    lens += [200, 5] * 6
+    kv += [9, 40] * 6
+    for io in ("f32", "bf16"):
+        Attn(Cache(lens, kv, Hkv=1, G=3, D=D, io=io, seed=D), cuda_lib).run().check()
