@@ -647,6 +647,8 @@ KDA_API int kda_paged_append_decode(const kda_paged_params* p, int32_t B, const 
  *   Whatever lies in the cache's places past a sequence's tokens has no
  *       effect.  A NaN or an infinity in a query or key reaches rows that
  *       see it, in a value also rows of the same chunk that do not.
+ *   A wait that gives up (KDA_DEV_TIMEOUT): rows that its CTA had not finished keep
+ *       what out held (lse: that, or their own), also those that it had a part in.
  *   workspace: kda_paged_attn_workspace_bytes(p, N, T) (decode: kda_paged_attn_
  *       decode_workspace_bytes(p, B)) bytes, contents need no init.  Calls that
  *       may run at the same time take a workspace each.
@@ -661,6 +663,21 @@ KDA_API int kda_paged_attn_decode(const kda_paged_params* p, int32_t B, const in
                                   const void* q, const void* k_cache, const void* v_cache, void* out, float* lse,
                                   void* workspace, size_t ws_bytes, int32_t* dev_status, cudaStream_t stream);
 KDA_API size_t kda_paged_attn_decode_workspace_bytes(const kda_paged_params* p, int32_t B);
+
+/*
+ * Test hook for the bounded on-chip waits of the two calls above (cu_seqlens
+ * NULL: of the single tokens, T = N).  Waits give up after poll_limit polls, those
+ * that last a whole unit after unit_poll_limit (both > 0), and CTA stalled_cta
+ * (none below 0 or past the grid) loads no keys and values, so that those who
+ * wait for them run out: KDA_DEV_TIMEOUT is set, nothing is in flight, rows
+ * that this CTA had a part in keep what they held, the others are computed.
+ * (fp32 chunks have no such waits.)
+ */
+KDA_API int kda_debug_paged_attn_stalled(const kda_paged_params* p, const int32_t* cu_seqlens, int32_t N, int32_t T,
+                                         const int32_t* kv_lens, const int32_t* pages, const void* q,
+                                         const void* k_cache, const void* v_cache, void* out, float* lse,
+                                         void* workspace, size_t ws_bytes, int32_t* dev_status, uint32_t poll_limit,
+                                         uint32_t unit_poll_limit, int32_t stalled_cta, cudaStream_t stream);
 
 /* Human-readable name of a return code. */
 KDA_API const char* kda_status_string(int status);

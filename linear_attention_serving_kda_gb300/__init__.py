@@ -20,6 +20,7 @@ from .kda import (  # noqa: F401
     kda_gdn_prefill_varlen, kda_gdn_prefill_workspace_bytes, kda_slots_compact_plan, kda_slots_copy,
     kda_slots_zero,
     # softmax attention over a paged cache, and what stands in front of it
+    kda_debug_paged_attn_stalled,
     KDA_DEV_BAD_PAGE, KDA_DEV_TIMEOUT, KDA_ROPE_HALF, KDA_ROPE_MAX_DIM, KDA_ROPE_PAIRS, KDA_ROPE_SCALE_BASE, KDA_ROPE_SCALE_LINEAR,
     KDA_ROPE_SCALE_NONE, KDA_ROPE_SCALE_RAMP, KDA_ROPE_SCALE_SMOOTH, PagedParams, RopeParams, RopeScaling,
     kda_paged_append_decode, kda_paged_append_varlen, kda_paged_attn_decode, kda_paged_attn_decode_workspace_bytes,

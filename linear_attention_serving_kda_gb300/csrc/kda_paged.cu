@@ -501,7 +501,7 @@ size_t attn_workspace(const kda_paged_params* p, int32_t N, int32_t T, bool toke
 
 int attend(const kda_paged_params* p, const int32_t* cu_seqlens, int32_t N, int32_t T, const int32_t* kv_lens, const int32_t* pages,
            const void* q, const void* k_cache, const void* v_cache, void* out, float* lse, void* workspace, size_t ws_bytes,
-           int32_t* dev_status, bool token, cudaStream_t stream)
+           int32_t* dev_status, bool token, cudaStream_t stream, uint32_t polls = PAGED_POLLS, uint32_t unit_polls = PAGED_POLLS, int stalled = -1)
 {
     int rc;
     if ((rc = check_ptrs({kv_lens, pages, q, k_cache, v_cache, out})) != KDA_OK || (rc = check_opt(lse)) != KDA_OK) return rc;
@@ -531,6 +531,9 @@ int attend(const kda_paged_params* p, const int32_t* cu_seqlens, int32_t N, int3
     a.lse = lse;
     a.workspace = workspace;
     a.dev_status = dev_status;
+    a.polls = polls;
+    a.unit_polls = unit_polls;
+    a.stalled = stalled;
     const cudaError_t e = token && paged_token_wanted(a, io == 4) ? launch_paged_token(a, io == 4, stream)
                           : io == 4                               ? launch_paged_f32(a, stream)
                                                                   : launch_paged_bf16(a, stream);
@@ -687,6 +690,21 @@ KDA_API int kda_paged_attn_decode(const kda_paged_params* p, int32_t B, const in
     if (!good_counts(p, B, B)) return KDA_ERR_INVALID_ARGUMENT;
     if (B == 0) return KDA_OK;
     return attend(p, nullptr, B, B, kv_lens, pages, q, k_cache, v_cache, out, lse, workspace, ws_bytes, dev_status, true, stream);
+}
+
+KDA_API int kda_debug_paged_attn_stalled(const kda_paged_params* p, const int32_t* cu_seqlens, int32_t N, int32_t T, const int32_t* kv_lens,
+                                         const int32_t* pages, const void* q, const void* k_cache, const void* v_cache, void* out, float* lse,
+                                         void* workspace, size_t ws_bytes, int32_t* dev_status, uint32_t poll_limit, uint32_t unit_poll_limit,
+                                         int32_t stalled_cta, cudaStream_t stream)
+{
+    int rc = check_attn(p);
+    if (rc != KDA_OK) return rc;
+    const bool token = cu_seqlens == nullptr;
+    if (!good_counts(p, N, T) || (token && N != T) || poll_limit == 0 || unit_poll_limit == 0) return KDA_ERR_INVALID_ARGUMENT;
+    if (N == 0 || T == 0) return KDA_OK;
+    if (!token && (rc = check_ptrs({cu_seqlens})) != KDA_OK) return rc;
+    return attend(p, cu_seqlens, N, T, kv_lens, pages, q, k_cache, v_cache, out, lse, workspace, ws_bytes, dev_status, token, stream, poll_limit,
+                  unit_poll_limit, stalled_cta);
 }
 
 }  // extern "C"

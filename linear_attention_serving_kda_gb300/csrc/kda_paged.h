@@ -26,7 +26,13 @@ struct PagedArgs {
     float* lse;
     void* workspace;
     int32_t* dev_status;
+    uint32_t polls, unit_polls;  // after which a wait gives up: for a tile, for a whole unit
+    int stalled;                 // the CTA that loads nothing, -1: none (kda_debug_paged_attn_stalled)
 };
+
+constexpr uint32_t PAGED_POLLS = 1u << 22;
+// Sum of the weights of a part, or of a warp's share of one, whose waits gave up: there is no other value below zero.  The joins leave its rows out.
+constexpr float PART_LOST = -1.f;
 
 // n / G for 0 <= n < 2^31, as n M / 2^(31 + s) with 2^(s - 1) < G <= 2^s and M = floor(2^(31 + s) / G) + 1: M G is above
 // 2^(31 + s) by at most G <= 2^s, which makes less than n 2^s / (G 2^(31 + s)) < 1 / G of difference, too little to reach the next quotient.

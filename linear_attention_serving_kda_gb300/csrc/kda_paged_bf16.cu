@@ -26,7 +26,6 @@ using namespace paged;
 
 constexpr int THREADS = 384;  // two softmax warpgroups, a warp that issues products, one that loads keys and values, two that load rows and store outputs
 constexpr int CTAS = 152;  // one an SM
-constexpr uint32_t WAIT = 1u << 20;
 constexpr float LAG = 8.f;
 
 template <int DP> struct Shape {
@@ -46,6 +45,7 @@ template <int DP> struct Shape {
         unsigned char ring[SLOTS * SLOT];
         uint64_t full[SLOTS], empty[SLOTS], scores[2], weights[2], product[2], rows[2], free[2], taken[2], ready[2], drained;
         uint32_t hidden[8], tmem;
+        int dead;  // a wait ran out
         Start start;
     };
 };
@@ -177,6 +177,7 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
             ptx::mbar_init(&s.taken[i], 4);
             ptx::mbar_init(&s.ready[i], 4);
         }
+        s.dead = 0;
         ptx::mbar_init(&s.drained, 1);
         ptx::fence_mbar_init();
         ptx::fence_proxy_async_smem();
@@ -194,8 +195,12 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
     ptx::grid_dependency_wait();
     find_start<THREADS / 32>(a, p, s.start);
     if (tid == 0) p.cut[blockIdx.x].rows = 0;
-    // A wait that runs out ends its role's work (and with it, one by one, the others').
-    const auto wait = [&](uint64_t* bar, uint32_t parity) { return ptx::mbar_wait(bar, parity & 1, WAIT); };
+    // A wait that runs out ends its role's work (and with it, one by one, the others').  What the CTA has not written by then stays unwritten, by
+    // the storing warps and by the join (PART_LOST): softmax warps that go on without waits arrive early at barriers that others of their tile share, so that nothing
+    // behind those is sure.  They set `dead` before such an arrival; it is looked at after it.
+    const auto wait = [&](uint64_t* bar, uint32_t parity) { return ptx::mbar_wait(bar, parity & 1, a.polls); };
+    const auto wait_unit = [&](uint64_t* bar, uint32_t parity) { return ptx::mbar_wait(bar, parity & 1, a.unit_polls); };
+    const auto dead = [&] { return *reinterpret_cast<volatile int*>(&s.dead) != 0; };
     constexpr uint32_t O0 = 256;  // S: columns 0 .. 2 KEYS - 1, O behind
 
     if (warp >= 8) {
@@ -203,7 +208,7 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
         if (warp == 9) {
             // ---- loads: keys and values in the order in which the products meet them
             uint32_t use = 0, kt = 0;
-            bool ok = true;
+            bool ok = (int)blockIdx.x != a.stalled;
             const int box = min(KEYS, 1 << a.page_shift), boxes = KEYS / box;
             Work w;
             for (w.start(p, s.start); ok && w.step(a, p);) {
@@ -245,9 +250,8 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
                         if (lane == 0) ptx::mbar_arrive(&s.full[use % SLOTS]);
                     }
             }
-            // a CTA that gave up: what is on its way has to land first
-            if (!ok)
-                for (uint32_t u = use > SLOTS ? use - SLOTS : 0; u < use; ++u) ptx::mbar_wait(&s.full[u % SLOTS], (u / SLOTS) & 1, WAIT);
+            // what is on its way has to land first (it has, unless those who wait for it gave up)
+            for (uint32_t u = use > SLOTS ? use - SLOTS : 0; u < use; ++u) ptx::mbar_wait(&s.full[u % SLOTS], (u / SLOTS) & 1, PAGED_POLLS);
         } else if (warp >= 10) {
             // ---- rows: a tensor copy, or (tiles that cut tokens) half of each tile by either warp, 16-byte pieces permuted within
             // eight rows as the descriptor expects; and the outputs of the unit before from the ring's slots, the first slot by one warp,
@@ -268,7 +272,8 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
                 out.any = false;
                 constexpr int COLS = L::COLS, PC = COLS / 8, ROWS_AT_ONCE = 32 / PC;
                 const int t = L::OUT == 1 ? me : 0, col = L::OUT == 1 ? 0 : me * COLS, c8 = lane % PC;
-                if (!(ok = wait(&s.ready[me], stored++))) return;
+                ok = wait_unit(&s.ready[me], stored++);
+                if (!(ok = !__any_sync(0xffffffffu, !ok || dead()))) return;
                 const unsigned char* slot = s.ring + out.use % SLOTS * SLOT;
                 const int last = min(128, out.rows - t * 128);
                 if (last == 128 && whole_tokens(a.G)) {
@@ -307,7 +312,7 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
 #pragma unroll
                 for (int t = 0; t < L::TILES; ++t) {
                     if (t >= w.tiles || (whole_tokens(a.G) && me == 1)) break;
-                    if (!(ok = wait(&s.free[t], count[t] + 1))) break;  // the scores of the unit before are done
+                    if (!(ok = wait_unit(&s.free[t], count[t] + 1))) break;  // the scores of the unit before are done
                     ++count[t];
                     unsigned char* base = s.q + t * (128 * DP * 2);
                     if (whole_tokens(a.G)) {
@@ -354,10 +359,10 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
             }
             store();
             ptx::bulk_wait_all();
-            // what is on its way has to land first
-            if (!ok && whole_tokens(a.G) && me == 0)
+            // what is on its way has to land first (as above)
+            if (whole_tokens(a.G) && me == 0)
                 for (int t = 0; t < L::TILES; ++t)
-                    if (count[t]) ptx::mbar_wait(&s.rows[t], (count[t] - 1) & 1, WAIT);
+                    if (count[t]) ptx::mbar_wait(&s.rows[t], (count[t] - 1) & 1, PAGED_POLLS);
         } else if (warp == 8) {
             // ---- products
             const bool leader = ptx::elect_one();
@@ -509,11 +514,11 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
             // nothing may be on its way when TMEM is freed
             if (leader) ptx::mma_commit(&s.drained);
             __syncwarp();
-            ptx::mbar_wait(&s.drained, 0, WAIT);
+            ptx::mbar_wait(&s.drained, 0, PAGED_POLLS);
         }
     } else {
         // ---- a thread a row: exponentials, rescaling, outputs.  (After a wait that ran out a warp goes on without waits
-        // and stores, so that it still meets the others at the named barriers.)
+        // and outputs, so that it still meets the others at the barriers.)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         const int t = warp >> 2, r = tid & 127;  // tile, row of it
         const uint32_t tl = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes
@@ -612,7 +617,10 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
                     }
                     ptx::tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(&s.weights[b]);
+                    if (lane == 0) {
+                        if (!ok) *reinterpret_cast<volatile int*>(&s.dead) = 1;
+                        ptx::mbar_arrive(&s.weights[b]);
+                    }
                 }
             }
             kt += w.count;
@@ -620,9 +628,9 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
                 if (w.count > 0) {
                     const int last = w.steps - 1, b = w.tiles == 2 ? t : last & 1;
                     ok = ok && wait(&s.product[b], w.tiles == 2 ? pcount[b] : pcount[b] + last / 2);
+                    if (!ok) *reinterpret_cast<volatile int*>(&s.dead) = 1;
                     ptx::tc_fence_after();
                 }
-                const bool has = row < w.rows && ok;
                 const float inv = sum == 0.f ? 0.f : 1.f / sum;
                 const size_t cell = (size_t)blockIdx.x * 2 + (w.t0 == 0);
                 if (w.staged) {
@@ -633,6 +641,7 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
                     for (int i = 0; i < L::OUT; ++i, ++use) {
                         unsigned char* slot = s.ring + use % SLOTS * SLOT;
                         ok = ok && wait(&s.full[use % SLOTS], use / SLOTS);
+                        if (!ok) *reinterpret_cast<volatile int*>(&s.dead) = 1;
                         if (live && ok) {
 #pragma unroll 1
                             for (int e = 0; e < COLS; e += 32) {
@@ -652,7 +661,7 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
                         __syncwarp();
                         if (lane == 0) {
                             if (i == L::OUT - 1) ptx::mbar_arrive(&s.taken[t]);  // O may be overwritten
-                            if (ok) ptx::mbar_arrive(&s.ready[L::OUT == 1 ? t : i]);
+                            ptx::mbar_arrive(&s.ready[L::OUT == 1 ? t : i]);
                         }
                     }
                     use += (w.tiles - 1 - t) * L::OUT;
@@ -667,7 +676,7 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
 #pragma unroll
                                 for (int i = 0; i < 32; ++i) o[i] = 0.f;
                             }
-                            if (!has) continue;
+                            if (row >= w.rows || !ok) continue;
                             if (w.count > 0) {
 #pragma unroll
                                 for (int i = 0; i < 8; ++i)
@@ -686,14 +695,15 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
                         use += 2 * w.count;
                     }
                 }
-                if (live && has) {
-                    if (!w.whole()) p.ml[cell * p.part_rows + row] = make_float2(m, sum);
-                    else if (a.lse) a.lse[(size_t)(w.begin + tok) * a.Hq + head] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994531f;
+                ok = !__any_sync(0xffffffffu, !ok || dead());
+                if (live && row < w.rows) {
+                    if (!w.whole()) p.ml[cell * p.part_rows + row] = make_float2(m, ok ? sum : PART_LOST);
+                    else if (a.lse && ok) a.lse[(size_t)(w.begin + tok) * a.Hq + head] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994531f;
                 }
             } else {
                 use += 2 * w.count + (w.staged ? w.tiles * L::OUT : 0);
             }
-            if (tid == 0 && ok && w.t0 == 0 && !w.whole())
+            if (tid == 0 && w.t0 == 0 && !w.whole())
                 p.cut[blockIdx.x] = {s.start.line, w.begin, w.row0, w.rows, w.head, owner(s.start.line, w.end(p) - 1, p.ctas)};
             for (int b = 0; b < 2; ++b) {
                 scount[b] = sbase[b] += w.tiles == 2 ? w.count : (w.count + 1 - b) / 2;

@@ -280,6 +280,7 @@ template <typename IO, int D> __global__ void __launch_bounds__(JT) join_kernel(
     const bool in = r < cut.rows;
     constexpr int GROUPS = D / 4, EACH = GROUPS < 8 ? 1 : GROUPS / 8;
     float m = -INFINITY, l = 0.f;
+    bool lost = false;
     float4 y[EACH];
 #pragma unroll
     for (int i = 0; i < EACH; ++i) y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -298,6 +299,7 @@ template <typename IO, int D> __global__ void __launch_bounds__(JT) join_kernel(
 #pragma unroll 4
         for (int s = 0; s < n; ++s) {
             const float2 x = held[s][lane];
+            lost |= x.y < 0.f;
             if (x.y == 0.f) continue;  // a part that saw nothing, or none (one that met only NaN has no maximum either, but its sum)
             const float f = exp2f(x.x - base);
             l += f * x.y;
@@ -319,9 +321,11 @@ template <typename IO, int D> __global__ void __launch_bounds__(JT) join_kernel(
         const int f = cut.row0 + blockIdx.y * 32 + rr, tok = group_of(a, f);
         return (size_t)(cut.begin + tok) * a.Hq + cut.head * a.G + f - tok * a.G;
     };
-    if (a.lse && warp == 0 && in) a.lse[row_of(lane)] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+    const uint32_t kept = __ballot_sync(0xffffffffu, in && !lost);
+    if (a.lse && warp == 0 && ((kept >> lane) & 1)) a.lse[row_of(lane)] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
     __syncthreads();
-    for (int rr = warp; rr < 32 && blockIdx.y * 32 + rr < cut.rows; rr += JT / 32) {
+    for (int rr = warp; rr < 32; rr += JT / 32) {
+        if (!((kept >> rr) & 1)) continue;
         IO* out = static_cast<IO*>(a.out) + row_of(rr) * D;
         for (int i = lane; i < GROUPS; i += 32) {
             const float4 z = turned[rr][i];

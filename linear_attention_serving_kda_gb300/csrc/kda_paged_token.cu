@@ -21,7 +21,6 @@ namespace {
 
 constexpr int CTAS = 152;     // one an SM
 constexpr int KNOWN = 512;    // sequences whose lengths a CTA keeps
-constexpr uint32_t WAIT = 1u << 22;
 constexpr float LAG = 8.f;
 
 // What the stretches leave for token_join_kernel.
@@ -269,7 +268,7 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
     if (per == 1 && tid < a.N && tid >= s.first && tid - s.first < KNOWN) s.kv[tid - s.first] = known;  // a sequence a thread: it is at hand
     __syncthreads();
     const auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (ptx::mbar_wait(bar, parity & 1, WAIT) && !*reinterpret_cast<volatile int*>(&s.dead)) return true;
+        if (ptx::mbar_wait(bar, parity & 1, a.polls) && !*reinterpret_cast<volatile int*>(&s.dead)) return true;
         *reinterpret_cast<volatile int*>(&s.dead) = 1;
         return false;
     };
@@ -278,6 +277,7 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
     bool ok = true;
     if (warp == WARPS) {
         // ---- loads
+        ok = (int)blockIdx.x != a.stalled;
         const uint64_t once = ptx::policy_evict_first();
         const int box = min(KEYS, 1 << a.page_shift), boxes = KEYS / box;
         uint32_t use = 0, unit = 0;
@@ -310,17 +310,17 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
                                 tok & ((1 << a.page_shift) - 1), 0, h, gone ? -1 : page, &s.full[stage], once);
             }
         }
-        if (!ok) {  // what is on its way has to land first
-            for (uint32_t u = use > STAGES ? use - STAGES : 0; u < use; ++u) ptx::mbar_wait(&s.full[u % STAGES], (u / STAGES) & 1, WAIT);
-            for (uint32_t u = unit > 1 ? unit - 1 : 0; u <= unit; ++u) ptx::mbar_wait(&s.qfull[u & 1], (u >> 1) & 1, 1u << 12);
-        }
+        // what is on its way has to land first (it has, unless those who wait for it gave up)
+        for (uint32_t u = use > STAGES ? use - STAGES : 0; u < use; ++u) ptx::mbar_wait(&s.full[u % STAGES], (u / STAGES) & 1, PAGED_POLLS);
+        for (uint32_t u = unit > 2 ? unit - 2 : 0; u < unit; ++u) ptx::mbar_wait(&s.qfull[u & 1], (u >> 1) & 1, PAGED_POLLS);
     } else {
         const int team = warp / TEAM, k16 = warp % TEAM * 16;  // this warp's tokens of a tile
         const float c = a.scale * 1.4426950408889634f;
         uint32_t use = 0, unit = 0;
         const uint32_t ring = ptx::smem_u32(s.ring);
         if (tid == 0) work.cut[blockIdx.x].seq = -1;
-        // (a wait that ran out: the warps go on without waiting and without tiles, so that they still meet at the barriers)
+        // (a wait that ran out: the warps go on without waiting and without tiles, so that they still meet at the barriers; a unit that a warp gave up on
+        // is written nowhere, PART_LOST in its place)
         for (; w.left > 0; next_unit<KEYS>(a, s, w, units), ++unit) {
             const int h = w.u / blocks, g0 = w.u % blocks * ROWS, rows = min(ROWS, a.G - g0);
             ok = ok && wait(&s.qfull[unit & 1], unit >> 1);
@@ -542,7 +542,7 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
 #pragma unroll
                 for (int g = 0; g < 8; ++g) {
                     lf[g] = warp_sum(lf[g]);
-                    if (lane == 0) s.ml[warp][g] = make_float2(mf[g], lf[g]);
+                    if (lane == 0) s.ml[warp][g] = make_float2(mf[g], ok ? lf[g] : PART_LOST);
                 }
             } else {
 #pragma unroll
@@ -551,7 +551,7 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
                 for (int e = 0; e < 2; ++e) {
 #pragma unroll
                     for (int d = 4; d < 32; d <<= 1) l[b][e] += __shfl_xor_sync(0xffffffffu, l[b][e], d);
-                    if (lane < 4) s.ml[warp][b * 8 + lane * 2 + e] = make_float2(m[b][e], l[b][e]);
+                    if (lane < 4) s.ml[warp][b * 8 + lane * 2 + e] = make_float2(m[b][e], ok ? l[b][e] : PART_LOST);
                 }
             }
             __syncwarp();
@@ -578,9 +578,13 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
             // two of CH channels of a row at a time, by a thread each
             constexpr int CH = L::CH;
             const int row = tid / (CH / 2), ch = tid % (CH / 2) * 2;  // (threads past the last row have none)
-            const bool in = row < rows && !*reinterpret_cast<volatile int*>(&s.dead);
             float top = -INFINITY, sum = 0.f;
-            for (int x = 0; x < WARPS; ++x) top = fmaxf(top, s.ml[x][row % ROWS].x);
+            bool lost = false;
+            for (int x = 0; x < WARPS; ++x) {
+                top = fmaxf(top, s.ml[x][row % ROWS].x);
+                lost |= s.ml[x][row % ROWS].y < 0.f;
+            }
+            const bool in = row < rows && !lost;
             const float base = top == -INFINITY ? 0.f : top;  // (warps that met only NaN have no maximum, but their sum)
             for (int x = 0; x < WARPS; ++x) sum += s.ml[x][row % ROWS].y * exp2_sfu(s.ml[x][row % ROWS].x - base);
             const bool whole = w.t0 == 0 && w.t1 == w.n;
@@ -620,9 +624,9 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
                 }
                 asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory");
             }
-            if (in && ch == 0) {
-                if (!whole) work.ml[cell] = make_float2(top, sum);
-                else if (a.lse) a.lse[head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+            if (row < rows && ch == 0) {
+                if (!whole) work.ml[cell] = make_float2(top, lost ? PART_LOST : sum);
+                else if (a.lse && in) a.lse[head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
             }
             if (w.t0 == 0 && !whole && tid == 0) {
                 const long long last = x1 - 1 + (w.n - w.t1);  // the unit's last tile in the line
@@ -635,14 +639,18 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
 }
 
 // A warp joins the parts of one row: part s has its maximum and sum at ml(s) and its D values at o(s), both
-// null for a part without any.  Returns the sum and the maximum, and in y the lane's D / 32 neighbouring values, not divided.
+// null for a part without any.  Returns the maximum and the sum (PART_LOST where a part is), and in y the lane's D / 32 neighbouring values, not divided.
 template <int D, class ML, class O> __device__ __forceinline__ float2 join_row(int parts, ML&& ml, O&& o, float (&y)[D / 32])
 {
     constexpr int PER = D / 32;
     const int lane = threadIdx.x & 31;
     float m = -INFINITY, l = 0.f;
+    bool lost = false;
     for (int s = lane; s < parts; s += 32)
-        if (const float2* x = ml(s)) m = fmaxf(m, x->x);
+        if (const float2* x = ml(s)) {
+            m = fmaxf(m, x->x);
+            lost |= x->y < 0.f;
+        }
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
     const float base = m == -INFINITY ? 0.f : m;
@@ -676,13 +684,15 @@ template <int D, class ML, class O> __device__ __forceinline__ float2 join_row(i
             }
         }
     }
-    return make_float2(m, warp_sum(l));
+    l = warp_sum(l);
+    return make_float2(m, __any_sync(0xffffffffu, lost) ? PART_LOST : l);
 }
 // The joined row to out and lse (row: of [T][Hq]).
 template <typename IO, int D> __device__ __forceinline__ void write_row(const PagedArgs& a, size_t row, float2 ml, const float (&y)[D / 32])
 {
     constexpr int PER = D / 32;
     const int lane = threadIdx.x & 31;
+    if (ml.y < 0.f) return;
     const float inv = ml.y == 0.f ? 0.f : 1.f / ml.y;
     IO* out = static_cast<IO*>(a.out) + row * D + lane * PER;
 #pragma unroll

@@ -168,6 +168,8 @@ _SIG = {
     "kda_paged_attn_decode": (ctypes.c_int, [ctypes.POINTER(kda_paged_params), _I32] + [_VP] * 8 +
                               [ctypes.c_size_t, _VP, _VP]),
     "kda_paged_attn_decode_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(kda_paged_params), _I32]),
+    "kda_debug_paged_attn_stalled": (ctypes.c_int, [ctypes.POINTER(kda_paged_params), _VP, _I32, _I32] + [_VP] * 8 +
+                                     [ctypes.c_size_t, _VP, ctypes.c_uint32, ctypes.c_uint32, _I32, _VP]),
     "kda_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "kda_abi_version": (ctypes.c_int, []),
 }
@@ -613,6 +615,17 @@ def kda_paged_attn_decode(params: PagedParams, B: int, kv_lens, pages, q, k_cach
     return load().kda_paged_attn_decode(
         ctypes.byref(params.c_struct()), B, _ptr(kv_lens), _ptr(pages), _ptr(q), _ptr(k_cache), _ptr(v_cache),
         _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes, _ptr(dev_status), _stream(stream))
+
+
+def kda_debug_paged_attn_stalled(params: PagedParams, cu_seqlens, N: int, T: int, kv_lens, pages, q, k_cache, v_cache, out,
+                                 lse, workspace, ws_bytes: int, dev_status, poll_limit: int, unit_poll_limit: int,
+                                 stalled_cta: int, stream=None) -> int:
+    """Test hook: the attention (cu_seqlens None: of single tokens) with short waits, which run out in the CTA that loads
+    nothing (KDA_DEV_TIMEOUT)."""
+    return load().kda_debug_paged_attn_stalled(
+        ctypes.byref(params.c_struct()), _ptr(cu_seqlens), N, T, _ptr(kv_lens), _ptr(pages), _ptr(q), _ptr(k_cache),
+        _ptr(v_cache), _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes, _ptr(dev_status), poll_limit, unit_poll_limit,
+        stalled_cta, _stream(stream))
 
 
 class Prepared:

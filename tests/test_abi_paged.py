@@ -186,6 +186,16 @@ def test_attn_pointers():
     assert _attn(p, cu=None) == INVALID and _attn(p, T=-1) == INVALID and _attn(p, T=0) == OK
 
 
+def test_stalled_refusals():
+    def call(cu=addr(1), N=2, T=6, polls=1, unit=1, **kw):
+        return kda.kda_debug_paged_attn_stalled(_params(**kw), cu, N, T, addr(2), addr(3), addr(4), addr(8), addr(10), addr(11), addr(12), None, 0, None,
+                                                polls, unit, 0, 0)
+
+    assert call(polls=0) == INVALID and call(unit=0) == INVALID and call(cu=None) == INVALID and call(scale=0.0) == INVALID
+    assert call(head_dim=96) == GEOMETRY and call(N=-1) == INVALID and call(T=0) == OK
+    assert call() == kda.KDA_ERR_WORKSPACE and call(cu=None, T=2) == kda.KDA_ERR_WORKSPACE
+
+
 def test_workspaces():
     p = _params()
     assert kda.kda_paged_attn_workspace_bytes(p, -1, 6) == 0 and kda.kda_paged_attn_workspace_bytes(p, 2, 0) == 0

@@ -312,3 +312,34 @@ def test_rows_without_tokens_between_rows_with_some(cuda_lib, D):
     kv += [9, 40] * 6
     for io in ("f32", "bf16"):
         Attn(Cache(lens, kv, Hkv=1, G=3, D=D, io=io, seed=D), cuda_lib).run().check()
+
+
+@pytest.mark.parametrize("decode,io,D,G", [(False, "bf16", 64, 4), (False, "bf16", 128, 4), (False, "bf16", 128, 3), (False, "bf16", 256, 2),
+                                           (True, "bf16", 128, 4), (True, "bf16", 256, 12), (True, "f32", 64, 3)])
+def test_waits_that_run_out(cuda_lib, decode, io, D, G):
+    """A CTA that loads nothing (made by the host: those who wait for its tiles give up after 2^16 polls): the status says so, a row of which any part
+    is missing keeps what it held, every other one has its bits; and the next call is as ever."""
+    kda = cuda_lib
+    lens = [1] * 5 if decode else [300, 40, 500, 7, 1]
+    c = Cache(lens, [6000, 100, 2500, 7, 20000], Hkv=2, G=G, D=D, page=64, io=io)
+    a = Attn(c, kda, decode=decode).run()
+    want, lse = a.out.tensor.clone(), a.lse.tensor.clone()
+    kept_rows = 0
+    for cta in (0, 70, 151):
+        a.out.tensor.fill_(7.0)
+        a.lse.tensor.fill_(7.0)
+        a.ws.tensor.fill_(0xFF)
+        kda.check(kda.kda_debug_paged_attn_stalled(a.p, None if decode else c.cu, c.N, a.rows, c.kv_lens, c.pages, a.q, *[g.tensor for g in c.pools],
+                                                   a.out.tensor, a.lse.tensor, a.ws.tensor, a.need, c.status, 1 << 16, 1 << 16, cta))
+        torch.cuda.synchronize()
+        assert int(c.status.item()) == kda.KDA_DEV_TIMEOUT
+        c.status.zero_()
+        same, kept = (a.out.tensor == want).all(-1), (a.out.tensor == 7.0).all(-1)
+        assert (same | kept)[:c.T].all() and kept[:c.T].any() and same[:c.T].any() and kept[c.T:].all()
+        assert torch.equal(a.lse.tensor, torch.where(kept, 7.0, lse))
+        kept_rows += int(kept[:c.T].sum())
+        a.run()
+        assert torch.equal(a.out.tensor, want) and torch.equal(a.lse.tensor, lse) and int(c.status.item()) == 0
+    assert kept_rows < 2 * c.T * c.Hq  # a CTA has a part in a few units only
+    for g in (a.out, a.lse, a.ws, *c.pools):
+        assert g.intact()
