@@ -648,7 +648,8 @@ KDA_API int kda_paged_append_decode(const kda_paged_params* p, int32_t B, const 
  *       effect.  A NaN or an infinity in a query or key reaches rows that
  *       see it, in a value also rows of the same chunk that do not.
  *   A wait that gives up (KDA_DEV_TIMEOUT): rows that its CTA had not finished keep
- *       what out held (lse: that, or their own), also those that it had a part in.
+ *       what out held (heads of 256: a half of them may), lse that or their own; so
+ *       do those that it had a part in.
  *   workspace: kda_paged_attn_workspace_bytes(p, N, T) (decode: kda_paged_attn_
  *       decode_workspace_bytes(p, B)) bytes, contents need no init.  Calls that
  *       may run at the same time take a workspace each.

@@ -200,6 +200,9 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
     // behind those is sure.  They set `dead` before such an arrival; it is looked at after it.
     const auto wait = [&](uint64_t* bar, uint32_t parity) { return ptx::mbar_wait(bar, parity & 1, a.polls); };
     const auto wait_unit = [&](uint64_t* bar, uint32_t parity) { return ptx::mbar_wait(bar, parity & 1, a.unit_polls); };
+    const auto report = [&](bool ok) {
+        if (!ok && lane == 0) flag_status(a.dev_status, KDA_DEV_TIMEOUT);
+    };
     const auto dead = [&] { return *reinterpret_cast<volatile int*>(&s.dead) != 0; };
     constexpr uint32_t O0 = 256;  // S: columns 0 .. 2 KEYS - 1, O behind
 
@@ -250,6 +253,7 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
                         if (lane == 0) ptx::mbar_arrive(&s.full[use % SLOTS]);
                     }
             }
+            report(ok);
             // what is on its way has to land first (it has, unless those who wait for it gave up)
             for (uint32_t u = use > SLOTS ? use - SLOTS : 0; u < use; ++u) ptx::mbar_wait(&s.full[u % SLOTS], (u / SLOTS) & 1, PAGED_POLLS);
         } else if (warp >= 10) {
@@ -358,6 +362,7 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
                 }
             }
             store();
+            report(ok);
             ptx::bulk_wait_all();
             // what is on its way has to land first (as above)
             if (whole_tokens(a.G) && me == 0)
@@ -511,6 +516,7 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
                 ++qcount[0];
                 qcount[1] += two;
             }
+            report(ok);
             // nothing may be on its way when TMEM is freed
             if (leader) ptx::mma_commit(&s.drained);
             __syncwarp();
@@ -714,7 +720,7 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
                 asm volatile("bar.sync 1, 256;" ::: "memory");
             }
         }
-        if (!ok && lane == 0) flag_status(a.dev_status, KDA_DEV_TIMEOUT);
+        report(ok);
     }
     ptx::tc_fence_before();
     __syncthreads();

@@ -310,6 +310,7 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
                                 tok & ((1 << a.page_shift) - 1), 0, h, gone ? -1 : page, &s.full[stage], once);
             }
         }
+        if (!ok && lane == 0) flag_status(a.dev_status, KDA_DEV_TIMEOUT);
         // what is on its way has to land first (it has, unless those who wait for it gave up)
         for (uint32_t u = use > STAGES ? use - STAGES : 0; u < use; ++u) ptx::mbar_wait(&s.full[u % STAGES], (u / STAGES) & 1, PAGED_POLLS);
         for (uint32_t u = unit > 2 ? unit - 2 : 0; u < unit; ++u) ptx::mbar_wait(&s.qfull[u & 1], (u >> 1) & 1, PAGED_POLLS);

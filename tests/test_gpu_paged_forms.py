@@ -343,3 +343,25 @@ def test_waits_that_run_out(cuda_lib, decode, io, D, G):
     assert kept_rows < 2 * c.T * c.Hq  # a CTA has a part in a few units only
     for g in (a.out, a.lse, a.ws, *c.pools):
         assert g.intact()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("G,lens,kv", [(4, [20] * 8, [100] * 8), (3, [20] * 8, [100] * 8), (16, [20] * 40, [1500] * 40)], ids=["whole tokens", "cut tokens", "long units"])
+def test_no_wait_runs_out_in_silence(cuda_lib, D, G, lens, kv):
+    """The waits that last a unit (for its rows' place, for its outputs) limited to one poll, nothing else wrong: whatever did not come is flagged."""
+    kda = cuda_lib
+    c = Cache(lens, kv, Hkv=2, G=G, D=D, page=64)
+    a = Attn(c, kda).run()
+    want, lse = a.out.tensor.clone(), a.lse.tensor.clone()
+    for _ in range(5):
+        a.out.tensor.fill_(7.0)
+        kda.check(kda.kda_debug_paged_attn_stalled(a.p, c.cu, c.N, a.rows, c.kv_lens, c.pages, a.q, *[g.tensor for g in c.pools], a.out.tensor,
+                                                   a.lse.tensor, a.ws.tensor, a.need, c.status, 1 << 14, 1, -1))
+        torch.cuda.synchronize()
+        # outputs leave 128 channels at a time
+        same, kept = ((a.out.tensor == x).view(-1, c.Hq, max(D // 128, 1), min(D, 128)).all(-1)[:c.T] for x in (want, 7.0))
+        assert (same | kept).all()
+        assert int(c.status.item()) in ((kda.KDA_DEV_TIMEOUT,) if kept.any() else (0, kda.KDA_DEV_TIMEOUT))
+        c.status.zero_()
+    a.run()
+    assert torch.equal(a.out.tensor, want) and torch.equal(a.lse.tensor, lse) and int(c.status.item()) == 0
