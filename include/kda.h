@@ -668,7 +668,7 @@ KDA_API size_t kda_paged_attn_decode_workspace_bytes(const kda_paged_params* p, 
 /*
  * Test hook for the bounded on-chip waits of the two calls above (cu_seqlens
  * NULL: of the single tokens, T = N).  Waits give up after poll_limit polls, those
- * that last a whole unit after unit_poll_limit (both > 0), and CTA stalled_cta
+ * that last a whole unit after unit_poll_limit for each 2^16 of its key tiles (both > 0), and CTA stalled_cta
  * (none below 0 or past the grid) loads no keys and values, so that those who
  * wait for them run out: KDA_DEV_TIMEOUT is set, nothing is in flight, rows
  * that this CTA had a part in keep what they held, the others are computed.

@@ -26,7 +26,7 @@ struct PagedArgs {
     float* lse;
     void* workspace;
     int32_t* dev_status;
-    uint32_t polls, unit_polls;  // after which a wait gives up: for a tile, for a whole unit
+    uint32_t polls, unit_polls;  // after which a wait gives up: for a tile, for 2^16 tiles of a unit
     int stalled;                 // the CTA that loads nothing, -1: none (kda_debug_paged_attn_stalled)
 };
 

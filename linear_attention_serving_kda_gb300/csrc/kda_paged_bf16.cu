@@ -199,7 +199,9 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
     // the storing warps and by the join (PART_LOST): softmax warps that go on without waits arrive early at barriers that others of their tile share, so that nothing
     // behind those is sure.  They set `dead` before such an arrival; it is looked at after it.
     const auto wait = [&](uint64_t* bar, uint32_t parity) { return ptx::mbar_wait(bar, parity & 1, a.polls); };
-    const auto wait_unit = [&](uint64_t* bar, uint32_t parity) { return ptx::mbar_wait(bar, parity & 1, a.unit_polls); };
+    // One that lasts a piece of a unit, of n key tiles: a poll that nothing ends lasts 3.7 us, a tile 1.3 (two tiles of 128 rows by 128 keys of 64), so that
+    // PAGED_POLLS are 15 s, 12 million tiles; the limit grows with n from 2^16 of them on.
+    const auto wait_unit = [&](uint64_t* bar, uint32_t parity, int n) { return ptx::mbar_wait(bar, parity & 1, a.unit_polls * (1 + ((uint32_t)n >> 16))); };
     const auto report = [&](bool ok) {
         if (!ok && lane == 0) flag_status(a.dev_status, KDA_DEV_TIMEOUT);
     };
@@ -264,11 +266,12 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
             const int me = warp & 1, e = lane % PIECES, r0 = me * 64 + lane / PIECES;
             const int dt = group_of(a, AT_ONCE), dg = AT_ONCE - dt * a.G;
             uint32_t count[2] = {0, 0}, stored = 0, use = 0;
+            int before = 0;  // key tiles of the piece before
             bool ok = true;
             // slot `me` of a unit that leaves through the ring
             struct {
                 bool any = false;
-                int begin, row0, rows, head;
+                int begin, row0, rows, head, count;
                 uint32_t use;
             } out;
             const auto store = [&] {
@@ -276,7 +279,7 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
                 out.any = false;
                 constexpr int COLS = L::COLS, PC = COLS / 8, ROWS_AT_ONCE = 32 / PC;
                 const int t = L::OUT == 1 ? me : 0, col = L::OUT == 1 ? 0 : me * COLS, c8 = lane % PC;
-                ok = wait_unit(&s.ready[me], stored++);
+                ok = wait_unit(&s.ready[me], stored++, out.count);
                 if (!(ok = !__any_sync(0xffffffffu, !ok || dead()))) return;
                 const unsigned char* slot = s.ring + out.use % SLOTS * SLOT;
                 const int last = min(128, out.rows - t * 128);
@@ -316,7 +319,7 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
 #pragma unroll
                 for (int t = 0; t < L::TILES; ++t) {
                     if (t >= w.tiles || (whole_tokens(a.G) && me == 1)) break;
-                    if (!(ok = wait_unit(&s.free[t], count[t] + 1))) break;  // the scores of the unit before are done
+                    if (!(ok = wait_unit(&s.free[t], count[t] + 1, before))) break;  // the scores of the unit before are done
                     ++count[t];
                     unsigned char* base = s.q + t * (128 * DP * 2);
                     if (whole_tokens(a.G)) {
@@ -349,6 +352,7 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(&s.rows[t]);
                 }
+                before = w.count;
                 store();  // of the unit before: these rows went first
                 use += 2 * w.count;
                 if (w.staged) {
@@ -357,6 +361,7 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
                     out.row0 = w.row0;
                     out.rows = w.rows;
                     out.head = w.head;
+                    out.count = w.count;
                     out.use = use + me;
                     use += w.tiles * L::OUT;
                 }

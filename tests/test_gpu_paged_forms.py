@@ -365,3 +365,30 @@ def test_no_wait_runs_out_in_silence(cuda_lib, D, G, lens, kv):
         c.status.zero_()
     a.run()
     assert torch.equal(a.out.tensor, want) and torch.equal(a.lse.tensor, lse) and int(c.status.item()) == 0
+
+
+def test_waits_over_a_long_unit_are_as_long(cuda_lib):
+    """Units of 2^24 tokens (two pages again and again), one a CTA: the waits that last a unit go by its length.  Their limit here, 2^14 polls of less than 4 us
+    (a poll that nothing ends), is shorter than the unit; by its length it is three times that."""
+    kda = cuda_lib
+    Hkv, G, D, page, T, pages = 152, 2, 64, 1024, 128, 1 << 14
+    g = torch.Generator(device="cuda").manual_seed(5)
+    k, v = (torch.randn(2, Hkv, page, D, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    q = torch.randn(T, Hkv * G, D, generator=g, device="cuda").to(torch.bfloat16)
+    table = (torch.arange(pages, device="cuda") % 2).to(torch.int32)[None].contiguous()
+    p = kda.PagedParams(Hkv * G, Hkv, D, page, 2, pages, causal=False, scale=D ** -0.5, cache_page_stride=Hkv * page * D, cache_token_stride=D,
+                        cache_head_stride=page * D)
+    outs = []
+    for tokens in (2 * page, pages * page):
+        need = kda.kda_paged_attn_workspace_bytes(p, 1, T)
+        ws, out, status = torch.empty(need, dtype=torch.uint8, device="cuda"), torch.full_like(q, 7.0), _i32([0])
+        start, end = torch.cuda.Event(True), torch.cuda.Event(True)
+        start.record()
+        kda.check(kda.kda_debug_paged_attn_stalled(p, _i32([0, T]), 1, T, _i32([tokens]), table, q, k, v, out, None, ws, need, status, 1 << 22, 1 << 14, -1))
+        end.record()
+        torch.cuda.synchronize()
+        assert int(status.item()) == 0, (tokens, start.elapsed_time(end))
+        outs.append(out.double())
+    # the same tokens 2^13 times each: the same means, but for 2^17 sums of tiles in fp32 (2^-24 of each, 2^-23 where a product's sum is cut off),
+    # over values of mean size below 1 (of either sign; the weights are positive), and the outputs' rounding
+    assert (outs[0] - outs[1]).abs().max() <= 2 * 2.0 ** (17 - 23) + 2.0 ** -7
