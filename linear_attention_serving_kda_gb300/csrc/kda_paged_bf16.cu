@@ -490,7 +490,9 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
                         at_keys();
                         at_values();
                         ok = values_here(j);
-                        if (j == 0) ok = ok && wait(&s.taken[0], qcount[0] + 1);
+                        // O of the unit before is read, also its second tile's, if it had one (else of the last that had): product[1] is about to be used again, and whoever
+                        // still waits for its last use would take two for none
+                        if (j == 0) ok = ok && wait(&s.taken[0], qcount[0] + 1) && (L::TILES == 1 || wait(&s.taken[1], qcount[1] + 1));
                         const bool there = __all_sync(0xffffffffu, more && ptx::mbar_test(&s.full[kp.slot], kp.phase));
                         ok = ok && wait(&s.weights[b], b ? wcount[1]++ : wcount[0]++);
                         ptx::tc_fence_after();

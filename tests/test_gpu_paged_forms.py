@@ -392,3 +392,20 @@ def test_waits_over_a_long_unit_are_as_long(cuda_lib):
     # the same tokens 2^13 times each: the same means, but for 2^17 sums of tiles in fp32 (2^-24 of each, 2^-23 where a product's sum is cut off),
     # over values of mean size below 1 (of either sign; the weights are positive), and the outputs' rounding
     assert (outs[0] - outs[1]).abs().max() <= 2 * 2.0 ** (17 - 23) + 2.0 ** -7
+
+
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("G", [4, 3])
+def test_units_of_two_tiles_and_of_one_in_turn(cuda_lib, D, G):
+    """Thousands of short units, with the second tile of rows in use or not from one to the next."""
+    r = np.random.default_rng(G)
+    n = 256 // G
+    lens = [int(x) for _ in range(300) for x in (r.integers(n // 2 + 1, n + 1), r.integers(1, n // 2 + 1))]
+    kv = [int(x + r.integers(0, 300)) for x in lens]
+    c = Cache(lens, kv, Hkv=8, G=G, D=D, page=64)
+    a = Attn(c, cuda_lib).run()
+    want = a.out.tensor.clone()
+    for _ in range(20):
+        a.run()
+        assert torch.equal(a.out.tensor, want) and int(c.status.item()) == 0
+    a.check(rows=sorted(r.choice(c.T, 40, replace=False).tolist()))
