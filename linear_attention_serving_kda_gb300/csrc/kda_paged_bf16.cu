@@ -43,7 +43,7 @@ template <int DP> struct Shape {
     struct Smem {
         unsigned char q[Q];
         unsigned char ring[SLOTS * SLOT];
-        uint64_t full[SLOTS], empty[SLOTS], scores[2], weights[2], product[2], rows[2], free[2], taken[2], ready[2], drained;
+        uint64_t full[SLOTS], empty[SLOTS], scores[2], weights[2], product[2], rows[2], free[2], taken[2], ready[2][2], drained;
         uint32_t hidden[8], tmem;
         int dead;  // a wait ran out
         Start start;
@@ -175,7 +175,8 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
             ptx::mbar_init(&s.rows[i], whole_tokens(a.G) ? 1 : 2);
             ptx::mbar_init(&s.free[i], 1);
             ptx::mbar_init(&s.taken[i], 4);
-            ptx::mbar_init(&s.ready[i], 4);
+            ptx::mbar_init(&s.ready[i][0], 4);
+            ptx::mbar_init(&s.ready[i][1], 4);
         }
         s.dead = 0;
         ptx::mbar_init(&s.drained, 1);
@@ -261,7 +262,10 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
         } else if (warp >= 10) {
             // ---- rows: a tensor copy, or (tiles that cut tokens) half of each tile by either warp, 16-byte pieces permuted within
             // eight rows as the descriptor expects; and the outputs of the unit before from the ring's slots, the first slot by one warp,
-            // the second by the other.  (Pieces by threads take 3 us a unit, copies nothing that shows: 64 prompts of 333 rows 202 -> 190 us.)
+            // the second by the other.  (Outputs of units in turn are announced on two barriers: with one, softmax warps that are through with the next unit
+            // before this warp looks for the one before would make two uses look like none.  They cannot be through with the one after that: its rows come from this
+            // warp, behind its stores, or (second slot, rows by the other warp) its slot lies two units, eight places of the ring at least, behind this one's.)  (Pieces by threads take 3 us a unit, copies nothing that shows: 64 prompts of 333 rows 202 -> 190 us.)
+            static_assert(SLOTS <= 8, "two units use the whole ring");
             constexpr int PIECES = DP / 8, AT_ONCE = 32 / PIECES;  // rows that a warp's 32 pieces make
             const int me = warp & 1, e = lane % PIECES, r0 = me * 64 + lane / PIECES;
             const int dt = group_of(a, AT_ONCE), dg = AT_ONCE - dt * a.G;
@@ -279,7 +283,8 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
                 out.any = false;
                 constexpr int COLS = L::COLS, PC = COLS / 8, ROWS_AT_ONCE = 32 / PC;
                 const int t = L::OUT == 1 ? me : 0, col = L::OUT == 1 ? 0 : me * COLS, c8 = lane % PC;
-                ok = wait_unit(&s.ready[me], stored++, out.count);
+                ok = wait_unit(&s.ready[me][stored & 1], stored >> 1, out.count);
+                ++stored;
                 if (!(ok = !__any_sync(0xffffffffu, !ok || dead()))) return;
                 const unsigned char* slot = s.ring + out.use % SLOTS * SLOT;
                 const int last = min(128, out.rows - t * 128);
@@ -536,7 +541,7 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
         const int t = warp >> 2, r = tid & 127;  // tile, row of it
         const uint32_t tl = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes
         const float c = a.scale * 1.4426950408889634f;
-        uint32_t scount[2] = {0, 0}, sbase[2] = {0, 0}, pcount[2] = {0, 0}, kt = 0, use = 0;
+        uint32_t scount[2] = {0, 0}, sbase[2] = {0, 0}, pcount[2] = {0, 0}, kt = 0, use = 0, staged = 0;
         bool ok = true;
         Work w;
         for (w.start(p, s.start); w.step(a, p);) {
@@ -674,10 +679,11 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
                         __syncwarp();
                         if (lane == 0) {
                             if (i == L::OUT - 1) ptx::mbar_arrive(&s.taken[t]);  // O may be overwritten
-                            ptx::mbar_arrive(&s.ready[L::OUT == 1 ? t : i]);
+                            ptx::mbar_arrive(&s.ready[L::OUT == 1 ? t : i][staged & 1]);
                         }
                     }
                     use += (w.tiles - 1 - t) * L::OUT;
+                    ++staged;
                 } else {
                     if (live) {
 #pragma unroll 1

@@ -409,3 +409,15 @@ def test_units_of_two_tiles_and_of_one_in_turn(cuda_lib, D, G):
         a.run()
         assert torch.equal(a.out.tensor, want) and int(c.status.item()) == 0
     a.check(rows=sorted(r.choice(c.T, 40, replace=False).tolist()))
+
+
+@pytest.mark.parametrize("D", [32, 64, 128, 256])
+def test_short_units_through_the_ring(cuda_lib, D):
+    """Thousands of units of one key tile, all of whole tokens: outputs of neighbouring units close behind one another."""
+    c = Cache([64] * 500, [64 + i % 40 for i in range(500)], Hkv=8, G=4, D=D, page=64)
+    a = Attn(c, cuda_lib).run()
+    want = a.out.tensor.clone()
+    for _ in range(20):
+        a.run()
+        assert torch.equal(a.out.tensor, want) and int(c.status.item()) == 0
+    a.check(rows=[0, 63, 64, 16000, 31937, 31999])
