@@ -532,6 +532,8 @@ typedef struct kda_rope_scaling {
  *   radians: HOST, nullable; rotary_dim / 2 finite angles in place of
  *            base^(-2 i / rotary_dim), for any other scheme (kind BASE then
  *            gives KDA_ERR_INVALID_ARGUMENT).
+ * A factor with which f_i / factor or the scaled base is not finite (or the base 0)
+ * is KDA_ERR_INVALID_ARGUMENT; turns may be partly written then.
  * rotary_dim: even, 2 .. KDA_ROPE_MAX_DIM.  Touches no GPU.
  */
 #define KDA_ROPE_MAX_DIM 512

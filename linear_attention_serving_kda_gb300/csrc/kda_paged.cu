@@ -570,6 +570,7 @@ KDA_API int kda_rope_turns(const kda_rope_scaling* s, int32_t rotary_dim, const 
         for (int i = 0; i < n; ++i)
             if (!std::isfinite(radians[i])) return KDA_ERR_INVALID_ARGUMENT;
     const double base = kind == KDA_ROPE_SCALE_BASE ? s->base * std::pow(s->factor, (double)rotary_dim / (rotary_dim - 2)) : s->base;
+    if (kind == KDA_ROPE_SCALE_BASE && !(std::isfinite(base) && base > 0.0)) return KDA_ERR_INVALID_ARGUMENT;
     double low = 0, high = 1;
     if (kind == KDA_ROPE_SCALE_RAMP) {
         const auto dim = [&](double b) { return rotary_dim * std::log(s->length / (b * two_pi)) / (2 * std::log(s->base)); };
@@ -587,6 +588,7 @@ KDA_API int kda_rope_turns(const kda_rope_scaling* s, int32_t rotary_dim, const 
             const double k = std::min(std::max((s->length * f / two_pi - s->slow) / (s->fast - s->slow), 0.0), 1.0);
             f = f * k + f / s->factor * (1 - k);
         }
+        if (!std::isfinite(f)) return KDA_ERR_INVALID_ARGUMENT;
         double t = f / two_pi;
         t -= std::floor(t);
         turns[i] = t >= 1.0 ? 0 : (uint64_t)std::ldexp(t, 64);

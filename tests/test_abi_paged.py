@@ -68,6 +68,16 @@ def test_turns_refusals(kw, rc):
     assert _turns(**kw)[0] == rc
 
 
+def test_turns_without_a_finite_angle():
+    big = torch.full((32,), 1e308, dtype=torch.float64)
+    for kind in (1, 3, 4):
+        assert _turns(kind=kind, factor=1e-320)[0] == INVALID, kind
+        assert _turns(kind=kind, factor=1e-5, radians=big)[0] == INVALID, kind
+    for factor in (1e-300, 1e300):
+        assert _turns(4, kind=2, factor=factor)[0] == INVALID
+    assert _turns(kind=2, factor=1e-4, base=10.0)[0] == OK
+
+
 ROPE = dict(num_heads=4, head_dim=64, rotary_dim=32, rope_turns=addr(9))
 
 
