@@ -584,7 +584,7 @@ typedef struct kda_paged_params {
     int32_t head_dim;             /* D in {32, 64, 128, 256}                    */
     int32_t io_dtype;             /* rows, cache and out: KDA_DTYPE_F32 / _BF16 */
     int32_t page_size;            /* 16, 32, 64, 128, 256, 512 or 1024          */
-    int32_t num_pages;            /* >= 1                                       */
+    int32_t num_pages;            /* >= 1; times the stride between pages at most 2^60 */
     int32_t pages_per_seq;        /* >= 1; times page_size <= KDA_MAX_ROWS      */
     int32_t causal;               /* attention: 1, or 0 (every row sees every token) */
     int32_t window;               /* attention: 0, or with causal = 1 the tokens a row sees, its own the last */

@@ -366,6 +366,7 @@ int check_paged(const kda_paged_params* p)
     if (!(p->num_heads_kv == 1 || ts >= heads || hs >= tokens)) return KDA_ERR_INVALID_ARGUMENT;
     if (p->num_heads_kv == 1 && ts < D) return KDA_ERR_INVALID_ARGUMENT;
     if (p->num_pages > 1 && ps < heads + (P - 1) * ts) return KDA_ERR_INVALID_ARGUMENT;
+    if (p->num_pages - 1 > ((int64_t)1 << 60) / ps) return KDA_ERR_INVALID_ARGUMENT;  // (its bytes are counted in 64 bits)
     const int64_t kw = (int64_t)p->num_heads_kv * D, qw = (int64_t)p->num_heads_q * D;
     if (!good_stride(p->q_in_row_stride, qw, unit) || !good_stride(p->q_row_stride, qw, unit) ||
         !good_stride(p->k_row_stride, kw, unit) || !good_stride(p->v_row_stride, kw, unit))

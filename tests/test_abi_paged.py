@@ -158,6 +158,15 @@ def test_append_rotation(kw, rc):
         assert _append(_params(**{**dict(rotary_dim=64, rope_turns=addr(9)), **kw}), d) == rc
 
 
+def test_caches_past_64_bits():
+    """Pages and strides that are in their ranges, and a cache of 2^67 values, whose bytes no overlap could be told from."""
+    for pages, stride in (((1 << 31) - 1, 1 << 36), (1 << 25, 1 << 36)):
+        p = _params(num_pages=pages, cache_page_stride=stride)
+        for d in (False, True):
+            assert _attn(p, d, out=addr(8)) == INVALID and _attn(p, d) == INVALID and _append(p, d) == INVALID
+        assert kda.kda_paged_attn_workspace_bytes(p, 2, 6) == 0
+
+
 def test_append_pointers():
     p = _params()
     for d in (False, True):
