@@ -616,7 +616,8 @@ typedef struct kda_paged_params {
  *       (default: their token).
  *   k: [T][Hkv][D], v: [T][Hkv][D], q: [T][Hq][D], nullable with q_out; q_out may
  *       be q itself (with the same stride), other overlaps of what is written
- *       with an input are KDA_ERR_INVALID_ARGUMENT.  rotary_dim = 0: no rotation.
+ *       with an input, and places that k_cache and v_cache share, are
+ *       KDA_ERR_INVALID_ARGUMENT.  rotary_dim = 0: no rotation.
  * Rows of one call go to distinct places of the cache.
  */
 KDA_API int kda_paged_append_varlen(const kda_paged_params* p, const int32_t* cu_seqlens, int32_t N, int32_t T,

@@ -420,6 +420,29 @@ size_t cache_bytes(const PagedArgs& a, int io)
 
 size_t strided(int64_t rows, int64_t stride, int64_t width, int io) { return (size_t)((rows - 1) * stride + width) * io; }
 
+// Whether a cache and one of the same strides d elements on share a place.  Pages, and tokens and heads in either order, lie one within the other, so that
+// only the two nearest numbers of each stride can bring the places together.
+bool places_meet(const PagedArgs& a, int64_t d)
+{
+    const int64_t P = (int64_t)1 << a.page_shift;
+    const bool heads_inside = a.Hkv == 1 || a.token_stride >= (a.Hkv - 1) * a.head_stride + a.D;
+    const int64_t stride[3] = {a.num_pages > 1 ? a.page_stride : (int64_t)1 << 60, heads_inside ? a.token_stride : a.head_stride, heads_inside ? a.head_stride : a.token_stride};
+    const int64_t count[3] = {a.num_pages, heads_inside ? P : a.Hkv, heads_inside ? a.Hkv : P};
+    for (int which = 0; which < 8; ++which) {
+        int64_t left = d;
+        bool in = true;
+        for (int i = 0; i < 3 && in; ++i) {
+            int64_t n = left / stride[i];
+            if (left < 0 && left % stride[i] != 0) --n;  // down
+            n += (which >> i) & 1;
+            in = n < count[i] && -n < count[i];
+            left -= n * stride[i];
+        }
+        if (in && left < a.D && -left < a.D) return true;
+    }
+    return false;
+}
+
 template <class F> bool disjoint(const void* const* out, const size_t* nout, int n, const void* const* in, const size_t* nin, int m, F&& same)
 {
     for (int i = 0; i < n; ++i)
@@ -433,21 +456,24 @@ int append(const kda_paged_params* p, const int32_t* cu_seqlens, int32_t N, int3
            int32_t* dev_status, cudaStream_t stream)
 {
     int rc;
+    AppendArgs a = {};
+    fill_paged(a.p, p);
+    const int io = io_size(p->io_dtype);
+    const size_t cache = cache_bytes(a.p, io);
+    if (overlap(k_cache, cache, v_cache, cache) && places_meet(a.p, (static_cast<const char*>(v_cache) - static_cast<const char*>(k_cache)) / io))
+        return KDA_ERR_INVALID_ARGUMENT;
     if (p->rotary_dim != 0 && (rc = check_turn(p->head_dim, p->rotary_dim, p->rope_layout, p->rope_amplitude, p->rope_turns)) != KDA_OK) return rc;
     if ((rc = check_ptrs({kv_lens, pages, k, v, k_cache, v_cache})) != KDA_OK || (rc = check_opt(positions)) != KDA_OK ||
         (rc = check_opt(q)) != KDA_OK || (rc = check_opt(q_out)) != KDA_OK)
         return rc;
     if ((q == nullptr) != (q_out == nullptr)) return KDA_ERR_INVALID_ARGUMENT;
-    const int io = io_size(p->io_dtype);
-    AppendArgs a = {};
-    fill_paged(a.p, p);
     a.p.N = N;
     a.p.T = T;
     const int64_t kw = (int64_t)a.p.Hkv * a.p.D, qw = (int64_t)a.p.Hq * a.p.D;
     a.qis = p->q_in_row_stride ? p->q_in_row_stride : qw;
     a.ks = p->k_row_stride ? p->k_row_stride : kw;
     a.vs = p->v_row_stride ? p->v_row_stride : kw;
-    const size_t cache = cache_bytes(a.p, io), nq = strided(T, a.qis, qw, io), nqo = strided(T, a.p.q_stride, qw, io);
+    const size_t nq = strided(T, a.qis, qw, io), nqo = strided(T, a.p.q_stride, qw, io);
     const void* out[3] = {k_cache, v_cache, q_out};
     const size_t nout[3] = {cache, cache, nqo};
     const void* in[8] = {q, k, v, cu_seqlens, kv_lens, pages, positions, p->rotary_dim ? p->rope_turns : nullptr};
@@ -464,7 +490,7 @@ int append(const kda_paged_params* p, const int32_t* cu_seqlens, int32_t N, int3
         return js == s && d >= qw && d + kw <= s;
     };
     if (!disjoint(out, nout, 3, in, nin, 8, apart)) return KDA_ERR_INVALID_ARGUMENT;
-    if (overlap(q_out, nqo, k_cache, cache) || overlap(q_out, nqo, v_cache, cache) || k_cache == v_cache) return KDA_ERR_INVALID_ARGUMENT;
+    if (overlap(q_out, nqo, k_cache, cache) || overlap(q_out, nqo, v_cache, cache)) return KDA_ERR_INVALID_ARGUMENT;
     if ((rc = check_device()) != KDA_OK) return rc;
     a.p.cu_seqlens = cu_seqlens;
     a.p.kv_lens = kv_lens;

@@ -167,6 +167,28 @@ def test_caches_past_64_bits():
         assert kda.kda_paged_attn_workspace_bytes(p, 2, 6) == 0
 
 
+@pytest.mark.parametrize("io", [kda.KDA_DTYPE_BF16, kda.KDA_DTYPE_F32])
+def test_keys_and_values_that_share_places(io):
+    """Against all places of a small cache, counted one by one.  (A call that gets past this check stops at its rotation, whose width is odd.)"""
+    size = 2 if io == kda.KDA_DTYPE_BF16 else 4
+    D = 32
+    # key heads, strides of pages, tokens and heads: dense, either order, with gaps, pools side by side in a page, one head
+    for Hkv, ps, ts, hs, pages in [(*x, 3) for x in [(2, 16 * 64, 64, 32), (2, 16 * 64, 32, 16 * 32), (2, 2048, 64, 32), (2, 2048, 32, 512), (2, 4096, 128, 32), (2, 4096, 128, 64),
+                            (3, 4992, 48, 1024), (1, 16 * 32, 32, 32), (1, 1024, 64, 8192), (1, 576, 32, 8192)]] + [
+                                   (2, 64, 64, 32, 1), (2, 128, 32, 512, 1), (1, 32, 64, 32, 1)]:
+        p = _params(num_heads_q=Hkv, num_heads_kv=Hkv, head_dim=D, num_pages=pages, io_dtype=io, cache_page_stride=ps, cache_token_stride=ts,
+                    cache_head_stride=hs, rotary_dim=5)
+        starts = {pg * ps + t * ts + h * hs for pg in range(pages) for t in range(16) for h in range(Hkv)}
+        taken = {s + i for s in starts for i in range(0, D, 8)}
+        seen = set()
+        for delta in {8 * i for i in range(-40, 41)} | {x + 8 * i for x in (ps, 2 * ps, 3 * ps, -ps, 15 * ts, 16 * ts, hs, hs * Hkv, ps // 2) for i in range(-9, 10)}:
+            meet = any(s + delta + i in taken for s in starts for i in range(0, D, 8))
+            seen.add(meet)
+            for d in (False, True):
+                assert _append(p, d, kc=addr(8), vc=addr(8) + delta * size) == (INVALID if meet else GEOMETRY), (Hkv, ps, ts, hs, delta)
+        assert seen == {True, False}
+
+
 def test_append_pointers():
     p = _params()
     for d in (False, True):
