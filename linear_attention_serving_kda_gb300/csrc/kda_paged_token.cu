@@ -35,7 +35,7 @@ struct TokenWork {
     float* o;                  // [CTAS][2][rows][D]   0: of a unit that began before, 1: of the one that goes on
 };
 
-// Heads of a unit: eight (a column block of a product) or sixteen.
+// Places for a unit's heads: eight (a column block of a product) or sixteen; a group has no more (paged_token_wanted).
 int unit_rows(const PagedArgs& a) { return a.G <= 8 ? 8 : 16; }
 
 size_t lay_out(TokenWork& w, const PagedArgs& a)
@@ -145,7 +145,7 @@ __device__ __forceinline__ int owner(long long line, long long x) { return (int)
 
 // A CTA's walk along its stretch, unit after unit.
 struct Walk {
-    int s, kv, u;            // sequence, its tokens, unit within it (key head, block of heads)
+    int s, kv, u;            // sequence, its tokens, key head
     int lo, start, n;        // as in Span
     int t0, t1;              // tiles of the unit in this stretch
     long long left;          // tiles of the stretch from t0 on
@@ -179,11 +179,11 @@ template <int KEYS, class S> __device__ __forceinline__ void begin_walk(const Pa
     w.t0 = (int)(sm.offset % w.n);
     w.t1 = (int)min((long long)w.n, w.t0 + w.left);
 }
-template <int KEYS, class S> __device__ __forceinline__ void next_unit(const PagedArgs& a, const S& sm, Walk& w, int units)
+template <int KEYS, class S> __device__ __forceinline__ void next_unit(const PagedArgs& a, const S& sm, Walk& w)
 {
     w.left -= w.t1 - w.t0;
     if (w.left <= 0) return;
-    if (++w.u == units) {
+    if (++w.u == a.Hkv) {
         w.u = 0;
         ++w.s;
         enter<KEYS>(a, sm, w);
@@ -200,7 +200,7 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
     constexpr int ROWS = L::ROWS, STAGES = L::STAGES, BLOCKS = L::BLOCKS, KEYS = L::KEYS, WARPS = L::WARPS, TEAM = L::TEAM, TT = L::THREADS;
     extern __shared__ __align__(1024) unsigned char raw[];
     auto& s = *reinterpret_cast<typename L::Smem*>(raw);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, blocks = (a.G + ROWS - 1) / ROWS, units = a.Hkv * blocks;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     ptx::grid_launch_dependents();
     if (tid == 0) {
         for (int i = 0; i < STAGES; ++i) {
@@ -247,15 +247,15 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
         line += s.sum[w];
     }
     before -= mine;
-    line *= units;
-    before *= units;
+    line *= a.Hkv;
+    before *= a.Hkv;
     const long long x0 = stretch(line, blockIdx.x), x1 = stretch(line, blockIdx.x + 1);
-    if (x0 < x1 && before <= x0 && x0 < before + mine * units) {
+    if (x0 < x1 && before <= x0 && x0 < before + mine * a.Hkv) {
         int i = s0, f = 0;
         for (;; ++i) {
             const int n = Span<KEYS>(a, length_of(a, i, &f)).n;
-            if (x0 < before + (long long)n * units) break;
-            before += (long long)n * units;
+            if (x0 < before + (long long)n * a.Hkv) break;
+            before += (long long)n * a.Hkv;
         }
         s.first = i;
         s.offset = x0 - before;
@@ -281,13 +281,13 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
         const uint64_t once = ptx::policy_evict_first();
         const int box = min(KEYS, 1 << a.page_shift), boxes = KEYS / box;
         uint32_t use = 0, unit = 0;
-        for (; w.left > 0 && ok; next_unit<KEYS>(a, s, w, units), ++unit) {
-            const int h = w.u / blocks, g0 = w.u % blocks * ROWS, rows = min(ROWS, a.G - g0);
+        for (; w.left > 0 && ok; next_unit<KEYS>(a, s, w), ++unit) {
+            const int h = w.u;
             if (!(ok = wait(&s.qempty[unit & 1], (unit >> 1) + 1))) break;
-            if (lane == 0) ptx::mbar_arrive_expect_tx(&s.qfull[unit & 1], rows * D * L::SIZE);
+            if (lane == 0) ptx::mbar_arrive_expect_tx(&s.qfull[unit & 1], a.G * D * L::SIZE);
             __syncwarp();
-            if (lane < rows)
-                ptx::bulk_g2s(s.q[unit & 1] + lane * L::QS, static_cast<const IO*>(a.q) + w.s * a.q_stride + (long long)(h * a.G + g0 + lane) * D,
+            if (lane < a.G)
+                ptx::bulk_g2s(s.q[unit & 1] + lane * L::QS, static_cast<const IO*>(a.q) + w.s * a.q_stride + (long long)(h * a.G + lane) * D,
                               D * L::SIZE, &s.qfull[unit & 1]);
             for (int t = w.t0; t < w.t1; ++t, ++use) {
                 const int stage = use % STAGES, k0 = w.start + t * KEYS, tok = k0 + lane % boxes * box;
@@ -322,8 +322,8 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
         if (tid == 0) work.cut[blockIdx.x].seq = -1;
         // (a wait that ran out: the warps go on without waiting and without tiles, so that they still meet at the barriers; a unit that a warp gave up on
         // is written nowhere, PART_LOST in its place)
-        for (; w.left > 0; next_unit<KEYS>(a, s, w, units), ++unit) {
-            const int h = w.u / blocks, g0 = w.u % blocks * ROWS, rows = min(ROWS, a.G - g0);
+        for (; w.left > 0; next_unit<KEYS>(a, s, w), ++unit) {
+            const int h = w.u, rows = a.G;
             ok = ok && wait(&s.qfull[unit & 1], unit >> 1);
             // tokens are the products' rows, heads their columns: S^T = K Q^T, O^T += V^T W^T
             const uint32_t qbase = ptx::smem_u32(s.q[unit & 1]) + (lane & 7) * L::QS + (lane >> 3) * 16;
@@ -590,7 +590,7 @@ paged_token_kernel(const PagedArgs a, const TokenWork work, const __grid_constan
             for (int x = 0; x < WARPS; ++x) sum += s.ml[x][row % ROWS].y * exp2_sfu(s.ml[x][row % ROWS].x - base);
             const bool whole = w.t0 == 0 && w.t1 == w.n;
             const int slot = w.t0 == 0 ? 1 : 0;
-            const size_t head = (size_t)w.s * a.Hq + h * a.G + g0 + row, cell = ((size_t)blockIdx.x * 2 + slot) * ROWS + row;
+            const size_t head = (size_t)w.s * a.Hq + h * a.G + row, cell = ((size_t)blockIdx.x * 2 + slot) * ROWS + row;
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
             for (int e = 0; e < D; e += CH) {
@@ -708,15 +708,14 @@ template <typename IO, int D, int ROWS> __global__ void __launch_bounds__(32 * R
     ptx::grid_dependency_wait();
     const Cut cut = work.cut[blockIdx.x];
     if (cut.seq < 0) return;
-    const int blocks = (a.G + ROWS - 1) / ROWS, h = cut.unit / blocks, g0 = cut.unit % blocks * ROWS, row = threadIdx.x >> 5;
-    if (g0 + row >= a.G) return;
+    const int row = threadIdx.x >> 5;
     // stretches without a tile (fewer tiles than stretches) left nothing
     const auto used = [&](int s) { return stretch(cut.line, blockIdx.x + s) < stretch(cut.line, blockIdx.x + s + 1); };
     const auto cell = [&](int s) { return ((size_t)(blockIdx.x + s) * 2 + (s == 0)) * ROWS + row; };
     float y[D / 32];
     const float2 ml = join_row<D>(cut.last - (int)blockIdx.x + 1, [&](int s) { return used(s) ? work.ml + cell(s) : nullptr; },
                                          [&](int s) { return used(s) ? work.o + cell(s) * D : nullptr; }, y);
-    write_row<IO, D>(a, (size_t)cut.seq * a.Hq + h * a.G + g0 + row, ml, y);
+    write_row<IO, D>(a, (size_t)cut.seq * a.Hq + cut.unit * a.G + row, ml, y);
 }
 
 // [num_pages][Hkv][D / 64][page_size][64] (fp32: 32 values, 128 bytes either way) by the cache's strides; boxes of a page's (or a tile's) tokens and all channels of one head.
