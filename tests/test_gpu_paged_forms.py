@@ -421,3 +421,13 @@ def test_short_units_through_the_ring(cuda_lib, D):
         a.run()
         assert torch.equal(a.out.tensor, want) and int(c.status.item()) == 0
     a.check(rows=[0, 63, 64, 16000, 31937, 31999])
+
+
+@pytest.mark.parametrize("decode", [False, True])
+@pytest.mark.parametrize("G", [2, 32, 64, 128])
+@pytest.mark.parametrize("D", [32, 64, 128, 256])
+def test_groups_whose_tokens_fill_a_tile(cuda_lib, D, G, decode):
+    """Powers of two: rows and outputs in boxes of 128 / G tokens (single tokens of more than 16 heads as chunks of one)."""
+    lens, kv = ([1] * 5, [300, 1, 64, 700, 129]) if decode else ([1, 9, 128 // G, 3], [200, 9, 90, 500])
+    c = Cache(lens, kv, Hkv=2, G=G, D=D, page=32)
+    Attn(c, cuda_lib, decode=decode, q_extra=32).run().check()
