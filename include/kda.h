@@ -528,7 +528,9 @@ typedef struct kda_rope_scaling {
  * The angles of rotary_dim / 2 pairs as the kernels take them, into HOST
  * memory (the caller copies them to the device once): turns[i] =
  * frac(f_i / (2 pi)) * 2^64.  A position times that, modulo 2^64, is the
- * angle's fraction of a turn, exactly: far positions lose nothing.
+ * product's fraction of a turn, exactly.  What far positions lose is turns[i]'s
+ * own rounding: at position p an angle is off by up to p (f_i 2^-51 + 2^-61)
+ * radians (bases to 10^7), less than the fp32 angle's 2^-23 up to p = 2^27.
  *   radians: HOST, nullable; rotary_dim / 2 finite angles in place of
  *            base^(-2 i / rotary_dim), for any other scheme (kind BASE then
  *            gives KDA_ERR_INVALID_ARGUMENT).
@@ -577,6 +579,8 @@ KDA_API int kda_rope(const kda_rope_params* p, int64_t rows, const int32_t* posi
  * tokens and heads, and pools of several layers or of keys and values side
  * by side, fit (a page is a slot of kda_slots_copy then: copies of shared pages).
  * Table entries past a sequence's tokens are not read.
+ * Calls with (T + N) num_heads_q above 2^31 - 65537 (single tokens: T = N = B) are
+ * KDA_ERR_INVALID_ARGUMENT.
  */
 typedef struct kda_paged_params {
     int32_t num_heads_q;          /* Hq, a multiple of Hkv                      */
