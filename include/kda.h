@@ -651,9 +651,10 @@ KDA_API int kda_paged_append_decode(const kda_paged_params* p, int32_t B, const 
  *   Products take the rows' type and sum in fp32; weights are fp32 and, for bf16
  *       rows of a chunk, rounded to bf16 where they meet the values (single tokens
  *       of up to 16 heads a key head: in two bf16 parts).
- *   Whatever lies in the cache's places past a sequence's tokens has no
- *       effect.  A NaN or an infinity in a query or key reaches rows that
- *       see it, in a value also rows of the same chunk that do not.
+ *   Whatever lies in the cache's places past a sequence's tokens, or before the
+ *       window of all its rows, has no effect.  A NaN or an infinity in a query or
+ *       key reaches rows that see it, in a value also rows of the same chunk that
+ *       do not.
  *   A wait that gives up (KDA_DEV_TIMEOUT): rows that its CTA had not finished keep
  *       what out held (heads of 256: a half of them may), lse that or their own; so
  *       do those that it had a part in.

@@ -421,13 +421,15 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
                 };
                 const auto values_here = [&](int j) {
                     if (!wait(&s.full[vp.slot], vp.phase)) return false;
-                    const int have = w.k1 - w.k0 - j * KEYS;
-                    if (have < KEYS) {  // what lies behind the tokens may be anything: zeros, whose weights are zero
+                    const int have = w.k1 - w.k0 - j * KEYS, from = w.seen - w.k0 - j * KEYS;
+                    if (have < KEYS || from > 0) {  // what lies behind the tokens, or before the window, may be anything: zeros, whose weights are zero
                         // (a linear fill of each block's last rows: with a division a piece it took 5500 cycles, the next unit's start)
 #pragma unroll
-                        for (int blk = 0; blk < BLOCKS; ++blk)
-                            for (int at = have * 128 + lane * 16; at < KEYS * 128; at += 512)
-                                *reinterpret_cast<uint4*>(s.ring + vp.slot * SLOT + blk * (KEYS * 128) + at) = make_uint4(0, 0, 0, 0);
+                        for (int blk = 0; blk < BLOCKS; ++blk) {
+                            unsigned char* v = s.ring + vp.slot * SLOT + blk * (KEYS * 128);
+                            for (int at = have * 128 + lane * 16; at < KEYS * 128; at += 512) *reinterpret_cast<uint4*>(v + at) = make_uint4(0, 0, 0, 0);
+                            for (int at = lane * 16; at < from * 128; at += 512) *reinterpret_cast<uint4*>(v + at) = make_uint4(0, 0, 0, 0);
+                        }
                         ptx::fence_proxy_async_smem();
                         __syncwarp();
                     }

@@ -24,7 +24,7 @@ template <int D, int R> struct F32 {
     static constexpr int KW = KEYS * QS > R * WS ? KEYS * QS : R * WS;
     struct Smem {
         float q[R * QS], k[KW], v[KEYS * D];  // k: then the weights
-        long long at[KEYS];                   // a token's place in the cache, -1: none
+        long long at[KEYS];                   // a token's place in the cache, -1: none, or none that a row sees
     };
 };
 
@@ -73,7 +73,7 @@ template <int D, int R> __global__ void __launch_bounds__(FT, D == 256 ? 1 : 2) 
             if (tid < KEYS) {
                 const int t = k0 + tid;
                 long long at = -1;
-                if (t < last) {
+                if (t < last && t >= it.seen) {
                     const int page = a.pages[(long long)it.seq * a.width + (t >> a.page_shift)];
                     if (page < 0 || page >= a.num_pages) flag_status(a.dev_status, KDA_DEV_BAD_PAGE);
                     else at = page * a.page_stride + (t & ((1 << a.page_shift) - 1)) * a.token_stride + h * a.head_stride;

@@ -63,15 +63,18 @@ inline size_t lay_out(Plan& p, const PagedArgs& a, int rows, int keys, int ctas,
 __device__ __forceinline__ long long stretch(long long line, int c, int ctas) { return line * c / ctas; }
 __device__ __forceinline__ int owner(long long line, long long x, int ctas) { return (int)(((x + 1) * ctas + line - 1) / line) - 1; }
 
-// Tokens that rows row0 .. row0 + rows - 1 see: [lo, hi), lo down to the start of a page or of a tile of `keys` in it.
-__device__ __forceinline__ void span(const PagedArgs& a, int keys, int pos0, int kv, int row0, int rows, int& lo, int& hi)
+// Tokens that rows row0 .. row0 + rows - 1 see: [seen, hi), and lo: seen down to the start of a page or of a tile of `keys` in it.
+__device__ __forceinline__ void span(const PagedArgs& a, int keys, int pos0, int kv, int row0, int rows, int& lo, int& seen, int& hi)
 {
-    lo = 0;
+    lo = seen = 0;
     hi = kv;
     if (!a.causal) return;
     const int p0 = pos0 + group_of(a, row0), p1 = pos0 + group_of(a, row0 + rows - 1);
     hi = max(0, min(kv, p1 + 1));
-    if (a.window) lo = min(hi, p0 >= a.window ? p0 - a.window + 1 : 0) & ~(min(keys, 1 << a.page_shift) - 1);
+    if (a.window) {
+        seen = min(hi, p0 >= a.window ? p0 - a.window + 1 : 0);
+        lo = seen & ~(min(keys, 1 << a.page_shift) - 1);
+    }
 }
 
 // A walk along a stretch, piece of a unit after piece of a unit.
@@ -79,7 +82,7 @@ struct Walk {
     int seq, begin, kv;         // sequence, its first row, its tokens in the cache
     int tokens, all;            // its rows, and times G
     int row0, rows, head;       // the unit
-    int lo, hi, n;              // its tokens (lo may lie before the first that is seen) and key tiles
+    int lo, seen, hi, n;        // its tokens (from lo on; the first that a row sees) and key tiles
     int t0, t1;                 // the piece's key tiles
     bool act;                   // the piece has something to do
     int from;                   // the piece's first place in the unit
@@ -106,7 +109,7 @@ struct Walk {
     __device__ __forceinline__ void unit(const PagedArgs& a, const Plan& p)
     {
         rows = min(p.rows, all - row0);
-        span(a, p.keys, pos0(), kv, row0, rows, lo, hi);
+        span(a, p.keys, pos0(), kv, row0, rows, lo, seen, hi);
         n = (hi - lo + p.keys - 1) >> p.key_shift;
     }
     __device__ __forceinline__ void piece(const Plan& p)
@@ -167,8 +170,8 @@ struct Walk {
 // Places of a tile of rows of one key head.
 __device__ __forceinline__ int places(const PagedArgs& a, const Plan& p, int pos0, int kv, int row0, int rows)
 {
-    int lo, hi;
-    span(a, p.keys, pos0, kv, row0, rows, lo, hi);
+    int lo, seen, hi;
+    span(a, p.keys, pos0, kv, row0, rows, lo, seen, hi);
     return ((hi - lo + p.keys - 1) >> p.key_shift) + p.unit;
 }
 

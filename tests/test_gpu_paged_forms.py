@@ -431,3 +431,19 @@ def test_groups_whose_tokens_fill_a_tile(cuda_lib, D, G, decode):
     lens, kv = ([1] * 5, [300, 1, 64, 700, 129]) if decode else ([1, 9, 128 // G, 3], [200, 9, 90, 500])
     c = Cache(lens, kv, Hkv=2, G=G, D=D, page=32)
     Attn(c, cuda_lib, decode=decode, q_extra=32).run().check()
+
+
+@pytest.mark.parametrize("io,G,decode", [("bf16", 4, True), ("bf16", 20, True), ("bf16", 32, True), ("f32", 3, True), ("f32", 9, True), ("bf16", 4, False), ("f32", 4, False)])
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 128), (256, 64)])
+def test_values_before_the_window_have_no_effect(cuda_lib, D, page, io, G, decode):
+    """NaN and infinities in values that no row of the call sees, in the page and the tile in which the window begins."""
+    c = Cache([1, 1, 1] if decode else [3, 1, 2], [300, 1000, 130], Hkv=2, G=G, D=D, page=page, io=io)
+    window = 77
+    a = Attn(c, cuda_lib, decode=decode, window=window).run()
+    want, lse = a.out.tensor.clone(), a.lse.tensor.clone()
+    for s, (n, L) in enumerate(zip(c.lens, c.kv)):
+        for t in range(0, L - n - window + 1):
+            c.views[1][int(c.table[s, t // page]), t % page] = float("nan") if t % 3 else float("inf")
+    a.run()
+    assert torch.equal(a.out.tensor, want) and torch.equal(a.lse.tensor, lse)
+    a.check()
