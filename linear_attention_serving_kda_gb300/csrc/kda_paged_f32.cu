@@ -74,7 +74,7 @@ template <int D, int R> __global__ void __launch_bounds__(FT, D == 256 ? 1 : 2) 
                 const int t = k0 + tid;
                 long long at = -1;
                 // (the first token that a row sees, from the rows: it.seen kept over the loop costs registers, 885 us for 874)
-                if (t < last && !(a.window && t <= it.pos0() + group_of(a, it.row0) - a.window)) {
+                if (t < last && !(a.window && t <= it.pos0() + group_of(a, it.row0) - (long long)a.window)) {
                     const int page = a.pages[(long long)it.seq * a.width + (t >> a.page_shift)];
                     if (page < 0 || page >= a.num_pages) flag_status(a.dev_status, KDA_DEV_BAD_PAGE);
                     else at = page * a.page_stride + (t & ((1 << a.page_shift) - 1)) * a.token_stride + h * a.head_stride;

@@ -447,3 +447,12 @@ def test_values_before_the_window_have_no_effect(cuda_lib, D, page, io, G, decod
     a.run()
     assert torch.equal(a.out.tensor, want) and torch.equal(a.lse.tensor, lse)
     a.check()
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("window", [(1 << 31) - 1, (1 << 31) - 100])
+def test_the_widest_window_and_rows_before_the_first_token(cuda_lib, window, io):
+    """Positions below zero less the window pass 32 bits."""
+    c = Cache([300, 5, 40], [20, 2, 90], io=io)
+    Attn(c, cuda_lib, window=window).run().check()
+    Attn(Cache([1] * 3, [0, 1, 90], io=io), cuda_lib, decode=True, window=window).run().check()
