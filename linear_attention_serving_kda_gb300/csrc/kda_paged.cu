@@ -6,7 +6,8 @@
 // one place of a pair (16 bytes of either half) and goes through the heads with
 // it, so that a sine and cosine serve a row's heads.  Measured: rotation of 32768
 // rows of 40 heads of 128, bf16, 98 us, 6.8 TB/s (the copy rate); append of 32768
-// rows of 48 heads 120 us, 6.7 TB/s; 64 rows of single tokens 2.9 and 4.3 us.
+// rows of 48 heads, call after call, 120 us, 6.7 TB/s; 64 rows of single tokens 2.9
+// and 4.3 us.
 #include <cmath>
 #include <cstring>
 
@@ -148,8 +149,8 @@ template <typename IO, int V> struct Unit {
 
 constexpr int RT = 512;    // most threads of a CTA
 // Heads whose loads a thread has in flight together: more take registers from other CTAs (append of 32768 rows of 48 heads of
-// 128: 144 us with one, 130 with two, 136 with three, 149 with four, and of single tokens of 64 sequences 4.2, 4.3, 4.4 and 3.5 us,
-// of 200 4.3, 4.4, 4.5 and 6.2; rotation of 40 heads: 106 with two, 99 with four).
+// 128, a call by itself: 138 us with one, 127 with two, 129 with three, 134 with four, and of single tokens of 64 sequences 4.2, 4.3, 4.5 and
+// 3.5 us, of 200 4.3, 4.4, 4.5 and 6.3; rotation of 32768 rows of 40 heads: 105 with one, 99 with two, 98 with four).
 constexpr int RAHEAD = 4, AAHEAD = 2;
 
 struct RopeArgs {
@@ -318,9 +319,9 @@ int piece_of(int rd, int io_bf16)
 }
 
 // Threads for each row and unit (`groups`), rows of a CTA and its threads: a head a thread until half of the GPU's threads
-// are taken, then up to eight heads, which share their angles (2000 rows of 40 heads of 128: 10.4 us where all threads were to be taken first,
-// 8.5 so; a quarter: 7.9, but 7001 rows of 12 fp32 heads of 64 9.0 in place of 7.7).  CTAs of 128 threads or a row: 8192 fp32 rows of 16 heads
-// of 128 23.1 us with 256, 19.3 with 128, 19.3 with 64, append of 32768 rows 129, 127 and 138.
+// are taken, then up to eight heads, which share their angles (2000 rows of 40 heads of 128, the same again and again: 10.4 us where all threads
+// are to be taken first, 8.5 so, 7.9 with a quarter; 7001 rows of 12 fp32 heads of 64 7.4, 7.6, 9.0).  CTAs of 128 threads or a row: rotation of
+// 32768 rows of 40 heads 99 us with 256, 98 with 128, 115 with 64, of 8192 fp32 rows of 16 heads 20.5, 19.2, 19.1, append of 32768 rows 129, 127, 137.
 void split_rows(long long rows, int heads, int units, int max_rows, int& groups, int& rows_per_cta, int& threads)
 {
     const long long all = rows * heads * units;

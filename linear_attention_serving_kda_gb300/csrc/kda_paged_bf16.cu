@@ -10,11 +10,11 @@
 // The two tiles' products and exponentials alternate: while one tile's scores are exponentiated, the tensor
 // cores work for the other; with one tile, two steps of it do.
 // The weights are rounded to bf16 (2^-8 of each at most, with either sign: their sum is off by less than the outputs' own rounding).
-// What bounds it: for long chunks of wide heads the products, and the power that they draw.  8192 rows of 32 heads of 128 run
-// at 1590 TFLOP/s without a mask (1515 when called without a pause), at 1440 with one; the library's plain product reaches 1908.  16 heads
-// of 256 run at 1140 to 1230: with one tile of rows every key and value is loaded from L2 once a 128 rows.  Heads of 64 do half
-// the products a score and stop at 950, at the way of a row's scores through its thread (not at the exponential unit: polynomials in place of
-// a quarter of them, 846).  A unit costs 10 us besides where prompts are short, mostly waiting for instructions.
+// What bounds it: for long chunks of heads of 128 the products, and the power that they draw.  8192 rows of 32 heads of 128 run
+// at 1580 TFLOP/s without a mask (1540 when called without a pause), at 1440 with one; the library's plain product reaches 1908.  Heads of 64 do
+// half the products a score and stop at 940 (860 with a mask), 16 heads of 256 at 1120: latency in both, no unit is full (64: tensor cores
+// 36 % of their cycles, issue slots 46, exponential unit 37; 256: 47, 21, 12 and L2 37, where the one tile of rows of a CTA leaves a warpgroup
+// idle and its steps stand one behind the other).  A unit costs some 10 us besides where prompts are short (64 prompts of 333 rows 193 us).
 #include <cuda.h>
 
 #include "kda_paged_plan.cuh"
@@ -31,8 +31,8 @@ constexpr float LAG = 8.f;
 template <int DP> struct Shape {
     static constexpr int TILES = DP == 256 ? 1 : 2;    // tiles of 128 rows: TMEM holds 512 columns, O takes DP of them a tile
     static constexpr int KEYS = DP == 256 ? 64 : 128;
-    // Places of a unit besides its key tiles.  32 heads of 128: a prompt of 8192 rows 398 us with one, 382 with two; eight of 4096
-    // 926, 794, 809, 825 with none to three.  Of 256: a prompt of 8192 rows 602, 524, 490, 492 with none, one, three, four
+    // Places of a unit besides its key tiles.  None to four, 32 heads of 128: a prompt of 8192 rows 515, 405, 383, 388, 394 us; eight of 4096
+    // 935, 800, 793, 808, 823.  16 of 256: a prompt of 8192 rows 627, 546, 493, 495, 498.
     static constexpr int UNIT = DP == 256 ? 3 : 2;
     static constexpr int BLOCKS = DP / 64;             // 128-byte pieces of a row
     static constexpr int SLOT = KEYS * DP * 2;
@@ -264,7 +264,7 @@ paged_bf16_kernel(const PagedArgs a, const Plan p, const __grid_constant__ CUten
             // eight rows as the descriptor expects; and the outputs of the unit before from the ring's slots, the first slot by one warp,
             // the second by the other.  (Outputs of units in turn are announced on two barriers: with one, softmax warps that are through with the next unit
             // before this warp looks for the one before would make two uses look like none.  They cannot be through with the one after that: its rows come from this
-            // warp, behind its stores, or (second slot, rows by the other warp) its slot lies two units, eight places of the ring at least, behind this one's.)  (Pieces by threads take 3 us a unit, copies nothing that shows: 64 prompts of 333 rows 202 -> 190 us.)
+            // warp, behind its stores, or (second slot, rows by the other warp) its slot lies two units, eight places of the ring at least, behind this one's.)  (Pieces by threads take 3 us a unit, copies nothing that shows: 64 prompts of 333 rows 202 us with them, 190 with copies.)
             static_assert(SLOTS <= 8, "two units use the whole ring");
             constexpr int PIECES = DP / 8, AT_ONCE = 32 / PIECES;  // rows that a warp's 32 pieces make
             const int me = warp & 1, e = lane % PIECES, r0 = me * 64 + lane / PIECES;

@@ -1,12 +1,13 @@
 // kda_paged_f32.cu -- attention of chunks of fp32 rows over a paged cache.
 //
-// Everything in fp32 on the ordinary pipes (the tensor cores' fp32 form drops 13 of 24 bits): a CTA holds a tile of R
+// Everything in fp32 on the ordinary pipes (the tensor cores' own fp32 form drops 13 of 24 bits; operands in three bf16 pieces, six products,
+// would keep them and were not tried): a CTA holds a tile of R
 // rows (all of one key head) and goes through its tokens KEYS at a time: scores S = Q K^T, running maximum and sum of
 // each row, O = O 2^(m - m') + W V.  A thread has R / 16 rows x KEYS / 16 scores and the same rows x D / 16 outputs in
 // registers, so that a value from shared memory serves four products; two operations an instruction.  The weights take the
 // keys' place in shared memory, which leaves room for a second CTA to compute while one loads.
 // The multiplications bound it (half of the issue slots, the rest waits for shared memory): 2048 rows of 32 heads of 128 run
-// at 40 TFLOP/s, of 256 at 35.
+// at 39 TFLOP/s, of 256 at 35.
 #include "kda_paged_plan.cuh"
 
 namespace kda {

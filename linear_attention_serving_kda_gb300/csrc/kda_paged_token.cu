@@ -8,9 +8,9 @@
 // A warp loads (tensor copies, a ring of tiles); teams of warps that take the tiles in turn hold 16 tokens of a tile
 // a warp: scores and values by mma.sync with up to 16 heads as rows (a tcgen05 tile would have 128 of them, nearly all empty), weights
 // in two bf16 parts (2^-17 of each: the outputs keep fp32's places), running maximum and sum of each warp by itself, joined at the pair's end.
-// Measured: 64 sequences of up to 32768 tokens, eight key heads of 128 (4.3 GB), 615 us, 7.1 TB/s; 128 of 2048 tokens, two key heads of
-// 256 in pages of 16 (0.54 GB), 5.2 TB/s with the start and the join (10 us together); fp32, 64 of 4096 tokens, 362 us, 5.9 TB/s.  One sequence of
-// 32768 tokens (134 MB) takes 28 us, of which the join is 6.
+// Measured: 64 sequences of up to 32768 tokens, eight key heads of 128 (4.3 GB), 627 us, 6.9 TB/s; 128 of 2048 tokens, two key heads of
+// 256 in pages of 16 (0.54 GB), 93 us, 5.8 TB/s with the start and the join (10 us together); fp32, 64 of 4096 tokens, 341 us, 6.3 TB/s.  One sequence of
+// 32768 tokens (134 MB) takes 30 us, of which the join is 6; 250 sequences of 1 to 100 tokens 45.
 #include <cuda.h>
 
 #include "kda_paged.h"
