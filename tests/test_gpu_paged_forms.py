@@ -368,8 +368,8 @@ def test_no_wait_runs_out_in_silence(cuda_lib, D, G, lens, kv):
 
 
 def test_waits_over_a_long_unit_are_as_long(cuda_lib):
-    """Units of 2^24 tokens (two pages again and again), one a CTA: the waits that last a unit go by its length.  Their limit here, 2^14 polls of less than 4 us
-    (a poll that nothing ends), is shorter than the unit; by its length it is three times that."""
+    """Units of 2^24 tokens (two pages again and again), one a CTA, 170 ms: the waits that last a unit go by its length.  Their limit here, 2^15 polls (3.7 us each
+    where nothing ends them, 121 ms), is shorter than the unit; by its length it is three times that."""
     kda = cuda_lib
     Hkv, G, D, page, T, pages = 152, 2, 64, 1024, 128, 1 << 14
     g = torch.Generator(device="cuda").manual_seed(5)
@@ -384,7 +384,7 @@ def test_waits_over_a_long_unit_are_as_long(cuda_lib):
         ws, out, status = torch.empty(need, dtype=torch.uint8, device="cuda"), torch.full_like(q, 7.0), _i32([0])
         start, end = torch.cuda.Event(True), torch.cuda.Event(True)
         start.record()
-        kda.check(kda.kda_debug_paged_attn_stalled(p, _i32([0, T]), 1, T, _i32([tokens]), table, q, k, v, out, None, ws, need, status, 1 << 22, 1 << 14, -1))
+        kda.check(kda.kda_debug_paged_attn_stalled(p, _i32([0, T]), 1, T, _i32([tokens]), table, q, k, v, out, None, ws, need, status, 1 << 22, 1 << 15, -1))
         end.record()
         torch.cuda.synchronize()
         assert int(status.item()) == 0, (tokens, start.elapsed_time(end))
